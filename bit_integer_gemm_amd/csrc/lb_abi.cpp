@@ -283,6 +283,23 @@ int run_gemm(int kind, int dtype, int variant, const void *A, const void *B, voi
 
 }  // namespace
 
+// The scaled product's launches are the linear layer's.
+int lb::scaled_auto(const int8_t *X, const int8_t *W, const float *sx, const float *sw, void *out, int64_t M,
+                    int64_t N, int64_t K, const lb::ScaledOut &so, hipStream_t stream)
+{
+    const Plan p = make_plan(lb::KIND_LINEAR, LB_S8, LB_AUTO, M, N, K, K, 0);
+    const int64_t elem = so.ftype == LB_F32 ? 4 : 2;
+    for (int i = 0; i < p.np; ++i) {
+        const Part &q = p.parts[i];
+        const lb::ScaledOut part{so.bias ? (const char *)so.bias + q.n0 * elem : nullptr, so.ftype};
+        const hipError_t e = lb::launch_scaled(q.variant, X + q.m0 * K, W + q.n0 * K,
+                                               (char *)out + (q.m0 * N + q.n0) * elem, sx + q.m0, sw + q.n0, q.m,
+                                               q.n, K, N, part, stream);
+        if (e != hipSuccess) return LB_ERR_HIP;
+    }
+    return LB_OK;
+}
+
 extern "C" {
 
 int lb_gemm_s8(const int8_t *A, const int8_t *B, int32_t *C, int64_t M, int64_t N, int64_t K,
@@ -444,6 +461,7 @@ const char *lb_status_string(int status)
     case LB_ERR_OVERFLOW: return "K above the limit for this type (the exact int32 sum must fit), "
                                  "or a convolution beyond 32-bit byte offsets";
     case LB_ERR_HIP: return "HIP runtime error";
+    case LB_ERR_WORKSPACE: return "workspace smaller than the call needs";
     default: return "unknown status";
     }
 }

@@ -1,0 +1,49 @@
+// lb_float.hpp -- 16-bit and 32-bit floating types of the serving operators:
+// loads, exact widening and one rounding (to nearest, ties to even) back.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "lb_device.hpp"
+
+namespace lb {
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+// Two 16-bit floats packed in a word.
+template <class T> __device__ inline float lo_f32(uint32_t w);
+template <class T> __device__ inline float hi_f32(uint32_t w);
+template <> __device__ inline float lo_f32<__bf16>(uint32_t w) { return __uint_as_float(w << 16); }
+template <> __device__ inline float hi_f32<__bf16>(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+template <> __device__ inline float lo_f32<_Float16>(uint32_t w)
+{
+    return (float)__builtin_bit_cast(f16x2, w).x;
+}
+template <> __device__ inline float hi_f32<_Float16>(uint32_t w)
+{
+    return (float)__builtin_bit_cast(f16x2, w).y;
+}
+
+// Round two floats to T and pack them (the first in the low half).
+template <class T> __device__ inline uint32_t pack2(float a, float b)
+{
+    typedef T t2 __attribute__((ext_vector_type(2)));
+    const t2 v = {(T)a, (T)b};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+// Largest value of a float in a 16-bit type's exponent field, as a bit test:
+// |x| >= inf (infinity or NaN) in either half of a word.
+template <class T> __device__ inline bool any_nonfinite(uint32_t w)
+{
+    const uint32_t inf = sizeof(T) == 2 && __is_same(T, __bf16) ? 0x7F80u : 0x7C00u;
+    return (w & 0x7FFFu) >= inf || ((w >> 16) & 0x7FFFu) >= inf;
+}
+
+}  // namespace lb

@@ -4,12 +4,16 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "lb_gemm.h"
+
 namespace lb {
 
 // KIND_B1 runs the 1-bit GEMM on the int8 instruction (eight weighted bit
 // planes per 64-byte block), KIND_B1F4 on the FP4 instruction (four bit planes
 // per block, fp32 accumulation exact below 2^24).
-enum { KIND_S8 = 0, KIND_S4 = 1, KIND_LINEAR = 2, KIND_B1 = 3, KIND_B1F4 = 4 };
+// KIND_SCALED is the int8 product with both scales, a bias and a 16- or 32-bit
+// floating output (launch_scaled).
+enum { KIND_S8 = 0, KIND_S4 = 1, KIND_LINEAR = 2, KIND_B1 = 3, KIND_B1F4 = 4, KIND_SCALED = 5 };
 
 // Internal tile codes beside the nine public variants (never accepted from a
 // caller): the four-wave kernel on 256x192 tiles (int8, int4 and 1-bit FP4-
@@ -29,6 +33,28 @@ enum { CONV_64x64_K64 = 18 };
 hipError_t launch_mfma(int kind, int variant, const void *A, const void *B, void *out,
                        const float *sx, const float *sw, int64_t M, int64_t N, int64_t Kb,
                        int64_t ldo, int64_t ksplit, hipStream_t s);
+// Output of a scaled product: its float type (lb_ftype) and the bias of each
+// column in that type (null: none).
+struct ScaledOut {
+    const void *bias;
+    int32_t ftype;
+};
+// out = ((float)(A x B) * sx[m]) * sw[n] + bias[n], rounded to so.ftype; tiles as
+// launch_mfma's linear layer.
+hipError_t launch_scaled(int variant, const int8_t *A, const int8_t *B, void *out, const float *sx,
+                         const float *sw, int64_t M, int64_t N, int64_t K, int64_t ldo,
+                         const ScaledOut &so, hipStream_t s);
+// The same with the launches of an automatic choice; an lb_status.
+int scaled_auto(const int8_t *X, const int8_t *W, const float *sx, const float *sw, void *out, int64_t M,
+                int64_t N, int64_t K, const ScaledOut &so, hipStream_t s);
+// Rows of X (K elements, ldx apart, 16-byte aligned) quantised to int8 with a
+// scale each.
+hipError_t launch_quant_rows(int ftype, const void *X, int64_t ldx, int8_t *Q, float *sx, int64_t M,
+                             int64_t K, hipStream_t s);
+// The scaled product for at most LINEAR_FEW_MAX rows of X.
+enum { LINEAR_FEW_MAX = 64 };
+hipError_t launch_linear_few(int ftype, const int8_t *Xq, const int8_t *W, const float *sx, const float *sw,
+                             const void *bias, void *out, int64_t M, int64_t N, int64_t K, hipStream_t s);
 // Zero n int32 values on the stream (a kernel, not a memset).
 hipError_t launch_zero_i32(int32_t *p, int64_t n, hipStream_t s);
 // Workgroup tile and stage of a variant; bk_bytes is the K depth of a stage in bytes.
@@ -45,6 +71,34 @@ struct ConvGeom {
 // kind KIND_S8 or KIND_S4; M = N*Ho*Wo, N = Co, Kb = Kh*Kw*Cb.
 hipError_t launch_conv(int kind, int variant, const void *X, const void *F, int32_t *Y,
                        int64_t M, int64_t N, int64_t Kb, const ConvGeom &g, hipStream_t s);
+
+// The 4-bit paged cache (layout in lb_gemm.h).
+struct Kv4Cache {
+    uint8_t *k, *v;
+    uint32_t *kp, *vp;   // one word per vector: scale in the low half, minimum in the high half
+    int64_t pages;
+    int32_t page, heads;
+};
+// New keys and values (T tokens, ld elements apart, heads x D each) into slots;
+// and vectors of slots out again.
+hipError_t launch_kv4_write(int ftype, const void *K, const void *V, int64_t ldk, int64_t ldv,
+                            const int64_t *slots, const Kv4Cache &c, int64_t T, int D, hipStream_t s);
+hipError_t launch_kv4_read(int ftype, const Kv4Cache &c, const int64_t *slots, void *K, void *V, int64_t T,
+                           int D, hipStream_t s);
+
+struct AttnArgs {
+    const void *q;
+    void *out;
+    float *lse;
+    const int32_t *table, *q_off, *lens;
+    float *part;          // partial results of key ranges, if splits > 1
+    Kv4Cache c;
+    int64_t ldq, ldo, ldt, width;
+    int64_t total_q;
+    int32_t group, batch, window, causal, splits, tiles;
+    float scale2;         // softmax scale * log2(e)
+};
+hipError_t launch_attn_rows(int ftype, int D, const AttnArgs &a, hipStream_t s);
 
 // Measured selection table lookup (host only).
 int select_from_table(int dtype, int64_t M, int64_t N, int64_t K, int cu_count, int *best,

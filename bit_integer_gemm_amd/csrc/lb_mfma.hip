@@ -250,17 +250,49 @@ __device__ inline f32x4 mfma_fp4(i32x4 b, i32x4 a, f32x4 c)
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b8, a8, c, 4, 4, 0, sc, 0, sc);
 }
 
+// Store of the scaled product (KIND_SCALED): four consecutive columns of a row
+// as ((float)acc * sx[m]) * sw[n] + bias[n] in fp32, rounded once to the output
+// type.  o: element offset of the first; left: columns from it to N; vec: all
+// four exist and the row stride keeps them aligned.
+template <class T>
+__device__ inline void store_scaled_t(const ScaledOut &so, void *out, int64_t o, int64_t n, int64_t left,
+                                      bool vec, f32x4 v)
+{
+    typedef T t4 __attribute__((ext_vector_type(4)));
+    if (vec) {
+        if (so.bias) {
+            const t4 b = *(const t4 *)((const T *)so.bias + n);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] += (float)b[r];
+        }
+        *(t4 *)((T *)out + o) = t4{(T)v.x, (T)v.y, (T)v.z, (T)v.w};
+    } else {
+        for (int r = 0; r < 4 && r < left; ++r) {
+            const float b = so.bias ? (float)((const T *)so.bias)[n + r] : 0.f;
+            ((T *)out)[o + r] = (T)(so.bias ? v[r] + b : v[r]);
+        }
+    }
+}
+__device__ inline void store_scaled(const ScaledOut &so, void *out, int64_t o, int64_t n, int64_t left,
+                                    bool vec, f32x4 v)
+{
+    if (so.ftype == LB_BF16) store_scaled_t<__bf16>(so, out, o, n, left, vec, v);
+    else if (so.ftype == LB_F16) store_scaled_t<_Float16>(so, out, o, n, left, vec, v);
+    else store_scaled_t<float>(so, out, o, n, left, vec, v);
+}
+
 template <class C, int KIND, bool CONV>
-__global__ __launch_bounds__(C::NT) void mfma_gemm_kernel(
+__device__ __forceinline__ void mfma_gemm_tile(
     const int8_t *__restrict__ A, const int8_t *__restrict__ B, void *__restrict__ out,
     const float *__restrict__ sx, const float *__restrict__ sw,
     int32_t M, int32_t N, int32_t Kb, uint32_t tiles_m, uint32_t tiles_n, int32_t ldo,
-    int32_t ksplit, ConvGeom g)
+    int32_t ksplit, const ConvGeom &g, const ScaledOut &so)
 {
     // Linear layer: the tile's row and column scales follow the stage ring
     // (medium and large tiles; the small tile keeps its five workgroups per CU
     // and reads the scales from global memory).
-    constexpr bool LDS_SCALES = KIND == KIND_LINEAR && C::BM >= 128;
+    constexpr bool SCALES = KIND == KIND_LINEAR || KIND == KIND_SCALED;
+    constexpr bool LDS_SCALES = SCALES && C::BM >= 128;
     // LATE_COPIES (four-wave tiles and int4): the next stage's copies go out
     // right after the stage wait, ahead of this stage's fragment reads; the
     // other tiles issue them behind the first fragment reads (see the loop).
@@ -578,7 +610,7 @@ __global__ __launch_bounds__(C::NT) void mfma_gemm_kernel(
         const int64_t m = m0 + wm * C::TM + i * 16 + (lane % 16);
         if (m >= M) continue;
         float scale_m = 0.f;
-        if constexpr (KIND == KIND_LINEAR) scale_m = LDS_SCALES ? lds_sx[m - m0] : sx[m];
+        if constexpr (SCALES) scale_m = LDS_SCALES ? lds_sx[m - m0] : sx[m];
 #pragma unroll
         for (int j = 0; j < C::FN; ++j) {
             const int64_t n = n0 + wn * C::TN + j * 16 + (lane / 16) * 4;
@@ -593,7 +625,15 @@ __global__ __launch_bounds__(C::NT) void mfma_gemm_kernel(
             }
             if constexpr (KIND == KIND_S4) v = v >> 8;
             if constexpr (KIND == KIND_B1) v = v >> 6;
-            if constexpr (KIND == KIND_LINEAR) {
+            if constexpr (KIND == KIND_SCALED) {
+                f32x4 r;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float s = LDS_SCALES ? lds_sw[n - n0 + e] : n + e < N ? sw[n + e] : 0.f;
+                    r[e] = ((float)v[e] * scale_m) * s;
+                }
+                store_scaled(so, out, m * (int64_t)ldo + n, n, N - n, vec_ok, r);
+            } else if constexpr (KIND == KIND_LINEAR) {
                 float *o = (float *)out + m * (int64_t)ldo + n;
                 if (vec_ok) {
                     const f32x4 s = LDS_SCALES ? *(const f32x4 *)(lds_sw + (n - n0))
@@ -619,6 +659,24 @@ __global__ __launch_bounds__(C::NT) void mfma_gemm_kernel(
             }
         }
     }
+}
+
+template <class C, int KIND, bool CONV>
+__global__ __launch_bounds__(C::NT) void mfma_gemm_kernel(
+    const int8_t *__restrict__ A, const int8_t *__restrict__ B, void *__restrict__ out,
+    const float *__restrict__ sx, const float *__restrict__ sw,
+    int32_t M, int32_t N, int32_t Kb, uint32_t tiles_m, uint32_t tiles_n, int32_t ldo,
+    int32_t ksplit, ConvGeom g)
+{
+    mfma_gemm_tile<C, KIND, CONV>(A, B, out, sx, sw, M, N, Kb, tiles_m, tiles_n, ldo, ksplit, g, ScaledOut{});
+}
+template <class C>
+__global__ __launch_bounds__(C::NT) void scaled_gemm_kernel(
+    const int8_t *__restrict__ A, const int8_t *__restrict__ B, void *__restrict__ out,
+    const float *__restrict__ sx, const float *__restrict__ sw,
+    int32_t M, int32_t N, int32_t Kb, uint32_t tiles_m, uint32_t tiles_n, int32_t ldo, ScaledOut so)
+{
+    mfma_gemm_tile<C, KIND_SCALED, false>(A, B, out, sx, sw, M, N, Kb, tiles_m, tiles_n, ldo, Kb, ConvGeom{}, so);
 }
 
 // ---- large tile on four waves (int8, int4, 1-bit, int8 linear) ----------
@@ -704,20 +762,22 @@ __device__ constexpr int spread_item(int s)
 // spread_item; for 8 x 8 that is the fixed pattern of one copy per four slots
 // and one read per two.
 template <int KIND, int FM, int FN>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void mfma_w4_kernel(
+__device__ __forceinline__ void mfma_w4_tile(
     const int8_t *__restrict__ A, const int8_t *__restrict__ B, void *__restrict__ out,
     const float *__restrict__ sx, const float *__restrict__ sw,
-    int32_t M, int32_t N, int32_t Kb, uint32_t tiles_m, uint32_t tiles_n, int32_t ldo, int32_t ksplit)
+    int32_t M, int32_t N, int32_t Kb, uint32_t tiles_m, uint32_t tiles_n, int32_t ldo, int32_t ksplit,
+    const ScaledOut &so)
 {
+    constexpr bool SCALES = KIND == KIND_LINEAR || KIND == KIND_SCALED;
     static_assert(FM % 2 == 0 && FM >= 4 && FM <= 8 && FN % 2 == 0 && FN >= 4 && FN <= 8, "wave sub-tile");
-    static_assert((FM == 8 && FN == 8) || KIND == KIND_S8 || KIND == KIND_LINEAR ||
+    static_assert((FM == 8 && FN == 8) || KIND == KIND_S8 || SCALES ||
                       ((KIND == KIND_S4 || KIND == KIND_B1F4) && FM == 8 && FN == 6),
                   "int4 and 1-bit run the 256x256 and 256x192 tiles");
     constexpr int BM = 32 * FM, BN = 32 * FN;
     constexpr int SS = (BM + BN) * 128;   // one super-stage: 128 K-bytes of A and B
     constexpr int BOFF = BM * 128;        // B's blocks within a super-stage
     constexpr int NCP = FM + FN;          // refill copies per wave per super-stage
-    constexpr int SCALE_BYTES = KIND == KIND_LINEAR ? (BM + BN) * 4 : 0;
+    constexpr int SCALE_BYTES = SCALES ? (BM + BN) * 4 : 0;
     __shared__ __attribute__((aligned(1024))) char smem[2 * SS + SCALE_BYTES];
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -802,7 +862,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     // stage wait covers these older copies, and the epilogue reads the scales
     // from LDS (read from global memory at the end of the tile, they made the
     // layer 5% slower at 8192 x 11008 x 4096).
-    if constexpr (KIND == KIND_LINEAR) {
+    if constexpr (SCALES) {
         if (wave == 0) {
             const uint32_t sbase = smem_base + 2 * SS;
             const i32x4 rx = make_rsrc(sx + m0, (uint64_t)(M - m0) * 4);
@@ -921,7 +981,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     using P0 = std::integral_constant<int, 0>;
     using P1 = std::integral_constant<int, 1>;
     using F0 = std::false_type;
-    if constexpr (KIND == KIND_S8 || KIND == KIND_LINEAR) {
+    if constexpr (KIND == KIND_S8 || SCALES) {
         body(P0{}, std::true_type{}, 0, fa0, fb0, fa1, fb1);
         int t = 1;
         for (; t + 1 < nk; t += 2) {
@@ -1237,7 +1297,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         const float *lds_sx = (const float *)(smem + 2 * SS);
         const float *lds_sw = lds_sx + BM;
         float scale_m = 0.f;
-        if constexpr (KIND == KIND_LINEAR) scale_m = lds_sx[m - m0];
+        if constexpr (SCALES) scale_m = lds_sx[m - m0];
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
             const int64_t n = n0 + wn * (16 * FN) + j * 16 + (lane / 16) * 4;
@@ -1250,7 +1310,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
             } else
                 v = acc[i][j];
             if constexpr (KIND == KIND_S4) v = v >> 8;
-            if constexpr (KIND == KIND_LINEAR) {
+            if constexpr (KIND == KIND_SCALED) {
+                const f32x4 s = *(const f32x4 *)(lds_sw + (n - n0));
+                f32x4 r;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) r[e] = ((float)v[e] * scale_m) * s[e];
+                store_scaled(so, out, m * (int64_t)ldo + n, n, N - n, vec_ok, r);
+            } else if constexpr (KIND == KIND_LINEAR) {
                 float *o = (float *)out + m * (int64_t)ldo + n;
                 if (vec_ok) {
                     const f32x4 s = *(const f32x4 *)(lds_sw + (n - n0));
@@ -1275,6 +1341,23 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
             }
         }
     }
+}
+
+template <int KIND, int FM, int FN>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void mfma_w4_kernel(
+    const int8_t *__restrict__ A, const int8_t *__restrict__ B, void *__restrict__ out,
+    const float *__restrict__ sx, const float *__restrict__ sw,
+    int32_t M, int32_t N, int32_t Kb, uint32_t tiles_m, uint32_t tiles_n, int32_t ldo, int32_t ksplit)
+{
+    mfma_w4_tile<KIND, FM, FN>(A, B, out, sx, sw, M, N, Kb, tiles_m, tiles_n, ldo, ksplit, ScaledOut{});
+}
+template <int FM, int FN>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void scaled_w4_tile_kernel(
+    const int8_t *__restrict__ A, const int8_t *__restrict__ B, void *__restrict__ out,
+    const float *__restrict__ sx, const float *__restrict__ sw,
+    int32_t M, int32_t N, int32_t Kb, uint32_t tiles_m, uint32_t tiles_n, int32_t ldo, ScaledOut so)
+{
+    mfma_w4_tile<KIND_SCALED, FM, FN>(A, B, out, sx, sw, M, N, Kb, tiles_m, tiles_n, ldo, Kb, so);
 }
 
 template <int KIND, int FM, int FN>
@@ -1455,6 +1538,48 @@ hipError_t launch_conv(int kind, int variant, const void *X, const void *F, int3
     switch (kind) {
     case KIND_S8: return dispatch<KIND_S8, true>(variant, X, F, Y, nullptr, nullptr, M, N, Kb, N, Kb, g, s);
     case KIND_S4: return dispatch<KIND_S4, true>(variant, X, F, Y, nullptr, nullptr, M, N, Kb, N, Kb, g, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+// The scaled product: each variant's tile as the linear layer has it.
+template <class C>
+static hipError_t launch_scaled_one(const int8_t *A, const int8_t *B, void *out, const float *sx, const float *sw,
+                                    int64_t M, int64_t N, int64_t K, int64_t ldo, const ScaledOut &so, hipStream_t s)
+{
+    const uint64_t tm = (uint64_t)((M + C::BM - 1) / C::BM), tn = (uint64_t)((N + C::BN - 1) / C::BN);
+    if (tm * tn > 0x7FFFFFFFull) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((scaled_gemm_kernel<C>), dim3((uint32_t)(tm * tn)), dim3(C::NT), 0, s, A, B, out, sx, sw,
+                       (int32_t)M, (int32_t)N, (int32_t)K, (uint32_t)tm, (uint32_t)tn, (int32_t)ldo, so);
+    return hipGetLastError();
+}
+template <int FM, int FN>
+static hipError_t launch_scaled_w4(const int8_t *A, const int8_t *B, void *out, const float *sx, const float *sw,
+                                   int64_t M, int64_t N, int64_t K, int64_t ldo, const ScaledOut &so, hipStream_t s)
+{
+    constexpr int64_t BM = 32 * FM, BN = 32 * FN;
+    const uint64_t tm = (uint64_t)((M + BM - 1) / BM), tn = (uint64_t)((N + BN - 1) / BN);
+    if (tm * tn > 0x7FFFFFFFull) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((scaled_w4_tile_kernel<FM, FN>), dim3((uint32_t)(tm * tn)), dim3(256), 0, s, A, B, out, sx, sw,
+                       (int32_t)M, (int32_t)N, (int32_t)K, (uint32_t)tm, (uint32_t)tn, (int32_t)ldo, so);
+    return hipGetLastError();
+}
+
+hipError_t launch_scaled(int variant, const int8_t *A, const int8_t *B, void *out, const float *sx, const float *sw,
+                         int64_t M, int64_t N, int64_t K, int64_t ldo, const ScaledOut &so, hipStream_t s)
+{
+    switch (variant) {
+    case 0: return launch_scaled_one<S2>(A, B, out, sx, sw, M, N, K, ldo, so, s);
+    case 1: return launch_scaled_one<S3>(A, B, out, sx, sw, M, N, K, ldo, so, s);
+    case 2: return launch_scaled_one<S4>(A, B, out, sx, sw, M, N, K, ldo, so, s);
+    case 3: return launch_scaled_one<M2>(A, B, out, sx, sw, M, N, K, ldo, so, s);
+    case 4: return launch_scaled_one<M3>(A, B, out, sx, sw, M, N, K, ldo, so, s);
+    case 5: return launch_scaled_one<M4>(A, B, out, sx, sw, M, N, K, ldo, so, s);
+    case 6: return launch_scaled_w4<8, 8>(A, B, out, sx, sw, M, N, K, ldo, so, s);
+    case 7: return launch_scaled_one<L3W8>(A, B, out, sx, sw, M, N, K, ldo, so, s);
+    case 8: return launch_scaled_one<L4W16>(A, B, out, sx, sw, M, N, K, ldo, so, s);
+    case W4_256x192: return launch_scaled_w4<8, 6>(A, B, out, sx, sw, M, N, K, ldo, so, s);
+    case W4_192x256: return launch_scaled_w4<6, 8>(A, B, out, sx, sw, M, N, K, ldo, so, s);
     default: return hipErrorInvalidValue;
     }
 }

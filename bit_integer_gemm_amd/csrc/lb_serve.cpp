@@ -1,0 +1,243 @@
+// lb_serve.cpp -- the extern "C" boundary of the serving operators: argument
+// checks, planning of the attention's key ranges, launches on the caller's stream.
+#include "lb_gemm.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "lb_internal.hpp"
+
+namespace {
+
+const int64_t kLim = 0x7FFFFFFF;
+
+bool aligned(const void *p, uintptr_t to = 16) { return (uintptr_t)p % to == 0; }
+int64_t elem_of(int ftype) { return ftype == LB_F32 ? 4 : 2; }
+bool any_ftype(int t) { return t == LB_BF16 || t == LB_F16 || t == LB_F32; }
+bool short_ftype(int t) { return t == LB_BF16 || t == LB_F16; }
+int finish(hipError_t e) { return e == hipSuccess ? LB_OK : LB_ERR_HIP; }
+
+// Sizes, K rule, type and K limit of the int8 product, in the documented order.
+int check_product(int64_t M, int64_t N, int64_t K, int ftype)
+{
+    if (M <= 0 || N <= 0 || K <= 0 || M > kLim || N > kLim) return LB_ERR_SHAPE;
+    if (K % LB_S8_K_ALIGN != 0) return LB_ERR_ALIGN;
+    if (!any_ftype(ftype)) return LB_ERR_VARIANT;
+    if (K > LB_S8_K_MAX) return LB_ERR_OVERFLOW;
+    return LB_OK;
+}
+
+int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+
+int scaled(const int8_t *X, const int8_t *W, const float *sx, const float *sw, const void *bias, void *out,
+           int64_t M, int64_t N, int64_t K, int ftype, hipStream_t s)
+{
+    if (M <= lb::LINEAR_FEW_MAX)
+        return finish(lb::launch_linear_few(ftype, X, W, sx, sw, bias, out, M, N, K, s));
+    return lb::scaled_auto(X, W, sx, sw, out, M, N, K, lb::ScaledOut{bias, ftype}, s);
+}
+
+// Sizes of the cache.
+int check_cache(int64_t heads, int64_t D, int64_t pages, int64_t page, int ftype)
+{
+    if (heads <= 0 || pages <= 0 || page <= 0 || (D != 64 && D != 128 && D != 256)) return LB_ERR_SHAPE;
+    if (heads > 65535 || pages > kLim || page > kLim || (double)pages * (double)page >= 2147483648.0)
+        return LB_ERR_SHAPE;
+    if (page % LB_KV4_PAGE_ALIGN != 0) return LB_ERR_ALIGN;
+    if (!short_ftype(ftype)) return LB_ERR_VARIANT;
+    return LB_OK;
+}
+
+lb::Kv4Cache cache_of(const uint8_t *Kc, const uint8_t *Vc, const void *Kp, const void *Vp, int64_t heads,
+                      int64_t pages, int64_t page)
+{
+    lb::Kv4Cache c;
+    c.k = const_cast<uint8_t *>(Kc);
+    c.v = const_cast<uint8_t *>(Vc);
+    c.kp = (uint32_t *)const_cast<void *>(Kp);
+    c.vp = (uint32_t *)const_cast<void *>(Vp);
+    c.pages = pages;
+    c.page = (int32_t)page;
+    c.heads = (int32_t)heads;
+    return c;
+}
+
+struct AttnPlan {
+    int64_t tiles, splits, per_split;   // row tiles of a key head; key ranges; workspace bytes per range
+};
+
+AttnPlan plan_attn(int64_t B, int64_t total_q, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D,
+                   int64_t max_len, int64_t window, int cu)
+{
+    AttnPlan p;
+    const int64_t group = Hq / Hkv;
+    p.tiles = (max_q * group + 15) / 16;
+    int64_t keys = max_len;
+    if (window > 0) keys = std::min(keys, window + max_q);
+    const int64_t wgs = B * Hkv * p.tiles;
+    p.splits = 1;
+    if (cu > 0 && wgs < 4 * (int64_t)cu) {
+        p.splits = std::min((4 * (int64_t)cu + wgs - 1) / wgs, (keys + 255) / 256);
+        p.splits = std::max<int64_t>(1, std::min<int64_t>(p.splits, 64));
+    }
+    p.per_split = total_q * Hq * (D + 2) * 4;
+    return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+int lb_quant_rows_s8(const void *X, int64_t ldx, int8_t *Q, float *sx, int64_t M, int64_t K, int ftype,
+                     void *stream)
+{
+    if (!X || !Q || !sx) return LB_ERR_NULL;
+    if (ldx < K) return LB_ERR_SHAPE;
+    const int st = check_product(M, 1, K, ftype);
+    if (st != LB_OK) return st;
+    if (!aligned(X) || !aligned(Q) || ldx * elem_of(ftype) % 16 != 0) return LB_ERR_ALIGN;
+    return finish(lb::launch_quant_rows(ftype, X, ldx, Q, sx, M, K, (hipStream_t)stream));
+}
+
+int lb_gemm_s8_scaled(const int8_t *X, const int8_t *W, const float *sx, const float *sw, const void *bias,
+                      void *out, int64_t M, int64_t N, int64_t K, int ftype, void *stream)
+{
+    if (!X || !W || !sx || !sw || !out) return LB_ERR_NULL;
+    const int st = check_product(M, N, K, ftype);
+    if (st != LB_OK) return st;
+    if (!aligned(X) || !aligned(W) || !aligned(out) || !aligned(bias) || !aligned(sw)) return LB_ERR_ALIGN;
+    return scaled(X, W, sx, sw, bias, out, M, N, K, ftype, (hipStream_t)stream);
+}
+
+int64_t lb_linear_w8a8_workspace(int64_t M, int64_t K, int64_t N)
+{
+    if (check_product(M, N, K, LB_BF16) != LB_OK) return 0;
+    return round_up(M * K, 256) + round_up(M * 4, 256);
+}
+
+int lb_linear_w8a8(const void *X, int64_t ldx, const int8_t *W, const float *sw, const void *bias, void *out,
+                   int64_t M, int64_t N, int64_t K, int ftype, void *workspace, int64_t workspace_bytes,
+                   void *stream)
+{
+    if (!X || !W || !sw || !out) return LB_ERR_NULL;
+    if (ldx < K) return LB_ERR_SHAPE;
+    const int st = check_product(M, N, K, ftype);
+    if (st != LB_OK) return st;
+    if (!aligned(X) || !aligned(W) || !aligned(out) || !aligned(bias) || !aligned(sw) ||
+        ldx * elem_of(ftype) % 16 != 0)
+        return LB_ERR_ALIGN;
+    if (!workspace || workspace_bytes < lb_linear_w8a8_workspace(M, K, N)) return LB_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return LB_ERR_ALIGN;
+    int8_t *q = (int8_t *)workspace;
+    float *sx = (float *)(q + round_up(M * K, 256));
+    const hipStream_t s = (hipStream_t)stream;
+    if (lb::launch_quant_rows(ftype, X, ldx, q, sx, M, K, s) != hipSuccess) return LB_ERR_HIP;
+    return scaled(q, W, sx, sw, bias, out, M, N, K, ftype, s);
+}
+
+int lb_kv4_write(const void *K, const void *V, int64_t ldk, int64_t ldv, const int64_t *slots, uint8_t *Kc,
+                 uint8_t *Vc, void *Kp, void *Vp, int64_t T, int64_t heads, int64_t D, int64_t pages,
+                 int64_t page, int ftype, void *stream)
+{
+    if (!K || !V || !slots || !Kc || !Vc || !Kp || !Vp) return LB_ERR_NULL;
+    if (T <= 0 || T > kLim) return LB_ERR_SHAPE;
+    const int st = check_cache(heads, D, pages, page, ftype);
+    if (st != LB_OK) return st;
+    if (ldk < heads * D || ldv < heads * D) return LB_ERR_SHAPE;
+    if (!aligned(K) || !aligned(V) || !aligned(Kc) || !aligned(Vc) || !aligned(Kp) || !aligned(Vp) ||
+        ldk % 8 != 0 || ldv % 8 != 0)
+        return LB_ERR_ALIGN;
+    return finish(lb::launch_kv4_write(ftype, K, V, ldk, ldv, slots, cache_of(Kc, Vc, Kp, Vp, heads, pages, page),
+                                       T, (int)D, (hipStream_t)stream));
+}
+
+int lb_kv4_read(const uint8_t *Kc, const uint8_t *Vc, const void *Kp, const void *Vp, const int64_t *slots,
+                void *K, void *V, int64_t T, int64_t heads, int64_t D, int64_t pages, int64_t page, int ftype,
+                void *stream)
+{
+    if (!K || !V || !slots || !Kc || !Vc || !Kp || !Vp) return LB_ERR_NULL;
+    if (T <= 0 || T > kLim) return LB_ERR_SHAPE;
+    const int st = check_cache(heads, D, pages, page, ftype);
+    if (st != LB_OK) return st;
+    if (!aligned(K) || !aligned(V) || !aligned(Kc) || !aligned(Vc) || !aligned(Kp) || !aligned(Vp))
+        return LB_ERR_ALIGN;
+    return finish(lb::launch_kv4_read(ftype, cache_of(Kc, Vc, Kp, Vp, heads, pages, page), slots, K, V, T, (int)D,
+                                      (hipStream_t)stream));
+}
+
+static int check_attn(int64_t B, int64_t total_q, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D,
+                      int64_t max_len, int64_t window)
+{
+    if (B <= 0 || total_q <= 0 || max_q <= 0 || Hq <= 0 || Hkv <= 0 || max_len < 0 || window < 0)
+        return LB_ERR_SHAPE;
+    if (B > kLim || total_q > kLim || max_q > kLim || Hq > 65535 || Hkv > 65535 || max_len > kLim || window > kLim)
+        return LB_ERR_SHAPE;
+    if (Hq % Hkv != 0 || (D != 64 && D != 128 && D != 256)) return LB_ERR_SHAPE;
+    // row numbers of a key head, and of the whole batch's tiles, are 32-bit
+    if ((double)max_q * (double)(Hq / Hkv) >= 2147483632.0) return LB_ERR_OVERFLOW;
+    if ((double)B * (double)Hkv * (double)((max_q * (Hq / Hkv) + 15) / 16) >= 2147483648.0) return LB_ERR_OVERFLOW;
+    return LB_OK;
+}
+
+int64_t lb_attn_kv4_workspace(int64_t B, int64_t total_q, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D,
+                              int64_t max_len, int64_t window, int cu_count)
+{
+    if (check_attn(B, total_q, max_q, Hq, Hkv, D, max_len, window) != LB_OK) return 0;
+    if (cu_count <= 0 && lb::device_cu_count(&cu_count) != LB_OK) return 0;
+    const AttnPlan p = plan_attn(B, total_q, std::min(max_q, total_q), Hq, Hkv, D, max_len, window, cu_count);
+    return p.splits > 1 ? round_up(p.splits * p.per_split, 256) : 0;
+}
+
+int lb_attn_kv4(const void *Q, int64_t ldq, const uint8_t *Kc, const uint8_t *Vc, const void *Kp,
+                const void *Vp, const int32_t *table, int64_t ldt, int64_t table_width, const int32_t *q_off,
+                const int32_t *lens, void *out, int64_t ldo, float *lse, int64_t B, int64_t total_q,
+                int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D, int64_t pages, int64_t page,
+                int64_t max_len, float scale, int64_t window, int causal, int ftype, void *workspace,
+                int64_t workspace_bytes, void *stream)
+{
+    if (!Q || !Kc || !Vc || !Kp || !Vp || !table || !q_off || !lens || !out) return LB_ERR_NULL;
+    int st = check_attn(B, total_q, max_q, Hq, Hkv, D, max_len, window);
+    if (st == LB_ERR_SHAPE) return st;
+    if (table_width <= 0 || ldt < table_width || table_width > kLim || ldq < Hq * D || ldo < Hq * D)
+        return LB_ERR_SHAPE;
+    const int sc = check_cache(Hkv, D, pages, page, ftype);
+    if (sc != LB_OK) return sc;
+    if (st != LB_OK) return st;
+    if ((double)table_width * (double)page >= 2147483616.0) return LB_ERR_OVERFLOW;  // key numbers are 32-bit
+    if (!aligned(Q) || !aligned(Kc) || !aligned(Vc) || !aligned(Kp) || !aligned(Vp) || !aligned(out) ||
+        ldq % 8 != 0 || ldo % 8 != 0 || !aligned(workspace, 256))
+        return LB_ERR_ALIGN;
+    int cu = 0;
+    if (lb::device_cu_count(&cu) != LB_OK) cu = 0;
+    max_q = std::min(max_q, total_q);
+    const AttnPlan p = plan_attn(B, total_q, max_q, Hq, Hkv, D, max_len, window, cu);
+    int64_t splits = p.splits;
+    if (!workspace || workspace_bytes <= 0) splits = 1;
+    else splits = std::max<int64_t>(1, std::min(splits, workspace_bytes / p.per_split));
+
+    lb::AttnArgs a;
+    a.q = Q;
+    a.out = out;
+    a.lse = lse;
+    a.table = table;
+    a.q_off = q_off;
+    a.lens = lens;
+    a.part = (float *)workspace;
+    a.c = cache_of(Kc, Vc, Kp, Vp, Hkv, pages, page);
+    a.ldq = ldq;
+    a.ldo = ldo;
+    a.ldt = ldt;
+    a.width = table_width;
+    a.total_q = total_q;
+    a.group = (int32_t)(Hq / Hkv);
+    a.batch = (int32_t)B;
+    a.window = (int32_t)window;
+    a.causal = causal != 0;
+    a.splits = (int32_t)splits;
+    a.tiles = (int32_t)p.tiles;
+    a.scale2 = scale * 1.44269504088896340736f;
+    return finish(lb::launch_attn_rows(ftype, (int)D, a, (hipStream_t)stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,532 @@
+// lb_serve_kv4.hip -- a paged cache of keys and values in 4 bits: written, read back
+// and attended over.
+//
+// A vector x (the D numbers of one token and head) is held as levels u[d] in
+// 0..15, a scale s and a minimum m, both in the type T of x:
+//   m = min_d x[d],  s = T((max_d x[d] - m) / 15),
+//   u[d] = clamp(round_half_even((x[d] - m) / s), 0, 15)   (0 where s = 0),
+// and stands for u[d] s + m.  A vector that holds an infinity or a NaN, or whose
+// range is beyond fp32, stands for NaN.
+#include "lb_float.hpp"
+#include "lb_internal.hpp"
+
+namespace lb {
+
+// ---- write -----------------------------------------------------------------
+// (x - m) / s decides between levels at half-integers.  The product with 1/s is
+// off by less than 2^-19 (15 * 3 * 2^-24), so it settles the level unless it lies
+// within 2^-12 of a half-integer; there the correctly rounded quotient decides.
+__device__ inline uint32_t level_of(float x, float m, float s, float inv, bool direct)
+{
+    const float y = x - m, t = y * inv;
+    float n = __builtin_rintf(t);
+    if (direct || __builtin_fabsf(t - n) > 0.5f - 0x1p-12f) n = __builtin_rintf(y / s);
+    return (uint32_t)fminf(n, 15.f);
+}
+
+// D/8 lanes per vector, 8 elements (16 bytes in, one word of levels out) each;
+// blockIdx.y: 0 keys, 1 values.  A slot outside the cache is not written.
+template <class T, int D>
+__global__ __launch_bounds__(256) void kv4_write_kernel(const T *__restrict__ K, const T *__restrict__ V,
+                                                        int64_t ldk, int64_t ldv,
+                                                        const int64_t *__restrict__ slots, Kv4Cache c,
+                                                        int64_t vectors)
+{
+    constexpr int LPV = D / 8;
+    const int64_t vec = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPV;
+    const uint32_t sub = threadIdx.x % LPV;
+    if (vec >= vectors) return;  // whole groups of LPV lanes
+    const bool val = blockIdx.y != 0;
+    const int64_t t = vec / c.heads, h = vec - t * c.heads;
+    const int64_t slot = slots[t];
+    const T *src = (val ? V + t * ldv : K + t * ldk) + h * D + sub * 8;
+    const i32x4 w = *(const i32x4 *)src;
+    float x[8];
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = lo_f32<T>((uint32_t)w[i]);
+        x[2 * i + 1] = hi_f32<T>((uint32_t)w[i]);
+        odd |= any_nonfinite<T>((uint32_t)w[i]);
+    }
+    float lo = x[0], hi = x[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+        lo = fminf(lo, x[i]);
+        hi = fmaxf(hi, x[i]);
+    }
+    int bad = odd;
+#pragma unroll
+    for (int d = 1; d < LPV; d <<= 1) {
+        lo = fminf(lo, __shfl_xor(lo, d));
+        hi = fmaxf(hi, __shfl_xor(hi, d));
+        bad |= __shfl_xor(bad, d);
+    }
+    const T st = (T)((hi - lo) / 15.0f);
+    const float s = (float)st;
+    bad |= !(s < __builtin_inff());  // the range of the vector overflows
+    const bool flat = !(s > 0.f) || bad;
+    const bool direct = s < 0x1p-100f;
+    const float inv = 1.0f / s;
+    uint32_t word = 0;
+    if (!flat) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) word |= level_of(x[i], lo, s, inv, direct) << (4 * i);
+    }
+    if ((uint64_t)slot >= (uint64_t)(c.pages * c.page)) return;
+    const int64_t p = slot / c.page, off = slot - p * c.page;
+    const int64_t at = (p * c.heads + h) * c.page + off;
+    ((uint32_t *)(val ? c.v : c.k))[at * LPV + sub] = word;
+    if (sub == 0) {
+        const float nan = __uint_as_float(0x7FC00000u);
+        (val ? c.vp : c.kp)[at] = bad ? pack2<T>(nan, nan) : pack2<T>(s, lo);
+    }
+}
+
+// ---- read back -------------------------------------------------------------
+// One rounding, of u s + m (u s is exact in fp32).  A slot outside the cache
+// reads as zeros.
+template <class T, int D>
+__global__ __launch_bounds__(256) void kv4_read_kernel(Kv4Cache c, const int64_t *__restrict__ slots,
+                                                       T *__restrict__ K, T *__restrict__ V, int64_t vectors)
+{
+    constexpr int LPV = D / 8;
+    const int64_t vec = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPV;
+    const uint32_t sub = threadIdx.x % LPV;
+    if (vec >= vectors) return;
+    const bool val = blockIdx.y != 0;
+    const int64_t t = vec / c.heads, h = vec - t * c.heads;
+    const int64_t slot = slots[t];
+    i32x4 o = {0, 0, 0, 0};
+    if ((uint64_t)slot < (uint64_t)(c.pages * c.page)) {
+        const int64_t p = slot / c.page, off = slot - p * c.page;
+        const int64_t at = (p * c.heads + h) * c.page + off;
+        const uint32_t w = ((const uint32_t *)(val ? c.v : c.k))[at * LPV + sub];
+        const uint32_t prm = (val ? c.vp : c.kp)[at];
+        const float s = lo_f32<T>(prm), m = hi_f32<T>(prm);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            o[i] = (int)pack2<T>((float)((w >> (8 * i)) & 15u) * s + m, (float)((w >> (8 * i + 4)) & 15u) * s + m);
+    }
+    *(i32x4 *)((val ? V : K) + vec * D + sub * 8) = o;
+}
+
+template <class T, int D>
+static hipError_t write_t(const void *K, const void *V, int64_t ldk, int64_t ldv, const int64_t *slots,
+                          const Kv4Cache &c, int64_t T_, hipStream_t s)
+{
+    const int64_t vectors = T_ * c.heads, blocks = (vectors * (D / 8) + 255) / 256;
+    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((kv4_write_kernel<T, D>), dim3((uint32_t)blocks, 2), dim3(256), 0, s, (const T *)K,
+                       (const T *)V, ldk, ldv, slots, c, vectors);
+    return hipGetLastError();
+}
+template <class T, int D>
+static hipError_t read_t(const Kv4Cache &c, const int64_t *slots, void *K, void *V, int64_t T_, hipStream_t s)
+{
+    const int64_t vectors = T_ * c.heads, blocks = (vectors * (D / 8) + 255) / 256;
+    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((kv4_read_kernel<T, D>), dim3((uint32_t)blocks, 2), dim3(256), 0, s, c, slots, (T *)K,
+                       (T *)V, vectors);
+    return hipGetLastError();
+}
+
+#define LB_KV4_BY_TYPE(CALL)                                   \
+    if (ftype == LB_BF16) {                                    \
+        if (D == 64) return CALL(__bf16, 64);                  \
+        if (D == 128) return CALL(__bf16, 128);                \
+        if (D == 256) return CALL(__bf16, 256);                \
+    } else if (ftype == LB_F16) {                              \
+        if (D == 64) return CALL(_Float16, 64);                \
+        if (D == 128) return CALL(_Float16, 128);              \
+        if (D == 256) return CALL(_Float16, 256);              \
+    }                                                          \
+    return hipErrorInvalidValue;
+
+hipError_t launch_kv4_write(int ftype, const void *K, const void *V, int64_t ldk, int64_t ldv,
+                            const int64_t *slots, const Kv4Cache &c, int64_t T, int D, hipStream_t s)
+{
+#define CALL(TY, DD) write_t<TY, DD>(K, V, ldk, ldv, slots, c, T, s)
+    LB_KV4_BY_TYPE(CALL)
+#undef CALL
+}
+hipError_t launch_kv4_read(int ftype, const Kv4Cache &c, const int64_t *slots, void *K, void *V, int64_t T,
+                           int D, hipStream_t s)
+{
+#define CALL(TY, DD) read_t<TY, DD>(c, slots, K, V, T, s)
+    LB_KV4_BY_TYPE(CALL)
+#undef CALL
+}
+
+// ---- attention -------------------------------------------------------------
+// The rows of one sequence and key head: query i and head j of the group is row
+// i * group + j; query i stands at position len - nq + i and sees the keys
+// [lo, hi) with hi = position + 1 (causal) or len, lo = position - window + 1
+// (window > 0) or 0.
+//
+// Scores without ever scaling a key: u s + m is linear in u, so
+//   q . k = s (sum_d q[d] u[d]) + m (sum_d q[d]),
+// and the first sum runs on the matrix cores with the levels exact in T.  A
+// nibble becomes a T by writing it into the mantissa of a power of two,
+// B + u (bf16: B = 128, fp16: B = 64): one AND-OR for two nibbles, and a
+// constant to take off, -B sum_d q[d], which is the accumulator's start.
+// The values are summed the same way with the weights carrying the scale:
+//   sum_t p[t] v[t,d] = sum_t (p[t] s[t]) (u[t,d] - 8) + sum_t p[t] (m[t] + 8 s[t]).
+// Levels are taken about 8 so that a rounding of the weight counts against a
+// small number; the weight p s is split in two bf16 parts (16 bits in all, with
+// fp32's range, which fp16 scales or weights would not have).
+template <class T> struct Mfma;
+template <> struct Mfma<__bf16> {
+    typedef bf16x8 frag;
+    static constexpr float base = 128.f;
+    static constexpr uint32_t magic = 0x43004300u, mask = 0x000F000Fu;
+    static __device__ inline f32x4 mul(i32x4 a, i32x4 b, f32x4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(frag, a), __builtin_bit_cast(frag, b), c,
+                                                       0, 0, 0);
+    }
+    // nibbles i and i+4 of w as a pair
+    static __device__ inline uint32_t pair(uint32_t w, int i) { return ((w >> (4 * i)) & mask) | magic; }
+};
+template <> struct Mfma<_Float16> {
+    typedef f16x8 frag;
+    static constexpr float base = 64.f;
+    static constexpr uint32_t magic = 0x54005400u, mask = 0x00F000F0u;
+    static __device__ inline f32x4 mul(i32x4 a, i32x4 b, f32x4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(frag, a), __builtin_bit_cast(frag, b), c,
+                                                      0, 0, 0);
+    }
+    static __device__ inline uint32_t pair(uint32_t w, int i)
+    {
+        return ((i == 0 ? w << 4 : w >> (4 * i - 4)) & mask) | magic;
+    }
+};
+using MfmaV = Mfma<__bf16>;  // the values' product, whatever T is
+
+// What one workgroup of either attention kernel works on.
+struct Span {
+    int32_t n, nq, rows;   // keys and queries of the sequence, rows of its key head
+    int64_t q0;            // first query
+};
+__device__ inline Span span_of(const AttnArgs &a, int32_t b)
+{
+    Span s;
+    const int64_t cap = a.width * a.c.page;
+    const int64_t n = a.lens[b];
+    s.n = (int32_t)(n < 0 ? 0 : n > cap ? cap : n);
+    int64_t q0 = a.q_off[b], q1 = a.q_off[b + 1];
+    q0 = q0 < 0 ? 0 : q0 > a.total_q ? a.total_q : q0;
+    q1 = q1 < q0 ? q0 : q1 > a.total_q ? a.total_q : q1;
+    s.q0 = q0;
+    s.nq = (int32_t)(q1 - q0);
+    s.rows = s.nq * a.group;
+    return s;
+}
+__device__ inline int32_t key_hi(const AttnArgs &a, const Span &s, int32_t qi)
+{
+    return a.causal ? max(0, min(s.n, s.n - s.nq + qi + 1)) : s.n;
+}
+__device__ inline int32_t key_lo(const AttnArgs &a, const Span &s, int32_t qi)
+{
+    return a.window > 0 ? max(0, s.n - s.nq + qi + 1 - a.window) : 0;
+}
+
+__device__ inline float max_over_groups(float x)
+{
+    x = fmaxf(x, __shfl_xor(x, 16));
+    return fmaxf(x, __shfl_xor(x, 32));
+}
+__device__ inline float sum_over_groups(float x)
+{
+    x += __shfl_xor(x, 16);
+    return x + __shfl_xor(x, 32);
+}
+
+// Sixteen rows against a range of keys.  Each of the four waves takes blocks of
+// 32 keys (two half-blocks of 16, each inside one page) and keeps its own
+// maximum, sum and output; they meet in LDS.  Lane l = 16 c + r:
+//   scores    A: key r of a half-block, levels [c D/4, (c+1) D/4);  B: row r.
+//             It ends with keys 4c .. 4c+3 of each half-block for row r;
+//   values    those eight keys are its share of the contraction as they stand:
+//             B: their weights; A: their levels of dims r D/16 .. (r+1) D/16 - 1,
+//             one MFMA per dim.  It ends with dims (4c+i) D/16 + j of row r.
+// Neither the weights nor the values change lanes.
+template <class T, int D>
+__global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
+{
+    using MM = Mfma<T>;
+    constexpr int KW = D / 32;     // words of a key a lane reads, = MFMAs per half-block
+    constexpr int DPL = D / 16;    // dims of a value a lane reads, = MFMAs per block
+    constexpr int VW = DPL / 8 ? DPL / 8 : 1;
+    constexpr int LDO = D + 4;
+    __shared__ float osum[4 * 16 * LDO];
+    __shared__ float stat[4][16][4];
+    const uint32_t lane = threadIdx.x & 63u;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int32_t r = (int32_t)(lane & 15u), c = (int32_t)(lane >> 4);
+    const int32_t bh = (int32_t)(blockIdx.x / (uint32_t)a.tiles), tile = (int32_t)(blockIdx.x % (uint32_t)a.tiles);
+    const int32_t b = bh / a.c.heads, h = bh - b * a.c.heads;
+    const Span sp = span_of(a, b);
+    const int32_t r0 = tile * 16;
+    if (r0 >= sp.rows) return;
+
+    const int32_t row = min(r0 + r, sp.rows - 1);
+    const int32_t qi = row / a.group, hq = h * a.group + (row - qi * a.group);
+    const int32_t my_lo = key_lo(a, sp, qi), my_hi = key_hi(a, sp, qi);
+    const int32_t qi_first = r0 / a.group, qi_last = min(r0 + 15, sp.rows - 1) / a.group;
+    const int32_t lo = key_lo(a, sp, qi_first), hi = key_hi(a, sp, qi_last);
+    const int32_t full_lo = key_lo(a, sp, qi_last), full_hi = key_hi(a, sp, qi_first);
+    const int32_t b0 = lo / 32, nb = max(0, (hi + 31) / 32 - b0);
+    const int32_t per = (nb + a.splits - 1) / a.splits;
+    const int32_t first = b0 + (int32_t)blockIdx.y * per, last = min(b0 + nb, first + per);
+
+    // queries: element 2i of a fragment is level i of the word, 2i+1 level i+4
+    i32x4 qf[KW];
+    float qsum = 0.f;
+    {
+        const T *q = (const T *)a.q + (sp.q0 + qi) * a.ldq + (int64_t)hq * D + c * (D / 4);
+#pragma unroll
+        for (int j = 0; j < KW; ++j) {
+            const i32x4 w = *(const i32x4 *)(q + 8 * j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) qsum += lo_f32<T>((uint32_t)w[i]) + hi_f32<T>((uint32_t)w[i]);
+            const uint32_t w0 = (uint32_t)w.x, w1 = (uint32_t)w.y, w2 = (uint32_t)w.z, w3 = (uint32_t)w.w;
+            qf[j] = i32x4{(int)((w0 & 0xFFFFu) | (w2 << 16)), (int)((w0 >> 16) | (w2 & 0xFFFF0000u)),
+                          (int)((w1 & 0xFFFFu) | (w3 << 16)), (int)((w1 >> 16) | (w3 & 0xFFFF0000u))};
+        }
+        qsum = sum_over_groups(qsum);
+    }
+    const float start = -MM::base * qsum;
+
+    const float NEG = -__builtin_inff();
+    float m_run = NEG, l_run = 0.f, pm = 0.f;
+    f32x4 acc[DPL], ones = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < DPL; ++j) acc[j] = f32x4{0, 0, 0, 0};
+    const i32x4 one = {0x3F803F80, 0x3F803F80, 0x3F803F80, 0x3F803F80};
+
+    for (int32_t blk = first + (int32_t)wave; blk < last; blk += 4) {
+        const int32_t t0 = blk * 32;
+        int64_t vecs[2];
+        bool there[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int32_t t = t0 + 16 * s < hi ? t0 + 16 * s : t0;
+            const int32_t pi = t / a.c.page;
+            const int32_t p = __builtin_amdgcn_readfirstlane(a.table[(int64_t)b * a.ldt + pi]);
+            there[s] = (uint32_t)p < (uint32_t)a.c.pages;
+            vecs[s] = ((int64_t)(there[s] ? p : 0) * a.c.heads + h) * a.c.page + (t - pi * a.c.page);
+        }
+        uint32_t kw[2][KW], vw[8][VW];
+        u32x4 kp[2], vp[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const uint32_t *k = (const uint32_t *)(a.c.k + (vecs[s] + r) * (D / 2)) + c * KW;
+#pragma unroll
+            for (int j = 0; j < KW; ++j) kw[s][j] = k[j];
+            kp[s] = *(const u32x4 *)(a.c.kp + vecs[s] + 4 * c);
+            vp[s] = *(const u32x4 *)(a.c.vp + vecs[s] + 4 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint8_t *v = a.c.v + (vecs[s] + 4 * c + i) * (D / 2) + r * (DPL / 2);
+                if constexpr (DPL == 4) vw[4 * s + i][0] = *(const uint16_t *)v;
+                else
+#pragma unroll
+                    for (int j = 0; j < VW; ++j) vw[4 * s + i][j] = ((const uint32_t *)v)[j];
+            }
+        }
+        // scores
+        float sc[2][4];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            f32x4 x = {start, start, start, start};
+#pragma unroll
+            for (int j = 0; j < KW; ++j) {
+                const uint32_t w = kw[s][j];
+                x = MM::mul(i32x4{(int)MM::pair(w, 0), (int)MM::pair(w, 1), (int)MM::pair(w, 2), (int)MM::pair(w, 3)},
+                            qf[j], x);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                sc[s][i] = (lo_f32<T>(kp[s][i]) * x[i] + hi_f32<T>(kp[s][i]) * qsum) * a.scale2;
+        }
+        const bool whole = t0 >= full_lo && t0 + 32 <= full_hi && there[0] && there[1];
+        bool ok[2][4];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int32_t t = t0 + 16 * s + 4 * c + i;
+                ok[s][i] = whole || (there[s] && t >= my_lo && t < my_hi);
+                if (!ok[s][i]) sc[s][i] = NEG;
+            }
+        // running maximum: taken anew only when a score passes it by 2^8
+        float mx = sc[0][0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) mx = fmaxf(mx, sc[e / 4][e % 4]);
+        mx = max_over_groups(mx);
+        if (__any(mx > m_run + 8.f)) {
+            const float m_new = fmaxf(m_run, mx);
+            const float al = m_run == NEG ? 0.f : __builtin_amdgcn_exp2f(m_run - m_new);
+            m_run = m_new;
+            l_run *= al;
+            pm *= al;
+            ones *= al;
+#pragma unroll
+            for (int j = 0; j < DPL; ++j) acc[j] *= al;
+        }
+        const float m_use = m_run == NEG ? 0.f : m_run;
+        i32x4 whi, wlo;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            float w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float p = __builtin_amdgcn_exp2f(sc[s][i] - m_use);
+                const float vs = lo_f32<T>(vp[s][i]), vm = hi_f32<T>(vp[s][i]);
+                l_run += p;
+                pm += ok[s][i] ? p * (vm + 8.f * vs) : 0.f;
+                w[i] = ok[s][i] ? p * vs : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t hi2 = pack2<__bf16>(w[2 * i], w[2 * i + 1]);
+                whi[2 * s + i] = (int)hi2;
+                wlo[2 * s + i] = (int)pack2<__bf16>(w[2 * i] - lo_f32<__bf16>(hi2), w[2 * i + 1] - hi_f32<__bf16>(hi2));
+            }
+        }
+        // values
+        ones = MfmaV::mul(one, whi, ones);
+        ones = MfmaV::mul(one, wlo, ones);
+#pragma unroll
+        for (int v = 0; v < VW; ++v)
+#pragma unroll
+            for (int half = 0; half < (DPL == 4 ? 1 : 2); ++half) {
+                uint32_t x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t u0 = vw[2 * i][v], u1 = vw[2 * i + 1][v];
+                    x[i] = half ? (u0 >> 16) | (u1 & 0xFFFF0000u) : (u0 & 0xFFFFu) | (u1 << 16);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    i32x4 f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) f[i] = (int)MfmaV::pair(x[i], j);
+                    const int d = 8 * v + 4 * half + j;
+                    acc[d] = MfmaV::mul(f, whi, acc[d]);
+                    acc[d] = MfmaV::mul(f, wlo, acc[d]);
+                }
+            }
+    }
+
+    // the four waves' results
+    l_run = sum_over_groups(l_run);
+    pm = sum_over_groups(pm);
+    if (c == 0) {
+        stat[wave][r][0] = m_run;
+        stat[wave][r][1] = l_run;
+        stat[wave][r][2] = pm;
+    }
+    const float off = (MfmaV::base + 8.f) * ones.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < DPL; ++j)
+            osum[((int)wave * 16 + r) * LDO + (4 * c + i) * DPL + j] = acc[j][i] - off;
+    __syncthreads();
+    const int32_t orow = (int32_t)threadIdx.x / 16, oc = (int32_t)threadIdx.x % 16;
+    if (r0 + orow >= sp.rows) return;
+    float m = NEG;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) m = fmaxf(m, stat[w][orow][0]);
+    float o[DPL], l = 0.f, pmt = 0.f;
+#pragma unroll
+    for (int j = 0; j < DPL; ++j) o[j] = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        if (stat[w][orow][1] == 0.f) continue;  // nothing seen (a NaN score leaves a NaN sum)
+        const float f = __builtin_amdgcn_exp2f(stat[w][orow][0] - m);
+        l += f * stat[w][orow][1];
+        pmt += f * stat[w][orow][2];
+#pragma unroll
+        for (int j = 0; j < DPL; ++j) o[j] += f * osum[(w * 16 + orow) * LDO + oc * DPL + j];
+    }
+    const int32_t oq = (r0 + orow) / a.group, oh = h * a.group + (r0 + orow - oq * a.group);
+    const int64_t grow = (sp.q0 + oq) * (int64_t)(a.group * a.c.heads) + oh;
+    if (a.splits > 1) {
+        const int64_t nrows = a.total_q * (int64_t)(a.group * a.c.heads);
+        float *po = a.part + ((int64_t)blockIdx.y * nrows + grow) * D + oc * DPL;
+#pragma unroll
+        for (int j = 0; j < DPL; ++j) po[j] = o[j] + pmt;
+        if (oc == 0) {
+            float *ps = a.part + (int64_t)a.splits * nrows * D + ((int64_t)blockIdx.y * nrows + grow) * 2;
+            ps[0] = m;
+            ps[1] = l;
+        }
+        return;
+    }
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    T *po = (T *)a.out + (sp.q0 + oq) * a.ldo + (int64_t)oh * D + oc * DPL;
+#pragma unroll
+    for (int j = 0; j < DPL; ++j) po[j] = (T)((o[j] + pmt) * inv);
+    if (a.lse && oc == 0) a.lse[grow] = l == 0.f ? NEG : (m + __builtin_log2f(l)) * 0.6931471805599453f;
+}
+
+// The partial results of key ranges joined, in the ranges' order: 16 rows per
+// workgroup, 16 lanes per row.
+template <class T, int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int32_t row_tiles)
+{
+    constexpr int DPL = D / 16;
+    const int32_t bh = (int32_t)(blockIdx.x / (uint32_t)row_tiles), tile = (int32_t)(blockIdx.x % (uint32_t)row_tiles);
+    const int32_t b = bh / a.c.heads, h = bh - b * a.c.heads;
+    const Span sp = span_of(a, b);
+    const int32_t row = tile * 16 + (int32_t)threadIdx.x / 16, oc = (int32_t)threadIdx.x % 16;
+    if (row >= sp.rows) return;
+    const int32_t oq = row / a.group, oh = h * a.group + (row - oq * a.group);
+    const int64_t hq = (int64_t)a.group * a.c.heads, nrows = a.total_q * hq;
+    const int64_t grow = (sp.q0 + oq) * hq + oh;
+    const float *ps = a.part + (int64_t)a.splits * nrows * D + grow * 2;
+    const float NEG = -__builtin_inff();
+    float m = NEG;
+    for (int32_t s = 0; s < a.splits; ++s) m = fmaxf(m, ps[(int64_t)s * nrows * 2]);
+    float o[DPL], l = 0.f;
+#pragma unroll
+    for (int j = 0; j < DPL; ++j) o[j] = 0.f;
+    for (int32_t s = 0; s < a.splits; ++s) {
+        const float ls = ps[(int64_t)s * nrows * 2 + 1];
+        if (ls == 0.f) continue;
+        const float f = __builtin_amdgcn_exp2f(ps[(int64_t)s * nrows * 2] - m);
+        l += f * ls;
+        const float *po = a.part + ((int64_t)s * nrows + grow) * D + oc * DPL;
+#pragma unroll
+        for (int j = 0; j < DPL; ++j) o[j] += f * po[j];
+    }
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    T *out = (T *)a.out + (sp.q0 + oq) * a.ldo + (int64_t)oh * D + oc * DPL;
+#pragma unroll
+    for (int j = 0; j < DPL; ++j) out[j] = (T)(o[j] * inv);
+    if (a.lse && oc == 0) a.lse[grow] = l == 0.f ? NEG : (m + __builtin_log2f(l)) * 0.6931471805599453f;
+}
+
+template <class T, int D> static hipError_t attn_rows_t(const AttnArgs &a, hipStream_t s)
+{
+    const int64_t wgs = (int64_t)a.batch * a.c.heads * a.tiles;
+    if (wgs > 0x7FFFFFFF) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((attn_rows_kernel<T, D>), dim3((uint32_t)wgs, (uint32_t)a.splits), dim3(256), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.splits == 1) return e;
+    hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3((uint32_t)wgs), dim3(256), 0, s, a, a.tiles);
+    return hipGetLastError();
+}
+
+hipError_t launch_attn_rows(int ftype, int D, const AttnArgs &a, hipStream_t s)
+{
+#define CALL(TY, DD) attn_rows_t<TY, DD>(a, s)
+    LB_KV4_BY_TYPE(CALL)
+#undef CALL
+}
+
+}  // namespace lb

@@ -81,7 +81,8 @@ typedef enum {
     LB_ERR_VARIANT = 4,  /* variant outside LB_AUTO..8, or dtype unknown */
     LB_ERR_OVERFLOW = 5, /* K above the type's limit (the exact int32 sum must fit);
                             convolutions: also 32-bit offset range */
-    LB_ERR_HIP = 6       /* the HIP runtime reported an error */
+    LB_ERR_HIP = 6,      /* the HIP runtime reported an error */
+    LB_ERR_WORKSPACE = 7 /* the workspace is smaller than the call needs */
 } lb_status;
 
 typedef enum { LB_S8 = 0, LB_S4 = 1, LB_B1 = 2 } lb_dtype;
@@ -217,6 +218,120 @@ int lb_select_variant(int dtype, int64_t M, int64_t N, int64_t K, int cu_count,
 #define LB_PLAN_LINEAR 3
 int lb_auto_plan(int op, int64_t M, int64_t N, int64_t K, int cu_count, int *launches,
                  int *tile_m, int *tile_n, int *k_bands);
+
+/*
+ * Serving operators: what a decoder layer with int8 weights and a 4-bit cache
+ * needs around the int8 product.  Activations, keys, values and outputs are of
+ * one floating type, an lb_ftype (a 16-bit one for the cache and the attention).
+ * Conventions as above (device pointers, caller-owned buffers, asynchronous on
+ * the stream, statuses; nothing is allocated or kept between calls), and:
+ *   - every data pointer is 16-byte aligned, and strides between rows or tokens
+ *     are in elements and keep rows 16-byte aligned (LB_ERR_ALIGN otherwise);
+ *   - a workspace is scratch memory of the caller, 256-byte aligned, whose
+ *     contents need not survive between calls; two calls that may run at the
+ *     same time need one each.
+ */
+typedef enum { LB_BF16 = 0, LB_F16 = 1, LB_F32 = 2 } lb_ftype;
+
+/*
+ * Rows of X quantised to int8, a scale for each row (token):
+ *   amax = max_k |X[m,k]|,  sx[m] = amax / 127 (fp32),
+ *   Q[m,k] = 127 X[m,k] / amax rounded to the nearest integer, ties to even.
+ * The rounding is that of the exact quotient.  A row of zeros gets scale 0; a
+ * row that holds an infinity or a NaN gets that as its scale and Q = 0, so that
+ * what is computed from it is NaN.  ldx: elements between rows (>= K).
+ * K % LB_S8_K_ALIGN == 0, K <= LB_S8_K_MAX.  Q: M x K dense, sx: M.
+ */
+int lb_quant_rows_s8(const void *X, int64_t ldx, int8_t *Q, float *sx, int64_t M, int64_t K, int ftype,
+                     void *stream);
+
+/*
+ * The int8 product with both scales, a bias and a floating output:
+ *   out[m,n] = ((float)acc[m,n] * sx[m]) * sw[n] + bias[n],
+ * acc exact in int32, the rest in fp32, rounded once to ftype.  bias: N values
+ * of ftype, or NULL.  X: M x K int8, W: N x K int8 (nn.Linear's [N, K]); sizes
+ * and K as for lb_gemm_s8.  Tiles are chosen as lb_gemm_s8_linear's automatic
+ * choice does, except that few rows (at most 64) have a kernel of their own.
+ */
+int lb_gemm_s8_scaled(const int8_t *X, const int8_t *W, const float *sx, const float *sw, const void *bias,
+                      void *out, int64_t M, int64_t N, int64_t K, int ftype, void *stream);
+
+/*
+ * The linear layer on floating activations: lb_quant_rows_s8 of X, then
+ * lb_gemm_s8_scaled; X, bias and out are of ftype.  workspace: at least
+ * lb_linear_w8a8_workspace(M, K, N) bytes (LB_ERR_WORKSPACE otherwise).
+ */
+int lb_linear_w8a8(const void *X, int64_t ldx, const int8_t *W, const float *sw, const void *bias, void *out,
+                   int64_t M, int64_t N, int64_t K, int ftype, void *workspace, int64_t workspace_bytes,
+                   void *stream);
+/* Workspace bytes of lb_linear_w8a8; 0 for sizes that it refuses. */
+int64_t lb_linear_w8a8_workspace(int64_t M, int64_t K, int64_t N);
+
+/*
+ * A paged cache of keys and values in 4 bits.  The D numbers x of one token and
+ * key head are held as levels u in 0..15, a scale s and a minimum m, both of the
+ * cache's 16-bit type:
+ *   m = min x,  s = (max x - m) / 15 (fp32, rounded to the type),
+ *   u = (x - m) / s rounded to the nearest integer, ties to even, at most 15
+ *       (0 where s = 0),
+ * and stand for u s + m.  Numbers that are not finite (or whose range is beyond
+ * fp32) make the whole vector stand for NaN.
+ *   Kc, Vc: pages x heads x page x D/2 bytes, even d in the low nibble;
+ *   Kp, Vp: pages x heads x page x 2 of the type, (s, m) of each vector.
+ * Token slot i is position i % page of page i / page.  D is 64, 128 or 256;
+ * page is a multiple of 16; pages * page < 2^31 (the cache may pass 4 GiB).
+ */
+#define LB_KV4_PAGE_ALIGN 16
+
+/*
+ * T new tokens into their slots.  K, V: T tokens ldk / ldv elements apart, each
+ * heads x D dense (a slice of a fused projection's rows has ldk > heads * D).
+ * slots: T int64, one per token and all different; a slot outside the cache
+ * (a padding token's -1) is skipped.
+ */
+int lb_kv4_write(const void *K, const void *V, int64_t ldk, int64_t ldv, const int64_t *slots, uint8_t *Kc,
+                 uint8_t *Vc, void *Kp, void *Vp, int64_t T, int64_t heads, int64_t D, int64_t pages,
+                 int64_t page, int ftype, void *stream);
+/* T slots' keys and values out again: K, V: T x heads x D dense.  A slot outside
+ * the cache reads as zeros. */
+int lb_kv4_read(const uint8_t *Kc, const uint8_t *Vc, const void *Kp, const void *Vp, const int64_t *slots,
+                void *K, void *V, int64_t T, int64_t heads, int64_t D, int64_t pages, int64_t page, int ftype,
+                void *stream);
+
+/*
+ * Attention of the last queries of each of B sequences over their pages.
+ *   Q, out: total_q x Hq x D (tokens ldq / ldo elements apart, each Hq x D dense);
+ *   sequence b holds rows q_off[b] .. q_off[b+1] - 1 (q_off: B + 1 int32, not
+ *   decreasing), which are its last ones: query i of nq stands at position
+ *   lens[b] - nq + i.  lens: B int32 keys in the cache, the queries' own included.
+ *   table: B rows of table_width int32 page numbers, ldt apart; key t is in
+ *   page table[b][t / page].  Head j of Q reads key head j / (Hq / Hkv).
+ * A query sees the keys up to its own position (causal != 0) or all of them,
+ * and with window > 0 only those less than window before it.  A query that sees
+ * none (an empty sequence, a position before the first key) gets zeros, and
+ * -infinity in lse.  lse (total_q x Hq fp32, or NULL): log of the sum of
+ * exp(scale * q . k).  scale multiplies the scores.
+ * Keys whose page number lies outside the cache are not seen; lens beyond the
+ * table's width count as its width.  Rows of Q outside every sequence are left
+ * as they are.
+ *   max_q, max_len: at least the longest nq (LB_ERR_SHAPE if below 1; rows past
+ *   it may be left as they are) and, for the planning alone, about the longest
+ *   lens.  workspace: partial results of key ranges, which few rows are split
+ *   into; with fewer than lb_attn_kv4_workspace() bytes (0 and NULL too) fewer
+ *   ranges are made.  The ranges are joined in a fixed order: the same arguments
+ *   give the same bits.
+ */
+int lb_attn_kv4(const void *Q, int64_t ldq, const uint8_t *Kc, const uint8_t *Vc, const void *Kp,
+                const void *Vp, const int32_t *table, int64_t ldt, int64_t table_width, const int32_t *q_off,
+                const int32_t *lens, void *out, int64_t ldo, float *lse, int64_t B, int64_t total_q,
+                int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D, int64_t pages, int64_t page,
+                int64_t max_len, float scale, int64_t window, int causal, int ftype, void *workspace,
+                int64_t workspace_bytes, void *stream);
+/* Workspace bytes that let lb_attn_kv4 split the keys as it likes (on a GPU of
+ * cu_count compute units; <= 0 asks the current device); 0 for sizes that it
+ * refuses. */
+int64_t lb_attn_kv4_workspace(int64_t B, int64_t total_q, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D,
+                              int64_t max_len, int64_t window, int cu_count);
 
 /* Hash of the source files this library was built from (16 hex digits, static
  * storage; never NULL).  The build stamps it in, so that a caller can check a
