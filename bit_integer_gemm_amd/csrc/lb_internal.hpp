@@ -95,10 +95,11 @@ struct AttnArgs {
     Kv4Cache c;
     int64_t ldq, ldo, ldt, width;
     int64_t total_q;
-    int32_t group, batch, window, causal, splits, tiles;
+    int32_t group, batch, window, causal, splits;
+    int32_t chunk, tiles; // which kernel: 128 rows per workgroup, or 16; and how many such tiles a key head has
     float scale2;         // softmax scale * log2(e)
 };
-hipError_t launch_attn_rows(int ftype, int D, const AttnArgs &a, hipStream_t s);
+hipError_t launch_attn(int ftype, int D, const AttnArgs &a, hipStream_t s);
 
 // Measured selection table lookup (host only).
 int select_from_table(int dtype, int64_t M, int64_t N, int64_t K, int cu_count, int *best,

@@ -253,40 +253,31 @@ __device__ inline f32x4 mfma_fp4(i32x4 b, i32x4 a, f32x4 c)
 // Store of the scaled product (KIND_SCALED): four consecutive columns of a row
 // as ((float)acc * sx[m]) * sw[n] + bias[n] in fp32, rounded once to the output
 // type.  o: element offset of the first; left: columns from it to N; vec: all
-// four exist and the row stride keeps them aligned.
+// four exist and the row stride keeps them aligned.  (The type is a template
+// parameter of the kernel: chosen at run time inside the unrolled epilogue, its
+// three copies of every store cost 90 us of 350 at 8192 x 11008 x 4096.)
 template <class T>
-__device__ inline void store_scaled_t(const ScaledOut &so, void *out, int64_t o, int64_t n, int64_t left,
-                                      bool vec, f32x4 v)
+__device__ inline void store_scaled(const T *bias, T *out, int64_t o, int64_t n, int64_t left, bool vec, f32x4 v)
 {
     typedef T t4 __attribute__((ext_vector_type(4)));
     if (vec) {
-        if (so.bias) {
-            const t4 b = *(const t4 *)((const T *)so.bias + n);
+        if (bias) {
+            const t4 b = *(const t4 *)(bias + n);
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[r] += (float)b[r];
         }
-        *(t4 *)((T *)out + o) = t4{(T)v.x, (T)v.y, (T)v.z, (T)v.w};
+        *(t4 *)(out + o) = t4{(T)v.x, (T)v.y, (T)v.z, (T)v.w};
     } else {
-        for (int r = 0; r < 4 && r < left; ++r) {
-            const float b = so.bias ? (float)((const T *)so.bias)[n + r] : 0.f;
-            ((T *)out)[o + r] = (T)(so.bias ? v[r] + b : v[r]);
-        }
+        for (int r = 0; r < 4 && r < left; ++r) out[o + r] = (T)(bias ? v[r] + (float)bias[n + r] : v[r]);
     }
 }
-__device__ inline void store_scaled(const ScaledOut &so, void *out, int64_t o, int64_t n, int64_t left,
-                                    bool vec, f32x4 v)
-{
-    if (so.ftype == LB_BF16) store_scaled_t<__bf16>(so, out, o, n, left, vec, v);
-    else if (so.ftype == LB_F16) store_scaled_t<_Float16>(so, out, o, n, left, vec, v);
-    else store_scaled_t<float>(so, out, o, n, left, vec, v);
-}
 
-template <class C, int KIND, bool CONV>
+template <class C, int KIND, bool CONV, class T = float>
 __device__ __forceinline__ void mfma_gemm_tile(
     const int8_t *__restrict__ A, const int8_t *__restrict__ B, void *__restrict__ out,
     const float *__restrict__ sx, const float *__restrict__ sw,
     int32_t M, int32_t N, int32_t Kb, uint32_t tiles_m, uint32_t tiles_n, int32_t ldo,
-    int32_t ksplit, const ConvGeom &g, const ScaledOut &so)
+    int32_t ksplit, const ConvGeom &g, const T *__restrict__ bias)
 {
     // Linear layer: the tile's row and column scales follow the stage ring
     // (medium and large tiles; the small tile keeps its five workgroups per CU
@@ -632,7 +623,7 @@ __device__ __forceinline__ void mfma_gemm_tile(
                     const float s = LDS_SCALES ? lds_sw[n - n0 + e] : n + e < N ? sw[n + e] : 0.f;
                     r[e] = ((float)v[e] * scale_m) * s;
                 }
-                store_scaled(so, out, m * (int64_t)ldo + n, n, N - n, vec_ok, r);
+                store_scaled<T>(bias, (T *)out, m * (int64_t)ldo + n, n, N - n, vec_ok, r);
             } else if constexpr (KIND == KIND_LINEAR) {
                 float *o = (float *)out + m * (int64_t)ldo + n;
                 if (vec_ok) {
@@ -668,15 +659,15 @@ __global__ __launch_bounds__(C::NT) void mfma_gemm_kernel(
     int32_t M, int32_t N, int32_t Kb, uint32_t tiles_m, uint32_t tiles_n, int32_t ldo,
     int32_t ksplit, ConvGeom g)
 {
-    mfma_gemm_tile<C, KIND, CONV>(A, B, out, sx, sw, M, N, Kb, tiles_m, tiles_n, ldo, ksplit, g, ScaledOut{});
+    mfma_gemm_tile<C, KIND, CONV>(A, B, out, sx, sw, M, N, Kb, tiles_m, tiles_n, ldo, ksplit, g, (const float *)nullptr);
 }
-template <class C>
+template <class C, class T>
 __global__ __launch_bounds__(C::NT) void scaled_gemm_kernel(
     const int8_t *__restrict__ A, const int8_t *__restrict__ B, void *__restrict__ out,
     const float *__restrict__ sx, const float *__restrict__ sw,
-    int32_t M, int32_t N, int32_t Kb, uint32_t tiles_m, uint32_t tiles_n, int32_t ldo, ScaledOut so)
+    int32_t M, int32_t N, int32_t Kb, uint32_t tiles_m, uint32_t tiles_n, int32_t ldo, const T *__restrict__ bias)
 {
-    mfma_gemm_tile<C, KIND_SCALED, false>(A, B, out, sx, sw, M, N, Kb, tiles_m, tiles_n, ldo, Kb, ConvGeom{}, so);
+    mfma_gemm_tile<C, KIND_SCALED, false, T>(A, B, out, sx, sw, M, N, Kb, tiles_m, tiles_n, ldo, Kb, ConvGeom{}, bias);
 }
 
 // ---- large tile on four waves (int8, int4, 1-bit, int8 linear) ----------
@@ -761,12 +752,12 @@ __device__ constexpr int spread_item(int s)
 // block's fragment reads are spread over a half-block's MFMA slots by
 // spread_item; for 8 x 8 that is the fixed pattern of one copy per four slots
 // and one read per two.
-template <int KIND, int FM, int FN>
+template <int KIND, int FM, int FN, class T = float>
 __device__ __forceinline__ void mfma_w4_tile(
     const int8_t *__restrict__ A, const int8_t *__restrict__ B, void *__restrict__ out,
     const float *__restrict__ sx, const float *__restrict__ sw,
     int32_t M, int32_t N, int32_t Kb, uint32_t tiles_m, uint32_t tiles_n, int32_t ldo, int32_t ksplit,
-    const ScaledOut &so)
+    const T *__restrict__ bias)
 {
     constexpr bool SCALES = KIND == KIND_LINEAR || KIND == KIND_SCALED;
     static_assert(FM % 2 == 0 && FM >= 4 && FM <= 8 && FN % 2 == 0 && FN >= 4 && FN <= 8, "wave sub-tile");
@@ -1315,7 +1306,7 @@ __device__ __forceinline__ void mfma_w4_tile(
                 f32x4 r;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) r[e] = ((float)v[e] * scale_m) * s[e];
-                store_scaled(so, out, m * (int64_t)ldo + n, n, N - n, vec_ok, r);
+                store_scaled<T>(bias, (T *)out, m * (int64_t)ldo + n, n, N - n, vec_ok, r);
             } else if constexpr (KIND == KIND_LINEAR) {
                 float *o = (float *)out + m * (int64_t)ldo + n;
                 if (vec_ok) {
@@ -1349,15 +1340,15 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     const float *__restrict__ sx, const float *__restrict__ sw,
     int32_t M, int32_t N, int32_t Kb, uint32_t tiles_m, uint32_t tiles_n, int32_t ldo, int32_t ksplit)
 {
-    mfma_w4_tile<KIND, FM, FN>(A, B, out, sx, sw, M, N, Kb, tiles_m, tiles_n, ldo, ksplit, ScaledOut{});
+    mfma_w4_tile<KIND, FM, FN>(A, B, out, sx, sw, M, N, Kb, tiles_m, tiles_n, ldo, ksplit, (const float *)nullptr);
 }
-template <int FM, int FN>
+template <int FM, int FN, class T>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void scaled_w4_tile_kernel(
     const int8_t *__restrict__ A, const int8_t *__restrict__ B, void *__restrict__ out,
     const float *__restrict__ sx, const float *__restrict__ sw,
-    int32_t M, int32_t N, int32_t Kb, uint32_t tiles_m, uint32_t tiles_n, int32_t ldo, ScaledOut so)
+    int32_t M, int32_t N, int32_t Kb, uint32_t tiles_m, uint32_t tiles_n, int32_t ldo, const T *__restrict__ bias)
 {
-    mfma_w4_tile<KIND_SCALED, FM, FN>(A, B, out, sx, sw, M, N, Kb, tiles_m, tiles_n, ldo, Kb, so);
+    mfma_w4_tile<KIND_SCALED, FM, FN, T>(A, B, out, sx, sw, M, N, Kb, tiles_m, tiles_n, ldo, Kb, bias);
 }
 
 template <int KIND, int FM, int FN>
@@ -1543,43 +1534,55 @@ hipError_t launch_conv(int kind, int variant, const void *X, const void *F, int3
 }
 
 // The scaled product: each variant's tile as the linear layer has it.
-template <class C>
+template <class C, class T>
 static hipError_t launch_scaled_one(const int8_t *A, const int8_t *B, void *out, const float *sx, const float *sw,
-                                    int64_t M, int64_t N, int64_t K, int64_t ldo, const ScaledOut &so, hipStream_t s)
+                                    int64_t M, int64_t N, int64_t K, int64_t ldo, const void *bias, hipStream_t s)
 {
     const uint64_t tm = (uint64_t)((M + C::BM - 1) / C::BM), tn = (uint64_t)((N + C::BN - 1) / C::BN);
     if (tm * tn > 0x7FFFFFFFull) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((scaled_gemm_kernel<C>), dim3((uint32_t)(tm * tn)), dim3(C::NT), 0, s, A, B, out, sx, sw,
-                       (int32_t)M, (int32_t)N, (int32_t)K, (uint32_t)tm, (uint32_t)tn, (int32_t)ldo, so);
+    hipLaunchKernelGGL((scaled_gemm_kernel<C, T>), dim3((uint32_t)(tm * tn)), dim3(C::NT), 0, s, A, B, out, sx, sw,
+                       (int32_t)M, (int32_t)N, (int32_t)K, (uint32_t)tm, (uint32_t)tn, (int32_t)ldo, (const T *)bias);
     return hipGetLastError();
 }
-template <int FM, int FN>
+template <int FM, int FN, class T>
 static hipError_t launch_scaled_w4(const int8_t *A, const int8_t *B, void *out, const float *sx, const float *sw,
-                                   int64_t M, int64_t N, int64_t K, int64_t ldo, const ScaledOut &so, hipStream_t s)
+                                   int64_t M, int64_t N, int64_t K, int64_t ldo, const void *bias, hipStream_t s)
 {
     constexpr int64_t BM = 32 * FM, BN = 32 * FN;
     const uint64_t tm = (uint64_t)((M + BM - 1) / BM), tn = (uint64_t)((N + BN - 1) / BN);
     if (tm * tn > 0x7FFFFFFFull) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((scaled_w4_tile_kernel<FM, FN>), dim3((uint32_t)(tm * tn)), dim3(256), 0, s, A, B, out, sx, sw,
-                       (int32_t)M, (int32_t)N, (int32_t)K, (uint32_t)tm, (uint32_t)tn, (int32_t)ldo, so);
+    hipLaunchKernelGGL((scaled_w4_tile_kernel<FM, FN, T>), dim3((uint32_t)(tm * tn)), dim3(256), 0, s, A, B, out, sx, sw,
+                       (int32_t)M, (int32_t)N, (int32_t)K, (uint32_t)tm, (uint32_t)tn, (int32_t)ldo, (const T *)bias);
     return hipGetLastError();
+}
+
+template <class T>
+static hipError_t launch_scaled_t(int variant, const int8_t *A, const int8_t *B, void *out, const float *sx, const float *sw,
+                         int64_t M, int64_t N, int64_t K, int64_t ldo, const void *bias, hipStream_t s)
+{
+    switch (variant) {
+    case 0: return launch_scaled_one<S2, T>(A, B, out, sx, sw, M, N, K, ldo, bias, s);
+    case 1: return launch_scaled_one<S3, T>(A, B, out, sx, sw, M, N, K, ldo, bias, s);
+    case 2: return launch_scaled_one<S4, T>(A, B, out, sx, sw, M, N, K, ldo, bias, s);
+    case 3: return launch_scaled_one<M2, T>(A, B, out, sx, sw, M, N, K, ldo, bias, s);
+    case 4: return launch_scaled_one<M3, T>(A, B, out, sx, sw, M, N, K, ldo, bias, s);
+    case 5: return launch_scaled_one<M4, T>(A, B, out, sx, sw, M, N, K, ldo, bias, s);
+    case 6: return launch_scaled_w4<8, 8, T>(A, B, out, sx, sw, M, N, K, ldo, bias, s);
+    case 7: return launch_scaled_one<L3W8, T>(A, B, out, sx, sw, M, N, K, ldo, bias, s);
+    case 8: return launch_scaled_one<L4W16, T>(A, B, out, sx, sw, M, N, K, ldo, bias, s);
+    case W4_256x192: return launch_scaled_w4<8, 6, T>(A, B, out, sx, sw, M, N, K, ldo, bias, s);
+    case W4_192x256: return launch_scaled_w4<6, 8, T>(A, B, out, sx, sw, M, N, K, ldo, bias, s);
+    default: return hipErrorInvalidValue;
+    }
 }
 
 hipError_t launch_scaled(int variant, const int8_t *A, const int8_t *B, void *out, const float *sx, const float *sw,
                          int64_t M, int64_t N, int64_t K, int64_t ldo, const ScaledOut &so, hipStream_t s)
 {
-    switch (variant) {
-    case 0: return launch_scaled_one<S2>(A, B, out, sx, sw, M, N, K, ldo, so, s);
-    case 1: return launch_scaled_one<S3>(A, B, out, sx, sw, M, N, K, ldo, so, s);
-    case 2: return launch_scaled_one<S4>(A, B, out, sx, sw, M, N, K, ldo, so, s);
-    case 3: return launch_scaled_one<M2>(A, B, out, sx, sw, M, N, K, ldo, so, s);
-    case 4: return launch_scaled_one<M3>(A, B, out, sx, sw, M, N, K, ldo, so, s);
-    case 5: return launch_scaled_one<M4>(A, B, out, sx, sw, M, N, K, ldo, so, s);
-    case 6: return launch_scaled_w4<8, 8>(A, B, out, sx, sw, M, N, K, ldo, so, s);
-    case 7: return launch_scaled_one<L3W8>(A, B, out, sx, sw, M, N, K, ldo, so, s);
-    case 8: return launch_scaled_one<L4W16>(A, B, out, sx, sw, M, N, K, ldo, so, s);
-    case W4_256x192: return launch_scaled_w4<8, 6>(A, B, out, sx, sw, M, N, K, ldo, so, s);
-    case W4_192x256: return launch_scaled_w4<6, 8>(A, B, out, sx, sw, M, N, K, ldo, so, s);
+    switch (so.ftype) {
+    case LB_BF16: return launch_scaled_t<__bf16>(variant, A, B, out, sx, sw, M, N, K, ldo, so.bias, s);
+    case LB_F16: return launch_scaled_t<_Float16>(variant, A, B, out, sx, sw, M, N, K, ldo, so.bias, s);
+    case LB_F32: return launch_scaled_t<float>(variant, A, B, out, sx, sw, M, N, K, ldo, so.bias, s);
     default: return hipErrorInvalidValue;
     }
 }

@@ -64,6 +64,7 @@ lb::Kv4Cache cache_of(const uint8_t *Kc, const uint8_t *Vc, const void *Kp, cons
 }
 
 struct AttnPlan {
+    bool chunk;
     int64_t tiles, splits, per_split;   // row tiles of a key head; key ranges; workspace bytes per range
 };
 
@@ -72,7 +73,10 @@ AttnPlan plan_attn(int64_t B, int64_t total_q, int64_t max_q, int64_t Hq, int64_
 {
     AttnPlan p;
     const int64_t group = Hq / Hkv;
-    p.tiles = (max_q * group + 15) / 16;
+    // Many rows of a key head share its keys through LDS; few would leave most of
+    // that kernel's 128 rows empty.
+    p.chunk = max_q * group > 32;
+    p.tiles = p.chunk ? (max_q * group + 127) / 128 : (max_q * group + 15) / 16;
     int64_t keys = max_len;
     if (window > 0) keys = std::min(keys, window + max_q);
     const int64_t wgs = B * Hkv * p.tiles;
@@ -235,9 +239,10 @@ int lb_attn_kv4(const void *Q, int64_t ldq, const uint8_t *Kc, const uint8_t *Vc
     a.window = (int32_t)window;
     a.causal = causal != 0;
     a.splits = (int32_t)splits;
+    a.chunk = p.chunk;
     a.tiles = (int32_t)p.tiles;
     a.scale2 = scale * 1.44269504088896340736f;
-    return finish(lb::launch_attn_rows(ftype, (int)D, a, (hipStream_t)stream));
+    return finish(lb::launch_attn(ftype, (int)D, a, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -204,6 +204,15 @@ template <> struct Mfma<_Float16> {
 };
 using MfmaV = Mfma<__bf16>;  // the values' product, whatever T is
 
+// Eight numbers of a query in the order of a word's nibble pairs: element 2i is
+// number i, element 2i+1 number i+4.
+__device__ inline i32x4 query_order(i32x4 w)
+{
+    const uint32_t w0 = (uint32_t)w.x, w1 = (uint32_t)w.y, w2 = (uint32_t)w.z, w3 = (uint32_t)w.w;
+    return i32x4{(int)((w0 & 0xFFFFu) | (w2 << 16)), (int)((w0 >> 16) | (w2 & 0xFFFF0000u)),
+                 (int)((w1 & 0xFFFFu) | (w3 << 16)), (int)((w1 >> 16) | (w3 & 0xFFFF0000u))};
+}
+
 // What one workgroup of either attention kernel works on.
 struct Span {
     int32_t n, nq, rows;   // keys and queries of the sequence, rows of its key head
@@ -281,7 +290,6 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
     const int32_t per = (nb + a.splits - 1) / a.splits;
     const int32_t first = b0 + (int32_t)blockIdx.y * per, last = min(b0 + nb, first + per);
 
-    // queries: element 2i of a fragment is level i of the word, 2i+1 level i+4
     i32x4 qf[KW];
     float qsum = 0.f;
     {
@@ -291,9 +299,7 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
             const i32x4 w = *(const i32x4 *)(q + 8 * j);
 #pragma unroll
             for (int i = 0; i < 4; ++i) qsum += lo_f32<T>((uint32_t)w[i]) + hi_f32<T>((uint32_t)w[i]);
-            const uint32_t w0 = (uint32_t)w.x, w1 = (uint32_t)w.y, w2 = (uint32_t)w.z, w3 = (uint32_t)w.w;
-            qf[j] = i32x4{(int)((w0 & 0xFFFFu) | (w2 << 16)), (int)((w0 >> 16) | (w2 & 0xFFFF0000u)),
-                          (int)((w1 & 0xFFFFu) | (w3 << 16)), (int)((w1 >> 16) | (w3 & 0xFFFF0000u))};
+            qf[j] = query_order(w);
         }
         qsum = sum_over_groups(qsum);
     }
@@ -474,6 +480,414 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
     if (a.lse && oc == 0) a.lse[grow] = l == 0.f ? NEG : (m + __builtin_log2f(l)) * 0.6931471805599453f;
 }
 
+// ---- many rows -------------------------------------------------------------
+// 32 rows per wave, 128 per workgroup, against tiles of 64 keys that the four
+// waves turn from nibbles into matrix operands once, in LDS, for all of them
+// (16 rows per wave, each turning its own, spends half its instructions there).
+// The lanes' shares of a tile are attn_rows_kernel's: keys as the A operand with
+// the levels exact, so that a score is (s acc + m sum q) with per-key s and m;
+// a wave's weights are already the B operand of the values' product.
+//
+// Two tiles in LDS: while one is multiplied the next one's nibbles are on their
+// way to registers; they are turned and written after it, one barrier a tile.
+// Rows are padded by 16 bytes (keys: D numbers of a key; values: 64 keys of a
+// dim), which spreads eight lanes' 16-byte pieces over all banks.
+//
+// The values' product, by type:
+//   bf16  values are made whole, u s + m, in fp16 scaled by one power of two for
+//         the workgroup (2^vexp brings the largest |m| + 16 s of its keys to about
+//         2^10, found by a pass over their scales first), and weights are fp16:
+//         both are off by 2^-12, an eighth of the output's own rounding, and a
+//         value 2^-24 of the largest still counts.  A value vector that is not
+//         finite is left out of the product and its rows are made NaN apart.
+//   fp16  that would be as coarse as the output: levels stay exact and the weights
+//         p s go in two bf16 parts, as in attn_rows_kernel.
+template <class T, int D> struct ChunkTile {
+    static constexpr bool WHOLE = __is_same(T, __bf16);
+    static constexpr int KROW = 2 * D + 16, VROW = 144;
+    static constexpr int V_AT = 64 * KROW, P_AT = V_AT + D * VROW;
+    static constexpr int BYTES = P_AT + (WHOLE ? 2 : 4) * 256;
+};
+
+template <class T, int D>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnArgs a)
+{
+    using MM = Mfma<T>;
+    using LT = ChunkTile<T, D>;
+    constexpr bool WHOLE = LT::WHOLE;
+    constexpr int KW = D / 32;      // words of a key a lane turns, = MFMAs per 16 keys
+    constexpr int DPT = D / 32;     // dims of eight keys a lane turns
+    constexpr int ND = D / 16;      // 16-dim fragments of the output
+    __shared__ __attribute__((aligned(16))) char smem[2 * LT::BYTES];
+    __shared__ uint32_t red[4];
+    const uint32_t lane = threadIdx.x & 63u;
+    const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int32_t r = (int32_t)(lane & 15u), c = (int32_t)(lane >> 4);
+    // the last rows of a sequence see the most keys: they start first
+    const int32_t heads = a.batch * a.c.heads;
+    const int32_t bh = (int32_t)(blockIdx.x % (uint32_t)heads), tile = a.tiles - 1 - (int32_t)(blockIdx.x / (uint32_t)heads);
+    const int32_t b = bh / a.c.heads, h = bh - b * a.c.heads;
+    const Span sp = span_of(a, b);
+    const int32_t r0 = tile * 128;
+    if (r0 >= sp.rows) return;
+
+    // key range of the workgroup, of this wave, and of each of its lanes' two rows
+    const int32_t lo = key_lo(a, sp, r0 / a.group), hi = key_hi(a, sp, min(r0 + 127, sp.rows - 1) / a.group);
+    const int32_t t_first = lo / 64, nt = max(0, (hi + 63) / 64 - t_first);
+    const int32_t per = (nt + a.splits - 1) / a.splits;
+    const int32_t first = t_first + (int32_t)blockIdx.y * per, last = min(t_first + nt, first + per);
+    const int32_t w0 = r0 + 32 * wave;
+    const bool busy = w0 < sp.rows;
+    const int32_t wf = min(w0, sp.rows - 1) / a.group, wl = min(w0 + 31, sp.rows - 1) / a.group;
+    const int32_t wlo = key_lo(a, sp, wf), whi = busy ? key_hi(a, sp, wl) : 0;
+    const int32_t full_lo = key_lo(a, sp, wl), full_hi = key_hi(a, sp, wf);
+    int32_t my_lo[2], my_hi[2];
+    i32x4 qf[2][KW];
+    float qsum[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int32_t row = min(w0 + 16 * x + r, sp.rows - 1);
+        const int32_t qi = row / a.group, hq = h * a.group + (row - qi * a.group);
+        my_lo[x] = key_lo(a, sp, qi);
+        my_hi[x] = key_hi(a, sp, qi);
+        const T *q = (const T *)a.q + (sp.q0 + qi) * a.ldq + (int64_t)hq * D + c * (D / 4);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < KW; ++j) {
+            const i32x4 w = *(const i32x4 *)(q + 8 * j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum += lo_f32<T>((uint32_t)w[i]) + hi_f32<T>((uint32_t)w[i]);
+            qf[x][j] = query_order(w);
+        }
+        qsum[x] = sum_over_groups(sum);
+    }
+
+    // 2^vexp for the values of this key range
+    float vscale = 1.f;
+    bool odd = false;   // some value vector of the range is not finite
+    if constexpr (WHOLE) {
+        uint32_t mx = 0;
+        for (int32_t t = first * 64 + 4 * (int32_t)threadIdx.x; t < min(last * 64, hi); t += 1024) {
+            const int32_t pi = t / a.c.page, p = a.table[(int64_t)b * a.ldt + pi];
+            if ((uint32_t)p >= (uint32_t)a.c.pages) continue;
+            const u32x4 w = *(const u32x4 *)(a.c.vp + ((int64_t)p * a.c.heads + h) * a.c.page + (t - pi * a.c.page));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // a quarter of |m| + 16 s: cannot overflow for finite vectors
+                const float g = 0.25f * __builtin_fabsf(hi_f32<T>(w[i])) + 4.f * lo_f32<T>(w[i]);
+                const uint32_t bits = __float_as_uint(g);
+                if (t + i < hi) {
+                    if (bits < 0x7F800000u) mx = max(mx, bits);
+                    else odd = true;
+                }
+            }
+        }
+#pragma unroll
+        for (int d = 32; d; d >>= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, d));
+        if (__any(odd)) mx |= 0x80000000u;
+        if (lane == 0) red[wave] = mx;
+        __syncthreads();
+        odd = ((red[0] | red[1] | red[2] | red[3]) & 0x80000000u) != 0;
+        mx = max(max(red[0] & 0x7FFFFFFFu, red[1] & 0x7FFFFFFFu), max(red[2] & 0x7FFFFFFFu, red[3] & 0x7FFFFFFFu));
+        // the largest quarter comes to 2^8 .. 2^9; 2^125 at most, whose reciprocal is a normal number
+        const uint32_t e = min(254u + 8u - (mx >> 23), 252u);
+        vscale = __uint_as_float(e << 23);
+    }
+
+    // What a thread turns: key 16 wave + r, levels [c D/4, (c+1) D/4); and of the
+    // values eight keys, 4 vc + i of the half-blocks 2 kb and 2 kb + 1, dims vd ..
+    const int32_t kb = wave >> 1, vc = (int32_t)(lane & 3u), vd = ((wave & 1) * 16 + (int32_t)(lane >> 2)) * DPT;
+    uint32_t kw[KW], vw[8], kpw = 0, vpw = 0;
+    u32x4 vp[2];
+    uint32_t there = 0, there_next = 0;   // half-blocks whose page exists
+    auto fetch = [&](int32_t t) {
+        there_next = 0;
+        int64_t vec[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int32_t tg = 64 * t + 16 * g < hi ? 64 * t + 16 * g : 64 * t;
+            const int32_t pi = tg / a.c.page;
+            const int32_t p = __builtin_amdgcn_readfirstlane(a.table[(int64_t)b * a.ldt + pi]);
+            const bool ok = (uint32_t)p < (uint32_t)a.c.pages;
+            there_next |= ok ? 1u << g : 0u;
+            vec[g] = ((int64_t)(ok ? p : 0) * a.c.heads + h) * a.c.page + (tg - pi * a.c.page);
+        }
+        const int64_t mine = wave == 0 ? vec[0] : wave == 1 ? vec[1] : wave == 2 ? vec[2] : vec[3];
+        const uint32_t *k = (const uint32_t *)(a.c.k + (mine + r) * (D / 2)) + c * KW;
+#pragma unroll
+        for (int j = 0; j < KW; ++j) kw[j] = k[j];
+        if (c == 0) {
+            kpw = a.c.kp[mine + r];
+            if constexpr (!WHOLE) vpw = a.c.vp[mine + r];
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int64_t at = kb == 0 ? vec[s] : vec[2 + s];
+            if constexpr (WHOLE) vp[s] = *(const u32x4 *)(a.c.vp + at + 4 * vc);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint8_t *v = a.c.v + (at + 4 * vc + i) * (D / 2) + vd / 2;
+                if constexpr (DPT == 2) vw[4 * s + i] = *v;
+                else if constexpr (DPT == 4) vw[4 * s + i] = *(const uint16_t *)v;
+                else vw[4 * s + i] = *(const uint32_t *)v;
+            }
+        }
+    };
+    auto turn = [&](int32_t t, char *buf) {
+        there = there_next;
+        char *krow = buf + (16 * wave + r) * LT::KROW + c * (D / 2);
+#pragma unroll
+        for (int j = 0; j < KW; ++j)
+            *(i32x4 *)(krow + 16 * j) = i32x4{(int)MM::pair(kw[j], 0), (int)MM::pair(kw[j], 1),
+                                              (int)MM::pair(kw[j], 2), (int)MM::pair(kw[j], 3)};
+        float *prm = (float *)(buf + LT::P_AT);
+        if (c == 0) {
+            prm[16 * wave + r] = lo_f32<T>(kpw) * a.scale2;
+            prm[64 + 16 * wave + r] = hi_f32<T>(kpw) * a.scale2;
+            if constexpr (!WHOLE) {
+                prm[128 + 16 * wave + r] = lo_f32<T>(vpw);
+                prm[192 + 16 * wave + r] = hi_f32<T>(vpw) + 8.f * lo_f32<T>(vpw);
+            }
+        }
+        uint32_t sc[4], of[4];
+        if constexpr (WHOLE) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                float vs[4], vm[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float s0 = lo_f32<T>(vp[s][i]), m0 = hi_f32<T>(vp[s][i]);
+                    // keys past the range and vectors that are not finite count as zeros
+                    const bool in = 64 * t + 32 * kb + 16 * s + 4 * vc + i < hi && ((there >> (2 * kb + s)) & 1u) &&
+                                    0.25f * __builtin_fabsf(m0) + 4.f * s0 < __builtin_inff();
+                    vs[i] = in ? s0 * vscale : 0.f;
+                    vm[i] = in ? (m0 + 8.f * s0) * vscale : 0.f;
+                }
+                sc[2 * s] = pack2<_Float16>(vs[0], vs[1]);
+                sc[2 * s + 1] = pack2<_Float16>(vs[2], vs[3]);
+                of[2 * s] = pack2<_Float16>(vm[0], vm[1]);
+                of[2 * s + 1] = pack2<_Float16>(vm[2], vm[3]);
+            }
+        }
+#pragma unroll
+        for (int half = 0; half < (DPT == 8 ? 2 : 1); ++half) {
+            uint32_t x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x[i] = half ? (vw[2 * i] >> 16) | (vw[2 * i + 1] & 0xFFFF0000u)
+                            : (vw[2 * i] & 0xFFFFu) | (vw[2 * i + 1] << 16);
+#pragma unroll
+            for (int j = 0; j < (DPT == 2 ? 2 : 4); ++j) {
+                i32x4 f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (WHOLE) {
+                        const f16x2 u = __builtin_bit_cast(f16x2, Mfma<_Float16>::pair(x[i], j)) - (_Float16)72.f;
+                        f[i] = __builtin_bit_cast(int, __builtin_elementwise_fma(
+                                   u, __builtin_bit_cast(f16x2, sc[i]), __builtin_bit_cast(f16x2, of[i])));
+                    } else {
+                        f[i] = (int)MfmaV::pair(x[i], j);
+                    }
+                }
+                *(i32x4 *)(buf + LT::V_AT + (vd + 4 * half + j) * LT::VROW + kb * 64 + vc * 16) = f;
+            }
+        }
+    };
+
+    const float NEG = -__builtin_inff();
+    float m_run[2] = {NEG, NEG}, l_run[2] = {0.f, 0.f}, extra[2] = {0.f, 0.f};
+    f32x4 acc[2][ND], ones[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        ones[x] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int d = 0; d < ND; ++d) acc[x][d] = f32x4{0, 0, 0, 0};
+    }
+    const i32x4 one = {0x3F803F80, 0x3F803F80, 0x3F803F80, 0x3F803F80};
+
+    if (first < last) {
+        fetch(first);
+        turn(first, smem);
+    }
+    uint32_t ok_pages = there;
+    __syncthreads();
+    for (int32_t t = first; t < last; ++t) {
+        const char *buf = smem + ((t - first) & 1) * LT::BYTES;
+        if (t + 1 < last) fetch(t + 1);
+        const int32_t t0 = 64 * t;
+        if (t0 < whi && t0 + 64 > wlo) {
+            const bool whole = t0 >= full_lo && t0 + 64 <= full_hi && ok_pages == 15u;
+            const float *prm = (const float *)(buf + LT::P_AT) + 4 * c;
+            float sc[2][4][4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                f32x4 z[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float start = -MM::base * qsum[x];
+                    z[x] = f32x4{start, start, start, start};
+                }
+                const char *k = buf + (16 * g + r) * LT::KROW + c * (D / 2);
+#pragma unroll
+                for (int j = 0; j < KW; ++j) {
+                    const i32x4 kf = *(const i32x4 *)(k + 16 * j);
+                    z[0] = MM::mul(kf, qf[0][j], z[0]);
+                    z[1] = MM::mul(kf, qf[1][j], z[1]);
+                }
+                const f32x4 ks = *(const f32x4 *)(prm + 16 * g), km = *(const f32x4 *)(prm + 64 + 16 * g);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sc[x][g][i] = ks[i] * z[x][i] + km[i] * qsum[x];
+            }
+            uint32_t seen[2] = {0xFFFFu, 0xFFFFu};
+            if (!whole) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    seen[x] = 0;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int32_t key = t0 + 16 * g + 4 * c + i;
+                            const bool ok = key >= my_lo[x] && key < my_hi[x] && ((ok_pages >> g) & 1u);
+                            seen[x] |= ok ? 1u << (4 * g + i) : 0u;
+                            if (!ok) sc[x][g][i] = NEG;
+                        }
+                }
+            }
+            if constexpr (WHOLE)
+                if (odd) {
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int32_t key = t0 + 16 * g + 4 * c + i;
+                            if (key >= hi || !((ok_pages >> g) & 1u)) continue;
+                            const int32_t pi = key / a.c.page;
+                            const int64_t at = ((int64_t)a.table[(int64_t)b * a.ldt + pi] * a.c.heads + h) * a.c.page +
+                                               (key - pi * a.c.page);
+                            const uint32_t w = a.c.vp[at];
+                            const float gsum = 0.25f * __builtin_fabsf(hi_f32<T>(w)) + 4.f * lo_f32<T>(w);
+                            if (!(gsum < __builtin_inff()))
+#pragma unroll
+                                for (int x = 0; x < 2; ++x)
+                                    if ((seen[x] >> (4 * g + i)) & 1u) extra[x] = __builtin_nanf("");
+                        }
+                }
+            i32x4 whi[2][2], wlo2[2][2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float mx = sc[x][0][0];
+#pragma unroll
+                for (int e = 1; e < 16; ++e) mx = fmaxf(mx, sc[x][e / 4][e % 4]);
+                mx = max_over_groups(mx);
+                if (__any(mx > m_run[x] + 8.f)) {
+                    const float m_new = fmaxf(m_run[x], mx);
+                    const float al = m_run[x] == NEG ? 0.f : __builtin_amdgcn_exp2f(m_run[x] - m_new);
+                    m_run[x] = m_new;
+                    l_run[x] *= al;
+                    if constexpr (!WHOLE) {
+                        extra[x] *= al;
+                        ones[x] *= al;
+                    }
+#pragma unroll
+                    for (int d = 0; d < ND; ++d) acc[x][d] *= al;
+                }
+                const float m_use = m_run[x] == NEG ? 0.f : m_run[x];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    float w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        w[i] = __builtin_amdgcn_exp2f(sc[x][g][i] - m_use);
+                        l_run[x] += w[i];
+                    }
+                    if constexpr (WHOLE) {
+                        whi[x][g / 2][2 * (g % 2)] = (int)pack2<_Float16>(w[0], w[1]);
+                        whi[x][g / 2][2 * (g % 2) + 1] = (int)pack2<_Float16>(w[2], w[3]);
+                    } else {
+                        const f32x4 vs = *(const f32x4 *)(prm + 128 + 16 * g), vm = *(const f32x4 *)(prm + 192 + 16 * g);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const bool ok = (seen[x] >> (4 * g + i)) & 1u;
+                            extra[x] += ok ? w[i] * vm[i] : 0.f;
+                            w[i] = ok ? w[i] * vs[i] : 0.f;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t hi2 = pack2<__bf16>(w[2 * i], w[2 * i + 1]);
+                            whi[x][g / 2][2 * (g % 2) + i] = (int)hi2;
+                            wlo2[x][g / 2][2 * (g % 2) + i] = (int)pack2<__bf16>(w[2 * i] - lo_f32<__bf16>(hi2),
+                                                                                 w[2 * i + 1] - hi_f32<__bf16>(hi2));
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const char *v = buf + LT::V_AT + r * LT::VROW + q * 64 + c * 16;
+                if constexpr (!WHOLE) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        ones[x] = MfmaV::mul(one, whi[x][q], ones[x]);
+                        ones[x] = MfmaV::mul(one, wlo2[x][q], ones[x]);
+                    }
+                }
+#pragma unroll
+                for (int d = 0; d < ND; ++d) {
+                    const i32x4 vf = *(const i32x4 *)(v + 16 * d * LT::VROW);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if constexpr (WHOLE) {
+                            acc[x][d] = Mfma<_Float16>::mul(vf, whi[x][q], acc[x][d]);
+                        } else {
+                            acc[x][d] = MfmaV::mul(vf, whi[x][q], acc[x][d]);
+                            acc[x][d] = MfmaV::mul(vf, wlo2[x][q], acc[x][d]);
+                        }
+                    }
+                }
+            }
+        }
+        if (t + 1 < last) turn(t + 1, smem + ((t + 1 - first) & 1) * LT::BYTES);
+        ok_pages = there;
+        __syncthreads();
+    }
+
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int32_t row = w0 + 16 * x + r;
+        float l = sum_over_groups(l_run[x]);
+        float add = WHOLE ? extra[x] : sum_over_groups(extra[x]);
+        if constexpr (WHOLE) add += __shfl_xor(add, 16), add += __shfl_xor(add, 32);  // 0, or NaN in any
+        if (row >= sp.rows) continue;
+        const float mul = WHOLE ? 1.f / vscale : 1.f;
+        const float off = WHOLE ? -add : (MfmaV::base + 8.f) * ones[x].x - add;
+        const int32_t oq = row / a.group, oh = h * a.group + (row - oq * a.group);
+        const int64_t hq = (int64_t)a.group * a.c.heads, grow = (sp.q0 + oq) * hq + oh;
+        if (a.splits > 1) {
+            const int64_t nrows = a.total_q * hq;
+            float *po = a.part + ((int64_t)blockIdx.y * nrows + grow) * D + 4 * c;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) *(f32x4 *)(po + 16 * d) = acc[x][d] * mul - off;
+            if (c == 0) {
+                float *ps = a.part + (int64_t)a.splits * nrows * D + ((int64_t)blockIdx.y * nrows + grow) * 2;
+                ps[0] = m_run[x];
+                ps[1] = l;
+            }
+            continue;
+        }
+        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        T *po = (T *)a.out + (sp.q0 + oq) * a.ldo + (int64_t)oh * D + 4 * c;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+            const f32x4 o = acc[x][d] * mul - off;
+            *(u32x2 *)(po + 16 * d) = u32x2{pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv)};
+        }
+        if (a.lse && c == 0) a.lse[grow] = l == 0.f ? NEG : (m_run[x] + __builtin_log2f(l)) * 0.6931471805599453f;
+    }
+}
+
 // The partial results of key ranges joined, in the ranges' order: 16 rows per
 // workgroup, 16 lanes per row.
 template <class T, int D>
@@ -511,20 +925,26 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int32_t row_
     if (a.lse && oc == 0) a.lse[grow] = l == 0.f ? NEG : (m + __builtin_log2f(l)) * 0.6931471805599453f;
 }
 
-template <class T, int D> static hipError_t attn_rows_t(const AttnArgs &a, hipStream_t s)
+template <class T, int D> static hipError_t attn_t(const AttnArgs &a, hipStream_t s)
 {
     const int64_t wgs = (int64_t)a.batch * a.c.heads * a.tiles;
     if (wgs > 0x7FFFFFFF) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((attn_rows_kernel<T, D>), dim3((uint32_t)wgs, (uint32_t)a.splits), dim3(256), 0, s, a);
+    if (a.chunk)
+        hipLaunchKernelGGL((attn_chunk_kernel<T, D>), dim3((uint32_t)wgs, (uint32_t)a.splits), dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((attn_rows_kernel<T, D>), dim3((uint32_t)wgs, (uint32_t)a.splits), dim3(256), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
-    hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3((uint32_t)wgs), dim3(256), 0, s, a, a.tiles);
+    const int64_t row_tiles = a.chunk ? 8 * (int64_t)a.tiles : a.tiles;
+    if ((int64_t)a.batch * a.c.heads * row_tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3((uint32_t)(a.batch * a.c.heads * row_tiles)), dim3(256), 0, s, a,
+                       (int32_t)row_tiles);
     return hipGetLastError();
 }
 
-hipError_t launch_attn_rows(int ftype, int D, const AttnArgs &a, hipStream_t s)
+hipError_t launch_attn(int ftype, int D, const AttnArgs &a, hipStream_t s)
 {
-#define CALL(TY, DD) attn_rows_t<TY, DD>(a, s)
+#define CALL(TY, DD) attn_t<TY, DD>(a, s)
     LB_KV4_BY_TYPE(CALL)
 #undef CALL
 }
