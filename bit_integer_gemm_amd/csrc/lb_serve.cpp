@@ -74,9 +74,9 @@ AttnPlan plan_attn(int64_t B, int64_t total_q, int64_t max_q, int64_t Hq, int64_
     AttnPlan p;
     const int64_t group = Hq / Hkv;
     // Many rows of a key head share its keys through LDS; few would leave most of
-    // that kernel's 128 rows empty.
+    // that kernel's 256 rows empty.
     p.chunk = max_q * group > 32;
-    p.tiles = p.chunk ? (max_q * group + 127) / 128 : (max_q * group + 15) / 16;
+    p.tiles = p.chunk ? (max_q * group + (D == 256 ? 127 : 255)) / (D == 256 ? 128 : 256) : (max_q * group + 15) / 16;
     int64_t keys = max_len;
     if (window > 0) keys = std::min(keys, window + max_q);
     const int64_t wgs = B * Hkv * p.tiles;
@@ -241,6 +241,12 @@ int lb_attn_kv4(const void *Q, int64_t ldq, const uint8_t *Kc, const uint8_t *Vc
     a.splits = (int32_t)splits;
     a.chunk = p.chunk;
     a.tiles = (int32_t)p.tiles;
+    // key / page = mulhi(key, mul) >> shift with 2^shift the power of two below page:
+    // mul = ceil(2^(32 + shift) / page) < 2^32, and mul page - 2^(32 + shift) < page
+    // <= 2^(shift + 1), so the quotient is exact for keys below 2^31.
+    a.page_shift = 31 - (uint32_t)__builtin_clz((uint32_t)page);
+    if ((page & (page - 1)) == 0) --a.page_shift;
+    a.page_mul = (uint32_t)((((uint64_t)1 << (32 + a.page_shift)) + (uint64_t)page - 1) / (uint64_t)page);
     a.scale2 = scale * 1.44269504088896340736f;
     return finish(lb::launch_attn(ftype, (int)D, a, (hipStream_t)stream));
 }

@@ -232,6 +232,12 @@ __device__ inline Span span_of(const AttnArgs &a, int32_t b)
     s.rows = s.nq * a.group;
     return s;
 }
+// key / page by a multiplication: exact for keys below 2^31 (page_mul is
+// 2^(32 + page_shift) / page rounded up).
+__device__ inline int32_t page_of(const AttnArgs &a, int32_t key)
+{
+    return (int32_t)(__umulhi((uint32_t)key, a.page_mul) >> a.page_shift);
+}
 __device__ inline int32_t key_hi(const AttnArgs &a, const Span &s, int32_t qi)
 {
     return a.causal ? max(0, min(s.n, s.n - s.nq + qi + 1)) : s.n;
@@ -319,7 +325,7 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const int32_t t = t0 + 16 * s < hi ? t0 + 16 * s : t0;
-            const int32_t pi = t / a.c.page;
+            const int32_t pi = page_of(a, t);
             const int32_t p = __builtin_amdgcn_readfirstlane(a.table[(int64_t)b * a.ldt + pi]);
             there[s] = (uint32_t)p < (uint32_t)a.c.pages;
             vecs[s] = ((int64_t)(there[s] ? p : 0) * a.c.heads + h) * a.c.page + (t - pi * a.c.page);
@@ -481,17 +487,21 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
 }
 
 // ---- many rows -------------------------------------------------------------
-// 32 rows per wave, 128 per workgroup, against tiles of 64 keys that the four
+// 32 rows per wave, 256 per workgroup (D = 256: 16 and 128, whose outputs are as
+// many registers), against tiles of 64 keys that the eight
 // waves turn from nibbles into matrix operands once, in LDS, for all of them
-// (16 rows per wave, each turning its own, spends half its instructions there).
+// (16 rows per wave, each turning its own, spends half its instructions there):
+// waves 0-3 the keys, waves 4-7 the values.
 // The lanes' shares of a tile are attn_rows_kernel's: keys as the A operand with
 // the levels exact, so that a score is (s acc + m sum q) with per-key s and m;
 // a wave's weights are already the B operand of the values' product.
 //
 // Two tiles in LDS: while one is multiplied the next one's nibbles are on their
 // way to registers; they are turned and written after it, one barrier a tile.
-// Rows are padded by 16 bytes (keys: D numbers of a key; values: 64 keys of a
-// dim), which spreads eight lanes' 16-byte pieces over all banks.
+// The numbers of its page come a tile earlier still.  A fragment read takes 16
+// lanes' 16-byte pieces at a time, so piece p of row n (keys: D numbers of a key;
+// values: 64 keys of a dim) lies at p ^ (n % 16 or n % 8) of its row: 4 cycles a
+// read, counted, where rows padded by 16 bytes took 8 (and every write 8).
 //
 // The values' product, by type:
 //   bf16  values are made whole, u s + m, in fp16 scaled by one power of two for
@@ -503,23 +513,40 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
 //   fp16  that would be as coarse as the output: levels stay exact and the weights
 //         p s go in two bf16 parts, as in attn_rows_kernel.
 template <class T, int D> struct ChunkTile {
+    static constexpr int RX = D == 256 ? 1 : 2;   // 16-row fragments per wave
+    static constexpr int ROWS = 8 * 16 * RX;
     static constexpr bool WHOLE = __is_same(T, __bf16);
-    static constexpr int KROW = 2 * D + 16, VROW = 144;
+    static constexpr int KROW = 2 * D, VROW = 128;
     static constexpr int V_AT = 64 * KROW, P_AT = V_AT + D * VROW;
-    static constexpr int BYTES = P_AT + (WHOLE ? 2 : 4) * 256;
+    // per-key numbers: scale and minimum of keys (fp32), of values (fp16 or fp32)
+    static constexpr int BYTES = P_AT + (WHOLE ? 3 : 4) * 256;
+    // byte of piece 4 j + c of key n, and of piece 4 q + c of dim n
+    static __device__ inline int key_at(int n, int j, int c)
+    {
+        return n * KROW + 16 * ((4 * j + c) ^ (n & (D == 64 ? 7 : 15)));
+    }
+    static __device__ inline int val_at(int n, int q, int c) { return V_AT + n * VROW + 16 * ((4 * q + c) ^ (n & 7)); }
 };
 
+// A page number of the table, by a scalar load.
+__device__ inline int32_t page_number(const AttnArgs &a, int32_t b, int32_t key)
+{
+    typedef const __attribute__((address_space(4))) int32_t *const_ptr;
+    return ((const_ptr)(uintptr_t)(a.table + (int64_t)b * a.ldt))[page_of(a, key)];
+}
+
 template <class T, int D>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnArgs a)
+__global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
 {
     using MM = Mfma<T>;
     using LT = ChunkTile<T, D>;
     constexpr bool WHOLE = LT::WHOLE;
+    constexpr int RX = LT::RX;
     constexpr int KW = D / 32;      // words of a key a lane turns, = MFMAs per 16 keys
     constexpr int DPT = D / 32;     // dims of eight keys a lane turns
     constexpr int ND = D / 16;      // 16-dim fragments of the output
     __shared__ __attribute__((aligned(16))) char smem[2 * LT::BYTES];
-    __shared__ uint32_t red[4];
+    __shared__ uint32_t red[8];
     const uint32_t lane = threadIdx.x & 63u;
     const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int32_t r = (int32_t)(lane & 15u), c = (int32_t)(lane >> 4);
@@ -528,24 +555,24 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnA
     const int32_t bh = (int32_t)(blockIdx.x % (uint32_t)heads), tile = a.tiles - 1 - (int32_t)(blockIdx.x / (uint32_t)heads);
     const int32_t b = bh / a.c.heads, h = bh - b * a.c.heads;
     const Span sp = span_of(a, b);
-    const int32_t r0 = tile * 128;
+    const int32_t r0 = tile * LT::ROWS;
     if (r0 >= sp.rows) return;
 
     // key range of the workgroup, of this wave, and of each of its lanes' two rows
-    const int32_t lo = key_lo(a, sp, r0 / a.group), hi = key_hi(a, sp, min(r0 + 127, sp.rows - 1) / a.group);
+    const int32_t lo = key_lo(a, sp, r0 / a.group), hi = key_hi(a, sp, min(r0 + LT::ROWS - 1, sp.rows - 1) / a.group);
     const int32_t t_first = lo / 64, nt = max(0, (hi + 63) / 64 - t_first);
     const int32_t per = (nt + a.splits - 1) / a.splits;
     const int32_t first = t_first + (int32_t)blockIdx.y * per, last = min(t_first + nt, first + per);
-    const int32_t w0 = r0 + 32 * wave;
+    const int32_t w0 = r0 + 16 * RX * wave;
     const bool busy = w0 < sp.rows;
-    const int32_t wf = min(w0, sp.rows - 1) / a.group, wl = min(w0 + 31, sp.rows - 1) / a.group;
+    const int32_t wf = min(w0, sp.rows - 1) / a.group, wl = min(w0 + 16 * RX - 1, sp.rows - 1) / a.group;
     const int32_t wlo = key_lo(a, sp, wf), whi = busy ? key_hi(a, sp, wl) : 0;
     const int32_t full_lo = key_lo(a, sp, wl), full_hi = key_hi(a, sp, wf);
-    int32_t my_lo[2], my_hi[2];
-    i32x4 qf[2][KW];
-    float qsum[2];
+    int32_t my_lo[RX], my_hi[RX];
+    i32x4 qf[RX][KW];
+    float qsum[RX];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < RX; ++x) {
         const int32_t row = min(w0 + 16 * x + r, sp.rows - 1);
         const int32_t qi = row / a.group, hq = h * a.group + (row - qi * a.group);
         my_lo[x] = key_lo(a, sp, qi);
@@ -567,8 +594,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnA
     bool odd = false;   // some value vector of the range is not finite
     if constexpr (WHOLE) {
         uint32_t mx = 0;
-        for (int32_t t = first * 64 + 4 * (int32_t)threadIdx.x; t < min(last * 64, hi); t += 1024) {
-            const int32_t pi = t / a.c.page, p = a.table[(int64_t)b * a.ldt + pi];
+        for (int32_t t = first * 64 + 4 * (int32_t)threadIdx.x; t < min(last * 64, hi); t += 2048) {
+            const int32_t pi = page_of(a, t), p = a.table[(int64_t)b * a.ldt + pi];
             if ((uint32_t)p >= (uint32_t)a.c.pages) continue;
             const u32x4 w = *(const u32x4 *)(a.c.vp + ((int64_t)p * a.c.heads + h) * a.c.page + (t - pi * a.c.page));
 #pragma unroll
@@ -587,86 +614,112 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnA
         if (__any(odd)) mx |= 0x80000000u;
         if (lane == 0) red[wave] = mx;
         __syncthreads();
-        odd = ((red[0] | red[1] | red[2] | red[3]) & 0x80000000u) != 0;
-        mx = max(max(red[0] & 0x7FFFFFFFu, red[1] & 0x7FFFFFFFu), max(red[2] & 0x7FFFFFFFu, red[3] & 0x7FFFFFFFu));
+        mx = 0;
+        odd = false;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            odd |= (red[w] >> 31) != 0;
+            mx = max(mx, red[w] & 0x7FFFFFFFu);
+        }
         // the largest quarter comes to 2^8 .. 2^9; 2^125 at most, whose reciprocal is a normal number
         const uint32_t e = min(254u + 8u - (mx >> 23), 252u);
         vscale = __uint_as_float(e << 23);
     }
 
-    // What a thread turns: key 16 wave + r, levels [c D/4, (c+1) D/4); and of the
-    // values eight keys, 4 vc + i of the half-blocks 2 kb and 2 kb + 1, dims vd ..
-    const int32_t kb = wave >> 1, vc = (int32_t)(lane & 3u), vd = ((wave & 1) * 16 + (int32_t)(lane >> 2)) * DPT;
+    // What a thread turns.  Waves 0-3: key 16 part + r, levels [c D/4, (c+1) D/4).
+    // Waves 4-7: eight keys' values, 4 vc + i of the half-blocks 2 kb and 2 kb + 1,
+    // dims vd .. vd + DPT - 1.
+    const bool keys = wave < 4;
+    const int32_t part = wave & 3, kb = part >> 1;
+    const int32_t vc = (int32_t)(lane & 3u), vd = ((part & 1) * 16 + (int32_t)(lane >> 2)) * DPT;
     uint32_t kw[KW], vw[8], kpw = 0, vpw = 0;
-    u32x4 vp[2];
-    uint32_t there = 0, there_next = 0;   // half-blocks whose page exists
-    auto fetch = [&](int32_t t) {
-        there_next = 0;
-        int64_t vec[4];
+    // Half-blocks of tile t, t + 1 and t + 2: first vector of each, whether its page
+    // exists, and page numbers on their way.
+    int64_t vec[4], vec1[4];
+    int32_t page2[4];
+    uint32_t there = 0, there1 = 0;
+    auto half_key = [&](int32_t t, int g) { return 64 * t + 16 * g < hi ? 64 * t + 16 * g : max(hi - 1, 0) / 16 * 16; };
+    auto ask = [&](int32_t t) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) page2[g] = page_number(a, b, half_key(t, g));
+    };
+    auto advance = [&](int32_t t) {   // page2 holds tile t's numbers
+        there = there1;
+        there1 = 0;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            const int32_t tg = 64 * t + 16 * g < hi ? 64 * t + 16 * g : 64 * t;
-            const int32_t pi = tg / a.c.page;
-            const int32_t p = __builtin_amdgcn_readfirstlane(a.table[(int64_t)b * a.ldt + pi]);
+            vec[g] = vec1[g];
+            const int32_t tg = half_key(t, g), p = page2[g];
             const bool ok = (uint32_t)p < (uint32_t)a.c.pages;
-            there_next |= ok ? 1u << g : 0u;
-            vec[g] = ((int64_t)(ok ? p : 0) * a.c.heads + h) * a.c.page + (tg - pi * a.c.page);
+            there1 |= ok ? 1u << g : 0u;
+            vec1[g] = ((int64_t)(ok ? p : 0) * a.c.heads + h) * a.c.page + (tg - page_of(a, tg) * a.c.page);
         }
-        const int64_t mine = wave == 0 ? vec[0] : wave == 1 ? vec[1] : wave == 2 ? vec[2] : vec[3];
-        const uint32_t *k = (const uint32_t *)(a.c.k + (mine + r) * (D / 2)) + c * KW;
+    };
+    auto of_part = [&](const int64_t *v) { return part == 0 ? v[0] : part == 1 ? v[1] : part == 2 ? v[2] : v[3]; };
+    // tile t's nibbles, and the values' scales of tile t + 1 (WHOLE: turned a tile
+    // before the values)
+    auto fetch = [&]() {
+        if (keys) {
+            const int64_t mine = of_part(vec);
+            const uint32_t *k = (const uint32_t *)(a.c.k + (mine + r) * (D / 2)) + c * KW;
 #pragma unroll
-        for (int j = 0; j < KW; ++j) kw[j] = k[j];
-        if (c == 0) {
-            kpw = a.c.kp[mine + r];
-            if constexpr (!WHOLE) vpw = a.c.vp[mine + r];
-        }
+            for (int j = 0; j < KW; ++j) kw[j] = k[j];
+            if (c == 0) {
+                kpw = a.c.kp[mine + r];
+                vpw = a.c.vp[(WHOLE ? of_part(vec1) : mine) + r];
+            }
+        } else {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int64_t at = kb == 0 ? vec[s] : vec[2 + s];
-            if constexpr (WHOLE) vp[s] = *(const u32x4 *)(a.c.vp + at + 4 * vc);
+            for (int s = 0; s < 2; ++s) {
+                const int64_t at = kb == 0 ? vec[s] : vec[2 + s];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint8_t *v = a.c.v + (at + 4 * vc + i) * (D / 2) + vd / 2;
-                if constexpr (DPT == 2) vw[4 * s + i] = *v;
-                else if constexpr (DPT == 4) vw[4 * s + i] = *(const uint16_t *)v;
-                else vw[4 * s + i] = *(const uint32_t *)v;
+                for (int i = 0; i < 4; ++i) {
+                    const uint8_t *v = a.c.v + (at + 4 * vc + i) * (D / 2) + vd / 2;
+                    if constexpr (DPT == 2) vw[4 * s + i] = *v;
+                    else if constexpr (DPT == 4) vw[4 * s + i] = *(const uint16_t *)v;
+                    else vw[4 * s + i] = *(const uint32_t *)v;
+                }
             }
         }
     };
-    auto turn = [&](int32_t t, char *buf) {
-        there = there_next;
-        char *krow = buf + (16 * wave + r) * LT::KROW + c * (D / 2);
+    // WHOLE: scale and (minimum + 8 scales) of key 16 part + r of a tile, in fp16; a
+    // key past the range, on a page that is not there, or whose vector is not finite
+    // counts as zeros.
+    auto turn_scales = [&](int32_t t, uint32_t pages_there, char *buf) {
+        const float s0 = lo_f32<T>(vpw), m0 = hi_f32<T>(vpw);
+        const bool in = 64 * t + 16 * part + r < hi && ((pages_there >> part) & 1u) &&
+                        0.25f * __builtin_fabsf(m0) + 4.f * s0 < __builtin_inff();
+        _Float16 *prm = (_Float16 *)(buf + LT::P_AT + 512) + 16 * part + r;
+        prm[0] = (_Float16)(in ? s0 * vscale : 0.f);
+        prm[64] = (_Float16)(in ? (m0 + 8.f * s0) * vscale : 0.f);
+    };
+    auto turn = [&](int32_t t, char *buf, char *other) {
+        if (keys) {
 #pragma unroll
-        for (int j = 0; j < KW; ++j)
-            *(i32x4 *)(krow + 16 * j) = i32x4{(int)MM::pair(kw[j], 0), (int)MM::pair(kw[j], 1),
-                                              (int)MM::pair(kw[j], 2), (int)MM::pair(kw[j], 3)};
-        float *prm = (float *)(buf + LT::P_AT);
-        if (c == 0) {
-            prm[16 * wave + r] = lo_f32<T>(kpw) * a.scale2;
-            prm[64 + 16 * wave + r] = hi_f32<T>(kpw) * a.scale2;
-            if constexpr (!WHOLE) {
-                prm[128 + 16 * wave + r] = lo_f32<T>(vpw);
-                prm[192 + 16 * wave + r] = hi_f32<T>(vpw) + 8.f * lo_f32<T>(vpw);
+            for (int j = 0; j < KW; ++j)
+                *(i32x4 *)(buf + LT::key_at(16 * part + r, j, c)) =
+                    i32x4{(int)MM::pair(kw[j], 0), (int)MM::pair(kw[j], 1), (int)MM::pair(kw[j], 2),
+                          (int)MM::pair(kw[j], 3)};
+            float *prm = (float *)(buf + LT::P_AT) + 16 * part + r;
+            if (c == 0) {
+                prm[0] = lo_f32<T>(kpw) * a.scale2;
+                prm[64] = hi_f32<T>(kpw) * a.scale2;
+                if constexpr (WHOLE) {
+                    turn_scales(t + 1, there1, other);
+                } else {
+                    prm[128] = lo_f32<T>(vpw);
+                    prm[192] = hi_f32<T>(vpw) + 8.f * lo_f32<T>(vpw);
+                }
             }
+            return;
         }
-        uint32_t sc[4], of[4];
+        u32x2 sc[2], of[2];
         if constexpr (WHOLE) {
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                float vs[4], vm[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float s0 = lo_f32<T>(vp[s][i]), m0 = hi_f32<T>(vp[s][i]);
-                    // keys past the range and vectors that are not finite count as zeros
-                    const bool in = 64 * t + 32 * kb + 16 * s + 4 * vc + i < hi && ((there >> (2 * kb + s)) & 1u) &&
-                                    0.25f * __builtin_fabsf(m0) + 4.f * s0 < __builtin_inff();
-                    vs[i] = in ? s0 * vscale : 0.f;
-                    vm[i] = in ? (m0 + 8.f * s0) * vscale : 0.f;
-                }
-                sc[2 * s] = pack2<_Float16>(vs[0], vs[1]);
-                sc[2 * s + 1] = pack2<_Float16>(vs[2], vs[3]);
-                of[2 * s] = pack2<_Float16>(vm[0], vm[1]);
-                of[2 * s + 1] = pack2<_Float16>(vm[2], vm[3]);
+                const char *prm = buf + LT::P_AT + 512 + 2 * (32 * kb + 16 * s + 4 * vc);
+                sc[s] = *(const u32x2 *)prm;
+                of[s] = *(const u32x2 *)(prm + 128);
             }
         }
 #pragma unroll
@@ -684,21 +737,24 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnA
                     if constexpr (WHOLE) {
                         const f16x2 u = __builtin_bit_cast(f16x2, Mfma<_Float16>::pair(x[i], j)) - (_Float16)72.f;
                         f[i] = __builtin_bit_cast(int, __builtin_elementwise_fma(
-                                   u, __builtin_bit_cast(f16x2, sc[i]), __builtin_bit_cast(f16x2, of[i])));
+                                   u, __builtin_bit_cast(f16x2, (uint32_t)sc[i / 2][i % 2]),
+                                   __builtin_bit_cast(f16x2, (uint32_t)of[i / 2][i % 2])));
                     } else {
                         f[i] = (int)MfmaV::pair(x[i], j);
                     }
                 }
-                *(i32x4 *)(buf + LT::V_AT + (vd + 4 * half + j) * LT::VROW + kb * 64 + vc * 16) = f;
+                *(i32x4 *)(buf + LT::val_at(vd + 4 * half + j, kb, vc)) = f;
             }
         }
     };
 
     const float NEG = -__builtin_inff();
-    float m_run[2] = {NEG, NEG}, l_run[2] = {0.f, 0.f}, extra[2] = {0.f, 0.f};
-    f32x4 acc[2][ND], ones[2];
+    float m_run[RX], l_run[RX], extra[RX];
+    f32x4 acc[RX][ND], ones[RX];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < RX; ++x) {
+        m_run[x] = NEG;
+        l_run[x] = extra[x] = 0.f;
         ones[x] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int d = 0; d < ND; ++d) acc[x][d] = f32x4{0, 0, 0, 0};
@@ -706,51 +762,74 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnA
     const i32x4 one = {0x3F803F80, 0x3F803F80, 0x3F803F80, 0x3F803F80};
 
     if (first < last) {
-        fetch(first);
-        turn(first, smem);
+        ask(first);
+        advance(first);
+        if constexpr (WHOLE) {
+            if (keys && c == 0) {
+                vpw = a.c.vp[of_part(vec1) + r];
+                turn_scales(first, there1, smem);
+            }
+            __syncthreads();
+        }
+        ask(first + 1);
+        advance(first + 1);
+        ask(first + 2);
+        fetch();
+        turn(first, smem, smem + LT::BYTES);
     }
     uint32_t ok_pages = there;
     __syncthreads();
     for (int32_t t = first; t < last; ++t) {
-        const char *buf = smem + ((t - first) & 1) * LT::BYTES;
-        if (t + 1 < last) fetch(t + 1);
+        char *buf = smem + ((t - first) & 1) * LT::BYTES, *next = smem + ((t + 1 - first) & 1) * LT::BYTES;
+        if (t + 1 < last) {
+            advance(t + 2);
+            fetch();
+            ask(t + 3);
+        }
         const int32_t t0 = 64 * t;
         if (t0 < whi && t0 + 64 > wlo) {
             const bool whole = t0 >= full_lo && t0 + 64 <= full_hi && ok_pages == 15u;
             const float *prm = (const float *)(buf + LT::P_AT) + 4 * c;
-            float sc[2][4][4];
+            // scores in units of log 2 above the row's running maximum
+            float sc[RX][4][4];
+            float top[RX];
+#pragma unroll
+            for (int x = 0; x < RX; ++x) top[x] = m_run[x] == NEG ? 0.f : m_run[x];
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                f32x4 z[2];
+                f32x4 z[RX];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
+                for (int x = 0; x < RX; ++x) {
                     const float start = -MM::base * qsum[x];
                     z[x] = f32x4{start, start, start, start};
                 }
-                const char *k = buf + (16 * g + r) * LT::KROW + c * (D / 2);
 #pragma unroll
                 for (int j = 0; j < KW; ++j) {
-                    const i32x4 kf = *(const i32x4 *)(k + 16 * j);
-                    z[0] = MM::mul(kf, qf[0][j], z[0]);
-                    z[1] = MM::mul(kf, qf[1][j], z[1]);
+                    const i32x4 kf = *(const i32x4 *)(buf + LT::key_at(16 * g + r, j, c));
+#pragma unroll
+                    for (int x = 0; x < RX; ++x) z[x] = MM::mul(kf, qf[x][j], z[x]);
                 }
                 const f32x4 ks = *(const f32x4 *)(prm + 16 * g), km = *(const f32x4 *)(prm + 64 + 16 * g);
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
+                for (int x = 0; x < RX; ++x)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[x][g][i] = ks[i] * z[x][i] + km[i] * qsum[x];
+                    for (int i = 0; i < 4; ++i)
+                        sc[x][g][i] = __builtin_fmaf(ks[i], z[x][i], __builtin_fmaf(km[i], qsum[x], -top[x]));
             }
-            uint32_t seen[2] = {0xFFFFu, 0xFFFFu};
-            if (!whole) {
+            uint32_t seen[RX];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
+            for (int x = 0; x < RX; ++x) seen[x] = 0xFFFFu;
+            if (!whole) {
+                asm volatile("" ::: "memory");  // keeps the comparisons in this branch
+#pragma unroll
+                for (int x = 0; x < RX; ++x) {
+                    const int32_t from = my_lo[x] - t0 - 4 * c, to = my_hi[x] - t0 - 4 * c;
                     seen[x] = 0;
 #pragma unroll
                     for (int g = 0; g < 4; ++g)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const int32_t key = t0 + 16 * g + 4 * c + i;
-                            const bool ok = key >= my_lo[x] && key < my_hi[x] && ((ok_pages >> g) & 1u);
+                            const bool ok = 16 * g + i >= from && 16 * g + i < to && ((ok_pages >> g) & 1u);
                             seen[x] |= ok ? 1u << (4 * g + i) : 0u;
                             if (!ok) sc[x][g][i] = NEG;
                         }
@@ -758,33 +837,37 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnA
             }
             if constexpr (WHOLE)
                 if (odd) {
-#pragma unroll
+#pragma unroll 1
                     for (int g = 0; g < 4; ++g)
-#pragma unroll
+#pragma unroll 1
                         for (int i = 0; i < 4; ++i) {
                             const int32_t key = t0 + 16 * g + 4 * c + i;
                             if (key >= hi || !((ok_pages >> g) & 1u)) continue;
-                            const int32_t pi = key / a.c.page;
+                            const int32_t pi = page_of(a, key);
                             const int64_t at = ((int64_t)a.table[(int64_t)b * a.ldt + pi] * a.c.heads + h) * a.c.page +
                                                (key - pi * a.c.page);
                             const uint32_t w = a.c.vp[at];
                             const float gsum = 0.25f * __builtin_fabsf(hi_f32<T>(w)) + 4.f * lo_f32<T>(w);
                             if (!(gsum < __builtin_inff()))
 #pragma unroll
-                                for (int x = 0; x < 2; ++x)
+                                for (int x = 0; x < RX; ++x)
                                     if ((seen[x] >> (4 * g + i)) & 1u) extra[x] = __builtin_nanf("");
                         }
                 }
-            i32x4 whi[2][2], wlo2[2][2];
+            i32x4 whi[RX][2], wlo2[RX][2];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
+            for (int x = 0; x < RX; ++x) {
                 float mx = sc[x][0][0];
 #pragma unroll
                 for (int e = 1; e < 16; ++e) mx = fmaxf(mx, sc[x][e / 4][e % 4]);
-                mx = max_over_groups(mx);
-                if (__any(mx > m_run[x] + 8.f)) {
-                    const float m_new = fmaxf(m_run[x], mx);
+                // The running maximum is taken anew only when a score passes it by
+                // 2^8, and first of all; only then do the lanes of a row compare.
+                if (__any(mx > 8.f || m_run[x] == NEG)) {
+                    const float m_new = fmaxf(m_run[x], max_over_groups(mx) + top[x]);
+                    const float m_use = m_new == NEG ? 0.f : m_new;
                     const float al = m_run[x] == NEG ? 0.f : __builtin_amdgcn_exp2f(m_run[x] - m_new);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) sc[x][e / 4][e % 4] += top[x] - m_use;
                     m_run[x] = m_new;
                     l_run[x] *= al;
                     if constexpr (!WHOLE) {
@@ -794,13 +877,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnA
 #pragma unroll
                     for (int d = 0; d < ND; ++d) acc[x][d] *= al;
                 }
-                const float m_use = m_run[x] == NEG ? 0.f : m_run[x];
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     float w[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        w[i] = __builtin_amdgcn_exp2f(sc[x][g][i] - m_use);
+                        w[i] = __builtin_amdgcn_exp2f(sc[x][g][i]);
                         l_run[x] += w[i];
                     }
                     if constexpr (WHOLE) {
@@ -811,7 +893,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnA
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const bool ok = (seen[x] >> (4 * g + i)) & 1u;
-                            extra[x] += ok ? w[i] * vm[i] : 0.f;
+                            extra[x] = __builtin_fmaf(w[i], ok ? vm[i] : 0.f, extra[x]);
                             w[i] = ok ? w[i] * vs[i] : 0.f;
                         }
 #pragma unroll
@@ -826,19 +908,18 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnA
             }
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const char *v = buf + LT::V_AT + r * LT::VROW + q * 64 + c * 16;
                 if constexpr (!WHOLE) {
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
+                    for (int x = 0; x < RX; ++x) {
                         ones[x] = MfmaV::mul(one, whi[x][q], ones[x]);
                         ones[x] = MfmaV::mul(one, wlo2[x][q], ones[x]);
                     }
                 }
 #pragma unroll
                 for (int d = 0; d < ND; ++d) {
-                    const i32x4 vf = *(const i32x4 *)(v + 16 * d * LT::VROW);
+                    const i32x4 vf = *(const i32x4 *)(buf + LT::val_at(16 * d + r, q, c));
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
+                    for (int x = 0; x < RX; ++x) {
                         if constexpr (WHOLE) {
                             acc[x][d] = Mfma<_Float16>::mul(vf, whi[x][q], acc[x][d]);
                         } else {
@@ -849,13 +930,13 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnA
                 }
             }
         }
-        if (t + 1 < last) turn(t + 1, smem + ((t + 1 - first) & 1) * LT::BYTES);
+        if (t + 1 < last) turn(t + 1, next, buf);
         ok_pages = there;
         __syncthreads();
     }
 
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < RX; ++x) {
         const int32_t row = w0 + 16 * x + r;
         float l = sum_over_groups(l_run[x]);
         float add = WHOLE ? extra[x] : sum_over_groups(extra[x]);
@@ -930,12 +1011,12 @@ template <class T, int D> static hipError_t attn_t(const AttnArgs &a, hipStream_
     const int64_t wgs = (int64_t)a.batch * a.c.heads * a.tiles;
     if (wgs > 0x7FFFFFFF) return hipErrorInvalidValue;
     if (a.chunk)
-        hipLaunchKernelGGL((attn_chunk_kernel<T, D>), dim3((uint32_t)wgs, (uint32_t)a.splits), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((attn_chunk_kernel<T, D>), dim3((uint32_t)wgs, (uint32_t)a.splits), dim3(512), 0, s, a);
     else
         hipLaunchKernelGGL((attn_rows_kernel<T, D>), dim3((uint32_t)wgs, (uint32_t)a.splits), dim3(256), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
-    const int64_t row_tiles = a.chunk ? 8 * (int64_t)a.tiles : a.tiles;
+    const int64_t row_tiles = a.chunk ? ChunkTile<T, D>::ROWS / 16 * (int64_t)a.tiles : a.tiles;
     if ((int64_t)a.batch * a.c.heads * row_tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
     hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3((uint32_t)(a.batch * a.c.heads * row_tiles)), dim3(256), 0, s, a,
                        (int32_t)row_tiles);
