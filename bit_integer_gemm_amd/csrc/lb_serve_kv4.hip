@@ -519,7 +519,8 @@ template <class T, int D> struct ChunkTile {
     static constexpr int KROW = 2 * D, VROW = 128;
     static constexpr int V_AT = 64 * KROW, P_AT = V_AT + D * VROW;
     // per-key numbers: scale and minimum of keys (fp32), of values (fp16 or fp32)
-    static constexpr int BYTES = P_AT + (WHOLE ? 3 : 4) * 256;
+    static constexpr int FLAG_AT = P_AT + (WHOLE ? 3 : 4) * 256;   // bit g in word g: half-block g's page exists
+    static constexpr int BYTES = FLAG_AT + 16;
     // byte of piece 4 j + c of key n, and of piece 4 q + c of dim n
     static __device__ inline int key_at(int n, int j, int c)
     {
@@ -633,48 +634,48 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
     const int32_t part = wave & 3, kb = part >> 1;
     const int32_t vc = (int32_t)(lane & 3u), vd = ((part & 1) * 16 + (int32_t)(lane >> 2)) * DPT;
     uint32_t kw[KW], vw[8], kpw = 0, vpw = 0;
-    // Half-blocks of tile t, t + 1 and t + 2: first vector of each, whether its page
-    // exists, and page numbers on their way.
-    int64_t vec[4], vec1[4];
-    int32_t page2[4];
-    uint32_t there = 0, there1 = 0;
-    auto half_key = [&](int32_t t, int g) { return 64 * t + 16 * g < hi ? 64 * t + 16 * g : max(hi - 1, 0) / 16 * 16; };
+    // The wave's half-blocks (keys: one) of tile t, t + 1 and t + 2: first vector of
+    // each, whether its page exists, and page numbers on their way.
+    constexpr int NG = 2;
+    int64_t vec[NG], vec1[NG];
+    int32_t page2[NG];
+    bool there = false, there1 = false;
+    const int32_t g0 = keys ? part : 2 * kb, g1 = keys ? part : 2 * kb + 1;
+    const int32_t hi16 = max(hi - 1, 0) & ~15;
+    const int64_t head_at = (int64_t)h * a.c.page, page_step = (int64_t)a.c.heads * a.c.page;
     auto ask = [&](int32_t t) {
-#pragma unroll
-        for (int g = 0; g < 4; ++g) page2[g] = page_number(a, b, half_key(t, g));
+        page2[0] = page_number(a, b, min(64 * t + 16 * g0, hi16));
+        page2[1] = keys ? page2[0] : page_number(a, b, min(64 * t + 16 * g1, hi16));
     };
     auto advance = [&](int32_t t) {   // page2 holds tile t's numbers
         there = there1;
-        there1 = 0;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < NG; ++g) {
             vec[g] = vec1[g];
-            const int32_t tg = half_key(t, g), p = page2[g];
+            const int32_t tg = min(64 * t + 16 * (g ? g1 : g0), hi16), p = page2[g];
             const bool ok = (uint32_t)p < (uint32_t)a.c.pages;
-            there1 |= ok ? 1u << g : 0u;
-            vec1[g] = ((int64_t)(ok ? p : 0) * a.c.heads + h) * a.c.page + (tg - page_of(a, tg) * a.c.page);
+            if (g == 0) there1 = ok;
+            vec1[g] = (ok ? p : 0) * page_step + head_at + (tg - page_of(a, tg) * a.c.page);
         }
     };
-    auto of_part = [&](const int64_t *v) { return part == 0 ? v[0] : part == 1 ? v[1] : part == 2 ? v[2] : v[3]; };
     // tile t's nibbles, and the values' scales of tile t + 1 (WHOLE: turned a tile
     // before the values)
     auto fetch = [&]() {
         if (keys) {
-            const int64_t mine = of_part(vec);
+            const int64_t mine = vec[0];
             const uint32_t *k = (const uint32_t *)(a.c.k + (mine + r) * (D / 2)) + c * KW;
 #pragma unroll
             for (int j = 0; j < KW; ++j) kw[j] = k[j];
             if (c == 0) {
                 kpw = a.c.kp[mine + r];
-                vpw = a.c.vp[(WHOLE ? of_part(vec1) : mine) + r];
+                vpw = a.c.vp[(WHOLE ? vec1[0] : mine) + r];
             }
         } else {
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const int64_t at = kb == 0 ? vec[s] : vec[2 + s];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint8_t *v = a.c.v + (at + 4 * vc + i) * (D / 2) + vd / 2;
+                    const uint8_t *v = a.c.v + (vec[s] + 4 * vc + i) * (D / 2) + vd / 2;
                     if constexpr (DPT == 2) vw[4 * s + i] = *v;
                     else if constexpr (DPT == 4) vw[4 * s + i] = *(const uint16_t *)v;
                     else vw[4 * s + i] = *(const uint32_t *)v;
@@ -685,9 +686,9 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
     // WHOLE: scale and (minimum + 8 scales) of key 16 part + r of a tile, in fp16; a
     // key past the range, on a page that is not there, or whose vector is not finite
     // counts as zeros.
-    auto turn_scales = [&](int32_t t, uint32_t pages_there, char *buf) {
+    auto turn_scales = [&](int32_t t, bool page_there, char *buf) {
         const float s0 = lo_f32<T>(vpw), m0 = hi_f32<T>(vpw);
-        const bool in = 64 * t + 16 * part + r < hi && ((pages_there >> part) & 1u) &&
+        const bool in = 64 * t + 16 * part + r < hi && page_there &&
                         0.25f * __builtin_fabsf(m0) + 4.f * s0 < __builtin_inff();
         _Float16 *prm = (_Float16 *)(buf + LT::P_AT + 512) + 16 * part + r;
         prm[0] = (_Float16)(in ? s0 * vscale : 0.f);
@@ -710,6 +711,7 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
                     prm[128] = lo_f32<T>(vpw);
                     prm[192] = hi_f32<T>(vpw) + 8.f * lo_f32<T>(vpw);
                 }
+                if (r == 0) ((uint32_t *)(buf + LT::FLAG_AT))[part] = there ? 1u << part : 0u;
             }
             return;
         }
@@ -766,7 +768,7 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
         advance(first);
         if constexpr (WHOLE) {
             if (keys && c == 0) {
-                vpw = a.c.vp[of_part(vec1) + r];
+                vpw = a.c.vp[vec1[0] + r];
                 turn_scales(first, there1, smem);
             }
             __syncthreads();
@@ -777,7 +779,6 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
         fetch();
         turn(first, smem, smem + LT::BYTES);
     }
-    uint32_t ok_pages = there;
     __syncthreads();
     for (int32_t t = first; t < last; ++t) {
         char *buf = smem + ((t - first) & 1) * LT::BYTES, *next = smem + ((t + 1 - first) & 1) * LT::BYTES;
@@ -788,6 +789,8 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
         }
         const int32_t t0 = 64 * t;
         if (t0 < whi && t0 + 64 > wlo) {
+            const u32x4 flags = *(const u32x4 *)(buf + LT::FLAG_AT);
+            const uint32_t ok_pages = __builtin_amdgcn_readfirstlane(flags.x | flags.y | flags.z | flags.w);
             const bool whole = t0 >= full_lo && t0 + 64 <= full_hi && ok_pages == 15u;
             const float *prm = (const float *)(buf + LT::P_AT) + 4 * c;
             // scores in units of log 2 above the row's running maximum
@@ -931,7 +934,6 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
             }
         }
         if (t + 1 < last) turn(t + 1, next, buf);
-        ok_pages = there;
         __syncthreads();
     }
 
