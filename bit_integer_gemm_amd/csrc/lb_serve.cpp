@@ -81,8 +81,9 @@ AttnPlan plan_attn(int64_t B, int64_t total_q, int64_t max_q, int64_t Hq, int64_
     if (window > 0) keys = std::min(keys, window + max_q);
     const int64_t wgs = B * Hkv * p.tiles;
     p.splits = 1;
-    if (cu > 0 && wgs < 4 * (int64_t)cu) {
-        p.splits = std::min((4 * (int64_t)cu + wgs - 1) / wgs, (keys + 255) / 256);
+    const int64_t want = (p.chunk ? 2 : 4) * (int64_t)cu;   // workgroups
+    if (wgs < want) {
+        p.splits = std::min((want + wgs - 1) / wgs, (keys + 255) / 256);
         p.splits = std::max<int64_t>(1, std::min<int64_t>(p.splits, 64));
     }
     p.per_split = total_q * Hq * (D + 2) * 4;
@@ -208,7 +209,8 @@ int lb_attn_kv4(const void *Q, int64_t ldq, const uint8_t *Kc, const uint8_t *Vc
     const int sc = check_cache(Hkv, D, pages, page, ftype);
     if (sc != LB_OK) return sc;
     if (st != LB_OK) return st;
-    if ((double)table_width * (double)page >= 2147483616.0) return LB_ERR_OVERFLOW;  // key numbers are 32-bit
+    // key numbers, and those up to three tiles past the last, are 32-bit
+    if ((double)table_width * (double)page >= 2147482624.0) return LB_ERR_OVERFLOW;
     if (!aligned(Q) || !aligned(Kc) || !aligned(Vc) || !aligned(Kp) || !aligned(Vp) || !aligned(out) ||
         ldq % 8 != 0 || ldo % 8 != 0 || !aligned(workspace, 256))
         return LB_ERR_ALIGN;

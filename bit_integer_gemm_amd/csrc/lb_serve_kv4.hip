@@ -490,15 +490,16 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
 // 32 rows per wave, 256 per workgroup (D = 256: 16 and 128, whose outputs are as
 // many registers), against tiles of 64 keys that the eight
 // waves turn from nibbles into matrix operands once, in LDS, for all of them
-// (16 rows per wave, each turning its own, spends half its instructions there):
-// waves 0-3 the keys, waves 4-7 the values.
+// (16 rows per wave, each turning its own, spends half its instructions there).
 // The lanes' shares of a tile are attn_rows_kernel's: keys as the A operand with
 // the levels exact, so that a score is (s acc + m sum q) with per-key s and m;
 // a wave's weights are already the B operand of the values' product.
 //
-// Two tiles in LDS: while one is multiplied the next one's nibbles are on their
-// way to registers; they are turned and written after it, one barrier a tile.
-// The numbers of its page come a tile earlier still.  A fragment read takes 16
+// A wave's matrix instructions of one tile run beside its vector instructions of
+// another: the sums q . u of tile t + 1 beside the softmax of tile t, the values'
+// product of tile t beside the turning of the values of t + 1 and the keys of
+// t + 2, whose nibbles were asked for at the tile's start, and the numbers of
+// their pages a tile before.  One barrier a tile.  A fragment read takes 16
 // lanes' 16-byte pieces at a time, so piece p of row n (keys: D numbers of a key;
 // values: 64 keys of a dim) lies at p ^ (n % 16 or n % 8) of its row: 4 cycles a
 // read, counted, where rows padded by 16 bytes took 8 (and every write 8).
@@ -517,16 +518,20 @@ template <class T, int D> struct ChunkTile {
     static constexpr int ROWS = 8 * 16 * RX;
     static constexpr bool WHOLE = __is_same(T, __bf16);
     static constexpr int KROW = 2 * D, VROW = 128;
-    static constexpr int V_AT = 64 * KROW, P_AT = V_AT + D * VROW;
-    // per-key numbers: scale and minimum of keys (fp32), of values (fp16 or fp32)
-    static constexpr int FLAG_AT = P_AT + (WHOLE ? 3 : 4) * 256;   // bit g in word g: half-block g's page exists
-    static constexpr int BYTES = FLAG_AT + 16;
+    static constexpr int KBYTES = 64 * KROW, VBYTES = D * VROW;
+    // per-key numbers of a tile: scale and minimum of keys (fp32), of values (fp16 or
+    // fp32), and bit g in word g where half-block g's page exists
+    static constexpr int FLAG_AT = (WHOLE ? 3 : 4) * 256, PBYTES = FLAG_AT + 16;
+    static constexpr int V_AT = 2 * KBYTES, P_AT = V_AT + 2 * VBYTES, Q_AT = P_AT + 4 * PBYTES;
+    // D = 128: the queries' fragments stay in LDS; in registers they would spill
+    static constexpr bool Q_LDS = D == 128;
+    static constexpr int BYTES = Q_AT + (Q_LDS ? ROWS * 2 * D : 0);
     // byte of piece 4 j + c of key n, and of piece 4 q + c of dim n
     static __device__ inline int key_at(int n, int j, int c)
     {
         return n * KROW + 16 * ((4 * j + c) ^ (n & (D == 64 ? 7 : 15)));
     }
-    static __device__ inline int val_at(int n, int q, int c) { return V_AT + n * VROW + 16 * ((4 * q + c) ^ (n & 7)); }
+    static __device__ inline int val_at(int n, int q, int c) { return n * VROW + 16 * ((4 * q + c) ^ (n & 7)); }
 };
 
 // A page number of the table, by a scalar load.
@@ -543,10 +548,11 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
     using LT = ChunkTile<T, D>;
     constexpr bool WHOLE = LT::WHOLE;
     constexpr int RX = LT::RX;
-    constexpr int KW = D / 32;      // words of a key a lane turns, = MFMAs per 16 keys
-    constexpr int DPT = D / 32;     // dims of eight keys a lane turns
+    constexpr int KW = D / 32;      // MFMAs per 16 keys
+    constexpr int KH = KW / 2;      // words of a key a lane turns
+    constexpr int DPT = D / 64;     // dims of eight keys a lane turns
     constexpr int ND = D / 16;      // 16-dim fragments of the output
-    __shared__ __attribute__((aligned(16))) char smem[2 * LT::BYTES];
+    __shared__ __attribute__((aligned(16))) char smem[LT::BYTES];
     __shared__ uint32_t red[8];
     const uint32_t lane = threadIdx.x & 63u;
     const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -559,7 +565,8 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
     const int32_t r0 = tile * LT::ROWS;
     if (r0 >= sp.rows) return;
 
-    // key range of the workgroup, of this wave, and of each of its lanes' two rows
+    // key range of the workgroup, keys that every row of this wave sees, and the
+    // range of each of its lanes' rows
     const int32_t lo = key_lo(a, sp, r0 / a.group), hi = key_hi(a, sp, min(r0 + LT::ROWS - 1, sp.rows - 1) / a.group);
     const int32_t t_first = lo / 64, nt = max(0, (hi + 63) / 64 - t_first);
     const int32_t per = (nt + a.splits - 1) / a.splits;
@@ -567,10 +574,10 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
     const int32_t w0 = r0 + 16 * RX * wave;
     const bool busy = w0 < sp.rows;
     const int32_t wf = min(w0, sp.rows - 1) / a.group, wl = min(w0 + 16 * RX - 1, sp.rows - 1) / a.group;
-    const int32_t wlo = key_lo(a, sp, wf), whi = busy ? key_hi(a, sp, wl) : 0;
     const int32_t full_lo = key_lo(a, sp, wl), full_hi = key_hi(a, sp, wf);
     int32_t my_lo[RX], my_hi[RX];
-    i32x4 qf[RX][KW];
+    i32x4 qf[RX][LT::Q_LDS ? 1 : KW];
+    char *const qlds = smem + LT::Q_AT + wave * (RX * KW * 1024) + lane * 16;
     float qsum[RX];
 #pragma unroll
     for (int x = 0; x < RX; ++x) {
@@ -585,7 +592,8 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
             const i32x4 w = *(const i32x4 *)(q + 8 * j);
 #pragma unroll
             for (int i = 0; i < 4; ++i) sum += lo_f32<T>((uint32_t)w[i]) + hi_f32<T>((uint32_t)w[i]);
-            qf[x][j] = query_order(w);
+            if constexpr (LT::Q_LDS) *(i32x4 *)(qlds + (x * KW + j) * 1024) = query_order(w);
+            else qf[x][j] = query_order(w);
         }
         qsum[x] = sum_over_groups(sum);
     }
@@ -627,132 +635,118 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
         vscale = __uint_as_float(e << 23);
     }
 
-    // What a thread turns.  Waves 0-3: key 16 part + r, levels [c D/4, (c+1) D/4).
-    // Waves 4-7: eight keys' values, 4 vc + i of the half-blocks 2 kb and 2 kb + 1,
-    // dims vd .. vd + DPT - 1.
-    const bool keys = wave < 4;
-    const int32_t part = wave & 3, kb = part >> 1;
-    const int32_t vc = (int32_t)(lane & 3u), vd = ((part & 1) * 16 + (int32_t)(lane >> 2)) * DPT;
-    uint32_t kw[KW], vw[8], kpw = 0, vpw = 0;
-    // The wave's half-blocks (keys: one) of tile t, t + 1 and t + 2: first vector of
-    // each, whether its page exists, and page numbers on their way.
-    constexpr int NG = 2;
-    int64_t vec[NG], vec1[NG];
-    int32_t page2[NG];
-    bool there = false, there1 = false;
-    const int32_t g0 = keys ? part : 2 * kb, g1 = keys ? part : 2 * kb + 1;
+    // What a thread turns: words khalf KH .. of the levels [c D/4, (c+1) D/4) of key
+    // 16 part + r; and of the values eight keys, 4 vc + i of the half-blocks 2 kb and
+    // 2 kb + 1, dims vd .. vd + DPT - 1 (lanes 4 apart lie 4 dims apart, which spreads
+    // their writes over the banks).
+    const int32_t part = wave & 3, khalf = wave >> 2, kb = wave & 1, vc = (int32_t)(lane & 3u);
+    int32_t vd;
+    {
+        const int32_t u = (int32_t)(lane >> 2);
+        const int32_t v = DPT == 4   ? u
+                          : DPT == 2 ? (u & 12) | ((u & 1) << 1) | ((u >> 1) & 1)
+                                     : (u & 8) | ((u & 1) << 2) | ((u >> 1) & 3);
+        vd = ((wave >> 1) * 16 + v) * DPT;
+    }
+    uint32_t kw[KH], vw[8], kpw, vpw;
     const int32_t hi16 = max(hi - 1, 0) & ~15;
     const int64_t head_at = (int64_t)h * a.c.page, page_step = (int64_t)a.c.heads * a.c.page;
-    auto ask = [&](int32_t t) {
-        page2[0] = page_number(a, b, min(64 * t + 16 * g0, hi16));
-        page2[1] = keys ? page2[0] : page_number(a, b, min(64 * t + 16 * g1, hi16));
+    // Page numbers of the half-blocks to turn next, asked for a tile ahead: keys 16
+    // part of one tile, values 32 kb and 32 kb + 16 of the one before it.
+    int32_t pages_of_keys = 0, pages_of_vals[2] = {0, 0};
+    bool there = false;
+    auto ask_keys = [&](int32_t t) { pages_of_keys = page_number(a, b, min(64 * t + 16 * part, hi16)); };
+    auto ask_vals = [&](int32_t t) {
+        pages_of_vals[0] = page_number(a, b, min(64 * t + 32 * kb, hi16));
+        pages_of_vals[1] = page_number(a, b, min(64 * t + 32 * kb + 16, hi16));
     };
-    auto advance = [&](int32_t t) {   // page2 holds tile t's numbers
-        there = there1;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            vec[g] = vec1[g];
-            const int32_t tg = min(64 * t + 16 * (g ? g1 : g0), hi16), p = page2[g];
-            const bool ok = (uint32_t)p < (uint32_t)a.c.pages;
-            if (g == 0) there1 = ok;
-            vec1[g] = (ok ? p : 0) * page_step + head_at + (tg - page_of(a, tg) * a.c.page);
-        }
+    auto vector_of = [&](int32_t key, int32_t p) {
+        key = min(key, hi16);
+        return ((uint32_t)p < (uint32_t)a.c.pages ? p : 0) * page_step + head_at + (key - page_of(a, key) * a.c.page);
     };
-    // tile t's nibbles, and the values' scales of tile t + 1 (WHOLE: turned a tile
-    // before the values)
-    auto fetch = [&]() {
-        if (keys) {
-            const int64_t mine = vec[0];
-            const uint32_t *k = (const uint32_t *)(a.c.k + (mine + r) * (D / 2)) + c * KW;
+    auto fetch_keys = [&](int32_t t) {
+        there = (uint32_t)pages_of_keys < (uint32_t)a.c.pages;
+        const int64_t at = vector_of(64 * t + 16 * part, pages_of_keys) + r;
+        const uint32_t *k = (const uint32_t *)(a.c.k + at * (D / 2)) + c * KW + khalf * KH;
 #pragma unroll
-            for (int j = 0; j < KW; ++j) kw[j] = k[j];
-            if (c == 0) {
-                kpw = a.c.kp[mine + r];
-                vpw = a.c.vp[(WHOLE ? vec1[0] : mine) + r];
-            }
-        } else {
+        for (int j = 0; j < KH; ++j) kw[j] = k[j];
+        kpw = a.c.kp[at];
+        vpw = a.c.vp[at];
+    };
+    auto fetch_vals = [&](int32_t t) {
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < 2; ++s) {
+            const int64_t at = vector_of(64 * t + 32 * kb + 16 * s, pages_of_vals[s]) + 4 * vc;
+            const uint8_t *v = a.c.v + at * (D / 2) + vd / 2;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint8_t *v = a.c.v + (vec[s] + 4 * vc + i) * (D / 2) + vd / 2;
-                    if constexpr (DPT == 2) vw[4 * s + i] = *v;
-                    else if constexpr (DPT == 4) vw[4 * s + i] = *(const uint16_t *)v;
-                    else vw[4 * s + i] = *(const uint32_t *)v;
-                }
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (DPT == 4) vw[4 * s + i] = *(const uint16_t *)(v + i * (D / 2));
+                else vw[4 * s + i] = v[i * (D / 2)];
             }
         }
     };
-    // WHOLE: scale and (minimum + 8 scales) of key 16 part + r of a tile, in fp16; a
-    // key past the range, on a page that is not there, or whose vector is not finite
-    // counts as zeros.
-    auto turn_scales = [&](int32_t t, bool page_there, char *buf) {
+    // Turning, in units of one 16-byte write: word j of the keys, the per-key
+    // numbers, dim j of the values.
+    auto turn_key_word = [&](int j, char *kbuf) {
+        *(i32x4 *)(kbuf + LT::key_at(16 * part + r, khalf * KH + j, c)) = i32x4{
+            (int)MM::pair(kw[j], 0), (int)MM::pair(kw[j], 1), (int)MM::pair(kw[j], 2), (int)MM::pair(kw[j], 3)};
+    };
+    auto turn_numbers = [&](int32_t t, char *prm) {
+        // (lanes and waves that share a key write the same numbers)
+        float *f = (float *)prm + 16 * part + r;
+        // the levels are base + u in the products
+        f[0] = lo_f32<T>(kpw) * a.scale2;
+        f[64] = (hi_f32<T>(kpw) - MM::base * lo_f32<T>(kpw)) * a.scale2;
         const float s0 = lo_f32<T>(vpw), m0 = hi_f32<T>(vpw);
-        const bool in = 64 * t + 16 * part + r < hi && page_there &&
-                        0.25f * __builtin_fabsf(m0) + 4.f * s0 < __builtin_inff();
-        _Float16 *prm = (_Float16 *)(buf + LT::P_AT + 512) + 16 * part + r;
-        prm[0] = (_Float16)(in ? s0 * vscale : 0.f);
-        prm[64] = (_Float16)(in ? (m0 + 8.f * s0) * vscale : 0.f);
-    };
-    auto turn = [&](int32_t t, char *buf, char *other) {
-        if (keys) {
-#pragma unroll
-            for (int j = 0; j < KW; ++j)
-                *(i32x4 *)(buf + LT::key_at(16 * part + r, j, c)) =
-                    i32x4{(int)MM::pair(kw[j], 0), (int)MM::pair(kw[j], 1), (int)MM::pair(kw[j], 2),
-                          (int)MM::pair(kw[j], 3)};
-            float *prm = (float *)(buf + LT::P_AT) + 16 * part + r;
-            if (c == 0) {
-                prm[0] = lo_f32<T>(kpw) * a.scale2;
-                prm[64] = hi_f32<T>(kpw) * a.scale2;
-                if constexpr (WHOLE) {
-                    turn_scales(t + 1, there1, other);
-                } else {
-                    prm[128] = lo_f32<T>(vpw);
-                    prm[192] = hi_f32<T>(vpw) + 8.f * lo_f32<T>(vpw);
-                }
-                if (r == 0) ((uint32_t *)(buf + LT::FLAG_AT))[part] = there ? 1u << part : 0u;
-            }
-            return;
-        }
-        u32x2 sc[2], of[2];
         if constexpr (WHOLE) {
+            // a key past the range, on a page that is not there, or whose value is not
+            // finite counts as zeros
+            const bool in = (64 * t + 16 * part + r < hi) & there & (0.25f * __builtin_fabsf(m0) + 4.f * s0 < __builtin_inff());
+            const float sv = s0 * vscale, mv = (m0 + 8.f * s0) * vscale;
+            _Float16 *g = (_Float16 *)(prm + 512) + 16 * part + r;
+            g[0] = (_Float16)(in ? sv : 0.f);
+            g[64] = (_Float16)(in ? mv : 0.f);
+        } else {
+            f[128] = s0;
+            f[192] = m0 + 8.f * s0;
+        }
+        ((uint32_t *)(prm + LT::FLAG_AT))[part] = there ? 1u << part : 0u;
+    };
+    auto turn_val_dim = [&](int j, char *vbuf, const char *prm) {
+        i32x4 f;
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const char *prm = buf + LT::P_AT + 512 + 2 * (32 * kb + 16 * s + 4 * vc);
-                sc[s] = *(const u32x2 *)prm;
-                of[s] = *(const u32x2 *)(prm + 128);
+        for (int i = 0; i < 4; ++i) {
+            uint32_t x = vw[2 * i] | (vw[2 * i + 1] << 16);
+            if constexpr (DPT == 1) x >>= 4 * (vd & 1);
+            if constexpr (WHOLE) {
+                const char *g = prm + 512 + 2 * (32 * kb + 16 * (i / 2) + 4 * vc + 2 * (i % 2));
+                const f16x2 u = __builtin_bit_cast(f16x2, Mfma<_Float16>::pair(x, j)) - (_Float16)72.f;
+                f[i] = __builtin_bit_cast(int, __builtin_elementwise_fma(u, *(const f16x2 *)g, *(const f16x2 *)(g + 128)));
+            } else {
+                f[i] = (int)MfmaV::pair(x, j);
             }
         }
+        *(i32x4 *)(vbuf + LT::val_at(vd + j, kb, vc)) = f;
+    };
+    constexpr int UNITS = DPT + KH + 1;
+    auto turn_unit = [&](int u, int32_t t, char *kbuf, char *kprm, char *vbuf, const char *vprm) {
+        if (u < DPT) turn_val_dim(u, vbuf, vprm);
+        else if (u < DPT + KH) turn_key_word(u - DPT, kbuf);
+        else turn_numbers(t, kprm);
+    };
+    auto turn_keys = [&](int32_t t, char *kbuf, char *prm) {
 #pragma unroll
-        for (int half = 0; half < (DPT == 8 ? 2 : 1); ++half) {
-            uint32_t x[4];
+        for (int j = 0; j < KH; ++j) turn_key_word(j, kbuf);
+        turn_numbers(t, prm);
+    };
+    auto turn_vals = [&](char *vbuf, const char *prm) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x[i] = half ? (vw[2 * i] >> 16) | (vw[2 * i + 1] & 0xFFFF0000u)
-                            : (vw[2 * i] & 0xFFFFu) | (vw[2 * i + 1] << 16);
-#pragma unroll
-            for (int j = 0; j < (DPT == 2 ? 2 : 4); ++j) {
-                i32x4 f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if constexpr (WHOLE) {
-                        const f16x2 u = __builtin_bit_cast(f16x2, Mfma<_Float16>::pair(x[i], j)) - (_Float16)72.f;
-                        f[i] = __builtin_bit_cast(int, __builtin_elementwise_fma(
-                                   u, __builtin_bit_cast(f16x2, (uint32_t)sc[i / 2][i % 2]),
-                                   __builtin_bit_cast(f16x2, (uint32_t)of[i / 2][i % 2])));
-                    } else {
-                        f[i] = (int)MfmaV::pair(x[i], j);
-                    }
-                }
-                *(i32x4 *)(buf + LT::val_at(vd + 4 * half + j, kb, vc)) = f;
-            }
-        }
+        for (int j = 0; j < DPT; ++j) turn_val_dim(j, vbuf, prm);
     };
 
     const float NEG = -__builtin_inff();
     float m_run[RX], l_run[RX], extra[RX];
-    f32x4 acc[RX][ND], ones[RX];
+    f32x4 acc[RX][ND], ones[RX], z[RX][4];
 #pragma unroll
     for (int x = 0; x < RX; ++x) {
         m_run[x] = NEG;
@@ -762,156 +756,201 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
         for (int d = 0; d < ND; ++d) acc[x][d] = f32x4{0, 0, 0, 0};
     }
     const i32x4 one = {0x3F803F80, 0x3F803F80, 0x3F803F80, 0x3F803F80};
+    // Sums q . (base + u) of the 64 keys in kbuf, in 4 KW steps of one fragment read
+    // and RX products; beside(step) adds the caller's vector instructions to a step.
+    // A step is fenced, so that its read goes out PF steps before its products: left
+    // to itself the compiler waits for each read where it stands.
+    constexpr int STEPS = 4 * KW, PF = 3;
+    auto products = [&](const char *kbuf, auto beside) {
+        i32x4 kf[PF + 1], q[2][RX];
+        auto read_key = [&](int st) { kf[st % (PF + 1)] = *(const i32x4 *)(kbuf + LT::key_at(16 * (st % 4) + r, st / 4, c)); };
+        auto read_query = [&](int j) {
+#pragma unroll
+            for (int x = 0; x < RX; ++x) {
+                if constexpr (LT::Q_LDS) q[j & 1][x] = *(const i32x4 *)(qlds + (x * KW + j) * 1024);
+                else q[j & 1][x] = qf[x][j];
+            }
+        };
+        read_query(0);
+#pragma unroll
+        for (int st = 0; st < PF; ++st) read_key(st);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int st = 0; st < STEPS; ++st) {
+            const int j = st / 4, g = st % 4;
+            if (st + PF < STEPS) read_key(st + PF);
+            if (g == 0 && j + 1 < KW) read_query(j + 1);
+#pragma unroll
+            for (int x = 0; x < RX; ++x)
+                z[x][g] = MM::mul(kf[st % (PF + 1)], q[j & 1][x], j ? z[x][g] : f32x4{0, 0, 0, 0});
+            beside(st);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
 
     if (first < last) {
-        ask(first);
-        advance(first);
-        if constexpr (WHOLE) {
-            if (keys && c == 0) {
-                vpw = a.c.vp[vec1[0] + r];
-                turn_scales(first, there1, smem);
-            }
-            __syncthreads();
-        }
-        ask(first + 1);
-        advance(first + 1);
-        ask(first + 2);
-        fetch();
-        turn(first, smem, smem + LT::BYTES);
+        ask_keys(first);
+        fetch_keys(first);
+        ask_keys(first + 1);
+        turn_keys(first, smem, smem + LT::P_AT);
+        ask_vals(first);
+        fetch_keys(first + 1);
+        turn_keys(first + 1, smem + LT::KBYTES, smem + LT::P_AT + LT::PBYTES);
+        fetch_vals(first);
+        ask_keys(first + 2);
+        ask_vals(first + 1);
+        __syncthreads();
+        turn_vals(smem + LT::V_AT, smem + LT::P_AT);
+        products(smem, [](int) {});
     }
     __syncthreads();
+    // Tile t: its scores' sums are in z; the next tile's are made beside its softmax,
+    // the next values and the keys after those are turned beside its values' product.
     for (int32_t t = first; t < last; ++t) {
-        char *buf = smem + ((t - first) & 1) * LT::BYTES, *next = smem + ((t + 1 - first) & 1) * LT::BYTES;
-        if (t + 1 < last) {
-            advance(t + 2);
-            fetch();
-            ask(t + 3);
+        const int32_t n = t - first;
+        char *const kcur = smem + (n & 1) * LT::KBYTES, *const knext = smem + (~n & 1) * LT::KBYTES;
+        char *const vcur = smem + LT::V_AT + (n & 1) * LT::VBYTES, *const vnext = smem + LT::V_AT + (~n & 1) * LT::VBYTES;
+        auto slot = [&](int k) { return smem + LT::P_AT + ((n + k) & 3) * LT::PBYTES; };
+        fetch_keys(t + 2);
+        fetch_vals(t + 1);
+        ask_keys(t + 3);
+        ask_vals(t + 2);
+        if (!busy) {
+            turn_vals(vnext, slot(1));
+            turn_keys(t + 2, kcur, slot(2));
+            __syncthreads();
+            continue;
         }
         const int32_t t0 = 64 * t;
-        if (t0 < whi && t0 + 64 > wlo) {
-            const u32x4 flags = *(const u32x4 *)(buf + LT::FLAG_AT);
-            const uint32_t ok_pages = __builtin_amdgcn_readfirstlane(flags.x | flags.y | flags.z | flags.w);
-            const bool whole = t0 >= full_lo && t0 + 64 <= full_hi && ok_pages == 15u;
-            const float *prm = (const float *)(buf + LT::P_AT) + 4 * c;
-            // scores in units of log 2 above the row's running maximum
-            float sc[RX][4][4];
-            float top[RX];
+        const char *prm = slot(0);
+        const u32x4 flags = *(const u32x4 *)(prm + LT::FLAG_AT);
+        const uint32_t ok_pages = __builtin_amdgcn_readfirstlane(flags.x | flags.y | flags.z | flags.w);
+        const bool whole = t0 >= full_lo && t0 + 64 <= full_hi && ok_pages == 15u;
+        // scores in units of log 2 above the row's running maximum
+        float top[RX];
 #pragma unroll
-            for (int x = 0; x < RX; ++x) top[x] = m_run[x] == NEG ? 0.f : m_run[x];
+        for (int x = 0; x < RX; ++x) top[x] = m_run[x] == NEG ? 0.f : m_run[x];
+        f32x4 sc[RX][4];
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                f32x4 z[RX];
+        for (int g = 0; g < 4; ++g) {
+            const f32x4 ks = *(const f32x4 *)(prm + 4 * (16 * g + 4 * c)), km = *(const f32x4 *)(prm + 256 + 4 * (16 * g + 4 * c));
 #pragma unroll
-                for (int x = 0; x < RX; ++x) {
-                    const float start = -MM::base * qsum[x];
-                    z[x] = f32x4{start, start, start, start};
-                }
+            for (int x = 0; x < RX; ++x)
 #pragma unroll
-                for (int j = 0; j < KW; ++j) {
-                    const i32x4 kf = *(const i32x4 *)(buf + LT::key_at(16 * g + r, j, c));
+                for (int i = 0; i < 4; ++i)
+                    sc[x][g][i] = __builtin_fmaf(ks[i], z[x][g][i], __builtin_fmaf(km[i], qsum[x], -top[x]));
+        }
+        uint32_t seen[RX];
 #pragma unroll
-                    for (int x = 0; x < RX; ++x) z[x] = MM::mul(kf, qf[x][j], z[x]);
-                }
-                const f32x4 ks = *(const f32x4 *)(prm + 16 * g), km = *(const f32x4 *)(prm + 64 + 16 * g);
+        for (int x = 0; x < RX; ++x) seen[x] = 0xFFFFu;
+        if (!whole) {
+            asm volatile("" ::: "memory");  // keeps the comparisons in this branch
 #pragma unroll
-                for (int x = 0; x < RX; ++x)
+            for (int x = 0; x < RX; ++x) {
+                const int32_t from = my_lo[x] - t0 - 4 * c, to = my_hi[x] - t0 - 4 * c;
+                seen[x] = 0;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        sc[x][g][i] = __builtin_fmaf(ks[i], z[x][i], __builtin_fmaf(km[i], qsum[x], -top[x]));
+                for (int g = 0; g < 4; ++g)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool ok = 16 * g + i >= from && 16 * g + i < to && ((ok_pages >> g) & 1u);
+                        seen[x] |= ok ? 1u << (4 * g + i) : 0u;
+                        if (!ok) sc[x][g][i] = NEG;
+                    }
             }
-            uint32_t seen[RX];
+        }
+        if constexpr (WHOLE)
+            if (odd) {
+#pragma unroll 1
+                for (int e = 0; e < 16; ++e) {
+                    const int32_t key = t0 + 16 * (e >> 2) + 4 * c + (e & 3);
+                    if (key >= hi || !((ok_pages >> (e >> 2)) & 1u)) continue;
+                    const int32_t pi = page_of(a, key);
+                    const uint32_t w = a.c.vp[((int64_t)a.table[(int64_t)b * a.ldt + pi] * a.c.heads + h) * a.c.page +
+                                              (key - pi * a.c.page)];
+                    if (!(0.25f * __builtin_fabsf(hi_f32<T>(w)) + 4.f * lo_f32<T>(w) < __builtin_inff()))
 #pragma unroll
-            for (int x = 0; x < RX; ++x) seen[x] = 0xFFFFu;
-            if (!whole) {
-                asm volatile("" ::: "memory");  // keeps the comparisons in this branch
-#pragma unroll
-                for (int x = 0; x < RX; ++x) {
-                    const int32_t from = my_lo[x] - t0 - 4 * c, to = my_hi[x] - t0 - 4 * c;
-                    seen[x] = 0;
-#pragma unroll
-                    for (int g = 0; g < 4; ++g)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const bool ok = 16 * g + i >= from && 16 * g + i < to && ((ok_pages >> g) & 1u);
-                            seen[x] |= ok ? 1u << (4 * g + i) : 0u;
-                            if (!ok) sc[x][g][i] = NEG;
-                        }
+                        for (int x = 0; x < RX; ++x)
+                            if ((seen[x] >> e) & 1u) extra[x] = __builtin_nanf("");
                 }
             }
-            if constexpr (WHOLE)
-                if (odd) {
-#pragma unroll 1
-                    for (int g = 0; g < 4; ++g)
-#pragma unroll 1
-                        for (int i = 0; i < 4; ++i) {
-                            const int32_t key = t0 + 16 * g + 4 * c + i;
-                            if (key >= hi || !((ok_pages >> g) & 1u)) continue;
-                            const int32_t pi = page_of(a, key);
-                            const int64_t at = ((int64_t)a.table[(int64_t)b * a.ldt + pi] * a.c.heads + h) * a.c.page +
-                                               (key - pi * a.c.page);
-                            const uint32_t w = a.c.vp[at];
-                            const float gsum = 0.25f * __builtin_fabsf(hi_f32<T>(w)) + 4.f * lo_f32<T>(w);
-                            if (!(gsum < __builtin_inff()))
+        // The running maximum is taken anew only when a score passes it by 2^8, and
+        // first of all; only then do the lanes of a row compare.
+        bool raise = false;
 #pragma unroll
-                                for (int x = 0; x < RX; ++x)
-                                    if ((seen[x] >> (4 * g + i)) & 1u) extra[x] = __builtin_nanf("");
-                        }
-                }
-            i32x4 whi[RX][2], wlo2[RX][2];
+        for (int x = 0; x < RX; ++x) {
+            float mx = sc[x][0][0];
+#pragma unroll
+            for (int e = 1; e < 16; ++e) mx = fmaxf(mx, sc[x][e / 4][e % 4]);
+            raise |= mx > 8.f || m_run[x] == NEG;
+        }
+        if (__any(raise)) {
 #pragma unroll
             for (int x = 0; x < RX; ++x) {
                 float mx = sc[x][0][0];
 #pragma unroll
                 for (int e = 1; e < 16; ++e) mx = fmaxf(mx, sc[x][e / 4][e % 4]);
-                // The running maximum is taken anew only when a score passes it by
-                // 2^8, and first of all; only then do the lanes of a row compare.
-                if (__any(mx > 8.f || m_run[x] == NEG)) {
-                    const float m_new = fmaxf(m_run[x], max_over_groups(mx) + top[x]);
-                    const float m_use = m_new == NEG ? 0.f : m_new;
-                    const float al = m_run[x] == NEG ? 0.f : __builtin_amdgcn_exp2f(m_run[x] - m_new);
+                const float m_new = fmaxf(m_run[x], max_over_groups(mx) + top[x]);
+                const float m_use = m_new == NEG ? 0.f : m_new;
+                const float al = m_run[x] == NEG ? 0.f : __builtin_amdgcn_exp2f(m_run[x] - m_new);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) sc[x][e / 4][e % 4] += top[x] - m_use;
-                    m_run[x] = m_new;
-                    l_run[x] *= al;
-                    if constexpr (!WHOLE) {
-                        extra[x] *= al;
-                        ones[x] *= al;
-                    }
-#pragma unroll
-                    for (int d = 0; d < ND; ++d) acc[x][d] *= al;
+                for (int e = 0; e < 16; ++e) sc[x][e / 4][e % 4] += top[x] - m_use;
+                m_run[x] = m_new;
+                l_run[x] *= al;
+                if constexpr (!WHOLE) {
+                    extra[x] *= al;
+                    ones[x] *= al;
                 }
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    float w[4];
+                for (int d = 0; d < ND; ++d) acc[x][d] *= al;
+            }
+        }
+        // this tile's weights, beside the next tile's sums
+        i32x4 whi[RX][2], wlo2[RX][2];
+        constexpr int QUADS = 4 * RX;   // four weights each
+        products(knext, [&](int st) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        w[i] = __builtin_amdgcn_exp2f(sc[x][g][i]);
-                        l_run[x] += w[i];
+            for (int e = 4 * QUADS * st / STEPS; e < 4 * QUADS * (st + 1) / STEPS; ++e) {
+                const int x = e / 16, g = e / 4 % 4, i = e % 4;
+                sc[x][g][i] = __builtin_amdgcn_exp2f(sc[x][g][i]);
+                l_run[x] += sc[x][g][i];
+                if (i != 3) continue;
+                float w[4] = {sc[x][g][0], sc[x][g][1], sc[x][g][2], sc[x][g][3]};
+                if constexpr (WHOLE) {
+                    whi[x][g / 2][2 * (g % 2)] = (int)pack2<_Float16>(w[0], w[1]);
+                    whi[x][g / 2][2 * (g % 2) + 1] = (int)pack2<_Float16>(w[2], w[3]);
+                } else {
+                    const f32x4 vs = *(const f32x4 *)(prm + 512 + 4 * (16 * g + 4 * c));
+                    const f32x4 vm = *(const f32x4 *)(prm + 768 + 4 * (16 * g + 4 * c));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const bool ok = (seen[x] >> (4 * g + k)) & 1u;
+                        extra[x] = __builtin_fmaf(w[k], ok ? vm[k] : 0.f, extra[x]);
+                        w[k] = ok ? w[k] * vs[k] : 0.f;
                     }
-                    if constexpr (WHOLE) {
-                        whi[x][g / 2][2 * (g % 2)] = (int)pack2<_Float16>(w[0], w[1]);
-                        whi[x][g / 2][2 * (g % 2) + 1] = (int)pack2<_Float16>(w[2], w[3]);
-                    } else {
-                        const f32x4 vs = *(const f32x4 *)(prm + 128 + 16 * g), vm = *(const f32x4 *)(prm + 192 + 16 * g);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const bool ok = (seen[x] >> (4 * g + i)) & 1u;
-                            extra[x] = __builtin_fmaf(w[i], ok ? vm[i] : 0.f, extra[x]);
-                            w[i] = ok ? w[i] * vs[i] : 0.f;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint32_t hi2 = pack2<__bf16>(w[2 * i], w[2 * i + 1]);
-                            whi[x][g / 2][2 * (g % 2) + i] = (int)hi2;
-                            wlo2[x][g / 2][2 * (g % 2) + i] = (int)pack2<__bf16>(w[2 * i] - lo_f32<__bf16>(hi2),
-                                                                                 w[2 * i + 1] - hi_f32<__bf16>(hi2));
-                        }
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t hi2 = pack2<__bf16>(w[2 * k], w[2 * k + 1]);
+                        whi[x][g / 2][2 * (g % 2) + k] = (int)hi2;
+                        wlo2[x][g / 2][2 * (g % 2) + k] = (int)pack2<__bf16>(w[2 * k] - lo_f32<__bf16>(hi2),
+                                                                             w[2 * k + 1] - hi_f32<__bf16>(hi2));
                     }
                 }
             }
+        });
+        // the values' product, beside the turning of what comes next
+        constexpr int VSTEPS = 2 * ND;
+        i32x4 vf[PF + 1];
+        auto read_val = [&](int st) { vf[st % (PF + 1)] = *(const i32x4 *)(vcur + LT::val_at(16 * (st % ND) + r, st / ND, c)); };
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                if constexpr (!WHOLE) {
+        for (int st = 0; st < PF; ++st) read_val(st);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int st = 0; st < VSTEPS; ++st) {
+            const int d = st % ND, q = st / ND;
+            if (st + PF < VSTEPS) read_val(st + PF);
+            if constexpr (!WHOLE)
+                if (d == 0) {
 #pragma unroll
                     for (int x = 0; x < RX; ++x) {
                         ones[x] = MfmaV::mul(one, whi[x][q], ones[x]);
@@ -919,21 +958,18 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
                     }
                 }
 #pragma unroll
-                for (int d = 0; d < ND; ++d) {
-                    const i32x4 vf = *(const i32x4 *)(buf + LT::val_at(16 * d + r, q, c));
-#pragma unroll
-                    for (int x = 0; x < RX; ++x) {
-                        if constexpr (WHOLE) {
-                            acc[x][d] = Mfma<_Float16>::mul(vf, whi[x][q], acc[x][d]);
-                        } else {
-                            acc[x][d] = MfmaV::mul(vf, whi[x][q], acc[x][d]);
-                            acc[x][d] = MfmaV::mul(vf, wlo2[x][q], acc[x][d]);
-                        }
-                    }
-                }
+            for (int x = 0; x < RX; ++x) {
+                if constexpr (WHOLE) acc[x][d] = Mfma<_Float16>::mul(vf[st % (PF + 1)], whi[x][q], acc[x][d]);
+                else acc[x][d] = MfmaV::mul(vf[st % (PF + 1)], whi[x][q], acc[x][d]);
             }
+            if constexpr (!WHOLE)
+#pragma unroll
+                for (int x = 0; x < RX; ++x) acc[x][d] = MfmaV::mul(vf[st % (PF + 1)], wlo2[x][q], acc[x][d]);
+#pragma unroll
+            for (int u = UNITS * st / VSTEPS; u < UNITS * (st + 1) / VSTEPS; ++u)
+                turn_unit(u, t + 2, kcur, slot(2), vnext, slot(1));
+            __builtin_amdgcn_sched_barrier(0);
         }
-        if (t + 1 < last) turn(t + 1, next, buf);
         __syncthreads();
     }
 
