@@ -96,6 +96,7 @@ struct AttnArgs {
     int64_t ldq, ldo, ldt, width;
     int64_t total_q;
     int32_t group, batch, window, causal, splits;
+    int32_t unit;         // fewest blocks of keys (64 keys, or 32) worth a workgroup of their own
     int32_t chunk, tiles; // which kernel: 256 (D = 256: 128) rows per workgroup, or 16; and how many such tiles a key head has
     uint32_t page_mul, page_shift; // division by the page size
     float scale2;         // softmax scale * log2(e)

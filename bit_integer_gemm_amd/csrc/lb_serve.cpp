@@ -65,7 +65,8 @@ lb::Kv4Cache cache_of(const uint8_t *Kc, const uint8_t *Vc, const void *Kp, cons
 
 struct AttnPlan {
     bool chunk;
-    int64_t tiles, splits, per_split;   // row tiles of a key head; key ranges; workspace bytes per range
+    int64_t tiles, splits, unit, per_split;   // row tiles of a key head; key ranges at most; blocks of keys in
+                                              // one; workspace bytes per range
 };
 
 AttnPlan plan_attn(int64_t B, int64_t total_q, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D,
@@ -79,13 +80,18 @@ AttnPlan plan_attn(int64_t B, int64_t total_q, int64_t max_q, int64_t Hq, int64_
     p.tiles = p.chunk ? (max_q * group + (D == 256 ? 127 : 255)) / (D == 256 ? 128 : 256) : (max_q * group + 15) / 16;
     int64_t keys = max_len;
     if (window > 0) keys = std::min(keys, window + max_q);
-    const int64_t wgs = B * Hkv * p.tiles;
+    const int64_t wgs = B * Hkv * p.tiles, block = p.chunk ? 64 : 32, blocks = std::max<int64_t>((keys + block - 1) / block, 1);
     p.splits = 1;
-    const int64_t want = (p.chunk ? 2 : 4) * (int64_t)cu;   // workgroups
-    if (wgs < want) {
-        p.splits = std::min((want + wgs - 1) / wgs, (keys + 255) / 256);
-        p.splits = std::max<int64_t>(1, std::min<int64_t>(p.splits, 64));
+    if (p.chunk && cu > 0) {
+        // One workgroup to a compute unit.  A range costs its rows' partial results in
+        // fp32, written and read, about as much as nine tiles of 64 keys: no ranges
+        // once there are workgroups for all units, and none below 16 tiles.
+        p.splits = std::min((int64_t)cu / wgs, blocks / 16);
+    } else if (wgs < 4 * (int64_t)cu) {
+        p.splits = std::min((4 * (int64_t)cu + wgs - 1) / wgs, (blocks + 7) / 8);
     }
+    p.splits = std::max<int64_t>(1, std::min<int64_t>(p.splits, 64));
+    p.unit = (blocks + p.splits - 1) / p.splits;
     p.per_split = total_q * Hq * (D + 2) * 4;
     return p;
 }
@@ -241,6 +247,7 @@ int lb_attn_kv4(const void *Q, int64_t ldq, const uint8_t *Kc, const uint8_t *Vc
     a.window = (int32_t)window;
     a.causal = causal != 0;
     a.splits = (int32_t)splits;
+    a.unit = splits == p.splits ? (int32_t)p.unit : 1;
     a.chunk = p.chunk;
     a.tiles = (int32_t)p.tiles;
     // key / page = mulhi(key, mul) >> shift with 2^shift the power of two below page:

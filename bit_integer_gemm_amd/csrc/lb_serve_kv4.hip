@@ -247,6 +247,22 @@ __device__ inline int32_t key_lo(const AttnArgs &a, const Span &s, int32_t qi)
     return a.window > 0 ? max(0, s.n - s.nq + qi + 1 - a.window) : 0;
 }
 
+// How the keys [lo, hi) of a tile of rows are shared: nb blocks of keys from block
+// b0, `per` to a workgroup, `ranges` workgroups (at most a.splits; one writes the
+// output itself).
+struct Ranges {
+    int32_t b0, nb, per, ranges;
+};
+template <int BLOCK> __device__ inline Ranges ranges_of(const AttnArgs &a, int32_t lo, int32_t hi)
+{
+    Ranges s;
+    s.b0 = lo / BLOCK;
+    s.nb = max(0, (hi + BLOCK - 1) / BLOCK - s.b0);
+    s.per = max(a.unit, (s.nb + a.splits - 1) / a.splits);
+    s.ranges = max(1, (s.nb + s.per - 1) / s.per);
+    return s;
+}
+
 __device__ inline float max_over_groups(float x)
 {
     x = fmaxf(x, __shfl_xor(x, 16));
@@ -292,9 +308,9 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
     const int32_t qi_first = r0 / a.group, qi_last = min(r0 + 15, sp.rows - 1) / a.group;
     const int32_t lo = key_lo(a, sp, qi_first), hi = key_hi(a, sp, qi_last);
     const int32_t full_lo = key_lo(a, sp, qi_last), full_hi = key_hi(a, sp, qi_first);
-    const int32_t b0 = lo / 32, nb = max(0, (hi + 31) / 32 - b0);
-    const int32_t per = (nb + a.splits - 1) / a.splits;
-    const int32_t first = b0 + (int32_t)blockIdx.y * per, last = min(b0 + nb, first + per);
+    const Ranges rg = ranges_of<32>(a, lo, hi);
+    if ((int32_t)blockIdx.y >= rg.ranges) return;
+    const int32_t first = rg.b0 + (int32_t)blockIdx.y * rg.per, last = min(rg.b0 + rg.nb, first + rg.per);
 
     i32x4 qf[KW];
     float qsum = 0.f;
@@ -467,7 +483,7 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
     }
     const int32_t oq = (r0 + orow) / a.group, oh = h * a.group + (r0 + orow - oq * a.group);
     const int64_t grow = (sp.q0 + oq) * (int64_t)(a.group * a.c.heads) + oh;
-    if (a.splits > 1) {
+    if (rg.ranges > 1) {
         const int64_t nrows = a.total_q * (int64_t)(a.group * a.c.heads);
         float *po = a.part + ((int64_t)blockIdx.y * nrows + grow) * D + oc * DPL;
 #pragma unroll
@@ -568,9 +584,9 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
     // key range of the workgroup, keys that every row of this wave sees, and the
     // range of each of its lanes' rows
     const int32_t lo = key_lo(a, sp, r0 / a.group), hi = key_hi(a, sp, min(r0 + LT::ROWS - 1, sp.rows - 1) / a.group);
-    const int32_t t_first = lo / 64, nt = max(0, (hi + 63) / 64 - t_first);
-    const int32_t per = (nt + a.splits - 1) / a.splits;
-    const int32_t first = t_first + (int32_t)blockIdx.y * per, last = min(t_first + nt, first + per);
+    const Ranges rg = ranges_of<64>(a, lo, hi);
+    if ((int32_t)blockIdx.y >= rg.ranges) return;
+    const int32_t first = rg.b0 + (int32_t)blockIdx.y * rg.per, last = min(rg.b0 + rg.nb, first + rg.per);
     const int32_t w0 = r0 + 16 * RX * wave;
     const bool busy = w0 < sp.rows;
     const int32_t wf = min(w0, sp.rows - 1) / a.group, wl = min(w0 + 16 * RX - 1, sp.rows - 1) / a.group;
@@ -984,7 +1000,7 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
         const float off = WHOLE ? -add : (MfmaV::base + 8.f) * ones[x].x - add;
         const int32_t oq = row / a.group, oh = h * a.group + (row - oq * a.group);
         const int64_t hq = (int64_t)a.group * a.c.heads, grow = (sp.q0 + oq) * hq + oh;
-        if (a.splits > 1) {
+        if (rg.ranges > 1) {
             const int64_t nrows = a.total_q * hq;
             float *po = a.part + ((int64_t)blockIdx.y * nrows + grow) * D + 4 * c;
 #pragma unroll
@@ -1008,8 +1024,8 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
 }
 
 // The partial results of key ranges joined, in the ranges' order: 16 rows per
-// workgroup, 16 lanes per row.
-template <class T, int D>
+// workgroup, 16 lanes per row.  ROWS and BLOCK are the kernel's that made them.
+template <class T, int D, int ROWS, int BLOCK>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int32_t row_tiles)
 {
     constexpr int DPL = D / 16;
@@ -1018,17 +1034,21 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int32_t row_
     const Span sp = span_of(a, b);
     const int32_t row = tile * 16 + (int32_t)threadIdx.x / 16, oc = (int32_t)threadIdx.x % 16;
     if (row >= sp.rows) return;
+    const int32_t r0 = row / ROWS * ROWS;
+    const Ranges rg = ranges_of<BLOCK>(a, key_lo(a, sp, r0 / a.group),
+                                       key_hi(a, sp, min(r0 + ROWS - 1, sp.rows - 1) / a.group));
+    if (rg.ranges == 1) return;
     const int32_t oq = row / a.group, oh = h * a.group + (row - oq * a.group);
     const int64_t hq = (int64_t)a.group * a.c.heads, nrows = a.total_q * hq;
     const int64_t grow = (sp.q0 + oq) * hq + oh;
     const float *ps = a.part + (int64_t)a.splits * nrows * D + grow * 2;
     const float NEG = -__builtin_inff();
     float m = NEG;
-    for (int32_t s = 0; s < a.splits; ++s) m = fmaxf(m, ps[(int64_t)s * nrows * 2]);
+    for (int32_t s = 0; s < rg.ranges; ++s) m = fmaxf(m, ps[(int64_t)s * nrows * 2]);
     float o[DPL], l = 0.f;
 #pragma unroll
     for (int j = 0; j < DPL; ++j) o[j] = 0.f;
-    for (int32_t s = 0; s < a.splits; ++s) {
+    for (int32_t s = 0; s < rg.ranges; ++s) {
         const float ls = ps[(int64_t)s * nrows * 2 + 1];
         if (ls == 0.f) continue;
         const float f = __builtin_amdgcn_exp2f(ps[(int64_t)s * nrows * 2] - m);
@@ -1054,10 +1074,16 @@ template <class T, int D> static hipError_t attn_t(const AttnArgs &a, hipStream_
         hipLaunchKernelGGL((attn_rows_kernel<T, D>), dim3((uint32_t)wgs, (uint32_t)a.splits), dim3(256), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
-    const int64_t row_tiles = a.chunk ? ChunkTile<T, D>::ROWS / 16 * (int64_t)a.tiles : a.tiles;
-    if ((int64_t)a.batch * a.c.heads * row_tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3((uint32_t)(a.batch * a.c.heads * row_tiles)), dim3(256), 0, s, a,
-                       (int32_t)row_tiles);
+    constexpr int ROWS = ChunkTile<T, D>::ROWS;
+    const int64_t row_tiles = a.chunk ? ROWS / 16 * (int64_t)a.tiles : a.tiles;
+    const int64_t joins = (int64_t)a.batch * a.c.heads * row_tiles;
+    if (joins > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (a.chunk)
+        hipLaunchKernelGGL((attn_join_kernel<T, D, ROWS, 64>), dim3((uint32_t)joins), dim3(256), 0, s, a,
+                           (int32_t)row_tiles);
+    else
+        hipLaunchKernelGGL((attn_join_kernel<T, D, 16, 32>), dim3((uint32_t)joins), dim3(256), 0, s, a,
+                           (int32_t)row_tiles);
     return hipGetLastError();
 }
 
