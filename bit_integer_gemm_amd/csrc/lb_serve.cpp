@@ -87,8 +87,8 @@ AttnPlan plan_attn(int64_t B, int64_t total_q, int64_t max_q, int64_t Hq, int64_
         // fp32, written and read, about as much as nine tiles of 64 keys: no ranges
         // once there are workgroups for all units, and none below 16 tiles.
         p.splits = std::min((int64_t)cu / wgs, blocks / 16);
-    } else if (wgs < 4 * (int64_t)cu) {
-        p.splits = std::min((4 * (int64_t)cu + wgs - 1) / wgs, (blocks + 7) / 8);
+    } else if (wgs < 8 * (int64_t)cu) {
+        p.splits = std::min((8 * (int64_t)cu + wgs - 1) / wgs, (blocks + 7) / 8);
     }
     p.splits = std::max<int64_t>(1, std::min<int64_t>(p.splits, 64));
     p.unit = (blocks + p.splits - 1) / p.splits;

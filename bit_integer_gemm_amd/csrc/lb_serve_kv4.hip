@@ -171,10 +171,10 @@ hipError_t launch_kv4_read(int ftype, const Kv4Cache &c, const int64_t *slots, v
 // B + u (bf16: B = 128, fp16: B = 64): one AND-OR for two nibbles, and a
 // constant to take off, -B sum_d q[d], which is the accumulator's start.
 // The values are summed the same way with the weights carrying the scale:
-//   sum_t p[t] v[t,d] = sum_t (p[t] s[t]) (u[t,d] - 8) + sum_t p[t] (m[t] + 8 s[t]).
-// Levels are taken about 8 so that a rounding of the weight counts against a
-// small number; the weight p s is split in two bf16 parts (16 bits in all, with
-// fp32's range, which fp16 scales or weights would not have).
+//   sum_t p[t] v[t,d] = sum_t (p[t] s[t]) u[t,d] + sum_t p[t] m[t].
+// The weight p s goes in two bf16 parts (16 bits in all, with fp32's range, which
+// fp16 scales or weights would not have), and the sum of both parts, by one more
+// product with ones, takes off what the nibbles' power of two adds.
 template <class T> struct Mfma;
 template <> struct Mfma<__bf16> {
     typedef bf16x8 frag;
@@ -238,6 +238,13 @@ __device__ inline int32_t page_of(const AttnArgs &a, int32_t key)
 {
     return (int32_t)(__umulhi((uint32_t)key, a.page_mul) >> a.page_shift);
 }
+// A page number of the table, by a scalar load.
+__device__ inline int32_t page_number(const AttnArgs &a, int32_t b, int32_t key)
+{
+    typedef const __attribute__((address_space(4))) int32_t *const_ptr;
+    return ((const_ptr)(uintptr_t)(a.table + (int64_t)b * a.ldt))[page_of(a, key)];
+}
+
 __device__ inline int32_t key_hi(const AttnArgs &a, const Span &s, int32_t qi)
 {
     return a.causal ? max(0, min(s.n, s.n - s.nq + qi + 1)) : s.n;
@@ -282,9 +289,13 @@ __device__ inline float sum_over_groups(float x)
 //   values    those eight keys are its share of the contraction as they stand:
 //             B: their weights; A: their levels of dims r D/16 .. (r+1) D/16 - 1,
 //             one MFMA per dim.  It ends with dims (4c+i) D/16 + j of row r.
-// Neither the weights nor the values change lanes.
+// Neither the weights nor the values change lanes, and nothing passes through LDS.
+// The next block's keys are asked for as soon as this one's are multiplied, its
+// values as soon as this one's are, into the same registers, and the numbers of
+// its pages a block earlier.  (Two blocks' worth of registers cost more in waves
+// per SIMD than the longer lead gave.)
 template <class T, int D>
-__global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
+__global__ __launch_bounds__(256, D == 256 ? 2 : 3) void attn_rows_kernel(AttnArgs a)
 {
     using MM = Mfma<T>;
     constexpr int KW = D / 32;     // words of a key a lane reads, = MFMAs per half-block
@@ -294,7 +305,7 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
     __shared__ float osum[4 * 16 * LDO];
     __shared__ float stat[4][16][4];
     const uint32_t lane = threadIdx.x & 63u;
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int32_t r = (int32_t)(lane & 15u), c = (int32_t)(lane >> 4);
     const int32_t bh = (int32_t)(blockIdx.x / (uint32_t)a.tiles), tile = (int32_t)(blockIdx.x % (uint32_t)a.tiles);
     const int32_t b = bh / a.c.heads, h = bh - b * a.c.heads;
@@ -302,16 +313,62 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
     const int32_t r0 = tile * 16;
     if (r0 >= sp.rows) return;
 
-    const int32_t row = min(r0 + r, sp.rows - 1);
-    const int32_t qi = row / a.group, hq = h * a.group + (row - qi * a.group);
-    const int32_t my_lo = key_lo(a, sp, qi), my_hi = key_hi(a, sp, qi);
     const int32_t qi_first = r0 / a.group, qi_last = min(r0 + 15, sp.rows - 1) / a.group;
     const int32_t lo = key_lo(a, sp, qi_first), hi = key_hi(a, sp, qi_last);
-    const int32_t full_lo = key_lo(a, sp, qi_last), full_hi = key_hi(a, sp, qi_first);
     const Ranges rg = ranges_of<32>(a, lo, hi);
     if ((int32_t)blockIdx.y >= rg.ranges) return;
     const int32_t first = rg.b0 + (int32_t)blockIdx.y * rg.per, last = min(rg.b0 + rg.nb, first + rg.per);
 
+    uint32_t kw[2][KW], vw[8][VW];
+    u32x4 kp[2], vp[2];
+    const int32_t hi16 = max(hi - 1, 0) & ~15;
+    const int64_t head_at = (int64_t)h * a.c.page, page_step = (int64_t)a.c.heads * a.c.page;
+    int32_t pages[2];
+    int64_t at[2];           // first vector of the half-blocks asked for
+    bool there[2], there1[2];
+    // (past the range the last half-block is read again)
+    auto ask = [&](int32_t blk) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) pages[s] = page_number(a, b, min(32 * blk + 16 * s, hi16));
+    };
+    auto fetch_keys = [&](int32_t blk) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int32_t t = min(32 * blk + 16 * s, hi16), p = pages[s];
+            there1[s] = (uint32_t)p < (uint32_t)a.c.pages;
+            at[s] = (there1[s] ? p : 0) * page_step + head_at + (t - page_of(a, t) * a.c.page);
+            const uint32_t *kk = (const uint32_t *)(a.c.k + at[s] * (D / 2)) + r * (D / 8) + c * KW;
+#pragma unroll
+            for (int j = 0; j < KW; ++j) kw[s][j] = kk[j];
+            kp[s] = *(const u32x4 *)(a.c.kp + at[s] + 4 * c);
+        }
+    };
+    auto fetch_vals = [&]() {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            vp[s] = *(const u32x4 *)(a.c.vp + at[s] + 4 * c);
+            const uint8_t *v = a.c.v + at[s] * (D / 2) + 4 * c * (D / 2) + r * (DPL / 2);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (DPL == 4) vw[4 * s + i][0] = *(const uint16_t *)(v + i * (D / 2));
+                else
+#pragma unroll
+                    for (int j = 0; j < VW; ++j) vw[4 * s + i][j] = ((const uint32_t *)(v + i * (D / 2)))[j];
+            }
+        }
+    };
+    const int32_t mine = first + wave;
+    if (mine < last) {
+        ask(mine);
+        fetch_keys(mine);
+        fetch_vals();
+        ask(mine + 4);
+    }
+
+    const int32_t row = min(r0 + r, sp.rows - 1);
+    const int32_t qi = row / a.group, hq = h * a.group + (row - qi * a.group);
+    const int32_t my_lo = key_lo(a, sp, qi), my_hi = key_hi(a, sp, qi);
+    const int32_t full_lo = key_lo(a, sp, qi_last), full_hi = key_hi(a, sp, qi_first);
     i32x4 qf[KW];
     float qsum = 0.f;
     {
@@ -325,7 +382,7 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
         }
         qsum = sum_over_groups(qsum);
     }
-    const float start = -MM::base * qsum;
+    const float start = -MM::base * qsum, qsum2 = qsum * a.scale2;
 
     const float NEG = -__builtin_inff();
     float m_run = NEG, l_run = 0.f, pm = 0.f;
@@ -334,38 +391,13 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
     for (int j = 0; j < DPL; ++j) acc[j] = f32x4{0, 0, 0, 0};
     const i32x4 one = {0x3F803F80, 0x3F803F80, 0x3F803F80, 0x3F803F80};
 
-    for (int32_t blk = first + (int32_t)wave; blk < last; blk += 4) {
+    for (int32_t blk = mine; blk < last; blk += 4) {
         const int32_t t0 = blk * 32;
-        int64_t vecs[2];
-        bool there[2];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int32_t t = t0 + 16 * s < hi ? t0 + 16 * s : t0;
-            const int32_t pi = page_of(a, t);
-            const int32_t p = __builtin_amdgcn_readfirstlane(a.table[(int64_t)b * a.ldt + pi]);
-            there[s] = (uint32_t)p < (uint32_t)a.c.pages;
-            vecs[s] = ((int64_t)(there[s] ? p : 0) * a.c.heads + h) * a.c.page + (t - pi * a.c.page);
-        }
-        uint32_t kw[2][KW], vw[8][VW];
-        u32x4 kp[2], vp[2];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const uint32_t *k = (const uint32_t *)(a.c.k + (vecs[s] + r) * (D / 2)) + c * KW;
-#pragma unroll
-            for (int j = 0; j < KW; ++j) kw[s][j] = k[j];
-            kp[s] = *(const u32x4 *)(a.c.kp + vecs[s] + 4 * c);
-            vp[s] = *(const u32x4 *)(a.c.vp + vecs[s] + 4 * c);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint8_t *v = a.c.v + (vecs[s] + 4 * c + i) * (D / 2) + r * (DPL / 2);
-                if constexpr (DPL == 4) vw[4 * s + i][0] = *(const uint16_t *)v;
-                else
-#pragma unroll
-                    for (int j = 0; j < VW; ++j) vw[4 * s + i][j] = ((const uint32_t *)v)[j];
-            }
-        }
-        // scores
+        there[0] = there1[0];
+        there[1] = there1[1];
+        // scores in units of log 2 above the running maximum
         float sc[2][4];
+        const float top = m_run == NEG ? 0.f : m_run;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             f32x4 x = {start, start, start, start};
@@ -377,26 +409,37 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                sc[s][i] = (lo_f32<T>(kp[s][i]) * x[i] + hi_f32<T>(kp[s][i]) * qsum) * a.scale2;
+                sc[s][i] = __builtin_fmaf(lo_f32<T>(kp[s][i]), x[i] * a.scale2,
+                                          __builtin_fmaf(hi_f32<T>(kp[s][i]), qsum2, -top));
         }
+        fetch_keys(blk + 4);
+        ask(blk + 8);
         const bool whole = t0 >= full_lo && t0 + 32 <= full_hi && there[0] && there[1];
-        bool ok[2][4];
+        uint32_t seen = 0xFFu;
+        if (!whole) {
+            asm volatile("" ::: "memory");  // keeps the comparisons in this branch
+            const int32_t from = my_lo - t0 - 4 * c, to = my_hi - t0 - 4 * c;
+            seen = 0;
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+            for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int32_t t = t0 + 16 * s + 4 * c + i;
-                ok[s][i] = whole || (there[s] && t >= my_lo && t < my_hi);
-                if (!ok[s][i]) sc[s][i] = NEG;
-            }
-        // running maximum: taken anew only when a score passes it by 2^8
+                for (int i = 0; i < 4; ++i) {
+                    const bool ok = 16 * s + i >= from && 16 * s + i < to && there[s];
+                    seen |= ok ? 1u << (4 * s + i) : 0u;
+                    if (!ok) sc[s][i] = NEG;
+                }
+        }
+        // The running maximum is taken anew only when a score passes it by 2^8, and
+        // first of all; only then do the lanes of a row compare.
         float mx = sc[0][0];
 #pragma unroll
         for (int e = 1; e < 8; ++e) mx = fmaxf(mx, sc[e / 4][e % 4]);
-        mx = max_over_groups(mx);
-        if (__any(mx > m_run + 8.f)) {
-            const float m_new = fmaxf(m_run, mx);
+        if (__any(mx > 8.f || m_run == NEG)) {
+            const float m_new = fmaxf(m_run, max_over_groups(mx) + top);
+            const float m_use = m_new == NEG ? 0.f : m_new;
             const float al = m_run == NEG ? 0.f : __builtin_amdgcn_exp2f(m_run - m_new);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sc[e / 4][e % 4] += top - m_use;
             m_run = m_new;
             l_run *= al;
             pm *= al;
@@ -404,18 +447,17 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
 #pragma unroll
             for (int j = 0; j < DPL; ++j) acc[j] *= al;
         }
-        const float m_use = m_run == NEG ? 0.f : m_run;
         i32x4 whi, wlo;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             float w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float p = __builtin_amdgcn_exp2f(sc[s][i] - m_use);
-                const float vs = lo_f32<T>(vp[s][i]), vm = hi_f32<T>(vp[s][i]);
+                const float p = __builtin_amdgcn_exp2f(sc[s][i]);
+                const bool ok = (seen >> (4 * s + i)) & 1u;
                 l_run += p;
-                pm += ok[s][i] ? p * (vm + 8.f * vs) : 0.f;
-                w[i] = ok[s][i] ? p * vs : 0.f;
+                pm = __builtin_fmaf(p, ok ? hi_f32<T>(vp[s][i]) : 0.f, pm);
+                w[i] = p * (ok ? lo_f32<T>(vp[s][i]) : 0.f);
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -447,6 +489,7 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
                     acc[d] = MfmaV::mul(f, wlo, acc[d]);
                 }
             }
+        fetch_vals();
     }
 
     // the four waves' results
@@ -457,7 +500,7 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
         stat[wave][r][1] = l_run;
         stat[wave][r][2] = pm;
     }
-    const float off = (MfmaV::base + 8.f) * ones.x;
+    const float off = MfmaV::base * ones.x;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -549,13 +592,6 @@ template <class T, int D> struct ChunkTile {
     }
     static __device__ inline int val_at(int n, int q, int c) { return n * VROW + 16 * ((4 * q + c) ^ (n & 7)); }
 };
-
-// A page number of the table, by a scalar load.
-__device__ inline int32_t page_number(const AttnArgs &a, int32_t b, int32_t key)
-{
-    typedef const __attribute__((address_space(4))) int32_t *const_ptr;
-    return ((const_ptr)(uintptr_t)(a.table + (int64_t)b * a.ldt))[page_of(a, key)];
-}
 
 template <class T, int D>
 __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
@@ -724,7 +760,7 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
             g[64] = (_Float16)(in ? mv : 0.f);
         } else {
             f[128] = s0;
-            f[192] = m0 + 8.f * s0;
+            f[192] = m0;
         }
         ((uint32_t *)(prm + LT::FLAG_AT))[part] = there ? 1u << part : 0u;
     };
@@ -997,7 +1033,7 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
         if constexpr (WHOLE) add += __shfl_xor(add, 16), add += __shfl_xor(add, 32);  // 0, or NaN in any
         if (row >= sp.rows) continue;
         const float mul = WHOLE ? 1.f / vscale : 1.f;
-        const float off = WHOLE ? -add : (MfmaV::base + 8.f) * ones[x].x - add;
+        const float off = WHOLE ? -add : MfmaV::base * ones[x].x - add;
         const int32_t oq = row / a.group, oh = h * a.group + (row - oq * a.group);
         const int64_t hq = (int64_t)a.group * a.c.heads, grow = (sp.q0 + oq) * hq + oh;
         if (rg.ranges > 1) {
@@ -1023,16 +1059,18 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
     }
 }
 
-// The partial results of key ranges joined, in the ranges' order: 16 rows per
-// workgroup, 16 lanes per row.  ROWS and BLOCK are the kernel's that made them.
+// The partial results of key ranges joined, in the ranges' order: a wave per row,
+// whose lanes read whole partial rows, eight ranges at a time.  ROWS and BLOCK are
+// the kernel's that made them.
 template <class T, int D, int ROWS, int BLOCK>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int32_t row_tiles)
 {
-    constexpr int DPL = D / 16;
+    constexpr int DPL = D / 64;
+    const int32_t lane = (int32_t)(threadIdx.x & 63u);
     const int32_t bh = (int32_t)(blockIdx.x / (uint32_t)row_tiles), tile = (int32_t)(blockIdx.x % (uint32_t)row_tiles);
     const int32_t b = bh / a.c.heads, h = bh - b * a.c.heads;
     const Span sp = span_of(a, b);
-    const int32_t row = tile * 16 + (int32_t)threadIdx.x / 16, oc = (int32_t)threadIdx.x % 16;
+    const int32_t row = tile * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     if (row >= sp.rows) return;
     const int32_t r0 = row / ROWS * ROWS;
     const Ranges rg = ranges_of<BLOCK>(a, key_lo(a, sp, r0 / a.group),
@@ -1041,27 +1079,42 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int32_t row_
     const int32_t oq = row / a.group, oh = h * a.group + (row - oq * a.group);
     const int64_t hq = (int64_t)a.group * a.c.heads, nrows = a.total_q * hq;
     const int64_t grow = (sp.q0 + oq) * hq + oh;
-    const float *ps = a.part + (int64_t)a.splits * nrows * D + grow * 2;
     const float NEG = -__builtin_inff();
-    float m = NEG;
-    for (int32_t s = 0; s < rg.ranges; ++s) m = fmaxf(m, ps[(int64_t)s * nrows * 2]);
-    float o[DPL], l = 0.f;
+    // lane s holds range s's maximum and sum (at most 64 ranges)
+    f32x2 ml = {NEG, 0.f};
+    if (lane < rg.ranges)
+        ml = *(const f32x2 *)(a.part + (int64_t)a.splits * nrows * D + ((int64_t)lane * nrows + grow) * 2);
+    float m = ml.x;
+#pragma unroll
+    for (int d = 32; d; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+    const float f = ml.y == 0.f ? 0.f : __builtin_amdgcn_exp2f(ml.x - m);
+    float l = f * ml.y;
+#pragma unroll
+    for (int d = 32; d; d >>= 1) l += __shfl_xor(l, d);
+    float o[DPL];
 #pragma unroll
     for (int j = 0; j < DPL; ++j) o[j] = 0.f;
-    for (int32_t s = 0; s < rg.ranges; ++s) {
-        const float ls = ps[(int64_t)s * nrows * 2 + 1];
-        if (ls == 0.f) continue;
-        const float f = __builtin_amdgcn_exp2f(ps[(int64_t)s * nrows * 2] - m);
-        l += f * ls;
-        const float *po = a.part + ((int64_t)s * nrows + grow) * D + oc * DPL;
+    const float *po = a.part + grow * D + lane * DPL;
+    for (int32_t s0 = 0; s0 < rg.ranges; s0 += 8) {
+        float w[8], v[8][DPL];
 #pragma unroll
-        for (int j = 0; j < DPL; ++j) o[j] += f * po[j];
+        for (int k = 0; k < 8; ++k) {
+            const int32_t s = min(s0 + k, rg.ranges - 1);
+            w[k] = s0 + k < rg.ranges ? __shfl(f, s) : 0.f;
+#pragma unroll
+            for (int j = 0; j < DPL; ++j) v[k][j] = po[(int64_t)s * nrows * D + j];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (w[k] != 0.f)   // a range that saw nothing holds zeros; a NaN weight counts
+#pragma unroll
+                for (int j = 0; j < DPL; ++j) o[j] = __builtin_fmaf(w[k], v[k][j], o[j]);
     }
     const float inv = l == 0.f ? 0.f : 1.0f / l;
-    T *out = (T *)a.out + (sp.q0 + oq) * a.ldo + (int64_t)oh * D + oc * DPL;
+    T *out = (T *)a.out + (sp.q0 + oq) * a.ldo + (int64_t)oh * D + lane * DPL;
 #pragma unroll
     for (int j = 0; j < DPL; ++j) out[j] = (T)(o[j] * inv);
-    if (a.lse && oc == 0) a.lse[grow] = l == 0.f ? NEG : (m + __builtin_log2f(l)) * 0.6931471805599453f;
+    if (a.lse && lane == 0) a.lse[grow] = l == 0.f ? NEG : (m + __builtin_log2f(l)) * 0.6931471805599453f;
 }
 
 template <class T, int D> static hipError_t attn_t(const AttnArgs &a, hipStream_t s)
@@ -1075,7 +1128,7 @@ template <class T, int D> static hipError_t attn_t(const AttnArgs &a, hipStream_
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
     constexpr int ROWS = ChunkTile<T, D>::ROWS;
-    const int64_t row_tiles = a.chunk ? ROWS / 16 * (int64_t)a.tiles : a.tiles;
+    const int64_t row_tiles = (a.chunk ? ROWS / 4 : 4) * (int64_t)a.tiles;
     const int64_t joins = (int64_t)a.batch * a.c.heads * row_tiles;
     if (joins > 0x7FFFFFFF) return hipErrorInvalidValue;
     if (a.chunk)
