@@ -176,6 +176,16 @@ hipError_t launch_kv4_read(int ftype, const Kv4Cache &c, const int64_t *slots, v
 // fp16 scales or weights would not have), and the sum of both parts, by one more
 // product with ones, takes off what the nibbles' power of two adds.
 template <class T> struct Mfma;
+// A constant kept in a vector register: AND-OR takes one scalar operand, and with
+// mask and magic both scalar the compiler makes two instructions of it.
+__device__ inline uint32_t in_vgpr(uint32_t x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
+// The low halves, and the high halves, of two words.
+__device__ inline uint32_t low_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
+__device__ inline uint32_t high_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
 template <> struct Mfma<__bf16> {
     typedef bf16x8 frag;
     static constexpr float base = 128.f;
@@ -185,8 +195,8 @@ template <> struct Mfma<__bf16> {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(frag, a), __builtin_bit_cast(frag, b), c,
                                                        0, 0, 0);
     }
-    // nibbles i and i+4 of w as a pair
-    static __device__ inline uint32_t pair(uint32_t w, int i) { return ((w >> (4 * i)) & mask) | magic; }
+    // nibbles i and i+4 of w as a pair; mg is in_vgpr(magic)
+    static __device__ inline uint32_t pair(uint32_t w, int i, uint32_t mg) { return ((w >> (4 * i)) & mask) | mg; }
 };
 template <> struct Mfma<_Float16> {
     typedef f16x8 frag;
@@ -197,9 +207,9 @@ template <> struct Mfma<_Float16> {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(frag, a), __builtin_bit_cast(frag, b), c,
                                                       0, 0, 0);
     }
-    static __device__ inline uint32_t pair(uint32_t w, int i)
+    static __device__ inline uint32_t pair(uint32_t w, int i, uint32_t mg)
     {
-        return ((i == 0 ? w << 4 : w >> (4 * i - 4)) & mask) | magic;
+        return ((i == 0 ? w << 4 : w >> (4 * i - 4)) & mask) | mg;
     }
 };
 using MfmaV = Mfma<__bf16>;  // the values' product, whatever T is
@@ -389,6 +399,7 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 3) void attn_rows_kernel(AttnAr
     f32x4 acc[DPL], ones = {0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < DPL; ++j) acc[j] = f32x4{0, 0, 0, 0};
+    const uint32_t mk = in_vgpr(MM::magic), mv = in_vgpr(MfmaV::magic);
     const i32x4 one = {0x3F803F80, 0x3F803F80, 0x3F803F80, 0x3F803F80};
 
     for (int32_t blk = mine; blk < last; blk += 4) {
@@ -404,7 +415,8 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 3) void attn_rows_kernel(AttnAr
 #pragma unroll
             for (int j = 0; j < KW; ++j) {
                 const uint32_t w = kw[s][j];
-                x = MM::mul(i32x4{(int)MM::pair(w, 0), (int)MM::pair(w, 1), (int)MM::pair(w, 2), (int)MM::pair(w, 3)},
+                x = MM::mul(i32x4{(int)MM::pair(w, 0, mk), (int)MM::pair(w, 1, mk), (int)MM::pair(w, 2, mk),
+                                  (int)MM::pair(w, 3, mk)},
                             qf[j], x);
             }
 #pragma unroll
@@ -415,18 +427,18 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 3) void attn_rows_kernel(AttnAr
         fetch_keys(blk + 4);
         ask(blk + 8);
         const bool whole = t0 >= full_lo && t0 + 32 <= full_hi && there[0] && there[1];
-        uint32_t seen = 0xFFu;
         if (!whole) {
             asm volatile("" ::: "memory");  // keeps the comparisons in this branch
             const int32_t from = my_lo - t0 - 4 * c, to = my_hi - t0 - 4 * c;
-            seen = 0;
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const bool ok = 16 * s + i >= from && 16 * s + i < to && there[s];
-                    seen |= ok ? 1u << (4 * s + i) : 0u;
-                    if (!ok) sc[s][i] = NEG;
+                    if (!ok) {  // whatever the place holds
+                        sc[s][i] = NEG;
+                        vp[s][i] = 0;
+                    }
                 }
         }
         // The running maximum is taken anew only when a score passes it by 2^8, and
@@ -454,10 +466,9 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 3) void attn_rows_kernel(AttnAr
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float p = __builtin_amdgcn_exp2f(sc[s][i]);
-                const bool ok = (seen >> (4 * s + i)) & 1u;
                 l_run += p;
-                pm = __builtin_fmaf(p, ok ? hi_f32<T>(vp[s][i]) : 0.f, pm);
-                w[i] = p * (ok ? lo_f32<T>(vp[s][i]) : 0.f);
+                pm = __builtin_fmaf(p, hi_f32<T>(vp[s][i]), pm);
+                w[i] = p * lo_f32<T>(vp[s][i]);
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -477,13 +488,13 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 3) void attn_rows_kernel(AttnAr
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t u0 = vw[2 * i][v], u1 = vw[2 * i + 1][v];
-                    x[i] = half ? (u0 >> 16) | (u1 & 0xFFFF0000u) : (u0 & 0xFFFFu) | (u1 << 16);
+                    x[i] = half ? high_halves(u0, u1) : low_halves(u0, u1);
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     i32x4 f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) f[i] = (int)MfmaV::pair(x[i], j);
+                    for (int i = 0; i < 4; ++i) f[i] = (int)MfmaV::pair(x[i], j, mv);
                     const int d = 8 * v + 4 * half + j;
                     acc[d] = MfmaV::mul(f, whi, acc[d]);
                     acc[d] = MfmaV::mul(f, wlo, acc[d]);
@@ -701,6 +712,7 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
         vd = ((wave >> 1) * 16 + v) * DPT;
     }
     uint32_t kw[KH], vw[8], kpw, vpw;
+    const uint32_t mk = in_vgpr(MM::magic), mv = in_vgpr(WHOLE ? Mfma<_Float16>::magic : MfmaV::magic);
     const int32_t hi16 = max(hi - 1, 0) & ~15;
     const int64_t head_at = (int64_t)h * a.c.page, page_step = (int64_t)a.c.heads * a.c.page;
     // Page numbers of the half-blocks to turn next, asked for a tile ahead: keys 16
@@ -741,7 +753,7 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
     // numbers, dim j of the values.
     auto turn_key_word = [&](int j, char *kbuf) {
         *(i32x4 *)(kbuf + LT::key_at(16 * part + r, khalf * KH + j, c)) = i32x4{
-            (int)MM::pair(kw[j], 0), (int)MM::pair(kw[j], 1), (int)MM::pair(kw[j], 2), (int)MM::pair(kw[j], 3)};
+            (int)MM::pair(kw[j], 0, mk), (int)MM::pair(kw[j], 1, mk), (int)MM::pair(kw[j], 2, mk), (int)MM::pair(kw[j], 3, mk)};
     };
     auto turn_numbers = [&](int32_t t, char *prm) {
         // (lanes and waves that share a key write the same numbers)
@@ -772,10 +784,10 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
             if constexpr (DPT == 1) x >>= 4 * (vd & 1);
             if constexpr (WHOLE) {
                 const char *g = prm + 512 + 2 * (32 * kb + 16 * (i / 2) + 4 * vc + 2 * (i % 2));
-                const f16x2 u = __builtin_bit_cast(f16x2, Mfma<_Float16>::pair(x, j)) - (_Float16)72.f;
+                const f16x2 u = __builtin_bit_cast(f16x2, Mfma<_Float16>::pair(x, j, mv)) - (_Float16)72.f;
                 f[i] = __builtin_bit_cast(int, __builtin_elementwise_fma(u, *(const f16x2 *)g, *(const f16x2 *)(g + 128)));
             } else {
-                f[i] = (int)MfmaV::pair(x, j);
+                f[i] = (int)MfmaV::pair(x, j, mv);
             }
         }
         *(i32x4 *)(vbuf + LT::val_at(vd + j, kb, vc)) = f;
