@@ -287,95 +287,121 @@ def ops(dtype: int, M: int, N: int, K: int) -> int:
 # in 4 bits and attention over it
 # ---------------------------------------------------------------------------
 
-_FTYPES = {}
+# These run once per layer and token, where the host's time counts: one pass over the
+# operands' attributes, and words only for an operand that is refused.
 
+class _Torch:
+    """torch and what the checks below take from it, looked up at the first call."""
 
-def _ftype(t, what, short=False):
-    if not _FTYPES:
+    def __init__(self):
         import torch
-        _FTYPES.update({torch.bfloat16: LB_BF16, torch.float16: LB_F16, torch.float32: LB_F32})
-    f = _FTYPES.get(t.dtype)
-    if f is None or (short and f == LB_F32):
-        raise TypeError(f"{what}: dtype {t.dtype} is not a {'16-bit ' if short else ''}floating type of the library")
+        self.torch = torch
+        self.i8, self.u8, self.i32, self.i64, self.f32 = (torch.int8, torch.uint8, torch.int32, torch.int64,
+                                                          torch.float32)
+        self.any = {torch.bfloat16: LB_BF16, torch.float16: LB_F16, torch.float32: LB_F32}
+        self.short = {torch.bfloat16: LB_BF16, torch.float16: LB_F16}
+        self.current_stream = torch._C._cuda_getCurrentRawStream
+
+
+_t = None
+
+
+def _torch():
+    global _t
+    if _t is None:
+        _t = _Torch()
+    return _t
+
+
+def _refuse(t, what, dtype, shape, device, dense=True):
+    """Raises for an operand that is not a GPU tensor of this type, shape and device."""
+    if t.get_device() < 0:
+        raise ValueError(f"{what} must be on a GPU (got {t.device})")
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != tuple(shape):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{what} is on another GPU")
+    raise ValueError(f"{what}: strides {t.stride()}; " +
+                     ("it must be contiguous" if dense else "only the first dimension may be strided"))
+
+
+def _dense(t, what, dtype, shape, device):
+    """Address of a contiguous tensor of this type, shape and GPU."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device or device < 0:
+        _refuse(t, what, dtype, shape, device)
+    return t.data_ptr()
+
+
+def _rows(t, what, dtype, shape, device, row):
+    """(address, elements between rows) of a tensor whose rows of `row` elements are dense, `row` the product
+    of all dimensions but the first."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or device < 0:
+        _refuse(t, what, dtype, shape, device)
+    if t.is_contiguous():
+        return t.data_ptr(), row
+    st, dense = t.stride(), 1
+    for d in range(len(st) - 1, 0, -1):
+        if st[d] != dense and shape[d] != 1:
+            _refuse(t, what, dtype, shape, device, dense=False)
+        dense *= shape[d]
+    return t.data_ptr(), st[0] if shape[0] > 1 else row
+
+
+def _ftype(table, t, what):
+    f = table.get(t.dtype)
+    if f is None:
+        raise TypeError(f"{what}: dtype {t.dtype} not in {tuple(table)}")
     return f
 
 
-def _rows(t, dtype, shape, what):
-    """A GPU tensor whose last dimensions are dense and whose first has any stride; returns that stride."""
-    if t.dtype != dtype or not t.is_cuda or t.shape != shape:
-        raise ValueError(f"{what}: expected a {dtype} GPU tensor of shape {tuple(shape)}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    st = t.stride()
-    dense = 1
-    for d in range(len(st) - 1, 0, -1):
-        if st[d] != dense and shape[d] != 1:
-            raise ValueError(f"{what}: only the first dimension may be strided (strides {st})")
-        dense *= shape[d]
-    return st[0] if shape[0] > 1 else max(st[0], dense)
-
-
-def _dense(t, dtype, shape, what):
-    if t.dtype != dtype or not t.is_cuda or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous {dtype} GPU tensor of shape {tuple(shape)}, "
-                         f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
-
-
-def _raw_stream(stream, device):
-    import torch
+def _on(T, stream, device):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device)
+        return T.current_stream(device)
     return int(getattr(stream, "cuda_stream", stream))
 
 
-def _scratch(workspace, needed, t, stream, what):
-    """(address, bytes) of a caller's workspace, or of one from torch's allocator
-    (then ordered on torch's current stream, so not with a stream argument), and
-    the tensor that keeps it."""
-    import torch
-    if workspace is None:
-        if needed == 0:
-            return None, 0, None
-        if stream is not None:
-            raise ValueError(f"{what}: a call on a stream of its own needs a workspace of {needed} bytes")
-        workspace = torch.empty(needed, dtype=torch.uint8, device=t.device)
-    elif not workspace.is_contiguous() or workspace.get_device() != t.get_device():
-        raise ValueError(f"{what}: the workspace must be contiguous and on the operands' GPU")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+def _scratch(T, workspace, needed, device, stream, what):
+    """The workspace tensor: the caller's, or one from torch's allocator (then ordered on torch's current
+    stream, so not with a stream argument), or None where none is needed."""
+    if workspace is not None:
+        if not workspace.is_contiguous() or workspace.get_device() != device:
+            raise ValueError(f"{what}: the workspace must be contiguous and on the operands' GPU")
+        return workspace
+    if needed == 0:
+        return None
+    if stream is not None:
+        raise ValueError(f"{what}: a call on a stream of its own needs a workspace of {needed} bytes")
+    return T.torch.empty(needed, dtype=T.u8, device=f"cuda:{device}")
 
 
 def lb_quant_rows_s8(X, Q, sx, stream=None) -> None:
     """Rows of X (M, K) bf16, fp16 or fp32 (rows may be strided) quantised to Q (M, K) int8 with a scale
     each, sx (M,) fp32 = largest magnitude / 127."""
-    import torch
+    T = _torch()
     M, K = X.shape
-    ldx = _rows(X, X.dtype, (M, K), "X")
-    _dense(Q, torch.int8, (M, K), "Q")
-    _dense(sx, torch.float32, (M,), "sx")
-    f = _ftype(X, "X")
-    dev = _same_device(X, Q, sx)
-    _raise(load().lb_quant_rows_s8(X.data_ptr(), ldx, Q.data_ptr(), sx.data_ptr(), M, K, f,
-                                   _raw_stream(stream, dev)), "lb_quant_rows_s8")
+    dev = X.get_device()
+    f = _ftype(T.any, X, "X")
+    x, ldx = _rows(X, "X", X.dtype, (M, K), dev, K)
+    st = load().lb_quant_rows_s8(x, ldx, _dense(Q, "Q", T.i8, (M, K), dev), _dense(sx, "sx", T.f32, (M,), dev),
+                                 M, K, f, _on(T, stream, dev))
+    _raise(st, "lb_quant_rows_s8")
 
 
 def lb_gemm_s8_scaled(X, W, sx, sw, out, bias=None, stream=None) -> None:
     """out (M, N) bf16, fp16 or fp32 = (X (M, K) int8 x W (N, K) int8) * sx[m] * sw[n] + bias[n]; bias (N,)
     of out's type or None."""
-    import torch
+    T = _torch()
     M, K = X.shape
     N = W.shape[0]
-    _dense(X, torch.int8, (M, K), "X")
-    _dense(W, torch.int8, (N, K), "W")
-    _dense(sx, torch.float32, (M,), "sx")
-    _dense(sw, torch.float32, (N,), "sw")
-    _dense(out, out.dtype, (M, N), "out")
-    f = _ftype(out, "out")
-    dev = _same_device(X, W, sx, sw, out)
-    if bias is not None:
-        _dense(bias, out.dtype, (N,), "bias")
-        _same_device(bias, out)
-    _raise(load().lb_gemm_s8_scaled(X.data_ptr(), W.data_ptr(), sx.data_ptr(), sw.data_ptr(),
-                                    None if bias is None else bias.data_ptr(), out.data_ptr(), M, N, K, f,
-                                    _raw_stream(stream, dev)), "lb_gemm_s8_scaled")
+    dev, dt = X.get_device(), out.dtype
+    f = _ftype(T.any, out, "out")
+    st = load().lb_gemm_s8_scaled(
+        _dense(X, "X", T.i8, (M, K), dev), _dense(W, "W", T.i8, (N, K), dev), _dense(sx, "sx", T.f32, (M,), dev),
+        _dense(sw, "sw", T.f32, (N,), dev), None if bias is None else _dense(bias, "bias", dt, (N,), dev),
+        _dense(out, "out", dt, (M, N), dev), M, N, K, f, _on(T, stream, dev))
+    _raise(st, "lb_gemm_s8_scaled")
 
 
 def lb_linear_w8a8_workspace(M: int, K: int, N: int) -> int:
@@ -388,39 +414,35 @@ def lb_linear_w8a8(X, W, sw, out, bias=None, workspace=None, stream=None) -> Non
     magnitude of each row of X (M, K).  X (rows may be strided), bias and out share a type: bf16, fp16 or
     fp32.  workspace: a GPU tensor of at least lb_linear_w8a8_workspace(M, K, N) bytes, or None for one
     from torch's allocator."""
-    import torch
+    T = _torch()
+    lib = load()
     M, K = X.shape
     N = W.shape[0]
-    ldx = _rows(X, X.dtype, (M, K), "X")
-    _dense(W, torch.int8, (N, K), "W")
-    _dense(sw, torch.float32, (N,), "sw")
-    _dense(out, X.dtype, (M, N), "out")
-    f = _ftype(X, "X")
-    dev = _same_device(X, W, sw, out)
-    if bias is not None:
-        _dense(bias, X.dtype, (N,), "bias")
-        _same_device(bias, out)
-    lib = load()
-    need = 0 if workspace is not None else lib.lb_linear_w8a8_workspace(M, K, N)
-    ws, size, kept = _scratch(workspace, need, X, stream, "lb_linear_w8a8")
-    _raise(lib.lb_linear_w8a8(X.data_ptr(), ldx, W.data_ptr(), sw.data_ptr(),
-                              None if bias is None else bias.data_ptr(), out.data_ptr(), M, N, K, f, ws, size,
-                              _raw_stream(stream, dev)), "lb_linear_w8a8")
+    dev, dt = X.get_device(), X.dtype
+    f = _ftype(T.any, X, "X")
+    x, ldx = _rows(X, "X", dt, (M, K), dev, K)
+    w = _dense(W, "W", T.i8, (N, K), dev)
+    s = _dense(sw, "sw", T.f32, (N,), dev)
+    o = _dense(out, "out", dt, (M, N), dev)
+    b = None if bias is None else _dense(bias, "bias", dt, (N,), dev)
+    ws = _scratch(T, workspace, 0 if workspace is not None else lib.lb_linear_w8a8_workspace(M, K, N), dev, stream,
+                  "lb_linear_w8a8")
+    st = lib.lb_linear_w8a8(x, ldx, w, s, b, o, M, N, K, f, None if ws is None else ws.data_ptr(),
+                            0 if ws is None else ws.nbytes, _on(T, stream, dev))
+    _raise(st, "lb_linear_w8a8")
 
 
-def _kv4_cache(Kc, Vc, Kp, Vp, heads, D, like):
-    """Checks the four tensors of a cache; returns (pages, page)."""
-    import torch
+def _kv4_cache(T, Kc, Vc, Kp, Vp, heads, D, dtype, dev):
+    """(pages, page, addresses) of the four tensors of a cache."""
     if Kc.dim() != 4:
         raise ValueError(f"Kc: expected (pages, heads, page, D/2), got {tuple(Kc.shape)}")
-    pages, h, page, half = Kc.shape
+    shape = Kc.shape
+    pages, h, page, half = shape
     if h != heads or 2 * half != D:
-        raise ValueError(f"Kc: shape {tuple(Kc.shape)} does not fit {heads} heads of {D}")
-    _dense(Kc, torch.uint8, (pages, heads, page, half), "Kc")
-    _dense(Vc, torch.uint8, (pages, heads, page, half), "Vc")
-    _dense(Kp, like.dtype, (pages, heads, page, 2), "Kp")
-    _dense(Vp, like.dtype, (pages, heads, page, 2), "Vp")
-    return pages, page
+        raise ValueError(f"Kc: shape {tuple(shape)} does not fit {heads} heads of {D}")
+    prm = (pages, h, page, 2)
+    return pages, page, (_dense(Kc, "Kc", T.u8, shape, dev), _dense(Vc, "Vc", T.u8, shape, dev),
+                         _dense(Kp, "Kp", dtype, prm, dev), _dense(Vp, "Vp", dtype, prm, dev))
 
 
 def lb_kv4_write(K, V, slots, Kc, Vc, Kp, Vp, stream=None) -> None:
@@ -428,33 +450,29 @@ def lb_kv4_write(K, V, slots, Kc, Vc, Kp, Vp, stream=None) -> None:
     to 4 bits into their slots (T,) int64 of the paged cache: Kc, Vc (pages, heads, page, D/2) uint8 and
     Kp, Vp (pages, heads, page, 2), scale and minimum of each vector in K's type.  Slots outside the cache
     (-1) are skipped."""
-    import torch
-    T, H, D = K.shape
-    ldk = _rows(K, K.dtype, (T, H, D), "K")
-    ldv = _rows(V, K.dtype, (T, H, D), "V")
-    _dense(slots, torch.int64, (T,), "slots")
-    f = _ftype(K, "K", short=True)
-    pages, page = _kv4_cache(Kc, Vc, Kp, Vp, H, D, K)
-    dev = _same_device(K, V, slots, Kc, Vc, Kp, Vp)
-    _raise(load().lb_kv4_write(K.data_ptr(), V.data_ptr(), ldk, ldv, slots.data_ptr(), Kc.data_ptr(),
-                               Vc.data_ptr(), Kp.data_ptr(), Vp.data_ptr(), T, H, D, pages, page, f,
-                               _raw_stream(stream, dev)), "lb_kv4_write")
+    T = _torch()
+    shape = n, H, D = K.shape
+    dev, dt = K.get_device(), K.dtype
+    f = _ftype(T.short, K, "K")
+    k, ldk = _rows(K, "K", dt, shape, dev, H * D)
+    v, ldv = _rows(V, "V", dt, shape, dev, H * D)
+    pages, page, cache = _kv4_cache(T, Kc, Vc, Kp, Vp, H, D, dt, dev)
+    st = load().lb_kv4_write(k, v, ldk, ldv, _dense(slots, "slots", T.i64, (n,), dev), *cache, n, H, D, pages,
+                             page, f, _on(T, stream, dev))
+    _raise(st, "lb_kv4_write")
 
 
 def lb_kv4_read(Kc, Vc, Kp, Vp, slots, K, V, stream=None) -> None:
     """Keys and values of slots (T,) int64 of the cache into K and V (T, heads, D); slots outside it read
     as zeros."""
-    import torch
-    T, H, D = K.shape
-    _dense(K, K.dtype, (T, H, D), "K")
-    _dense(V, K.dtype, (T, H, D), "V")
-    _dense(slots, torch.int64, (T,), "slots")
-    f = _ftype(K, "K", short=True)
-    pages, page = _kv4_cache(Kc, Vc, Kp, Vp, H, D, K)
-    dev = _same_device(K, V, slots, Kc, Vc, Kp, Vp)
-    _raise(load().lb_kv4_read(Kc.data_ptr(), Vc.data_ptr(), Kp.data_ptr(), Vp.data_ptr(), slots.data_ptr(),
-                              K.data_ptr(), V.data_ptr(), T, H, D, pages, page, f, _raw_stream(stream, dev)),
-           "lb_kv4_read")
+    T = _torch()
+    shape = n, H, D = K.shape
+    dev, dt = K.get_device(), K.dtype
+    f = _ftype(T.short, K, "K")
+    pages, page, cache = _kv4_cache(T, Kc, Vc, Kp, Vp, H, D, dt, dev)
+    st = load().lb_kv4_read(*cache, _dense(slots, "slots", T.i64, (n,), dev), _dense(K, "K", dt, shape, dev),
+                            _dense(V, "V", dt, shape, dev), n, H, D, pages, page, f, _on(T, stream, dev))
+    _raise(st, "lb_kv4_read")
 
 
 def lb_attn_kv4_workspace(B: int, total_q: int, max_q: int, Hq: int, Hkv: int, D: int, max_len: int,
@@ -473,30 +491,26 @@ def lb_attn_kv4(Q, Kc, Vc, Kp, Vp, table, q_off, lens, out, lse=None, max_q=None
     sequence (default: total_q); max_len: about the longest sequence, for the planning (default: the
     table's width).  scale defaults to D ** -0.5; window > 0 keeps the last window keys.  A query that sees
     nothing gets zeros.  workspace: as for lb_linear_w8a8; a smaller one makes fewer key ranges."""
-    import torch
-    total, Hq, D = Q.shape
-    B, width = table.shape
-    Hkv = Kc.shape[1] if Kc.dim() == 4 else 0
-    ldq = _rows(Q, Q.dtype, (total, Hq, D), "Q")
-    ldo = _rows(out, Q.dtype, (total, Hq, D), "out")
-    ldt = _rows(table, torch.int32, (B, width), "table")
-    _dense(q_off, torch.int32, (B + 1,), "q_off")
-    _dense(lens, torch.int32, (B,), "lens")
-    f = _ftype(Q, "Q", short=True)
-    pages, page = _kv4_cache(Kc, Vc, Kp, Vp, Hkv, D, Q)
-    dev = _same_device(Q, Kc, Vc, Kp, Vp, table, q_off, lens, out)
-    if lse is not None:
-        _dense(lse, torch.float32, (total, Hq), "lse")
-        _same_device(lse, out)
-    max_q = total if max_q is None else max_q
-    max_len = width * page if max_len is None else max_len
+    T = _torch()
     lib = load()
-    need = 0
-    if workspace is None and Hkv > 0:
-        need = lib.lb_attn_kv4_workspace(B, total, max_q, Hq, Hkv, D, max_len, window, 0)
-    ws, size, kept = _scratch(workspace, need, Q, stream, "lb_attn_kv4")
-    _raise(lib.lb_attn_kv4(Q.data_ptr(), ldq, Kc.data_ptr(), Vc.data_ptr(), Kp.data_ptr(), Vp.data_ptr(),
-                           table.data_ptr(), ldt, width, q_off.data_ptr(), lens.data_ptr(), out.data_ptr(), ldo,
-                           None if lse is None else lse.data_ptr(), B, total, max_q, Hq, Hkv, D, pages, page,
-                           max_len, D ** -0.5 if scale is None else scale, window, int(causal), f, ws, size,
-                           _raw_stream(stream, dev)), "lb_attn_kv4")
+    shape = total, Hq, D = Q.shape
+    dev, dt = Q.get_device(), Q.dtype
+    f = _ftype(T.short, Q, "Q")
+    rows = B, width = table.shape
+    Hkv = Kc.shape[1]
+    q, ldq = _rows(Q, "Q", dt, shape, dev, Hq * D)
+    o, ldo = _rows(out, "out", dt, shape, dev, Hq * D)
+    t, ldt = _rows(table, "table", T.i32, rows, dev, width)
+    pages, page, cache = _kv4_cache(T, Kc, Vc, Kp, Vp, Hkv, D, dt, dev)
+    if max_q is None:
+        max_q = total
+    if max_len is None:
+        max_len = width * page
+    ws = _scratch(T, workspace, 0 if workspace is not None else
+                  lib.lb_attn_kv4_workspace(B, total, max_q, Hq, Hkv, D, max_len, window, 0), dev, stream, "lb_attn_kv4")
+    st = lib.lb_attn_kv4(q, ldq, *cache, t, ldt, width, _dense(q_off, "q_off", T.i32, (B + 1,), dev),
+                         _dense(lens, "lens", T.i32, (B,), dev), o, ldo,
+                         None if lse is None else _dense(lse, "lse", T.f32, (total, Hq), dev), B, total, max_q, Hq,
+                         Hkv, D, pages, page, max_len, D ** -0.5 if scale is None else scale, window, int(causal), f,
+                         None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes, _on(T, stream, dev))
+    _raise(st, "lb_attn_kv4")

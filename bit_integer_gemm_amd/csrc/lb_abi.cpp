@@ -283,6 +283,8 @@ int run_gemm(int kind, int dtype, int variant, const void *A, const void *B, voi
 
 }  // namespace
 
+bool lb::variant_is_forced() { return auto_override() >= 0; }
+
 // The scaled product's launches are the linear layer's.
 int lb::scaled_auto(const int8_t *X, const int8_t *W, const float *sx, const float *sw, void *out, int64_t M,
                     int64_t N, int64_t K, const lb::ScaledOut &so, hipStream_t stream)

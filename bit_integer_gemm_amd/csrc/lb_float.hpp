@@ -38,6 +38,28 @@ template <class T> __device__ inline uint32_t pack2(float a, float b)
     return __builtin_bit_cast(uint32_t, v);
 }
 
+// Store of the scaled product: four consecutive columns of a row
+// as ((float)acc * sx[m]) * sw[n] + bias[n] in fp32, rounded once to the output
+// type.  o: element offset of the first; left: columns from it to N; vec: all
+// four exist and the row stride keeps them aligned.  (The type is a template
+// parameter of the kernel: chosen at run time inside the unrolled epilogue, its
+// three copies of every store cost 90 us of 350 at 8192 x 11008 x 4096.)
+template <class T>
+__device__ inline void store_scaled(const T *bias, T *out, int64_t o, int64_t n, int64_t left, bool vec, f32x4 v)
+{
+    typedef T t4 __attribute__((ext_vector_type(4)));
+    if (vec) {
+        if (bias) {
+            const t4 b = *(const t4 *)(bias + n);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] += (float)b[r];
+        }
+        *(t4 *)(out + o) = t4{(T)v.x, (T)v.y, (T)v.z, (T)v.w};
+    } else {
+        for (int r = 0; r < 4 && r < left; ++r) out[o + r] = (T)(bias ? v[r] + (float)bias[n + r] : v[r]);
+    }
+}
+
 // Largest value of a float in a 16-bit type's exponent field, as a bit test:
 // |x| >= inf (infinity or NaN) in either half of a word.
 template <class T> __device__ inline bool any_nonfinite(uint32_t w)

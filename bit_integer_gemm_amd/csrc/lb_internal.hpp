@@ -47,14 +47,21 @@ hipError_t launch_scaled(int variant, const int8_t *A, const int8_t *B, void *ou
 // The same with the launches of an automatic choice; an lb_status.
 int scaled_auto(const int8_t *X, const int8_t *W, const float *sx, const float *sw, void *out, int64_t M,
                 int64_t N, int64_t K, const ScaledOut &so, hipStream_t s);
+// Whether LB_AUTO_VARIANT fixes the variant of automatic calls.
+bool variant_is_forced();
 // Rows of X (K elements, ldx apart, 16-byte aligned) quantised to int8 with a
 // scale each.
 hipError_t launch_quant_rows(int ftype, const void *X, int64_t ldx, int8_t *Q, float *sx, int64_t M,
                              int64_t K, hipStream_t s);
-// The scaled product for at most LINEAR_FEW_MAX rows of X.
-enum { LINEAR_FEW_MAX = 64 };
+// The scaled product where few tiles cover it (linear_is_few).
+bool linear_is_few(int64_t M, int64_t N, int cu);
 hipError_t launch_linear_few(int ftype, const int8_t *Xq, const int8_t *W, const float *sx, const float *sw,
-                             const void *bias, void *out, int64_t M, int64_t N, int64_t K, hipStream_t s);
+                             const void *bias, void *out, int64_t M, int64_t N, int64_t K, int cu,
+                             hipStream_t s);
+// The same from floating activations, quantised on the way (where linear_fuses).
+bool linear_fuses(int64_t M, int64_t N, int64_t K, int cu);
+hipError_t launch_linear_fused(int ftype, const void *X, int64_t ldx, const int8_t *W, const float *sw,
+                               const void *bias, void *out, int64_t M, int64_t N, int64_t K, hipStream_t s);
 // Zero n int32 values on the stream (a kernel, not a memset).
 hipError_t launch_zero_i32(int32_t *p, int64_t n, hipStream_t s);
 // Workgroup tile and stage of a variant; bk_bytes is the K depth of a stage in bytes.

@@ -69,6 +69,7 @@
 #include <type_traits>
 
 #include "lb_device.hpp"
+#include "lb_float.hpp"
 #include "lb_internal.hpp"
 
 namespace lb {
@@ -248,28 +249,6 @@ __device__ inline f32x4 mfma_fp4(i32x4 b, i32x4 a, f32x4 c)
     constexpr int sc = S == 0 ? 128 : S == 1 ? 127 : 126;  // E8M0: 2^(sc - 127)
     const i32x8 b8 = {b.x, b.y, b.z, b.w, 0, 0, 0, 0}, a8 = {a.x, a.y, a.z, a.w, 0, 0, 0, 0};
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b8, a8, c, 4, 4, 0, sc, 0, sc);
-}
-
-// Store of the scaled product (KIND_SCALED): four consecutive columns of a row
-// as ((float)acc * sx[m]) * sw[n] + bias[n] in fp32, rounded once to the output
-// type.  o: element offset of the first; left: columns from it to N; vec: all
-// four exist and the row stride keeps them aligned.  (The type is a template
-// parameter of the kernel: chosen at run time inside the unrolled epilogue, its
-// three copies of every store cost 90 us of 350 at 8192 x 11008 x 4096.)
-template <class T>
-__device__ inline void store_scaled(const T *bias, T *out, int64_t o, int64_t n, int64_t left, bool vec, f32x4 v)
-{
-    typedef T t4 __attribute__((ext_vector_type(4)));
-    if (vec) {
-        if (bias) {
-            const t4 b = *(const t4 *)(bias + n);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] += (float)b[r];
-        }
-        *(t4 *)(out + o) = t4{(T)v.x, (T)v.y, (T)v.z, (T)v.w};
-    } else {
-        for (int r = 0; r < 4 && r < left; ++r) out[o + r] = (T)(bias ? v[r] + (float)bias[n + r] : v[r]);
-    }
 }
 
 template <class C, int KIND, bool CONV, class T = float>

@@ -28,13 +28,21 @@ int check_product(int64_t M, int64_t N, int64_t K, int ftype)
     return LB_OK;
 }
 
+// Compute units of the current device; if it cannot be asked, as on a whole chip.
+int cu_count()
+{
+    int cu = 0;
+    return lb::device_cu_count(&cu) == LB_OK ? cu : 256;
+}
+
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
 int scaled(const int8_t *X, const int8_t *W, const float *sx, const float *sw, const void *bias, void *out,
            int64_t M, int64_t N, int64_t K, int ftype, hipStream_t s)
 {
-    if (M <= lb::LINEAR_FEW_MAX)
-        return finish(lb::launch_linear_few(ftype, X, W, sx, sw, bias, out, M, N, K, s));
+    const int cu = cu_count();
+    if (lb::linear_is_few(M, N, cu) && !lb::variant_is_forced())
+        return finish(lb::launch_linear_few(ftype, X, W, sx, sw, bias, out, M, N, K, cu, s));
     return lb::scaled_auto(X, W, sx, sw, out, M, N, K, lb::ScaledOut{bias, ftype}, s);
 }
 
@@ -140,9 +148,11 @@ int lb_linear_w8a8(const void *X, int64_t ldx, const int8_t *W, const float *sw,
         return LB_ERR_ALIGN;
     if (!workspace || workspace_bytes < lb_linear_w8a8_workspace(M, K, N)) return LB_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return LB_ERR_ALIGN;
+    const hipStream_t s = (hipStream_t)stream;
+    if (lb::linear_fuses(M, N, K, cu_count()) && !lb::variant_is_forced())
+        return finish(lb::launch_linear_fused(ftype, X, ldx, W, sw, bias, out, M, N, K, s));
     int8_t *q = (int8_t *)workspace;
     float *sx = (float *)(q + round_up(M * K, 256));
-    const hipStream_t s = (hipStream_t)stream;
     if (lb::launch_quant_rows(ftype, X, ldx, q, sx, M, K, s) != hipSuccess) return LB_ERR_HIP;
     return scaled(q, W, sx, sw, bias, out, M, N, K, ftype, s);
 }
@@ -220,8 +230,7 @@ int lb_attn_kv4(const void *Q, int64_t ldq, const uint8_t *Kc, const uint8_t *Vc
     if (!aligned(Q) || !aligned(Kc) || !aligned(Vc) || !aligned(Kp) || !aligned(Vp) || !aligned(out) ||
         ldq % 8 != 0 || ldo % 8 != 0 || !aligned(workspace, 256))
         return LB_ERR_ALIGN;
-    int cu = 0;
-    if (lb::device_cu_count(&cu) != LB_OK) cu = 0;
+    const int cu = cu_count();
     max_q = std::min(max_q, total_q);
     const AttnPlan p = plan_attn(B, total_q, max_q, Hq, Hkv, D, max_len, window, cu);
     int64_t splits = p.splits;

@@ -68,6 +68,35 @@ template <class T> __device__ inline uint32_t widen_bits(uint32_t m)
     else return __float_as_uint(lo_f32<_Float16>(m));
 }
 
+// The 16 bytes of a chunk quantised to q.
+template <class T> __device__ inline void put_chunk(int8_t *q, i32x4 v, const RowScale &rs)
+{
+    constexpr int EPT = 16 / sizeof(T);
+    uint32_t b[EPT / 4];
+#pragma unroll
+    for (int i = 0; i < EPT / 4; ++i) {
+        float x[4];
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = __int_as_float(v[e]);
+        } else {
+            x[0] = lo_f32<T>((uint32_t)v[2 * i]);
+            x[1] = hi_f32<T>((uint32_t)v[2 * i]);
+            x[2] = lo_f32<T>((uint32_t)v[2 * i + 1]);
+            x[3] = hi_f32<T>((uint32_t)v[2 * i + 1]);
+        }
+        uint32_t w = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int n = rs.zero ? 0 : quant_s8(x[e], rs.inv, rs.amax, rs.direct);
+            w |= ((uint32_t)n & 0xFFu) << (8 * e);
+        }
+        b[i] = w;
+    }
+    if constexpr (EPT == 8) *(u32x2 *)q = u32x2{b[0], b[1]};
+    else *(uint32_t *)q = b[0];
+}
+
 // One workgroup per row; EPT elements per 16-byte chunk.  The row is read once
 // if it fits the workgroup's registers (NC chunks per thread), else twice.
 template <class T, int NC>
@@ -101,38 +130,13 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const T *__restrict__ X
     const RowScale rs = row_scale(widen_bits<T>(mx));
     if (threadIdx.x == 0) sx[m] = rs.scale;
 
-    auto put = [&](int32_t c, i32x4 v) {
-        uint32_t b[EPT / 4];
-#pragma unroll
-        for (int i = 0; i < EPT / 4; ++i) {
-            float x[4];
-            if constexpr (sizeof(T) == 4) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = __int_as_float(v[e]);
-            } else {
-                x[0] = lo_f32<T>((uint32_t)v[2 * i]);
-                x[1] = hi_f32<T>((uint32_t)v[2 * i]);
-                x[2] = lo_f32<T>((uint32_t)v[2 * i + 1]);
-                x[3] = hi_f32<T>((uint32_t)v[2 * i + 1]);
-            }
-            uint32_t w = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int n = rs.zero ? 0 : quant_s8(x[e], rs.inv, rs.amax, rs.direct);
-                w |= ((uint32_t)n & 0xFFu) << (8 * e);
-            }
-            b[i] = w;
-        }
-        if constexpr (EPT == 8) *(u32x2 *)(q + (int64_t)c * 8) = u32x2{b[0], b[1]};
-        else *(uint32_t *)(q + (int64_t)c * 4) = b[0];
-    };
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int32_t c = (int32_t)threadIdx.x + 256 * i;
-        if (c < chunks) put(c, keep[i]);
+        if (c < chunks) put_chunk<T>(q + (int64_t)c * EPT, keep[i], rs);
     }
     for (int32_t c = (int32_t)threadIdx.x + 256 * NC; c < chunks; c += 256)
-        put(c, *(const i32x4 *)(row + (int64_t)c * EPT));
+        put_chunk<T>(q + (int64_t)c * EPT, *(const i32x4 *)(row + (int64_t)c * EPT), rs);
 }
 
 template <class T>
@@ -161,103 +165,251 @@ hipError_t launch_quant_rows(int ftype, const void *X, int64_t ldx, int8_t *Q, f
     }
 }
 
-// ---- few tokens ------------------------------------------------------------
-// 16 output channels per workgroup, all of K: wave w takes every NW-th block of
-// 128 K-bytes, and the waves' exact partial sums meet in LDS.  The weight is the
-// MFMA's A operand (lane l: channel l%16, K bytes 32*(l/16) .. +31 of the block,
-// so the four lane groups read one whole 128-byte line of each row), the tokens
-// its B operand with the same K order; lane l ends with channels 4*(l/16) .. +3
-// of token l%16.
-template <class T, int MT>
-__global__ __launch_bounds__(512) void linear_few_kernel(
-    const int8_t *__restrict__ Xq, const int8_t *__restrict__ W, const float *__restrict__ sx,
-    const float *__restrict__ sw, const T *__restrict__ bias, T *__restrict__ out, int32_t M, int32_t N,
-    int32_t K)
-{
-    constexpr int NW = 8;
-    __shared__ i32x4 part[NW][MT][64];
-    const uint32_t lane = threadIdx.x & 63u;
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int32_t r = (int32_t)(lane & 15u), c = (int32_t)(lane >> 4);
-    const int64_t n0 = (int64_t)blockIdx.x * 16;
-    const int8_t *wrow = W + min(n0 + r, (int64_t)N - 1) * K + 32 * c;
-    const int8_t *xrow[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) xrow[t] = Xq + (int64_t)min(16 * t + r, M - 1) * K + 32 * c;
+// ---- few rows --------------------------------------------------------------
+// A tile of 16 MT rows of X by 16 NT rows of W (output columns) per workgroup, and
+// all of K: the eight waves each take an eighth of K for the whole tile, through
+// rings of LDS of their own, and their exact sums meet in LDS by integer adds
+// (whose order does not matter).  Every operand byte is read once per workgroup,
+// but no wave waits for another before the end, and DEPTH - 1 stages of copies are
+// under way in each: what bounds these products is the latency and number of bytes
+// on their way, not the matrix cores.
+//   A copy fills a block of 16 rows x 64 K-bytes, four lanes to a row (64 bytes in
+//   one piece; straight to registers in fragment order, 16 rows to a load, delivers
+//   half as much: 18.1 us at 16 x 11008 x 4096).  Piece p of row n lies at
+//   p ^ (n / 2) % 4, which keeps the fragment reads off each other's banks.
+//   W is the MFMA's A operand (lane l: row l % 16, piece l / 16), X its B operand;
+//   lane l ends with columns 4 (l / 16) .. + 3 of row l % 16.
+// FUSED (MT = 1, few rows): X is the layer's floating activations; while the first
+// weights are on their way every workgroup quantises the rows for itself into LDS,
+// which saves the launch that would do it once.
+template <int MT, int NT, int S, int DEPTH, bool FUSED> struct FewTile {
+    static constexpr int NW = 8;                              // waves
+    static constexpr int BLOCKS = (FUSED ? 0 : MT) + NT;      // 1 KiB blocks of a 64-byte step
+    static constexpr int STAGE = S * BLOCKS * 1024, RING = DEPTH * STAGE;
+    static constexpr int TM = 16 * MT, TN = 16 * NT, LD = TN + 4;
+    static constexpr int SUMS_AT = NW * RING, SCALE_AT = SUMS_AT + TM * LD * 4, RED_AT = SCALE_AT + TM * 4;
+    static constexpr int X_AT = RED_AT + (FUSED ? NW * 16 : 0);   // FUSED: M x K int8
+    static_assert((DEPTH - 1) * S * BLOCKS < 64, "vmcnt is 6 bits");
+};
 
-    i32x4 acc[MT];
+template <int N> __device__ inline void wait_copies() { asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory"); }
+
+template <class T, int MT, int NT, int S, int DEPTH, bool FUSED>
+__global__ __launch_bounds__(512) void linear_few_kernel(
+    const void *__restrict__ X, int64_t ldx, const int8_t *__restrict__ W, const float *__restrict__ sx,
+    const float *__restrict__ sw, const T *__restrict__ bias, T *__restrict__ out, int32_t M, int32_t N,
+    int32_t K, uint32_t tiles_m, uint32_t tiles_n)
+{
+    using FT = FewTile<MT, NT, S, DEPTH, FUSED>;
+    constexpr int NW = FT::NW, TM = FT::TM, TN = FT::TN, LD = FT::LD;
+    extern __shared__ __attribute__((aligned(1024))) char smem[];
+    int32_t *const sums = (int32_t *)(smem + FT::SUMS_AT);
+    float *const row_scales = (float *)(smem + FT::SCALE_AT);
+    const int32_t lane = (int32_t)(threadIdx.x & 63u);
+    const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int32_t r = lane & 15, c = lane >> 4;
+    uint32_t tm, tn;
+    tile_of_block(blockIdx.x, tiles_m, tiles_n, 4u, tm, tn);
+    const int32_t m0 = (int32_t)tm * TM, n0 = (int32_t)tn * TN;
+
+    // Copies: lane i takes piece (i % 4) ^ (i / 8) % 4 of row i / 4.  Rows past the
+    // operand, pieces past K and steps past this wave's share lie beyond the
+    // buffer's range and read as zeros.
+    const i32x4 rw = make_rsrc(W + (int64_t)n0 * K, (uint64_t)min(TN, N - n0) * (uint32_t)K);
+    const i32x4 rx = FUSED ? rw : make_rsrc((const int8_t *)X + (int64_t)m0 * K, (uint64_t)min(TM, M - m0) * (uint32_t)K);
+    const uint32_t row_at = (uint32_t)(lane >> 2) * (uint32_t)K;
+    const int32_t piece = 16 * ((lane & 3) ^ ((lane >> 3) & 3));
+    const uint32_t ring = lds_addr(smem) + (uint32_t)(wave * FT::RING);
+    const int32_t steps = (K + 63) / 64;
+    const int32_t first = wave * steps / NW, last = (wave + 1) * steps / NW;
+    auto copy = [&](int d, int32_t st) {
 #pragma unroll
-    for (int t = 0; t < MT; ++t) acc[t] = i32x4{0, 0, 0, 0};
-    const int32_t full = K / 128;
-    for (int32_t b = (int32_t)wave; b < full; b += NW) {
-        const i32x4 w0 = *(const i32x4 *)(wrow + b * 128), w1 = *(const i32x4 *)(wrow + b * 128 + 16);
+        for (int s = 0; s < S; ++s) {
+            const int32_t k = 64 * (st + s) + piece;
+            const bool in = st + s < last && k < K;
+            const uint32_t dst = ring + (uint32_t)(d * FT::STAGE + s * FT::BLOCKS * 1024);
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            const i32x4 x0 = *(const i32x4 *)(xrow[t] + b * 128), x1 = *(const i32x4 *)(xrow[t] + b * 128 + 16);
-            acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w0, x0, acc[t], 0, 0, 0);
-            acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w1, x1, acc[t], 0, 0, 0);
+            for (int t = 0; t < NT; ++t)
+                dma16(rw, in ? row_at + (uint32_t)(16 * t) * (uint32_t)K + (uint32_t)k : 0xFFFFFFF0u, dst + t * 1024);
+            if constexpr (!FUSED)
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+                    dma16(rx, in ? row_at + (uint32_t)(16 * t) * (uint32_t)K + (uint32_t)k : 0xFFFFFFF0u,
+                          dst + (NT + t) * 1024);
         }
-    }
-    if (K % 128 != 0 && (int32_t)wave == full % NW) {
-        // the last, partial block: 16-byte pieces past K are not read and count as 0
-        const i32x4 zero = {0, 0, 0, 0};
-        const bool in0 = full * 128 + 32 * c < K, in1 = full * 128 + 32 * c + 16 < K;
-        const i32x4 w0 = in0 ? *(const i32x4 *)(wrow + full * 128) : zero;
-        const i32x4 w1 = in1 ? *(const i32x4 *)(wrow + full * 128 + 16) : zero;
+    };
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            const i32x4 x0 = in0 ? *(const i32x4 *)(xrow[t] + full * 128) : zero;
-            const i32x4 x1 = in1 ? *(const i32x4 *)(xrow[t] + full * 128 + 16) : zero;
-            acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w0, x0, acc[t], 0, 0, 0);
-            acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w1, x1, acc[t], 0, 0, 0);
+    for (int d = 0; d < DEPTH - 1; ++d) copy(d, first + S * d);
+    for (int32_t i = (int32_t)threadIdx.x; i < TM * LD; i += 512) sums[i] = 0;
+
+    const int8_t *xq = nullptr;
+    if constexpr (FUSED) {
+        constexpr int EPT = 16 / sizeof(T);
+        const int32_t chunks = K / EPT;
+        uint32_t(*red)[4] = (uint32_t(*)[4])(smem + FT::RED_AT);
+        for (int32_t m = 0; m < M; ++m) {
+            const T *x = (const T *)X + m * ldx;
+            uint32_t mx = 0;
+            for (int32_t q = (int32_t)threadIdx.x; q < chunks; q += 512)
+                mx = max(mx, chunk_amax<T>(*(const i32x4 *)(x + (int64_t)q * EPT)));
+#pragma unroll
+            for (int d = 32; d; d >>= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, d));
+            if (lane == 0) red[wave][m] = mx;
         }
-    }
+        __syncthreads();
+        for (int32_t m = 0; m < M; ++m) {
+            const T *x = (const T *)X + m * ldx;
+            uint32_t mx = 0;
 #pragma unroll
-    for (int t = 0; t < MT; ++t) part[wave][t][lane] = acc[t];
+            for (int w = 0; w < NW; ++w) mx = max(mx, red[w][m]);
+            const RowScale rs = row_scale(widen_bits<T>(mx));
+            if (threadIdx.x == 0) row_scales[m] = rs.scale;
+            for (int32_t q = (int32_t)threadIdx.x; q < chunks; q += 512)
+                put_chunk<T>((int8_t *)(smem + FT::X_AT) + (int64_t)m * K + q * EPT, *(const i32x4 *)(x + (int64_t)q * EPT), rs);
+        }
+        xq = (const int8_t *)(smem + FT::X_AT) + (int64_t)min(r, M - 1) * K + 16 * c;
+    } else {
+        if (threadIdx.x < TM) row_scales[threadIdx.x] = sx[min(m0 + (int32_t)threadIdx.x, M - 1)];
+    }
     __syncthreads();
-    if (wave >= MT) return;
-    i32x4 sum = part[0][wave][lane];
+
+    i32x4 acc[MT][NT];
 #pragma unroll
-    for (int w = 1; w < NW; ++w) sum += part[w][wave][lane];
-    const int32_t m = 16 * (int32_t)wave + r;
-    if (m >= M) return;
-    const float scale = sx[m];
+    for (int t = 0; t < MT; ++t)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int64_t n = n0 + 4 * c + e;
-        if (n < N) {
-            float y = ((float)sum[e] * scale) * sw[n];
-            if (bias) y += (float)bias[n];
-            out[m * (int64_t)N + n] = (T)y;
+        for (int u = 0; u < NT; ++u) acc[t][u] = i32x4{0, 0, 0, 0};
+    const char *const frag = smem + wave * FT::RING + (4 * r + (c ^ ((r >> 1) & 3))) * 16;
+    for (int32_t st = first; st < last; st += S * DEPTH) {
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+            // Stage d: copied DEPTH - 1 stages ago.  (Stages past the wave's share
+            // hold zeros.)
+            const int32_t at = st + S * d;
+            copy((d + DEPTH - 1) % DEPTH, at + S * (DEPTH - 1));
+            wait_copies<(DEPTH - 1) * S * FT::BLOCKS>();
+            i32x4 wf[S][NT], xf[S][MT];
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) wf[s][t] = *(const i32x4 *)(frag + d * FT::STAGE + (s * FT::BLOCKS + t) * 1024);
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    if constexpr (FUSED) xf[s][t] = *(const i32x4 *)(xq + min(64 * (at + s), K - 16 - 16 * c));
+                    else xf[s][t] = *(const i32x4 *)(frag + d * FT::STAGE + (s * FT::BLOCKS + NT + t) * 1024);
+                }
+            }
+            // the next copies overwrite what has been read here
+            asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int u = 0; u < NT; ++u)
+                        acc[t][u] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[s][u], xf[s][t], acc[t][u], 0, 0, 0);
         }
+    }
+    wait_copies<0>();
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int u = 0; u < NT; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) atomicAdd(&sums[(16 * t + r) * LD + 16 * u + 4 * c + e], acc[t][u][e]);
+    __syncthreads();
+    const bool vec = N % 4 == 0;
+    for (int32_t i = (int32_t)threadIdx.x; i < TM * TN / 4; i += 512) {
+        const int32_t m = i / (TN / 4), n = i % (TN / 4) * 4;
+        if (m0 + m >= M || n0 + n >= N) continue;
+        const i32x4 v = *(const i32x4 *)(sums + m * LD + n);
+        const float scale = row_scales[m];
+        f32x4 y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = vec || n0 + n + e < N ? ((float)v[e] * scale) * sw[n0 + n + e] : 0.f;
+        store_scaled<T>(bias, out, (m0 + m) * (int64_t)N + n0 + n, n0 + n, N - n0 - n, vec, y);
     }
 }
 
-template <class T>
-static hipError_t linear_few_t(const int8_t *Xq, const int8_t *W, const float *sx, const float *sw,
-                               const void *bias, void *out, int64_t M, int64_t N, int64_t K, hipStream_t s)
+// Rows that every workgroup quantises for itself, and the LDS for them: four rows
+// of 4096 take a workgroup about a us, a launch of their own about three.
+enum { FUSED_ROWS = 4, FUSED_BYTES = 64 * 1024 };
+
+template <class T, int MT, int NT, int S, int DEPTH, bool FUSED>
+static hipError_t few_t(const void *X, int64_t ldx, const int8_t *W, const float *sx, const float *sw,
+                        const void *bias, void *out, int64_t M, int64_t N, int64_t K, hipStream_t s)
 {
-    const dim3 grid((uint32_t)((N + 15) / 16)), block(512);
-    if (M <= 16)
-        hipLaunchKernelGGL((linear_few_kernel<T, 1>), grid, block, 0, s, Xq, W, sx, sw, (const T *)bias, (T *)out,
-                           (int32_t)M, (int32_t)N, (int32_t)K);
-    else if (M <= 32)
-        hipLaunchKernelGGL((linear_few_kernel<T, 2>), grid, block, 0, s, Xq, W, sx, sw, (const T *)bias, (T *)out,
-                           (int32_t)M, (int32_t)N, (int32_t)K);
-    else
-        hipLaunchKernelGGL((linear_few_kernel<T, 4>), grid, block, 0, s, Xq, W, sx, sw, (const T *)bias, (T *)out,
-                           (int32_t)M, (int32_t)N, (int32_t)K);
+    using FT = FewTile<MT, NT, S, DEPTH, FUSED>;
+    const uint64_t tm = (uint64_t)((M + FT::TM - 1) / FT::TM), tn = (uint64_t)((N + FT::TN - 1) / FT::TN);
+    if (tm * tn > 0x7FFFFFFFull) return hipErrorInvalidValue;
+    static_assert(FT::X_AT + (FUSED ? FUSED_BYTES : 0) <= 160 * 1024, "LDS");
+    hipLaunchKernelGGL((linear_few_kernel<T, MT, NT, S, DEPTH, FUSED>), dim3((uint32_t)(tm * tn)), dim3(512),
+                       (uint32_t)(FT::X_AT + (FUSED ? M * K : 0)), s, X, ldx, W, sx, sw, (const T *)bias, (T *)out,
+                       (int32_t)M, (int32_t)N, (int32_t)K, (uint32_t)tm, (uint32_t)tn);
     return hipGetLastError();
 }
 
-hipError_t launch_linear_few(int ftype, const int8_t *Xq, const int8_t *W, const float *sx, const float *sw,
-                             const void *bias, void *out, int64_t M, int64_t N, int64_t K, hipStream_t s)
+// Which tile a product takes; 0 rows: none of these, the LDS-tiled kernels of
+// lb_gemm_s8_linear.  A workgroup takes about as long whatever its tile (latency,
+// and some 47 KB a us of copies to a compute unit), so the narrowest tile whose
+// workgroups run at once, and the other kernels where none does.  Measured, bf16,
+// weights from memory, us here and there: 16 x 6000 x 4096 7.4 / 12.7, 1 x 8192 x
+// 8192 14.5 / 24.2, 24 x 8192 x 4096 9.4 / 13.7, 100 x 4096 x 4096 9.8 / 19.7,
+// 256 x 1376 x 4096 9.4 / 19.3, 64 x 8192 x 8192 24.2 / 26.2; past the rule 16 x
+// 11008 x 4096 15.4 / 13.9, 64 x 11008 x 4096 20.0 / 16.2, 100 x 8192 x 4096
+// 15.9 / 14.7, 331 x 4097 x 5504 34.3 / 22.8.
+struct FewShape {
+    int tm, tn;
+};
+static FewShape few_shape(int64_t M, int64_t N, int cu)
 {
-    if (M > LINEAR_FEW_MAX) return hipErrorInvalidValue;
+    auto count = [&](int64_t tm, int64_t tn) { return ((M + tm - 1) / tm) * ((N + tn - 1) / tn); };
+    // (two workgroups of the 16 x 16 tile run on a compute unit)
+    if (M <= 16) return count(16, 16) <= 2 * (int64_t)cu ? FewShape{16, 16} : FewShape{0, 0};
+    const int tm = M <= 32 ? 32 : 64;
+    if (count(tm, 16) <= cu) return {tm, 16};
+    if (count(tm, 32) <= cu) return {tm, 32};
+    return {0, 0};
+}
+bool linear_is_few(int64_t M, int64_t N, int cu) { return few_shape(M, N, cu).tm != 0; }
+
+template <class T>
+static hipError_t linear_few_t(const int8_t *Xq, const int8_t *W, const float *sx, const float *sw,
+                               const void *bias, void *out, int64_t M, int64_t N, int64_t K, int cu, hipStream_t s)
+{
+    const FewShape f = few_shape(M, N, cu);
+#define LB_FEW(...) few_t<T, __VA_ARGS__, false>(Xq, K, W, sx, sw, bias, out, M, N, K, s)
+    if (f.tm == 16) return LB_FEW(1, 1, 2, 2);
+    if (f.tm == 32) return f.tn == 16 ? LB_FEW(2, 1, 2, 2) : LB_FEW(2, 2, 2, 2);
+    if (f.tm == 64) return f.tn == 16 ? LB_FEW(4, 1, 1, 3) : LB_FEW(4, 2, 1, 2);
+#undef LB_FEW
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_linear_few(int ftype, const int8_t *Xq, const int8_t *W, const float *sx, const float *sw,
+                             const void *bias, void *out, int64_t M, int64_t N, int64_t K, int cu,
+                             hipStream_t s)
+{
     switch (ftype) {
-    case LB_BF16: return linear_few_t<__bf16>(Xq, W, sx, sw, bias, out, M, N, K, s);
-    case LB_F16: return linear_few_t<_Float16>(Xq, W, sx, sw, bias, out, M, N, K, s);
-    case LB_F32: return linear_few_t<float>(Xq, W, sx, sw, bias, out, M, N, K, s);
+    case LB_BF16: return linear_few_t<__bf16>(Xq, W, sx, sw, bias, out, M, N, K, cu, s);
+    case LB_F16: return linear_few_t<_Float16>(Xq, W, sx, sw, bias, out, M, N, K, cu, s);
+    case LB_F32: return linear_few_t<float>(Xq, W, sx, sw, bias, out, M, N, K, cu, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+bool linear_fuses(int64_t M, int64_t N, int64_t K, int cu)
+{
+    return M <= FUSED_ROWS && M * K <= FUSED_BYTES && linear_is_few(M, N, cu);
+}
+
+hipError_t launch_linear_fused(int ftype, const void *X, int64_t ldx, const int8_t *W, const float *sw,
+                               const void *bias, void *out, int64_t M, int64_t N, int64_t K, hipStream_t s)
+{
+    if (M > FUSED_ROWS || M * K > FUSED_BYTES) return hipErrorInvalidValue;
+    switch (ftype) {
+    case LB_BF16: return few_t<__bf16, 1, 1, 2, 3, true>(X, ldx, W, nullptr, sw, bias, out, M, N, K, s);
+    case LB_F16: return few_t<_Float16, 1, 1, 2, 3, true>(X, ldx, W, nullptr, sw, bias, out, M, N, K, s);
+    case LB_F32: return few_t<float, 1, 1, 2, 3, true>(X, ldx, W, nullptr, sw, bias, out, M, N, K, s);
     default: return hipErrorInvalidValue;
     }
 }
