@@ -61,7 +61,8 @@ hipError_t launch_linear_few(int ftype, const int8_t *Xq, const int8_t *W, const
 // The same from floating activations, quantised on the way (where linear_fuses).
 bool linear_fuses(int64_t M, int64_t N, int64_t K, int cu);
 hipError_t launch_linear_fused(int ftype, const void *X, int64_t ldx, const int8_t *W, const float *sw,
-                               const void *bias, void *out, int64_t M, int64_t N, int64_t K, hipStream_t s);
+                               const void *bias, void *out, int64_t M, int64_t N, int64_t K, int cu,
+                               hipStream_t s);
 // Zero n int32 values on the stream (a kernel, not a memset).
 hipError_t launch_zero_i32(int32_t *p, int64_t n, hipStream_t s);
 // Workgroup tile and stage of a variant; bk_bytes is the K depth of a stage in bytes.
@@ -93,6 +94,9 @@ hipError_t launch_kv4_write(int ftype, const void *K, const void *V, int64_t ldk
 hipError_t launch_kv4_read(int ftype, const Kv4Cache &c, const int64_t *slots, void *K, void *V, int64_t T,
                            int D, hipStream_t s);
 
+// The attention kernels: 16 rows to a workgroup of four waves, or of as many as a
+// compute unit holds; 256 rows (D = 256: 128).
+enum { ATTN_ROWS = 0, ATTN_WIDE = 1, ATTN_CHUNK = 2 };
 struct AttnArgs {
     const void *q;
     void *out;
@@ -104,10 +108,12 @@ struct AttnArgs {
     int64_t total_q;
     int32_t group, batch, window, causal, splits;
     int32_t unit;         // fewest blocks of keys (64 keys, or 32) worth a workgroup of their own
-    int32_t chunk, tiles; // which kernel: 256 (D = 256: 128) rows per workgroup, or 16; and how many such tiles a key head has
+    int32_t kernel, tiles; // ATTN_*, and how many tiles of its rows a key head has
     uint32_t page_mul, page_shift; // division by the page size
     float scale2;         // softmax scale * log2(e)
 };
+// Waves of an ATTN_WIDE workgroup.
+constexpr int attn_wide_waves(int D) { return D == 64 ? 16 : D == 128 ? 12 : 8; }
 hipError_t launch_attn(int ftype, int D, const AttnArgs &a, hipStream_t s);
 
 // Measured selection table lookup (host only).

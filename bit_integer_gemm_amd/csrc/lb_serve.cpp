@@ -72,7 +72,7 @@ lb::Kv4Cache cache_of(const uint8_t *Kc, const uint8_t *Vc, const void *Kp, cons
 }
 
 struct AttnPlan {
-    bool chunk;
+    int kernel;
     int64_t tiles, splits, unit, per_split;   // row tiles of a key head; key ranges at most; blocks of keys in
                                               // one; workspace bytes per range
 };
@@ -81,22 +81,29 @@ AttnPlan plan_attn(int64_t B, int64_t total_q, int64_t max_q, int64_t Hq, int64_
                    int64_t max_len, int64_t window, int cu)
 {
     AttnPlan p;
-    const int64_t group = Hq / Hkv;
+    const int64_t rows = max_q * (Hq / Hkv);
     // Many rows of a key head share its keys through LDS; few would leave most of
     // that kernel's 256 rows empty.
-    p.chunk = max_q * group > 32;
-    p.tiles = p.chunk ? (max_q * group + (D == 256 ? 127 : 255)) / (D == 256 ? 128 : 256) : (max_q * group + 15) / 16;
-    int64_t keys = max_len;
-    if (window > 0) keys = std::min(keys, window + max_q);
-    const int64_t wgs = B * Hkv * p.tiles, block = p.chunk ? 64 : 32, blocks = std::max<int64_t>((keys + block - 1) / block, 1);
-    p.splits = 1;
-    if (p.chunk && cu > 0) {
+    const bool chunk = rows > 32;
+    const int64_t tile = !chunk ? 16 : D == 256 ? 128 : 256, block = chunk ? 64 : 32;
+    p.tiles = (rows + tile - 1) / tile;
+    const int64_t keys = window > 0 ? std::min(max_len, window + max_q) : max_len;
+    const int64_t wgs = B * Hkv * p.tiles, blocks = std::max<int64_t>((keys + block - 1) / block, 1);
+    if (chunk) {
         // One workgroup to a compute unit.  A range costs its rows' partial results in
         // fp32, written and read, about as much as nine tiles of 64 keys: no ranges
         // once there are workgroups for all units, and none below 16 tiles.
+        p.kernel = lb::ATTN_CHUNK;
         p.splits = std::min((int64_t)cu / wgs, blocks / 16);
-    } else if (wgs < 8 * (int64_t)cu) {
-        p.splits = std::min((8 * (int64_t)cu + wgs - 1) / wgs, (blocks + 7) / 8);
+    } else if (2 * wgs <= cu) {
+        // Few tiles: workgroups that fill a compute unit, two blocks to a wave at
+        // least before there is a second range (and a launch to join them).
+        p.kernel = lb::ATTN_WIDE;
+        p.splits = std::min((int64_t)cu / wgs, blocks / (2 * lb::attn_wide_waves((int)D)));
+    } else {
+        // Small workgroups in number even out sequences of different lengths.
+        p.kernel = lb::ATTN_ROWS;
+        p.splits = std::min((8 * (int64_t)cu + wgs - 1) / wgs, blocks / 32);
     }
     p.splits = std::max<int64_t>(1, std::min<int64_t>(p.splits, 64));
     p.unit = (blocks + p.splits - 1) / p.splits;
@@ -149,8 +156,9 @@ int lb_linear_w8a8(const void *X, int64_t ldx, const int8_t *W, const float *sw,
     if (!workspace || workspace_bytes < lb_linear_w8a8_workspace(M, K, N)) return LB_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return LB_ERR_ALIGN;
     const hipStream_t s = (hipStream_t)stream;
-    if (lb::linear_fuses(M, N, K, cu_count()) && !lb::variant_is_forced())
-        return finish(lb::launch_linear_fused(ftype, X, ldx, W, sw, bias, out, M, N, K, s));
+    const int cu = cu_count();
+    if (lb::linear_fuses(M, N, K, cu) && !lb::variant_is_forced())
+        return finish(lb::launch_linear_fused(ftype, X, ldx, W, sw, bias, out, M, N, K, cu, s));
     int8_t *q = (int8_t *)workspace;
     float *sx = (float *)(q + round_up(M * K, 256));
     if (lb::launch_quant_rows(ftype, X, ldx, q, sx, M, K, s) != hipSuccess) return LB_ERR_HIP;
@@ -257,7 +265,7 @@ int lb_attn_kv4(const void *Q, int64_t ldq, const uint8_t *Kc, const uint8_t *Vc
     a.causal = causal != 0;
     a.splits = (int32_t)splits;
     a.unit = splits == p.splits ? (int32_t)p.unit : 1;
-    a.chunk = p.chunk;
+    a.kernel = p.kernel;
     a.tiles = (int32_t)p.tiles;
     // key / page = mulhi(key, mul) >> shift with 2^shift the power of two below page:
     // mul = ceil(2^(32 + shift) / page) < 2^32, and mul page - 2^(32 + shift) < page

@@ -291,9 +291,9 @@ __device__ inline float sum_over_groups(float x)
     return x + __shfl_xor(x, 32);
 }
 
-// Sixteen rows against a range of keys.  Each of the four waves takes blocks of
-// 32 keys (two half-blocks of 16, each inside one page) and keeps its own
-// maximum, sum and output; they meet in LDS.  Lane l = 16 c + r:
+// Sixteen rows against a range of keys.  Each of NW waves takes blocks of 32 keys
+// (two half-blocks of 16, each inside one page) and keeps its own maximum, sum and
+// output; they meet in LDS.  Lane l = 16 c + r:
 //   scores    A: key r of a half-block, levels [c D/4, (c+1) D/4);  B: row r.
 //             It ends with keys 4c .. 4c+3 of each half-block for row r;
 //   values    those eight keys are its share of the contraction as they stand:
@@ -304,16 +304,16 @@ __device__ inline float sum_over_groups(float x)
 // values as soon as this one's are, into the same registers, and the numbers of
 // its pages a block earlier.  (Two blocks' worth of registers cost more in waves
 // per SIMD than the longer lead gave.)
-template <class T, int D>
-__global__ __launch_bounds__(256, D == 256 ? 2 : 3) void attn_rows_kernel(AttnArgs a)
+template <class T, int D, int NW>
+__global__ __launch_bounds__(64 * NW, NW == 4 ? (D == 256 ? 2 : 3) : NW / 4) void attn_rows_kernel(AttnArgs a)
 {
     using MM = Mfma<T>;
     constexpr int KW = D / 32;     // words of a key a lane reads, = MFMAs per half-block
     constexpr int DPL = D / 16;    // dims of a value a lane reads, = MFMAs per block
     constexpr int VW = DPL / 8 ? DPL / 8 : 1;
     constexpr int LDO = D + 4;
-    __shared__ float osum[4 * 16 * LDO];
-    __shared__ float stat[4][16][4];
+    __shared__ float osum[NW * 16 * LDO];
+    __shared__ float stat[NW][16][4];
     const uint32_t lane = threadIdx.x & 63u;
     const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int32_t r = (int32_t)(lane & 15u), c = (int32_t)(lane >> 4);
@@ -372,7 +372,7 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 3) void attn_rows_kernel(AttnAr
         ask(mine);
         fetch_keys(mine);
         fetch_vals();
-        ask(mine + 4);
+        ask(mine + NW);
     }
 
     const int32_t row = min(r0 + r, sp.rows - 1);
@@ -402,7 +402,7 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 3) void attn_rows_kernel(AttnAr
     const uint32_t mk = in_vgpr(MM::magic), mv = in_vgpr(MfmaV::magic);
     const i32x4 one = {0x3F803F80, 0x3F803F80, 0x3F803F80, 0x3F803F80};
 
-    for (int32_t blk = mine; blk < last; blk += 4) {
+    for (int32_t blk = mine; blk < last; blk += NW) {
         const int32_t t0 = blk * 32;
         there[0] = there1[0];
         there[1] = there1[1];
@@ -424,8 +424,8 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 3) void attn_rows_kernel(AttnAr
                 sc[s][i] = __builtin_fmaf(lo_f32<T>(kp[s][i]), x[i] * a.scale2,
                                           __builtin_fmaf(hi_f32<T>(kp[s][i]), qsum2, -top));
         }
-        fetch_keys(blk + 4);
-        ask(blk + 8);
+        fetch_keys(blk + NW);
+        ask(blk + 2 * NW);
         const bool whole = t0 >= full_lo && t0 + 32 <= full_hi && there[0] && there[1];
         if (!whole) {
             asm volatile("" ::: "memory");  // keeps the comparisons in this branch
@@ -503,7 +503,7 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 3) void attn_rows_kernel(AttnAr
         fetch_vals();
     }
 
-    // the four waves' results
+    // the waves' results
     l_run = sum_over_groups(l_run);
     pm = sum_over_groups(pm);
     if (c == 0) {
@@ -519,15 +519,15 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : 3) void attn_rows_kernel(AttnAr
             osum[((int)wave * 16 + r) * LDO + (4 * c + i) * DPL + j] = acc[j][i] - off;
     __syncthreads();
     const int32_t orow = (int32_t)threadIdx.x / 16, oc = (int32_t)threadIdx.x % 16;
-    if (r0 + orow >= sp.rows) return;
+    if (orow >= 16 || r0 + orow >= sp.rows) return;
     float m = NEG;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) m = fmaxf(m, stat[w][orow][0]);
+    for (int w = 0; w < NW; ++w) m = fmaxf(m, stat[w][orow][0]);
     float o[DPL], l = 0.f, pmt = 0.f;
 #pragma unroll
     for (int j = 0; j < DPL; ++j) o[j] = 0.f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < NW; ++w) {
         if (stat[w][orow][1] == 0.f) continue;  // nothing seen (a NaN score leaves a NaN sum)
         const float f = __builtin_amdgcn_exp2f(stat[w][orow][0] - m);
         l += f * stat[w][orow][1];
@@ -1133,17 +1133,20 @@ template <class T, int D> static hipError_t attn_t(const AttnArgs &a, hipStream_
 {
     const int64_t wgs = (int64_t)a.batch * a.c.heads * a.tiles;
     if (wgs > 0x7FFFFFFF) return hipErrorInvalidValue;
-    if (a.chunk)
-        hipLaunchKernelGGL((attn_chunk_kernel<T, D>), dim3((uint32_t)wgs, (uint32_t)a.splits), dim3(512), 0, s, a);
+    const dim3 grid((uint32_t)wgs, (uint32_t)a.splits);
+    constexpr int WIDE = attn_wide_waves(D), ROWS = ChunkTile<T, D>::ROWS;
+    if (a.kernel == ATTN_CHUNK)
+        hipLaunchKernelGGL((attn_chunk_kernel<T, D>), grid, dim3(512), 0, s, a);
+    else if (a.kernel == ATTN_WIDE)
+        hipLaunchKernelGGL((attn_rows_kernel<T, D, WIDE>), grid, dim3(64 * WIDE), 0, s, a);
     else
-        hipLaunchKernelGGL((attn_rows_kernel<T, D>), dim3((uint32_t)wgs, (uint32_t)a.splits), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((attn_rows_kernel<T, D, 4>), grid, dim3(256), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
-    constexpr int ROWS = ChunkTile<T, D>::ROWS;
-    const int64_t row_tiles = (a.chunk ? ROWS / 4 : 4) * (int64_t)a.tiles;
+    const int64_t row_tiles = (a.kernel == ATTN_CHUNK ? ROWS / 4 : 4) * (int64_t)a.tiles;
     const int64_t joins = (int64_t)a.batch * a.c.heads * row_tiles;
     if (joins > 0x7FFFFFFF) return hipErrorInvalidValue;
-    if (a.chunk)
+    if (a.kernel == ATTN_CHUNK)
         hipLaunchKernelGGL((attn_join_kernel<T, D, ROWS, 64>), dim3((uint32_t)joins), dim3(256), 0, s, a,
                            (int32_t)row_tiles);
     else

@@ -352,22 +352,20 @@ static hipError_t few_t(const void *X, int64_t ldx, const int8_t *W, const float
 // lb_gemm_s8_linear.  A workgroup takes about as long whatever its tile (latency,
 // and some 47 KB a us of copies to a compute unit), so the narrowest tile whose
 // workgroups run at once, and the other kernels where none does.  Measured, bf16,
-// weights from memory, us here and there: 16 x 6000 x 4096 7.4 / 12.7, 1 x 8192 x
-// 8192 14.5 / 24.2, 24 x 8192 x 4096 9.4 / 13.7, 100 x 4096 x 4096 9.8 / 19.7,
-// 256 x 1376 x 4096 9.4 / 19.3, 64 x 8192 x 8192 24.2 / 26.2; past the rule 16 x
-// 11008 x 4096 15.4 / 13.9, 64 x 11008 x 4096 20.0 / 16.2, 100 x 8192 x 4096
-// 15.9 / 14.7, 331 x 4097 x 5504 34.3 / 22.8.
+// weights from HBM, us here and there: 1 x 4096 x 4096 6.5 / 18.6, 16 x 8000 x 2048
+// 6.1 / 10.9, 16 x 11008 x 4096 (48 columns) 12.9 / 14.0, 32 x 11008 x 4096 14.3 /
+// 14.7, 24 x 8192 x 4096 9.4 / 13.7, 100 x 4096 x 4096 9.8 / 19.7, 256 x 1376 x 4096
+// 9.4 / 19.3, 64 x 8192 x 8192 24.2 / 26.2; past the rule 16 x 16384 x 4096 (64
+// columns) 18.1 / 17.3, 64 x 11008 x 4096 (48) 17.5 / 15.9, 100 x 6000 x 4096 (48)
+// 13.9 / 14.1, 331 x 4097 x 5504 (64) 34.3 / 22.8.
 struct FewShape {
     int tm, tn;
 };
 static FewShape few_shape(int64_t M, int64_t N, int cu)
 {
-    auto count = [&](int64_t tm, int64_t tn) { return ((M + tm - 1) / tm) * ((N + tn - 1) / tn); };
-    // (two workgroups of the 16 x 16 tile run on a compute unit)
-    if (M <= 16) return count(16, 16) <= 2 * (int64_t)cu ? FewShape{16, 16} : FewShape{0, 0};
-    const int tm = M <= 32 ? 32 : 64;
-    if (count(tm, 16) <= cu) return {tm, 16};
-    if (count(tm, 32) <= cu) return {tm, 32};
+    const int tm = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+    for (int tn = 16; tn <= (tm == 64 ? 32 : 48); tn += 16)
+        if (((M + tm - 1) / tm) * ((N + tn - 1) / tn) <= cu) return {tm, tn};
     return {0, 0};
 }
 bool linear_is_few(int64_t M, int64_t N, int cu) { return few_shape(M, N, cu).tm != 0; }
@@ -378,8 +376,8 @@ static hipError_t linear_few_t(const int8_t *Xq, const int8_t *W, const float *s
 {
     const FewShape f = few_shape(M, N, cu);
 #define LB_FEW(...) few_t<T, __VA_ARGS__, false>(Xq, K, W, sx, sw, bias, out, M, N, K, s)
-    if (f.tm == 16) return LB_FEW(1, 1, 2, 2);
-    if (f.tm == 32) return f.tn == 16 ? LB_FEW(2, 1, 2, 2) : LB_FEW(2, 2, 2, 2);
+    if (f.tm == 16) return f.tn == 16 ? LB_FEW(1, 1, 2, 2) : f.tn == 32 ? LB_FEW(1, 2, 1, 3) : LB_FEW(1, 3, 2, 2);
+    if (f.tm == 32) return f.tn == 16 ? LB_FEW(2, 1, 2, 2) : f.tn == 32 ? LB_FEW(2, 2, 1, 3) : LB_FEW(2, 3, 1, 2);
     if (f.tm == 64) return f.tn == 16 ? LB_FEW(4, 1, 1, 3) : LB_FEW(4, 2, 1, 2);
 #undef LB_FEW
     return hipErrorInvalidValue;
@@ -402,14 +400,28 @@ bool linear_fuses(int64_t M, int64_t N, int64_t K, int cu)
     return M <= FUSED_ROWS && M * K <= FUSED_BYTES && linear_is_few(M, N, cu);
 }
 
-hipError_t launch_linear_fused(int ftype, const void *X, int64_t ldx, const int8_t *W, const float *sw,
-                               const void *bias, void *out, int64_t M, int64_t N, int64_t K, hipStream_t s)
+template <class T>
+static hipError_t linear_fused_t(const void *X, int64_t ldx, const int8_t *W, const float *sw, const void *bias,
+                                 void *out, int64_t M, int64_t N, int64_t K, int cu, hipStream_t s)
 {
-    if (M > FUSED_ROWS || M * K > FUSED_BYTES) return hipErrorInvalidValue;
+#define LB_FUSED(...) few_t<T, __VA_ARGS__, true>(X, ldx, W, nullptr, sw, bias, out, M, N, K, s)
+    switch (few_shape(M, N, cu).tn) {
+    case 16: return LB_FUSED(1, 1, 2, 3);
+    case 32: return LB_FUSED(1, 2, 1, 3);
+    case 48: return LB_FUSED(1, 3, 1, 3);
+    default: return hipErrorInvalidValue;
+    }
+#undef LB_FUSED
+}
+
+hipError_t launch_linear_fused(int ftype, const void *X, int64_t ldx, const int8_t *W, const float *sw,
+                               const void *bias, void *out, int64_t M, int64_t N, int64_t K, int cu, hipStream_t s)
+{
+    if (!linear_fuses(M, N, K, cu)) return hipErrorInvalidValue;
     switch (ftype) {
-    case LB_BF16: return few_t<__bf16, 1, 1, 2, 3, true>(X, ldx, W, nullptr, sw, bias, out, M, N, K, s);
-    case LB_F16: return few_t<_Float16, 1, 1, 2, 3, true>(X, ldx, W, nullptr, sw, bias, out, M, N, K, s);
-    case LB_F32: return few_t<float, 1, 1, 2, 3, true>(X, ldx, W, nullptr, sw, bias, out, M, N, K, s);
+    case LB_BF16: return linear_fused_t<__bf16>(X, ldx, W, sw, bias, out, M, N, K, cu, s);
+    case LB_F16: return linear_fused_t<_Float16>(X, ldx, W, sw, bias, out, M, N, K, cu, s);
+    case LB_F32: return linear_fused_t<float>(X, ldx, W, sw, bias, out, M, N, K, cu, s);
     default: return hipErrorInvalidValue;
     }
 }
