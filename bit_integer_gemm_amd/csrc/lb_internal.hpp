@@ -94,20 +94,23 @@ hipError_t launch_kv4_write(int ftype, const void *K, const void *V, int64_t ldk
 hipError_t launch_kv4_read(int ftype, const Kv4Cache &c, const int64_t *slots, void *K, void *V, int64_t T,
                            int D, hipStream_t s);
 
-// The attention kernels: 16 rows to a workgroup of four waves, or of as many as a
-// compute unit holds; 256 rows (D = 256: 128).
-enum { ATTN_ROWS = 0, ATTN_WIDE = 1, ATTN_CHUNK = 2 };
+// The attention kernels: a tile of 16 rows to a workgroup of four waves, or of as
+// many as a compute unit holds; the work of all such tiles in equal shares; tiles of
+// 256 rows (D = 256: 128).
+enum { ATTN_ROWS = 0, ATTN_WIDE = 1, ATTN_FLAT = 2, ATTN_CHUNK = 3 };
+enum { ATTN_FLAT_BATCH = 1024 };   // sequences, at most
 struct AttnArgs {
     const void *q;
     void *out;
     float *lse;
     const int32_t *table, *q_off, *lens;
-    float *part;          // partial results of key ranges, if splits > 1
+    float *part;          // workspace: partial results of key ranges or shares
     Kv4Cache c;
     int64_t ldq, ldo, ldt, width;
     int64_t total_q;
-    int32_t group, batch, window, causal, splits;
-    int32_t unit;         // fewest blocks of keys (64 keys, or 32) worth a workgroup of their own
+    int32_t group, batch, window, causal;
+    int32_t splits;       // key ranges of a tile at most; ATTN_FLAT: shares at most
+    int32_t unit;         // fewest blocks of keys (ATTN_CHUNK: of 64, else of 32) worth a workgroup of their own
     int32_t kernel, tiles; // ATTN_*, and how many tiles of its rows a key head has
     uint32_t page_mul, page_shift; // division by the page size
     float scale2;         // softmax scale * log2(e)

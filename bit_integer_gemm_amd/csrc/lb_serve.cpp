@@ -71,43 +71,56 @@ lb::Kv4Cache cache_of(const uint8_t *Kc, const uint8_t *Vc, const void *Kp, cons
     return c;
 }
 
+// One attention call: the kernel, its tiles of rows per key head, the key ranges or
+// shares that it makes at most, and the workspace these take.
 struct AttnPlan {
     int kernel;
-    int64_t tiles, splits, unit, per_split;   // row tiles of a key head; key ranges at most; blocks of keys in
-                                              // one; workspace bytes per range
+    int64_t tiles, splits, unit, bytes;
 };
 
 AttnPlan plan_attn(int64_t B, int64_t total_q, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D,
-                   int64_t max_len, int64_t window, int cu)
+                   int64_t max_len, int64_t window, int cu, bool have_workspace, int64_t workspace_bytes)
 {
-    AttnPlan p;
+    AttnPlan p{lb::ATTN_ROWS, 0, 1, 1, 0};
     const int64_t rows = max_q * (Hq / Hkv);
-    // Many rows of a key head share its keys through LDS; few would leave most of
-    // that kernel's 256 rows empty.
-    const bool chunk = rows > 32;
-    const int64_t tile = !chunk ? 16 : D == 256 ? 128 : 256, block = chunk ? 64 : 32;
-    p.tiles = (rows + tile - 1) / tile;
     const int64_t keys = window > 0 ? std::min(max_len, window + max_q) : max_len;
-    const int64_t wgs = B * Hkv * p.tiles, blocks = std::max<int64_t>((keys + block - 1) / block, 1);
-    if (chunk) {
-        // One workgroup to a compute unit.  A range costs its rows' partial results in
-        // fp32, written and read, about as much as nine tiles of 64 keys: no ranges
-        // once there are workgroups for all units, and none below 16 tiles.
+    if (rows > 192) {
+        // Many rows of a key head share its keys through LDS.  One workgroup to a
+        // compute unit; a range costs its rows' partial results in fp32, written and
+        // read, about as much as nine tiles of 64 keys: no ranges once there are
+        // workgroups for all units, and none below 16 tiles.
         p.kernel = lb::ATTN_CHUNK;
-        p.splits = std::min((int64_t)cu / wgs, blocks / 16);
-    } else if (2 * wgs <= cu) {
-        // Few tiles: workgroups that fill a compute unit, two blocks to a wave at
-        // least before there is a second range (and a launch to join them).
+        p.tiles = D == 256 ? (rows + 127) / 128 : (rows + 255) / 256;
+        const int64_t blocks = std::max<int64_t>((keys + 63) / 64, 1), per = total_q * Hq * (D + 2) * 4;
+        p.splits = std::min((int64_t)cu / (B * Hkv * p.tiles), blocks / 16);
+        if (!have_workspace) workspace_bytes = p.splits * per;
+        p.splits = std::max<int64_t>(1, std::min({p.splits, (int64_t)64, workspace_bytes / per}));
+        p.unit = (blocks + p.splits - 1) / p.splits;
+        p.bytes = p.splits > 1 ? p.splits * per : 0;
+        return p;
+    }
+    p.tiles = (rows + 15) / 16;
+    const int64_t wgs = B * Hkv * p.tiles, blocks = std::max<int64_t>((keys + 31) / 32, 1), part = 16 * (D + 2) * 4;
+    if (wgs <= cu) {
+        // Workgroups that fill a compute unit, two blocks to a wave at least before
+        // there is a second range (and a launch to join them).
         p.kernel = lb::ATTN_WIDE;
         p.splits = std::min((int64_t)cu / wgs, blocks / (2 * lb::attn_wide_waves((int)D)));
-    } else {
-        // Small workgroups in number even out sequences of different lengths.
-        p.kernel = lb::ATTN_ROWS;
-        p.splits = std::min((8 * (int64_t)cu + wgs - 1) / wgs, blocks / 32);
+        if (!have_workspace) workspace_bytes = p.splits * wgs * part;
+        p.splits = std::max<int64_t>(1, std::min({p.splits, (int64_t)64, workspace_bytes / (wgs * part)}));
+        p.unit = (blocks + p.splits - 1) / p.splits;
+        p.bytes = p.splits > 1 ? p.splits * wgs * part : 0;
+    } else if (wgs < 8 * (int64_t)cu && B <= lb::ATTN_FLAT_BATCH && window == 0 && blocks >= 96) {
+        // Some tiles to a compute unit, whose lengths may differ: equal shares, as many
+        // as run at once.  (Many more tiles even out by themselves, windows make them
+        // equal, and short ones are not worth a second launch.)
+        const int64_t shares = (D == 256 ? 2 : 3) * (int64_t)cu, bytes = shares * (2 * part + 16);
+        if (!have_workspace || workspace_bytes >= bytes) {
+            p.kernel = lb::ATTN_FLAT;
+            p.splits = shares;
+            p.bytes = bytes;
+        }
     }
-    p.splits = std::max<int64_t>(1, std::min<int64_t>(p.splits, 64));
-    p.unit = (blocks + p.splits - 1) / p.splits;
-    p.per_split = total_q * Hq * (D + 2) * 4;
     return p;
 }
 
@@ -214,8 +227,8 @@ int64_t lb_attn_kv4_workspace(int64_t B, int64_t total_q, int64_t max_q, int64_t
 {
     if (check_attn(B, total_q, max_q, Hq, Hkv, D, max_len, window) != LB_OK) return 0;
     if (cu_count <= 0 && lb::device_cu_count(&cu_count) != LB_OK) return 0;
-    const AttnPlan p = plan_attn(B, total_q, std::min(max_q, total_q), Hq, Hkv, D, max_len, window, cu_count);
-    return p.splits > 1 ? round_up(p.splits * p.per_split, 256) : 0;
+    return round_up(plan_attn(B, total_q, std::min(max_q, total_q), Hq, Hkv, D, max_len, window, cu_count, false, 0).bytes,
+                    256);
 }
 
 int lb_attn_kv4(const void *Q, int64_t ldq, const uint8_t *Kc, const uint8_t *Vc, const void *Kp,
@@ -240,10 +253,8 @@ int lb_attn_kv4(const void *Q, int64_t ldq, const uint8_t *Kc, const uint8_t *Vc
         return LB_ERR_ALIGN;
     const int cu = cu_count();
     max_q = std::min(max_q, total_q);
-    const AttnPlan p = plan_attn(B, total_q, max_q, Hq, Hkv, D, max_len, window, cu);
-    int64_t splits = p.splits;
-    if (!workspace || workspace_bytes <= 0) splits = 1;
-    else splits = std::max<int64_t>(1, std::min(splits, workspace_bytes / p.per_split));
+    const AttnPlan p = plan_attn(B, total_q, max_q, Hq, Hkv, D, max_len, window, cu, true,
+                                 workspace ? std::max<int64_t>(workspace_bytes, 0) : 0);
 
     lb::AttnArgs a;
     a.q = Q;
@@ -263,8 +274,8 @@ int lb_attn_kv4(const void *Q, int64_t ldq, const uint8_t *Kc, const uint8_t *Vc
     a.batch = (int32_t)B;
     a.window = (int32_t)window;
     a.causal = causal != 0;
-    a.splits = (int32_t)splits;
-    a.unit = splits == p.splits ? (int32_t)p.unit : 1;
+    a.splits = (int32_t)p.splits;
+    a.unit = (int32_t)p.unit;
     a.kernel = p.kernel;
     a.tiles = (int32_t)p.tiles;
     // key / page = mulhi(key, mul) >> shift with 2^shift the power of two below page:

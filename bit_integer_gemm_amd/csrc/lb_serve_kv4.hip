@@ -223,12 +223,12 @@ __device__ inline i32x4 query_order(i32x4 w)
                  (int)((w1 & 0xFFFFu) | (w3 << 16)), (int)((w1 >> 16) | (w3 & 0xFFFF0000u))};
 }
 
-// What one workgroup of either attention kernel works on.
+// What one workgroup of an attention kernel works on.
 struct Span {
     int32_t n, nq, rows;   // keys and queries of the sequence, rows of its key head
     int64_t q0;            // first query
 };
-__device__ inline Span span_of(const AttnArgs &a, int32_t b)
+__device__ inline Span lane_span_of(const AttnArgs &a, int32_t b)   // b may differ between lanes
 {
     Span s;
     const int64_t cap = a.width * a.c.page;
@@ -239,6 +239,15 @@ __device__ inline Span span_of(const AttnArgs &a, int32_t b)
     q1 = q1 < q0 ? q0 : q1 > a.total_q ? a.total_q : q1;
     s.q0 = q0;
     s.nq = (int32_t)(q1 - q0);
+    s.rows = s.nq * a.group;
+    return s;
+}
+__device__ inline Span span_of(const AttnArgs &a, int32_t b)        // b is the same in all
+{
+    Span s = lane_span_of(a, b);
+    s.n = __builtin_amdgcn_readfirstlane(s.n);
+    s.nq = __builtin_amdgcn_readfirstlane(s.nq);
+    s.q0 = __builtin_amdgcn_readfirstlane((int32_t)s.q0);
     s.rows = s.nq * a.group;
     return s;
 }
@@ -264,9 +273,31 @@ __device__ inline int32_t key_lo(const AttnArgs &a, const Span &s, int32_t qi)
     return a.window > 0 ? max(0, s.n - s.nq + qi + 1 - a.window) : 0;
 }
 
-// How the keys [lo, hi) of a tile of rows are shared: nb blocks of keys from block
-// b0, `per` to a workgroup, `ranges` workgroups (at most a.splits; one writes the
-// output itself).
+// Keys that some row of r0 .. r0 + n - 1 sees.
+__device__ inline void tile_keys(const AttnArgs &a, const Span &sp, int32_t r0, int32_t n, int32_t &lo, int32_t &hi)
+{
+    lo = key_lo(a, sp, r0 / a.group);
+    hi = key_hi(a, sp, min(r0 + n - 1, sp.rows - 1) / a.group);
+}
+
+// Row `row` of key head h, dims oc D/16 .. of it: o / l, and m + log2(l).
+template <class T, int D>
+__device__ inline void rows_out(const AttnArgs &a, const Span &sp, int32_t h, int32_t row, int32_t oc,
+                                const float (&o)[D / 16], float m, float l)
+{
+    const int32_t oq = row / a.group, oh = h * a.group + (row - oq * a.group);
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    T *po = (T *)a.out + (sp.q0 + oq) * a.ldo + (int64_t)oh * D + oc * (D / 16);
+#pragma unroll
+    for (int j = 0; j < D / 16; j += 2) *(uint32_t *)(po + j) = pack2<T>(o[j] * inv, o[j + 1] * inv);
+    if (a.lse && oc == 0)
+        a.lse[(sp.q0 + oq) * (int64_t)(a.group * a.c.heads) + oh] =
+            l == 0.f ? -__builtin_inff() : (m + __builtin_log2f(l)) * 0.6931471805599453f;
+}
+
+// How the keys [lo, hi) of a tile of rows are shared where each tile is cut by
+// itself: nb blocks of keys from block b0, `per` to a workgroup, `ranges` workgroups
+// (at most a.splits; one writes the output itself).
 struct Ranges {
     int32_t b0, nb, per, ranges;
 };
@@ -291,9 +322,11 @@ __device__ inline float sum_over_groups(float x)
     return x + __shfl_xor(x, 32);
 }
 
-// Sixteen rows against a range of keys.  Each of NW waves takes blocks of 32 keys
-// (two half-blocks of 16, each inside one page) and keeps its own maximum, sum and
-// output; they meet in LDS.  Lane l = 16 c + r:
+// Sixteen rows (r0 ..) of a key head against blocks [first, last) of 32 keys.  Each
+// of NW waves takes its share of the blocks (two half-blocks of 16 keys, each inside
+// one page) and keeps its own maximum, sum and output; they meet in LDS.  part: where
+// the rows' outputs (16 x D), maxima and sums (16 x 2) go unweighted, or null where
+// these are all their keys and the output is written.  Lane l = 16 c + r:
 //   scores    A: key r of a half-block, levels [c D/4, (c+1) D/4);  B: row r.
 //             It ends with keys 4c .. 4c+3 of each half-block for row r;
 //   values    those eight keys are its share of the contraction as they stand:
@@ -304,30 +337,27 @@ __device__ inline float sum_over_groups(float x)
 // values as soon as this one's are, into the same registers, and the numbers of
 // its pages a block earlier.  (Two blocks' worth of registers cost more in waves
 // per SIMD than the longer lead gave.)
+template <int D, int NW> struct RowsLds {
+    static constexpr int LDO = D + 4;
+    float osum[NW * 16 * LDO];
+    float stat[NW][16][4];
+};
+
 template <class T, int D, int NW>
-__global__ __launch_bounds__(64 * NW, NW == 4 ? (D == 256 ? 2 : 3) : NW / 4) void attn_rows_kernel(AttnArgs a)
+__device__ __forceinline__ void rows_segment(const AttnArgs &a, RowsLds<D, NW> &lds, const Span &sp, int32_t b, int32_t h,
+                                             int32_t r0, int32_t lo, int32_t hi, int32_t first, int32_t last, float *part)
 {
     using MM = Mfma<T>;
     constexpr int KW = D / 32;     // words of a key a lane reads, = MFMAs per half-block
     constexpr int DPL = D / 16;    // dims of a value a lane reads, = MFMAs per block
     constexpr int VW = DPL / 8 ? DPL / 8 : 1;
-    constexpr int LDO = D + 4;
-    __shared__ float osum[NW * 16 * LDO];
-    __shared__ float stat[NW][16][4];
+    constexpr int LDO = RowsLds<D, NW>::LDO;
+    auto &osum = lds.osum;
+    auto &stat = lds.stat;
     const uint32_t lane = threadIdx.x & 63u;
     const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int32_t r = (int32_t)(lane & 15u), c = (int32_t)(lane >> 4);
-    const int32_t bh = (int32_t)(blockIdx.x / (uint32_t)a.tiles), tile = (int32_t)(blockIdx.x % (uint32_t)a.tiles);
-    const int32_t b = bh / a.c.heads, h = bh - b * a.c.heads;
-    const Span sp = span_of(a, b);
-    const int32_t r0 = tile * 16;
-    if (r0 >= sp.rows) return;
-
     const int32_t qi_first = r0 / a.group, qi_last = min(r0 + 15, sp.rows - 1) / a.group;
-    const int32_t lo = key_lo(a, sp, qi_first), hi = key_hi(a, sp, qi_last);
-    const Ranges rg = ranges_of<32>(a, lo, hi);
-    if ((int32_t)blockIdx.y >= rg.ranges) return;
-    const int32_t first = rg.b0 + (int32_t)blockIdx.y * rg.per, last = min(rg.b0 + rg.nb, first + rg.per);
 
     uint32_t kw[2][KW], vw[8][VW];
     u32x4 kp[2], vp[2];
@@ -535,25 +565,240 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? (D == 256 ? 2 : 3) : NW / 4) voi
 #pragma unroll
         for (int j = 0; j < DPL; ++j) o[j] += f * osum[(w * 16 + orow) * LDO + oc * DPL + j];
     }
-    const int32_t oq = (r0 + orow) / a.group, oh = h * a.group + (r0 + orow - oq * a.group);
-    const int64_t grow = (sp.q0 + oq) * (int64_t)(a.group * a.c.heads) + oh;
-    if (rg.ranges > 1) {
-        const int64_t nrows = a.total_q * (int64_t)(a.group * a.c.heads);
-        float *po = a.part + ((int64_t)blockIdx.y * nrows + grow) * D + oc * DPL;
+    if (part) {
 #pragma unroll
-        for (int j = 0; j < DPL; ++j) po[j] = o[j] + pmt;
-        if (oc == 0) {
-            float *ps = a.part + (int64_t)a.splits * nrows * D + ((int64_t)blockIdx.y * nrows + grow) * 2;
-            ps[0] = m;
-            ps[1] = l;
-        }
+        for (int j = 0; j < DPL; ++j) part[orow * D + oc * DPL + j] = o[j] + pmt;
+        if (oc == 0) *(f32x2 *)(part + 16 * D + 2 * orow) = f32x2{m, l};
         return;
     }
-    const float inv = l == 0.f ? 0.f : 1.0f / l;
-    T *po = (T *)a.out + (sp.q0 + oq) * a.ldo + (int64_t)oh * D + oc * DPL;
 #pragma unroll
-    for (int j = 0; j < DPL; ++j) po[j] = (T)((o[j] + pmt) * inv);
-    if (a.lse && oc == 0) a.lse[grow] = l == 0.f ? NEG : (m + __builtin_log2f(l)) * 0.6931471805599453f;
+    for (int j = 0; j < DPL; ++j) o[j] += pmt;
+    rows_out<T, D>(a, sp, h, r0 + orow, oc, o, m, l);
+}
+
+// Where a workgroup leaves a part of a tile: outputs, maxima and sums of 16 rows.
+template <int D> struct Part {
+    static constexpr int64_t FLOATS = 16 * (D + 2);
+};
+
+// Row `row` of a tile joined from n parts, part k at part_of(k), in their order.
+template <class T, int D, class F>
+__device__ inline void join_parts(const AttnArgs &a, const Span &sp, int32_t h, int32_t r0, int32_t n, F part_of)
+{
+    constexpr int DPL = D / 16;
+    const int32_t orow = (int32_t)threadIdx.x / 16, oc = (int32_t)threadIdx.x % 16;
+    if (r0 + orow >= sp.rows) return;
+    float m = -__builtin_inff(), l = 0.f, o[DPL];
+#pragma unroll
+    for (int j = 0; j < DPL; ++j) o[j] = 0.f;
+    for (int32_t k0 = 0; k0 < n; k0 += 8) {
+        f32x2 ml[8];
+        float v[8][DPL];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float *part = part_of(min(k0 + k, n - 1));
+            ml[k] = *(const f32x2 *)(part + 16 * D + 2 * orow);
+#pragma unroll
+            for (int j = 0; j < DPL; ++j) v[k][j] = part[orow * D + oc * DPL + j];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (k0 + k >= n || ml[k].y == 0.f) continue;   // nothing seen there
+            const float m_new = fmaxf(m, ml[k].x);
+            const float f0 = l == 0.f ? 0.f : __builtin_amdgcn_exp2f(m - m_new);
+            const float f1 = __builtin_amdgcn_exp2f(ml[k].x - m_new);
+            m = m_new;
+            l = l * f0 + f1 * ml[k].y;
+#pragma unroll
+            for (int j = 0; j < DPL; ++j) o[j] = o[j] * f0 + f1 * v[k][j];
+        }
+    }
+    rows_out<T, D>(a, sp, h, r0 + orow, oc, o, m, l);
+}
+
+// A tile of sixteen rows, or a range of its keys, to a workgroup.
+template <class T, int D, int NW>
+__global__ __launch_bounds__(64 * NW, NW == 4 ? (D == 256 ? 2 : 3) : NW / 4) void attn_rows_kernel(AttnArgs a)
+{
+    __shared__ RowsLds<D, NW> lds;
+    const int32_t bh = (int32_t)(blockIdx.x / (uint32_t)a.tiles), tile = (int32_t)(blockIdx.x % (uint32_t)a.tiles);
+    const int32_t b = bh / a.c.heads, h = bh - b * a.c.heads;
+    const Span sp = span_of(a, b);
+    const int32_t r0 = tile * 16;
+    if (r0 >= sp.rows) return;
+    int32_t lo, hi;
+    tile_keys(a, sp, r0, 16, lo, hi);
+    const Ranges rg = ranges_of<32>(a, lo, hi);
+    if ((int32_t)blockIdx.y >= rg.ranges) return;
+    const int32_t first = rg.b0 + (int32_t)blockIdx.y * rg.per, last = min(rg.b0 + rg.nb, first + rg.per);
+    rows_segment<T, D, NW>(a, lds, sp, b, h, r0, lo, hi, first, last,
+                           rg.ranges == 1 ? nullptr
+                                          : a.part + ((int64_t)blockIdx.x * a.splits + blockIdx.y) * Part<D>::FLOATS);
+}
+
+template <class T, int D> __global__ __launch_bounds__(256) void attn_rows_join_kernel(AttnArgs a)
+{
+    const int32_t bh = (int32_t)(blockIdx.x / (uint32_t)a.tiles), tile = (int32_t)(blockIdx.x % (uint32_t)a.tiles);
+    const int32_t b = bh / a.c.heads, h = bh - b * a.c.heads;
+    const Span sp = span_of(a, b);
+    const int32_t r0 = tile * 16;
+    if (r0 >= sp.rows) return;
+    int32_t lo, hi;
+    tile_keys(a, sp, r0, 16, lo, hi);
+    const Ranges rg = ranges_of<32>(a, lo, hi);
+    if (rg.ranges == 1) return;
+    join_parts<T, D>(a, sp, h, r0, rg.ranges,
+                     [&](int32_t k) { return a.part + ((int64_t)blockIdx.x * a.splits + k) * Part<D>::FLOATS; });
+}
+
+// The tiles of all sequences laid end to end, FLAT_COST units for a tile's start
+// (which takes about as long as that many blocks) and one for each of its blocks, and
+// cut into equal shares, one to a workgroup: lengths may differ as they like, and
+// every compute unit has the same work.  Tiles that are nearly equal anyway, and no
+// more than there are workgroups, stay whole, one to each.  A share's cut tiles leave
+// their parts, the one that continues from the share before in part 2 i, the one that
+// goes on in the next in 2 i + 1; the workgroup that ends a cut tile notes where it
+// started, for attn_flat_join_kernel.
+enum { FLAT_COST = 14, FLAT_LEAST = 24, FLAT_BATCH = ATTN_FLAT_BATCH };
+template <class T, int D>
+__global__ __launch_bounds__(256, D == 256 ? 2 : 3) void attn_flat_kernel(AttnArgs a)
+{
+    __shared__ RowsLds<D, 4> lds;
+    __shared__ int64_t before[FLAT_BATCH + 1];         // units of the sequences before each
+    __shared__ int32_t tiles_before[FLAT_BATCH + 1];   // and their tiles
+    __shared__ int64_t wave_sum[4];
+    __shared__ int32_t wave_tiles[4], wave_most[4];   // tiles, and units of the largest
+    __shared__ int32_t start_b;
+    const int32_t tid = (int32_t)threadIdx.x;
+    const int32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    auto tile_blocks = [&](const Span &sp, int32_t r0) {
+        int32_t lo, hi;
+        tile_keys(a, sp, r0, 16, lo, hi);
+        return max(0, (hi + 31) / 32 - lo / 32);
+    };
+    auto tiles_of = [&](const Span &sp) { return min((sp.rows + 15) / 16, a.tiles); };
+    {
+        int64_t mine[4], sum = 0;
+        int32_t mine_tiles[4], count = 0, most = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int32_t b = 4 * tid + k;
+            mine[k] = sum;
+            mine_tiles[k] = count;
+            if (b >= a.batch) continue;
+            const Span sp = lane_span_of(a, b);
+            const int32_t tiles = tiles_of(sp);
+            int64_t u = 0;
+            for (int32_t t = 0; t < tiles; ++t) {
+                const int32_t len = FLAT_COST + tile_blocks(sp, 16 * t);
+                u += len;
+                most = max(most, len);
+            }
+            sum += u * a.c.heads;
+            count += tiles * a.c.heads;
+        }
+        int64_t upto = sum;
+        int32_t upto_tiles = count;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int64_t x = __shfl_up(upto, d);
+            const int32_t y = __shfl_up(upto_tiles, d);
+            if ((tid & 63) >= d) {
+                upto += x;
+                upto_tiles += y;
+            }
+            most = max(most, __shfl_xor(most, d));
+        }
+        if ((tid & 63) == 63) {
+            wave_sum[wave] = upto;
+            wave_tiles[wave] = upto_tiles;
+            wave_most[wave] = most;
+        }
+        __syncthreads();
+        int64_t base = upto - sum;
+        int32_t base_tiles = upto_tiles - count;
+        for (int w = 0; w < wave; ++w) {
+            base += wave_sum[w];
+            base_tiles += wave_tiles[w];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            before[4 * tid + k] = base + mine[k];
+            tiles_before[4 * tid + k] = base_tiles + mine_tiles[k];
+        }
+        if (tid == 255) {
+            before[FLAT_BATCH] = base + sum;
+            tiles_before[FLAT_BATCH] = base_tiles + count;
+        }
+        __syncthreads();
+    }
+    const int64_t total = before[FLAT_BATCH];
+    const int32_t tiles = tiles_before[FLAT_BATCH];
+    const int64_t most = max(max(wave_most[0], wave_most[1]), max(wave_most[2], wave_most[3]));
+    const bool whole = tiles <= (int32_t)gridDim.x && 8 * most * tiles <= 9 * total;
+    const int64_t shares = whole ? tiles : min((int64_t)gridDim.x, max((total + FLAT_LEAST - 1) / FLAT_LEAST, (int64_t)1));
+    const int64_t i = blockIdx.x;
+    int32_t *note = (int32_t *)(a.part + (int64_t)gridDim.x * 2 * Part<D>::FLOATS) + 4 * i;
+    if (tid == 0) note[3] = -1;
+    if (i >= shares) return;
+    const int64_t each = total / shares, more = total - each * shares;   // a share: `each` units, or one more
+    int64_t u = each * i + min(i, more), end = u + each + (i < more);
+    for (int32_t b = tid; b < a.batch; b += 256)
+        if (whole ? tiles_before[b] <= i && i < tiles_before[b + 1] : before[b] <= u && u < before[b + 1]) start_b = b;
+    __syncthreads();
+    int32_t b = __builtin_amdgcn_readfirstlane(start_b);
+    if (whole) {
+        const Span sp = span_of(a, b);
+        const int32_t per_head = tiles_of(sp), n = (int32_t)i - tiles_before[b];
+        u = before[b] + n / per_head * ((before[b + 1] - before[b]) / a.c.heads);
+        for (int32_t t = 0; t < n % per_head; ++t) u += FLAT_COST + tile_blocks(sp, 16 * t);
+        end = u + 1;   // as far as the tile goes, below
+    }
+    while (u < end) {
+        while (before[b + 1] <= u) ++b;
+        b = __builtin_amdgcn_readfirstlane(b);
+        const Span sp = span_of(a, b);
+        const int64_t in_b = u - before[b], per_head = (before[b + 1] - before[b]) / a.c.heads;
+        const int32_t h = __builtin_amdgcn_readfirstlane((int32_t)(in_b / per_head));
+        int64_t from = in_b - h * per_head;
+        int32_t t = 0, len = FLAT_COST + tile_blocks(sp, 0);
+        while (from >= len) {
+            from -= len;
+            ++t;
+            len = FLAT_COST + tile_blocks(sp, 16 * t);
+        }
+        t = __builtin_amdgcn_readfirstlane(t);
+        len = __builtin_amdgcn_readfirstlane(len);
+        const int32_t u0 = __builtin_amdgcn_readfirstlane((int32_t)from);
+        const int32_t u1 = __builtin_amdgcn_readfirstlane(whole ? len : (int32_t)min((int64_t)len, from + (end - u)));
+        int32_t lo, hi;
+        tile_keys(a, sp, 16 * t, 16, lo, hi);
+        const int32_t b0 = lo / 32;
+        float *part = u0 == 0 && u1 == len ? nullptr : a.part + (2 * i + (u0 == 0)) * Part<D>::FLOATS;
+        if (u0 > 0 && u1 == len && tid == 0) {
+            const int64_t s = u - u0, wide = (each + 1) * more;   // the tile's first unit, and its share
+            note[0] = b;
+            note[1] = h;
+            note[2] = 16 * t;
+            note[3] = (int32_t)(s < wide ? s / (each + 1) : more + (s - wide) / each);
+        }
+        rows_segment<T, D, 4>(a, lds, sp, b, h, 16 * t, lo, hi, b0 + max(u0 - FLAT_COST, 0), b0 + max(u1 - FLAT_COST, 0), part);
+        __syncthreads();
+        u += u1 - u0;
+    }
+}
+
+// The parts of the cut tiles, each joined where it ends, in the shares' order.
+template <class T, int D>
+__global__ __launch_bounds__(256) void attn_flat_join_kernel(AttnArgs a)
+{
+    const int32_t i = (int32_t)blockIdx.x;
+    const int32_t *note = (const int32_t *)(a.part + (int64_t)gridDim.x * 2 * Part<D>::FLOATS) + 4 * (int64_t)i;
+    const int32_t b = note[0], h = note[1], r0 = note[2], i0 = note[3];
+    if (i0 < 0) return;
+    const Span sp = span_of(a, b);
+    join_parts<T, D>(a, sp, h, r0, i - i0 + 1,
+                     [&](int32_t k) { return a.part + (2 * (int64_t)(i0 + k) + (k == 0)) * Part<D>::FLOATS; });
 }
 
 // ---- many rows -------------------------------------------------------------
@@ -1071,10 +1316,9 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
     }
 }
 
-// The partial results of key ranges joined, in the ranges' order: a wave per row,
-// whose lanes read whole partial rows, eight ranges at a time.  ROWS and BLOCK are
-// the kernel's that made them.
-template <class T, int D, int ROWS, int BLOCK>
+// The partial results of attn_chunk_kernel's key ranges joined, in the ranges'
+// order: a wave per row, whose lanes read whole partial rows, eight ranges at a time.
+template <class T, int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int32_t row_tiles)
 {
     constexpr int DPL = D / 64;
@@ -1084,8 +1328,9 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int32_t row_
     const Span sp = span_of(a, b);
     const int32_t row = tile * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     if (row >= sp.rows) return;
+    constexpr int ROWS = ChunkTile<T, D>::ROWS;
     const int32_t r0 = row / ROWS * ROWS;
-    const Ranges rg = ranges_of<BLOCK>(a, key_lo(a, sp, r0 / a.group),
+    const Ranges rg = ranges_of<64>(a, key_lo(a, sp, r0 / a.group),
                                        key_hi(a, sp, min(r0 + ROWS - 1, sp.rows - 1) / a.group));
     if (rg.ranges == 1) return;
     const int32_t oq = row / a.group, oh = h * a.group + (row - oq * a.group);
@@ -1131,27 +1376,34 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int32_t row_
 
 template <class T, int D> static hipError_t attn_t(const AttnArgs &a, hipStream_t s)
 {
+    if (a.kernel == ATTN_FLAT) {
+        hipLaunchKernelGGL((attn_flat_kernel<T, D>), dim3((uint32_t)a.splits), dim3(256), 0, s, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL((attn_flat_join_kernel<T, D>), dim3((uint32_t)a.splits), dim3(256), 0, s, a);
+        return hipGetLastError();
+    }
     const int64_t wgs = (int64_t)a.batch * a.c.heads * a.tiles;
     if (wgs > 0x7FFFFFFF) return hipErrorInvalidValue;
+    constexpr int WIDE = attn_wide_waves(D);
     const dim3 grid((uint32_t)wgs, (uint32_t)a.splits);
-    constexpr int WIDE = attn_wide_waves(D), ROWS = ChunkTile<T, D>::ROWS;
-    if (a.kernel == ATTN_CHUNK)
-        hipLaunchKernelGGL((attn_chunk_kernel<T, D>), grid, dim3(512), 0, s, a);
-    else if (a.kernel == ATTN_WIDE)
-        hipLaunchKernelGGL((attn_rows_kernel<T, D, WIDE>), grid, dim3(64 * WIDE), 0, s, a);
-    else
-        hipLaunchKernelGGL((attn_rows_kernel<T, D, 4>), grid, dim3(256), 0, s, a);
+    if (a.kernel != ATTN_CHUNK) {
+        if (a.kernel == ATTN_WIDE)
+            hipLaunchKernelGGL((attn_rows_kernel<T, D, WIDE>), grid, dim3(64 * WIDE), 0, s, a);
+        else
+            hipLaunchKernelGGL((attn_rows_kernel<T, D, 4>), grid, dim3(256), 0, s, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess || a.splits == 1) return e;
+        hipLaunchKernelGGL((attn_rows_join_kernel<T, D>), dim3((uint32_t)wgs), dim3(256), 0, s, a);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL((attn_chunk_kernel<T, D>), grid, dim3(512), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
-    const int64_t row_tiles = (a.kernel == ATTN_CHUNK ? ROWS / 4 : 4) * (int64_t)a.tiles;
+    const int64_t row_tiles = ChunkTile<T, D>::ROWS / 4 * (int64_t)a.tiles;
     const int64_t joins = (int64_t)a.batch * a.c.heads * row_tiles;
     if (joins > 0x7FFFFFFF) return hipErrorInvalidValue;
-    if (a.kernel == ATTN_CHUNK)
-        hipLaunchKernelGGL((attn_join_kernel<T, D, ROWS, 64>), dim3((uint32_t)joins), dim3(256), 0, s, a,
-                           (int32_t)row_tiles);
-    else
-        hipLaunchKernelGGL((attn_join_kernel<T, D, 16, 32>), dim3((uint32_t)joins), dim3(256), 0, s, a,
-                           (int32_t)row_tiles);
+    hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3((uint32_t)joins), dim3(256), 0, s, a, (int32_t)row_tiles);
     return hipGetLastError();
 }
 
