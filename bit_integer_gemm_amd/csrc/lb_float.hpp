@@ -60,12 +60,4 @@ __device__ inline void store_scaled(const T *bias, T *out, int64_t o, int64_t n,
     }
 }
 
-// Largest value of a float in a 16-bit type's exponent field, as a bit test:
-// |x| >= inf (infinity or NaN) in either half of a word.
-template <class T> __device__ inline bool any_nonfinite(uint32_t w)
-{
-    const uint32_t inf = sizeof(T) == 2 && __is_same(T, __bf16) ? 0x7F80u : 0x7C00u;
-    return (w & 0x7FFFu) >= inf || ((w >> 16) & 0x7FFFu) >= inf;
-}
-
 }  // namespace lb

@@ -86,6 +86,7 @@ struct Kv4Cache {
     uint32_t *kp, *vp;   // one word per vector: scale in the low half, minimum in the high half
     int64_t pages;
     int32_t page, heads;
+    uint32_t page_mul, page_shift;   // slot / page = mulhi(slot, page_mul) >> page_shift, slots below 2^31
 };
 // New keys and values (T tokens, ld elements apart, heads x D each) into slots;
 // and vectors of slots out again.
@@ -112,7 +113,6 @@ struct AttnArgs {
     int32_t splits;       // key ranges of a tile at most; ATTN_FLAT: shares at most
     int32_t unit;         // fewest blocks of keys (ATTN_CHUNK: of 64, else of 32) worth a workgroup of their own
     int32_t kernel, tiles; // ATTN_*, and how many tiles of its rows a key head has
-    uint32_t page_mul, page_shift; // division by the page size
     float scale2;         // softmax scale * log2(e)
 };
 // Waves of an ATTN_WIDE workgroup.

@@ -50,7 +50,7 @@ int scaled(const int8_t *X, const int8_t *W, const float *sx, const float *sw, c
 int check_cache(int64_t heads, int64_t D, int64_t pages, int64_t page, int ftype)
 {
     if (heads <= 0 || pages <= 0 || page <= 0 || (D != 64 && D != 128 && D != 256)) return LB_ERR_SHAPE;
-    if (heads > 65535 || pages > kLim || page > kLim || (double)pages * (double)page >= 2147483648.0)
+    if (heads > 32767 || pages > kLim || page > kLim || (double)pages * (double)page >= 2147483648.0)
         return LB_ERR_SHAPE;
     if (page % LB_KV4_PAGE_ALIGN != 0) return LB_ERR_ALIGN;
     if (!short_ftype(ftype)) return LB_ERR_VARIANT;
@@ -68,6 +68,12 @@ lb::Kv4Cache cache_of(const uint8_t *Kc, const uint8_t *Vc, const void *Kp, cons
     c.pages = pages;
     c.page = (int32_t)page;
     c.heads = (int32_t)heads;
+    // slot / page = mulhi(slot, mul) >> shift with 2^shift the power of two below page:
+    // mul = ceil(2^(32 + shift) / page) < 2^32, and mul page - 2^(32 + shift) < page
+    // <= 2^(shift + 1), so the quotient is exact for slots below 2^31.
+    c.page_shift = 31 - (uint32_t)__builtin_clz((uint32_t)page);
+    if ((page & (page - 1)) == 0) --c.page_shift;
+    c.page_mul = (uint32_t)((((uint64_t)1 << (32 + c.page_shift)) + (uint64_t)page - 1) / (uint64_t)page);
     return c;
 }
 
@@ -213,7 +219,7 @@ static int check_attn(int64_t B, int64_t total_q, int64_t max_q, int64_t Hq, int
 {
     if (B <= 0 || total_q <= 0 || max_q <= 0 || Hq <= 0 || Hkv <= 0 || max_len < 0 || window < 0)
         return LB_ERR_SHAPE;
-    if (B > kLim || total_q > kLim || max_q > kLim || Hq > 65535 || Hkv > 65535 || max_len > kLim || window > kLim)
+    if (B > kLim || total_q > kLim || max_q > kLim || Hq > 65535 || Hkv > 32767 || max_len > kLim || window > kLim)
         return LB_ERR_SHAPE;
     if (Hq % Hkv != 0 || (D != 64 && D != 128 && D != 256)) return LB_ERR_SHAPE;
     // row numbers of a key head, and of the whole batch's tiles, are 32-bit
@@ -278,12 +284,6 @@ int lb_attn_kv4(const void *Q, int64_t ldq, const uint8_t *Kc, const uint8_t *Vc
     a.unit = (int32_t)p.unit;
     a.kernel = p.kernel;
     a.tiles = (int32_t)p.tiles;
-    // key / page = mulhi(key, mul) >> shift with 2^shift the power of two below page:
-    // mul = ceil(2^(32 + shift) / page) < 2^32, and mul page - 2^(32 + shift) < page
-    // <= 2^(shift + 1), so the quotient is exact for keys below 2^31.
-    a.page_shift = 31 - (uint32_t)__builtin_clz((uint32_t)page);
-    if ((page & (page - 1)) == 0) --a.page_shift;
-    a.page_mul = (uint32_t)((((uint64_t)1 << (32 + a.page_shift)) + (uint64_t)page - 1) / (uint64_t)page);
     a.scale2 = scale * 1.44269504088896340736f;
     return finish(lb::launch_attn(ftype, (int)D, a, (hipStream_t)stream));
 }

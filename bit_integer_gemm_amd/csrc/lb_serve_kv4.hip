@@ -13,41 +13,48 @@
 namespace lb {
 
 // ---- write -----------------------------------------------------------------
-// (x - m) / s decides between levels at half-integers.  The product with 1/s is
-// off by less than 2^-19 (15 * 3 * 2^-24), so it settles the level unless it lies
-// within 2^-12 of a half-integer; there the correctly rounded quotient decides.
-__device__ inline uint32_t level_of(float x, float m, float s, float inv, bool direct)
+// Both kernels: D/8 lanes per vector, eight numbers (16 bytes) and one word of levels
+// each, of a key and its value; a workgroup takes neighbouring tokens of one head,
+// whose levels lie next to each other in the cache where their slots do, and the
+// next workgroup the next head of the same tokens, whose numbers lie next to theirs.
+
+// slot / page by a multiplication (page_mul is 2^(32 + page_shift) / page rounded up).
+__device__ inline int32_t slot_page(const Kv4Cache &c, int64_t slot) { return (int32_t)(__umulhi((uint32_t)slot, c.page_mul) >> c.page_shift); }
+
+// Least (most) of x over the N lanes (8, 16 or 32) of a vector, in all of them.
+template <int CTRL> __device__ inline float lane_dpp(float x)
 {
-    const float y = x - m, t = y * inv;
-    float n = __builtin_rintf(t);
-    if (direct || __builtin_fabsf(t - n) > 0.5f - 0x1p-12f) n = __builtin_rintf(y / s);
-    return (uint32_t)fminf(n, 15.f);
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xF, 0xF, true));
+}
+template <int N, class F> __device__ inline float over_lanes(float x, F f)
+{
+    x = f(x, lane_dpp<0xB1>(x));     // lane ^ 1
+    x = f(x, lane_dpp<0x4E>(x));     // lane ^ 2
+    x = f(x, lane_dpp<0x141>(x));    // the other four of eight, mirrored
+    if constexpr (N >= 16) x = f(x, lane_dpp<0x140>(x));   // the other eight of sixteen
+    if constexpr (N >= 32) x = f(x, __shfl_xor(x, 16));
+    return x;
 }
 
-// D/8 lanes per vector, 8 elements (16 bytes in, one word of levels out) each;
-// blockIdx.y: 0 keys, 1 values.  A slot outside the cache is not written.
+// (x - m) / s decides between levels at half-integers.  The product with 1/s (one
+// step off at most) is off by less than 2^-18 (15 * 4 * 2^-24), so it settles the
+// levels unless one lies within 2^-16 of a half-integer; then the correctly rounded
+// quotients decide (a division for every number made the kernel's time that of its
+// vector instructions).  So they do for subnormal scales, whose rounding may put the
+// largest number past 15.5; a normal one puts it below 15.1.  A slot outside the
+// cache is not written.
 template <class T, int D>
-__global__ __launch_bounds__(256) void kv4_write_kernel(const T *__restrict__ K, const T *__restrict__ V,
-                                                        int64_t ldk, int64_t ldv,
-                                                        const int64_t *__restrict__ slots, Kv4Cache c,
-                                                        int64_t vectors)
+__device__ inline void write_vector(const Kv4Cache &c, i32x4 w, int64_t slot, int32_t h, uint32_t sub, uint8_t *levels,
+                                    uint32_t *params)
 {
     constexpr int LPV = D / 8;
-    const int64_t vec = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPV;
-    const uint32_t sub = threadIdx.x % LPV;
-    if (vec >= vectors) return;  // whole groups of LPV lanes
-    const bool val = blockIdx.y != 0;
-    const int64_t t = vec / c.heads, h = vec - t * c.heads;
-    const int64_t slot = slots[t];
-    const T *src = (val ? V + t * ldv : K + t * ldk) + h * D + sub * 8;
-    const i32x4 w = *(const i32x4 *)src;
     float x[8];
     bool odd = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         x[2 * i] = lo_f32<T>((uint32_t)w[i]);
         x[2 * i + 1] = hi_f32<T>((uint32_t)w[i]);
-        odd |= any_nonfinite<T>((uint32_t)w[i]);
+        odd |= __builtin_isunordered(x[2 * i], x[2 * i + 1]);
     }
     float lo = x[0], hi = x[0];
 #pragma unroll
@@ -55,32 +62,61 @@ __global__ __launch_bounds__(256) void kv4_write_kernel(const T *__restrict__ K,
         lo = fminf(lo, x[i]);
         hi = fmaxf(hi, x[i]);
     }
-    int bad = odd;
-#pragma unroll
-    for (int d = 1; d < LPV; d <<= 1) {
-        lo = fminf(lo, __shfl_xor(lo, d));
-        hi = fmaxf(hi, __shfl_xor(hi, d));
-        bad |= __shfl_xor(bad, d);
-    }
-    const T st = (T)((hi - lo) / 15.0f);
-    const float s = (float)st;
-    bad |= !(s < __builtin_inff());  // the range of the vector overflows
-    const bool flat = !(s > 0.f) || bad;
-    const bool direct = s < 0x1p-100f;
-    const float inv = 1.0f / s;
+    lo = over_lanes<LPV>(lo, [](float p, float q) { return fminf(p, q); });
+    hi = over_lanes<LPV>(hi, [](float p, float q) { return fmaxf(p, q); });
+    const float s = (float)(T)((hi - lo) / 15.0f);
+    // a NaN, or a range that is not finite
+    const uint64_t odds = __ballot(odd) >> ((threadIdx.x & 63u) / LPV * LPV);
+    const bool bad = (odds & (((uint64_t)1 << LPV) - 1)) != 0 || !(s < __builtin_inff());
     uint32_t word = 0;
-    if (!flat) {
+    if (s > 0.f && !bad) {
+        const float inv = __builtin_amdgcn_rcpf(s);
+        float n[8], far = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) word |= level_of(x[i], lo, s, inv, direct) << (4 * i);
+        for (int i = 0; i < 8; ++i) {
+            const float q = (x[i] - lo) * inv;
+            n[i] = __builtin_rintf(q);
+            far = fmaxf(far, __builtin_fabsf(q - n[i]));
+        }
+        if (far > 0.5f - 0x1p-16f || s < (__is_same(T, __bf16) ? 0x1p-100f : 0x1p-14f)) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) n[i] = fminf(__builtin_rintf((x[i] - lo) / s), 15.f);
+        }
+        uint32_t even = 0, odd_levels = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            even = __builtin_amdgcn_cvt_pk_u8_f32(n[2 * i], (uint32_t)i, even);
+            odd_levels = __builtin_amdgcn_cvt_pk_u8_f32(n[2 * i + 1], (uint32_t)i, odd_levels);
+        }
+        word = even | odd_levels << 4;
     }
     if ((uint64_t)slot >= (uint64_t)(c.pages * c.page)) return;
-    const int64_t p = slot / c.page, off = slot - p * c.page;
-    const int64_t at = (p * c.heads + h) * c.page + off;
-    ((uint32_t *)(val ? c.v : c.k))[at * LPV + sub] = word;
+    const int32_t p = slot_page(c, slot);
+    const int64_t at = ((int64_t)p * c.heads + h) * c.page + ((int32_t)slot - p * c.page);
+    ((uint32_t *)levels)[at * LPV + sub] = word;
     if (sub == 0) {
         const float nan = __uint_as_float(0x7FC00000u);
-        (val ? c.vp : c.kp)[at] = bad ? pack2<T>(nan, nan) : pack2<T>(s, lo);
+        params[at] = bad ? pack2<T>(nan, nan) : pack2<T>(s, lo);
     }
+}
+
+template <class T, int D>
+__global__ __launch_bounds__(256) void kv4_write_kernel(const T *__restrict__ K, const T *__restrict__ V,
+                                                        int64_t ldk, int64_t ldv,
+                                                        const int64_t *__restrict__ slots, Kv4Cache c,
+                                                        int64_t tokens)
+{
+    constexpr int LPV = D / 8;
+    const uint32_t group = blockIdx.x / (uint32_t)c.heads;
+    const int32_t h = (int32_t)(blockIdx.x - group * (uint32_t)c.heads);
+    const int64_t t = (int64_t)group * (256 / LPV) + threadIdx.x / LPV;
+    const uint32_t sub = threadIdx.x % LPV;
+    if (t >= tokens) return;  // whole vectors
+    const int64_t slot = slots[t];
+    const i32x4 k = *(const i32x4 *)(K + t * ldk + h * D + sub * 8);
+    const i32x4 v = *(const i32x4 *)(V + t * ldv + h * D + sub * 8);
+    write_vector<T, D>(c, k, slot, h, sub, c.k, c.kp);
+    write_vector<T, D>(c, v, slot, h, sub, c.v, c.vp);
 }
 
 // ---- read back -------------------------------------------------------------
@@ -88,46 +124,52 @@ __global__ __launch_bounds__(256) void kv4_write_kernel(const T *__restrict__ K,
 // reads as zeros.
 template <class T, int D>
 __global__ __launch_bounds__(256) void kv4_read_kernel(Kv4Cache c, const int64_t *__restrict__ slots,
-                                                       T *__restrict__ K, T *__restrict__ V, int64_t vectors)
+                                                       T *__restrict__ K, T *__restrict__ V, int64_t tokens)
 {
     constexpr int LPV = D / 8;
-    const int64_t vec = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPV;
+    const uint32_t group = blockIdx.x / (uint32_t)c.heads;
+    const int32_t h = (int32_t)(blockIdx.x - group * (uint32_t)c.heads);
+    const int64_t t = (int64_t)group * (256 / LPV) + threadIdx.x / LPV;
     const uint32_t sub = threadIdx.x % LPV;
-    if (vec >= vectors) return;
-    const bool val = blockIdx.y != 0;
-    const int64_t t = vec / c.heads, h = vec - t * c.heads;
+    if (t >= tokens) return;
     const int64_t slot = slots[t];
-    i32x4 o = {0, 0, 0, 0};
+    i32x4 o[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
     if ((uint64_t)slot < (uint64_t)(c.pages * c.page)) {
-        const int64_t p = slot / c.page, off = slot - p * c.page;
-        const int64_t at = (p * c.heads + h) * c.page + off;
-        const uint32_t w = ((const uint32_t *)(val ? c.v : c.k))[at * LPV + sub];
-        const uint32_t prm = (val ? c.vp : c.kp)[at];
-        const float s = lo_f32<T>(prm), m = hi_f32<T>(prm);
+        const int32_t p = slot_page(c, slot);
+        const int64_t at = ((int64_t)p * c.heads + h) * c.page + ((int32_t)slot - p * c.page);
+        const uint32_t w[2] = {((const uint32_t *)c.k)[at * LPV + sub], ((const uint32_t *)c.v)[at * LPV + sub]};
+        const uint32_t prm[2] = {c.kp[at], c.vp[at]};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            o[i] = (int)pack2<T>((float)((w >> (8 * i)) & 15u) * s + m, (float)((w >> (8 * i + 4)) & 15u) * s + m);
+        for (int x = 0; x < 2; ++x) {
+            const float s = lo_f32<T>(prm[x]), m = hi_f32<T>(prm[x]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                o[x][i] = (int)pack2<T>((float)((w[x] >> (8 * i)) & 15u) * s + m,
+                                        (float)((w[x] >> (8 * i + 4)) & 15u) * s + m);
+        }
     }
-    *(i32x4 *)((val ? V : K) + vec * D + sub * 8) = o;
+    const int64_t to = (t * c.heads + h) * D + sub * 8;
+    *(i32x4 *)(K + to) = o[0];
+    *(i32x4 *)(V + to) = o[1];
 }
 
 template <class T, int D>
 static hipError_t write_t(const void *K, const void *V, int64_t ldk, int64_t ldv, const int64_t *slots,
                           const Kv4Cache &c, int64_t T_, hipStream_t s)
 {
-    const int64_t vectors = T_ * c.heads, blocks = (vectors * (D / 8) + 255) / 256;
+    const int64_t blocks = (T_ + 2048 / D - 1) / (2048 / D) * c.heads;
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((kv4_write_kernel<T, D>), dim3((uint32_t)blocks, 2), dim3(256), 0, s, (const T *)K,
-                       (const T *)V, ldk, ldv, slots, c, vectors);
+    hipLaunchKernelGGL((kv4_write_kernel<T, D>), dim3((uint32_t)blocks), dim3(256), 0, s,
+                       (const T *)K, (const T *)V, ldk, ldv, slots, c, T_);
     return hipGetLastError();
 }
 template <class T, int D>
 static hipError_t read_t(const Kv4Cache &c, const int64_t *slots, void *K, void *V, int64_t T_, hipStream_t s)
 {
-    const int64_t vectors = T_ * c.heads, blocks = (vectors * (D / 8) + 255) / 256;
+    const int64_t blocks = (T_ + 2048 / D - 1) / (2048 / D) * c.heads;
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((kv4_read_kernel<T, D>), dim3((uint32_t)blocks, 2), dim3(256), 0, s, c, slots, (T *)K,
-                       (T *)V, vectors);
+    hipLaunchKernelGGL((kv4_read_kernel<T, D>), dim3((uint32_t)blocks), dim3(256), 0, s, c,
+                       slots, (T *)K, (T *)V, T_);
     return hipGetLastError();
 }
 
@@ -251,12 +293,7 @@ __device__ inline Span span_of(const AttnArgs &a, int32_t b)        // b is the 
     s.rows = s.nq * a.group;
     return s;
 }
-// key / page by a multiplication: exact for keys below 2^31 (page_mul is
-// 2^(32 + page_shift) / page rounded up).
-__device__ inline int32_t page_of(const AttnArgs &a, int32_t key)
-{
-    return (int32_t)(__umulhi((uint32_t)key, a.page_mul) >> a.page_shift);
-}
+__device__ inline int32_t page_of(const AttnArgs &a, int32_t key) { return slot_page(a.c, key); }
 // A page number of the table, by a scalar load.
 __device__ inline int32_t page_number(const AttnArgs &a, int32_t b, int32_t key)
 {
