@@ -220,12 +220,18 @@ __global__ __launch_bounds__(512) void linear_few_kernel(
     const uint32_t row_at = (uint32_t)(lane >> 2) * (uint32_t)K;
     const int32_t piece = 16 * ((lane & 3) ^ ((lane >> 3) & 3));
     const uint32_t ring = lds_addr(smem) + (uint32_t)(wave * FT::RING);
-    const int32_t steps = (K + 63) / 64;
-    const int32_t first = wave * steps / NW, last = (wave + 1) * steps / NW;
+    // Shares of K: whole 128-byte lines.  With one 64-byte step to a stage, two waves
+    // take a share together, the left and the right halves of its lines, so that a
+    // line is asked for twice at about one time and comes once.
+    constexpr int PAIR = S == 1 ? 2 : 1;
+    const int32_t lines = (K + 127) / 128, share = wave / PAIR, shares = NW / PAIR;
+    const int32_t half = wave % PAIR;
+    const int32_t first = 2 / PAIR * (share * lines / shares), last = 2 / PAIR * ((share + 1) * lines / shares);
+    auto byte_of = [&](int32_t st) { return 64 * (PAIR * st + half); };
     auto copy = [&](int d, int32_t st) {
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            const int32_t k = 64 * (st + s) + piece;
+            const int32_t k = byte_of(st + s) + piece;
             const bool in = st + s < last && k < K;
             const uint32_t dst = ring + (uint32_t)(d * FT::STAGE + s * FT::BLOCKS * 1024);
 #pragma unroll
@@ -294,7 +300,7 @@ __global__ __launch_bounds__(512) void linear_few_kernel(
                 for (int t = 0; t < NT; ++t) wf[s][t] = *(const i32x4 *)(frag + d * FT::STAGE + (s * FT::BLOCKS + t) * 1024);
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
-                    if constexpr (FUSED) xf[s][t] = *(const i32x4 *)(xq + min(64 * (at + s), K - 16 - 16 * c));
+                    if constexpr (FUSED) xf[s][t] = *(const i32x4 *)(xq + min(byte_of(at + s), K - 16 - 16 * c));
                     else xf[s][t] = *(const i32x4 *)(frag + d * FT::STAGE + (s * FT::BLOCKS + NT + t) * 1024);
                 }
             }
@@ -350,21 +356,22 @@ static hipError_t few_t(const void *X, int64_t ldx, const int8_t *W, const float
 
 // Which tile a product takes; 0 rows: none of these, the LDS-tiled kernels of
 // lb_gemm_s8_linear.  A workgroup takes about as long whatever its tile (latency,
-// and some 47 KB a us of copies to a compute unit), so the narrowest tile whose
+// and some 50 KB a us of copies to a compute unit), so the narrowest tile whose
 // workgroups run at once, and the other kernels where none does.  Measured, bf16,
-// weights from HBM, us here and there: 1 x 4096 x 4096 6.5 / 18.6, 16 x 8000 x 2048
-// 6.1 / 10.9, 16 x 11008 x 4096 (48 columns) 12.9 / 14.0, 32 x 11008 x 4096 14.3 /
-// 14.7, 24 x 8192 x 4096 9.4 / 13.7, 100 x 4096 x 4096 9.8 / 19.7, 256 x 1376 x 4096
-// 9.4 / 19.3, 64 x 8192 x 8192 24.2 / 26.2; past the rule 16 x 16384 x 4096 (64
-// columns) 18.1 / 17.3, 64 x 11008 x 4096 (48) 17.5 / 15.9, 100 x 6000 x 4096 (48)
-// 13.9 / 14.1, 331 x 4097 x 5504 (64) 34.3 / 22.8.
+// weights from HBM, us here and there: 1 x 4096 x 4096 6.3 / 18.7, 16 x 8000 x 2048
+// 6.0 / 10.9, 16 x 11008 x 4096 13.0 / 13.9, 32 x 6000 x 4096 10.2 / 13.8, 32 x 11008
+// x 4096 13.7 / 14.7, 64 x 4096 x 4096 8.0 / 19.5, 100 x 4096 x 4096 8.6 / 19.5, 200 x
+// 2048 x 4096 8.2 / 19.3, 256 x 4096 x 4096 (64 columns) 12.5 / 19.6, 400 x 2048 x 4096
+// 12.2 / 13.7, 64 x 11008 x 4096 (48) 17.0 / 16.4 and 13.0 / 14.4 from the cache; past
+// the rule 16 x 16384 x 4096 (64) 18.1 / 17.3, 128 x 8192 x 4096 (64) 17.2 / 15.4,
+// 331 x 4097 x 5504 (64) 31.5 / 27.5, 200 x 11008 x 4096 (64) 39.1 / 30.9.
 struct FewShape {
     int tm, tn;
 };
 static FewShape few_shape(int64_t M, int64_t N, int cu)
 {
     const int tm = M <= 16 ? 16 : M <= 32 ? 32 : 64;
-    for (int tn = 16; tn <= (tm == 64 ? 32 : 48); tn += 16)
+    for (int tn = 16; tn <= (M > 128 ? 64 : 48); tn += 16)
         if (((M + tm - 1) / tm) * ((N + tn - 1) / tn) <= cu) return {tm, tn};
     return {0, 0};
 }
@@ -378,7 +385,8 @@ static hipError_t linear_few_t(const int8_t *Xq, const int8_t *W, const float *s
 #define LB_FEW(...) few_t<T, __VA_ARGS__, false>(Xq, K, W, sx, sw, bias, out, M, N, K, s)
     if (f.tm == 16) return f.tn == 16 ? LB_FEW(1, 1, 2, 2) : f.tn == 32 ? LB_FEW(1, 2, 1, 3) : LB_FEW(1, 3, 2, 2);
     if (f.tm == 32) return f.tn == 16 ? LB_FEW(2, 1, 2, 2) : f.tn == 32 ? LB_FEW(2, 2, 1, 3) : LB_FEW(2, 3, 1, 2);
-    if (f.tm == 64) return f.tn == 16 ? LB_FEW(4, 1, 1, 3) : LB_FEW(4, 2, 1, 2);
+    if (f.tm == 64 && f.tn <= 32) return f.tn == 16 ? LB_FEW(4, 1, 1, 3) : LB_FEW(4, 2, 1, 2);
+    if (f.tm == 64) return f.tn == 48 ? LB_FEW(4, 3, 1, 2) : LB_FEW(4, 4, 1, 2);
 #undef LB_FEW
     return hipErrorInvalidValue;
 }
