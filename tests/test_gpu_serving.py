@@ -118,6 +118,16 @@ def test_linear(dtype, M, N, K):
     assert (flat[M * N:] == 7).all(), "write past out"
 
 
+# one for each tile of the few-row kernel (rows x columns on 256 compute units), quantising for itself or not
+TILES = [(4, 5000, 48), (2, 9001, 112), (4, 12288, 16400), (5, 5001, 48), (16, 9000, 240), (20, 5000, 80), (17, 3001, 2032),
+         (30, 9001, 64), (33, 4000, 1040), (64, 5000, 80), (50, 9001, 48), (130, 6000, 80), (200, 4001, 144), (256, 4096, 272)]
+
+
+@pytest.mark.parametrize("M,N,K", TILES)
+def test_linear_tiles(M, N, K):
+    test_linear(BF if N % 2 else HF, M, N, K)
+
+
 @pytest.mark.parametrize("dtype", [BF, HF, FL])
 @pytest.mark.parametrize("M,N,K", [(4, 50, 256), (40, 96, 512), (300, 777, 1024), (2048, 1376, 512)])
 def test_scaled_product(dtype, M, N, K):
@@ -392,8 +402,9 @@ def test_attention_ragged_queries(dtype, D, page, window):
 
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("window", [0, 50])
-def test_attention_not_causal(dtype, window):
-    b = Batch([130, 5, 600], [3, 9, 40], 12, 3, 128, 16, dtype, seed=4)
+@pytest.mark.parametrize("Hq", [12, 24])
+def test_attention_not_causal(dtype, window, Hq):
+    b = Batch([130, 5, 600], [3, 9, 40], Hq, 3, 128, 16, dtype, seed=4)
     b.check(b.run(causal=False, window=window, scale=0.2), b.want(causal=False, window=window, scale=0.2))
 
 
@@ -411,6 +422,71 @@ def test_attention_split_keys(dtype, Hq, Hkv, D, nq):
         b.check(got, want)
         again = b.run(max_q=nq, max_len=6000, workspace=ws)
         assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1]), "not the same bits twice"
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("lens,nq,Hq,Hkv,D", [
+    ([1, 4000, 0, 700, 31, 3333, 32, 2000, 3999, 5] * 4, 1, 8, 8, 64),     # shares that cut and that hold many
+    ([3100] * 33, 1, 8, 8, 128),                                           # equal tiles, which stay whole
+    ([3500, 100, 40, 0, 2500, 3600, 3072, 1, 900, 77, 64, 3000], 5, 64, 8, 64),   # three tiles of rows to a head
+    ([6000, 50, 3000] * 11, 1, 16, 8, 256)])
+def test_attention_shares(dtype, lens, nq, Hq, Hkv, D):
+    """More tiles than compute units and lengths that differ: the work in equal shares, and with no workspace a
+    tile to a workgroup."""
+    b = Batch(lens, [nq] * len(lens), Hq, Hkv, D, 32, dtype, seed=len(lens))
+    want = b.want()
+    need = lb.lb_attn_kv4_workspace(len(lens), b.total, nq, Hq, Hkv, D, max(lens))
+    assert need > 0
+    for size in (need, 0):
+        ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+        got = b.run(max_q=nq, max_len=max(lens), workspace=ws)
+        b.check(got, want)
+        again = b.run(max_q=nq, max_len=max(lens), workspace=ws)
+        assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1]), "not the same bits twice"
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_chunks_of_several_sequences(dtype, D):
+    """Many rows of a key head, tiles in the order of their keys; one sequence's keys in ranges."""
+    b = Batch([300, 700, 90, 1100], [200, 60, 90, 1], 8, 2, D, 48, dtype, seed=D)
+    b.check(b.run(max_q=200), b.want())
+    b = Batch([2600], [100], 6, 2, D, 64, dtype, seed=D)
+    want = b.want()
+    need = lb.lb_attn_kv4_workspace(1, 100, 100, 6, 2, D, 2600)
+    assert need > 0
+    for size in (need, need // 2, 0):
+        b.check(b.run(max_q=100, max_len=2600, workspace=torch.empty(size, dtype=torch.uint8, device="cuda")), want)
+
+
+def test_attention_hints_are_only_hints():
+    """max_len far below and above the lengths, and a table wider than they need."""
+    b = Batch([900, 37, 2000], [1, 1, 1], 8, 2, 64, 16, HF, seed=12)
+    want = b.want()
+    for max_len in (0, 1, 100, 10 ** 6):
+        b.check(b.run(max_q=1, max_len=max_len), want)
+    b = Batch([900, 37, 500], [90, 30, 5], 8, 2, 64, 16, BF, seed=13)
+    want = b.want()
+    for max_len in (0, 64, 10 ** 6):
+        b.check(b.run(max_len=max_len), want)
+
+
+@pytest.mark.parametrize("nq", [1, 60])
+def test_attention_value_that_is_not_finite(nq):
+    """A value vector that is NaN makes NaN of the rows that see it and leaves the others, and every lse."""
+    b = Batch([100, 50], [nq, nq] if nq == 1 else [nq, 40], 8, 2, 128, 16, BF, seed=14)
+    want = b.want()
+    slot = int(b.slots[80])
+    b.cache[3][slot // 16, 1, slot % 16] = float("nan")   # sequence 0, key 80, key head 1
+    out, lse = b.run()
+    bad = torch.zeros(b.total, 8, dtype=torch.bool)
+    for i in range(b.nqs[0]):
+        bad[i, 4:] = 100 - b.nqs[0] + i >= 80
+    assert torch.equal(torch.isnan(out.cpu()).all(-1), bad) and torch.equal(torch.isnan(out.cpu()).any(-1), bad)
+    keep = ~bad
+    fixed = torch.where(bad[..., None], want[0].float(), out.cpu().float()).to(BF)
+    b.check((fixed, lse), want, vmax=10.0)
+    assert keep.any()
 
 
 @pytest.mark.parametrize("spread", [1e-3, 100.0])
@@ -433,27 +509,27 @@ def test_attention_constant_and_far_keys(nq):
     b.check(b.run(), b.want())
 
 
-@pytest.mark.parametrize("nq", [1, 24])
-def test_attention_nan_stays_in_its_row(nq):
+@pytest.mark.parametrize("nq,Hq", [(1, 4), (24, 4), (49, 16)])
+def test_attention_nan_stays_in_its_row(nq, Hq):
     """A key that is NaN makes NaN of the queries that see it, of its key head, and of no others; so does a query."""
-    b = Batch([100, 50], [nq, nq], 4, 2, 128, 16, HF, seed=3)
+    b = Batch([100, 50], [nq, nq], Hq, 2, 128, 16, HF, seed=3)
     kp = b.cache[2].permute(0, 2, 1, 3).reshape(-1, 2, 2)
     slot = int(b.slots[90])
     b.cache[2][slot // 16, 1, slot % 16] = float("nan")   # sequence 0, key 90, head 1
     b.q[b.total - 1, 0, 5] = float("nan")
     out, lse = b.run()
-    bad = torch.zeros(b.total, 4, dtype=torch.bool)
+    bad = torch.zeros(b.total, Hq, dtype=torch.bool)
     for i in range(nq):
-        bad[i, 2:] = 100 - nq + i >= 90
+        bad[i, Hq // 2:] = 100 - nq + i >= 90
     bad[b.total - 1, 0] = True
     assert kp is not None
     assert torch.equal(torch.isnan(out.cpu()).any(-1), bad) and torch.equal(torch.isnan(lse.cpu()), bad)
 
 
-@pytest.mark.parametrize("nq", [1, 24])
-def test_attention_pages_outside_the_cache(nq):
+@pytest.mark.parametrize("nq,Hq", [(1, 4), (24, 4), (30, 16)])
+def test_attention_pages_outside_the_cache(nq, Hq):
     """Keys of a page number outside the cache are not seen; lens beyond the table's width counts as its width."""
-    b = Batch([64, 80], [nq, nq], 4, 2, 64, 16, BF, seed=6)
+    b = Batch([64, 80], [nq, nq], Hq, 2, 64, 16, BF, seed=6)
     b.table[0, 1], b.table[1, 2] = -7, b.pages
     got = b.run()
     kv = []
@@ -461,18 +537,18 @@ def test_attention_pages_outside_the_cache(nq):
         keep = [t for t in range(len(k)) if t not in hole]
         kv.append((k, v, keep))
     # the same softmax with the holes' scores at minus infinity: keys so that only their absence matters
-    out = torch.zeros(b.total, 4, 64, dtype=torch.float64)
-    lse = torch.zeros(b.total, 4, dtype=torch.float64)
+    out = torch.zeros(b.total, Hq, 64, dtype=torch.float64)
+    lse = torch.zeros(b.total, Hq, dtype=torch.float64)
     for s, (k, v, keep) in enumerate(kv):
         for i in range(nq):
             pos = len(k) - nq + i
             t = [j for j in keep if j <= pos]
-            for h in range(4):
-                z = (k[t, h // 2] @ b.q[s * nq + i, h].double()) / 8
-                out[s * nq + i, h] = torch.softmax(z, 0) @ v[t, h // 2]
+            for h in range(Hq):
+                z = (k[t, h // (Hq // 2)] @ b.q[s * nq + i, h].double()) / 8
+                out[s * nq + i, h] = torch.softmax(z, 0) @ v[t, h // (Hq // 2)]
                 lse[s * nq + i, h] = torch.logsumexp(z, 0)
     b.check(got, (out, lse, b.want()[2]))
-    full = Batch([48, 48], [nq, nq], 4, 2, 64, 16, BF, seed=7)
+    full = Batch([48, 48], [nq, nq], Hq, 2, 64, 16, BF, seed=7)
     full.table = full.table[:, :3]
     want = full.want()
     full.lens = [100000, 2 ** 31 - 1]
