@@ -490,7 +490,7 @@ def lb_attn_kv4(Q, Kc, Vc, Kp, Vp, table, q_off, lens, out, lse=None, max_q=None
     (total_q, Hq) fp32 receives the log of each row's sum, if given.  max_q: at least the most queries of a
     sequence (default: total_q); max_len: about the longest sequence, for the planning (default: the
     table's width).  scale defaults to D ** -0.5; window > 0 keeps the last window keys.  A query that sees
-    nothing gets zeros.  workspace: as for lb_linear_w8a8; a smaller one makes fewer key ranges."""
+    nothing gets zeros.  workspace: as for lb_linear_w8a8; a smaller one splits the keys less."""
     T = _torch()
     lib = load()
     shape = total, Hq, D = Q.shape

@@ -251,7 +251,8 @@ int lb_quant_rows_s8(const void *X, int64_t ldx, int8_t *Q, float *sx, int64_t M
  * acc exact in int32, the rest in fp32, rounded once to ftype.  bias: N values
  * of ftype, or NULL.  X: M x K int8, W: N x K int8 (nn.Linear's [N, K]); sizes
  * and K as for lb_gemm_s8.  Tiles are chosen as lb_gemm_s8_linear's automatic
- * choice does, except that products of few tiles have a kernel of their own.
+ * choice does, except that products whose narrow tiles (16 to 64 rows by 16 to
+ * 64 columns) all run at once have a kernel of their own.
  */
 int lb_gemm_s8_scaled(const int8_t *X, const int8_t *W, const float *sx, const float *sw, const void *bias,
                       void *out, int64_t M, int64_t N, int64_t K, int ftype, void *stream);
@@ -316,10 +317,10 @@ int lb_kv4_read(const uint8_t *Kc, const uint8_t *Vc, const void *Kp, const void
  * as they are.
  *   max_q, max_len: at least the longest nq (LB_ERR_SHAPE if below 1; rows past
  *   it may be left as they are) and, for the planning alone, about the longest
- *   lens.  workspace: partial results of key ranges, which few rows are split
- *   into; with fewer than lb_attn_kv4_workspace() bytes (0 and NULL too) fewer
- *   ranges are made.  The ranges are joined in a fixed order: the same arguments
- *   give the same bits.
+ *   lens.  workspace: partial results where the keys of few rows are split over
+ *   workgroups; with fewer than lb_attn_kv4_workspace() bytes (0 and NULL too)
+ *   fewer parts are made, or none.  Parts are joined in a fixed order: the same
+ *   arguments give the same bits.
  */
 int lb_attn_kv4(const void *Q, int64_t ldq, const uint8_t *Kc, const uint8_t *Vc, const void *Kp,
                 const void *Vp, const int32_t *table, int64_t ldt, int64_t table_width, const int32_t *q_off,
