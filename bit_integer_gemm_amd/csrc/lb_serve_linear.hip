@@ -167,41 +167,48 @@ hipError_t launch_quant_rows(int ftype, const void *X, int64_t ldx, int8_t *Q, f
 
 // ---- few rows --------------------------------------------------------------
 // A tile of 16 MT rows of X by 16 NT rows of W (output columns) per workgroup, and
-// all of K: the eight waves each take an eighth of K for the whole tile, through
+// all of K: eight (four) waves each take their share of K for the whole tile, through
 // rings of LDS of their own, and their exact sums meet in LDS by integer adds
 // (whose order does not matter).  Every operand byte is read once per workgroup,
 // but no wave waits for another before the end, and DEPTH - 1 stages of copies are
 // under way in each: what bounds these products is the latency and number of bytes
 // on their way, not the matrix cores.
-//   A copy fills a block of 16 rows x 64 K-bytes, four lanes to a row (64 bytes in
-//   one piece; straight to registers in fragment order, 16 rows to a load, delivers
-//   half as much: 18.1 us at 16 x 11008 x 4096).  Piece p of row n lies at
-//   p ^ (n / 2) % 4, which keeps the fragment reads off each other's banks.
+//   A stage of a wave is S x 64 bytes of each row.  A copy fills 16 / S rows, 4 S
+//   lanes to a row, whose bytes come in one piece (straight to registers in fragment
+//   order, 16 rows to a load, delivers half as much: 18.1 us at 16 x 11008 x 4096).
+//   Piece p of row n lies at p ^ n % 8 (S = 1: p ^ (n / 2) % 4), which keeps the
+//   fragment reads off each other's banks.
 //   W is the MFMA's A operand (lane l: row l % 16, piece l / 16), X its B operand;
 //   lane l ends with columns 4 (l / 16) .. + 3 of row l % 16.
 // FUSED (MT = 1, few rows): X is the layer's floating activations; while the first
 // weights are on their way every workgroup quantises the rows for itself into LDS,
 // which saves the launch that would do it once.
 template <int MT, int NT, int S, int DEPTH, bool FUSED> struct FewTile {
-    static constexpr int NW = 8;                              // waves
+    // waves; of the largest tiles four, which leaves room for whole lines (eight with
+    // half a line each: 14.8 against 13.9 us at 256 x 4096 x 4096), and the sums lie
+    // over their rings
+    static constexpr bool OVER = MT > 3 && S == 2;
+    static constexpr int NW = OVER ? 4 : 8;
     static constexpr int BLOCKS = (FUSED ? 0 : MT) + NT;      // 1 KiB blocks of a 64-byte step
     static constexpr int STAGE = S * BLOCKS * 1024, RING = DEPTH * STAGE;
-    static constexpr int TM = 16 * MT, TN = 16 * NT, LD = TN + 4;
-    static constexpr int SUMS_AT = NW * RING, SCALE_AT = SUMS_AT + TM * LD * 4, RED_AT = SCALE_AT + TM * 4;
+    static constexpr int TM = 16 * MT, TN = 16 * NT, LD = TM + 4;   // a column of sums: TM and 4, so that 16 rows x 4 columns hit all banks once
+    static constexpr int SUMS_AT = OVER ? 0 : NW * RING;
+    static constexpr int SCALE_AT = OVER ? NW * RING : SUMS_AT + TN * LD * 4, RED_AT = SCALE_AT + TM * 4;
     static constexpr int X_AT = RED_AT + (FUSED ? NW * 16 : 0);   // FUSED: M x K int8
     static_assert((DEPTH - 1) * S * BLOCKS < 64, "vmcnt is 6 bits");
+    static_assert(!OVER || TN * LD * 4 <= NW * RING, "sums over the rings");
 };
 
 template <int N> __device__ inline void wait_copies() { asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory"); }
 
 template <class T, int MT, int NT, int S, int DEPTH, bool FUSED>
-__global__ __launch_bounds__(512) void linear_few_kernel(
+__global__ __launch_bounds__((64 * FewTile<MT, NT, S, DEPTH, FUSED>::NW)) void linear_few_kernel(
     const void *__restrict__ X, int64_t ldx, const int8_t *__restrict__ W, const float *__restrict__ sx,
     const float *__restrict__ sw, const T *__restrict__ bias, T *__restrict__ out, int32_t M, int32_t N,
     int32_t K, uint32_t tiles_m, uint32_t tiles_n)
 {
     using FT = FewTile<MT, NT, S, DEPTH, FUSED>;
-    constexpr int NW = FT::NW, TM = FT::TM, TN = FT::TN, LD = FT::LD;
+    constexpr int NW = FT::NW, THREADS = 64 * NW, TM = FT::TM, TN = FT::TN, LD = FT::LD;
     extern __shared__ __attribute__((aligned(1024))) char smem[];
     int32_t *const sums = (int32_t *)(smem + FT::SUMS_AT);
     float *const row_scales = (float *)(smem + FT::SCALE_AT);
@@ -212,13 +219,13 @@ __global__ __launch_bounds__(512) void linear_few_kernel(
     tile_of_block(blockIdx.x, tiles_m, tiles_n, 4u, tm, tn);
     const int32_t m0 = (int32_t)tm * TM, n0 = (int32_t)tn * TN;
 
-    // Copies: lane i takes piece (i % 4) ^ (i / 8) % 4 of row i / 4.  Rows past the
-    // operand, pieces past K and steps past this wave's share lie beyond the
-    // buffer's range and read as zeros.
+    // Copies: lane i takes piece (i % 8) ^ (i / 8) of row i / 8 (S = 1: piece
+    // (i % 4) ^ (i / 8) % 4 of row i / 4).  Rows past the operand, pieces past K and
+    // steps past this wave's share lie beyond the buffer's range and read as zeros.
     const i32x4 rw = make_rsrc(W + (int64_t)n0 * K, (uint64_t)min(TN, N - n0) * (uint32_t)K);
     const i32x4 rx = FUSED ? rw : make_rsrc((const int8_t *)X + (int64_t)m0 * K, (uint64_t)min(TM, M - m0) * (uint32_t)K);
-    const uint32_t row_at = (uint32_t)(lane >> 2) * (uint32_t)K;
-    const int32_t piece = 16 * ((lane & 3) ^ ((lane >> 3) & 3));
+    const uint32_t row_at = (uint32_t)(S == 1 ? lane >> 2 : lane >> 3) * (uint32_t)K;
+    const int32_t piece = 16 * (S == 1 ? (lane & 3) ^ ((lane >> 3) & 3) : (lane & 7) ^ (lane >> 3));
     const uint32_t ring = lds_addr(smem) + (uint32_t)(wave * FT::RING);
     // Shares of K: whole 128-byte lines.  With one 64-byte step to a stage, two waves
     // take a share together, the left and the right halves of its lines, so that a
@@ -229,24 +236,24 @@ __global__ __launch_bounds__(512) void linear_few_kernel(
     const int32_t first = 2 / PAIR * (share * lines / shares), last = 2 / PAIR * ((share + 1) * lines / shares);
     auto byte_of = [&](int32_t st) { return 64 * (PAIR * st + half); };
     auto copy = [&](int d, int32_t st) {
+        const int32_t k = byte_of(st) + piece;
+        const bool in = st < last && k < K;
+        const uint32_t dst = ring + (uint32_t)(d * FT::STAGE);
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const int32_t k = byte_of(st + s) + piece;
-            const bool in = st + s < last && k < K;
-            const uint32_t dst = ring + (uint32_t)(d * FT::STAGE + s * FT::BLOCKS * 1024);
+        for (int t = 0; t < S * NT; ++t)
+            dma16(rw, in ? row_at + (uint32_t)(16 / S * t) * (uint32_t)K + (uint32_t)k : 0xFFFFFFF0u, dst + t * 1024);
+        if constexpr (!FUSED)
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-                dma16(rw, in ? row_at + (uint32_t)(16 * t) * (uint32_t)K + (uint32_t)k : 0xFFFFFFF0u, dst + t * 1024);
-            if constexpr (!FUSED)
-#pragma unroll
-                for (int t = 0; t < MT; ++t)
-                    dma16(rx, in ? row_at + (uint32_t)(16 * t) * (uint32_t)K + (uint32_t)k : 0xFFFFFFF0u,
-                          dst + (NT + t) * 1024);
-        }
+            for (int t = 0; t < S * MT; ++t)
+                dma16(rx, in ? row_at + (uint32_t)(16 / S * t) * (uint32_t)K + (uint32_t)k : 0xFFFFFFF0u,
+                      dst + (S * NT + t) * 1024);
     };
 #pragma unroll
     for (int d = 0; d < DEPTH - 1; ++d) copy(d, first + S * d);
-    for (int32_t i = (int32_t)threadIdx.x; i < TM * LD; i += 512) sums[i] = 0;
+    auto clear_sums = [&] {
+        for (int32_t i = (int32_t)threadIdx.x; i < TN * LD; i += THREADS) sums[i] = 0;
+    };
+    if constexpr (!FT::OVER) clear_sums();
 
     const int8_t *xq = nullptr;
     if constexpr (FUSED) {
@@ -256,7 +263,7 @@ __global__ __launch_bounds__(512) void linear_few_kernel(
         for (int32_t m = 0; m < M; ++m) {
             const T *x = (const T *)X + m * ldx;
             uint32_t mx = 0;
-            for (int32_t q = (int32_t)threadIdx.x; q < chunks; q += 512)
+            for (int32_t q = (int32_t)threadIdx.x; q < chunks; q += THREADS)
                 mx = max(mx, chunk_amax<T>(*(const i32x4 *)(x + (int64_t)q * EPT)));
 #pragma unroll
             for (int d = 32; d; d >>= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, d));
@@ -270,7 +277,7 @@ __global__ __launch_bounds__(512) void linear_few_kernel(
             for (int w = 0; w < NW; ++w) mx = max(mx, red[w][m]);
             const RowScale rs = row_scale(widen_bits<T>(mx));
             if (threadIdx.x == 0) row_scales[m] = rs.scale;
-            for (int32_t q = (int32_t)threadIdx.x; q < chunks; q += 512)
+            for (int32_t q = (int32_t)threadIdx.x; q < chunks; q += THREADS)
                 put_chunk<T>((int8_t *)(smem + FT::X_AT) + (int64_t)m * K + q * EPT, *(const i32x4 *)(x + (int64_t)q * EPT), rs);
         }
         xq = (const int8_t *)(smem + FT::X_AT) + (int64_t)min(r, M - 1) * K + 16 * c;
@@ -284,7 +291,10 @@ __global__ __launch_bounds__(512) void linear_few_kernel(
     for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int u = 0; u < NT; ++u) acc[t][u] = i32x4{0, 0, 0, 0};
-    const char *const frag = smem + wave * FT::RING + (4 * r + (c ^ ((r >> 1) & 3))) * 16;
+    const char *frag[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+        frag[s] = smem + wave * FT::RING + (S == 1 ? 4 * r + (c ^ ((r >> 1) & 3)) : 8 * r + ((4 * s + c) ^ (r & 7))) * 16;
     for (int32_t st = first; st < last; st += S * DEPTH) {
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d) {
@@ -297,11 +307,11 @@ __global__ __launch_bounds__(512) void linear_few_kernel(
 #pragma unroll
             for (int s = 0; s < S; ++s) {
 #pragma unroll
-                for (int t = 0; t < NT; ++t) wf[s][t] = *(const i32x4 *)(frag + d * FT::STAGE + (s * FT::BLOCKS + t) * 1024);
+                for (int t = 0; t < NT; ++t) wf[s][t] = *(const i32x4 *)(frag[s] + d * FT::STAGE + S * t * 1024);
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
                     if constexpr (FUSED) xf[s][t] = *(const i32x4 *)(xq + min(byte_of(at + s), K - 16 - 16 * c));
-                    else xf[s][t] = *(const i32x4 *)(frag + d * FT::STAGE + (s * FT::BLOCKS + NT + t) * 1024);
+                    else xf[s][t] = *(const i32x4 *)(frag[s] + d * FT::STAGE + S * (NT + t) * 1024);
                 }
             }
             // the next copies overwrite what has been read here
@@ -316,22 +326,27 @@ __global__ __launch_bounds__(512) void linear_few_kernel(
         }
     }
     wait_copies<0>();
+    if constexpr (FT::OVER) {
+        __syncthreads();
+        clear_sums();
+        __syncthreads();
+    }
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int u = 0; u < NT; ++u)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) atomicAdd(&sums[(16 * t + r) * LD + 16 * u + 4 * c + e], acc[t][u][e]);
+            for (int e = 0; e < 4; ++e) atomicAdd(&sums[(16 * u + 4 * c + e) * LD + 16 * t + r], acc[t][u][e]);
     __syncthreads();
     const bool vec = N % 4 == 0;
-    for (int32_t i = (int32_t)threadIdx.x; i < TM * TN / 4; i += 512) {
+    for (int32_t i = (int32_t)threadIdx.x; i < TM * TN / 4; i += THREADS) {
         const int32_t m = i / (TN / 4), n = i % (TN / 4) * 4;
         if (m0 + m >= M || n0 + n >= N) continue;
-        const i32x4 v = *(const i32x4 *)(sums + m * LD + n);
+        const int32_t *v = sums + n * LD + m;
         const float scale = row_scales[m];
         f32x4 y;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = vec || n0 + n + e < N ? ((float)v[e] * scale) * sw[n0 + n + e] : 0.f;
+        for (int e = 0; e < 4; ++e) y[e] = vec || n0 + n + e < N ? ((float)v[e * LD] * scale) * sw[n0 + n + e] : 0.f;
         store_scaled<T>(bias, out, (m0 + m) * (int64_t)N + n0 + n, n0 + n, N - n0 - n, vec, y);
     }
 }
@@ -348,7 +363,7 @@ static hipError_t few_t(const void *X, int64_t ldx, const int8_t *W, const float
     const uint64_t tm = (uint64_t)((M + FT::TM - 1) / FT::TM), tn = (uint64_t)((N + FT::TN - 1) / FT::TN);
     if (tm * tn > 0x7FFFFFFFull) return hipErrorInvalidValue;
     static_assert(FT::X_AT + (FUSED ? FUSED_BYTES : 0) <= 160 * 1024, "LDS");
-    hipLaunchKernelGGL((linear_few_kernel<T, MT, NT, S, DEPTH, FUSED>), dim3((uint32_t)(tm * tn)), dim3(512),
+    hipLaunchKernelGGL((linear_few_kernel<T, MT, NT, S, DEPTH, FUSED>), dim3((uint32_t)(tm * tn)), dim3(64 * FT::NW),
                        (uint32_t)(FT::X_AT + (FUSED ? M * K : 0)), s, X, ldx, W, sx, sw, (const T *)bias, (T *)out,
                        (int32_t)M, (int32_t)N, (int32_t)K, (uint32_t)tm, (uint32_t)tn);
     return hipGetLastError();
@@ -386,7 +401,7 @@ static hipError_t linear_few_t(const int8_t *Xq, const int8_t *W, const float *s
     if (f.tm == 16) return f.tn == 16 ? LB_FEW(1, 1, 2, 2) : f.tn == 32 ? LB_FEW(1, 2, 1, 3) : LB_FEW(1, 3, 2, 2);
     if (f.tm == 32) return f.tn == 16 ? LB_FEW(2, 1, 2, 2) : f.tn == 32 ? LB_FEW(2, 2, 1, 3) : LB_FEW(2, 3, 1, 2);
     if (f.tm == 64 && f.tn <= 32) return f.tn == 16 ? LB_FEW(4, 1, 1, 3) : LB_FEW(4, 2, 1, 2);
-    if (f.tm == 64) return f.tn == 48 ? LB_FEW(4, 3, 1, 2) : LB_FEW(4, 4, 1, 2);
+    if (f.tm == 64) return f.tn == 48 ? LB_FEW(4, 3, 2, 2) : LB_FEW(4, 4, 2, 2);
 #undef LB_FEW
     return hipErrorInvalidValue;
 }
