@@ -285,10 +285,35 @@ int run_gemm(int kind, int dtype, int variant, const void *A, const void *B, voi
 
 bool lb::variant_is_forced() { return auto_override() >= 0; }
 
-// The scaled product's launches are the linear layer's.
+// Tiles with deep rings, one workgroup to a compute unit, for scaled products whose
+// tiles then all run at once though those of 64 x 64 would not; -1 where there are
+// none.  What bounds such a product is its operands' way into the busiest compute
+// unit: 128 x 64 tiles bring 192 rows there where two of 64 x 64 bring 256, and with
+// four stages instead of two most of it is under way.  Measured, us with these tiles
+// and with the linear layer's choice: 128 x 64 331 x 4097 x 5504 25.2 / 30.8, 100 x
+// 16384 x 4096 20.5 / 26.8, 400 x 4096 x 4096 17.2 / 21.9, 700 x 2048 x 4096 17.1 / 27.8,
+// 331 x 4097 x 1024 9.2 / 12.3; 64 x 128 300 x 6144 x 8192 34.9 / 41.5; 128 x 128 200 x
+// 11008 x 4096 23.8 / 31.3, 512 x 8192 x 4096 25.9 / 36.7, 2000 x 2048 x 4096 24.9 / 34.8,
+// 140 x 12000 x 512 7.1 / 8.1.  Where tiles of 64 x 64 do run at once: 128 x 8192 x 4096
+// 128 x 64 19.7, those 15.4.
+static int scaled_deep_tile(int64_t M, int64_t N)
+{
+    int cu = 0;
+    if (lb::variant_is_forced() || lb::device_cu_count(&cu) != LB_OK) return -1;
+    auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+    if (tiles(64, 64) <= cu) return -1;
+    if (tiles(128, 64) <= cu) return lb::SCALED_128x64;
+    if (tiles(64, 128) <= cu) return lb::SCALED_64x128;
+    return tiles(128, 128) <= cu ? lb::SCALED_128x128 : -1;
+}
+
+// The scaled product's launches are the linear layer's, but for those tiles.
 int lb::scaled_auto(const int8_t *X, const int8_t *W, const float *sx, const float *sw, void *out, int64_t M,
                     int64_t N, int64_t K, const lb::ScaledOut &so, hipStream_t stream)
 {
+    const int deep = scaled_deep_tile(M, N);
+    if (deep >= 0)
+        return lb::launch_scaled(deep, X, W, out, sx, sw, M, N, K, N, so, stream) == hipSuccess ? LB_OK : LB_ERR_HIP;
     const Plan p = make_plan(lb::KIND_LINEAR, LB_S8, LB_AUTO, M, N, K, K, 0);
     const int64_t elem = so.ftype == LB_F32 ? 4 : 2;
     for (int i = 0; i < p.np; ++i) {

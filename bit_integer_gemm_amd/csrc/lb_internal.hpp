@@ -22,6 +22,9 @@ enum { W4_256x192 = 16, W4_192x256 = 17 };
 // Internal tile code of the convolutions: a 64x64 tile with two 64-byte
 // stages (16 KiB of LDS, up to eight workgroups per CU).
 enum { CONV_64x64_K64 = 18 };
+// Internal tile codes of the scaled product: tiles with four 128-byte stages, one
+// workgroup per CU, where all of them run at once.
+enum { SCALED_128x64 = 19, SCALED_64x128 = 20, SCALED_128x128 = 21 };
 
 // int8 MFMA family (int8 GEMM, packed-int4 GEMM, int8 linear layer, and the
 // 1-bit GEMM on weighted bit planes).  Kb is the row length of A and B in

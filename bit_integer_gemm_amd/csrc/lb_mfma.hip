@@ -1512,7 +1512,11 @@ hipError_t launch_conv(int kind, int variant, const void *X, const void *F, int3
     }
 }
 
-// The scaled product: each variant's tile as the linear layer has it.
+// The scaled product: each variant's tile as the linear layer has it, and the tiles
+// with deep rings that scaled_auto takes where all of them run at once.
+using D128x64 = MfmaCfg<128, 64, 128, 4, 2, 4>;    // 96 KiB
+using D64x128 = MfmaCfg<64, 128, 128, 2, 4, 4>;    // 96 KiB
+using D128x128 = MfmaCfg<128, 128, 128, 4, 2, 4>;  // 128 KiB
 template <class C, class T>
 static hipError_t launch_scaled_one(const int8_t *A, const int8_t *B, void *out, const float *sx, const float *sw,
                                     int64_t M, int64_t N, int64_t K, int64_t ldo, const void *bias, hipStream_t s)
@@ -1551,6 +1555,9 @@ static hipError_t launch_scaled_t(int variant, const int8_t *A, const int8_t *B,
     case 8: return launch_scaled_one<L4W16, T>(A, B, out, sx, sw, M, N, K, ldo, bias, s);
     case W4_256x192: return launch_scaled_w4<8, 6, T>(A, B, out, sx, sw, M, N, K, ldo, bias, s);
     case W4_192x256: return launch_scaled_w4<6, 8, T>(A, B, out, sx, sw, M, N, K, ldo, bias, s);
+    case SCALED_128x64: return launch_scaled_one<D128x64, T>(A, B, out, sx, sw, M, N, K, ldo, bias, s);
+    case SCALED_64x128: return launch_scaled_one<D64x128, T>(A, B, out, sx, sw, M, N, K, ldo, bias, s);
+    case SCALED_128x128: return launch_scaled_one<D128x128, T>(A, B, out, sx, sw, M, N, K, ldo, bias, s);
     default: return hipErrorInvalidValue;
     }
 }

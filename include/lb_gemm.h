@@ -251,8 +251,9 @@ int lb_quant_rows_s8(const void *X, int64_t ldx, int8_t *Q, float *sx, int64_t M
  * acc exact in int32, the rest in fp32, rounded once to ftype.  bias: N values
  * of ftype, or NULL.  X: M x K int8, W: N x K int8 (nn.Linear's [N, K]); sizes
  * and K as for lb_gemm_s8.  Tiles are chosen as lb_gemm_s8_linear's automatic
- * choice does, except that products whose narrow tiles (16 to 64 rows by 16 to
- * 64 columns) all run at once have a kernel of their own.
+ * choice does, except that products whose tiles all run at once have a kernel
+ * (narrow tiles, 16 to 64 rows by 16 to 64 columns) or tiles (up to 128 x 128)
+ * of their own.
  */
 int lb_gemm_s8_scaled(const int8_t *X, const int8_t *W, const float *sx, const float *sw, const void *bias,
                       void *out, int64_t M, int64_t N, int64_t K, int ftype, void *stream);

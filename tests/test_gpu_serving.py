@@ -128,6 +128,15 @@ def test_linear_tiles(M, N, K):
     test_linear(BF if N % 2 else HF, M, N, K)
 
 
+# tiles with deep rings: 128 x 64, 64 x 128, 128 x 128; K of one stage and less, of
+# fewer stages than the ring has, of more; rows and columns that fill no tile
+@pytest.mark.parametrize("dtype", [BF, HF, FL])
+@pytest.mark.parametrize("M,N", [(331, 4097), (300, 6144), (1030, 2070)])
+@pytest.mark.parametrize("K", [16, 272, 784])
+def test_linear_deep_tiles(M, N, K, dtype):
+    test_linear(dtype, M, N, K)
+
+
 @pytest.mark.parametrize("dtype", [BF, HF, FL])
 @pytest.mark.parametrize("M,N,K", [(4, 50, 256), (40, 96, 512), (300, 777, 1024), (2048, 1376, 512)])
 def test_scaled_product(dtype, M, N, K):
