@@ -98,7 +98,9 @@ template <class T> __device__ inline void put_chunk(int8_t *q, i32x4 v, const Ro
 }
 
 // One workgroup per row; EPT elements per 16-byte chunk.  The row is read once
-// if it fits the workgroup's registers (NC chunks per thread), else twice.
+// if it fits the workgroup's registers (NC chunks per thread), else twice.  Bound by
+// memory: 8192 rows of 4096 bf16 in 25.0 us, 4.0 TB/s where a copy reaches 5.0; few
+// rows by latency, 16 of them 3.6 us.
 template <class T, int NC>
 __global__ __launch_bounds__(256) void quant_rows_kernel(const T *__restrict__ X, int64_t ldx,
                                                          int8_t *__restrict__ Q, float *__restrict__ sx,
@@ -178,6 +180,9 @@ hipError_t launch_quant_rows(int ftype, const void *X, int64_t ldx, int8_t *Q, f
 //   order, 16 rows to a load, delivers half as much: 18.1 us at 16 x 11008 x 4096).
 //   Piece p of row n lies at p ^ n % 8 (S = 1: p ^ (n / 2) % 4), which keeps the
 //   fragment reads off each other's banks.
+//   Kernel times, weights from HBM: 1 x 4096 x 4096 6.8 us (2.5 TB/s; the launch, the
+//   row's quantisation and one latency of HBM are most of it), 16 x 11008 x 4096 9.4 us
+//   (4.8 TB/s of weights, about what a copy reaches).
 //   W is the MFMA's A operand (lane l: row l % 16, piece l / 16), X its B operand;
 //   lane l ends with columns 4 (l / 16) .. + 3 of row l % 16.
 // FUSED (MT = 1, few rows): X is the layer's floating activations; while the first
@@ -374,12 +379,11 @@ static hipError_t few_t(const void *X, int64_t ldx, const int8_t *W, const float
 // and some 50 KB a us of copies to a compute unit), so the narrowest tile whose
 // workgroups run at once, and the other kernels where none does.  Measured, bf16,
 // weights from HBM, us here and there: 1 x 4096 x 4096 6.3 / 18.7, 16 x 8000 x 2048
-// 6.0 / 10.9, 16 x 11008 x 4096 13.0 / 13.9, 32 x 6000 x 4096 10.2 / 13.8, 32 x 11008
-// x 4096 13.7 / 14.7, 64 x 4096 x 4096 8.0 / 19.5, 100 x 4096 x 4096 8.6 / 19.5, 200 x
-// 2048 x 4096 8.2 / 19.3, 256 x 4096 x 4096 (64 columns) 12.5 / 19.6, 400 x 2048 x 4096
-// 12.2 / 13.7, 64 x 11008 x 4096 (48) 17.0 / 16.4 and 13.0 / 14.4 from the cache; past
-// the rule 16 x 16384 x 4096 (64) 18.1 / 17.3, 128 x 8192 x 4096 (64) 17.2 / 15.4,
-// 331 x 4097 x 5504 (64) 31.5 / 27.5, 200 x 11008 x 4096 (64) 39.1 / 30.9.
+// 6.0 / 10.9, 16 x 11008 x 4096 12.0 / 14.0, 32 x 6000 x 4096 10.2 / 13.8, 32 x 11008
+// x 4096 13.7 / 14.7, 64 x 4096 x 4096 (16 columns) 10.9 / 28, 100 x 4096 x 4096 (32) 10.8
+// / 28, 64 x 11008 x 4096 (48) 15.2 / 16.3, 256 x 4096 x 4096 (64) 13.9 / 17.7; past the
+// rule 16 x 16384 x 4096 (64) 18.1 / 17.3, 128 x 8192 x 4096 (64) 15.7 / 15.4, 331 x 4097
+// x 5504 (64) 32.0 / 25.2, 200 x 11008 x 4096 (64) 37.1 / 23.8.
 struct FewShape {
     int tm, tn;
 };
