@@ -376,8 +376,8 @@ __device__ inline float sum_over_groups(float x)
 // Neither the weights nor the values change lanes, and nothing passes through LDS.
 // Bound by the cache's bytes where keys are many: 8 heads of 128 of two sequences of
 // 131072 keys (285 MB) in 57 us, 5.0 TB/s, what a copy reaches; by latency where they
-// are few: one sequence of 777 keys 11.2 us, 12 sequences of 5 queries,
-// 32 heads of 64, windows of 1024 keys 15.6 us.
+// are few: one sequence of 777 keys 11.2 us, 12 sequences of 5 queries over windows
+// of 1024 keys, 32 heads of 64, 15.6 us.
 // The next block's keys are asked for as soon as this one's are multiplied, its
 // values as soon as this one's are, into the same registers, and the numbers of
 // its pages a block earlier.  (Two blocks' worth of registers cost more in waves
@@ -866,11 +866,10 @@ __global__ __launch_bounds__(256) void attn_flat_join_kernel(AttnArgs a)
 // read, counted, where rows padded by 16 bytes took 8 (and every write 8).
 //
 // 32 heads over 8 of 128, 700 to 2048 queries of three sequences of up to 8192 keys,
-// bf16: 533 us, 680
-// TFLOP/s, 56% of what a large bf16 product reaches.  The matrix cores are busy for
-// 166 us of it, the vector ALUs for about 300 (two fused multiply-adds, an exponential,
-// a maximum and a sum for each score, besides the turning), reads of LDS for about 230;
-// a wave waits a third of its time, mostly at the barrier that ends a tile.
+// bf16: 533 us, 680 TFLOP/s, 56% of what a large bf16 product reaches.  The matrix
+// cores are busy for 166 us of it, the vector ALUs for about 300 (two fused
+// multiply-adds, an exponential, a maximum and a sum for each score, besides the
+// turning), reads of LDS for about 230; a wave waits a third of its time.
 //
 // The values' product, by type:
 //   bf16  values are made whole, u s + m, in fp16 scaled by one power of two for
