@@ -1072,6 +1072,15 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
             }
         }
     };
+    // From here on what was fetched is used: without it the compiler turns numbers, and
+    // so waits for them, right where they are asked for.
+    auto fetched = [&] {
+#pragma unroll
+        for (int j = 0; j < KH; ++j) asm volatile("" : "+v"(kw[j]));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(vw[i]));
+        asm volatile("" : "+v"(kpw), "+v"(vpw));
+    };
     // Turning, in units of one 16-byte write: word j of the keys, the per-key
     // numbers, dim j of the values.
     auto turn_key_word = [&](int j, char *kbuf) {
@@ -1328,6 +1337,7 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
         });
         __builtin_amdgcn_s_setprio(0);
         // the values' product, beside the turning of what comes next
+        fetched();
         constexpr int VSTEPS = 2 * ND;
         i32x4 vf[PF + 1];
         auto read_val = [&](int st) { vf[st % (PF + 1)] = *(const i32x4 *)(vcur + LT::val_at(16 * (st % ND) + r, st / ND, c)); };
