@@ -1155,30 +1155,37 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
     // Sums q . (base + u) of the 64 keys in kbuf, in 4 KW steps of one fragment read
     // and RX products; beside(step) adds the caller's vector instructions to a step.
     // A step is fenced, so that its read goes out PF steps before its products: left
-    // to itself the compiler waits for each read where it stands.
+    // to itself the compiler waits for each read where it stands.  The first PF reads
+    // are start_products', some way ahead; the last PF steps make room for the
+    // caller's next ones, after(0 .. PF - 1).
     constexpr int STEPS = 4 * KW, PF = 3;
-    auto products = [&](const char *kbuf, auto beside) {
-        i32x4 kf[PF + 1], q[2][RX];
-        auto read_key = [&](int st) { kf[st % (PF + 1)] = *(const i32x4 *)(kbuf + LT::key_at(16 * (st % 4) + r, st / 4, c)); };
-        auto read_query = [&](int j) {
+    i32x4 kf[PF + 1], qr[2][RX];
+    auto read_key = [&](const char *kbuf, int st) {
+        kf[st % (PF + 1)] = *(const i32x4 *)(kbuf + LT::key_at(16 * (st % 4) + r, st / 4, c));
+    };
+    auto read_query = [&](int j) {
 #pragma unroll
-            for (int x = 0; x < RX; ++x) {
-                if constexpr (LT::Q_LDS) q[j & 1][x] = *(const i32x4 *)(qlds + (x * KW + j) * 1024);
-                else q[j & 1][x] = qf[x][j];
-            }
-        };
+        for (int x = 0; x < RX; ++x) {
+            if constexpr (LT::Q_LDS) qr[j & 1][x] = *(const i32x4 *)(qlds + (x * KW + j) * 1024);
+            else qr[j & 1][x] = qf[x][j];
+        }
+    };
+    auto start_products = [&](const char *kbuf) {
         read_query(0);
 #pragma unroll
-        for (int st = 0; st < PF; ++st) read_key(st);
+        for (int st = 0; st < PF; ++st) read_key(kbuf, st);
+    };
+    auto products = [&](const char *kbuf, auto beside, auto after) {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int st = 0; st < STEPS; ++st) {
             const int j = st / 4, g = st % 4;
-            if (st + PF < STEPS) read_key(st + PF);
+            if (st + PF < STEPS) read_key(kbuf, st + PF);
+            else after(st + PF - STEPS);
             if (g == 0 && j + 1 < KW) read_query(j + 1);
 #pragma unroll
             for (int x = 0; x < RX; ++x)
-                z[x][g] = MM::mul(kf[st % (PF + 1)], q[j & 1][x], j ? z[x][g] : f32x4{0, 0, 0, 0});
+                z[x][g] = MM::mul(kf[st % (PF + 1)], qr[j & 1][x], j ? z[x][g] : f32x4{0, 0, 0, 0});
             beside(st);
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -1197,7 +1204,8 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
         ask_vals(first + 1);
         __syncthreads();
         turn_vals(smem + LT::V_AT, smem + LT::P_AT);
-        products(smem, [](int) {});
+        start_products(smem);
+        products(smem, [](int) {}, [](int) {});
     }
     __syncthreads();
     // Tile t: its scores' sums are in z; the next tile's are made beside its softmax,
@@ -1270,6 +1278,7 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
                             if ((seen[x] >> e) & 1u) extra[x] = __builtin_nanf("");
                 }
             }
+        start_products(knext);
         // The running maximum is taken anew only when a score passes it by 2^8, and
         // first of all; only then do the lanes of a row compare.
         bool raise = false;
@@ -1304,6 +1313,9 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
         // this tile's weights, beside the next tile's sums
         i32x4 whi[RX][2], wlo2[RX][2];
         constexpr int QUADS = 4 * RX;   // four weights each
+        constexpr int VSTEPS = 2 * ND;
+        i32x4 vf[PF + 1];
+        auto read_val = [&](int st) { vf[st % (PF + 1)] = *(const i32x4 *)(vcur + LT::val_at(16 * (st % ND) + r, st / ND, c)); };
         __builtin_amdgcn_s_setprio(1);   // (2% faster than none, or than over both products)
         products(knext, [&](int st) {
 #pragma unroll
@@ -1334,16 +1346,10 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
                     }
                 }
             }
-        });
+        }, read_val);
         __builtin_amdgcn_s_setprio(0);
         // the values' product, beside the turning of what comes next
         fetched();
-        constexpr int VSTEPS = 2 * ND;
-        i32x4 vf[PF + 1];
-        auto read_val = [&](int st) { vf[st % (PF + 1)] = *(const i32x4 *)(vcur + LT::val_at(16 * (st % ND) + r, st / ND, c)); };
-#pragma unroll
-        for (int st = 0; st < PF; ++st) read_val(st);
-        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int st = 0; st < VSTEPS; ++st) {
             const int d = st % ND, q = st / ND;
