@@ -294,7 +294,8 @@ bool lb::variant_is_forced() { return auto_override() >= 0; }
 // 16384 x 4096 20.5 / 26.8, 400 x 4096 x 4096 17.2 / 21.9, 700 x 2048 x 4096 17.1 / 27.8,
 // 331 x 4097 x 1024 9.2 / 12.3; 64 x 128 300 x 6144 x 8192 34.9 / 41.5; 128 x 128 200 x
 // 11008 x 4096 23.8 / 31.3, 512 x 8192 x 4096 25.9 / 36.7, 2000 x 2048 x 4096 24.9 / 34.8,
-// 140 x 12000 x 512 7.1 / 8.1.  Where tiles of 64 x 64 do run at once: 128 x 8192 x 4096
+// 140 x 12000 x 512 7.1 / 8.1; tall ones the same (20000 x 64 x 4096 26.4, the best variant
+// 28.4), K below 512 within a launch's time of each other.  Where tiles of 64 x 64 do run at once: 128 x 8192 x 4096
 // 128 x 64 19.7, those 15.4.
 static int scaled_deep_tile(int64_t M, int64_t N)
 {
