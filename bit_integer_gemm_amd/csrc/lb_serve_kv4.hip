@@ -871,19 +871,23 @@ __global__ __launch_bounds__(256) void attn_flat_join_kernel(AttnArgs a)
 // multiply-adds, an exponential, a maximum and a sum for each score, besides the
 // turning), reads of LDS for about 230; a wave waits 30% of its time.
 //
-// The values' product, by type:
-//   bf16  values are made whole, u s + m, in fp16 scaled by one power of two for
-//         the workgroup (2^vexp brings the largest |m| + 16 s of its keys to about
-//         2^10, found by a pass over their scales first), and weights are fp16:
-//         both are off by 2^-12, an eighth of the output's own rounding, and a
-//         value 2^-24 of the largest still counts.  A value vector that is not
-//         finite is left out of the product and its rows are made NaN apart.
-//   fp16  that would be as coarse as the output: levels stay exact and the weights
-//         p s go in two bf16 parts, as in attn_rows_kernel.
-template <class T, int D> struct ChunkTile {
+// The values' product goes one of two ways:
+//   whole   values are made whole, u s + m, in fp16 scaled by one power of two for
+//           the workgroup, which brings the largest |m| + 16 s of its keys to about
+//           2^10, and weights are fp16: both are off by 2^-12, an eighth of a bf16
+//           output's own rounding.
+//   levels  levels stay exact and the weights p s go in two bf16 parts, as in
+//           attn_rows_kernel, with fp32's range; 650 us where the other way takes 470.
+// fp16 outputs take the levels: the other way would be as coarse as they are.  For bf16
+// a pass over the scales of the workgroup's keys decides (value_scale): some row may not
+// see the largest value, so whole values have to hold the smallest beside it, and
+// vectors that are not finite, or 2^20 apart, leave the workgroup to the levels.
+template <int D> struct ChunkRows {
     static constexpr int RX = D == 256 ? 1 : 2;   // 16-row fragments per wave
     static constexpr int ROWS = 8 * 16 * RX;
-    static constexpr bool WHOLE = __is_same(T, __bf16);
+};
+template <class T, int D, bool WHOLE> struct ChunkTile {
+    static constexpr int ROWS = ChunkRows<D>::ROWS;
     static constexpr int KROW = 2 * D, VROW = 128;
     static constexpr int KBYTES = 64 * KROW, VBYTES = D * VROW;
     // per-key numbers of a tile: scale and minimum of keys (fp32), of values (fp16 or
@@ -901,62 +905,71 @@ template <class T, int D> struct ChunkTile {
     static __device__ inline int val_at(int n, int q, int c) { return n * VROW + 16 * ((4 * q + c) ^ (n & 7)); }
 };
 
-template <class T, int D>
-__global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
+// The power of two by which a workgroup's values (keys first * 64 .. of them, below hi)
+// fit fp16 side by side, or 0 where they do not: it brings a quarter of the largest |m| +
+// 16 s to 2^8 .. 2^9, and with 2^20 between them the smallest to 2^-12, whose parts s and
+// m are then off by 2^-25 at most, 2^-13 of it.  (Vectors of zeros fit beside any.)
+template <class T>
+__device__ inline float value_scale(const AttnArgs &a, int32_t b, int32_t h, int32_t first, int32_t last, int32_t hi,
+                                    uint32_t (&red)[8][2])
+{
+    const uint32_t lane = threadIdx.x & 63u;
+    const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    uint32_t most = 0, least = 0xFFFFFFFFu;
+    for (int32_t t = first * 64 + 4 * (int32_t)threadIdx.x; t < min(last * 64, hi); t += 2048) {
+        const int32_t pi = page_of(a, t), p = a.table[(int64_t)b * a.ldt + pi];
+        if ((uint32_t)p >= (uint32_t)a.c.pages) continue;
+        const u32x4 w = *(const u32x4 *)(a.c.vp + ((int64_t)p * a.c.heads + h) * a.c.page + (t - pi * a.c.page));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // a quarter of |m| + 16 s: cannot overflow for finite vectors, and orders as its
+            // bits do (infinity and NaN above all)
+            const uint32_t bits = __float_as_uint(0.25f * __builtin_fabsf(hi_f32<T>(w[i])) + 4.f * lo_f32<T>(w[i])) & 0x7FFFFFFFu;
+            if (t + i >= hi || bits == 0) continue;
+            most = max(most, bits);
+            least = min(least, bits);
+        }
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+        most = max(most, (uint32_t)__shfl_xor((int)most, d));
+        least = min(least, (uint32_t)__shfl_xor((int)least, d));
+    }
+    if (lane == 0) {
+        red[wave][0] = most;
+        red[wave][1] = least;
+    }
+    __syncthreads();
+    most = red[0][0];
+    least = red[0][1];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) {
+        most = max(most, red[w][0]);
+        least = min(least, red[w][1]);
+    }
+    if (most == 0) return 1.f;
+    if (most >= 0x7F800000u || (most >> 23) - (least >> 23) > 20) return 0.f;
+    // 2^125 at most, whose reciprocal is a normal number
+    return __uint_as_float(min(254u + 8u - (most >> 23), 252u) << 23);
+}
+
+// What a workgroup of attn_chunk_kernel does: rows r0 .. of key head h against tiles
+// [first, last) of 64 keys.
+template <class T, int D, bool WHOLE>
+__device__ __forceinline__ void chunk_rows(const AttnArgs &a, char *smem, const Span &sp, int32_t b, int32_t h, int32_t r0,
+                                           int32_t hi, const Ranges &rg, int32_t first, int32_t last, float vscale)
 {
     using MM = Mfma<T>;
-    using LT = ChunkTile<T, D>;
-    constexpr bool WHOLE = LT::WHOLE;
-    constexpr int RX = LT::RX;
+    using LT = ChunkTile<T, D, WHOLE>;
+    constexpr int RX = ChunkRows<D>::RX;
     constexpr int KW = D / 32;      // MFMAs per 16 keys
     constexpr int KH = KW / 2;      // words of a key a lane turns
     constexpr int DPT = D / 64;     // dims of eight keys a lane turns
     constexpr int ND = D / 16;      // 16-dim fragments of the output
-    __shared__ __attribute__((aligned(16))) char smem[LT::BYTES];
-    __shared__ uint32_t red[8];
     const uint32_t lane = threadIdx.x & 63u;
     const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int32_t r = (int32_t)(lane & 15u), c = (int32_t)(lane >> 4);
-    // The tiles that see the most keys start first: the last of a sequence, and of
-    // several sequences (up to 512 tiles) this workgroup's place in the order of
-    // their keys, which each finds for itself.  (3 x 2048 queries over up to 8192
-    // keys, then 533 us; the last tile of every sequence first, and so on, 618.)
-    const int32_t place = (int32_t)(blockIdx.x / (uint32_t)a.c.heads), h = (int32_t)(blockIdx.x % (uint32_t)a.c.heads);
-    const int32_t tasks = a.batch * a.tiles;
-    int32_t b = place % a.batch, tile = a.tiles - 1 - place / a.batch;
-    if (a.batch > 1 && tasks <= 512) {
-        int32_t *cost = (int32_t *)smem, *found = cost + 512;
-        const int32_t mine = (int32_t)threadIdx.x;
-        if (mine < tasks) {
-            const Span s = lane_span_of(a, mine / a.tiles);
-            const int32_t from = mine % a.tiles * LT::ROWS;
-            int32_t from_key = 0, to_key = -1;   // no rows: after all others
-            if (from < s.rows) tile_keys(a, s, from, LT::ROWS, from_key, to_key);
-            cost[mine] = to_key - from_key;
-        }
-        __syncthreads();
-        if (mine < tasks) {
-            const int32_t c0 = cost[mine];
-            int32_t rank = 0;
-            for (int32_t k = 0; k < tasks; ++k) rank += cost[k] > c0 || (cost[k] == c0 && k < mine);
-            if (rank == place) *found = mine;
-        }
-        __syncthreads();
-        const int32_t f = __builtin_amdgcn_readfirstlane(*found);
-        b = f / a.tiles;
-        tile = f - b * a.tiles;
-        __syncthreads();
-    }
-    const Span sp = span_of(a, b);
-    const int32_t r0 = tile * LT::ROWS;
-    if (r0 >= sp.rows) return;
-
-    // key range of the workgroup, keys that every row of this wave sees, and the
-    // range of each of its lanes' rows
-    const int32_t lo = key_lo(a, sp, r0 / a.group), hi = key_hi(a, sp, min(r0 + LT::ROWS - 1, sp.rows - 1) / a.group);
-    const Ranges rg = ranges_of<64>(a, lo, hi);
-    if ((int32_t)blockIdx.y >= rg.ranges) return;
-    const int32_t first = rg.b0 + (int32_t)blockIdx.y * rg.per, last = min(rg.b0 + rg.nb, first + rg.per);
+    // keys that every row of this wave sees, and the range of each of its lanes' rows
     const int32_t w0 = r0 + 16 * RX * wave;
     const bool busy = w0 < sp.rows;
     const int32_t wf = min(w0, sp.rows - 1) / a.group, wl = min(w0 + 16 * RX - 1, sp.rows - 1) / a.group;
@@ -982,43 +995,6 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
             else qf[x][j] = query_order(w);
         }
         qsum[x] = sum_over_groups(sum);
-    }
-
-    // 2^vexp for the values of this key range
-    float vscale = 1.f;
-    bool odd = false;   // some value vector of the range is not finite
-    if constexpr (WHOLE) {
-        uint32_t mx = 0;
-        for (int32_t t = first * 64 + 4 * (int32_t)threadIdx.x; t < min(last * 64, hi); t += 2048) {
-            const int32_t pi = page_of(a, t), p = a.table[(int64_t)b * a.ldt + pi];
-            if ((uint32_t)p >= (uint32_t)a.c.pages) continue;
-            const u32x4 w = *(const u32x4 *)(a.c.vp + ((int64_t)p * a.c.heads + h) * a.c.page + (t - pi * a.c.page));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // a quarter of |m| + 16 s: cannot overflow for finite vectors
-                const float g = 0.25f * __builtin_fabsf(hi_f32<T>(w[i])) + 4.f * lo_f32<T>(w[i]);
-                const uint32_t bits = __float_as_uint(g);
-                if (t + i < hi) {
-                    if (bits < 0x7F800000u) mx = max(mx, bits);
-                    else odd = true;
-                }
-            }
-        }
-#pragma unroll
-        for (int d = 32; d; d >>= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, d));
-        if (__any(odd)) mx |= 0x80000000u;
-        if (lane == 0) red[wave] = mx;
-        __syncthreads();
-        mx = 0;
-        odd = false;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) {
-            odd |= (red[w] >> 31) != 0;
-            mx = max(mx, red[w] & 0x7FFFFFFFu);
-        }
-        // the largest quarter comes to 2^8 .. 2^9; 2^125 at most, whose reciprocal is a normal number
-        const uint32_t e = min(254u + 8u - (mx >> 23), 252u);
-        vscale = __uint_as_float(e << 23);
     }
 
     // What a thread turns: words khalf KH .. of the levels [c D/4, (c+1) D/4) of key
@@ -1095,9 +1071,8 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
         f[64] = (hi_f32<T>(kpw) - MM::base * lo_f32<T>(kpw)) * a.scale2;
         const float s0 = lo_f32<T>(vpw), m0 = hi_f32<T>(vpw);
         if constexpr (WHOLE) {
-            // a key past the range, on a page that is not there, or whose value is not
-            // finite counts as zeros
-            const bool in = (64 * t + 16 * part + r < hi) & there & (0.25f * __builtin_fabsf(m0) + 4.f * s0 < __builtin_inff());
+            // a key past the range or on a page that is not there counts as zeros
+            const bool in = (64 * t + 16 * part + r < hi) & there;
             const float sv = s0 * vscale, mv = (m0 + 8.f * s0) * vscale;
             _Float16 *g = (_Float16 *)(prm + 512) + 16 * part + r;
             g[0] = (_Float16)(in ? sv : 0.f);
@@ -1263,21 +1238,6 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
                     }
             }
         }
-        if constexpr (WHOLE)
-            if (odd) {
-#pragma unroll 1
-                for (int e = 0; e < 16; ++e) {
-                    const int32_t key = t0 + 16 * (e >> 2) + 4 * c + (e & 3);
-                    if (key >= hi || !((ok_pages >> (e >> 2)) & 1u)) continue;
-                    const int32_t pi = page_of(a, key);
-                    const uint32_t w = a.c.vp[((int64_t)a.table[(int64_t)b * a.ldt + pi] * a.c.heads + h) * a.c.page +
-                                              (key - pi * a.c.page)];
-                    if (!(0.25f * __builtin_fabsf(hi_f32<T>(w)) + 4.f * lo_f32<T>(w) < __builtin_inff()))
-#pragma unroll
-                        for (int x = 0; x < RX; ++x)
-                            if ((seen[x] >> e) & 1u) extra[x] = __builtin_nanf("");
-                }
-            }
         start_products(knext);
         // The running maximum is taken anew only when a score passes it by 2^8, and
         // first of all; only then do the lanes of a row compare.
@@ -1382,11 +1342,10 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
     for (int x = 0; x < RX; ++x) {
         const int32_t row = w0 + 16 * x + r;
         float l = sum_over_groups(l_run[x]);
-        float add = WHOLE ? extra[x] : sum_over_groups(extra[x]);
-        if constexpr (WHOLE) add += __shfl_xor(add, 16), add += __shfl_xor(add, 32);  // 0, or NaN in any
+        const float add = WHOLE ? 0.f : sum_over_groups(extra[x]);
         if (row >= sp.rows) continue;
         const float mul = WHOLE ? 1.f / vscale : 1.f;
-        const float off = WHOLE ? -add : MfmaV::base * ones[x].x - add;
+        const float off = WHOLE ? 0.f : MfmaV::base * ones[x].x - add;
         const int32_t oq = row / a.group, oh = h * a.group + (row - oq * a.group);
         const int64_t hq = (int64_t)a.group * a.c.heads, grow = (sp.q0 + oq) * hq + oh;
         if (rg.ranges > 1) {
@@ -1412,6 +1371,60 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
     }
 }
 
+template <class T, int D>
+__global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
+{
+    constexpr int ROWS = ChunkRows<D>::ROWS, LEVELS = ChunkTile<T, D, false>::BYTES, WHOLE = ChunkTile<T, D, true>::BYTES;
+    __shared__ __attribute__((aligned(16))) char smem[LEVELS > WHOLE ? LEVELS : WHOLE];
+    // The tiles that see the most keys start first: the last of a sequence, and of
+    // several sequences (up to 512 tiles) this workgroup's place in the order of
+    // their keys, which each finds for itself.  (3 x 2048 queries over up to 8192
+    // keys, then 533 us; the last tile of every sequence first, and so on, 618.)
+    const int32_t place = (int32_t)(blockIdx.x / (uint32_t)a.c.heads), h = (int32_t)(blockIdx.x % (uint32_t)a.c.heads);
+    const int32_t tasks = a.batch * a.tiles;
+    int32_t b = place % a.batch, tile = a.tiles - 1 - place / a.batch;
+    if (a.batch > 1 && tasks <= 512) {
+        int32_t *cost = (int32_t *)smem, *found = cost + 512;
+        const int32_t mine = (int32_t)threadIdx.x;
+        if (mine < tasks) {
+            const Span s = lane_span_of(a, mine / a.tiles);
+            const int32_t from = mine % a.tiles * ROWS;
+            int32_t from_key = 0, to_key = -1;   // no rows: after all others
+            if (from < s.rows) tile_keys(a, s, from, ROWS, from_key, to_key);
+            cost[mine] = to_key - from_key;
+        }
+        __syncthreads();
+        if (mine < tasks) {
+            const int32_t c0 = cost[mine];
+            int32_t rank = 0;
+            for (int32_t k = 0; k < tasks; ++k) rank += cost[k] > c0 || (cost[k] == c0 && k < mine);
+            if (rank == place) *found = mine;
+        }
+        __syncthreads();
+        const int32_t f = __builtin_amdgcn_readfirstlane(*found);
+        b = f / a.tiles;
+        tile = f - b * a.tiles;
+        __syncthreads();
+    }
+    const Span sp = span_of(a, b);
+    const int32_t r0 = tile * ROWS;
+    if (r0 >= sp.rows) return;
+
+    const int32_t lo = key_lo(a, sp, r0 / a.group), hi = key_hi(a, sp, min(r0 + ROWS - 1, sp.rows - 1) / a.group);
+    const Ranges rg = ranges_of<64>(a, lo, hi);
+    if ((int32_t)blockIdx.y >= rg.ranges) return;
+    const int32_t first = rg.b0 + (int32_t)blockIdx.y * rg.per, last = min(rg.b0 + rg.nb, first + rg.per);
+    if constexpr (__is_same(T, __bf16)) {
+        __shared__ uint32_t red[8][2];
+        const float vscale = value_scale<T>(a, b, h, first, last, hi, red);
+        if (vscale != 0.f) {
+            chunk_rows<T, D, true>(a, smem, sp, b, h, r0, hi, rg, first, last, vscale);
+            return;
+        }
+    }
+    chunk_rows<T, D, false>(a, smem, sp, b, h, r0, hi, rg, first, last, 1.f);
+}
+
 // The partial results of attn_chunk_kernel's key ranges joined, in the ranges'
 // order: a wave per row, whose lanes read whole partial rows, eight ranges at a time.
 template <class T, int D>
@@ -1424,7 +1437,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int32_t row_
     const Span sp = span_of(a, b);
     const int32_t row = tile * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     if (row >= sp.rows) return;
-    constexpr int ROWS = ChunkTile<T, D>::ROWS;
+    constexpr int ROWS = ChunkRows<D>::ROWS;
     const int32_t r0 = row / ROWS * ROWS;
     const Ranges rg = ranges_of<64>(a, key_lo(a, sp, r0 / a.group),
                                        key_hi(a, sp, min(r0 + ROWS - 1, sp.rows - 1) / a.group));
@@ -1496,7 +1509,7 @@ template <class T, int D> static hipError_t attn_t(const AttnArgs &a, hipStream_
     hipLaunchKernelGGL((attn_chunk_kernel<T, D>), grid, dim3(512), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
-    const int64_t row_tiles = ChunkTile<T, D>::ROWS / 4 * (int64_t)a.tiles;
+    const int64_t row_tiles = ChunkRows<D>::ROWS / 4 * (int64_t)a.tiles;
     const int64_t joins = (int64_t)a.batch * a.c.heads * row_tiles;
     if (joins > 0x7FFFFFFF) return hipErrorInvalidValue;
     hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3((uint32_t)joins), dim3(256), 0, s, a, (int32_t)row_tiles);

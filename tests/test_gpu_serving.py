@@ -681,3 +681,64 @@ def test_layer_in_a_graph():
         layer_step(**d)
         torch.cuda.synchronize()
         assert torch.equal(got, d["attn"]) and torch.isfinite(got).all(), i
+
+
+# ---------------------------------------------------------------------------
+# prompts: values and weights of any size
+# ---------------------------------------------------------------------------
+
+def refill(b, k, v, seq=0):
+    """Other keys and values (n, Hkv, D) for a sequence of a batch."""
+    at = sum(b.lens[:seq])
+    lb.lb_kv4_write(k.cuda(), v.cuda(), b.slots[at:at + len(k)].contiguous(), *b.cache)
+    held = [quantise_ref(x) for x in (k, v)]
+    b.kv[seq] = tuple(torch.from_numpy(u) * s.double() + low.double() for u, s, low in held)
+    b.smax = max(b.smax, float(held[0][1].float().max()))
+
+
+def largest_seen(b, window=0):
+    """The largest value that each row sees (total, 1, 1), of any head; rows that see nothing: 0."""
+    rows = []
+    for n, nq, (_, v) in zip(b.lens, b.nqs, b.kv):
+        for pos in range(n - nq, n):
+            seen = v[max(0, pos + 1 - window) if window else 0:max(0, pos + 1)]
+            rows.append(float(seen.abs().max()) if len(seen) else 0.0)
+    return torch.tensor(rows, dtype=torch.float64)[:, None, None]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("times", [2.0 ** 10, 2.0 ** 20, 2.0 ** 23, 2.0 ** 36, 1e30])
+def test_attention_prompt_large_value_that_only_some_rows_see(dtype, D, times):
+    """A vector of values far above the others: the rows before it come out as if it were not there."""
+    if dtype == HF and times > 2.0 ** 10:
+        pytest.skip("beyond the type")
+    b = Batch([700, 260], [200, 100], 8, 2, D, 48, dtype, seed=D)
+    k, v = torch.randn(700, 2, D, generator=gen(1)).to(dtype), torch.randn(700, 2, D, generator=gen(2)).to(dtype)
+    v[650] = (v[650].float() * times).to(dtype)
+    refill(b, k, v)
+    b.check(b.run(max_q=200), b.want(), vmax=largest_seen(b))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("times", [2.0 ** 23, 1e12, 1e30])
+def test_attention_prompt_large_values_before_the_window(D, times):
+    """Values that no row sees, in the first tile of keys: a page that a server has given to another sequence."""
+    b = Batch([700], [200], 8, 2, D, 16, BF, seed=D)
+    k, v = torch.randn(700, 2, D, generator=gen(1)).to(BF), torch.randn(700, 2, D, generator=gen(2)).to(BF)
+    v[384:401] = (v[384:401].float() * times).to(BF)   # the first query stands at 500 and sees 401 .. 500
+    refill(b, k, v)
+    b.check(b.run(window=100, max_q=200), b.want(window=100), vmax=largest_seen(b, 100))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_prompt_small_values_beside_zeros(D):
+    """Values of all sizes in one prompt, some exactly zero, and a sequence whose values are all tiny."""
+    b = Batch([600, 300], [150, 150], 8, 2, D, 16, BF, seed=D)
+    for seq, n in ((0, 600), (1, 300)):
+        k, v = torch.randn(n, 2, D, generator=gen(3)), torch.randn(n, 2, D, generator=gen(4))
+        size = 2.0 ** torch.randint(-9, 9, (n, 1, 1), generator=gen(5)).float() if seq == 0 else torch.tensor(2.0 ** -100)
+        v = v * size
+        v[5::7] = 0
+        refill(b, k.to(BF), v.to(BF), seq)
+    b.check(b.run(max_q=150), b.want(), vmax=largest_seen(b))
