@@ -363,6 +363,24 @@ __device__ inline float sum_over_groups(float x)
     return x + __shfl_xor(x, 32);
 }
 
+// A sum of many blocks' sums, with what each addition rounds away carried to the next:
+// a running fp32 sum drops weights below 2^-24 of it however many they are (20000 of
+// 2^-24.4 beside a 1: 9e-5 of it, and 131072 equal weights were off by as much).
+struct LongSum {
+    float s = 0.f, over = 0.f;   // over: what s holds too much
+    __device__ inline void add(float t)
+    {
+        const float y = t - over, n = s + y;
+        over = (n - s) - y;
+        s = n;
+    }
+    __device__ inline void scale(float f)   // by a power of two, or about one
+    {
+        s *= f;
+        over *= f;
+    }
+};
+
 // Sixteen rows (r0 ..) of a key head against blocks [first, last) of 32 keys.  Each
 // of NW waves takes its share of the blocks (two half-blocks of 16 keys, each inside
 // one page) and keeps its own maximum, sum and output; they meet in LDS.  part: where
@@ -470,7 +488,8 @@ __device__ __forceinline__ void rows_segment(const AttnArgs &a, RowsLds<D, NW> &
     const float start = -MM::base * qsum, qsum2 = qsum * a.scale2;
 
     const float NEG = -__builtin_inff();
-    float m_run = NEG, l_run = 0.f, pm = 0.f;
+    float m_run = NEG, pm = 0.f;
+    LongSum l_run;
     f32x4 acc[DPL], ones = {0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < DPL; ++j) acc[j] = f32x4{0, 0, 0, 0};
@@ -528,20 +547,21 @@ __device__ __forceinline__ void rows_segment(const AttnArgs &a, RowsLds<D, NW> &
 #pragma unroll
             for (int e = 0; e < 8; ++e) sc[e / 4][e % 4] += top - m_use;
             m_run = m_new;
-            l_run *= al;
+            l_run.scale(al);
             pm *= al;
             ones *= al;
 #pragma unroll
             for (int j = 0; j < DPL; ++j) acc[j] *= al;
         }
         i32x4 whi, wlo;
+        float sum = 0.f;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             float w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float p = __builtin_amdgcn_exp2f(sc[s][i]);
-                l_run += p;
+                sum += p;
                 pm = __builtin_fmaf(p, hi_f32<T>(vp[s][i]), pm);
                 w[i] = p * lo_f32<T>(vp[s][i]);
             }
@@ -552,6 +572,7 @@ __device__ __forceinline__ void rows_segment(const AttnArgs &a, RowsLds<D, NW> &
                 wlo[2 * s + i] = (int)pack2<__bf16>(w[2 * i] - lo_f32<__bf16>(hi2), w[2 * i + 1] - hi_f32<__bf16>(hi2));
             }
         }
+        l_run.add(sum);
         // values
         ones = MfmaV::mul(one, whi, ones);
         ones = MfmaV::mul(one, wlo, ones);
@@ -579,11 +600,11 @@ __device__ __forceinline__ void rows_segment(const AttnArgs &a, RowsLds<D, NW> &
     }
 
     // the waves' results
-    l_run = sum_over_groups(l_run);
+    const float l_wave = sum_over_groups(l_run.s);
     pm = sum_over_groups(pm);
     if (c == 0) {
         stat[wave][r][0] = m_run;
-        stat[wave][r][1] = l_run;
+        stat[wave][r][1] = l_wave;
         stat[wave][r][2] = pm;
     }
     const float off = MfmaV::base * ones.x;
@@ -1116,12 +1137,13 @@ __device__ __forceinline__ void chunk_rows(const AttnArgs &a, char *smem, const 
     };
 
     const float NEG = -__builtin_inff();
-    float m_run[RX], l_run[RX], extra[RX];
+    float m_run[RX], extra[RX];
+    LongSum l_run[RX];
     f32x4 acc[RX][ND], ones[RX], z[RX][4];
 #pragma unroll
     for (int x = 0; x < RX; ++x) {
         m_run[x] = NEG;
-        l_run[x] = extra[x] = 0.f;
+        extra[x] = 0.f;
         ones[x] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int d = 0; d < ND; ++d) acc[x][d] = f32x4{0, 0, 0, 0};
@@ -1261,7 +1283,7 @@ __device__ __forceinline__ void chunk_rows(const AttnArgs &a, char *smem, const 
 #pragma unroll
                 for (int e = 0; e < 16; ++e) sc[x][e / 4][e % 4] += top[x] - m_use;
                 m_run[x] = m_new;
-                l_run[x] *= al;
+                l_run[x].scale(al);
                 if constexpr (!WHOLE) {
                     extra[x] *= al;
                     ones[x] *= al;
@@ -1275,6 +1297,9 @@ __device__ __forceinline__ void chunk_rows(const AttnArgs &a, char *smem, const 
         constexpr int QUADS = 4 * RX;   // four weights each
         constexpr int VSTEPS = 2 * ND;
         i32x4 vf[PF + 1];
+        float sum[RX];
+#pragma unroll
+        for (int x = 0; x < RX; ++x) sum[x] = 0.f;
         auto read_val = [&](int st) { vf[st % (PF + 1)] = *(const i32x4 *)(vcur + LT::val_at(16 * (st % ND) + r, st / ND, c)); };
         __builtin_amdgcn_s_setprio(1);   // (2% faster than none, or than over both products)
         products(knext, [&](int st) {
@@ -1282,7 +1307,7 @@ __device__ __forceinline__ void chunk_rows(const AttnArgs &a, char *smem, const 
             for (int e = 4 * QUADS * st / STEPS; e < 4 * QUADS * (st + 1) / STEPS; ++e) {
                 const int x = e / 16, g = e / 4 % 4, i = e % 4;
                 sc[x][g][i] = __builtin_amdgcn_exp2f(sc[x][g][i]);
-                l_run[x] += sc[x][g][i];
+                sum[x] += sc[x][g][i];
                 if (i != 3) continue;
                 float w[4] = {sc[x][g][0], sc[x][g][1], sc[x][g][2], sc[x][g][3]};
                 if constexpr (WHOLE) {
@@ -1308,6 +1333,8 @@ __device__ __forceinline__ void chunk_rows(const AttnArgs &a, char *smem, const 
             }
         }, read_val);
         __builtin_amdgcn_s_setprio(0);
+#pragma unroll
+        for (int x = 0; x < RX; ++x) l_run[x].add(sum[x]);
         // the values' product, beside the turning of what comes next
         fetched();
 #pragma unroll
@@ -1341,7 +1368,7 @@ __device__ __forceinline__ void chunk_rows(const AttnArgs &a, char *smem, const 
 #pragma unroll
     for (int x = 0; x < RX; ++x) {
         const int32_t row = w0 + 16 * x + r;
-        float l = sum_over_groups(l_run[x]);
+        float l = sum_over_groups(l_run[x].s);
         const float add = WHOLE ? 0.f : sum_over_groups(extra[x]);
         if (row >= sp.rows) continue;
         const float mul = WHOLE ? 1.f / vscale : 1.f;

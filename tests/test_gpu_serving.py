@@ -742,3 +742,24 @@ def test_attention_prompt_small_values_beside_zeros(D):
         v[5::7] = 0
         refill(b, k.to(BF), v.to(BF), seq)
     b.check(b.run(max_q=150), b.want(), vmax=largest_seen(b))
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("n,nq,octaves", [(131072, 1, 24.4), (131072, 1, 3), (100000, 3, 24.4), (20000, 64, 24.4), (20000, 64, 5),
+                                          (60000, 64, 0)])
+def test_attention_sum_of_many_equal_weights(dtype, n, nq, octaves):
+    """The log of a long sum: one key of weight 1 and many of 2^-octaves, which fp32 sums lose one by one.
+
+    A weight is off by a step of exp2 and its score's error; the sixteen of a lane are added in turn, the lane's sums of
+    all blocks without loss, then 4 lanes, 16 waves and 64 ranges at most: 15 + 2 + 2 + 16 + 64 half steps, and 4 of
+    the exponential and the logarithm, below 2^-17."""
+    b = Batch([n], [nq], 4, 1, 64, 16, dtype, seed=1)
+    k, v = torch.full((n, 1, 64), -octaves * math.log(2) / 8), torch.randn(n, 1, 64, generator=gen(7))
+    k[3] = 0
+    b.smax = 0.0   # constant keys: no scale
+    refill(b, k.to(dtype), v.to(dtype))
+    b.q = torch.ones_like(b.q)
+    _, wlse, score = b.want()
+    for size in (0, lb.lb_attn_kv4_workspace(1, nq, nq, 4, 1, 64, n)):
+        lse = b.run(max_q=nq, max_len=n, workspace=torch.empty(size, dtype=torch.uint8, device="cuda"))[1].cpu().double()
+        assert ((lse - wlse).abs() <= score + 2.0 ** -17 + 2.0 ** -22 * wlse.abs()).all(), float((lse - wlse).abs().max())
