@@ -896,13 +896,19 @@ __global__ __launch_bounds__(256) void attn_flat_join_kernel(AttnArgs a)
 //   whole   values are made whole, u s + m, in fp16 scaled by one power of two for
 //           the workgroup, which brings the largest |m| + 16 s of its keys to about
 //           2^10, and weights are fp16: both are off by 2^-12, an eighth of a bf16
-//           output's own rounding.
+//           output's own rounding.  The reference of a row's weights lies 9 octaves below
+//           its largest score (at 13 the reference is taken anew more often, 495 us; at 7,
+//           475), so that weights down to 2^-23 of the largest keep that precision.  A
+//           lighter one is off by 2^-25 in these units, and n of them by n 2^-14 of a
+//           value: where a row's outputs are not 2^10 times that (a heavy key whose own
+//           value is nothing beside many light ones), the workgroup starts again with the
+//           levels.
 //   levels  levels stay exact and the weights p s go in two bf16 parts, as in
-//           attn_rows_kernel, with fp32's range; 650 us where the other way takes 470.
+//           attn_rows_kernel, with fp32's range; 650 us where the other way takes 479.
 // fp16 outputs take the levels: the other way would be as coarse as they are.  For bf16
 // a pass over the scales of the workgroup's keys decides (value_scale): some row may not
 // see the largest value, so whole values have to hold the smallest beside it, and
-// vectors that are not finite, or 2^20 apart, leave the workgroup to the levels.
+// vectors that are not finite, or 2^20 apart, leave the workgroup to the levels from the start.
 template <int D> struct ChunkRows {
     static constexpr int RX = D == 256 ? 1 : 2;   // 16-row fragments per wave
     static constexpr int ROWS = 8 * 16 * RX;
@@ -968,6 +974,8 @@ __device__ inline float value_scale(const AttnArgs &a, int32_t b, int32_t h, int
         most = max(most, red[w][0]);
         least = min(least, red[w][1]);
     }
+    most = (uint32_t)__builtin_amdgcn_readfirstlane((int)most);
+    least = (uint32_t)__builtin_amdgcn_readfirstlane((int)least);
     if (most == 0) return 1.f;
     if (most >= 0x7F800000u || (most >> 23) - (least >> 23) > 20) return 0.f;
     // 2^125 at most, whose reciprocal is a normal number
@@ -975,10 +983,12 @@ __device__ inline float value_scale(const AttnArgs &a, int32_t b, int32_t h, int
 }
 
 // What a workgroup of attn_chunk_kernel does: rows r0 .. of key head h against tiles
-// [first, last) of 64 keys.
+// [first, last) of 64 keys.  Not 0 (WHOLE only, nothing written): light weights count for
+// more than fp16 keeps of them.
 template <class T, int D, bool WHOLE>
-__device__ __forceinline__ void chunk_rows(const AttnArgs &a, char *smem, const Span &sp, int32_t b, int32_t h, int32_t r0,
-                                           int32_t hi, const Ranges &rg, int32_t first, int32_t last, float vscale)
+__device__ __forceinline__ int32_t chunk_rows(const AttnArgs &a, char *smem, const Span &sp, int32_t b, int32_t h, int32_t r0,
+                                           int32_t hi, const Ranges &rg, int32_t first, int32_t last, float vscale,
+                                           uint32_t (&red)[8][2])
 {
     using MM = Mfma<T>;
     using LT = ChunkTile<T, D, WHOLE>;
@@ -1227,7 +1237,7 @@ __device__ __forceinline__ void chunk_rows(const AttnArgs &a, char *smem, const 
         const u32x4 flags = *(const u32x4 *)(prm + LT::FLAG_AT);
         const uint32_t ok_pages = __builtin_amdgcn_readfirstlane(flags.x | flags.y | flags.z | flags.w);
         const bool whole = t0 >= full_lo && t0 + 64 <= full_hi && ok_pages == 15u;
-        // scores in units of log 2 above the row's running maximum
+        // scores in units of log 2 above the row's reference
         float top[RX];
 #pragma unroll
         for (int x = 0; x < RX; ++x) top[x] = m_run[x] == NEG ? 0.f : m_run[x];
@@ -1261,15 +1271,16 @@ __device__ __forceinline__ void chunk_rows(const AttnArgs &a, char *smem, const 
             }
         }
         start_products(knext);
-        // The running maximum is taken anew only when a score passes it by 2^8, and
-        // first of all; only then do the lanes of a row compare.
+        // The weights' reference is taken anew only when a weight passes 2^8 (WHOLE: 2^15),
+        // and first of all; only then do the lanes of a row compare.
+        constexpr float MOST = WHOLE ? 15.f : 8.f, BELOW = WHOLE ? 9.f : 0.f;
         bool raise = false;
 #pragma unroll
         for (int x = 0; x < RX; ++x) {
             float mx = sc[x][0][0];
 #pragma unroll
             for (int e = 1; e < 16; ++e) mx = fmaxf(mx, sc[x][e / 4][e % 4]);
-            raise |= mx > 8.f || m_run[x] == NEG;
+            raise |= mx > MOST || m_run[x] == NEG;
         }
         if (__any(raise)) {
 #pragma unroll
@@ -1277,7 +1288,7 @@ __device__ __forceinline__ void chunk_rows(const AttnArgs &a, char *smem, const 
                 float mx = sc[x][0][0];
 #pragma unroll
                 for (int e = 1; e < 16; ++e) mx = fmaxf(mx, sc[x][e / 4][e % 4]);
-                const float m_new = fmaxf(m_run[x], max_over_groups(mx) + top[x]);
+                const float m_new = fmaxf(m_run[x], max_over_groups(mx) + (top[x] - BELOW));
                 const float m_use = m_new == NEG ? 0.f : m_new;
                 const float al = m_run[x] == NEG ? 0.f : __builtin_amdgcn_exp2f(m_run[x] - m_new);
 #pragma unroll
@@ -1365,12 +1376,34 @@ __device__ __forceinline__ void chunk_rows(const AttnArgs &a, char *smem, const 
         __syncthreads();
     }
 
+    int32_t again = 0;
+    if constexpr (WHOLE) {
+        bool lost = false;   // outputs (2^11 stands for the largest value) below 2^10 n 2^-25 2^11
+#pragma unroll
+        for (int x = 0; x < RX; ++x) {
+            float most = 0.f;
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) most = fmaxf(most, __builtin_fabsf(acc[x][d][i]));
+            const int32_t n = min(my_hi[x], 64 * last) - max(my_lo[x], 64 * first);
+            lost |= max_over_groups(most) < 0.0625f * (float)n;
+        }
+        lost = __any(lost);
+        if (lane == 0) red[wave][0] = lost && busy;
+        __syncthreads();
+        uint32_t any = 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) any |= red[w][0];
+        again = __builtin_amdgcn_readfirstlane((int)any);
+    }
+
 #pragma unroll
     for (int x = 0; x < RX; ++x) {
         const int32_t row = w0 + 16 * x + r;
         float l = sum_over_groups(l_run[x].s);
         const float add = WHOLE ? 0.f : sum_over_groups(extra[x]);
-        if (row >= sp.rows) continue;
+        if (again || row >= sp.rows) continue;
         const float mul = WHOLE ? 1.f / vscale : 1.f;
         const float off = WHOLE ? 0.f : MfmaV::base * ones[x].x - add;
         const int32_t oq = row / a.group, oh = h * a.group + (row - oq * a.group);
@@ -1396,6 +1429,7 @@ __device__ __forceinline__ void chunk_rows(const AttnArgs &a, char *smem, const 
         }
         if (a.lse && c == 0) a.lse[grow] = l == 0.f ? NEG : (m_run[x] + __builtin_log2f(l)) * 0.6931471805599453f;
     }
+    return again;
 }
 
 template <class T, int D>
@@ -1441,15 +1475,12 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
     const Ranges rg = ranges_of<64>(a, lo, hi);
     if ((int32_t)blockIdx.y >= rg.ranges) return;
     const int32_t first = rg.b0 + (int32_t)blockIdx.y * rg.per, last = min(rg.b0 + rg.nb, first + rg.per);
+    __shared__ uint32_t red[8][2];
     if constexpr (__is_same(T, __bf16)) {
-        __shared__ uint32_t red[8][2];
         const float vscale = value_scale<T>(a, b, h, first, last, hi, red);
-        if (vscale != 0.f) {
-            chunk_rows<T, D, true>(a, smem, sp, b, h, r0, hi, rg, first, last, vscale);
-            return;
-        }
+        if (vscale != 0.f && !chunk_rows<T, D, true>(a, smem, sp, b, h, r0, hi, rg, first, last, vscale, red)) return;
     }
-    chunk_rows<T, D, false>(a, smem, sp, b, h, r0, hi, rg, first, last, 1.f);
+    chunk_rows<T, D, false>(a, smem, sp, b, h, r0, hi, rg, first, last, 1.f, red);
 }
 
 // The partial results of attn_chunk_kernel's key ranges joined, in the ranges'

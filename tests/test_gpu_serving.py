@@ -763,3 +763,43 @@ def test_attention_sum_of_many_equal_weights(dtype, n, nq, octaves):
     for size in (0, lb.lb_attn_kv4_workspace(1, nq, nq, 4, 1, 64, n)):
         lse = b.run(max_q=nq, max_len=n, workspace=torch.empty(size, dtype=torch.uint8, device="cuda"))[1].cpu().double()
         assert ((lse - wlse).abs() <= score + 2.0 ** -17 + 2.0 ** -22 * wlse.abs()).all(), float((lse - wlse).abs().max())
+
+
+def check_weighted(b, got, want, scale=None):
+    """Rows against what they see: off by half a step of the output, by the scores' errors, and by 2^-10 of the
+    weighted mean of the values' magnitudes (weights and values are held to 2^-12 at least, values in two roundings),
+    however small that is beside the largest value."""
+    mean = b.want(kv=[(k, v.abs().amax(-1, keepdim=True).expand_as(v)) for k, v in b.kv], scale=scale)[0]
+    out, (wout, wlse, score) = got[0].cpu().double(), want
+    tol = half_step(b.dtype) * wout.abs() + (2 * score[..., None] + 2.0 ** -10) * mean
+    off = (out - wout).abs()
+    assert (off <= tol + torch.finfo(b.dtype).smallest_normal).all(), float((off / tol).max())
+    assert ((got[1].cpu().double() - wlse).abs() <= score + 2.0 ** -20 * (1 + wlse.abs())).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("octaves", [5, 24.4, 25.2, 27.5, 31, 36])
+def test_attention_prompt_light_keys_beside_a_heavy_one(dtype, D, octaves):
+    """One key takes nearly all the weight and has no value: the output is what the many others add."""
+    if dtype == HF and octaves > 25:
+        pytest.skip("the output is below the type's normal numbers")
+    n, nq = 20000, 64
+    b = Batch([n], [nq], 4, 1, D, 16, dtype, seed=D)
+    k = torch.full((n, 1, D), -octaves * math.log(2) / math.sqrt(D))
+    v = 1 + 0.3 * torch.randn(n, 1, D, generator=gen(7))
+    k[3], v[3] = 0, 0
+    b.smax = 0.0   # constant keys: no scale
+    refill(b, k.to(dtype), v.to(dtype))
+    b.q = torch.ones_like(b.q)
+    for size in (0, lb.lb_attn_kv4_workspace(1, nq, nq, 4, 1, D, n)):
+        check_weighted(b, b.run(max_q=nq, max_len=n, workspace=torch.empty(size, dtype=torch.uint8, device="cuda")), b.want())
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("scale", [0.05, 0.5, 2.0])
+def test_attention_prompt_scores_far_apart(dtype, D, scale):
+    """Scores that differ by a few to hundreds of octaves, the maximum rising and lying far back."""
+    b = Batch([900, 300], [120, 90], 6, 2, D, 16, dtype, seed=D)
+    check_weighted(b, b.run(max_q=120, scale=scale), b.want(scale=scale), scale=scale)
