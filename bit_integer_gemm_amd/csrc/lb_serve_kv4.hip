@@ -311,7 +311,8 @@ __device__ inline int32_t key_hi(const AttnArgs &a, const Span &s, int32_t qi)
 }
 __device__ inline int32_t key_lo(const AttnArgs &a, const Span &s, int32_t qi)
 {
-    return a.window > 0 ? max(0, s.n - s.nq + qi + 1 - a.window) : 0;
+    // (a position before the first key counts as the first, or the largest windows would overflow)
+    return a.window > 0 ? max(0, max(0, s.n - s.nq + qi + 1) - a.window) : 0;
 }
 
 // Keys that some row of r0 .. r0 + n - 1 sees.

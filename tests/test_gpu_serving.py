@@ -803,3 +803,15 @@ def test_attention_prompt_scores_far_apart(dtype, D, scale):
     """Scores that differ by a few to hundreds of octaves, the maximum rising and lying far back."""
     b = Batch([900, 300], [120, 90], 6, 2, D, 16, dtype, seed=D)
     check_weighted(b, b.run(max_q=120, scale=scale), b.want(scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 3, 2 ** 31 - 400, 2 ** 30])
+@pytest.mark.parametrize("lens,nqs,Hq", [([5, 40, 3], [9, 1, 1], 8), ([5, 130, 70], [260, 3, 200], 4)])
+def test_attention_largest_windows(lens, nqs, Hq, window, causal, dtype):
+    """Windows up to the type's end, which hide nothing, with more queries than keys: a few and many."""
+    b = Batch(lens, nqs, Hq, 2, 64, 16, dtype, seed=5)
+    got, none = b.run(window=window, causal=causal, max_q=max(nqs)), b.run(causal=causal, max_q=max(nqs))
+    b.check(got, b.want(causal=causal))
+    assert torch.equal(got[0], none[0]) and torch.equal(got[1], none[1])
