@@ -944,16 +944,18 @@ __device__ inline float value_scale(const AttnArgs &a, int32_t b, int32_t h, int
     const uint32_t lane = threadIdx.x & 63u;
     const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     uint32_t most = 0, least = 0xFFFFFFFFu;
-    for (int32_t t = first * 64 + 4 * (int32_t)threadIdx.x; t < min(last * 64, hi); t += 2048) {
-        const int32_t pi = page_of(a, t), p = a.table[(int64_t)b * a.ldt + pi];
+    // (unsigned: the step past the last key may pass 2^31)
+    const uint32_t end = (uint32_t)min(last * 64, hi);
+    for (uint32_t t = (uint32_t)first * 64u + 4u * threadIdx.x; t < end; t += 2048u) {
+        const int32_t pi = page_of(a, (int32_t)t), p = a.table[(int64_t)b * a.ldt + pi];
         if ((uint32_t)p >= (uint32_t)a.c.pages) continue;
-        const u32x4 w = *(const u32x4 *)(a.c.vp + ((int64_t)p * a.c.heads + h) * a.c.page + (t - pi * a.c.page));
+        const u32x4 w = *(const u32x4 *)(a.c.vp + ((int64_t)p * a.c.heads + h) * a.c.page + ((int32_t)t - pi * a.c.page));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             // a quarter of |m| + 16 s: cannot overflow for finite vectors, and orders as its
             // bits do (infinity and NaN above all)
             const uint32_t bits = __float_as_uint(0.25f * __builtin_fabsf(hi_f32<T>(w[i])) + 4.f * lo_f32<T>(w[i])) & 0x7FFFFFFFu;
-            if (t + i >= hi || bits == 0) continue;
+            if (t + i >= (uint32_t)hi || bits == 0) continue;
             most = max(most, bits);
             least = min(least, bits);
         }

@@ -815,3 +815,24 @@ def test_attention_largest_windows(lens, nqs, Hq, window, causal, dtype):
     got, none = b.run(window=window, causal=causal, max_q=max(nqs)), b.run(causal=causal, max_q=max(nqs))
     b.check(got, b.want(causal=causal))
     assert torch.equal(got[0], none[0]) and torch.equal(got[1], none[1])
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("nq,Hq", [(1, 2), (5, 2), (60, 8)])
+def test_attention_keys_next_to_two_to_the_31(nq, Hq, dtype):
+    """The last key numbers that 32 bits hold, seen through a window: single tokens, some, a prompt's chunk."""
+    page, D, window = 16, 64, 3000
+    width = (2 ** 31 - 1040) // page                         # the widest table that is taken
+    b = Batch([4096], [nq], Hq, 1, D, page, dtype, seed=3)    # its keys stand at the end of a sequence of n
+    n, used = width * page, 4096 // page
+    table = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
+    table[:, width - used:] = b.table[:, :used]
+    want, b.table, b.lens = b.want(window=window), table, [n]
+    for max_len in (n, 4096):
+        got = b.run(window=window, max_q=nq, max_len=max_len)
+        b.lens = [4096]
+        b.check(got, want)
+        b.lens = [n]
+    with pytest.raises(lb.LbError):
+        b.table = torch.zeros(1, width + 1, dtype=torch.int32, device="cuda")
+        b.run(window=window, max_q=nq)
