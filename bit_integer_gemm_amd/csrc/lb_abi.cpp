@@ -310,19 +310,19 @@ static int scaled_deep_tile(int64_t M, int64_t N)
 
 // The scaled product's launches are the linear layer's, but for those tiles.
 int lb::scaled_auto(const int8_t *X, const int8_t *W, const float *sx, const float *sw, void *out, int64_t M,
-                    int64_t N, int64_t K, const lb::ScaledOut &so, hipStream_t stream)
+                    int64_t N, int64_t K, int64_t ldo, const lb::ScaledOut &so, hipStream_t stream)
 {
     const int deep = scaled_deep_tile(M, N);
     if (deep >= 0)
-        return lb::launch_scaled(deep, X, W, out, sx, sw, M, N, K, N, so, stream) == hipSuccess ? LB_OK : LB_ERR_HIP;
+        return lb::launch_scaled(deep, X, W, out, sx, sw, M, N, K, ldo, so, stream) == hipSuccess ? LB_OK : LB_ERR_HIP;
     const Plan p = make_plan(lb::KIND_LINEAR, LB_S8, LB_AUTO, M, N, K, K, 0);
     const int64_t elem = so.ftype == LB_F32 ? 4 : 2;
     for (int i = 0; i < p.np; ++i) {
         const Part &q = p.parts[i];
         const lb::ScaledOut part{so.bias ? (const char *)so.bias + q.n0 * elem : nullptr, so.ftype};
         const hipError_t e = lb::launch_scaled(q.variant, X + q.m0 * K, W + q.n0 * K,
-                                               (char *)out + (q.m0 * N + q.n0) * elem, sx + q.m0, sw + q.n0, q.m,
-                                               q.n, K, N, part, stream);
+                                               (char *)out + (q.m0 * ldo + q.n0) * elem, sx + q.m0, sw + q.n0, q.m,
+                                               q.n, K, ldo, part, stream);
         if (e != hipSuccess) return LB_ERR_HIP;
     }
     return LB_OK;

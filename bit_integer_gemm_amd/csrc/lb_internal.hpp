@@ -49,7 +49,10 @@ hipError_t launch_scaled(int variant, const int8_t *A, const int8_t *B, void *ou
                          const ScaledOut &so, hipStream_t s);
 // The same with the launches of an automatic choice; an lb_status.
 int scaled_auto(const int8_t *X, const int8_t *W, const float *sx, const float *sw, void *out, int64_t M,
-                int64_t N, int64_t K, const ScaledOut &so, hipStream_t s);
+                int64_t N, int64_t K, int64_t ldo, const ScaledOut &so, hipStream_t s);
+// Threads of one launch: the runtime takes fewer than 2^32, and calls that need more
+// make several launches.
+enum : int64_t { LAUNCH_THREADS = (int64_t)1 << 31 };
 // Whether LB_AUTO_VARIANT fixes the variant of automatic calls.
 bool variant_is_forced();
 // Rows of X (K elements, ldx apart, 16-byte aligned) quantised to int8 with a

@@ -43,7 +43,16 @@ int scaled(const int8_t *X, const int8_t *W, const float *sx, const float *sw, c
     const int cu = cu_count();
     if (lb::linear_is_few(M, N, cu) && !lb::variant_is_forced())
         return finish(lb::launch_linear_few(ftype, X, W, sx, sw, bias, out, M, N, K, cu, s));
-    return lb::scaled_auto(X, W, sx, sw, out, M, N, K, lb::ScaledOut{bias, ftype}, s);
+    // (4 threads to a row, or a column, of the narrowest tile)
+    const int64_t most = lb::LAUNCH_THREADS / 8, elem = elem_of(ftype);
+    for (int64_t m0 = 0; m0 < M; m0 += most)
+        for (int64_t n0 = 0; n0 < N; n0 += most) {
+            const lb::ScaledOut so{bias ? (const char *)bias + n0 * elem : nullptr, ftype};
+            const int st = lb::scaled_auto(X + m0 * K, W + n0 * K, sx + m0, sw + n0, (char *)out + (m0 * N + n0) * elem,
+                                           std::min(most, M - m0), std::min(most, N - n0), K, N, so, s);
+            if (st != LB_OK) return st;
+        }
+    return LB_OK;
 }
 
 // Sizes of the cache.
@@ -227,6 +236,8 @@ static int check_attn(int64_t B, int64_t total_q, int64_t max_q, int64_t Hq, int
     // row numbers of a key head, and of the whole batch's tiles, are 32-bit
     if ((double)max_q * (double)(Hq / Hkv) >= 2147483632.0) return LB_ERR_OVERFLOW;
     if ((double)B * (double)Hkv * (double)((max_q * (Hq / Hkv) + 15) / 16) >= 2147483648.0) return LB_ERR_OVERFLOW;
+    // one sequence is one launch
+    if (Hkv * ((std::min(max_q, total_q) * (Hq / Hkv) + 127) / 128) * 512 > lb::LAUNCH_THREADS) return LB_ERR_OVERFLOW;
     return LB_OK;
 }
 

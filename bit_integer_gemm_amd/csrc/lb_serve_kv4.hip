@@ -161,20 +161,28 @@ template <class T, int D>
 static hipError_t write_t(const void *K, const void *V, int64_t ldk, int64_t ldv, const int64_t *slots,
                           const Kv4Cache &c, int64_t T_, hipStream_t s)
 {
-    const int64_t blocks = (T_ + 2048 / D - 1) / (2048 / D) * c.heads;
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((kv4_write_kernel<T, D>), dim3((uint32_t)blocks), dim3(256), 0, s,
-                       (const T *)K, (const T *)V, ldk, ldv, slots, c, T_);
-    return hipGetLastError();
+    const int64_t most = LAUNCH_THREADS / 256 / c.heads * (2048 / D);   // tokens of a launch
+    for (int64_t t = 0; t < T_; t += most) {
+        const int64_t n = T_ - t < most ? T_ - t : most, blocks = (n + 2048 / D - 1) / (2048 / D) * c.heads;
+        hipLaunchKernelGGL((kv4_write_kernel<T, D>), dim3((uint32_t)blocks), dim3(256), 0, s,
+                           (const T *)K + t * ldk, (const T *)V + t * ldv, ldk, ldv, slots + t, c, n);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 template <class T, int D>
 static hipError_t read_t(const Kv4Cache &c, const int64_t *slots, void *K, void *V, int64_t T_, hipStream_t s)
 {
-    const int64_t blocks = (T_ + 2048 / D - 1) / (2048 / D) * c.heads;
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((kv4_read_kernel<T, D>), dim3((uint32_t)blocks), dim3(256), 0, s, c,
-                       slots, (T *)K, (T *)V, T_);
-    return hipGetLastError();
+    const int64_t most = LAUNCH_THREADS / 256 / c.heads * (2048 / D), row = (int64_t)c.heads * D;
+    for (int64_t t = 0; t < T_; t += most) {
+        const int64_t n = T_ - t < most ? T_ - t : most, blocks = (n + 2048 / D - 1) / (2048 / D) * c.heads;
+        hipLaunchKernelGGL((kv4_read_kernel<T, D>), dim3((uint32_t)blocks), dim3(256), 0, s, c,
+                           slots + t, (T *)K + t * row, (T *)V + t * row, n);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 #define LB_KV4_BY_TYPE(CALL)                                   \
@@ -1544,8 +1552,23 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int32_t row_
     if (a.lse && lane == 0) a.lse[grow] = l == 0.f ? NEG : (m + __builtin_log2f(l)) * 0.6931471805599453f;
 }
 
-template <class T, int D> static hipError_t attn_t(const AttnArgs &a, hipStream_t s)
+template <class T, int D> static hipError_t attn_t(const AttnArgs &all, hipStream_t s)
 {
+    const int64_t most = LAUNCH_THREADS / 512 / ((int64_t)all.c.heads * all.tiles);   // sequences of a launch
+    if (all.kernel != ATTN_FLAT && all.batch > most) {
+        // (so many tiles are not cut into ranges, and need no workspace)
+        for (int64_t b = 0; b < all.batch; b += most) {
+            AttnArgs a = all;
+            a.batch = (int32_t)(all.batch - b < most ? all.batch - b : most);
+            a.table += b * a.ldt;
+            a.q_off += b;
+            a.lens += b;
+            const hipError_t e = attn_t<T, D>(a, s);
+            if (e != hipSuccess) return e;
+        }
+        return hipSuccess;
+    }
+    const AttnArgs &a = all;
     if (a.kernel == ATTN_FLAT) {
         hipLaunchKernelGGL((attn_flat_kernel<T, D>), dim3((uint32_t)a.splits), dim3(256), 0, s, a);
         const hipError_t e = hipGetLastError();
@@ -1554,7 +1577,6 @@ template <class T, int D> static hipError_t attn_t(const AttnArgs &a, hipStream_
         return hipGetLastError();
     }
     const int64_t wgs = (int64_t)a.batch * a.c.heads * a.tiles;
-    if (wgs > 0x7FFFFFFF) return hipErrorInvalidValue;
     constexpr int WIDE = attn_wide_waves(D);
     const dim3 grid((uint32_t)wgs, (uint32_t)a.splits);
     if (a.kernel != ATTN_CHUNK) {
@@ -1572,7 +1594,6 @@ template <class T, int D> static hipError_t attn_t(const AttnArgs &a, hipStream_
     if (e != hipSuccess || a.splits == 1) return e;
     const int64_t row_tiles = ChunkRows<D>::ROWS / 4 * (int64_t)a.tiles;
     const int64_t joins = (int64_t)a.batch * a.c.heads * row_tiles;
-    if (joins > 0x7FFFFFFF) return hipErrorInvalidValue;
     hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3((uint32_t)joins), dim3(256), 0, s, a, (int32_t)row_tiles);
     return hipGetLastError();
 }

@@ -142,7 +142,7 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const T *__restrict__ X
 }
 
 template <class T>
-static hipError_t quant_rows_t(const void *X, int64_t ldx, int8_t *Q, float *sx, int64_t M, int64_t K,
+static hipError_t quant_rows_part(const void *X, int64_t ldx, int8_t *Q, float *sx, int64_t M, int64_t K,
                                hipStream_t s)
 {
     const int64_t per = 256 * (16 / (int64_t)sizeof(T));  // elements a workgroup holds per chunk
@@ -154,6 +154,19 @@ static hipError_t quant_rows_t(const void *X, int64_t ldx, int8_t *Q, float *sx,
     else
         hipLaunchKernelGGL((quant_rows_kernel<T, 6>), grid, block, 0, s, (const T *)X, ldx, Q, sx, (int32_t)K);
     return hipGetLastError();
+}
+
+template <class T>
+static hipError_t quant_rows_t(const void *X, int64_t ldx, int8_t *Q, float *sx, int64_t M, int64_t K,
+                               hipStream_t s)
+{
+    const int64_t most = LAUNCH_THREADS / 256;
+    for (int64_t m = 0; m < M; m += most) {
+        const hipError_t e = quant_rows_part<T>((const T *)X + m * ldx, ldx, Q + m * K, sx + m,
+                                                M - m < most ? M - m : most, K, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_quant_rows(int ftype, const void *X, int64_t ldx, int8_t *Q, float *sx, int64_t M,

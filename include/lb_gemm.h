@@ -80,7 +80,9 @@ typedef enum {
     LB_ERR_ALIGN = 3,    /* K violates the per-type alignment rule */
     LB_ERR_VARIANT = 4,  /* variant outside LB_AUTO..8, or dtype unknown */
     LB_ERR_OVERFLOW = 5, /* K above the type's limit (the exact int32 sum must fit);
-                            convolutions: also 32-bit offset range */
+                            convolutions: also 32-bit offset range; attention:
+                            more rows or keys than 32-bit numbers reach, or more
+                            rows of one sequence than one launch covers */
     LB_ERR_HIP = 6,      /* the HIP runtime reported an error */
     LB_ERR_WORKSPACE = 7 /* the workspace is smaller than the call needs */
 } lb_status;

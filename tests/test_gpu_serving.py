@@ -836,3 +836,62 @@ def test_attention_keys_next_to_two_to_the_31(nq, Hq, dtype):
     with pytest.raises(lb.LbError):
         b.table = torch.zeros(1, width + 1, dtype=torch.int32, device="cuda")
         b.run(window=window, max_q=nq)
+
+
+# ---------------------------------------------------------------------------
+# more rows, tokens and sequences than one launch holds (2^32 threads)
+# ---------------------------------------------------------------------------
+
+def test_linear_more_rows_than_a_launch_holds():
+    M, N, K = 2 ** 28 + 100, 5, 16
+    x = torch.randn(M, K, dtype=BF, device="cuda")
+    g = gen(1)
+    w, sw = torch.randint(-128, 128, (N, K), generator=g, dtype=torch.int8), torch.rand(N, generator=g) + 0.1
+    bias = torch.randn(N, generator=g).to(BF)
+    out = torch.full((M, N), 7.0, dtype=BF, device="cuda")
+    lb.lb_linear_w8a8(x, w.cuda(), sw.cuda(), out, bias=bias.cuda())
+    rows = torch.cat([torch.arange(300), torch.tensor([2 ** 23 - 1, 2 ** 23, 2 ** 24, 2 ** 24 + 1, 2 ** 28 - 1, 2 ** 28]),
+                      torch.randint(0, M, (3000,), generator=g), torch.arange(M - 300, M)]).cuda()
+    q, sx = quant_ref(x[rows].cpu())
+    check_linear(out[rows], *linear_want(q, w, sx, sw, bias), BF)
+
+
+def test_cache_more_tokens_than_a_launch_holds():
+    T, H, D, page = 16500, 32767, 64, 16
+    if torch.cuda.mem_get_info()[0] < 170 * 2 ** 30:
+        pytest.skip("needs 170 GiB")
+    x = torch.empty(T, H, D, dtype=HF, device="cuda")
+    ends = torch.tensor([0, 1, 8191, 8192, 8193, T - 2, T - 1]).cuda()
+    x[ends] = torch.randn(len(ends), H, D, dtype=HF, device="cuda")
+    slots = torch.full((T,), -1, dtype=torch.int64, device="cuda")
+    slots[ends] = torch.arange(len(ends)).cuda() * 2
+    cache = empty_cache(1, H, page, D, HF)
+    lb.lb_kv4_write(x, x, slots, *cache)
+    small = empty_cache(1, H, page, D, HF)
+    lb.lb_kv4_write(x[ends], x[ends], slots[ends], *small)
+    for a, b in zip(cache, small):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    want = torch.empty(len(ends), H, D, dtype=HF, device="cuda")
+    lb.lb_kv4_read(*small, slots[ends], want, torch.empty_like(want))
+    back = torch.empty_like(x)
+    lb.lb_kv4_read(*cache, slots, x, back)
+    for got in (x, back):
+        assert torch.equal(got[ends], want)
+        assert not got[2:8191].any() and not got[8194:T - 2].any()
+
+
+@pytest.mark.parametrize("max_q", [1, 256])
+def test_attention_more_sequences_than_a_launch_holds(max_q):
+    """2^24 tiles of rows and more; 61 different sequences over and over."""
+    P, H, D = 61, 16, 64
+    B = (2 ** 20 if max_q == 1 else 2 ** 19) + 77
+    b = Batch([1 + i % 16 for i in range(P)], [1] * P, H, H, D, 16, BF, seed=2)
+    want = b.want()
+    of = torch.arange(B, device="cuda") % P
+    q = b.q.cuda()[of].contiguous()
+    out, lse = torch.full_like(q, 5.0), torch.full((B, H), 9.0, device="cuda")
+    lens = torch.tensor(b.lens, dtype=torch.int32).cuda()[of].contiguous()
+    lb.lb_attn_kv4(q, *b.cache, b.table[of].contiguous(), torch.arange(B + 1, dtype=torch.int32, device="cuda"), lens, out,
+                   lse=lse, max_q=max_q, max_len=16)
+    b.check((out[:P], lse[:P]), want)
+    assert torch.equal(out, out[:P][of]) and torch.equal(lse, lse[:P][of])

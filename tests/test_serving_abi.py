@@ -142,3 +142,11 @@ def test_binding_checks_without_a_gpu():
     with pytest.raises(ValueError, match="GPU"):
         lb.lb_attn_kv4(k, c, c, p, p, torch.zeros(1, 2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32),
                        torch.zeros(1, dtype=torch.int32), k)
+
+
+def test_attention_rows_beyond_one_launch(lib):
+    """One sequence is one launch of fewer than 2^32 threads; more than that is refused, not left to the runtime."""
+    a = attn_args()
+    wide = dict(Hq=32767, Hkv=32767, ldq=32767 * 64, ldo=32767 * 64)
+    assert lib.lb_attn_kv4(*a(total_q=2 ** 18, max_q=2 ** 18, **wide)) == lb.LB_ERR_OVERFLOW
+    assert lb.lb_attn_kv4_workspace(2, 2 ** 18, 2 ** 18, 32767, 32767, 64, 100, cu_count=256) == 0
