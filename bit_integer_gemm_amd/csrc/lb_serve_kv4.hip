@@ -3,7 +3,8 @@
 //
 // A vector x (the D numbers of one token and head) is held as levels u[d] in
 // 0..15, a scale s and a minimum m, both in the type T of x:
-//   m = min_d x[d],  s = T((max_d x[d] - m) / 15),
+//   m = min_d x[d],  s = T((max_d x[d] - m) / 15), or T's number before that where
+//                        15 s + m would round to infinity,
 //   u[d] = clamp(round_half_even((x[d] - m) / s), 0, 15)   (0 where s = 0),
 // and stands for u[d] s + m.  A vector that holds an infinity or a NaN, or whose
 // range is beyond fp32, stands for NaN.
@@ -45,7 +46,7 @@ template <int N, class F> __device__ inline float over_lanes(float x, F f)
 // levels unless one lies within 2^-16 of a half-integer; then the correctly rounded
 // quotients decide (a division for every number made the kernel's time that of its
 // vector instructions).  So they do for subnormal scales, whose rounding may put the
-// largest number past 15.5; a normal one puts it below 15.1.  A slot outside the
+// largest number past 15.5; a normal one puts it below 15.2.  A slot outside the
 // cache is not written.
 template <class T, int D>
 __device__ inline void write_vector(const Kv4Cache &c, i32x4 w, int64_t slot, int32_t h, uint32_t sub, uint8_t *levels,
@@ -68,7 +69,12 @@ __device__ inline void write_vector(const Kv4Cache &c, i32x4 w, int64_t slot, in
     }
     lo = over_lanes<LPV>(lo, [](float p, float q) { return fminf(p, q); });
     hi = over_lanes<LPV>(hi, [](float p, float q) { return fmaxf(p, q); });
-    const float s = (float)(T)((hi - lo) / 15.0f);
+    float s = (float)(T)((hi - lo) / 15.0f);
+    // where T's rounding of 15 s + lo becomes infinite (the quotient was rounded up)
+    if (__builtin_fmaf(15.f, s, lo) >= (__is_same(T, __bf16) ? 0x1.FFp127f : 65520.f) && s < __builtin_inff()) {
+        if constexpr (__is_same(T, __bf16)) s = __uint_as_float(__float_as_uint(s) - 0x10000u);
+        else s = lo_f32<T>(pack2<T>(s, 0.f) - 1u);
+    }
     // a NaN, or a range that is not finite
     const uint64_t odds = __ballot(odd) >> ((threadIdx.x & 63u) / LPV * LPV);
     const bool bad = (odds & (((uint64_t)1 << LPV) - 1)) != 0 || !(s < __builtin_inff());

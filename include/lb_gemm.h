@@ -275,7 +275,8 @@ int64_t lb_linear_w8a8_workspace(int64_t M, int64_t K, int64_t N);
  * A paged cache of keys and values in 4 bits.  The D numbers x of one token and
  * key head are held as levels u in 0..15, a scale s and a minimum m, both of the
  * cache's 16-bit type:
- *   m = min x,  s = (max x - m) / 15 (fp32, rounded to the type),
+ *   m = min x,  s = (max x - m) / 15 (fp32, rounded to the type; the type's number
+ *       before that where 15 s + m would round to infinity),
  *   u = (x - m) / s rounded to the nearest integer, ties to even, at most 15
  *       (0 where s = 0),
  * and stand for u s + m.  Numbers that are not finite (or whose range is beyond

@@ -895,3 +895,47 @@ def test_attention_more_sequences_than_a_launch_holds(max_q):
                    lse=lse, max_q=max_q, max_len=16)
     b.check((out[:P], lse[:P]), want)
     assert torch.equal(out, out[:P][of]) and torch.equal(lse, lse[:P][of])
+
+
+# ---------------------------------------------------------------------------
+# the cache at the end of its type
+# ---------------------------------------------------------------------------
+
+def quantise_at_the_end(x):
+    """quantise_ref, with the scale that the cache takes where 15 scales above the minimum would be infinite."""
+    u, scale, low = quantise_ref(x)
+    top = (15 * scale.float() + low.float()).to(x.dtype)
+    down = (scale.view(torch.int16) - 1).view(x.dtype)
+    scale = torch.where(torch.isinf(top) & torch.isfinite(scale), down, scale)
+    s, f = scale.float().numpy(), x.float().numpy()
+    ok = (s > 0) & np.isfinite(s)
+    return np.clip(np.rint(np.divide(f - low.float().numpy(), s, out=np.zeros_like(f), where=ok)), 0, 15), scale, low
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_cache_finite_numbers_stay_finite(dtype, D):
+    """Vectors that reach the type's largest number, whose scale rounded up would stand for infinity."""
+    T, H, page, most = 500, 2, 16, torch.finfo(dtype).max
+    g = gen(D)
+    # (a bf16 range beyond fp32 stands for NaN, as the header says)
+    lo = (torch.rand(T, H, 1, generator=g, dtype=torch.float64) * (0.8 if dtype == BF else 1.6) - (0 if dtype == BF else 0.8)) * most
+    lo[0] = 0
+    x = lo + (most - lo) * torch.rand(T, H, D, generator=g, dtype=torch.float64)
+    x[..., 3:4], x[..., 5] = lo, most
+    x = x.to(dtype)
+    assert torch.isfinite(x).all()
+    cache, slots = empty_cache(T // page + 1, H, page, D, dtype), torch.arange(T).cuda()
+    lb.lb_kv4_write(x.cuda(), x.flip(0).cuda(), slots, *cache)
+    k, v = torch.empty(T, H, D, dtype=dtype, device="cuda"), torch.empty(T, H, D, dtype=dtype, device="cuda")
+    lb.lb_kv4_read(*cache, slots, k, v)
+    u, s, low = quantise_at_the_end(x)
+    down = s != quantise_ref(x)[1]
+    assert down.any() and not down.all()
+    want = (torch.from_numpy(u) * s.float() + low.float()).to(dtype)
+    assert torch.isfinite(want).all()
+    assert torch.equal(k.cpu(), want) and torch.equal(v.cpu(), want.flip(0))
+    # half a level, and a scale off by a step over 15 levels
+    step = s.double() * torch.finfo(dtype).eps * 15
+    off = (k.cpu().double() - x.double()).abs()
+    assert (off <= s.double() / 2 + step + half_step(dtype) * x.double().abs()).all()
