@@ -29,6 +29,7 @@ LB_OK, LB_ERR_NULL, LB_ERR_SHAPE, LB_ERR_ALIGN, LB_ERR_VARIANT, LB_ERR_OVERFLOW,
 LB_S8, LB_S4, LB_B1 = 0, 1, 2
 LB_BF16, LB_F16, LB_F32 = 0, 1, 2   # lb_ftype
 LB_PLAN_LINEAR = 3   # lb_auto_plan's op code for the linear layer
+LB_PLAN_SCALED = 5   # and for the scaled product
 LB_AUTO = -1
 LB_NUM_VARIANTS = 9
 LB_DEFAULT_VARIANT = 7
@@ -270,8 +271,8 @@ def lb_variant_info(dtype: int, variant: int) -> dict:
 
 def lb_auto_plan(op: int, M: int, N: int, K: int, cu_count: int = 0) -> dict:
     """What an LB_AUTO call makes for a shape: the number of launches, the first
-    launch's workgroup tile and its K bands.  op: LB_S8, LB_S4, LB_B1 or
-    LB_PLAN_LINEAR; cu_count <= 0 plans for the current device."""
+    launch's workgroup tile and its K bands.  op: LB_S8, LB_S4, LB_B1,
+    LB_PLAN_LINEAR or LB_PLAN_SCALED; cu_count <= 0 plans for the current device."""
     vals = [ctypes.c_int(0) for _ in range(4)]
     _raise(load().lb_auto_plan(op, M, N, K, cu_count, *[ctypes.byref(v) for v in vals]), "lb_auto_plan")
     return dict(zip(("launches", "tile_m", "tile_n", "k_bands"), (v.value for v in vals)))

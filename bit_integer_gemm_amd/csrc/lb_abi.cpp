@@ -297,10 +297,9 @@ bool lb::variant_is_forced() { return auto_override() >= 0; }
 // 140 x 12000 x 512 7.1 / 8.1; tall ones the same (20000 x 64 x 4096 26.4, the best variant
 // 28.4), K below 512 within a launch's time of each other.  Where tiles of 64 x 64 do run at once: 128 x 8192 x 4096
 // 128 x 64 19.7, those 15.4.
-static int scaled_deep_tile(int64_t M, int64_t N)
+static int scaled_deep_tile(int64_t M, int64_t N, int cu)
 {
-    int cu = 0;
-    if (lb::variant_is_forced() || lb::device_cu_count(&cu) != LB_OK) return -1;
+    if (lb::variant_is_forced() || (cu <= 0 && lb::device_cu_count(&cu) != LB_OK)) return -1;
     auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
     if (tiles(64, 64) <= cu) return -1;
     if (tiles(128, 64) <= cu) return lb::SCALED_128x64;
@@ -308,11 +307,24 @@ static int scaled_deep_tile(int64_t M, int64_t N)
     return tiles(128, 128) <= cu ? lb::SCALED_128x128 : -1;
 }
 
+// The tile of a scaled product that is not one of the linear layer's: a few-row tile or
+// one with a deep ring.  False where the linear layer's launches do.
+static bool scaled_own_tile(int64_t M, int64_t N, int cu, int *tm, int *tn)
+{
+    if (lb::variant_is_forced()) return false;
+    if (cu <= 0 && lb::device_cu_count(&cu) != LB_OK) cu = 0;
+    if (lb::linear_few_tile(M, N, cu > 0 ? cu : 256, tm, tn)) return true;
+    const int deep = cu > 0 ? scaled_deep_tile(M, N, cu) : -1;
+    *tm = deep == lb::SCALED_64x128 ? 64 : 128;
+    *tn = deep == lb::SCALED_128x64 ? 64 : 128;
+    return deep >= 0;
+}
+
 // The scaled product's launches are the linear layer's, but for those tiles.
 int lb::scaled_auto(const int8_t *X, const int8_t *W, const float *sx, const float *sw, void *out, int64_t M,
                     int64_t N, int64_t K, int64_t ldo, const lb::ScaledOut &so, hipStream_t stream)
 {
-    const int deep = scaled_deep_tile(M, N);
+    const int deep = scaled_deep_tile(M, N, 0);
     if (deep >= 0)
         return lb::launch_scaled(deep, X, W, out, sx, sw, M, N, K, ldo, so, stream) == hipSuccess ? LB_OK : LB_ERR_HIP;
     const Plan p = make_plan(lb::KIND_LINEAR, LB_S8, LB_AUTO, M, N, K, K, 0);
@@ -364,10 +376,19 @@ int lb_auto_plan(int op, int64_t M, int64_t N, int64_t K, int cu_count, int *lau
     case LB_S8: kind = lb::KIND_S8; kb = K; break;
     case LB_S4: kind = lb::KIND_S4; kb = K / 2; break;
     case LB_B1: kind = b1_kind(); kb = K / 8; break;
-    case LB_PLAN_LINEAR: kind = lb::KIND_LINEAR; dtype = LB_S8; kb = K; break;
+    case LB_PLAN_LINEAR:
+    case LB_PLAN_SCALED: kind = lb::KIND_LINEAR; dtype = LB_S8; kb = K; break;
     default: return LB_ERR_VARIANT;
     }
     if (kb <= 0) return LB_ERR_SHAPE;
+    int fm = 0, fn = 0;
+    if (op == LB_PLAN_SCALED && scaled_own_tile(M, N, cu_count, &fm, &fn)) {
+        if (launches) *launches = 1;
+        if (tile_m) *tile_m = fm;
+        if (tile_n) *tile_n = fn;
+        if (k_bands) *k_bands = 1;
+        return LB_OK;
+    }
     const Plan p = make_plan(kind, dtype, LB_AUTO, M, N, K, kb, cu_count);
     int bm = 0, bn = 0, bk = 0, st = 0;
     if (lb::mfma_variant_info(kind, p.parts[0].variant, &bm, &bn, &bk, &st) != 0) return LB_ERR_VARIANT;

@@ -61,6 +61,7 @@ hipError_t launch_quant_rows(int ftype, const void *X, int64_t ldx, int8_t *Q, f
                              int64_t K, hipStream_t s);
 // The scaled product where few tiles cover it (linear_is_few).
 bool linear_is_few(int64_t M, int64_t N, int cu);
+bool linear_few_tile(int64_t M, int64_t N, int cu, int *tm, int *tn);   // and the tile it takes there
 hipError_t launch_linear_few(int ftype, const int8_t *Xq, const int8_t *W, const float *sx, const float *sw,
                              const void *bias, void *out, int64_t M, int64_t N, int64_t K, int cu,
                              hipStream_t s);

@@ -408,6 +408,13 @@ static FewShape few_shape(int64_t M, int64_t N, int cu)
     return {0, 0};
 }
 bool linear_is_few(int64_t M, int64_t N, int cu) { return few_shape(M, N, cu).tm != 0; }
+bool linear_few_tile(int64_t M, int64_t N, int cu, int *tm, int *tn)
+{
+    const FewShape f = few_shape(M, N, cu);
+    *tm = f.tm;
+    *tn = f.tn;
+    return f.tm != 0;
+}
 
 template <class T>
 static hipError_t linear_few_t(const int8_t *Xq, const int8_t *W, const float *sx, const float *sw,

@@ -205,7 +205,8 @@ int lb_select_variant(int dtype, int64_t M, int64_t N, int64_t K, int cu_count,
 
 /* The launches an LB_AUTO call makes for a shape, without launching anything
  * (host-only; for tests and tuning).  op: LB_S8, LB_S4 or LB_B1 for the GEMMs,
- * LB_PLAN_LINEAR for the int8 linear layer; M, N, K as for that call.
+ * LB_PLAN_LINEAR for the int8 linear layer, LB_PLAN_SCALED for the scaled product
+ * (lb_gemm_s8_scaled, and lb_linear_w8a8's); M, N, K as for that call.
  * cu_count: compute units to plan for; <= 0 asks the current HIP device (if
  * none answers, the plan is the one a call would make without that
  * information: the default variant, no splits, bands or narrow tiles).
@@ -214,10 +215,12 @@ int lb_select_variant(int dtype, int64_t M, int64_t N, int64_t K, int cu_count,
  * variant's tile, or 256 x 192 / 192 x 256, the four-wave kernel's narrower
  * tiles that an automatic choice of variant 6 takes when its 256x256 grid
  * would fill less than one round of the CUs and the narrower grid still fits
- * in one), and k_bands (K bands of a single launch; 1: none).  Returns
+ * in one; the scaled product's own tiles, 16 to 64 rows by 16 to 64 columns, and
+ * 128 x 64, 64 x 128 and 128 x 128), and k_bands (K bands of a single launch; 1: none).  Returns
  * LB_ERR_SHAPE for a non-positive size (or K below one byte of the type),
  * LB_ERR_VARIANT for an unknown op. */
 #define LB_PLAN_LINEAR 3
+#define LB_PLAN_SCALED 5
 int lb_auto_plan(int op, int64_t M, int64_t N, int64_t K, int cu_count, int *launches,
                  int *tile_m, int *tile_n, int *k_bands);
 

@@ -170,3 +170,11 @@ def test_auto_plan_argument_checks(lib):
     # K below one byte of a packed type
     assert lib.lb_auto_plan(lb.LB_S4, 64, 64, 1, 256, *refs) == lb.LB_ERR_SHAPE
     assert lib.lb_auto_plan(lb.LB_B1, 64, 64, 7, 256, *refs) == lb.LB_ERR_SHAPE
+
+
+def test_scaled_plan_code(lib):
+    text = open(HEADER).read()
+    assert int(re.search(r"#define LB_PLAN_SCALED (\d+)", text).group(1)) == lb.LB_PLAN_SCALED
+    refs = [ctypes.byref(ctypes.c_int(0)) for _ in range(4)]
+    assert lib.lb_auto_plan(lb.LB_PLAN_SCALED, 0, 64, 64, 256, *refs) == lb.LB_ERR_SHAPE
+    assert lib.lb_auto_plan(lb.LB_PLAN_SCALED, 64, 64, 64, 256, None, None, None, None) == lb.LB_OK

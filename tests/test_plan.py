@@ -135,3 +135,23 @@ def test_forcing_a_variant_disables_the_override(forced):
     forced(4)
     assert plan(lb.LB_S4, 4096, 3072, 2048)[1] == tuple(
         lb.lb_variant_info(lb.LB_S4, 4)[k] for k in ("tile_m", "tile_n"))
+
+
+@pytest.mark.parametrize("M,N,K,launches,tile", [
+    (1, 4096, 4096, 1, (16, 16)), (16, 11008, 4096, 1, (16, 48)), (32, 4096, 1024, 1, (32, 16)), (256, 4096, 4096, 1, (64, 64)),
+    (331, 4097, 5504, 1, (128, 64)), (300, 6144, 8192, 1, (64, 128)), (2000, 2048, 4096, 1, (128, 128)),
+    (8192, 1376, 4096, 1, (256, 192)), (2850, 4349, 48, 1, (192, 256)), (4090, 4095, 528, 1, (256, 256)),
+    (8192, 11008, 4096, 2, (256, 256)), (4100, 4100, 48, 1, (64, 64))])
+def test_plan_of_the_scaled_product(M, N, K, launches, tile):
+    """Its own tiles where all of them run at once, else the linear layer's launches."""
+    got = plan(lb.LB_PLAN_SCALED, M, N, K)
+    assert got == (launches, tile, 1)
+    tiles = {(64, 64), (128, 64), (64, 128), (128, 128)}
+    fits = min(cdiv(M, m) * cdiv(N, n) for m, n in tiles) <= CU
+    assert fits or got == plan(lb.LB_PLAN_LINEAR, M, N, K)
+
+
+def test_plan_of_the_scaled_product_when_forced(forced):
+    forced(0)
+    for M, N, K in ((1, 4096, 4096), (331, 4097, 5504), (4090, 4095, 528)):
+        assert plan(lb.LB_PLAN_SCALED, M, N, K) == plan(lb.LB_PLAN_LINEAR, M, N, K) == (1, (64, 64), 1)
