@@ -939,3 +939,47 @@ def test_cache_finite_numbers_stay_finite(dtype, D):
     step = s.double() * torch.finfo(dtype).eps * 15
     off = (k.cpu().double() - x.double()).abs()
     assert (off <= s.double() / 2 + step + half_step(dtype) * x.double().abs()).all()
+
+
+# ---------------------------------------------------------------------------
+# the scaled product's large tiles
+# ---------------------------------------------------------------------------
+
+LARGE = [(4090, 4095, 528, 1, (256, 256)), (4096, 4096, 528, 1, (256, 256)),     # one round of them
+         (4692, 8190, 1040, 2, (256, 256)), (4692, 8192, 1040, 2, (256, 256)),   # whole rounds, then the last rows
+         (8190, 5038, 1040, 2, (256, 256)), (8190, 5036, 1040, 2, (256, 256)),   # whole rounds, then the last columns
+         (2850, 4349, 48, 1, (192, 256)), (2850, 4348, 48, 1, (192, 256)),
+         (4349, 2850, 48, 1, (256, 192)), (4349, 2852, 48, 1, (256, 192)),
+         (4100, 4101, 48, 1, (64, 64)), (8192, 11005, 48, 1, (128, 128))]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FL])
+@pytest.mark.parametrize("M,N,K,launches,tile", LARGE)
+def test_scaled_product_large_tiles(M, N, K, launches, tile, dtype):
+    """Every launch that the linear layer's rules give the scaled product, unforced, with bias and edges."""
+    plan = lb.lb_auto_plan(lb.LB_PLAN_SCALED, M, N, K, 256)
+    assert (plan["launches"], plan["tile_m"], plan["tile_n"]) == (launches, *tile)
+    if torch.cuda.get_device_properties(0).multi_processor_count != 256:
+        pytest.skip("planned for 256 compute units")
+    g = gen(M + N)
+    x = torch.randint(-128, 128, (M, K), generator=g, dtype=torch.int8).cuda()
+    w = torch.randint(-128, 128, (N, K), generator=g, dtype=torch.int8).cuda()
+    sx, sw = (torch.rand(M, generator=g) * 1e-2).cuda(), (torch.rand(N, generator=g) * 1e-3).cuda()
+    prod = torch.mm(x.double(), w.double().t().contiguous()) * sx.double()[:, None] * sw.double()
+    for bias in (None, torch.randn(N, generator=g).to(dtype).cuda()):
+        flat = torch.full((M * N + 64,), 7.0, dtype=dtype, device="cuda")
+        lb.lb_gemm_s8_scaled(x, w, sx, sw, flat[:M * N].view(M, N), bias=bias)
+        want = prod if bias is None else prod + bias.double()
+        # as check_linear
+        tol = (half_step(dtype) + 2 * STEP) * want.abs() + 5 * STEP * prod.abs()
+        tol = tol * 1.001 + torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps
+        assert ((flat[:M * N].view(M, N).double() - want).abs() <= tol).all()
+        assert (flat[M * N:] == 7).all(), "write past out"
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FL])
+def test_linear_layer_in_two_launches(dtype):
+    """The whole layer, rows quantised, by columns in two launches."""
+    M, N, K = 8190, 5038, 1040
+    assert lb.lb_auto_plan(lb.LB_PLAN_SCALED, M, N, K, 256)["launches"] == 2
+    test_linear(dtype, M, N, K)
