@@ -230,8 +230,10 @@ int lb_auto_plan(int op, int64_t M, int64_t N, int64_t K, int cu_count, int *lau
  * one floating type, an lb_ftype (a 16-bit one for the cache and the attention).
  * Conventions as above (device pointers, caller-owned buffers, asynchronous on
  * the stream, statuses; nothing is allocated or kept between calls), and:
- *   - every data pointer is 16-byte aligned, and strides between rows or tokens
- *     are in elements and keep rows 16-byte aligned (LB_ERR_ALIGN otherwise);
+ *   - matrices, biases, sw, keys, values and the cache are 16-byte aligned, and
+ *     strides between rows or tokens are in elements and keep rows 16-byte
+ *     aligned (LB_ERR_ALIGN otherwise); sx, slots, table, q_off, lens and lse may
+ *     start at any element;
  *   - a workspace is scratch memory of the caller, 256-byte aligned, whose
  *     contents need not survive between calls; two calls that may run at the
  *     same time need one each.

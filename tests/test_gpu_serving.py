@@ -983,3 +983,59 @@ def test_linear_layer_in_two_launches(dtype):
     M, N, K = 8190, 5038, 1040
     assert lb.lb_auto_plan(lb.LB_PLAN_SCALED, M, N, K, 256)["launches"] == 2
     test_linear(dtype, M, N, K)
+
+
+# ---------------------------------------------------------------------------
+# scales, slots, lengths and offsets that start anywhere
+# ---------------------------------------------------------------------------
+
+def shifted(t, by=1):
+    """The same values, `by` elements into an allocation, with NaN or the type's largest before and after."""
+    far = float("nan") if t.is_floating_point() else torch.iinfo(t.dtype).max
+    wide = torch.full((t.numel() + 16,), far, dtype=t.dtype, device="cuda")
+    wide[by:by + t.numel()] = t.reshape(-1).cuda()
+    return wide[by:by + t.numel()].view(t.shape)
+
+
+@pytest.mark.parametrize("by", [1, 2, 3])
+@pytest.mark.parametrize("M,N,K", [(5, 48, 64), (331, 4097, 272), (2850, 4349, 48), (4090, 4095, 528), (4692, 8190, 1040)])
+def test_row_scales_start_anywhere(M, N, K, by):
+    g = gen(M)
+    x = torch.randint(-128, 128, (M, K), generator=g, dtype=torch.int8).cuda()
+    w = torch.randint(-128, 128, (N, K), generator=g, dtype=torch.int8).cuda()
+    sx, sw = torch.rand(M, generator=g).cuda(), torch.rand(N, generator=g).cuda()
+    want, got = (torch.empty(M, N, dtype=BF, device="cuda") for _ in range(2))
+    lb.lb_gemm_s8_scaled(x, w, sx, sw, want)
+    lb.lb_gemm_s8_scaled(x, w, shifted(sx, by), sw, got)
+    assert torch.equal(got, want)
+    f, q = torch.randn(M, K, generator=g).to(BF).cuda(), torch.empty_like(x)
+    lb.lb_quant_rows_s8(f, q, sx)
+    moved, again = shifted(sx, by), torch.empty_like(q)
+    moved.zero_()
+    lb.lb_quant_rows_s8(f, again, moved)
+    assert torch.equal(q, again) and torch.equal(moved, sx)
+
+
+@pytest.mark.parametrize("nq,n", [(1, 90), (1, 4000), (70, 300)])
+def test_numbers_of_the_cache_start_anywhere(nq, n):
+    b = Batch([n, 5], [nq, 3], 8, 2, 64, 16, BF, seed=nq)
+    want = b.run(max_q=max(nq, 3))
+    b.q_off, b.table = shifted(b.q_off), shifted(b.table.contiguous(), 3)
+    lens = shifted(torch.tensor(b.lens, dtype=torch.int32), 1)
+    q = b.q.cuda()
+    out, lse = torch.empty_like(q), shifted(torch.empty(b.total, 8))
+    lb.lb_attn_kv4(q, *b.cache, b.table, b.q_off, lens, out, lse=lse, max_q=max(nq, 3))
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    k, v = torch.empty(len(b.slots), 2, 64, dtype=BF, device="cuda"), torch.empty(len(b.slots), 2, 64, dtype=BF, device="cuda")
+    k2, v2 = torch.empty_like(k), torch.empty_like(v)
+    lb.lb_kv4_read(*b.cache, b.slots, k, v)
+    lb.lb_kv4_read(*b.cache, shifted(b.slots), k2, v2)
+    assert torch.equal(k, k2) and torch.equal(v, v2)
+    old = [t.clone() for t in b.cache]
+    lb.lb_kv4_write(k, v, b.slots, *b.cache)
+    mid = [t.clone() for t in b.cache]
+    for t, o in zip(b.cache, old):
+        t.copy_(o)
+    lb.lb_kv4_write(k, v, shifted(b.slots), *b.cache)
+    for t, o in zip(b.cache, mid):
+        assert torch.equal(t.view(torch.uint8), o.view(torch.uint8))
