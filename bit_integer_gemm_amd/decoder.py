@@ -65,30 +65,37 @@ class Attention:
         return out, qkv, mixed
 
 
-def reference(layer, x, cache, b, n):
-    """In 64 bits: the projection of sequence b's newest tokens x, and the n keys and values that the
-    cache holds for it."""
-    G, D = layer.kv_heads, layer.D
+def linear(x, w, sw, bias=None):
+    """The int8 linear layer of x (T, K) in 64 bits."""
     x = x.cpu().double()
     amax = x.abs().amax(1, keepdim=True)
-    qkv = (127 * x / amax).round() @ layer.qkv.cpu().double().T * (amax / 127) * layer.qkv_s.cpu().double()
-    qkv += layer.bias.cpu().double()
+    y = (127 * x / amax.clamp(min=1e-300)).round() @ w.cpu().double().T * (amax / 127) * sw.cpu().double()
+    return y if bias is None else y + bias.cpu().double()
+
+
+def held(cache, b, n):
+    """What the cache holds for the n first tokens of sequence b, level * scale + minimum in 64 bits: keys and values
+    (n, heads, D), and the largest scale of a key."""
     pos = torch.arange(n, device=cache.table.device)
-    K = torch.empty(n, G, D, dtype=layer.bias.dtype, device=pos.device)
-    V = torch.empty_like(K)
-    lb.lb_kv4_read(*cache.tensors, cache.slots(torch.full_like(pos, b), pos), K, V)
-    return qkv, K.cpu().double(), V.cpu().double()
+    page, at = cache.table[b].long()[pos // cache.page], pos % cache.page
+    found = []
+    for levels, numbers in (cache.tensors[0::2], cache.tensors[1::2]):
+        byte, (scale, low) = levels[page, :, at].cpu(), numbers[page, :, at].cpu().double().unbind(-1)
+        u = torch.stack([byte & 15, byte >> 4], -1).flatten(-2).double()
+        found.append(u * scale[..., None] + low[..., None])
+    return (*found, float(cache.tensors[2][page, :, at, 0].float().max()))
 
 
 def attend(q, K, V):
-    """Causal attention of the last queries q (T, H, D) over K, V (n, G, D), float64."""
+    """Causal attention of the last queries q (T, H, D) over K, V (n, G, D), float64, and the largest score of
+    each query and head in magnitude (T, H, 1)."""
     T, H, D = q.shape
     n, G, _ = K.shape
     K, V = (a.repeat_interleave(H // G, 1).transpose(0, 1).contiguous() for a in (K, V))
     s = torch.matmul(q.transpose(0, 1), K.transpose(1, 2)) / math.sqrt(D)
     hidden = torch.arange(n)[None, :] > torch.arange(n - T, n)[:, None]
     p = s.masked_fill(hidden, -math.inf).softmax(-1)
-    return torch.matmul(p, V).transpose(0, 1)
+    return torch.matmul(p, V).transpose(0, 1), s.masked_fill(hidden, 0).abs().amax(-1).T[..., None]
 
 
 def run(hidden=4096, heads=32, kv_heads=8, D=128, prompts=(777, 1, 130, 600), steps=8, dtype=torch.bfloat16):
@@ -106,9 +113,9 @@ def run(hidden=4096, heads=32, kv_heads=8, D=128, prompts=(777, 1, 130, 600), st
     pos = torch.cat([torch.arange(n) for n in prompts]).to(dev)
     lens = torch.tensor(prompts, dtype=torch.int32, device=dev)
     args = (x, cache, seq, pos, off.to(torch.int32).to(dev), lens, max(prompts), longest)
-    _, qkv, mixed = layer(*args)
+    out, qkv, mixed = layer(*args)
     for b, n in enumerate(prompts):
-        check(layer, cache, b, n, x[off[b]:off[b + 1]], qkv[off[b]:off[b + 1]], mixed[off[b]:off[b + 1]])
+        check(layer, cache, b, n, *(a[off[b]:off[b + 1]] for a in (x, qkv, mixed, out)))
     prefill = clock(lambda: layer(*args), 20)
 
     # single tokens: one graph, whose inputs and lengths move on the GPU
@@ -135,28 +142,35 @@ def run(hidden=4096, heads=32, kv_heads=8, D=128, prompts=(777, 1, 130, 600), st
             lens.add_(1)
         graph.replay()
         for b, n in enumerate(prompts):
-            check(layer, cache, b, n + i + 1, one[b:b + 1], qkv[b:b + 1], mixed[b:b + 1])
+            check(layer, cache, b, n + i + 1, *(a[b:b + 1] for a in (one, qkv, mixed, out)))
     return prefill, clock(step, 50), clock(graph.replay, 50)
 
 
-def check(layer, cache, b, n, x, qkv, mixed):
-    """One call's projection and attention of sequence b against the formulas."""
+def check(layer, cache, b, n, x, qkv, mixed, out):
+    """One call's projections, cache and attention of sequence b against the formulas, each from what the step before
+    it left."""
     H, G, D = layer.heads, layer.kv_heads, layer.D
     T, eps, tiny = x.shape[0], torch.finfo(x.dtype).eps, torch.finfo(x.dtype).tiny
-    want, K, V = reference(layer, x, cache, b, n)
-    # one rounding of the output, and fp32 scales, product and bias before it
-    bias = layer.bias.cpu().double()
-    bound = eps / 2 * (want.abs() + tiny) + 2 ** -21 * ((want - bias).abs() + bias.abs())
-    assert ((qkv.cpu().double() - want).abs() <= bound).all(), "projection"
+    for name, got, want, bias in (
+            ("projection", qkv, linear(x, layer.qkv, layer.qkv_s, layer.bias), layer.bias.cpu().double()),
+            ("output projection", out, linear(mixed.reshape(T, H * D), layer.o, layer.o_s), torch.zeros(1).double())):
+        # one rounding of the output, and fp32 scales, product and bias before it
+        bound = eps / 2 * (want.abs() + tiny) + 2 ** -21 * ((want - bias).abs() + bias.abs())
+        assert ((got.cpu().double() - want).abs() <= bound).all(), name
+    K, V, largest = held(cache, b, n)
     kv = qkv.view(T, H + 2 * G, D)[:, H:].cpu().double()
-    for new, held in ((kv[:, :G], K[n - T:]), (kv[:, G:], V[n - T:])):
-        # half a level and the scale's rounding over 15 levels; one rounding each of minimum and result
+    for new, kept in ((kv[:, :G], K[n - T:]), (kv[:, G:], V[n - T:])):
+        # half a level, and the scale's rounding over 15 levels
         span = new.amax(-1, keepdim=True) - new.amin(-1, keepdim=True)
-        assert ((new - held).abs() <= span / 30 + eps * span + eps * new.abs().amax(-1, keepdim=True)).all(), "cache"
+        assert ((new - kept).abs() <= span / 30 + eps * span + tiny).all(), "cache"
     q = qkv.view(T, H + 2 * G, D)[:, :H].cpu().double()
-    # the output's rounding, and that of what is read back (K moves the scores by |q| |K| eps/2 sqrt(D) at most)
-    bound = 4 * eps * (1 + q.norm(dim=-1).amax() * K.norm(dim=-1).amax() / math.sqrt(D)) * V.abs().amax()
-    assert ((mixed.cpu().double() - attend(q, K, V)).abs() <= bound).all(), "attention"
+    want, top = attend(q, K, V)
+    # A score: D/32 products of 32 terms, about 8 rounded steps of partial sums up to 143 sum |q| each, and six more of
+    # its own; the output's rounding; weights and values to 2^-10 of the weighted values' magnitudes.
+    score = (D / 32 + 8) * 143 * 2 ** -23 * q.abs().sum(-1, keepdim=True) * largest / math.sqrt(D) + 6 * 2 ** -24 * (top + 1)
+    mean = attend(q, K, V.abs().amax(-1, keepdim=True).expand_as(V))[0]
+    bound = eps / 2 * (want.abs() + tiny) + (2 * score + 2 ** -10) * mean
+    assert ((mixed.cpu().double() - want).abs() <= bound).all(), "attention"
 
 
 def clock(f, n):
