@@ -321,12 +321,17 @@ int lb_kv4_read(const uint8_t *Kc, const uint8_t *Vc, const void *Kp, const void
  * none (an empty sequence, a position before the first key) gets zeros, and
  * -infinity in lse.  lse (total_q x Hq fp32, or NULL): log of the sum of
  * exp(scale * q . k).  scale multiplies the scores.
+ * Scores, weights and their sums are fp32; weights and values go into the products
+ * to at least 2^-12 of each weight and of each value vector's |m| + 16 s, for
+ * values of magnitudes between 2^-100 and 2^100 (sums of larger ones may leave
+ * fp32's range), whatever else a row does not see.
  * Keys whose page number lies outside the cache are not seen; lens beyond the
  * table's width count as its width.  Rows of Q outside every sequence are left
  * as they are.
  *   max_q, max_len: at least the longest nq (LB_ERR_SHAPE if below 1; rows past
- *   it may be left as they are) and, for the planning alone, about the longest
- *   lens.  workspace: partial results where the keys of few rows are split over
+ *   it may be left as they are; it also chooses the kernel, so that 1 for single
+ *   tokens is four times as fast as a bound of 64) and, for the planning alone,
+ *   about the longest lens.  workspace: partial results where the keys of few rows are split over
  *   workgroups; with fewer than lb_attn_kv4_workspace() bytes (0 and NULL too)
  *   fewer parts are made, or none.  Parts are joined in a fixed order: the same
  *   arguments give the same bits.
