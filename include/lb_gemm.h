@@ -321,10 +321,11 @@ int lb_kv4_read(const uint8_t *Kc, const uint8_t *Vc, const void *Kp, const void
  * none (an empty sequence, a position before the first key) gets zeros, and
  * -infinity in lse.  lse (total_q x Hq fp32, or NULL): log of the sum of
  * exp(scale * q . k).  scale multiplies the scores.
- * Scores, weights and their sums are fp32; weights and values go into the products
- * to at least 2^-12 of each weight and of each value vector's |m| + 16 s, for
- * values of magnitudes between 2^-100 and 2^100 (sums of larger ones may leave
- * fp32's range), whatever else a row does not see.
+ * Scores, weights and their sums are fp32.  Weights and values go into the products
+ * off by at most 2^-12 of each weight and 2^-11 of each value vector's |m| + 16 s,
+ * and weights too light for that by no more than 2^-10 of the row's largest output
+ * together, whatever other keys hold; for values between 2^-90 and 2^90 in
+ * magnitude (sums of larger ones may leave fp32's range).
  * Keys whose page number lies outside the cache are not seen; lens beyond the
  * table's width count as its width.  Rows of Q outside every sequence are left
  * as they are.

@@ -1039,3 +1039,13 @@ def test_numbers_of_the_cache_start_anywhere(nq, n):
     lb.lb_kv4_write(k, v, shifted(b.slots), *b.cache)
     for t, o in zip(b.cache, mid):
         assert torch.equal(t.view(torch.uint8), o.view(torch.uint8))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("power", [-90, 90])
+@pytest.mark.parametrize("nqs", [[1, 1], [5, 3], [120, 90]])
+def test_attention_values_at_the_ends_of_their_range(D, power, nqs):
+    b = Batch([900, 300], nqs, 6, 2, D, 16, BF, seed=D)
+    for seq, n in enumerate(b.lens):
+        refill(b, torch.randn(n, 2, D, generator=gen(seq)).to(BF), (torch.randn(n, 2, D, generator=gen(9)) * 2.0 ** power).to(BF), seq)
+    check_weighted(b, b.run(max_q=max(nqs)), b.want())
