@@ -1096,15 +1096,6 @@ __device__ __forceinline__ int32_t chunk_rows(const AttnArgs &a, char *smem, con
             }
         }
     };
-    // From here on what was fetched is used: without it the compiler turns numbers, and
-    // so waits for them, right where they are asked for (573 against 544 us).
-    auto fetched = [&] {
-#pragma unroll
-        for (int j = 0; j < KH; ++j) asm volatile("" : "+v"(kw[j]));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(vw[i]));
-        asm volatile("" : "+v"(kpw), "+v"(vpw));
-    };
     // Turning, in units of one 16-byte write: word j of the keys, the per-key
     // numbers, dim j of the values.
     auto turn_key_word = [&](int j, char *kbuf) {
@@ -1364,7 +1355,6 @@ __device__ __forceinline__ int32_t chunk_rows(const AttnArgs &a, char *smem, con
 #pragma unroll
         for (int x = 0; x < RX; ++x) l_run[x].add(sum[x]);
         // the values' product, beside the turning of what comes next
-        fetched();
 #pragma unroll
         for (int st = 0; st < VSTEPS; ++st) {
             const int d = st % ND, q = st / ND;
