@@ -18,9 +18,9 @@ namespace lb {
 // each, of a key and its value; a workgroup takes neighbouring tokens of one head,
 // whose levels lie next to each other in the cache where their slots do, and the
 // next workgroup the next head of the same tokens, whose numbers lie next to theirs.
-// 32768 tokens of 8 heads of 128 in bf16 are written in 54 us, 3.1 TB/s (its vector
-// instructions, 440 a wave, stand beside the latency of the slots and then of the
-// numbers); 40000 are read back in 40.5 us, 5.1 TB/s, what a copy reaches.  A few tokens
+// 32768 tokens of 8 heads of 128 in bf16 are written in 53 us, 3.2 TB/s, bound by its
+// vector instructions (2.95e7, 450 a wave; at 4 cycles each on 1024 SIMDs of 2.1 GHz
+// 55 us); 40000 are read back in 40.0 us, 5.1 TB/s, what a copy reaches.  A few tokens
 // take the latency of a launch, 3.5 and 2.8 us.
 
 // slot / page by a multiplication (page_mul is 2^(32 + page_shift) / page rounded up).
@@ -229,11 +229,14 @@ hipError_t launch_kv4_read(int ftype, const Kv4Cache &c, const int64_t *slots, v
 // and the first sum runs on the matrix cores with the levels exact in T.  A
 // nibble becomes a T by writing it into the mantissa of a power of two,
 // B + u (bf16: B = 128, fp16: B = 64): one AND-OR for two nibbles, and a
-// constant to take off, -B sum_d q[d], which is the accumulator's start.
+// constant to take off, -B sum_d q[d], which is the accumulator's start.  (The fp32 sums
+// are then of numbers up to 10 times the levels', and so are their roundings: 7e-6 of
+// a score at most in 65536 ordinary keys, where the plain sum's are 1e-6.)
 // The values are summed the same way with the weights carrying the scale:
 //   sum_t p[t] v[t,d] = sum_t (p[t] s[t]) u[t,d] + sum_t p[t] m[t].
-// The weight p s goes in two bf16 parts (16 bits in all, with fp32's range, which
-// fp16 scales or weights would not have), and the sum of both parts, by one more
+// The weight p s goes in two bf16 parts (16 bits in all, off by 2^-17, with fp32's
+// range, which fp16 scales or weights would not have; over 131072 keys outputs are
+// off by 5e-5 before their rounding, a tenth of fp16's half step), and the sum of both parts, by one more
 // product with ones, takes off what the nibbles' power of two adds.
 template <class T> struct Mfma;
 // A constant kept in a vector register: AND-OR takes one scalar operand, and with
@@ -408,9 +411,9 @@ struct LongSum {
 //             one MFMA per dim.  It ends with dims (4c+i) D/16 + j of row r.
 // Neither the weights nor the values change lanes, and nothing passes through LDS.
 // Bound by the cache's bytes where keys are many: 8 heads of 128 of two sequences of
-// 131072 keys (285 MB) in 57 us, 5.0 TB/s, what a copy reaches; by latency where they
-// are few: one sequence of 777 keys 11.2 us, 12 sequences of 5 queries over windows
-// of 1024 keys, 32 heads of 64, 15.6 us.
+// 131072 keys (285 MB) in 58 us, 4.9 TB/s, what a copy reaches; by latency where they
+// are few: one sequence of 777 keys 11.3 us, 12 sequences of 5 queries over windows
+// of 1024 keys, 32 heads of 64, 15.0 us.
 // The next block's keys are asked for as soon as this one's are multiplied, its
 // values as soon as this one's are, into the same registers, and the numbers of
 // its pages a block earlier.  (Two blocks' worth of registers cost more in waves
@@ -740,7 +743,7 @@ template <class T, int D> __global__ __launch_bounds__(256) void attn_rows_join_
 // their parts, the one that continues from the share before in part 2 i, the one that
 // goes on in the next in 2 i + 1; the workgroup that ends a cut tile notes where it
 // started, for attn_flat_join_kernel.  (64 sequences of 1 to 8191 keys, 8 heads of 128,
-// 286 MB: 66 us, 4.3 TB/s, and 5 us for the join.)
+// 286 MB: 67 us, 4.3 TB/s, and 5 us for the join.)
 enum { FLAT_COST = 14, FLAT_LEAST = 24, FLAT_BATCH = ATTN_FLAT_BATCH };
 template <class T, int D>
 __global__ __launch_bounds__(256, D == 256 ? 2 : 3) void attn_flat_kernel(AttnArgs a)
@@ -902,10 +905,11 @@ __global__ __launch_bounds__(256) void attn_flat_join_kernel(AttnArgs a)
 // read, counted, where rows padded by 16 bytes took 8 (and every write 8).
 //
 // 32 heads over 8 of 128, 700 to 2048 queries of three sequences of up to 8192 keys,
-// bf16: 477 us, 755 TFLOP/s, 62% of what a large bf16 product reaches.  The matrix
+// bf16: 476 us, 757 TFLOP/s, 62% of what a large bf16 product reaches (calls back to
+// back; the first ones after a pause, at a lower clock, take up to 540).  The matrix
 // cores are busy for 166 us of it, the vector ALUs for about 300 (two fused
 // multiply-adds, an exponential, a maximum and a sum for each score, besides the
-// turning), reads of LDS for about 230; a wave waits 30% of its time.
+// turning), reads of LDS for about 230; a wave waits 29% of its time.
 //
 // The values' product goes one of two ways:
 //   whole   values are made whole, u s + m, in fp16 scaled by one power of two for
@@ -913,13 +917,14 @@ __global__ __launch_bounds__(256) void attn_flat_join_kernel(AttnArgs a)
 //           2^10, and weights are fp16: both are off by 2^-12, an eighth of a bf16
 //           output's own rounding.  The reference of a row's weights lies 9 octaves below
 //           its largest score (at 13 the reference is taken anew more often, 495 us; at 7,
-//           475), so that weights down to 2^-23 of the largest keep that precision.  A
+//           477), so that weights down to 2^-23 of the largest keep that precision.  A
 //           lighter one is off by 2^-25 in these units, and n of them by n 2^-14 of a
 //           value: where a row's outputs are not 2^10 times that (a heavy key whose own
 //           value is nothing beside many light ones), the workgroup starts again with the
-//           levels.
+//           levels (1100 us where all of them do; scores of three and six times the
+//           ordinary spread do not: 500 and 512).
 //   levels  levels stay exact and the weights p s go in two bf16 parts, as in
-//           attn_rows_kernel, with fp32's range; 650 us where the other way takes 479.
+//           attn_rows_kernel, with fp32's range; 656 us where the other way takes 477.
 // fp16 outputs take the levels: the other way would be as coarse as they are.  For bf16
 // a pass over the scales of the workgroup's keys decides (value_scale): some row may not
 // see the largest value, so whole values have to hold the smallest beside it, and
@@ -1172,7 +1177,8 @@ __device__ __forceinline__ int32_t chunk_rows(const AttnArgs &a, char *smem, con
     // A step is fenced, so that its read goes out PF steps before its products: left
     // to itself the compiler waits for each read where it stands.  The first PF reads
     // are start_products', some way ahead; the last PF steps make room for the
-    // caller's next ones, after(0 .. PF - 1).  (Both inside products: 544 against 516 us.)
+    // caller's next ones, after(0 .. PF - 1).  (Both right before their products: 480
+    // against 477 us, fp16 665 against 656; D = 64 382 against 387.)
     constexpr int STEPS = 4 * KW, PF = 3;
     i32x4 kf[PF + 1], qr[2][RX];
     auto read_key = [&](const char *kbuf, int st) {
@@ -1447,7 +1453,7 @@ __global__ __launch_bounds__(512, 2) void attn_chunk_kernel(AttnArgs a)
     // The tiles that see the most keys start first: the last of a sequence, and of
     // several sequences (up to 512 tiles) this workgroup's place in the order of
     // their keys, which each finds for itself.  (3 x 2048 queries over up to 8192
-    // keys, then 533 us; the last tile of every sequence first, and so on, 618.)
+    // keys 477 us; the last tile of every sequence first, and so on, 574.)
     const int32_t place = (int32_t)(blockIdx.x / (uint32_t)a.c.heads), h = (int32_t)(blockIdx.x % (uint32_t)a.c.heads);
     const int32_t tasks = a.batch * a.tiles;
     int32_t b = place % a.batch, tile = a.tiles - 1 - place / a.batch;
