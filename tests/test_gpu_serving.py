@@ -706,13 +706,11 @@ def largest_seen(b, window=0):
     return torch.tensor(rows, dtype=torch.float64)[:, None, None]
 
 
-@pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("D", [64, 128, 256])
-@pytest.mark.parametrize("times", [2.0 ** 10, 2.0 ** 20, 2.0 ** 23, 2.0 ** 36, 1e30])
+@pytest.mark.parametrize("dtype,times", [(HF, 2.0 ** 10), (BF, 2.0 ** 10), (BF, 2.0 ** 20), (BF, 2.0 ** 23), (BF, 2.0 ** 36),
+                                         (BF, 1e30)])
 def test_attention_prompt_large_value_that_only_some_rows_see(dtype, D, times):
     """A vector of values far above the others: the rows before it come out as if it were not there."""
-    if dtype == HF and times > 2.0 ** 10:
-        pytest.skip("beyond the type")
     b = Batch([700, 260], [200, 100], 8, 2, D, 48, dtype, seed=D)
     k, v = torch.randn(700, 2, D, generator=gen(1)).to(dtype), torch.randn(700, 2, D, generator=gen(2)).to(dtype)
     v[650] = (v[650].float() * times).to(dtype)
@@ -777,13 +775,11 @@ def check_weighted(b, got, want, scale=None):
     assert ((got[1].cpu().double() - wlse).abs() <= score + 2.0 ** -20 * (1 + wlse.abs())).all()
 
 
-@pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("D", [64, 128, 256])
-@pytest.mark.parametrize("octaves", [5, 24.4, 25.2, 27.5, 31, 36])
+@pytest.mark.parametrize("dtype,octaves", [(HF, 5), (HF, 24.4)] + [(BF, o) for o in (5, 24.4, 25.2, 27.5, 31, 36)])
 def test_attention_prompt_light_keys_beside_a_heavy_one(dtype, D, octaves):
-    """One key takes nearly all the weight and has no value: the output is what the many others add."""
-    if dtype == HF and octaves > 25:
-        pytest.skip("the output is below the type's normal numbers")
+    """One key takes nearly all the weight and has no value: the output is what the many others add (in fp16 as long
+    as that is a normal number)."""
     n, nq = 20000, 64
     b = Batch([n], [nq], 4, 1, D, 16, dtype, seed=D)
     k = torch.full((n, 1, D), -octaves * math.log(2) / math.sqrt(D))
