@@ -39,6 +39,13 @@ K_MAX = {LB_S8: 131071, LB_S4: 131071, LB_B1: 134217600}
 # default, sums in fp32, exact to 2^24; the int8 route, LB_B1_ROUTE=int8, sums 64
 # per pair in int32); longer K runs as K bands (see the header).
 B1_PASS_K = {"fp4": 1 << 24, "int8": 33554304}
+LB_ROPE_HALF, LB_ROPE_PAIRS = 0, 1   # lb_rope_layout
+LB_ROPE_PLAIN, LB_ROPE_LINEAR, LB_ROPE_BASE, LB_ROPE_PARTS, LB_ROPE_BANDS = range(5)   # lb_rope_scaling
+W4_GROUPS = (32, 64, 128)
+W4_K_MAX = 1048576
+NORM_H_MAX = 32768
+MOE_EXPERTS_MAX = 1024
+MOE_TOP_MAX = 64
 KV4_PAGE_ALIGN = 16
 KV4_HEAD_DIMS = (64, 128, 256)
 CONV_C_ALIGN = {LB_S8: 16, LB_S4: 32}
@@ -48,7 +55,8 @@ EXPORTS = ("lb_gemm_s8", "lb_gemm_s4", "lb_gemm_b1", "lb_gemm_s8_linear", "lb_co
            "lb_conv2d_s4", "lb_select_variant", "lb_status_string", "lb_variant_info",
            "lb_build_id", "lb_auto_plan", "lb_quant_rows_s8", "lb_gemm_s8_scaled", "lb_linear_w8a8",
            "lb_linear_w8a8_workspace", "lb_kv4_write", "lb_kv4_read", "lb_attn_kv4",
-           "lb_attn_kv4_workspace")
+           "lb_attn_kv4_workspace", "lb_residual_norm", "lb_rope", "lb_rope_freqs", "lb_linear_w4",
+           "lb_linear_w4_workspace", "lb_moe_w4", "lb_moe_w4_workspace")
 
 
 class LbError(RuntimeError):
@@ -108,8 +116,18 @@ def load(path: str = LIB_PATH):
                                 [ctypes.c_float, i64, i32, i32, p, i64, p])
     lib.lb_attn_kv4_workspace.argtypes = [i64] * 8 + [i32]
     lib.lb_attn_kv4_workspace.restype = i64
+    f32, f64 = ctypes.c_float, ctypes.c_double
+    lib.lb_residual_norm.argtypes = [p, i64, p, i64, p, p, i64, p, p, i64, p, i64, i64, i64, f32, f32, i32, i32, p]
+    lib.lb_rope_freqs.argtypes = [ctypes.POINTER(f64), ctypes.POINTER(f32), i64, f64, i32] + [f64] * 4
+    lib.lb_rope.argtypes = [p, i64, p, i64, p, p, p, i64, p, i64] + [i64] * 5 + [i32, f32, i32, p]
+    lib.lb_linear_w4.argtypes = [p, i64, p, p, p, p] + [i64] * 4 + [i32, p, i64, p]
+    lib.lb_linear_w4_workspace.argtypes = [i64] * 4
+    lib.lb_linear_w4_workspace.restype = i64
+    lib.lb_moe_w4.argtypes = [p, i64] + [p] * 8 + [i64] * 6 + [i32, f32, i32, p, i64, p]
+    lib.lb_moe_w4_workspace.argtypes = [i64] * 5
+    lib.lb_moe_w4_workspace.restype = i64
     for name in ("lb_quant_rows_s8", "lb_gemm_s8_scaled", "lb_linear_w8a8", "lb_kv4_write", "lb_kv4_read",
-                 "lb_attn_kv4"):
+                 "lb_attn_kv4", "lb_residual_norm", "lb_rope_freqs", "lb_rope", "lb_linear_w4", "lb_moe_w4"):
         getattr(lib, name).restype = i32
     _lib = lib
     return lib
@@ -297,8 +315,8 @@ class _Torch:
     def __init__(self):
         import torch
         self.torch = torch
-        self.i8, self.u8, self.i32, self.i64, self.f32 = (torch.int8, torch.uint8, torch.int32, torch.int64,
-                                                          torch.float32)
+        self.i8, self.u8, self.i32, self.i64, self.f32, self.f64 = (torch.int8, torch.uint8, torch.int32, torch.int64,
+                                                                    torch.float32, torch.float64)
         self.any = {torch.bfloat16: LB_BF16, torch.float16: LB_F16, torch.float32: LB_F32}
         self.short = {torch.bfloat16: LB_BF16, torch.float16: LB_F16}
         self.current_stream = torch._C._cuda_getCurrentRawStream
@@ -517,3 +535,156 @@ def lb_attn_kv4(Q, Kc, Vc, Kp, Vp, table, q_off, lens, out, lse=None, max_q=None
                          Hkv, D, pages, page, max_len, D ** -0.5 if scale is None else scale, window, int(causal), f,
                          None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes, _on(T, stream, dev))
     _raise(st, "lb_attn_kv4")
+
+
+# ---------------------------------------------------------------------------
+# the rest of a decoder layer: norms with gate and residual, rotary positions, a linear
+# layer with 4-bit weights and a mixture of experts of them
+# ---------------------------------------------------------------------------
+
+def lb_residual_norm(Y, R, R_out, X, w=None, post_w=None, gate=None, alpha: float = 1.0, eps: float = 1e-5,
+                     stream=None) -> None:
+    """r' = R + alpha * gate * z with z = Y, or Y rms(Y) post_w where post_w is given; R_out receives r' and X
+    r' rms(r') w, rms(v) = 1 / sqrt(mean(v ** 2) + eps) over a row.
+
+    Y, X (M, H) and w, post_w (H,) share a type: bf16, fp16 or fp32; R, R_out (M, H) are of that type or fp32;
+    rows may be strided.  gate: (M, H), or (H,) for all rows, of Y's type.  Y or R may be None (r' = R; R = 0), and
+    R_out or X.  R_out may be R, X may be Y."""
+    T = _torch()
+    a = Y if Y is not None else R if R is not None else None
+    if a is None:
+        raise ValueError("lb_residual_norm: Y and R are both None")
+    shape = M, H = a.shape
+    dev = a.get_device()
+    o = Y if Y is not None else X if X is not None else w if w is not None else R
+    dt = o.dtype
+    f = _ftype(T.any, o, "Y" if Y is not None else "X")
+    y, ldy = (None, 0) if Y is None else _rows(Y, "Y", dt, shape, dev, H)
+    x, ldx = (None, 0) if X is None else _rows(X, "X", dt, shape, dev, H)
+    rt = R if R is not None else R_out
+    rd = dt if rt is None else rt.dtype
+    if rd is not dt and rd is not T.f32:
+        raise TypeError(f"R: dtype {rd}, expected {dt} or {T.f32}")
+    r, ldr = (None, 0) if R is None else _rows(R, "R", rd, shape, dev, H)
+    ro, ldro = (None, 0) if R_out is None else _rows(R_out, "R_out", rd, shape, dev, H)
+    g, ldg = None, 0
+    if gate is not None:
+        if gate.dim() == 1:
+            g = _dense(gate, "gate", dt, (H,), dev)
+        else:
+            g, ldg = _rows(gate, "gate", dt, shape, dev, H)
+    st = load().lb_residual_norm(y, ldy, r, ldr, None if post_w is None else _dense(post_w, "post_w", dt, (H,), dev), g,
+                                 ldg, None if w is None else _dense(w, "w", dt, (H,), dev), ro, ldro, x, ldx, M, H,
+                                 alpha, eps, f, T.any[rd], _on(T, stream, dev))
+    _raise(st, "lb_residual_norm")
+
+
+_ROPE_LAYOUTS = {"half": LB_ROPE_HALF, "pairs": LB_ROPE_PAIRS, LB_ROPE_HALF: LB_ROPE_HALF, LB_ROPE_PAIRS: LB_ROPE_PAIRS}
+_ROPE_SCALINGS = {"plain": LB_ROPE_PLAIN, "linear": LB_ROPE_LINEAR, "base": LB_ROPE_BASE, "parts": LB_ROPE_PARTS,
+                  "bands": LB_ROPE_BANDS}
+
+
+def lb_rope_freqs(R: int, base: float = 10000.0, scaling="plain", factor: float = 1.0, before: float = 0.0,
+                  low: float = 1.0, high: float = 32.0, device="cuda"):
+    """(freqs, mult) for lb_rope: R/2 frequencies, a float64 tensor on `device`, and the factor of the turned
+    numbers.  scaling: "plain", "linear", "base", "parts" or "bands" (see the header), for contexts `factor` times
+    longer than `before`."""
+    T = _torch()
+    f, m = (ctypes.c_double * max(R // 2, 1))(), ctypes.c_float()
+    _raise(load().lb_rope_freqs(f, ctypes.byref(m), R, base, _ROPE_SCALINGS.get(scaling, scaling), factor, before, low,
+                                high), "lb_rope_freqs")
+    return T.torch.tensor(list(f), dtype=T.torch.float64, device=device), m.value
+
+
+def lb_rope(Q, K, pos, freqs, Q_out, K_out, layout="half", mult: float = 1.0, stream=None) -> None:
+    """Rotary positions of Q (T, Hq, D) and K (T, Hk, D) or None, bf16, fp16 or fp32 (tokens may be strided), at
+    positions pos (T,) int64, into Q_out and K_out, which may be Q and K.  freqs (R/2,) float64: the first R
+    numbers of each head are turned, as pairs (i, i + R/2) with layout "half" and (2i, 2i + 1) with "pairs", and
+    multiplied by mult; lb_rope_freqs makes both."""
+    T = _torch()
+    shape = n, Hq, D = Q.shape
+    dev, dt = Q.get_device(), Q.dtype
+    f = _ftype(T.any, Q, "Q")
+    lay = _ROPE_LAYOUTS.get(layout)
+    if lay is None:
+        raise ValueError(f"layout: {layout!r}, expected 'half' or 'pairs'")
+    q, ldq = _rows(Q, "Q", dt, shape, dev, Hq * D)
+    qo, ldqo = _rows(Q_out, "Q_out", dt, shape, dev, Hq * D)
+    k = ko = None
+    Hk = ldk = ldko = 0
+    if K is not None:
+        Hk = K.shape[1]
+        k, ldk = _rows(K, "K", dt, (n, Hk, D), dev, Hk * D)
+        ko, ldko = _rows(K_out, "K_out", dt, (n, Hk, D), dev, Hk * D)
+    st = load().lb_rope(q, ldq, k, ldk, _dense(pos, "pos", T.i64, (n,), dev),
+                        _dense(freqs, "freqs", T.f64, (freqs.shape[0],), dev), qo, ldqo, ko, ldko, n, Hq, Hk, D,
+                        2 * freqs.shape[0], lay, mult, f, _on(T, stream, dev))
+    _raise(st, "lb_rope")
+
+
+def lb_linear_w4_workspace(M: int, K: int, N: int, group: int) -> int:
+    """Workspace bytes of lb_linear_w4 for X (M, K) and N rows of weights in groups of `group`."""
+    return load().lb_linear_w4_workspace(M, K, N, group)
+
+
+def lb_linear_w4(X, W, Wp, out, bias=None, workspace=None, stream=None) -> None:
+    """out (M, N) = X (M, K) x (levels * scale + minimum) + bias[n]: W (N, K/2) uint8, two levels to a byte, the
+    even k in the low nibble; Wp (N, K/group, 2), scale and minimum of each group of 32, 64 or 128.  X (rows may
+    be strided), Wp, bias and out share a type, bf16 or fp16.  workspace: a GPU tensor of at least
+    lb_linear_w4_workspace(M, K, N, group) bytes, or None for one from torch's allocator."""
+    T = _torch()
+    lib = load()
+    M, K = X.shape
+    N, groups, _ = Wp.shape
+    dev, dt = X.get_device(), X.dtype
+    f = _ftype(T.short, X, "X")
+    if groups == 0 or K % groups:
+        raise ValueError(f"Wp: {groups} groups do not divide {K}")
+    group = K // groups
+    x, ldx = _rows(X, "X", dt, (M, K), dev, K)
+    w = _dense(W, "W", T.u8, (N, K // 2), dev)
+    p = _dense(Wp, "Wp", dt, (N, groups, 2), dev)
+    o = _dense(out, "out", dt, (M, N), dev)
+    b = None if bias is None else _dense(bias, "bias", dt, (N,), dev)
+    ws = _scratch(T, workspace, 0 if workspace is not None else lib.lb_linear_w4_workspace(M, K, N, group), dev, stream,
+                  "lb_linear_w4")
+    st = lib.lb_linear_w4(x, ldx, w, p, b, o, M, N, K, group, f, None if ws is None else ws.data_ptr(),
+                          0 if ws is None else ws.nbytes, _on(T, stream, dev))
+    _raise(st, "lb_linear_w4")
+
+
+def lb_moe_w4_workspace(T: int, H: int, I: int, E: int, top_k: int) -> int:
+    """Workspace bytes of lb_moe_w4 for T tokens of H numbers and E experts I wide, top_k to a token."""
+    return load().lb_moe_w4_workspace(T, H, I, E, top_k)
+
+
+def lb_moe_w4(X, Wr, W1, P1, W2, P2, out, top_k: int, renorm: bool = False, scale: float = 1.0, ids=None, weights=None,
+              workspace=None, stream=None) -> None:
+    """A mixture of experts for a few tokens: out (T, H) = sum over the top_k largest of softmax(Wr x), Wr (E, H),
+    of its value (divided by their sum with renorm) times `scale` times W2_e (silu(Wg_e x) * (Wu_e x)).
+
+    W1 (E, 2I, H/2) uint8 holds an expert's I gate rows, then its I up rows, P1 (E, 2I, H/group, 2) their groups'
+    numbers; W2 (E, H, I/2) and P2 (E, H, I/group, 2) likewise, all as for lb_linear_w4.  X (rows may be strided),
+    Wr, P1, P2 and out share a type, bf16 or fp16.  ids (T, top_k) int32 and weights (T, top_k) fp32 receive the
+    chosen experts and their factors, if given.  workspace: as for lb_linear_w4, of lb_moe_w4_workspace bytes."""
+    T = _torch()
+    lib = load()
+    n, H = X.shape
+    E, rows, groups, _ = P1.shape
+    I = rows // 2
+    dev, dt = X.get_device(), X.dtype
+    f = _ftype(T.short, X, "X")
+    if groups == 0 or H % groups:
+        raise ValueError(f"P1: {groups} groups do not divide {H}")
+    group = H // groups
+    x, ldx = _rows(X, "X", dt, (n, H), dev, H)
+    args = (_dense(Wr, "Wr", dt, (E, H), dev), _dense(W1, "W1", T.u8, (E, 2 * I, H // 2), dev),
+            _dense(P1, "P1", dt, (E, 2 * I, groups, 2), dev), _dense(W2, "W2", T.u8, (E, H, I // 2), dev),
+            _dense(P2, "P2", dt, (E, H, I // group, 2), dev), _dense(out, "out", dt, (n, H), dev),
+            None if ids is None else _dense(ids, "ids", T.i32, (n, top_k), dev),
+            None if weights is None else _dense(weights, "weights", T.f32, (n, top_k), dev))
+    ws = _scratch(T, workspace, 0 if workspace is not None else lib.lb_moe_w4_workspace(n, H, I, E, top_k), dev, stream,
+                  "lb_moe_w4")
+    st = lib.lb_moe_w4(x, ldx, *args, n, H, I, E, top_k, group, int(renorm), scale, f,
+                       None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes, _on(T, stream, dev))
+    _raise(st, "lb_moe_w4")

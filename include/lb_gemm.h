@@ -349,6 +349,113 @@ int lb_attn_kv4(const void *Q, int64_t ldq, const uint8_t *Kc, const uint8_t *Vc
 int64_t lb_attn_kv4_workspace(int64_t B, int64_t total_q, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D,
                               int64_t max_len, int64_t window, int cu_count);
 
+/*
+ * The rest of a decoder layer.  Conventions as for the serving operators above: rows
+ * are 16-byte aligned, strides (ld..) are in elements; pos, ids and weights may start
+ * at any element of theirs, freqs too.
+ */
+
+/*
+ * What stands between two blocks, for each of M rows of H numbers:
+ *   z  = Y, or with post_w  Y rms(Y) post_w,     rms(v) = 1 / sqrt(mean(v^2) + eps)
+ *   r' = R + alpha * gate * z                    (R NULL: 0; Y NULL: r' = R)
+ *   X  = r' rms(r') w
+ * R_out receives r', X the normed rows; either may be NULL.  gate: a row for each token
+ * (ldg apart), or with ldg 0 one row for all, or NULL: 1.  Y, post_w, gate, w and X are
+ * of ftype; R and R_out of rtype, which is ftype or LB_F32.  fp32 inside; r' and X are
+ * rounded once each, X from r' before its rounding.  R_out may be R and X may be Y (with
+ * the same stride); no other overlap.  Squares of a row sum up in fp32, so that rows of
+ * numbers beyond 2^60 in magnitude overflow.  H % 8 == 0, H <= LB_NORM_H_MAX.
+ */
+#define LB_NORM_H_MAX 32768
+int lb_residual_norm(const void *Y, int64_t ldy, const void *R, int64_t ldr, const void *post_w,
+                     const void *gate, int64_t ldg, const void *w, void *R_out, int64_t ldro, void *X,
+                     int64_t ldx, int64_t M, int64_t H, float alpha, float eps, int ftype, int rtype,
+                     void *stream);
+
+/*
+ * Rotary positions of queries and keys: pair i of the first R numbers of each head,
+ *   (a, b) -> mult * (a cos t - b sin t, b cos t + a sin t),  t = pos[token] * freqs[i],
+ * where pair i is numbers (i, i + R/2) with LB_ROPE_HALF and (2i, 2i + 1) with
+ * LB_ROPE_PAIRS; the other D - R numbers are copied.  Angles are formed in fp64, turned
+ * numbers in fp32 and rounded once.  Q: T tokens ldq apart, each Hq x D dense; K: Hk
+ * heads likewise (Hk 0: none, K and K_out NULL).  Q_out may be Q, K_out may be K (with
+ * the same stride); no other overlap.  pos: T int64 (any, also negative).  freqs: R / 2
+ * fp64, on the GPU.  D % 8 == 0, R % 16 == 0, R <= D <= LB_ROPE_R_MAX.
+ */
+typedef enum { LB_ROPE_HALF = 0, LB_ROPE_PAIRS = 1 } lb_rope_layout;
+#define LB_ROPE_R_MAX 4096
+int lb_rope(const void *Q, int64_t ldq, const void *K, int64_t ldk, const int64_t *pos, const double *freqs,
+            void *Q_out, int64_t ldqo, void *K_out, int64_t ldko, int64_t T, int64_t Hq, int64_t Hk, int64_t D,
+            int64_t R, int layout, float mult, int ftype, void *stream);
+/* The frequencies, R / 2 of them, and mult, both in host memory (no GPU work):
+ *   LB_ROPE_PLAIN   f_i = base^(-2i/R)
+ *   LB_ROPE_LINEAR  f_i / factor
+ *   LB_ROPE_BASE    f_i of base * factor^(R/(R-2)) (R = 2: of base)
+ *   LB_ROPE_PARTS   f_i where pair i turns at least `high` times in `before` positions,
+ *                   f_i / factor where at most `low` times, a blend linear in i between (from
+ *                   the whole pair below the one to the whole pair above the other);
+ *                   mult = 0.1 ln(factor) + 1 (factor <= 1: 1)
+ *   LB_ROPE_BANDS   the same, the blend linear in the number of turns; mult = 1.
+ * before: the context length that the frequencies are stretched from.  factor > 0, base >
+ * 1; the last two need before > 0 and 0 < low < high.  LB_ERR_SHAPE otherwise. */
+typedef enum {
+    LB_ROPE_PLAIN = 0,
+    LB_ROPE_LINEAR = 1,
+    LB_ROPE_BASE = 2,
+    LB_ROPE_PARTS = 3,
+    LB_ROPE_BANDS = 4
+} lb_rope_scaling;
+int lb_rope_freqs(double *freqs, float *mult, int64_t R, double base, int scaling, double factor,
+                  double before, double low, double high);
+
+/*
+ * Linear layer with 4-bit weights:
+ *   out[m,n] = sum_k X[m,k] (u[n,k] s[n,g] + b[n,g]) + bias[n],  g = k / group.
+ *   W: N rows of K/2 bytes, levels u in 0..15, even k in the low nibble; Wp: N x K/group x
+ *   2 of ftype, the scale s and the minimum b of each group (signed levels -8..7 with a
+ *   scale alone: u = level + 8, b = -8 s, which is exact).  group is 32, 64 or 128 and
+ *   divides K <= LB_W4_K_MAX.  X (ldx elements between rows), bias (N, or NULL) and out
+ *   (dense) are of ftype, bf16 or fp16.
+ * Products are exact, sums and the groups' numbers fp32, out is rounded once; what comes
+ * from a row of X that holds an infinity or a NaN is not finite (NaN or infinite).  The sums run
+ * over 16 + u in place of u: up to four times fp32's rounding of the sum.
+ * workspace: at least lb_linear_w4_workspace(M, K, N, group) bytes (LB_ERR_WORKSPACE
+ * otherwise; NULL where that is 0).
+ */
+#define LB_W4_K_MAX 1048576
+int lb_linear_w4(const void *X, int64_t ldx, const uint8_t *W, const void *Wp, const void *bias, void *out,
+                 int64_t M, int64_t N, int64_t K, int64_t group, int ftype, void *workspace,
+                 int64_t workspace_bytes, void *stream);
+int64_t lb_linear_w4_workspace(int64_t M, int64_t K, int64_t N, int64_t group);
+
+/*
+ * A mixture of experts with 4-bit weights, for a few tokens:
+ *   p = softmax(Wr x) over E experts; e_1 .. e_k the top_k largest in that order (of equal
+ *   ones the lowest index first); q_j = scale * p_{e_j}, with renorm != 0 divided by the
+ *   sum of the chosen p;
+ *   out = sum_j q_j W2_{e_j} (silu(Wg_{e_j} x) * (Wu_{e_j} x)),  silu(v) = v / (1 + exp(-v)).
+ *   X: T x H (ldx apart), Wr: E x H, out: T x H dense, all of ftype (bf16 or fp16).
+ *   W1, P1: E x 2I rows of H weights, the I gate rows of an expert before its I up rows;
+ *   W2, P2: E x H rows of I weights; both laid out as lb_linear_w4's W and Wp.
+ *   ids (T x top_k int32) and weights (T x top_k fp32) receive e_j and q_j; either may be
+ *   NULL.
+ * fp32 sums; between the two products silu(..) * (..) is held in two bf16 parts (2^-17 of
+ * it).  A NaN among a token's logits counts as the largest and makes its row NaN.  Sums
+ * have a fixed order: the same arguments give the same bits.
+ * group divides H and I.  E <= LB_MOE_EXPERTS_MAX, top_k <= min(E, LB_MOE_TOP_MAX); H * I is
+ * bounded (LB_ERR_OVERFLOW above about 2^33).  More than 64 tokens run 64 at a time, each time
+ * reading the weights again.  workspace: at least lb_moe_w4_workspace() bytes
+ * (LB_ERR_WORKSPACE otherwise); that returns 0 for sizes that are refused.
+ */
+#define LB_MOE_EXPERTS_MAX 1024
+#define LB_MOE_TOP_MAX 64
+int lb_moe_w4(const void *X, int64_t ldx, const void *Wr, const uint8_t *W1, const void *P1, const uint8_t *W2,
+              const void *P2, void *out, int32_t *ids, float *weights, int64_t T, int64_t H, int64_t I,
+              int64_t E, int64_t top_k, int64_t group, int renorm, float scale, int ftype, void *workspace,
+              int64_t workspace_bytes, void *stream);
+int64_t lb_moe_w4_workspace(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k);
+
 /* Hash of the source files this library was built from (16 hex digits, static
  * storage; never NULL).  The build stamps it in, so that a caller can check a
  * loaded library against the sources it expects. */
