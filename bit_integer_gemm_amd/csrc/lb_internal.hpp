@@ -161,7 +161,7 @@ struct W4Args {
     void *out;
     int64_t M, N, K;
 };
-hipError_t launch_linear_w4(int ftype, int group, const W4Args &a, hipStream_t s);
+hipError_t launch_linear_w4(int ftype, int group, const W4Args &a, int cu, hipStream_t s);
 
 // The mixture of experts, for at most MOE_TOKENS tokens a launch.
 enum { MOE_TOKENS = 64 };
@@ -181,7 +181,7 @@ struct MoeArgs {
     void *h;           // two planes of T top_k x I, bf16
     float *y;          // T top_k x H
 };
-hipError_t launch_moe_w4(int ftype, int group, const MoeArgs &a, hipStream_t s);
+hipError_t launch_moe_w4(int ftype, int group, const MoeArgs &a, int cu, hipStream_t s);
 
 // Measured selection table lookup (host only).
 int select_from_table(int dtype, int64_t M, int64_t N, int64_t K, int cu_count, int *best,

@@ -38,6 +38,8 @@ int check_w4(int64_t M, int64_t N, int64_t K, int64_t group, int ftype)
     if (K > LB_W4_K_MAX) return LB_ERR_OVERFLOW;
     return LB_OK;
 }
+// Byte offsets between 64 rows of x are 32-bit.
+const int64_t kLdMax = (int64_t)1 << 24;
 
 int check_moe(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k, int64_t group, int ftype)
 {
@@ -49,6 +51,7 @@ int check_moe(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k, int64_t
     // times columns, are 32-bit; one launch covers all experts
     if ((double)(I + 256) * (double)H >= 8589934592.0) return LB_ERR_OVERFLOW;
     const int64_t tokens = std::min<int64_t>(T, lb::MOE_TOKENS);
+    if (tokens * top_k * I * 4 >= (int64_t)0xFFFF0000 || tokens * top_k * H >= kLim) return LB_ERR_OVERFLOW;
     if (std::min(tokens * top_k, E) * (std::max(I, H) / 16 + 1) * ((tokens + 15) / 16) * 512 > lb::LAUNCH_THREADS)
         return LB_ERR_OVERFLOW;
     return LB_OK;
@@ -191,6 +194,7 @@ int lb_linear_w4(const void *X, int64_t ldx, const uint8_t *W, const void *Wp, c
     if (st != LB_OK) return st;
     if (!aligned(X) || !aligned(W) || !aligned(Wp) || !aligned(bias) || !aligned(out) || !rows_aligned(ldx, ftype))
         return LB_ERR_ALIGN;
+    if (ldx > kLdMax) return LB_ERR_OVERFLOW;
     const int64_t need = lb_linear_w4_workspace(M, K, N, group);
     if (need > 0 && (!workspace || workspace_bytes < need)) return LB_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return LB_ERR_ALIGN;
@@ -204,7 +208,7 @@ int lb_linear_w4(const void *X, int64_t ldx, const uint8_t *W, const void *Wp, c
     a.M = M;
     a.N = N;
     a.K = K;
-    return finish(lb::launch_linear_w4(ftype, (int)group, a, (hipStream_t)stream));
+    return finish(lb::launch_linear_w4(ftype, (int)group, a, cu_count(), (hipStream_t)stream));
 }
 
 int64_t lb_moe_w4_workspace(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k)
@@ -225,9 +229,11 @@ int lb_moe_w4(const void *X, int64_t ldx, const void *Wr, const uint8_t *W1, con
     if (!aligned(X) || !aligned(Wr) || !aligned(W1) || !aligned(P1) || !aligned(W2) || !aligned(P2) || !aligned(out) ||
         !rows_aligned(ldx, ftype))
         return LB_ERR_ALIGN;
+    if (ldx > kLdMax) return LB_ERR_OVERFLOW;
     const MoeSpace m = moe_space(T, H, I, E, top_k);
     if (!workspace || workspace_bytes < m.bytes) return LB_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return LB_ERR_ALIGN;
+    const int cu = cu_count();
     for (int64_t t = 0; t < T; t += lb::MOE_TOKENS) {
         lb::MoeArgs a;
         a.x = (const char *)X + t * ldx * 2;
@@ -250,7 +256,7 @@ int lb_moe_w4(const void *X, int64_t ldx, const void *Wr, const uint8_t *W1, con
         a.logits = (float *)workspace;
         a.h = (char *)workspace + m.h;
         a.y = (float *)((char *)workspace + m.y);
-        const hipError_t e = lb::launch_moe_w4(ftype, (int)group, a, (hipStream_t)stream);
+        const hipError_t e = lb::launch_moe_w4(ftype, (int)group, a, cu, (hipStream_t)stream);
         if (e != hipSuccess) return LB_ERR_HIP;
     }
     return LB_OK;

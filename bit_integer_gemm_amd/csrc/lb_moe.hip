@@ -29,15 +29,14 @@ enum { ROUTER_WAVES = 8 };
 template <class T>
 __global__ __launch_bounds__(64 * ROUTER_WAVES) void moe_router_kernel(MoeArgs a)
 {
-    typedef W4Join<1, 1, ROUTER_WAVES> Join;
-    __shared__ float sums[Join::FLOATS];
+    __shared__ float sums[ROUTER_WAVES][16 * W4_SLOT_LD];
     const int32_t lane = (int32_t)(threadIdx.x & 63u), q = lane >> 4, r = lane & 15;
     const int32_t wave = (int32_t)(threadIdx.x >> 6);
     const int32_t e0 = (int32_t)blockIdx.x * 16, t0 = (int32_t)blockIdx.y * 16;
     const T *wrow = (const T *)a.wr + (int64_t)min(e0 + r, a.E - 1) * a.H;
     const T *xrow = (const T *)a.x + (int64_t)min(t0 + r, a.T - 1) * a.ldx;
     const int32_t steps = a.H / 32, last = (wave + 1) * steps / ROUTER_WAVES;
-    f32x4 acc[1][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}};
+    f32x4 acc[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
     for (int32_t st = wave * steps / ROUTER_WAVES; st < last; st += 4) {
         u32x4 x[4], w[4];
 #pragma unroll
@@ -49,13 +48,16 @@ __global__ __launch_bounds__(64 * ROUTER_WAVES) void moe_router_kernel(MoeArgs a
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[0][0] = mfma16<T>(x[i], w[i], acc[0][0]);
+        for (int i = 0; i < 4; ++i) acc[0] = mfma16<T>(x[i], w[i], acc[0]);
     }
-    Join::put(sums, wave, acc);
+    w4_put<1>(sums[wave], 16, acc);
     __syncthreads();
-    for (int32_t i = (int32_t)threadIdx.x; i < 256; i += 64 * ROUTER_WAVES) {
-        const int32_t t = t0 + i / 16, e = e0 + i % 16;
-        if (t < a.T && e < a.E) a.logits[t * a.E + e] = Join::sum(sums, i / 16, i % 16);
+    if (threadIdx.x < 256) {
+        const int32_t m = (int32_t)threadIdx.x / 16, n = (int32_t)threadIdx.x % 16;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < ROUTER_WAVES; ++w) v += sums[w][m * W4_SLOT_LD + n];
+        if (t0 + m < a.T && e0 + n < a.E) a.logits[(t0 + m) * a.E + e0 + n] = v;
     }
 }
 
@@ -63,51 +65,75 @@ __global__ __launch_bounds__(64 * ROUTER_WAVES) void moe_router_kernel(MoeArgs a
 // The expert of a workgroup and its tokens.  Slots are experts where tokens are many, and
 // (token, rank) pairs where those are fewer; of pairs that name the same expert the first
 // one's workgroups work for all its tokens, the others end.
+enum { EXPERTS_MAX = 1024 };
 struct MoeList {
     int32_t rank[MOE_TOKENS];   // the expert's rank in each token's order, if below k, else -1
     int32_t row[MOE_TOKENS];    // token * k + rank of each of its tokens
     int32_t expert, count, first;
 };
 
-template <int NW>
-__device__ inline bool moe_list(const MoeArgs &a, int32_t slot, bool by_pair, MoeList &l)
+// How many of a token's logits come before number e, whose order is `mine`.
+__device__ inline int32_t rank_of(const uint32_t *order, int32_t E, int32_t e, uint32_t mine)
 {
+    int32_t above = 0;
+    for (int32_t f = 0; f < E; f += 4) {   // (order[E ..] up to a multiple of 4 is 0)
+        const u32x4 o = *(const u32x4 *)(order + f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) above += o[i] > mine || (o[i] == mine && f + i < e);
+    }
+    return above;
+}
+// A token's logits' orders into LDS; barrier afterwards.
+__device__ inline void put_orders(uint32_t *order, const float *row, int32_t E, int32_t threads)
+{
+    for (int32_t e = (int32_t)threadIdx.x; e < (E + 3) / 4 * 4; e += threads) order[e] = e < E ? order_of(row[e]) : 0u;
+    __syncthreads();
+}
+
+// order: LDS for EXPERTS_MAX words, free again afterwards.
+__device__ inline bool moe_list(const MoeArgs &a, int32_t slot, bool by_pair, MoeList &l, uint32_t *order)
+{
+    constexpr int NW = W4_WAVES, AT_ONCE = MOE_TOKENS / NW;
     const int32_t tid = (int32_t)threadIdx.x, lane = tid & 63, wave = tid >> 6;
     if (by_pair) {
         const int32_t t = slot / a.top_k, j = slot % a.top_k;
-        const float *row = a.logits + t * a.E;
-        for (int32_t e = tid; e < a.E; e += 64 * NW) {
-            const uint32_t mine = order_of(row[e]);
-            int32_t above = 0;
-            for (int32_t f = 0; f < a.E; ++f) {
-                const uint32_t o = order_of(row[f]);
-                above += o > mine || (o == mine && f < e);
-            }
-            if (above == j) {
+        put_orders(order, a.logits + t * a.E, a.E, 64 * NW);
+        for (int32_t e = tid; e < a.E; e += 64 * NW)
+            if (rank_of(order, a.E, e, order[e]) == j) {
                 l.expert = e;
                 l.first = t;
             }
-        }
     } else if (tid == 0) {
         l.expert = slot;
         l.first = 0;
     }
     __syncthreads();
     const int32_t e = l.expert;
-    for (int32_t t = wave; t < a.T; t += NW) {
-        const float *row = a.logits + t * a.E;
-        const uint32_t mine = order_of(row[e]);
-        int32_t above = 0;
-        for (int32_t f0 = 0; f0 < a.E; f0 += 64) {
-            const int32_t f = f0 + lane;
-            const uint32_t o = f < a.E ? order_of(row[f]) : 0u;
-            above += __popcll(__ballot(f < a.E && (o > mine || (o == mine && f < e))));
-        }
-        if (lane == 0) l.rank[t] = above < a.top_k ? above : -1;
+    uint32_t mine[AT_ONCE];
+    int32_t above[AT_ONCE];
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) {
+        mine[i] = order_of(a.logits[min(wave + NW * i, a.T - 1) * a.E + e]);
+        above[i] = 0;
     }
+    for (int32_t f0 = 0; f0 < a.E; f0 += 64) {
+        const int32_t f = min(f0 + lane, a.E - 1);
+        const bool there = f0 + lane < a.E;
+        float v[AT_ONCE];
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) v[i] = a.logits[min(wave + NW * i, a.T - 1) * a.E + f];
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const uint32_t o = order_of(v[i]);
+            above[i] += __popcll(__ballot(there && (o > mine[i] || (o == mine[i] && f < e))));
+        }
+    }
+    if (lane == 0)
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) l.rank[wave + NW * i] = wave + NW * i < a.T && above[i] < a.top_k ? above[i] : -1;
     __syncthreads();
     if (wave == 0) {
-        const int32_t rank = lane < a.T ? l.rank[lane] : -1;
+        const int32_t rank = l.rank[lane];
         const uint64_t in = __ballot(rank >= 0);
         if (rank >= 0) l.row[__popcll(in & ((1ull << lane) - 1))] = lane * a.top_k + rank;
         if (lane == 0) l.count = (by_pair && (in & ((1ull << l.first) - 1))) ? 0 : __popcll(in);
@@ -117,63 +143,97 @@ __device__ inline bool moe_list(const MoeArgs &a, int32_t slot, bool by_pair, Mo
 }
 
 // ---- gate and up, activation -----------------------------------------------
-enum { MOE_WAVES = 8 };
-template <class T, int G>
-__global__ __launch_bounds__(64 * MOE_WAVES) void moe_up_kernel(MoeArgs a, bool by_pair)
+// A workgroup: an expert, some blocks of 16 columns (each a tile of gate rows and one of up rows),
+// at most 16 of its tokens.
+struct MoeGrid {
+    bool by_pair;
+    int32_t kw, each, lds_rows;   // W4Split over blocks (up) or tiles (down), rows that LDS is laid out for
+};
+template <class T, int G, bool XLDS, int DEPTH>
+__global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGrid g)
 {
-    typedef W4Join<1, 2, MOE_WAVES> Join;
-    __shared__ float sums[Join::FLOATS];
+    extern __shared__ __attribute__((aligned(16))) char smem[];
     __shared__ MoeList list;
-    if (!moe_list<MOE_WAVES>(a, (int32_t)blockIdx.y, by_pair, list)) return;
+    const uint32_t stride = w4_x_stride(a.H);
+    float *const slots = (float *)(smem + (XLDS ? (uint32_t)g.lds_rows * stride : 0u));
+    if (!moe_list(a, (int32_t)blockIdx.y, g.by_pair, list, (uint32_t *)smem)) return;
     const int32_t lane = (int32_t)(threadIdx.x & 63u);
     const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int32_t i0 = (int32_t)blockIdx.x * 16, at = (int32_t)blockIdx.z * 16, rows = min(16, list.count - at);
-    const int64_t n0 = (int64_t)__builtin_amdgcn_readfirstlane(list.expert) * 2 * a.I + i0;
-    const T *xrow[1] = {(const T *)a.x + (int64_t)(list.row[at + min(lane & 15, rows - 1)] / a.top_k) * a.ldx};
-    const int32_t lines = (a.H + 255) / 256;
-    const int64_t left = a.I + 16;   // rows from the first gate row of the tile to the last up row
-    f32x4 acc[1][2] = {{f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}}};
-    w4_product<T, T, 1, 2, G>(a.w1 + n0 * (a.H / 2), (uint64_t)left * (uint32_t)(a.H / 2), (const uint32_t *)a.p1 + n0 * (a.H / G),
-                              (uint64_t)left * (uint32_t)(a.H / G) * 4u, a.H, a.I, wave * lines / MOE_WAVES,
-                              (wave + 1) * lines / MOE_WAVES, xrow, 0, acc);
-    Join::put(sums, wave, acc);
+    const int32_t expert = __builtin_amdgcn_readfirstlane(list.expert);
+    const int32_t at = (int32_t)blockIdx.z * 16, rows = min(16, __builtin_amdgcn_readfirstlane(list.count) - at);
+    const int32_t per = W4_WAVES / g.kw * g.each, b0 = (int32_t)blockIdx.x * per, have = min(per, a.I / 16 - b0);
+    const int32_t lines = (a.H + 255) / 256, share = wave % g.kw, mine = wave / g.kw * g.each;
+    const int32_t slot = rows * W4_SLOT_LD, row = min(lane & 15, rows - 1);
+    auto row_at = [&](int32_t r) { return (const T *)a.x + (int64_t)(list.row[at + r] / a.top_k) * a.ldx; };
+    const uint32_t xat[1] = {XLDS ? (uint32_t)row * stride : (uint32_t)(list.row[at + row] / a.top_k) * (uint32_t)a.ldx * 2u};
+    W4Stage<decltype(row_at)> stage(smem, a.H, rows, 64 * W4_WAVES, row_at);
+    if constexpr (XLDS) stage.first();
+    w4_stream<T, T, 1, G, 1, XLDS, DEPTH>(
+        a.w1, (const uint32_t *)a.p1, a.H, share * lines / g.kw, (share + 1) * lines / g.kw, 2 * max(0, min(g.each, have - mine)),
+        w4_rsrc(a.x, 0xFFFFFFF0u), smem, xat, 0u,
+        [&](int32_t t) { return W4Tile{((int64_t)expert * 2 + t % 2) * a.I + (b0 + mine + t / 2) * 16, 16}; },
+        [&] {
+            if constexpr (XLDS) stage.rest();
+        },
+        [&](int32_t t, const f32x4(&acc)[1]) { w4_put<1>(slots + (wave * 2 * g.each + t) * slot, rows, acc); });
     __syncthreads();
     __bf16 *const hi = (__bf16 *)a.h, *const lo = hi + (int64_t)a.T * a.top_k * a.I;
-    for (int32_t i = (int32_t)threadIdx.x; i < 16 * rows; i += 64 * MOE_WAVES) {
-        const int32_t m = i / 16, n = i % 16;
-        const float g = Join::sum(sums, m, n), u = Join::sum(sums, m, 16 + n);
-        const float h = g / (1.0f + __expf(-g)) * u;
-        const int64_t o = (int64_t)list.row[at + m] * a.I + i0 + n;
+    for (int32_t i = (int32_t)threadIdx.x; i < rows * have * 16; i += 64 * W4_WAVES) {
+        const int32_t m = i / (have * 16), c = i - m * have * 16, b = c / 16;
+        const float *s = slots + (b / g.each * g.kw * 2 * g.each + b % g.each * 2) * slot + m * W4_SLOT_LD + c % 16;
+        float gate = 0.f, up = 0.f;
+        for (int32_t k = 0; k < g.kw; ++k)
+            if (k * lines / g.kw < (k + 1) * lines / g.kw) {
+                gate += s[k * 2 * g.each * slot];
+                up += s[(k * 2 * g.each + 1) * slot];
+            }
+        const float h = gate / (1.0f + __expf(-gate)) * up;
+        const int64_t o = (int64_t)list.row[at + m] * a.I + b0 * 16 + c;
         hi[o] = (__bf16)h;
         lo[o] = (__bf16)(h - (float)hi[o]);
     }
 }
 
 // ---- down ------------------------------------------------------------------
-template <class T, int G>
-__global__ __launch_bounds__(64 * MOE_WAVES) void moe_down_kernel(MoeArgs a, bool by_pair)
+template <class T, int G, bool XLDS, int DEPTH>
+__global__ __launch_bounds__(64 * W4_WAVES) void moe_down_kernel(MoeArgs a, MoeGrid g)
 {
-    typedef W4Join<1, 2, MOE_WAVES> Join;
-    __shared__ float sums[Join::FLOATS];
+    extern __shared__ __attribute__((aligned(16))) char smem[];
     __shared__ MoeList list;
-    if (!moe_list<MOE_WAVES>(a, (int32_t)blockIdx.y, by_pair, list)) return;
+    const uint32_t stride = w4_x_stride(a.I);
+    float *const slots = (float *)(smem + (XLDS ? 2u * (uint32_t)g.lds_rows * stride : 0u));
+    if (!moe_list(a, (int32_t)blockIdx.y, g.by_pair, list, (uint32_t *)smem)) return;
     const int32_t lane = (int32_t)(threadIdx.x & 63u);
     const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int32_t c0 = (int32_t)blockIdx.x * 32, at = (int32_t)blockIdx.z * 16, rows = min(16, list.count - at);
-    const int64_t n0 = (int64_t)__builtin_amdgcn_readfirstlane(list.expert) * a.H + c0;
-    const __bf16 *xrow[1] = {(const __bf16 *)a.h + (int64_t)list.row[at + min(lane & 15, rows - 1)] * a.I};
-    const int32_t lines = (a.I + 255) / 256;
-    const int32_t left = min(32, a.H - c0);
-    f32x4 acc[1][2] = {{f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}}};
-    w4_product<__bf16, T, 1, 2, G, 2>(a.w2 + n0 * (a.I / 2), (uint64_t)left * (uint32_t)(a.I / 2),
-                                      (const uint32_t *)a.p2 + n0 * (a.I / G), (uint64_t)left * (uint32_t)(a.I / G) * 4u, a.I,
-                                      16, wave * lines / MOE_WAVES, (wave + 1) * lines / MOE_WAVES, xrow,
-                                      (int64_t)a.T * a.top_k * a.I, acc);
-    Join::put(sums, wave, acc);
+    const int32_t expert = __builtin_amdgcn_readfirstlane(list.expert);
+    const int32_t at = (int32_t)blockIdx.z * 16, rows = min(16, __builtin_amdgcn_readfirstlane(list.count) - at);
+    const int32_t per = W4_WAVES / g.kw * g.each, t0 = (int32_t)blockIdx.x * per, have = min(per, a.H / 16 - t0);
+    const int32_t lines = (a.I + 255) / 256, share = wave % g.kw, mine = wave / g.kw * g.each;
+    const int32_t slot = rows * W4_SLOT_LD, row = min(lane & 15, rows - 1);
+    const int64_t plane = (int64_t)a.T * a.top_k * a.I;
+    auto row_at = [&](int32_t r) {
+        const int32_t p = r >= rows;
+        return (const __bf16 *)a.h + p * plane + (int64_t)list.row[at + r - p * rows] * a.I;
+    };
+    const uint32_t xat[1] = {XLDS ? (uint32_t)row * stride : (uint32_t)list.row[at + row] * (uint32_t)a.I * 2u};
+    W4Stage<decltype(row_at)> stage(smem, a.I, 2 * rows, 64 * W4_WAVES, row_at);
+    if constexpr (XLDS) stage.first();
+    w4_stream<__bf16, T, 1, G, 2, XLDS, DEPTH>(
+        a.w2, (const uint32_t *)a.p2, a.I, share * lines / g.kw, (share + 1) * lines / g.kw, max(0, min(g.each, have - mine)),
+        w4_rsrc(a.h, 0xFFFFFFF0u), smem, xat, XLDS ? (uint32_t)rows * stride : (uint32_t)plane * 2u,
+        [&](int32_t t) { return W4Tile{(int64_t)expert * a.H + (t0 + mine + t) * 16, 16}; },
+        [&] {
+            if constexpr (XLDS) stage.rest();
+        },
+        [&](int32_t t, const f32x4(&acc)[1]) { w4_put<1>(slots + (wave * g.each + t) * slot, rows, acc); });
     __syncthreads();
-    for (int32_t i = (int32_t)threadIdx.x; i < 32 * rows; i += 64 * MOE_WAVES) {
-        const int32_t m = i / 32, n = i % 32;
-        if (c0 + n < a.H) a.y[(int64_t)list.row[at + m] * a.H + c0 + n] = Join::sum(sums, m, n);
+    for (int32_t i = (int32_t)threadIdx.x; i < rows * have * 16; i += 64 * W4_WAVES) {
+        const int32_t m = i / (have * 16), c = i - m * have * 16, t = c / 16;
+        const float *s = slots + (t / g.each * g.kw * g.each + t % g.each) * slot + m * W4_SLOT_LD + c % 16;
+        float v = 0.f;
+        for (int32_t k = 0; k < g.kw; ++k)
+            if (k * lines / g.kw < (k + 1) * lines / g.kw) v += s[k * g.each * slot];
+        a.y[(int64_t)list.row[at + m] * a.H + t0 * 16 + c] = v;
     }
 }
 
@@ -182,24 +242,20 @@ enum { COMBINE_THREADS = 256, MOE_TOP_MAX = 64 };
 template <class T>
 __global__ __launch_bounds__(COMBINE_THREADS) void moe_combine_kernel(MoeArgs a)
 {
+    __shared__ uint32_t order[EXPERTS_MAX];
     __shared__ float part[COMBINE_THREADS / 64], chosen[MOE_TOP_MAX];
-    __shared__ float largest;
     const int32_t t = (int32_t)blockIdx.y, tid = (int32_t)threadIdx.x;
     const float *row = a.logits + t * a.E;
+    put_orders(order, row, a.E, COMBINE_THREADS);
     for (int32_t e = tid; e < a.E; e += COMBINE_THREADS) {
-        const uint32_t mine = order_of(row[e]);
-        int32_t above = 0;
-        for (int32_t f = 0; f < a.E; ++f) {
-            const uint32_t o = order_of(row[f]);
-            above += o > mine || (o == mine && f < e);
-        }
+        const int32_t above = rank_of(order, a.E, e, order[e]);
         if (above < a.top_k) {
             chosen[above] = row[e];
             if (a.ids && blockIdx.x == 0) a.ids[t * a.top_k + above] = e;
         }
-        if (above == 0) largest = row[e];
     }
     __syncthreads();
+    const float largest = chosen[0];
     float total = 0.f;
     if (a.renorm) {
         for (int32_t j = 0; j < a.top_k; ++j) total += expf(chosen[j] - largest);
@@ -226,24 +282,58 @@ __global__ __launch_bounds__(COMBINE_THREADS) void moe_combine_kernel(MoeArgs a)
     *(u32x2 *)((T *)a.out + (int64_t)t * a.H + c) = u32x2{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3])};
 }
 
-template <class T, int G> static hipError_t moe_t(const MoeArgs &a, hipStream_t s)
+// The workgroups of one of the two products: `tiles` per expert, `slots` experts or pairs, LDS for x
+// and for the sums of `per_tile` tiles of 16 columns each.
+struct MoeShape {
+    MoeGrid g;
+    uint32_t x, lds;
+    bool xlds;
+};
+enum { MOE_LDS = 150 * 1024 };
+static MoeShape moe_shape(const MoeArgs &a, int64_t tiles, int32_t K, int planes, int per_tile, int64_t slots, int cu)
 {
-    const bool by_pair = a.T * a.top_k < a.E;
-    const uint32_t slots = (uint32_t)(by_pair ? a.T * a.top_k : a.E), passes = (uint32_t)(a.T + 15) / 16;
+    MoeShape m;
+    m.g.by_pair = a.T * a.top_k < a.E;
+    m.g.lds_rows = a.T < 16 ? a.T : 16;
+    // about two workgroups to a compute unit
+    int64_t per = (tiles * slots + 2 * cu - 1) / (2 * cu);
+    const int64_t most = 32 * 1024 / (m.g.lds_rows * W4_SLOT_LD * 4 * per_tile);   // tiles whose sums LDS has room for
+    if (per > tiles) per = tiles;
+    W4Split sp = w4_split(per, (K + 255) / 256);
+    while (per > 1 && W4_WAVES * sp.each > most) sp = w4_split(--per, (K + 255) / 256);
+    m.g.kw = sp.kw;
+    m.g.each = sp.each;
+    const int64_t wide = (int64_t)(W4_WAVES / sp.kw) * sp.each;
+    m.x = (uint32_t)((tiles + wide - 1) / wide);
+    const int64_t sums = (int64_t)W4_WAVES * sp.each * per_tile * m.g.lds_rows * W4_SLOT_LD * 4;
+    const int64_t x = (int64_t)planes * m.g.lds_rows * w4_x_stride(K);
+    m.xlds = sums + x <= MOE_LDS;
+    m.lds = (uint32_t)max((int64_t)EXPERTS_MAX * 4, sums + (m.xlds ? x : 0));
+    return m;
+}
+
+template <class T, int G> static hipError_t moe_t(const MoeArgs &a, int cu, hipStream_t s)
+{
+    const uint32_t passes = (uint32_t)(a.T + 15) / 16, slots = (uint32_t)min(a.T * a.top_k, a.E);
+    const dim3 block(64 * W4_WAVES);
     hipLaunchKernelGGL((moe_router_kernel<T>), dim3((uint32_t)(a.E + 15) / 16, passes), dim3(64 * ROUTER_WAVES), 0, s, a);
-    hipLaunchKernelGGL((moe_up_kernel<T, G>), dim3((uint32_t)a.I / 16, slots, passes), dim3(64 * MOE_WAVES), 0, s, a, by_pair);
-    hipLaunchKernelGGL((moe_down_kernel<T, G>), dim3((uint32_t)(a.H + 31) / 32, slots, passes), dim3(64 * MOE_WAVES), 0, s, a, by_pair);
+    const MoeShape up = moe_shape(a, a.I / 16, a.H, 1, 2, slots, cu);
+    if (up.xlds) hipLaunchKernelGGL((moe_up_kernel<T, G, true, 3>), dim3(up.x, slots, passes), block, up.lds, s, a, up.g);
+    else hipLaunchKernelGGL((moe_up_kernel<T, G, false, 3>), dim3(up.x, slots, passes), block, up.lds, s, a, up.g);
+    const MoeShape dn = moe_shape(a, a.H / 16, a.I, 2, 1, slots, cu);
+    if (dn.xlds) hipLaunchKernelGGL((moe_down_kernel<T, G, true, 3>), dim3(dn.x, slots, passes), block, dn.lds, s, a, dn.g);
+    else hipLaunchKernelGGL((moe_down_kernel<T, G, false, 3>), dim3(dn.x, slots, passes), block, dn.lds, s, a, dn.g);
     hipLaunchKernelGGL((moe_combine_kernel<T>), dim3((uint32_t)(a.H + 4 * COMBINE_THREADS - 1) / (4 * COMBINE_THREADS), (uint32_t)a.T),
                        dim3(COMBINE_THREADS), 0, s, a);
     return hipGetLastError();
 }
 
-hipError_t launch_moe_w4(int ftype, int group, const MoeArgs &a, hipStream_t s)
+hipError_t launch_moe_w4(int ftype, int group, const MoeArgs &a, int cu, hipStream_t s)
 {
     if (ftype == LB_BF16)
-        return group == 32 ? moe_t<__bf16, 32>(a, s) : group == 64 ? moe_t<__bf16, 64>(a, s) : moe_t<__bf16, 128>(a, s);
+        return group == 32 ? moe_t<__bf16, 32>(a, cu, s) : group == 64 ? moe_t<__bf16, 64>(a, cu, s) : moe_t<__bf16, 128>(a, cu, s);
     if (ftype == LB_F16)
-        return group == 32 ? moe_t<_Float16, 32>(a, s) : group == 64 ? moe_t<_Float16, 64>(a, s) : moe_t<_Float16, 128>(a, s);
+        return group == 32 ? moe_t<_Float16, 32>(a, cu, s) : group == 64 ? moe_t<_Float16, 64>(a, cu, s) : moe_t<_Float16, 128>(a, cu, s);
     return hipErrorInvalidValue;
 }
 

@@ -90,130 +90,256 @@ __device__ inline void w4_transpose(u32x4 &p)
     p[3] = d[1];
 }
 
-// A tile of 16 NT rows of weights against 16 MT rows of x, lines `first` to `last` of K.
-//   w, wbytes: the tile's first row and the bytes from there to the operand's end (rows
-//     past it read as zeros); prm likewise, the groups' (scale, minimum) words.
-//   xrow[m]: this lane's row (16 m + lane % 16) of x, any valid row where there is none;
-//     PLANES 2: x is the sum of two planes, `plane` elements apart.
-//   tile_rows: rows between the first rows of two tiles of weights.
-//   T: the type of x as the matrix cores take it; PT: of the groups' numbers.
-//   acc[m][n][i]: row 4 (lane / 16) + i of tile m of x, row lane % 16 of tile n of weights.
-template <class T, class PT, int MT, int NT, int G, int PLANES = 1>
-__device__ inline void w4_product(const uint8_t *w, uint64_t wbytes, const uint32_t *prm, uint64_t pbytes, int32_t K,
-                                  int32_t tile_rows, int32_t first, int32_t last, const T *const (&xrow)[MT], int64_t plane,
-                                  f32x4 (&acc)[MT][NT])
+// One row tile's numbers of a line: GROUPS words (scale, minimum) of row lane % 16.
+template <int GROUPS> __device__ inline void w4_numbers(const __amdgpu_buffer_rsrc_t &rsrc, uint32_t at, int32_t left, uint32_t (&v)[GROUPS])
 {
-    constexpr int GROUPS = 256 / G, STEPS = G / 32;
+    if (left >= GROUPS) {
+        if constexpr (GROUPS == 2) {
+            const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rsrc, (int)at, 0, 0));
+            v[0] = a[0], v[1] = a[1];
+        } else {
+#pragma unroll
+            for (int g = 0; g < GROUPS; g += 4) {
+                const u32x4 a = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, (int)(at + 4u * g), 0, 0));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[g + i] = a[i];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g)
+            v[g] = g < left ? (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rsrc, (int)(at + 4u * g), 0, 0) : 0u;
+    }
+}
+
+__device__ inline __amdgpu_buffer_rsrc_t w4_rsrc(const void *base, uint64_t bytes)
+{
+    const i32x4 r = make_rsrc(base, bytes);
+    const uint64_t b = (uint64_t)(uint32_t)r.x | ((uint64_t)((uint32_t)r.y & 0xFFFFu) << 32);
+    return __builtin_amdgcn_make_buffer_rsrc((void *)(uintptr_t)b, (short)0, r.z, r.w);
+}
+__device__ inline u32x4 w4_load(const __amdgpu_buffer_rsrc_t &rsrc, uint32_t at)
+{
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, (int)at, 0, 0));
+}
+
+// The sixteen rows of weights of a tile, at row `row` of the operand; rows from `rows` on do not
+// exist and read as zeros.
+struct W4Tile {
+    int64_t row;
+    int32_t rows;
+};
+
+// Activations in LDS: rows of w4_x_stride(K) bytes (K up to whole lines, the rest zeros; 16
+// bytes more, so that 16 rows' pieces lie on all banks once), in the order of the levels.
+// first() takes what a batch of loads covers (8 of 16 bytes a thread) to registers, rest()
+// writes it to LDS and brings whatever is left: between the two a wave asks for its first
+// weights, whose latency then runs beside the copy.
+__host__ __device__ inline uint32_t w4_x_stride(int32_t K) { return (uint32_t)((K + 255) / 256) * 512u + 16u; }
+
+template <class RowAt> struct W4Stage {
+    enum : int { BATCH = 8 };
+    char *lds;
+    int32_t K, pieces, all, threads;   // pieces of 16 bytes of a row, and of all rows
+    RowAt row_at;                      // (row) -> its first element
+    u32x4 v[BATCH];
+    __device__ inline W4Stage(char *l, int32_t k, int32_t rows, int32_t n, const RowAt &at)
+        : lds(l), K(k), pieces((k + 255) / 256 * 32), all((k + 255) / 256 * 32 * rows), threads(n), row_at(at)
+    {
+    }
+    __device__ inline void fetch(int32_t i0)
+    {
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+            const int32_t i = i0 + b * threads;
+            v[b] = u32x4{0u, 0u, 0u, 0u};
+            if (i < all) {
+                const int32_t row = i / pieces, at = i - row * pieces;
+                if (8 * at < K) v[b] = ((const u32x4 *)row_at(row))[at];
+            }
+        }
+    }
+    __device__ inline void write(int32_t i0)
+    {
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+            const int32_t i = i0 + b * threads;
+            if (i < all) {
+                const int32_t row = i / pieces, at = i - row * pieces;
+                *(u32x4 *)(lds + (uint32_t)row * w4_x_stride(K) + 16u * (uint32_t)at) = w4_order(v[b]);
+            }
+        }
+    }
+    __device__ inline void first() { fetch((int32_t)threadIdx.x); }
+    __device__ inline void rest()
+    {
+        write((int32_t)threadIdx.x);
+        for (int32_t i = (int32_t)threadIdx.x + BATCH * threads; i < all; i += BATCH * threads) {
+            fetch(i);
+            write(i);
+        }
+        __syncthreads();
+    }
+};
+
+// The stream of a wave: lines `first` to `last` of K of its tiles, one tile after another,
+// DEPTH lines of weights on their way.
+//   tile_at(t): the W4Tile of tile t of `tiles`.
+//   ready(): called by every wave once its first loads are under way.
+//   done(t, acc): its sums; acc[m][i] is row 4 (lane / 16) + i of tile m of x, column lane % 16.
+// x: XLDS: in LDS as W4Stage leaves it, row 16 m + lane % 16 at xat[m], PLANES 2: the sum of two
+// planes, `plane` bytes apart.  Otherwise in memory, xat and plane byte offsets in rx, loaded
+// half a line ahead.
+//   T: the type of x as the matrix cores take it; PT: of the groups' numbers.
+template <class T, class PT, int MT, int G, int PLANES, bool XLDS, int DEPTH, class TileAt, class Ready, class Done>
+__device__ inline void w4_stream(const uint8_t *W, const uint32_t *P, int32_t K, int32_t first, int32_t last, int32_t tiles,
+                                 const __amdgpu_buffer_rsrc_t &rx, const char *xlds, const uint32_t (&xat)[MT],
+                                 uint32_t plane, TileAt &&tile_at, Ready &&ready, Done &&done)
+{
+    constexpr int GROUPS = 256 / G, HALF = GROUPS / 2, STEPS = G / 32;
+    const int32_t share = last - first, items = share * tiles;
+    if (items <= 0) {
+        ready();
+        return;
+    }
     const int32_t lane = (int32_t)(threadIdx.x & 63u), q = lane >> 4, r = lane & 15;
-    const i32x4 rw = make_rsrc(w, wbytes), rp = make_rsrc(prm, pbytes);
     const uint32_t kb = (uint32_t)K / 2u, groups = (uint32_t)K / G;
     const uint32_t piece = (uint32_t)(16 * (4 * ((lane >> 3) & 1) + q));
-    const uint32_t row_at = (uint32_t)(lane & 7) * kb;
-    u32x4 wv[NT][2];
-    uint32_t pv[NT][GROUPS];
-    auto load_line = [&](int32_t line) {
-        const uint32_t at = (uint32_t)line * 128u + piece;
-        const bool in = line < last && at < kb;
+    const uint32_t row_at = (uint32_t)(lane & 7) * kb + piece, p_at = (uint32_t)r * groups * 4u;
+
+    u32x4 wv[DEPTH][2];
+    uint32_t pv[DEPTH][GROUPS];
+    int32_t load_tile = 0, load_line = first;   // what is loaded next
+    auto load = [&](u32x4 (&w)[2], uint32_t (&p)[GROUPS]) {
+        if (load_tile >= tiles) return;
+        const W4Tile t = tile_at(load_tile);
+        const __amdgpu_buffer_rsrc_t rw = w4_rsrc(W + t.row * kb, (uint64_t)(uint32_t)t.rows * kb);
+        const __amdgpu_buffer_rsrc_t rp = w4_rsrc(P + t.row * groups, (uint64_t)(uint32_t)t.rows * groups * 4u);
+        const uint32_t at = (uint32_t)load_line * 128u;
+        const bool in = at + piece < kb;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                wv[n][i] = __builtin_bit_cast(u32x4, load16(rw, in ? row_at + (uint32_t)(tile_rows * n + 8 * i) * kb + at : 0xFFFFFFF0u));
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int g = 0; g < GROUPS; ++g) {
-                const uint32_t gi = (uint32_t)(line * GROUPS + g);
-                const uint64_t b = (uint64_t)(uint32_t)rp.x | ((uint64_t)((uint32_t)rp.y & 0xFFFFu) << 32);
-                const __amdgpu_buffer_rsrc_t br = __builtin_amdgcn_make_buffer_rsrc((void *)(uintptr_t)b, (short)0, rp.z, rp.w);
-                pv[n][g] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
-                    br, (int)(line < last && gi < groups ? ((uint32_t)(tile_rows * n + r) * groups + gi) * 4u : 0xFFFFFFFCu), 0, 0);
-            }
+        for (int i = 0; i < 2; ++i) w[i] = w4_load(rw, in ? row_at + (uint32_t)(8 * i) * kb + at : 0xFFFFFFF0u);
+        w4_numbers<GROUPS>(rp, p_at + (uint32_t)(load_line * GROUPS) * 4u, (int32_t)groups - load_line * GROUPS, p);
+        if (++load_line == last) {
+            load_line = first;
+            ++load_tile;
+        }
     };
-    load_line(first);
-    for (int32_t line = first; line < last; ++line) {
-        u32x4 cw[NT][2];
-        uint32_t cp[NT][GROUPS];
+    u32x4 xv[2][MT][4][PLANES];
+    auto load_x = [&](int h, int32_t line) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            cw[n][0] = wv[n][0];
-            cw[n][1] = wv[n][1];
+        for (int st = 0; st < 4; ++st)
 #pragma unroll
-            for (int g = 0; g < GROUPS; ++g) cp[n][g] = pv[n][g];
-        }
-        load_line(line + 1);
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            w4_rows(cw[n][0], cw[n][1]);
-            w4_transpose(cw[n][0]);
-            w4_transpose(cw[n][1]);
-        }
+                for (int pl = 0; pl < PLANES; ++pl) {
+                    const int32_t k = line * 256 + 128 * h + 32 * st + 8 * q;
+                    if constexpr (XLDS)
+                        xv[h][m][st][pl] = *(const u32x4 *)(xlds + xat[m] + pl * plane + (uint32_t)(2 * k));
+                    else
+                        xv[h][m][st][pl] = w4_load(rx, k < K ? xat[m] + pl * plane + (uint32_t)(2 * k) : 0xFFFFFFF0u);
+                }
+    };
+
+    f32x4 acc[MT];
 #pragma unroll
-        for (int g = 0; g < GROUPS; ++g) {
-            f32x4 sum[MT][NT], xs[MT];
+    for (int m = 0; m < MT; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto half = [&](int h, const u32x4 &w, const uint32_t (&p)[GROUPS]) {   // 128 weights
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                xs[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int g = 0; g < HALF; ++g) {
+            f32x4 sum[MT], xs[MT];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) sum[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-            }
+            for (int m = 0; m < MT; ++m) sum[m] = xs[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int st = 0; st < STEPS; ++st) {
-                const int j = g * STEPS + st;   // 32 weights of the line
-                const int32_t k = line * 256 + 32 * j + 8 * q;
-                u32x4 lv[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) lv[n] = w4_levels<T>(cw[n][j / 4][j % 4]);
+                const int j = g * STEPS + st;   // 32 weights of the half
+                const u32x4 lv = w4_levels<T>(w[j]);
+                const uint32_t one = one_pair<T>();
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
                     for (int pl = 0; pl < PLANES; ++pl) {
-                        u32x4 x = {0u, 0u, 0u, 0u};
-                        if (k < K) x = w4_order(*(const u32x4 *)(xrow[m] + pl * plane + k));
-                        const uint32_t one = one_pair<T>();
+                        const u32x4 x = XLDS ? xv[h][m][j][pl] : w4_order(xv[h][m][j][pl]);
                         xs[m] = mfma16<T>(x, u32x4{one, one, one, one}, xs[m]);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) sum[m][n] = mfma16<T>(x, lv[n], sum[m][n]);
+                        sum[m] = mfma16<T>(x, lv, sum[m]);
                     }
             }
+            const float s = lo_f32<PT>(p[h * HALF + g]), c = hi_f32<PT>(p[h * HALF + g]) - 16.0f * s;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float s = lo_f32<PT>(cp[n][g]), c = hi_f32<PT>(cp[n][g]) - 16.0f * s;
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
+                for (int i = 0; i < 4; ++i) {
+                    acc[m][i] = __builtin_fmaf(s, sum[m][i], acc[m][i]);
+                    acc[m][i] = __builtin_fmaf(c, xs[m][i], acc[m][i]);
+                }
+        }
+    };
+
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        acc[m][n][i] = __builtin_fmaf(s, sum[m][n][i], acc[m][n][i]);
-                        acc[m][n][i] = __builtin_fmaf(c, xs[m][i], acc[m][n][i]);
-                    }
+    for (int d = 0; d < DEPTH; ++d) load(wv[d], pv[d]);
+    ready();
+    load_x(0, first);
+    int32_t tile = 0, line = first;
+    for (int32_t i = 0; i < items; i += DEPTH) {
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+            if (i + d >= items) break;
+            u32x4 w0 = wv[d][0], w1 = wv[d][1];
+            uint32_t p[GROUPS];
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g) p[g] = pv[d][g];
+            w4_rows(w0, w1);
+            w4_transpose(w0);
+            w4_transpose(w1);
+            load(wv[d], pv[d]);
+            load_x(1, line);
+            half(0, w0, p);
+            const int32_t now = tile;
+            const bool end = ++line == last;
+            if (end) {
+                line = first;
+                ++tile;
+            }
+            load_x(0, line);
+            half(1, w1, p);
+            if (end) {
+                done(now, acc);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
             }
         }
     }
 }
 
-// Sums of the waves' tiles, in a fixed order, into LDS: NW tiles of 16 MT x 16 NT floats there,
-// rows of x of 16 NT + 4 (so that a lane's four rows lie on other banks).  Afterwards
-// w4_sum(lds, m, n) is the total; a barrier has passed.
-template <int MT, int NT, int NW>
-struct W4Join {
-    enum : int { LD = 16 * NT + 4, TILE = 16 * MT * LD, FLOATS = NW * TILE };
-    static __device__ inline void put(float *lds, int wave, const f32x4 (&acc)[MT][NT])
-    {
-        const int lane = (int)(threadIdx.x & 63u), q = lane >> 4, r = lane & 15;
+// Waves' sums in LDS: `rows` rows of x by 16 columns, rows 20 floats apart (a lane's four rows lie
+// on other banks).
+enum { W4_SLOT_LD = 20 };
+template <int MT> __device__ inline void w4_put(float *slot, int32_t rows, const f32x4 (&acc)[MT])
+{
+    const int lane = (int)(threadIdx.x & 63u), q = lane >> 4, r = lane & 15;
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) lds[wave * TILE + (16 * m + 4 * q + i) * LD + 16 * n + r] = acc[m][n][i];
-    }
-    static __device__ inline float sum(const float *lds, int m, int n)
-    {
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) v += lds[w * TILE + m * LD + n];
-        return v;
-    }
+        for (int i = 0; i < 4; ++i)
+            if (16 * m + 4 * q + i < rows) slot[(16 * m + 4 * q + i) * W4_SLOT_LD + r] = acc[m][i];
+}
+
+// How a workgroup of eight waves shares its tiles: kw waves take a share of K each, of `each`
+// tiles, the next kw waves of the next ones.
+constexpr int W4_WAVES = 8;
+struct W4Split {
+    int32_t kw, each;
 };
+// For `tiles` tiles of `lines` lines: the fewest lines for the busiest wave, and of equals the
+// fewest shares.
+inline W4Split w4_split(int64_t tiles, int64_t lines)
+{
+    W4Split best{1, (int32_t)((tiles + W4_WAVES - 1) / W4_WAVES)};
+    for (int kw = 2; kw <= W4_WAVES; kw *= 2) {
+        const W4Split s{kw, (int32_t)((tiles + W4_WAVES / kw - 1) / (W4_WAVES / kw))};
+        if ((lines + kw - 1) / kw * s.each < (lines + best.kw - 1) / best.kw * best.each) best = s;
+    }
+    return best;
+}
 
 }  // namespace lb
