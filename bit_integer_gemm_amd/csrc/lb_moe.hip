@@ -9,6 +9,8 @@
 // a workgroup finds the tokens of its expert from the logits itself (an expert's rank in a
 // token's order is the number of larger logits, a few ballots), and results lie at (token,
 // rank), so that every sum has a fixed order.
+#include <algorithm>
+
 #include "lb_internal.hpp"
 #include "lb_w4.hpp"
 
@@ -50,7 +52,7 @@ __global__ __launch_bounds__(64 * ROUTER_WAVES) void moe_router_kernel(MoeArgs a
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[0] = mfma16<T>(x[i], w[i], acc[0]);
     }
-    w4_put<1>(sums[wave], 16, acc);
+    w4_put<1>(sums[wave], 16, acc, false);
     __syncthreads();
     if (threadIdx.x < 256) {
         const int32_t m = (int32_t)threadIdx.x / 16, n = (int32_t)threadIdx.x % 16;
@@ -93,7 +95,7 @@ __device__ inline void put_orders(uint32_t *order, const float *row, int32_t E, 
 // order: LDS for EXPERTS_MAX words, free again afterwards.
 __device__ inline bool moe_list(const MoeArgs &a, int32_t slot, bool by_pair, MoeList &l, uint32_t *order)
 {
-    constexpr int NW = W4_WAVES, AT_ONCE = MOE_TOKENS / NW;
+    constexpr int NW = W4_WAVES, AT_ONCE = (MOE_TOKENS + NW - 1) / NW;
     const int32_t tid = (int32_t)threadIdx.x, lane = tid & 63, wave = tid >> 6;
     if (by_pair) {
         const int32_t t = slot / a.top_k, j = slot % a.top_k;
@@ -139,101 +141,118 @@ __device__ inline bool moe_list(const MoeArgs &a, int32_t slot, bool by_pair, Mo
         if (lane == 0) l.count = (by_pair && (in & ((1ull << l.first) - 1))) ? 0 : __popcll(in);
     }
     __syncthreads();
-    return l.count > (int32_t)blockIdx.z * 16;
+    return l.count > 0;
 }
 
 // ---- gate and up, activation -----------------------------------------------
-// A workgroup: an expert, some blocks of 16 columns (each a tile of gate rows and one of up rows),
-// at most 16 of its tokens.
+// A workgroup: an expert, some blocks of 16 columns, g.rows of its tokens at a time.
 struct MoeGrid {
     bool by_pair;
-    int32_t kw, each, lds_rows;   // W4Split over blocks (up) or tiles (down), rows that LDS is laid out for
+    int32_t rows;    // tokens at a time, at most 16
+    W4Split sp;      // of blocks (up: a tile of gate rows and one of up rows each) or tiles (down)
 };
-template <class T, int G, bool XLDS, int DEPTH>
+template <class T, int G>
 __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGrid g)
 {
-    extern __shared__ __attribute__((aligned(16))) char smem[];
+    extern __shared__ __attribute__((aligned(1024))) char smem[];
     __shared__ MoeList list;
-    const uint32_t stride = w4_x_stride(a.H);
-    float *const slots = (float *)(smem + (XLDS ? (uint32_t)g.lds_rows * stride : 0u));
     if (!moe_list(a, (int32_t)blockIdx.y, g.by_pair, list, (uint32_t *)smem)) return;
-    const int32_t lane = (int32_t)(threadIdx.x & 63u);
+    const int32_t lane = (int32_t)(threadIdx.x & 63u), q = lane >> 4, r = lane & 15;
     const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int32_t expert = __builtin_amdgcn_readfirstlane(list.expert);
-    const int32_t at = (int32_t)blockIdx.z * 16, rows = min(16, __builtin_amdgcn_readfirstlane(list.count) - at);
-    const int32_t per = W4_WAVES / g.kw * g.each, b0 = (int32_t)blockIdx.x * per, have = min(per, a.I / 16 - b0);
-    const int32_t lines = (a.H + 255) / 256, share = wave % g.kw, mine = wave / g.kw * g.each;
-    const int32_t slot = rows * W4_SLOT_LD, row = min(lane & 15, rows - 1);
-    auto row_at = [&](int32_t r) { return (const T *)a.x + (int64_t)(list.row[at + r] / a.top_k) * a.ldx; };
-    const uint32_t xat[1] = {XLDS ? (uint32_t)row * stride : (uint32_t)(list.row[at + row] / a.top_k) * (uint32_t)a.ldx * 2u};
-    W4Stage<decltype(row_at)> stage(smem, a.H, rows, 64 * W4_WAVES, row_at);
-    if constexpr (XLDS) stage.first();
-    w4_stream<T, T, 1, G, 1, XLDS, DEPTH>(
-        a.w1, (const uint32_t *)a.p1, a.H, share * lines / g.kw, (share + 1) * lines / g.kw, 2 * max(0, min(g.each, have - mine)),
-        w4_rsrc(a.x, 0xFFFFFFF0u), smem, xat, 0u,
-        [&](int32_t t) { return W4Tile{((int64_t)expert * 2 + t % 2) * a.I + (b0 + mine + t / 2) * 16, 16}; },
-        [&] {
-            if constexpr (XLDS) stage.rest();
-        },
-        [&](int32_t t, const f32x4(&acc)[1]) { w4_put<1>(slots + (wave * 2 * g.each + t) * slot, rows, acc); });
-    __syncthreads();
+    const int32_t expert = __builtin_amdgcn_readfirstlane(list.expert), count = __builtin_amdgcn_readfirstlane(list.count);
+    const int32_t kw = g.sp.kw, each = g.sp.each, lines = (a.H + 255) / 256;
+    const int32_t per = W4_WAVES / kw * each, b0 = (int32_t)blockIdx.x * per, have = min(per, a.I / 16 - b0);
+    const int32_t mine = wave / kw * each;
+    float *const slots = (float *)(smem + W4Lds<G>::x_bytes(g.rows, g.sp.chunk) + W4Lds<G>::RINGS);
     __bf16 *const hi = (__bf16 *)a.h, *const lo = hi + (int64_t)a.T * a.top_k * a.I;
-    for (int32_t i = (int32_t)threadIdx.x; i < rows * have * 16; i += 64 * W4_WAVES) {
-        const int32_t m = i / (have * 16), c = i - m * have * 16, b = c / 16;
-        const float *s = slots + (b / g.each * g.kw * 2 * g.each + b % g.each * 2) * slot + m * W4_SLOT_LD + c % 16;
-        float gate = 0.f, up = 0.f;
-        for (int32_t k = 0; k < g.kw; ++k)
-            if (k * lines / g.kw < (k + 1) * lines / g.kw) {
-                gate += s[k * 2 * g.each * slot];
-                up += s[(k * 2 * g.each + 1) * slot];
-            }
+    auto put = [&](int32_t m, int32_t c, float gate, float up) {
         const float h = gate / (1.0f + __expf(-gate)) * up;
-        const int64_t o = (int64_t)list.row[at + m] * a.I + b0 * 16 + c;
-        hi[o] = (__bf16)h;
-        lo[o] = (__bf16)(h - (float)hi[o]);
+        const int64_t o = (int64_t)list.row[m] * a.I + b0 * 16 + c;
+        const __bf16 top = (__bf16)h;
+        hi[o] = top;
+        lo[o] = (__bf16)(h - (float)top);
+    };
+    for (int32_t at = 0; at < count; at += g.rows) {
+        const int32_t rows = min(g.rows, count - at), slot = rows * W4_SLOT_LD;
+        const bool direct = kw == 1 && g.sp.chunk >= lines;   // a wave has whole sums
+        f32x4 gate[1];
+        if (at) __syncthreads();
+        w4_flow<T, T, 1, G, 1>(
+            smem, a.w1, (const uint32_t *)a.p1, a.H, rows, g.sp, 2 * max(0, min(each, have - mine)), make_rsrc(a.x, 0xFFFFFFF0u),
+            [&](int32_t i) { return (uint32_t)(list.row[at + i] / a.top_k) * (uint32_t)a.ldx * 2u; },
+            [&](int32_t t) { return W4Tile{((int64_t)expert * 2 + t % 2) * a.I + (b0 + mine + t / 2) * 16, 16}; },
+            [&](int32_t t, const f32x4(&acc)[1], bool more) {
+                if (!direct) {
+                    w4_put<1>(slots + (wave * 2 * each + t) * slot, rows, acc, more);
+                } else if (t % 2 == 0) {
+                    gate[0] = acc[0];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (4 * q + i < rows) put(at + 4 * q + i, (mine + t / 2) * 16 + r, gate[0][i], acc[0][i]);
+                }
+            });
+        if (direct) continue;
+        __syncthreads();
+        for (int32_t i = (int32_t)threadIdx.x; i < rows * have * 16; i += 64 * W4_WAVES) {
+            const int32_t m = i / (have * 16), c = i - m * have * 16, b = c / 16;
+            const float *s = slots + (b / each * kw * 2 * each + b % each * 2) * slot + m * W4_SLOT_LD + c % 16;
+            float v = 0.f, u = 0.f;
+            for (int32_t k = 0; k < kw; ++k)
+                if (k * lines / kw < (k + 1) * lines / kw) {
+                    v += s[k * 2 * each * slot];
+                    u += s[(k * 2 * each + 1) * slot];
+                }
+            put(at + m, c, v, u);
+        }
     }
 }
 
 // ---- down ------------------------------------------------------------------
-template <class T, int G, bool XLDS, int DEPTH>
+template <class T, int G>
 __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_kernel(MoeArgs a, MoeGrid g)
 {
-    extern __shared__ __attribute__((aligned(16))) char smem[];
+    extern __shared__ __attribute__((aligned(1024))) char smem[];
     __shared__ MoeList list;
-    const uint32_t stride = w4_x_stride(a.I);
-    float *const slots = (float *)(smem + (XLDS ? 2u * (uint32_t)g.lds_rows * stride : 0u));
     if (!moe_list(a, (int32_t)blockIdx.y, g.by_pair, list, (uint32_t *)smem)) return;
-    const int32_t lane = (int32_t)(threadIdx.x & 63u);
+    const int32_t lane = (int32_t)(threadIdx.x & 63u), q = lane >> 4, r = lane & 15;
     const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int32_t expert = __builtin_amdgcn_readfirstlane(list.expert);
-    const int32_t at = (int32_t)blockIdx.z * 16, rows = min(16, __builtin_amdgcn_readfirstlane(list.count) - at);
-    const int32_t per = W4_WAVES / g.kw * g.each, t0 = (int32_t)blockIdx.x * per, have = min(per, a.H / 16 - t0);
-    const int32_t lines = (a.I + 255) / 256, share = wave % g.kw, mine = wave / g.kw * g.each;
-    const int32_t slot = rows * W4_SLOT_LD, row = min(lane & 15, rows - 1);
-    const int64_t plane = (int64_t)a.T * a.top_k * a.I;
-    auto row_at = [&](int32_t r) {
-        const int32_t p = r >= rows;
-        return (const __bf16 *)a.h + p * plane + (int64_t)list.row[at + r - p * rows] * a.I;
-    };
-    const uint32_t xat[1] = {XLDS ? (uint32_t)row * stride : (uint32_t)list.row[at + row] * (uint32_t)a.I * 2u};
-    W4Stage<decltype(row_at)> stage(smem, a.I, 2 * rows, 64 * W4_WAVES, row_at);
-    if constexpr (XLDS) stage.first();
-    w4_stream<__bf16, T, 1, G, 2, XLDS, DEPTH>(
-        a.w2, (const uint32_t *)a.p2, a.I, share * lines / g.kw, (share + 1) * lines / g.kw, max(0, min(g.each, have - mine)),
-        w4_rsrc(a.h, 0xFFFFFFF0u), smem, xat, XLDS ? (uint32_t)rows * stride : (uint32_t)plane * 2u,
-        [&](int32_t t) { return W4Tile{(int64_t)expert * a.H + (t0 + mine + t) * 16, 16}; },
-        [&] {
-            if constexpr (XLDS) stage.rest();
-        },
-        [&](int32_t t, const f32x4(&acc)[1]) { w4_put<1>(slots + (wave * g.each + t) * slot, rows, acc); });
-    __syncthreads();
-    for (int32_t i = (int32_t)threadIdx.x; i < rows * have * 16; i += 64 * W4_WAVES) {
-        const int32_t m = i / (have * 16), c = i - m * have * 16, t = c / 16;
-        const float *s = slots + (t / g.each * g.kw * g.each + t % g.each) * slot + m * W4_SLOT_LD + c % 16;
-        float v = 0.f;
-        for (int32_t k = 0; k < g.kw; ++k)
-            if (k * lines / g.kw < (k + 1) * lines / g.kw) v += s[k * g.each * slot];
-        a.y[(int64_t)list.row[at + m] * a.H + t0 * 16 + c] = v;
+    const int32_t expert = __builtin_amdgcn_readfirstlane(list.expert), count = __builtin_amdgcn_readfirstlane(list.count);
+    const int32_t kw = g.sp.kw, each = g.sp.each, lines = (a.I + 255) / 256;
+    const int32_t per = W4_WAVES / kw * each, t0 = (int32_t)blockIdx.x * per, have = min(per, a.H / 16 - t0);
+    const int32_t mine = wave / kw * each;
+    float *const slots = (float *)(smem + W4Lds<G>::x_bytes(2 * g.rows, g.sp.chunk) + W4Lds<G>::RINGS);
+    const uint32_t plane = (uint32_t)(a.T * a.top_k) * (uint32_t)a.I * 2u;
+    for (int32_t at = 0; at < count; at += g.rows) {
+        const int32_t rows = min(g.rows, count - at), slot = rows * W4_SLOT_LD;
+        const bool direct = kw == 1 && g.sp.chunk >= lines;
+        if (at) __syncthreads();
+        w4_flow<__bf16, T, 1, G, 2>(
+            smem, a.w2, (const uint32_t *)a.p2, a.I, rows, g.sp, max(0, min(each, have - mine)), make_rsrc(a.h, 0xFFFFFFF0u),
+            [&](int32_t i) {
+                const int32_t second = i >= rows;
+                return (uint32_t)list.row[at + i - (second ? rows : 0)] * (uint32_t)a.I * 2u + (second ? plane : 0u);
+            },
+            [&](int32_t t) { return W4Tile{(int64_t)expert * a.H + (t0 + mine + t) * 16, 16}; },
+            [&](int32_t t, const f32x4(&acc)[1], bool more) {
+                if (!direct) {
+                    w4_put<1>(slots + (wave * each + t) * slot, rows, acc, more);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (4 * q + i < rows) a.y[(int64_t)list.row[at + 4 * q + i] * a.H + (t0 + mine + t) * 16 + r] = acc[0][i];
+                }
+            });
+        if (direct) continue;
+        __syncthreads();
+        for (int32_t i = (int32_t)threadIdx.x; i < rows * have * 16; i += 64 * W4_WAVES) {
+            const int32_t m = i / (have * 16), c = i - m * have * 16, t = c / 16;
+            const float *s = slots + (t / each * kw * each + t % each) * slot + m * W4_SLOT_LD + c % 16;
+            float v = 0.f;
+            for (int32_t k = 0; k < kw; ++k)
+                if (k * lines / kw < (k + 1) * lines / kw) v += s[k * each * slot];
+            a.y[(int64_t)list.row[at + m] * a.H + t0 * 16 + c] = v;
+        }
     }
 }
 
@@ -282,47 +301,44 @@ __global__ __launch_bounds__(COMBINE_THREADS) void moe_combine_kernel(MoeArgs a)
     *(u32x2 *)((T *)a.out + (int64_t)t * a.H + c) = u32x2{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3])};
 }
 
-// The workgroups of one of the two products: `tiles` per expert, `slots` experts or pairs, LDS for x
-// and for the sums of `per_tile` tiles of 16 columns each.
+// One of the two products' workgroups: `tiles` per expert, `slots` experts or pairs, sums of
+// `per_tile` tiles of 16 columns each in LDS.
 struct MoeShape {
     MoeGrid g;
     uint32_t x, lds;
-    bool xlds;
 };
-enum { MOE_LDS = 150 * 1024 };
-static MoeShape moe_shape(const MoeArgs &a, int64_t tiles, int32_t K, int planes, int per_tile, int64_t slots, int cu)
+enum { MOE_LDS = 156 * 1024 };
+template <int G> static MoeShape moe_shape(const MoeArgs &a, int64_t tiles, int32_t K, int planes, int per_tile, int64_t slots, int cu)
 {
     MoeShape m;
     m.g.by_pair = a.T * a.top_k < a.E;
-    m.g.lds_rows = a.T < 16 ? a.T : 16;
-    // about two workgroups to a compute unit
-    int64_t per = (tiles * slots + 2 * cu - 1) / (2 * cu);
-    const int64_t most = 32 * 1024 / (m.g.lds_rows * W4_SLOT_LD * 4 * per_tile);   // tiles whose sums LDS has room for
-    if (per > tiles) per = tiles;
-    W4Split sp = w4_split(per, (K + 255) / 256);
-    while (per > 1 && W4_WAVES * sp.each > most) sp = w4_split(--per, (K + 255) / 256);
-    m.g.kw = sp.kw;
-    m.g.each = sp.each;
-    const int64_t wide = (int64_t)(W4_WAVES / sp.kw) * sp.each;
+    m.g.rows = a.T < 16 ? a.T : 16;
+    const int64_t lines = (K + 255) / 256, slot = (int64_t)m.g.rows * W4_SLOT_LD * 4 * per_tile, xrows = planes * m.g.rows;
+    // a workgroup to a compute unit
+    const int64_t wgs = std::max<int64_t>(1, cu / slots);
+    int64_t per = (tiles + wgs - 1) / wgs;
+    for (;; --per) {
+        m.g.sp = w4_split(per, lines, xrows, 66 * 1024);
+        const bool direct = m.g.sp.kw == 1 && m.g.sp.chunk >= lines;
+        const int64_t sums = direct ? 0 : W4_WAVES * m.g.sp.each * slot;
+        const int64_t lds = W4Lds<G>::x_bytes((int32_t)xrows, m.g.sp.chunk) + W4Lds<G>::RINGS + sums;
+        m.lds = (uint32_t)max((int64_t)EXPERTS_MAX * 4, lds);
+        if (m.lds <= MOE_LDS || per == 1) break;
+    }
+    const int64_t wide = (int64_t)(W4_WAVES / m.g.sp.kw) * m.g.sp.each;
     m.x = (uint32_t)((tiles + wide - 1) / wide);
-    const int64_t sums = (int64_t)W4_WAVES * sp.each * per_tile * m.g.lds_rows * W4_SLOT_LD * 4;
-    const int64_t x = (int64_t)planes * m.g.lds_rows * w4_x_stride(K);
-    m.xlds = sums + x <= MOE_LDS;
-    m.lds = (uint32_t)max((int64_t)EXPERTS_MAX * 4, sums + (m.xlds ? x : 0));
     return m;
 }
 
 template <class T, int G> static hipError_t moe_t(const MoeArgs &a, int cu, hipStream_t s)
 {
-    const uint32_t passes = (uint32_t)(a.T + 15) / 16, slots = (uint32_t)min(a.T * a.top_k, a.E);
+    const uint32_t slots = (uint32_t)min(a.T * a.top_k, a.E);
     const dim3 block(64 * W4_WAVES);
-    hipLaunchKernelGGL((moe_router_kernel<T>), dim3((uint32_t)(a.E + 15) / 16, passes), dim3(64 * ROUTER_WAVES), 0, s, a);
-    const MoeShape up = moe_shape(a, a.I / 16, a.H, 1, 2, slots, cu);
-    if (up.xlds) hipLaunchKernelGGL((moe_up_kernel<T, G, true, 3>), dim3(up.x, slots, passes), block, up.lds, s, a, up.g);
-    else hipLaunchKernelGGL((moe_up_kernel<T, G, false, 3>), dim3(up.x, slots, passes), block, up.lds, s, a, up.g);
-    const MoeShape dn = moe_shape(a, a.H / 16, a.I, 2, 1, slots, cu);
-    if (dn.xlds) hipLaunchKernelGGL((moe_down_kernel<T, G, true, 3>), dim3(dn.x, slots, passes), block, dn.lds, s, a, dn.g);
-    else hipLaunchKernelGGL((moe_down_kernel<T, G, false, 3>), dim3(dn.x, slots, passes), block, dn.lds, s, a, dn.g);
+    const MoeShape up = moe_shape<G>(a, a.I / 16, a.H, 1, 2, slots, cu), dn = moe_shape<G>(a, a.H / 16, a.I, 2, 1, slots, cu);
+    if (up.lds > MOE_LDS || dn.lds > MOE_LDS) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((moe_router_kernel<T>), dim3((uint32_t)(a.E + 15) / 16, (uint32_t)(a.T + 15) / 16), dim3(64 * ROUTER_WAVES), 0, s, a);
+    hipLaunchKernelGGL((moe_up_kernel<T, G>), dim3(up.x, slots), block, up.lds, s, a, up.g);
+    hipLaunchKernelGGL((moe_down_kernel<T, G>), dim3(dn.x, slots), block, dn.lds, s, a, dn.g);
     hipLaunchKernelGGL((moe_combine_kernel<T>), dim3((uint32_t)(a.H + 4 * COMBINE_THREADS - 1) / (4 * COMBINE_THREADS), (uint32_t)a.T),
                        dim3(COMBINE_THREADS), 0, s, a);
     return hipGetLastError();

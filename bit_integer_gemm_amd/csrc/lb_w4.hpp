@@ -8,14 +8,13 @@
 // two weights (the nibble is written into the mantissa of 16.0), and both sums come from the
 // matrix cores in fp32: every product is exact, nothing is rounded to 16 bits on the way.
 //
-// A wave takes 16 rows of weights a line (256 weights, 128 bytes) at a time, two loads of 8
-// rows by 128 bytes: whole lines of memory, straight to registers.  With lane = 16 q + 8 h + r,
-// load i delivers piece 4 h + q (16 bytes) of row 8 i + r; exchanging halves of 8 lanes
-// between the two gives pieces q and 4 + q of row 8 h + r, the rows where a 16x16x32 matrix
-// instruction expects them.  Then the four pieces of the same row are transposed between
-// the lane rows q, so that word j of a lane is word q of piece j: one instruction
-// covers 32 consecutive weights, whatever G.  Eight nibbles of a word come out in the order
-// 0 4 1 5 2 6 3 7, and x is put in the same order.
+// A wave takes 16 rows of weights a line (256 weights, 128 bytes) at a time, copied straight
+// into a ring of its own in LDS, whole lines of memory 8 rows at a time.  A lane reads two
+// pieces of 16 bytes of a row there.  For G = 128 the four pieces of a group, one in each 16
+// lanes, make four matrix instructions word by word; for shorter groups they are first
+// transposed between the 16-lane rows, so that each instruction covers 32 consecutive
+// weights.  Eight nibbles of a word come out in the order 0 4 1 5 2 6 3 7, and x is put in
+// the same order, once, in LDS.
 #pragma once
 
 #include "lb_float.hpp"
@@ -43,15 +42,24 @@ template <class T> __device__ inline f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c)
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
 }
 
-// 16 + u of a word's eight levels, in the order 0 4, 1 5, 2 6, 3 7.
-template <class T> __device__ inline u32x4 w4_levels(uint32_t w)
+// 16 + u of a word's eight levels, in the order 0 4, 1 5, 2 6, 3 7.  (The constants are kept in
+// registers: two literals would make two instructions of the AND and the OR.)
+struct W4Const {
+    uint32_t mask, base;
+};
+template <class T> __device__ inline W4Const w4_const()
 {
-    constexpr uint32_t M = W4Vec<T>::MASK, B = W4Vec<T>::BASE;
+    W4Const c{W4Vec<T>::MASK, W4Vec<T>::BASE};
+    asm("" : "+v"(c.mask), "+s"(c.base));
+    return c;
+}
+template <class T> __device__ inline u32x4 w4_levels(uint32_t w, const W4Const &c)
+{
     u32x4 r;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int up = W4Vec<T>::AT - 4 * i;
-        r[i] = ((up >= 0 ? w << (up >= 0 ? up : 0) : w >> (up < 0 ? -up : 0)) & M) | B;
+        r[i] = ((up >= 0 ? w << (up >= 0 ? up : 0) : w >> (up < 0 ? -up : 0)) & c.mask) | c.base;
     }
     return r;
 }
@@ -67,16 +75,6 @@ __device__ inline u32x4 w4_order(u32x4 x)
 }
 template <class T> __device__ inline uint32_t one_pair() { return __is_same(T, __bf16) ? 0x3F803F80u : 0x3C003C00u; }
 
-// The two loads of a line, exchanged: pieces q (p0) and 4 + q (p1) of row lane % 16.
-__device__ inline void w4_rows(u32x4 &p0, u32x4 &p1)
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int a = (int)p0[i], b = (int)p1[i];
-        p0[i] = (uint32_t)__builtin_amdgcn_update_dpp(a, b, 0x128, 0xF, 0xC, false);   // lanes 8..15: b of lane - 8
-        p1[i] = (uint32_t)__builtin_amdgcn_update_dpp(b, a, 0x128, 0xF, 0x3, false);   // lanes 0..7: a of lane + 8
-    }
-}
 // Word j of lane row q becomes word q of lane row j.
 __device__ inline void w4_transpose(u32x4 &p)
 {
@@ -90,255 +88,250 @@ __device__ inline void w4_transpose(u32x4 &p)
     p[3] = d[1];
 }
 
-// One row tile's numbers of a line: GROUPS words (scale, minimum) of row lane % 16.
-template <int GROUPS> __device__ inline void w4_numbers(const __amdgpu_buffer_rsrc_t &rsrc, uint32_t at, int32_t left, uint32_t (&v)[GROUPS])
-{
-    if (left >= GROUPS) {
-        if constexpr (GROUPS == 2) {
-            const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rsrc, (int)at, 0, 0));
-            v[0] = a[0], v[1] = a[1];
-        } else {
-#pragma unroll
-            for (int g = 0; g < GROUPS; g += 4) {
-                const u32x4 a = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, (int)(at + 4u * g), 0, 0));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[g + i] = a[i];
-            }
-        }
-    } else {
-#pragma unroll
-        for (int g = 0; g < GROUPS; ++g)
-            v[g] = g < left ? (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rsrc, (int)(at + 4u * g), 0, 0) : 0u;
-    }
-}
-
-__device__ inline __amdgpu_buffer_rsrc_t w4_rsrc(const void *base, uint64_t bytes)
-{
-    const i32x4 r = make_rsrc(base, bytes);
-    const uint64_t b = (uint64_t)(uint32_t)r.x | ((uint64_t)((uint32_t)r.y & 0xFFFFu) << 32);
-    return __builtin_amdgcn_make_buffer_rsrc((void *)(uintptr_t)b, (short)0, r.z, r.w);
-}
-__device__ inline u32x4 w4_load(const __amdgpu_buffer_rsrc_t &rsrc, uint32_t at)
-{
-    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, (int)at, 0, 0));
-}
-
-// The sixteen rows of weights of a tile, at row `row` of the operand; rows from `rows` on do not
+// The sixteen rows of weights of a tile, from row `row` of the operand; rows from `rows` on do not
 // exist and read as zeros.
 struct W4Tile {
     int64_t row;
     int32_t rows;
 };
 
-// Activations in LDS: rows of w4_x_stride(K) bytes (K up to whole lines, the rest zeros; 16
-// bytes more, so that 16 rows' pieces lie on all banks once), in the order of the levels.
-// first() takes what a batch of loads covers (8 of 16 bytes a thread) to registers, rest()
-// writes it to LDS and brings whatever is left: between the two a wave asks for its first
-// weights, whose latency then runs beside the copy.
-__host__ __device__ inline uint32_t w4_x_stride(int32_t K) { return (uint32_t)((K + 255) / 256) * 512u + 16u; }
-
-template <class RowAt> struct W4Stage {
-    enum : int { BATCH = 8 };
-    char *lds;
-    int32_t K, pieces, all, threads;   // pieces of 16 bytes of a row, and of all rows
-    RowAt row_at;                      // (row) -> its first element
-    u32x4 v[BATCH];
-    __device__ inline W4Stage(char *l, int32_t k, int32_t rows, int32_t n, const RowAt &at)
-        : lds(l), K(k), pieces((k + 255) / 256 * 32), all((k + 255) / 256 * 32 * rows), threads(n), row_at(at)
-    {
-    }
-    __device__ inline void fetch(int32_t i0)
-    {
-#pragma unroll
-        for (int b = 0; b < BATCH; ++b) {
-            const int32_t i = i0 + b * threads;
-            v[b] = u32x4{0u, 0u, 0u, 0u};
-            if (i < all) {
-                const int32_t row = i / pieces, at = i - row * pieces;
-                if (8 * at < K) v[b] = ((const u32x4 *)row_at(row))[at];
-            }
-        }
-    }
-    __device__ inline void write(int32_t i0)
-    {
-#pragma unroll
-        for (int b = 0; b < BATCH; ++b) {
-            const int32_t i = i0 + b * threads;
-            if (i < all) {
-                const int32_t row = i / pieces, at = i - row * pieces;
-                *(u32x4 *)(lds + (uint32_t)row * w4_x_stride(K) + 16u * (uint32_t)at) = w4_order(v[b]);
-            }
-        }
-    }
-    __device__ inline void first() { fetch((int32_t)threadIdx.x); }
-    __device__ inline void rest()
-    {
-        write((int32_t)threadIdx.x);
-        for (int32_t i = (int32_t)threadIdx.x + BATCH * threads; i < all; i += BATCH * threads) {
-            fetch(i);
-            write(i);
-        }
-        __syncthreads();
-    }
+// How a workgroup shares its work.  K is taken in chunks of `chunk` lines, whose activations are
+// in LDS together; of a chunk's lines `kw` waves take a share each, for the same `each` tiles of
+// 16 columns, the next kw waves for the next ones.
+constexpr int W4_WAVES = 8;
+struct W4Split {
+    int32_t kw, each, chunk;
 };
 
-// The stream of a wave: lines `first` to `last` of K of its tiles, one tile after another,
-// DEPTH lines of weights on their way.
-//   tile_at(t): the W4Tile of tile t of `tiles`.
-//   ready(): called by every wave once its first loads are under way.
-//   done(t, acc): its sums; acc[m][i] is row 4 (lane / 16) + i of tile m of x, column lane % 16.
-// x: XLDS: in LDS as W4Stage leaves it, row 16 m + lane % 16 at xat[m], PLANES 2: the sum of two
-// planes, `plane` bytes apart.  Otherwise in memory, xat and plane byte offsets in rx, loaded
-// half a line ahead.
+// LDS of a workgroup: x (two planes: one row after the other's all), the rings, and what the
+// caller puts behind.
+template <int G> struct W4Lds {
+    enum : int {
+        GROUPS = 256 / G,
+        NUMBERS = G == 32 ? 512 : 256,          // (scale, minimum) words of a line's 16 rows, group by group
+        STAGE = 2048 + NUMBERS,
+        DEPTH = 4,
+        COPIES = G == 32 ? 4 : 3,               // copies of a stage
+        RING = DEPTH * STAGE,
+        RINGS = W4_WAVES * RING
+    };
+    // (a copy fills 1 KiB)
+    static __host__ __device__ inline uint32_t x_bytes(int32_t rows, int32_t chunk) { return (uint32_t)(rows * chunk + 1) / 2u * 1024u; }
+};
+
+template <int N> __device__ inline void w4_wait() { asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory"); }
+
+// The products of a wave's tiles: 16 MT rows of x at most (`rows` of them) by 16 columns each.
+//   lds: W4Lds; x rows are read through rx, row i's first byte at x_at(i) (PLANES 2: rows
+//     from `rows` on are the second plane's, x is the sum of both).
+//   tiles: this wave's; tile_at(t): a W4Tile.
+//   done(t, acc, more): sums of tile t over this wave's lines of a chunk, more: not the first chunk's;
+//     acc[m][i] is row 4 (lane / 16) + i of 16 rows m, column lane % 16.
 //   T: the type of x as the matrix cores take it; PT: of the groups' numbers.
-template <class T, class PT, int MT, int G, int PLANES, bool XLDS, int DEPTH, class TileAt, class Ready, class Done>
-__device__ inline void w4_stream(const uint8_t *W, const uint32_t *P, int32_t K, int32_t first, int32_t last, int32_t tiles,
-                                 const __amdgpu_buffer_rsrc_t &rx, const char *xlds, const uint32_t (&xat)[MT],
-                                 uint32_t plane, TileAt &&tile_at, Ready &&ready, Done &&done)
+// Every wave of the workgroup calls this, also without tiles (x is copied by all).  Copies of two
+// lines are under way while a third is worked on; each wave waits for its own by count.
+template <class T, class PT, int MT, int G, int PLANES, class XAt, class TileAt, class Done>
+__device__ inline void w4_flow(char *lds, const uint8_t *W, const uint32_t *P, int32_t K, int32_t rows, const W4Split &sp,
+                               int32_t tiles, const i32x4 rx, XAt &&x_at, TileAt &&tile_at, Done &&done)
 {
-    constexpr int GROUPS = 256 / G, HALF = GROUPS / 2, STEPS = G / 32;
-    const int32_t share = last - first, items = share * tiles;
-    if (items <= 0) {
-        ready();
-        return;
-    }
+    typedef W4Lds<G> L;
+    constexpr int GROUPS = L::GROUPS, HALF = GROUPS / 2, STEPS = G / 32;
     const int32_t lane = (int32_t)(threadIdx.x & 63u), q = lane >> 4, r = lane & 15;
+    const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), share = wave % sp.kw;
     const uint32_t kb = (uint32_t)K / 2u, groups = (uint32_t)K / G;
-    const uint32_t piece = (uint32_t)(16 * (4 * ((lane >> 3) & 1) + q));
-    const uint32_t row_at = (uint32_t)(lane & 7) * kb + piece, p_at = (uint32_t)r * groups * 4u;
+    const int32_t lines = (K + 255) / 256, xrows = PLANES * rows;
+    char *const ring = lds + L::x_bytes(xrows, sp.chunk) + wave * L::RING;
+    const uint32_t ring_at = lds_addr(ring), x_lds = lds_addr(lds);
 
-    u32x4 wv[DEPTH][2];
-    uint32_t pv[DEPTH][GROUPS];
-    int32_t load_tile = 0, load_line = first;   // what is loaded next
-    auto load = [&](u32x4 (&w)[2], uint32_t (&p)[GROUPS]) {
-        if (load_tile >= tiles) return;
-        const W4Tile t = tile_at(load_tile);
-        const __amdgpu_buffer_rsrc_t rw = w4_rsrc(W + t.row * kb, (uint64_t)(uint32_t)t.rows * kb);
-        const __amdgpu_buffer_rsrc_t rp = w4_rsrc(P + t.row * groups, (uint64_t)(uint32_t)t.rows * groups * 4u);
-        const uint32_t at = (uint32_t)load_line * 128u;
-        const bool in = at + piece < kb;
+    // Lines of a chunk that are this wave's.
+    auto bounds = [&](int32_t c, int32_t &lo, int32_t &hi) {
+        const int32_t n = min(sp.chunk, lines - c);
+        lo = c + n * share / sp.kw;
+        hi = c + n * (share + 1) / sp.kw;
+    };
+
+    // ---- the ring: lane l of a copy takes piece (l % 8) ^ (l / 8) of row l / 8, which keeps reads of
+    // eight rows off each other's banks
+    int32_t c_chunk = 0, c_tile = 0, c_line, c_hi, c_lo;   // what is copied next
+    i32x4 rw, rp;
+    const uint32_t piece = 16u * (uint32_t)((lane & 7) ^ (lane >> 3)), row_at = (uint32_t)(lane >> 3) * kb + piece;
+    auto aim = [&] {
+        const W4Tile t = tile_at(c_tile);
+        rw = make_rsrc(W + t.row * kb, (uint64_t)(uint32_t)t.rows * kb);
+        rp = make_rsrc(P + t.row * groups, (uint64_t)(uint32_t)t.rows * groups * 4u);
+    };
+    bounds(0, c_lo, c_hi);
+    c_line = c_lo;
+    bool left = tiles > 0;
+    if (left && c_lo == c_hi) left = false;   // (only where there is one chunk)
+    if (left) aim();
+    else rw = rp = make_rsrc(W, 0);
+    uint32_t c_at = ring_at, c_ring = 0;
+    auto copy = [&] {
+        const uint32_t at = (uint32_t)c_line * 128u;
+        const bool in = left && at + piece < kb;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) w[i] = w4_load(rw, in ? row_at + (uint32_t)(8 * i) * kb + at : 0xFFFFFFF0u);
-        w4_numbers<GROUPS>(rp, p_at + (uint32_t)(load_line * GROUPS) * 4u, (int32_t)groups - load_line * GROUPS, p);
-        if (++load_line == last) {
-            load_line = first;
-            ++load_tile;
+        for (int i = 0; i < 2; ++i) dma16(rw, in ? row_at + (uint32_t)(8 * i) * kb + at : 0xFFFFFFF0u, c_at + 1024u * (uint32_t)i);
+#pragma unroll
+        for (int i = 0; i < L::COPIES - 2; ++i) {
+            const uint32_t g = (uint32_t)(c_line * GROUPS + 4 * i + q);
+            const bool there = left && (GROUPS >= 4 || q < GROUPS) && g < groups;
+            dma4(rp, there ? ((uint32_t)r * groups + g) * 4u : 0xFFFFFFF0u, c_at + 2048u + 256u * (uint32_t)i);
+        }
+        c_at += L::STAGE;
+        if (++c_ring == L::DEPTH) {
+            c_ring = 0;
+            c_at = ring_at;
+        }
+        if (left && ++c_line == c_hi) {
+            if (++c_tile == tiles) {
+                c_tile = 0;
+                c_chunk += sp.chunk;
+                left = c_chunk < lines;
+                if (left) {
+                    bounds(c_chunk, c_lo, c_hi);
+                    left = c_lo < c_hi;   // (a last chunk of fewer lines than shares)
+                }
+            }
+            c_line = c_lo;
+            if (left) aim();
         }
     };
-    u32x4 xv[2][MT][4][PLANES];
-    auto load_x = [&](int h, int32_t line) {
-#pragma unroll
-        for (int st = 0; st < 4; ++st)
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int pl = 0; pl < PLANES; ++pl) {
-                    const int32_t k = line * 256 + 128 * h + 32 * st + 8 * q;
-                    if constexpr (XLDS)
-                        xv[h][m][st][pl] = *(const u32x4 *)(xlds + xat[m] + pl * plane + (uint32_t)(2 * k));
-                    else
-                        xv[h][m][st][pl] = w4_load(rx, k < K ? xat[m] + pl * plane + (uint32_t)(2 * k) : 0xFFFFFFF0u);
-                }
+
+    // ---- x of a chunk: piece p of row i lies at p ^ i % 8 of the row
+    auto ask_x = [&](int32_t c) {
+        const int32_t per = min(sp.chunk, lines - c) * 32, all = per * xrows;
+        for (int32_t i0 = wave * 64; i0 < all; i0 += 64 * W4_WAVES) {
+            const int32_t i = min(i0 + lane, all - 1), row = i / per, p = (i - row * per) ^ (row & 7);
+            const int32_t k = c * 256 + 8 * p;
+            dma16(rx, i0 + lane < all && k < K ? x_at(row) + 2u * (uint32_t)k : 0xFFFFFFF0u, x_lds + 16u * (uint32_t)i0);
+        }
+    };
+    auto order_x = [&](int32_t c) {   // each lane what it copied itself
+        const int32_t all = min(sp.chunk, lines - c) * 32 * xrows;
+        for (int32_t i = (int32_t)threadIdx.x; i < all; i += 64 * W4_WAVES) {
+            u32x4 *p = (u32x4 *)(lds + 16 * i);
+            *p = w4_order(*p);
+        }
     };
 
-    f32x4 acc[MT];
+    ask_x(0);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto half = [&](int h, const u32x4 &w, const uint32_t (&p)[GROUPS]) {   // 128 weights
+    for (int d = 0; d < L::DEPTH - 1; ++d) copy();
+    w4_wait<(L::DEPTH - 1) * L::COPIES>();
+    order_x(0);
+    __syncthreads();
+
+    const W4Const konst = w4_const<T>();
+    uint32_t at = 0, slot = 0;   // of the ring
+    uint32_t xrow[MT][PLANES];
+    for (int32_t c = 0; c < lines; c += sp.chunk) {
+        if (c) {
+            __syncthreads();
+            ask_x(c);
+            w4_wait<0>();
+            order_x(c);
+            __syncthreads();
+        }
+        const uint32_t bytes = (uint32_t)min(sp.chunk, lines - c) * 512u;
 #pragma unroll
-        for (int g = 0; g < HALF; ++g) {
-            f32x4 sum[MT], xs[MT];
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int m = 0; m < MT; ++m) sum[m] = xs[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int pl = 0; pl < PLANES; ++pl) xrow[m][pl] = (uint32_t)(min(16 * m + r, rows - 1) + pl * rows);
+        int32_t lo, hi;
+        bounds(c, lo, hi);
+        if (lo == hi) continue;
+        for (int32_t tile = 0; tile < tiles; ++tile) {
+            f32x4 acc[MT];
 #pragma unroll
-            for (int st = 0; st < STEPS; ++st) {
-                const int j = g * STEPS + st;   // 32 weights of the half
-                const u32x4 lv = w4_levels<T>(w[j]);
-                const uint32_t one = one_pair<T>();
+            for (int m = 0; m < MT; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int32_t line = lo; line < hi; ++line) {
+                copy();
+                w4_wait<(L::DEPTH - 1) * L::COPIES>();
+                const char *st = ring + at;
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
+                for (int h = 0; h < 2; ++h) {   // 128 weights
+                    u32x4 w = *(const u32x4 *)(st + 128 * r + 16 * ((4 * h + q) ^ (r & 7)));
+                    if constexpr (G != 128) w4_transpose(w);
+                    u32x4 x[4][MT][PLANES];
 #pragma unroll
-                    for (int pl = 0; pl < PLANES; ++pl) {
-                        const u32x4 x = XLDS ? xv[h][m][j][pl] : w4_order(xv[h][m][j][pl]);
-                        xs[m] = mfma16<T>(x, u32x4{one, one, one, one}, xs[m]);
-                        sum[m] = mfma16<T>(x, lv, sum[m]);
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int m = 0; m < MT; ++m)
+#pragma unroll
+                            for (int pl = 0; pl < PLANES; ++pl) {
+                                const int32_t p = 16 * h + (G == 128 ? 4 * q + j : 4 * j + q);
+                                x[j][m][pl] = *(const u32x4 *)(lds + xrow[m][pl] * bytes + (uint32_t)(line - c) * 512u +
+                                                               16u * ((uint32_t)p ^ (xrow[m][pl] & 7u)));
+                            }
+#pragma unroll
+                    for (int g = 0; g < HALF; ++g) {
+                        f32x4 sum[MT], xs[MT];
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) sum[m] = xs[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int j = g * STEPS; j < (g + 1) * STEPS; ++j) {
+                            const u32x4 lv = w4_levels<T>(w[j], konst);
+                            const uint32_t one = one_pair<T>();
+#pragma unroll
+                            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                                for (int pl = 0; pl < PLANES; ++pl) {
+                                    xs[m] = mfma16<T>(x[j][m][pl], u32x4{one, one, one, one}, xs[m]);
+                                    sum[m] = mfma16<T>(x[j][m][pl], lv, sum[m]);
+                                }
+                        }
+                        const uint32_t n = *(const uint32_t *)(st + 2048 + 64 * (h * HALF + g) + 4 * r);
+                        const float s = lo_f32<PT>(n), b = hi_f32<PT>(n) - 16.0f * s;
+#pragma unroll
+                        for (int m = 0; m < MT; ++m)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                acc[m][i] = __builtin_fmaf(s, sum[m][i], acc[m][i]);
+                                acc[m][i] = __builtin_fmaf(b, xs[m][i], acc[m][i]);
+                            }
                     }
-            }
-            const float s = lo_f32<PT>(p[h * HALF + g]), c = hi_f32<PT>(p[h * HALF + g]) - 16.0f * s;
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    acc[m][i] = __builtin_fmaf(s, sum[m][i], acc[m][i]);
-                    acc[m][i] = __builtin_fmaf(c, xs[m][i], acc[m][i]);
                 }
-        }
-    };
-
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d) load(wv[d], pv[d]);
-    ready();
-    load_x(0, first);
-    int32_t tile = 0, line = first;
-    for (int32_t i = 0; i < items; i += DEPTH) {
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-            if (i + d >= items) break;
-            u32x4 w0 = wv[d][0], w1 = wv[d][1];
-            uint32_t p[GROUPS];
-#pragma unroll
-            for (int g = 0; g < GROUPS; ++g) p[g] = pv[d][g];
-            w4_rows(w0, w1);
-            w4_transpose(w0);
-            w4_transpose(w1);
-            load(wv[d], pv[d]);
-            load_x(1, line);
-            half(0, w0, p);
-            const int32_t now = tile;
-            const bool end = ++line == last;
-            if (end) {
-                line = first;
-                ++tile;
+                // the next copies overwrite what has been read here
+                asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+                at += L::STAGE;
+                if (++slot == L::DEPTH) slot = at = 0;
             }
-            load_x(0, line);
-            half(1, w1, p);
-            if (end) {
-                done(now, acc);
-#pragma unroll
-                for (int m = 0; m < MT; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-            }
+            done(tile, acc, c > 0);
         }
     }
+    w4_wait<0>();   // no copy outlives the workgroup's LDS
 }
 
-// Waves' sums in LDS: `rows` rows of x by 16 columns, rows 20 floats apart (a lane's four rows lie
+// A wave's sums into LDS, or (more) onto what it left there: `rows` rows of x by 16 columns, rows 20 floats apart (a lane's four rows lie
 // on other banks).
 enum { W4_SLOT_LD = 20 };
-template <int MT> __device__ inline void w4_put(float *slot, int32_t rows, const f32x4 (&acc)[MT])
+template <int MT> __device__ inline void w4_put(float *slot, int32_t rows, const f32x4 (&acc)[MT], bool more)
 {
     const int lane = (int)(threadIdx.x & 63u), q = lane >> 4, r = lane & 15;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (16 * m + 4 * q + i < rows) slot[(16 * m + 4 * q + i) * W4_SLOT_LD + r] = acc[m][i];
+            if (16 * m + 4 * q + i < rows) {
+                float *s = slot + (16 * m + 4 * q + i) * W4_SLOT_LD + r;
+                *s = more ? *s + acc[m][i] : acc[m][i];
+            }
 }
 
-// How a workgroup of eight waves shares its tiles: kw waves take a share of K each, of `each`
-// tiles, the next kw waves of the next ones.
-constexpr int W4_WAVES = 8;
-struct W4Split {
-    int32_t kw, each;
-};
-// For `tiles` tiles of `lines` lines: the fewest lines for the busiest wave, and of equals the
-// fewest shares.
-inline W4Split w4_split(int64_t tiles, int64_t lines)
+// The split of `tiles` tiles of `lines` lines: the fewest lines for the busiest wave, and of equals
+// the fewest shares; chunks of x of at most x_bytes.
+inline W4Split w4_split(int64_t tiles, int64_t lines, int64_t xrows, int64_t x_bytes)
 {
-    W4Split best{1, (int32_t)((tiles + W4_WAVES - 1) / W4_WAVES)};
-    for (int kw = 2; kw <= W4_WAVES; kw *= 2) {
-        const W4Split s{kw, (int32_t)((tiles + W4_WAVES / kw - 1) / (W4_WAVES / kw))};
+    int64_t chunk = x_bytes / (512 * xrows);
+    if (chunk > lines) chunk = lines;
+    if (chunk < 1) chunk = 1;
+    W4Split best{1, (int32_t)((tiles + W4_WAVES - 1) / W4_WAVES), (int32_t)chunk};
+    for (int kw = 2; kw <= W4_WAVES && (chunk == lines || kw <= chunk); kw *= 2) {
+        const W4Split s{kw, (int32_t)((tiles + W4_WAVES / kw - 1) / (W4_WAVES / kw)), (int32_t)chunk};
         if ((lines + kw - 1) / kw * s.each < (lines + best.kw - 1) / best.kw * best.each) best = s;
     }
+    if (chunk < lines) best.chunk = (int32_t)(chunk / best.kw * best.kw);   // equal shares of every whole chunk
     return best;
 }
 
