@@ -26,8 +26,9 @@ __device__ inline uint32_t order_of(float v)
 }
 
 // ---- router ----------------------------------------------------------------
-// 16 experts by 16 tokens to a workgroup, a share of H to each wave.
-enum { ROUTER_WAVES = 8 };
+// 16 experts by 16 tokens to a workgroup, a share of H to each wave, whose loads (of up to 256
+// numbers of a row) are all under way at once.
+enum { ROUTER_WAVES = 16, ROUTER_STEPS = 8 };
 template <class T>
 __global__ __launch_bounds__(64 * ROUTER_WAVES) void moe_router_kernel(MoeArgs a)
 {
@@ -39,10 +40,10 @@ __global__ __launch_bounds__(64 * ROUTER_WAVES) void moe_router_kernel(MoeArgs a
     const T *xrow = (const T *)a.x + (int64_t)min(t0 + r, a.T - 1) * a.ldx;
     const int32_t steps = a.H / 32, last = (wave + 1) * steps / ROUTER_WAVES;
     f32x4 acc[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
-    for (int32_t st = wave * steps / ROUTER_WAVES; st < last; st += 4) {
-        u32x4 x[4], w[4];
+    for (int32_t st = wave * steps / ROUTER_WAVES; st < last; st += ROUTER_STEPS) {
+        u32x4 x[ROUTER_STEPS], w[ROUTER_STEPS];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < ROUTER_STEPS; ++i) {
             x[i] = w[i] = u32x4{0u, 0u, 0u, 0u};
             if (st + i < last) {
                 x[i] = *(const u32x4 *)(xrow + 32 * (st + i) + 8 * q);
@@ -50,7 +51,7 @@ __global__ __launch_bounds__(64 * ROUTER_WAVES) void moe_router_kernel(MoeArgs a
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[0] = mfma16<T>(x[i], w[i], acc[0]);
+        for (int i = 0; i < ROUTER_STEPS; ++i) acc[0] = mfma16<T>(x[i], w[i], acc[0]);
     }
     w4_put<1>(sums[wave], 16, acc, false);
     __syncthreads();
@@ -71,77 +72,105 @@ enum { EXPERTS_MAX = 1024 };
 struct MoeList {
     int32_t rank[MOE_TOKENS];   // the expert's rank in each token's order, if below k, else -1
     int32_t row[MOE_TOKENS];    // token * k + rank of each of its tokens
-    int32_t expert, count, first;
+    int32_t count;
 };
 
-// How many of a token's logits come before number e, whose order is `mine`.
-__device__ inline int32_t rank_of(const uint32_t *order, int32_t E, int32_t e, uint32_t mine)
+// Number j (from 0) in a token's order of its logits, by every wave for itself: lane l holds
+// logits l, l + 64, ...; the value bit by bit from the top, by counting those not below a
+// candidate, and of equal ones the lowest index.
+template <int NC> __device__ inline int32_t nth_expert(const float *row, int32_t E, int32_t j)
 {
-    int32_t above = 0;
-    for (int32_t f = 0; f < E; f += 4) {   // (order[E ..] up to a multiple of 4 is 0)
-        const u32x4 o = *(const u32x4 *)(order + f);
+    const int32_t lane = (int32_t)threadIdx.x & 63;
+    uint32_t o[NC];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) above += o[i] > mine || (o[i] == mine && f + i < e);
+    for (int i = 0; i < NC; ++i) {
+        const float v = row[min(64 * i + lane, E - 1)];
+        o[i] = 64 * i + lane < E ? order_of(v) : 0u;
     }
-    return above;
-}
-// A token's logits' orders into LDS; barrier afterwards.
-__device__ inline void put_orders(uint32_t *order, const float *row, int32_t E, int32_t threads)
-{
-    for (int32_t e = (int32_t)threadIdx.x; e < (E + 3) / 4 * 4; e += threads) order[e] = e < E ? order_of(row[e]) : 0u;
-    __syncthreads();
-}
-
-// order: LDS for EXPERTS_MAX words, free again afterwards.
-__device__ inline bool moe_list(const MoeArgs &a, int32_t slot, bool by_pair, MoeList &l, uint32_t *order)
-{
-    constexpr int NW = W4_WAVES, AT_ONCE = (MOE_TOKENS + NW - 1) / NW;
-    const int32_t tid = (int32_t)threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    if (by_pair) {
-        const int32_t t = slot / a.top_k, j = slot % a.top_k;
-        put_orders(order, a.logits + t * a.E, a.E, 64 * NW);
-        for (int32_t e = tid; e < a.E; e += 64 * NW)
-            if (rank_of(order, a.E, e, order[e]) == j) {
-                l.expert = e;
-                l.first = t;
-            }
-    } else if (tid == 0) {
-        l.expert = slot;
-        l.first = 0;
-    }
-    __syncthreads();
-    const int32_t e = l.expert;
-    uint32_t mine[AT_ONCE];
-    int32_t above[AT_ONCE];
+    uint32_t value = 0;
+    int32_t above = 0;   // those over value's candidates that were too large
+#pragma unroll 1
+    for (uint32_t bit = 0x80000000u; bit; bit >>= 1) {
+        int32_t n = 0;
 #pragma unroll
-    for (int i = 0; i < AT_ONCE; ++i) {
-        mine[i] = order_of(a.logits[min(wave + NW * i, a.T - 1) * a.E + e]);
+        for (int i = 0; i < NC; ++i) n += __popcll(__ballot(o[i] >= (value | bit)));
+        if (n > j) value |= bit;
+        else above = n;
+    }
+    int32_t left = j - above, e = 0;   // how many equal ones come before
+    bool found = false;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        uint64_t same = __ballot(o[i] == value && 64 * i + lane < E);
+        const int32_t n = __popcll(same);
+        if (!found && left < n) {
+            for (; left > 0; --left) same &= same - 1;
+            e = 64 * i + __builtin_ctzll(same);
+            found = true;
+        }
+        left -= n;
+    }
+    return e;
+}
+// The expert of a slot, and the first token that has to be its.
+struct MoeSlot {
+    int32_t expert, first;
+};
+__device__ inline MoeSlot moe_slot(const MoeArgs &a, int32_t slot, bool by_pair)
+{
+    if (!by_pair) return MoeSlot{slot, 0};
+    const int32_t t = slot / a.top_k, j = slot - t * a.top_k;
+    const float *row = a.logits + t * a.E;
+    const int32_t e = a.E <= 64 ? nth_expert<1>(row, a.E, j) : a.E <= 128 ? nth_expert<2>(row, a.E, j)
+                    : a.E <= 256 ? nth_expert<4>(row, a.E, j) : nth_expert<16>(row, a.E, j);
+    return MoeSlot{__builtin_amdgcn_readfirstlane(e), t};
+}
+// Ranks of an expert in the orders of the tokens of this wave (every eighth).
+constexpr int MOE_EACH = MOE_TOKENS / W4_WAVES;
+__device__ inline void moe_ranks(const MoeArgs &a, int32_t e, int32_t (&above)[MOE_EACH])
+{
+    constexpr int AHEAD = 2;   // 64 logits of all these tokens each, under way together
+    const int32_t lane = (int32_t)threadIdx.x & 63, wave = (int32_t)threadIdx.x >> 6;
+    float own[MOE_EACH];
+#pragma unroll
+    for (int i = 0; i < MOE_EACH; ++i) {
+        own[i] = a.logits[min(wave + W4_WAVES * i, a.T - 1) * a.E + e];
         above[i] = 0;
     }
-    for (int32_t f0 = 0; f0 < a.E; f0 += 64) {
-        const int32_t f = min(f0 + lane, a.E - 1);
-        const bool there = f0 + lane < a.E;
-        float v[AT_ONCE];
+    for (int32_t f0 = 0; f0 < a.E; f0 += 64 * AHEAD) {
+        float v[AHEAD][MOE_EACH];
 #pragma unroll
-        for (int i = 0; i < AT_ONCE; ++i) v[i] = a.logits[min(wave + NW * i, a.T - 1) * a.E + f];
+        for (int u = 0; u < AHEAD; ++u)
 #pragma unroll
-        for (int i = 0; i < AT_ONCE; ++i) {
-            const uint32_t o = order_of(v[i]);
-            above[i] += __popcll(__ballot(there && (o > mine[i] || (o == mine[i] && f < e))));
-        }
+            for (int i = 0; i < MOE_EACH; ++i)
+                v[u][i] = a.logits[min(wave + W4_WAVES * i, a.T - 1) * a.E + min(f0 + 64 * u + lane, a.E - 1)];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+            for (int i = 0; i < MOE_EACH; ++i) {
+                const int32_t f = f0 + 64 * u + lane;
+                const uint32_t mine = order_of(own[i]), o = order_of(v[u][i]);
+                above[i] += __popcll(__ballot(f < a.E && (o > mine || (o == mine && f < e))));
+            }
     }
+}
+// The list of the expert's tokens (to all threads).  Returns how many; 0 where an earlier slot's
+// workgroups work for them.
+__device__ inline int32_t moe_tokens(const MoeArgs &a, const MoeSlot &s, const int32_t (&above)[MOE_EACH], MoeList &l)
+{
+    const int32_t lane = (int32_t)threadIdx.x & 63, wave = (int32_t)threadIdx.x >> 6;
     if (lane == 0)
 #pragma unroll
-        for (int i = 0; i < AT_ONCE; ++i) l.rank[wave + NW * i] = wave + NW * i < a.T && above[i] < a.top_k ? above[i] : -1;
+        for (int i = 0; i < MOE_EACH; ++i) l.rank[wave + W4_WAVES * i] = wave + W4_WAVES * i < a.T && above[i] < a.top_k ? above[i] : -1;
     __syncthreads();
     if (wave == 0) {
         const int32_t rank = l.rank[lane];
         const uint64_t in = __ballot(rank >= 0);
         if (rank >= 0) l.row[__popcll(in & ((1ull << lane) - 1))] = lane * a.top_k + rank;
-        if (lane == 0) l.count = (by_pair && (in & ((1ull << l.first) - 1))) ? 0 : __popcll(in);
+        if (lane == 0) l.count = in & ((1ull << s.first) - 1) ? 0 : __popcll(in);
     }
     __syncthreads();
-    return l.count > 0;
+    return __builtin_amdgcn_readfirstlane(l.count);
 }
 
 // ---- gate and up, activation -----------------------------------------------
@@ -149,6 +178,7 @@ __device__ inline bool moe_list(const MoeArgs &a, int32_t slot, bool by_pair, Mo
 struct MoeGrid {
     bool by_pair;
     int32_t rows;    // tokens at a time, at most 16
+    uint32_t x_bytes;
     W4Split sp;      // of blocks (up: a tile of gate rows and one of up rows each) or tiles (down)
 };
 template <class T, int G>
@@ -156,14 +186,16 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGri
 {
     extern __shared__ __attribute__((aligned(1024))) char smem[];
     __shared__ MoeList list;
-    if (!moe_list(a, (int32_t)blockIdx.y, g.by_pair, list, (uint32_t *)smem)) return;
+    const MoeSlot ms = moe_slot(a, (int32_t)blockIdx.y, g.by_pair);
+    const int32_t expert = ms.expert;
+    int32_t above[MOE_EACH];
+    moe_ranks(a, expert, above);
     const int32_t lane = (int32_t)(threadIdx.x & 63u), q = lane >> 4, r = lane & 15;
     const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int32_t expert = __builtin_amdgcn_readfirstlane(list.expert), count = __builtin_amdgcn_readfirstlane(list.count);
     const int32_t kw = g.sp.kw, each = g.sp.each, lines = (a.H + 255) / 256;
     const int32_t per = W4_WAVES / kw * each, b0 = (int32_t)blockIdx.x * per, have = min(per, a.I / 16 - b0);
     const int32_t mine = wave / kw * each;
-    float *const slots = (float *)(smem + W4Lds<G>::x_bytes(g.rows, g.sp.chunk) + W4Lds<G>::RINGS);
+    float *const slots = (float *)(smem + g.x_bytes + W4Lds<G>::RINGS);
     __bf16 *const hi = (__bf16 *)a.h, *const lo = hi + (int64_t)a.T * a.top_k * a.I;
     auto put = [&](int32_t m, int32_t c, float gate, float up) {
         const float h = gate / (1.0f + __expf(-gate)) * up;
@@ -172,15 +204,21 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGri
         hi[o] = top;
         lo[o] = (__bf16)(h - (float)top);
     };
+    auto tile_at = [&](int32_t t) { return W4Tile{((int64_t)expert * 2 + t % 2) * a.I + (b0 + mine + t / 2) * 16, 16}; };
+    W4Flow<T, T, 1, G, 1, decltype(tile_at)> flow(smem, g.x_bytes, a.w1, (const uint32_t *)a.p1, a.H, g.sp,
+                                                  2 * max(0, min(each, have - mine)), tile_at);
+    // the first weights are on their way while the tokens are gathered
+    flow.start();
+    const int32_t count = moe_tokens(a, ms, above, list);
+    if (count == 0) flow.finish();
     for (int32_t at = 0; at < count; at += g.rows) {
         const int32_t rows = min(g.rows, count - at), slot = rows * W4_SLOT_LD;
         const bool direct = kw == 1 && g.sp.chunk >= lines;   // a wave has whole sums
         f32x4 gate[1];
         if (at) __syncthreads();
-        w4_flow<T, T, 1, G, 1>(
-            smem, a.w1, (const uint32_t *)a.p1, a.H, rows, g.sp, 2 * max(0, min(each, have - mine)), make_rsrc(a.x, 0xFFFFFFF0u),
+        flow.run(
+            rows, make_rsrc(a.x, 0xFFFFFFF0u), at == 0,
             [&](int32_t i) { return (uint32_t)(list.row[at + i] / a.top_k) * (uint32_t)a.ldx * 2u; },
-            [&](int32_t t) { return W4Tile{((int64_t)expert * 2 + t % 2) * a.I + (b0 + mine + t / 2) * 16, 16}; },
             [&](int32_t t, const f32x4(&acc)[1], bool more) {
                 if (!direct) {
                     w4_put<1>(slots + (wave * 2 * each + t) * slot, rows, acc, more);
@@ -214,26 +252,33 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_kernel(MoeArgs a, MoeG
 {
     extern __shared__ __attribute__((aligned(1024))) char smem[];
     __shared__ MoeList list;
-    if (!moe_list(a, (int32_t)blockIdx.y, g.by_pair, list, (uint32_t *)smem)) return;
+    const MoeSlot ms = moe_slot(a, (int32_t)blockIdx.y, g.by_pair);
+    const int32_t expert = ms.expert;
+    int32_t above[MOE_EACH];
+    moe_ranks(a, expert, above);
     const int32_t lane = (int32_t)(threadIdx.x & 63u), q = lane >> 4, r = lane & 15;
     const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int32_t expert = __builtin_amdgcn_readfirstlane(list.expert), count = __builtin_amdgcn_readfirstlane(list.count);
     const int32_t kw = g.sp.kw, each = g.sp.each, lines = (a.I + 255) / 256;
     const int32_t per = W4_WAVES / kw * each, t0 = (int32_t)blockIdx.x * per, have = min(per, a.H / 16 - t0);
     const int32_t mine = wave / kw * each;
-    float *const slots = (float *)(smem + W4Lds<G>::x_bytes(2 * g.rows, g.sp.chunk) + W4Lds<G>::RINGS);
+    float *const slots = (float *)(smem + g.x_bytes + W4Lds<G>::RINGS);
     const uint32_t plane = (uint32_t)(a.T * a.top_k) * (uint32_t)a.I * 2u;
+    auto tile_at = [&](int32_t t) { return W4Tile{(int64_t)expert * a.H + (t0 + mine + t) * 16, 16}; };
+    W4Flow<__bf16, T, 1, G, 2, decltype(tile_at)> flow(smem, g.x_bytes, a.w2, (const uint32_t *)a.p2, a.I, g.sp,
+                                                       max(0, min(each, have - mine)), tile_at);
+    flow.start();
+    const int32_t count = moe_tokens(a, ms, above, list);
+    if (count == 0) flow.finish();
     for (int32_t at = 0; at < count; at += g.rows) {
         const int32_t rows = min(g.rows, count - at), slot = rows * W4_SLOT_LD;
         const bool direct = kw == 1 && g.sp.chunk >= lines;
         if (at) __syncthreads();
-        w4_flow<__bf16, T, 1, G, 2>(
-            smem, a.w2, (const uint32_t *)a.p2, a.I, rows, g.sp, max(0, min(each, have - mine)), make_rsrc(a.h, 0xFFFFFFF0u),
+        flow.run(
+            rows, make_rsrc(a.h, 0xFFFFFFF0u), at == 0,
             [&](int32_t i) {
                 const int32_t second = i >= rows;
                 return (uint32_t)list.row[at + i - (second ? rows : 0)] * (uint32_t)a.I * 2u + (second ? plane : 0u);
             },
-            [&](int32_t t) { return W4Tile{(int64_t)expert * a.H + (t0 + mine + t) * 16, 16}; },
             [&](int32_t t, const f32x4(&acc)[1], bool more) {
                 if (!direct) {
                     w4_put<1>(slots + (wave * each + t) * slot, rows, acc, more);
@@ -257,6 +302,18 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_kernel(MoeArgs a, MoeG
 }
 
 // ---- weighted sum ----------------------------------------------------------
+// How many of a token's logits come before number e, whose order is `mine`.
+__device__ inline int32_t rank_of(const uint32_t *order, int32_t E, int32_t e, uint32_t mine)
+{
+    int32_t above = 0;
+    for (int32_t f = 0; f < E; f += 4) {   // (order[E ..] up to a multiple of 4 is 0)
+        const u32x4 o = *(const u32x4 *)(order + f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) above += o[i] > mine || (o[i] == mine && f + i < e);
+    }
+    return above;
+}
+
 enum { COMBINE_THREADS = 256, MOE_TOP_MAX = 64 };
 template <class T>
 __global__ __launch_bounds__(COMBINE_THREADS) void moe_combine_kernel(MoeArgs a)
@@ -265,7 +322,15 @@ __global__ __launch_bounds__(COMBINE_THREADS) void moe_combine_kernel(MoeArgs a)
     __shared__ float part[COMBINE_THREADS / 64], chosen[MOE_TOP_MAX];
     const int32_t t = (int32_t)blockIdx.y, tid = (int32_t)threadIdx.x;
     const float *row = a.logits + t * a.E;
-    put_orders(order, row, a.E, COMBINE_THREADS);
+    // the first results are on their way while the weights are found
+    constexpr int AHEAD = 8;
+    const int32_t c = ((int32_t)blockIdx.x * COMBINE_THREADS + tid) * 4, cc = min(c, a.H - 4);
+    const float *y0 = a.y + (int64_t)t * a.top_k * a.H + cc;
+    f32x4 y[AHEAD];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) y[j] = *(const f32x4 *)(y0 + (int64_t)min(j, a.top_k - 1) * a.H);
+    for (int32_t e = tid; e < (a.E + 3) / 4 * 4; e += COMBINE_THREADS) order[e] = e < a.E ? order_of(row[e]) : 0u;
+    __syncthreads();
     for (int32_t e = tid; e < a.E; e += COMBINE_THREADS) {
         const int32_t above = rank_of(order, a.E, e, order[e]);
         if (above < a.top_k) {
@@ -289,14 +354,20 @@ __global__ __launch_bounds__(COMBINE_THREADS) void moe_combine_kernel(MoeArgs a)
         for (int w = 0; w < COMBINE_THREADS / 64; ++w) total += part[w];
     }
     if (a.weights && blockIdx.x == 0 && tid < a.top_k) a.weights[t * a.top_k + tid] = a.scale * (expf(chosen[tid] - largest) / total);
-    const int32_t c = ((int32_t)blockIdx.x * COMBINE_THREADS + tid) * 4;
     if (c >= a.H) return;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    for (int32_t j = 0; j < a.top_k; ++j) {
-        const float p = a.scale * (expf(chosen[j] - largest) / total);
-        const f32x4 y = *(const f32x4 *)(a.y + (int64_t)(t * a.top_k + j) * a.H + c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += p * y[i];
+    for (int j = 0; j < AHEAD; ++j)
+        if (j < a.top_k) {
+            const float p = a.scale * (expf(chosen[j] - largest) / total);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += p * y[j][i];
+        }
+    for (int32_t j = AHEAD; j < a.top_k; ++j) {
+        const float p = a.scale * (expf(chosen[j] - largest) / total);
+        const f32x4 z = *(const f32x4 *)(y0 + (int64_t)j * a.H);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += p * z[i];
     }
     *(u32x2 *)((T *)a.out + (int64_t)t * a.H + c) = u32x2{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3])};
 }
@@ -316,13 +387,12 @@ template <int G> static MoeShape moe_shape(const MoeArgs &a, int64_t tiles, int3
     const int64_t lines = (K + 255) / 256, slot = (int64_t)m.g.rows * W4_SLOT_LD * 4 * per_tile, xrows = planes * m.g.rows;
     // a workgroup to a compute unit
     const int64_t wgs = std::max<int64_t>(1, cu / slots);
-    int64_t per = (tiles + wgs - 1) / wgs;
-    for (;; --per) {
+    for (int64_t per = (tiles + wgs - 1) / wgs;; --per) {
         m.g.sp = w4_split(per, lines, xrows, 66 * 1024);
         const bool direct = m.g.sp.kw == 1 && m.g.sp.chunk >= lines;
         const int64_t sums = direct ? 0 : W4_WAVES * m.g.sp.each * slot;
-        const int64_t lds = W4Lds<G>::x_bytes((int32_t)xrows, m.g.sp.chunk) + W4Lds<G>::RINGS + sums;
-        m.lds = (uint32_t)max((int64_t)EXPERTS_MAX * 4, lds);
+        m.g.x_bytes = W4Lds<G>::x_bytes((int32_t)xrows, m.g.sp.chunk);
+        m.lds = (uint32_t)(m.g.x_bytes + W4Lds<G>::RINGS + sums);
         if (m.lds <= MOE_LDS || per == 1) break;
     }
     const int64_t wide = (int64_t)(W4_WAVES / m.g.sp.kw) * m.g.sp.each;

@@ -29,11 +29,12 @@ __global__ __launch_bounds__(64 * W4_WAVES) void w4_few_kernel(const T *__restri
     const int32_t have = min(per, (a.N + 15) / 16 - t0), mine = wave / kw * each;
     float *const slots = (float *)(smem + W4Lds<G>::x_bytes(rows, a.sp.chunk) + W4Lds<G>::RINGS);
     const int32_t slot = rows * W4_SLOT_LD, lines = (a.K + 255) / 256;
-    w4_flow<T, T, MT, G, 1>(
-        smem, a.w, a.p, a.K, rows, a.sp, max(0, min(each, have - mine)), make_rsrc(X + (int64_t)m0 * a.ldx, 0xFFFFFFF0u),
-        [&](int32_t row) { return (uint32_t)row * (uint32_t)a.ldx * 2u; },
-        [&](int32_t t) { return W4Tile{(int64_t)(t0 + mine + t) * 16, min(16, a.N - (t0 + mine + t) * 16)}; },
-        [&](int32_t t, const f32x4(&acc)[MT], bool more) { w4_put<MT>(slots + (wave * each + t) * slot, rows, acc, more); });
+    auto tile_at = [&](int32_t t) { return W4Tile{(int64_t)(t0 + mine + t) * 16, min(16, a.N - (t0 + mine + t) * 16)}; };
+    W4Flow<T, T, MT, G, 1, decltype(tile_at)> flow(smem, W4Lds<G>::x_bytes(rows, a.sp.chunk), a.w, a.p, a.K, a.sp,
+                                                   max(0, min(each, have - mine)), tile_at);
+    flow.run(rows, make_rsrc(X + (int64_t)m0 * a.ldx, 0xFFFFFFF0u), false,
+             [&](int32_t row) { return (uint32_t)row * (uint32_t)a.ldx * 2u; },
+             [&](int32_t t, const f32x4(&acc)[MT], bool more) { w4_put<MT>(slots + (wave * each + t) * slot, rows, acc, more); });
     __syncthreads();
     for (int32_t i = (int32_t)threadIdx.x; i < rows * have * 16; i += 64 * W4_WAVES) {
         const int32_t m = i / (have * 16), c = i - m * have * 16, t = c / 16, n = t0 * 16 + c;

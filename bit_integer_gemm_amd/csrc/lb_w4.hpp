@@ -121,67 +121,72 @@ template <int G> struct W4Lds {
 
 template <int N> __device__ inline void w4_wait() { asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory"); }
 
-// The products of a wave's tiles: 16 MT rows of x at most (`rows` of them) by 16 columns each.
-//   lds: W4Lds; x rows are read through rx, row i's first byte at x_at(i) (PLANES 2: rows
-//     from `rows` on are the second plane's, x is the sum of both).
+// The products of a wave's tiles: 16 MT rows of x at most by 16 columns each.
+//   lds: x (x_bytes of it; PLANES 2: x is the sum of two planes, whose rows follow each other),
+//     then the rings.  Copies of three lines are under way while a fourth is worked on; each
+//     wave waits for its own by count.
 //   tiles: this wave's; tile_at(t): a W4Tile.
-//   done(t, acc, more): sums of tile t over this wave's lines of a chunk, more: not the first chunk's;
-//     acc[m][i] is row 4 (lane / 16) + i of 16 rows m, column lane % 16.
 //   T: the type of x as the matrix cores take it; PT: of the groups' numbers.
-// Every wave of the workgroup calls this, also without tiles (x is copied by all).  Copies of two
-// lines are under way while a third is worked on; each wave waits for its own by count.
-template <class T, class PT, int MT, int G, int PLANES, class XAt, class TileAt, class Done>
-__device__ inline void w4_flow(char *lds, const uint8_t *W, const uint32_t *P, int32_t K, int32_t rows, const W4Split &sp,
-                               int32_t tiles, const i32x4 rx, XAt &&x_at, TileAt &&tile_at, Done &&done)
-{
+// Every wave of a workgroup makes the same calls, also one without tiles (x is copied by all).
+template <class T, class PT, int MT, int G, int PLANES, class TileAt>
+struct W4Flow {
     typedef W4Lds<G> L;
-    constexpr int GROUPS = L::GROUPS, HALF = GROUPS / 2, STEPS = G / 32;
-    const int32_t lane = (int32_t)(threadIdx.x & 63u), q = lane >> 4, r = lane & 15;
-    const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), share = wave % sp.kw;
-    const uint32_t kb = (uint32_t)K / 2u, groups = (uint32_t)K / G;
-    const int32_t lines = (K + 255) / 256, xrows = PLANES * rows;
-    char *const ring = lds + L::x_bytes(xrows, sp.chunk) + wave * L::RING;
-    const uint32_t ring_at = lds_addr(ring), x_lds = lds_addr(lds);
+    enum : int { GROUPS = L::GROUPS, HALF = GROUPS / 2, STEPS = G / 32 };
+    char *const lds;
+    const uint8_t *const W;
+    const uint32_t *const P;
+    const int32_t K, lines, tiles;
+    const W4Split sp;
+    const TileAt tile_at;
+    const int32_t lane, wave, share;
+    const uint32_t kb, groups;
+    char *const ring;
+    // what is copied next
+    int32_t c_chunk, c_tile, c_line, c_lo, c_hi;
+    bool left;
+    i32x4 rw, rp;
+    uint32_t c_at, c_slot, row_at, piece;
 
-    // Lines of a chunk that are this wave's.
-    auto bounds = [&](int32_t c, int32_t &lo, int32_t &hi) {
+    __device__ inline W4Flow(char *lds_, uint32_t x_bytes, const uint8_t *W_, const uint32_t *P_, int32_t K_, const W4Split &sp_,
+                             int32_t tiles_, const TileAt &at_)
+        : lds(lds_), W(W_), P(P_), K(K_), lines((K_ + 255) / 256), tiles(tiles_), sp(sp_), tile_at(at_),
+          lane((int32_t)(threadIdx.x & 63u)), wave(__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6))), share(wave % sp_.kw),
+          kb((uint32_t)K_ / 2u), groups((uint32_t)K_ / G), ring(lds_ + x_bytes + wave * L::RING)
+    {
+    }
+
+    // Lines of the chunk from line c on that are this wave's.
+    __device__ inline void bounds(int32_t c, int32_t &lo, int32_t &hi) const
+    {
         const int32_t n = min(sp.chunk, lines - c);
         lo = c + n * share / sp.kw;
         hi = c + n * (share + 1) / sp.kw;
-    };
-
-    // ---- the ring: lane l of a copy takes piece (l % 8) ^ (l / 8) of row l / 8, which keeps reads of
-    // eight rows off each other's banks
-    int32_t c_chunk = 0, c_tile = 0, c_line, c_hi, c_lo;   // what is copied next
-    i32x4 rw, rp;
-    const uint32_t piece = 16u * (uint32_t)((lane & 7) ^ (lane >> 3)), row_at = (uint32_t)(lane >> 3) * kb + piece;
-    auto aim = [&] {
+    }
+    __device__ inline void aim()
+    {
         const W4Tile t = tile_at(c_tile);
         rw = make_rsrc(W + t.row * kb, (uint64_t)(uint32_t)t.rows * kb);
         rp = make_rsrc(P + t.row * groups, (uint64_t)(uint32_t)t.rows * groups * 4u);
-    };
-    bounds(0, c_lo, c_hi);
-    c_line = c_lo;
-    bool left = tiles > 0;
-    if (left && c_lo == c_hi) left = false;   // (only where there is one chunk)
-    if (left) aim();
-    else rw = rp = make_rsrc(W, 0);
-    uint32_t c_at = ring_at, c_ring = 0;
-    auto copy = [&] {
+    }
+    // The next line into the ring: lane l of a copy takes piece (l % 8) ^ (l / 8) of row l / 8, which
+    // keeps reads of eight rows off each other's banks.  Past the last one nothing is read.
+    __device__ inline void copy()
+    {
         const uint32_t at = (uint32_t)c_line * 128u;
         const bool in = left && at + piece < kb;
 #pragma unroll
         for (int i = 0; i < 2; ++i) dma16(rw, in ? row_at + (uint32_t)(8 * i) * kb + at : 0xFFFFFFF0u, c_at + 1024u * (uint32_t)i);
 #pragma unroll
         for (int i = 0; i < L::COPIES - 2; ++i) {
+            const int32_t q = lane >> 4, r = lane & 15;
             const uint32_t g = (uint32_t)(c_line * GROUPS + 4 * i + q);
             const bool there = left && (GROUPS >= 4 || q < GROUPS) && g < groups;
             dma4(rp, there ? ((uint32_t)r * groups + g) * 4u : 0xFFFFFFF0u, c_at + 2048u + 256u * (uint32_t)i);
         }
         c_at += L::STAGE;
-        if (++c_ring == L::DEPTH) {
-            c_ring = 0;
-            c_at = ring_at;
+        if (++c_slot == L::DEPTH) {
+            c_slot = 0;
+            c_at -= L::RING;
         }
         if (left && ++c_line == c_hi) {
             if (++c_tile == tiles) {
@@ -196,112 +201,142 @@ __device__ inline void w4_flow(char *lds, const uint8_t *W, const uint32_t *P, i
             c_line = c_lo;
             if (left) aim();
         }
-    };
+    }
+    // Asks for the first lines.
+    __device__ inline void start()
+    {
+        c_chunk = c_tile = 0;
+        bounds(0, c_lo, c_hi);
+        c_line = c_lo;
+        left = tiles > 0 && c_lo < c_hi;   // (no lines: only where there is one chunk)
+        if (left) aim();
+        else rw = rp = make_rsrc(W, 0);
+        c_at = lds_addr(ring);
+        c_slot = 0;
+        piece = 16u * (uint32_t)((lane & 7) ^ (lane >> 3));
+        row_at = (uint32_t)(lane >> 3) * kb + piece;
+#pragma unroll
+        for (int d = 0; d < L::DEPTH - 1; ++d) copy();
+    }
 
-    // ---- x of a chunk: piece p of row i lies at p ^ i % 8 of the row
-    auto ask_x = [&](int32_t c) {
+    // x of the chunk from line c on: piece p of row i lies at p ^ i % 8 of the row.
+    template <class XAt> __device__ inline void ask_x(int32_t c, int32_t xrows, const i32x4 rx, XAt &&x_at)
+    {
         const int32_t per = min(sp.chunk, lines - c) * 32, all = per * xrows;
         for (int32_t i0 = wave * 64; i0 < all; i0 += 64 * W4_WAVES) {
             const int32_t i = min(i0 + lane, all - 1), row = i / per, p = (i - row * per) ^ (row & 7);
             const int32_t k = c * 256 + 8 * p;
-            dma16(rx, i0 + lane < all && k < K ? x_at(row) + 2u * (uint32_t)k : 0xFFFFFFF0u, x_lds + 16u * (uint32_t)i0);
+            dma16(rx, i0 + lane < all && k < K ? x_at(row) + 2u * (uint32_t)k : 0xFFFFFFF0u, lds_addr(lds) + 16u * (uint32_t)i0);
         }
-    };
-    auto order_x = [&](int32_t c) {   // each lane what it copied itself
+    }
+    __device__ inline void order_x(int32_t c, int32_t xrows)   // each lane what it copied itself
+    {
         const int32_t all = min(sp.chunk, lines - c) * 32 * xrows;
         for (int32_t i = (int32_t)threadIdx.x; i < all; i += 64 * W4_WAVES) {
             u32x4 *p = (u32x4 *)(lds + 16 * i);
             *p = w4_order(*p);
         }
-    };
+        __syncthreads();
+    }
 
-    ask_x(0);
-#pragma unroll
-    for (int d = 0; d < L::DEPTH - 1; ++d) copy();
-    w4_wait<(L::DEPTH - 1) * L::COPIES>();
-    order_x(0);
-    __syncthreads();
-
-    const W4Const konst = w4_const<T>();
-    uint32_t at = 0, slot = 0;   // of the ring
-    uint32_t xrow[MT][PLANES];
-    for (int32_t c = 0; c < lines; c += sp.chunk) {
-        if (c) {
-            __syncthreads();
-            ask_x(c);
+    // `rows` rows of x through rx, row i's first byte at x_at(i) (PLANES 2: rows from `rows` on are
+    // the second plane's).  started: start() has been called.
+    //   done(t, acc, more): sums of tile t over this wave's lines of a chunk, more: not the first
+    //     chunk's; acc[m][i] is row 4 (lane / 16) + i of 16 rows m, column lane % 16.
+    template <class XAt, class Done> __device__ inline void run(int32_t rows, const i32x4 rx, bool started, XAt &&x_at, Done &&done)
+    {
+        const int32_t q = lane >> 4, r = lane & 15, xrows = PLANES * rows;
+        ask_x(0, xrows, rx, x_at);
+        if (started) {
             w4_wait<0>();
-            order_x(c);
-            __syncthreads();
+        } else {
+            start();
+            w4_wait<(L::DEPTH - 1) * L::COPIES>();
         }
-        const uint32_t bytes = (uint32_t)min(sp.chunk, lines - c) * 512u;
+        order_x(0, xrows);
+
+        const W4Const konst = w4_const<T>();
+        uint32_t at = 0, slot = 0;   // of the ring
+        uint32_t xrow[MT][PLANES];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int pl = 0; pl < PLANES; ++pl) xrow[m][pl] = (uint32_t)(min(16 * m + r, rows - 1) + pl * rows);
-        int32_t lo, hi;
-        bounds(c, lo, hi);
-        if (lo == hi) continue;
-        for (int32_t tile = 0; tile < tiles; ++tile) {
-            f32x4 acc[MT];
+        for (int32_t c = 0; c < lines; c += sp.chunk) {
+            if (c) {
+                __syncthreads();
+                ask_x(c, xrows, rx, x_at);
+                w4_wait<0>();
+                order_x(c, xrows);
+            }
+            const uint32_t bytes = (uint32_t)min(sp.chunk, lines - c) * 512u;
+            int32_t lo, hi;
+            bounds(c, lo, hi);
+            if (lo == hi) continue;
+            for (int32_t tile = 0; tile < tiles; ++tile) {
+                f32x4 acc[MT];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-            for (int32_t line = lo; line < hi; ++line) {
-                copy();
-                w4_wait<(L::DEPTH - 1) * L::COPIES>();
-                const char *st = ring + at;
+                for (int m = 0; m < MT; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int32_t line = lo; line < hi; ++line) {
+                    copy();
+                    w4_wait<(L::DEPTH - 1) * L::COPIES>();
+                    const char *st = ring + at;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {   // 128 weights
-                    u32x4 w = *(const u32x4 *)(st + 128 * r + 16 * ((4 * h + q) ^ (r & 7)));
-                    if constexpr (G != 128) w4_transpose(w);
-                    u32x4 x[4][MT][PLANES];
+                    for (int h = 0; h < 2; ++h) {   // 128 weights
+                        u32x4 w = *(const u32x4 *)(st + 128 * r + 16 * ((4 * h + q) ^ (r & 7)));
+                        if constexpr (G != 128) w4_transpose(w);
+                        u32x4 x[4][MT][PLANES];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-#pragma unroll
-                        for (int m = 0; m < MT; ++m)
-#pragma unroll
-                            for (int pl = 0; pl < PLANES; ++pl) {
-                                const int32_t p = 16 * h + (G == 128 ? 4 * q + j : 4 * j + q);
-                                x[j][m][pl] = *(const u32x4 *)(lds + xrow[m][pl] * bytes + (uint32_t)(line - c) * 512u +
-                                                               16u * ((uint32_t)p ^ (xrow[m][pl] & 7u)));
-                            }
-#pragma unroll
-                    for (int g = 0; g < HALF; ++g) {
-                        f32x4 sum[MT], xs[MT];
-#pragma unroll
-                        for (int m = 0; m < MT; ++m) sum[m] = xs[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int j = g * STEPS; j < (g + 1) * STEPS; ++j) {
-                            const u32x4 lv = w4_levels<T>(w[j], konst);
-                            const uint32_t one = one_pair<T>();
+                        for (int j = 0; j < 4; ++j)
 #pragma unroll
                             for (int m = 0; m < MT; ++m)
 #pragma unroll
                                 for (int pl = 0; pl < PLANES; ++pl) {
-                                    xs[m] = mfma16<T>(x[j][m][pl], u32x4{one, one, one, one}, xs[m]);
-                                    sum[m] = mfma16<T>(x[j][m][pl], lv, sum[m]);
+                                    const int32_t p = 16 * h + (G == 128 ? 4 * q + j : 4 * j + q);
+                                    x[j][m][pl] = *(const u32x4 *)(lds + xrow[m][pl] * bytes + (uint32_t)(line - c) * 512u +
+                                                                   16u * ((uint32_t)p ^ (xrow[m][pl] & 7u)));
+                                }
+#pragma unroll
+                        for (int g = 0; g < HALF; ++g) {
+                            f32x4 sum[MT], xs[MT];
+#pragma unroll
+                            for (int m = 0; m < MT; ++m) sum[m] = xs[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                            for (int j = g * STEPS; j < (g + 1) * STEPS; ++j) {
+                                const u32x4 lv = w4_levels<T>(w[j], konst);
+                                const uint32_t one = one_pair<T>();
+#pragma unroll
+                                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                                    for (int pl = 0; pl < PLANES; ++pl) {
+                                        xs[m] = mfma16<T>(x[j][m][pl], u32x4{one, one, one, one}, xs[m]);
+                                        sum[m] = mfma16<T>(x[j][m][pl], lv, sum[m]);
+                                    }
+                            }
+                            const uint32_t n = *(const uint32_t *)(st + 2048 + 64 * (h * HALF + g) + 4 * r);
+                            const float s = lo_f32<PT>(n), b = hi_f32<PT>(n) - 16.0f * s;
+#pragma unroll
+                            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    acc[m][i] = __builtin_fmaf(s, sum[m][i], acc[m][i]);
+                                    acc[m][i] = __builtin_fmaf(b, xs[m][i], acc[m][i]);
                                 }
                         }
-                        const uint32_t n = *(const uint32_t *)(st + 2048 + 64 * (h * HALF + g) + 4 * r);
-                        const float s = lo_f32<PT>(n), b = hi_f32<PT>(n) - 16.0f * s;
-#pragma unroll
-                        for (int m = 0; m < MT; ++m)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                acc[m][i] = __builtin_fmaf(s, sum[m][i], acc[m][i]);
-                                acc[m][i] = __builtin_fmaf(b, xs[m][i], acc[m][i]);
-                            }
                     }
+                    // the next copies overwrite what has been read here
+                    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+                    at += L::STAGE;
+                    if (++slot == L::DEPTH) slot = at = 0;
                 }
-                // the next copies overwrite what has been read here
-                asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
-                at += L::STAGE;
-                if (++slot == L::DEPTH) slot = at = 0;
+                done(tile, acc, c > 0);
             }
-            done(tile, acc, c > 0);
         }
+        finish();
     }
-    w4_wait<0>();   // no copy outlives the workgroup's LDS
-}
+    // No copy outlives the workgroup's use of the LDS.
+    __device__ inline void finish() { w4_wait<0>(); }
+};
 
 // A wave's sums into LDS, or (more) onto what it left there: `rows` rows of x by 16 columns, rows 20 floats apart (a lane's four rows lie
 // on other banks).
@@ -319,17 +354,20 @@ template <int MT> __device__ inline void w4_put(float *slot, int32_t rows, const
             }
 }
 
-// The split of `tiles` tiles of `lines` lines: the fewest lines for the busiest wave, and of equals
-// the fewest shares; chunks of x of at most x_bytes.
+// The split of `tiles` tiles of `lines` lines, x in chunks of at most x_bytes: about the fewest lines
+// for the busiest wave (a tenth more, where that takes fewer shares and so fewer sums to join).
 inline W4Split w4_split(int64_t tiles, int64_t lines, int64_t xrows, int64_t x_bytes)
 {
     int64_t chunk = x_bytes / (512 * xrows);
     if (chunk > lines) chunk = lines;
     if (chunk < 1) chunk = 1;
-    W4Split best{1, (int32_t)((tiles + W4_WAVES - 1) / W4_WAVES), (int32_t)chunk};
-    for (int kw = 2; kw <= W4_WAVES && (chunk == lines || kw <= chunk); kw *= 2) {
-        const W4Split s{kw, (int32_t)((tiles + W4_WAVES / kw - 1) / (W4_WAVES / kw)), (int32_t)chunk};
-        if ((lines + kw - 1) / kw * s.each < (lines + best.kw - 1) / best.kw * best.each) best = s;
+    W4Split best{};
+    int64_t least = 0;
+    for (int kw = W4_WAVES; kw; kw /= 2) {
+        if (kw > 1 && chunk < lines && kw > chunk) continue;
+        const int64_t each = (tiles + W4_WAVES / kw - 1) / (W4_WAVES / kw), cost = (lines + kw - 1) / kw * each;
+        if (!least || cost < least) least = cost;
+        if (!best.kw || 10 * cost <= 11 * least) best = W4Split{kw, (int32_t)each, (int32_t)chunk};
     }
     if (chunk < lines) best.chunk = (int32_t)(chunk / best.kw * best.kw);   // equal shares of every whole chunk
     return best;
