@@ -72,7 +72,6 @@ enum { EXPERTS_MAX = 1024 };
 struct MoeList {
     int32_t rank[MOE_TOKENS];   // the expert's rank in each token's order, if below k, else -1
     int32_t row[MOE_TOKENS];    // token * k + rank of each of its tokens
-    int32_t count;
 };
 
 // Number j (from 0) in a token's order of its logits, by every wave for itself: lane l holds
@@ -125,53 +124,68 @@ __device__ inline MoeSlot moe_slot(const MoeArgs &a, int32_t slot, bool by_pair)
                     : a.E <= 256 ? nth_expert<4>(row, a.E, j) : nth_expert<16>(row, a.E, j);
     return MoeSlot{__builtin_amdgcn_readfirstlane(e), t};
 }
-// Ranks of an expert in the orders of the tokens of this wave (every eighth).
+// Ranks of an expert in the orders of the tokens of this wave (every eighth).  ask() loads the first
+// 128 logits of each, ahead of the search for the expert.
 constexpr int MOE_EACH = MOE_TOKENS / W4_WAVES;
-__device__ inline void moe_ranks(const MoeArgs &a, int32_t e, int32_t (&above)[MOE_EACH])
-{
-    constexpr int AHEAD = 2;   // 64 logits of all these tokens each, under way together
-    const int32_t lane = (int32_t)threadIdx.x & 63, wave = (int32_t)threadIdx.x >> 6;
-    float own[MOE_EACH];
-#pragma unroll
-    for (int i = 0; i < MOE_EACH; ++i) {
-        own[i] = a.logits[min(wave + W4_WAVES * i, a.T - 1) * a.E + e];
-        above[i] = 0;
-    }
-    for (int32_t f0 = 0; f0 < a.E; f0 += 64 * AHEAD) {
-        float v[AHEAD][MOE_EACH];
+struct MoeRanks {
+    enum : int { AHEAD = 2 };
+    float v[AHEAD][MOE_EACH];
+    int32_t above[MOE_EACH];
+    __device__ inline void load(const MoeArgs &a, int32_t f0)
+    {
+        const int32_t lane = (int32_t)threadIdx.x & 63, wave = (int32_t)threadIdx.x >> 6;
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u)
 #pragma unroll
             for (int i = 0; i < MOE_EACH; ++i)
                 v[u][i] = a.logits[min(wave + W4_WAVES * i, a.T - 1) * a.E + min(f0 + 64 * u + lane, a.E - 1)];
+    }
+    __device__ inline void ask(const MoeArgs &a) { load(a, 0); }
+    __device__ inline void count(const MoeArgs &a, int32_t e)
+    {
+        const int32_t lane = (int32_t)threadIdx.x & 63, wave = (int32_t)threadIdx.x >> 6;
+        float own[MOE_EACH];
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u)
+        for (int i = 0; i < MOE_EACH; ++i) {
+            own[i] = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(e < 64 ? v[0][i] : v[1][i]), e & 63));
+            above[i] = 0;
+        }
+        if (e >= 64 * AHEAD)
+#pragma unroll
+            for (int i = 0; i < MOE_EACH; ++i) own[i] = a.logits[min(wave + W4_WAVES * i, a.T - 1) * a.E + e];
+        for (int32_t f0 = 0;;) {
 #pragma unroll
             for (int i = 0; i < MOE_EACH; ++i) {
-                const int32_t f = f0 + 64 * u + lane;
-                const uint32_t mine = order_of(own[i]), o = order_of(v[u][i]);
-                above[i] += __popcll(__ballot(f < a.E && (o > mine || (o == mine && f < e))));
-            }
-    }
-}
-// The list of the expert's tokens (to all threads).  Returns how many; 0 where an earlier slot's
-// workgroups work for them.
-__device__ inline int32_t moe_tokens(const MoeArgs &a, const MoeSlot &s, const int32_t (&above)[MOE_EACH], MoeList &l)
-{
-    const int32_t lane = (int32_t)threadIdx.x & 63, wave = (int32_t)threadIdx.x >> 6;
-    if (lane == 0)
+                if (__builtin_amdgcn_readfirstlane(wave) + W4_WAVES * i >= a.T) break;
+                const uint32_t mine = order_of(own[i]);
 #pragma unroll
-        for (int i = 0; i < MOE_EACH; ++i) l.rank[wave + W4_WAVES * i] = wave + W4_WAVES * i < a.T && above[i] < a.top_k ? above[i] : -1;
-    __syncthreads();
-    if (wave == 0) {
+                for (int u = 0; u < AHEAD; ++u) {
+                    if (f0 + 64 * u >= a.E) break;
+                    const int32_t f = f0 + 64 * u + lane;
+                    const uint32_t o = order_of(v[u][i]);
+                    above[i] += __popcll(__ballot(f < a.E && (o > mine || (o == mine && f < e))));
+                }
+            }
+            f0 += 64 * AHEAD;
+            if (f0 >= a.E) break;
+            load(a, f0);
+        }
+    }
+    // The list of the expert's tokens.  Returns how many; 0 where an earlier slot's workgroups work for
+    // them.  (Every wave writes the same list and reads what it wrote.)
+    __device__ inline int32_t list(const MoeArgs &a, const MoeSlot &s, MoeList &l) const
+    {
+        const int32_t lane = (int32_t)threadIdx.x & 63, wave = (int32_t)threadIdx.x >> 6;
+        if (lane == 0)
+#pragma unroll
+            for (int i = 0; i < MOE_EACH; ++i) l.rank[wave + W4_WAVES * i] = wave + W4_WAVES * i < a.T && above[i] < a.top_k ? above[i] : -1;
+        __syncthreads();
         const int32_t rank = l.rank[lane];
         const uint64_t in = __ballot(rank >= 0);
         if (rank >= 0) l.row[__popcll(in & ((1ull << lane) - 1))] = lane * a.top_k + rank;
-        if (lane == 0) l.count = in & ((1ull << s.first) - 1) ? 0 : __popcll(in);
+        return in & ((1ull << s.first) - 1) ? 0 : __popcll(in);
     }
-    __syncthreads();
-    return __builtin_amdgcn_readfirstlane(l.count);
-}
+};
 
 // ---- gate and up, activation -----------------------------------------------
 // A workgroup: an expert, some blocks of 16 columns, g.rows of its tokens at a time.
@@ -186,10 +200,11 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGri
 {
     extern __shared__ __attribute__((aligned(1024))) char smem[];
     __shared__ MoeList list;
+    MoeRanks ranks;
+    ranks.ask(a);
     const MoeSlot ms = moe_slot(a, (int32_t)blockIdx.y, g.by_pair);
     const int32_t expert = ms.expert;
-    int32_t above[MOE_EACH];
-    moe_ranks(a, expert, above);
+    ranks.count(a, expert);
     const int32_t lane = (int32_t)(threadIdx.x & 63u), q = lane >> 4, r = lane & 15;
     const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int32_t kw = g.sp.kw, each = g.sp.each, lines = (a.H + 255) / 256;
@@ -209,7 +224,7 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGri
                                                   2 * max(0, min(each, have - mine)), tile_at);
     // the first weights are on their way while the tokens are gathered
     flow.start();
-    const int32_t count = moe_tokens(a, ms, above, list);
+    const int32_t count = ranks.list(a, ms, list);
     if (count == 0) flow.finish();
     for (int32_t at = 0; at < count; at += g.rows) {
         const int32_t rows = min(g.rows, count - at), slot = rows * W4_SLOT_LD;
@@ -252,10 +267,11 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_kernel(MoeArgs a, MoeG
 {
     extern __shared__ __attribute__((aligned(1024))) char smem[];
     __shared__ MoeList list;
+    MoeRanks ranks;
+    ranks.ask(a);
     const MoeSlot ms = moe_slot(a, (int32_t)blockIdx.y, g.by_pair);
     const int32_t expert = ms.expert;
-    int32_t above[MOE_EACH];
-    moe_ranks(a, expert, above);
+    ranks.count(a, expert);
     const int32_t lane = (int32_t)(threadIdx.x & 63u), q = lane >> 4, r = lane & 15;
     const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int32_t kw = g.sp.kw, each = g.sp.each, lines = (a.I + 255) / 256;
@@ -267,7 +283,7 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_kernel(MoeArgs a, MoeG
     W4Flow<__bf16, T, 1, G, 2, decltype(tile_at)> flow(smem, g.x_bytes, a.w2, (const uint32_t *)a.p2, a.I, g.sp,
                                                        max(0, min(each, have - mine)), tile_at);
     flow.start();
-    const int32_t count = moe_tokens(a, ms, above, list);
+    const int32_t count = ranks.list(a, ms, list);
     if (count == 0) flow.finish();
     for (int32_t at = 0; at < count; at += g.rows) {
         const int32_t rows = min(g.rows, count - at), slot = rows * W4_SLOT_LD;
