@@ -164,9 +164,9 @@ struct W4Args {
 hipError_t launch_linear_w4(int ftype, int group, const W4Args &a, int cu, hipStream_t s);
 
 // The same for many rows, with a workspace of linear_w4_rows_workspace bytes.
-hipError_t launch_linear_w4_rows(int ftype, int group, const W4Args &a, void *workspace, hipStream_t s);
-int64_t linear_w4_rows_workspace(int64_t M, int64_t K, int64_t group);
-enum { W4_FEW_ROWS = 64 };   // rows that the first of these takes
+hipError_t launch_linear_w4_rows(int ftype, int group, const W4Args &a, int cu, void *workspace, hipStream_t s);
+int64_t linear_w4_rows_workspace(int64_t M, int64_t N, int64_t K, int64_t group, int cu);
+enum { W4_FEW_ROWS = 16 };   // rows that the first of these takes
 
 // The mixture of experts, for at most MOE_TOKENS tokens a launch.
 enum { MOE_TOKENS = 64 };

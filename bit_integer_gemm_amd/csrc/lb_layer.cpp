@@ -182,7 +182,7 @@ int lb_rope(const void *Q, int64_t ldq, const void *K, int64_t ldk, const int64_
 int64_t lb_linear_w4_workspace(int64_t M, int64_t K, int64_t N, int64_t group)
 {
     if (check_w4(M, N, K, group, LB_BF16) != LB_OK || M <= lb::W4_FEW_ROWS) return 0;
-    return lb::linear_w4_rows_workspace(M, K, group);
+    return lb::linear_w4_rows_workspace(M, N, K, group, cu_count());
 }
 
 int lb_linear_w4(const void *X, int64_t ldx, const uint8_t *W, const void *Wp, const void *bias, void *out, int64_t M,
@@ -208,7 +208,7 @@ int lb_linear_w4(const void *X, int64_t ldx, const uint8_t *W, const void *Wp, c
     a.M = M;
     a.N = N;
     a.K = K;
-    if (need > 0) return finish(lb::launch_linear_w4_rows(ftype, (int)group, a, workspace, (hipStream_t)stream));
+    if (need > 0) return finish(lb::launch_linear_w4_rows(ftype, (int)group, a, cu_count(), workspace, (hipStream_t)stream));
     return finish(lb::launch_linear_w4(ftype, (int)group, a, cu_count(), (hipStream_t)stream));
 }
 

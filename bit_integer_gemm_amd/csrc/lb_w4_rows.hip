@@ -41,10 +41,10 @@ __global__ __launch_bounds__(256) void w4_prepare_kernel(const T *__restrict__ X
 }
 
 // ---- the product -----------------------------------------------------------
-// 128 rows by 256 columns to a workgroup of eight waves, 64 x 64 to a wave (2 x 2 tiles of
-// 32 x 32), stages of 128 weights in a ring of three in LDS.  A wave keeps a stage's
-// activations in registers and takes its two tiles of columns one after the other, so that
-// scaling the one's sums runs beside the other's matrix instructions.
+// 64 WM rows by 128 WN columns to a workgroup of eight waves (2 x 4), 32 WM x 32 WN to a wave,
+// stages of 128 weights in a ring of three in LDS.  A wave keeps a stage's activations in
+// registers; the sums of one tile of 32 columns are scaled beside the other's matrix
+// instructions.  Or a part of K to a workgroup, whose fp32 sums a second launch adds up.
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 template <class T> __device__ inline f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c)
 {
@@ -62,25 +62,28 @@ struct RowsArgs {
     const uint8_t *w;
     const uint32_t *p;
     const void *bias;
-    void *out;
+    void *out;              // or, with more than one part of K, parts of M x N fp32
     int64_t ldo;
-    int32_t M, N, K, Kp, groups, groups16;
+    int32_t M, N, K, Kp, groups, groups16, splits;
     uint32_t tiles_m, tiles_n;
 };
 
-template <int G> struct RowsLds {
+template <int G, int WM, int WN> struct RowsLds {
     enum : int {
-        BM = 128, BN = 256, STAGES = 3,
-        X = BM * 256, W = BN * 64, NUMBERS = G == 32 ? 4096 : 2048,
-        STAGE = X + W + NUMBERS,
-        COPIES = 4 + 2 + (G == 32 ? 2 : 1)   // a wave's copies of a stage
+        BM = 64 * WM, BN = 128 * WN, STAGES = 3,
+        X = BM * 256, W = BN * 64, WORDS = BN * 128 / G,
+        XC = 2 * WM, WC = WN,                                  // a wave's copies of a stage: x, weights,
+        NC = WORDS > 512 ? WORDS / 512 : 1,                    // numbers
+        NUMBERS = NC * 2048, STAGE = X + W + NUMBERS, COPIES = XC + WC + NC,
+        OUT_LD = BN + 8                                        // the tile on its way out, 16-bit
     };
+    static_assert(BM * OUT_LD * 2 <= STAGES * STAGE, "the tile over the ring");
 };
 
-template <class T, int G>
+template <class T, int G, int WM, int WN>
 __global__ __launch_bounds__(512, 2) void w4_rows_kernel(RowsArgs a)
 {
-    typedef RowsLds<G> L;
+    typedef RowsLds<G, WM, WN> L;
     constexpr int PER = 128 / G;   // groups of a stage
     extern __shared__ __attribute__((aligned(1024))) char smem[];
     const int32_t lane = (int32_t)(threadIdx.x & 63u), r = lane & 31, h = lane >> 5;
@@ -91,117 +94,126 @@ __global__ __launch_bounds__(512, 2) void w4_rows_kernel(RowsArgs a)
     const int32_t m0 = (int32_t)tm * L::BM, n0 = (int32_t)tn * L::BN;
     const int32_t rows = min((int)L::BM, a.M - m0), cols = min((int)L::BN, a.N - n0);
     const uint32_t kb = (uint32_t)a.K / 2u;
+    const int32_t stages = a.Kp / 128, part = (int32_t)blockIdx.y;
+    const int32_t first = part * stages / a.splits, last = (part + 1) * stages / a.splits;
 
     const i32x4 rx = make_rsrc((const T *)a.x + (int64_t)m0 * a.Kp, (uint64_t)(uint32_t)rows * (uint32_t)a.Kp * 2u);
     const i32x4 rw = make_rsrc(a.w + (int64_t)n0 * kb, (uint64_t)(uint32_t)cols * kb);
     const i32x4 rp = make_rsrc(a.p + (int64_t)n0 * a.groups, (uint64_t)(uint32_t)cols * (uint32_t)a.groups * 4u);
     const uint32_t lds0 = lds_addr(smem);
 
-    // Copies.  x: four rows of 16 pieces at a time, piece p of row i at p ^ i % 8; weights: 16 rows
-    // of 4 pieces, piece p of row i at p ^ i / 2 % 4; numbers: word (group, column).
-    const uint32_t x_row = 16u * (uint32_t)wave + (uint32_t)(lane >> 4);
-    const uint32_t w_row = 32u * (uint32_t)wave + (uint32_t)(lane >> 2);
-    const uint32_t w_piece = 16u * (uint32_t)((lane & 3) ^ ((lane >> 3) & 3));
-    auto copy = [&](int32_t st, uint32_t base) {
-        const bool there = st * 128 < a.Kp;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t row = x_row + 4u * (uint32_t)i, piece = (uint32_t)(lane & 15) ^ (row & 7u);
+    // Copies.  x: four rows of 16 pieces at a time, piece p of row i at p ^ i % 16; weights: 16
+    // rows of 4 pieces, piece p of row i at p ^ i / 4 % 4 (16 lanes' reads then lie on all 64
+    // banks); numbers: word (group, column).
+    const uint32_t x_row = 4u * (uint32_t)(L::XC * wave) + (uint32_t)(lane >> 4);
+    const uint32_t w_row = 16u * (uint32_t)(L::WC * wave) + (uint32_t)(lane >> 2);
+    const uint32_t w_piece = 16u * (uint32_t)((lane & 3) ^ ((lane >> 4) & 3));
+    auto copy = [&](int i, int32_t st, uint32_t base) {   // number i of a wave's copies of stage st
+        const bool there = st < last;
+        if (i < L::XC) {
+            const uint32_t row = x_row + 4u * (uint32_t)i, piece = (uint32_t)(lane & 15) ^ (row & 15u);
             dma16(rx, there ? row * (uint32_t)a.Kp * 2u + (uint32_t)st * 256u + 16u * piece : 0xFFFFFFF0u,
-                  base + 1024u * (uint32_t)(4 * wave + i));
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
+                  base + 1024u * (uint32_t)(L::XC * wave + i));
+        } else if (i < L::XC + L::WC) {
             const uint32_t at = (uint32_t)st * 64u + w_piece;
-            dma16(rw, there && at < kb ? (w_row + 16u * (uint32_t)i) * kb + at : 0xFFFFFFF0u,
-                  base + (uint32_t)L::X + 1024u * (uint32_t)(2 * wave + i));
-        }
-#pragma unroll
-        for (int i = 0; i < L::COPIES - 6; ++i) {
-            const int32_t word = 64 * ((L::COPIES - 6) * wave + i) + lane, g = st * PER + word / L::BN;
-            dma4(rp, there && word / L::BN < PER && g < a.groups ? ((uint32_t)(word % L::BN) * (uint32_t)a.groups + (uint32_t)g) * 4u : 0xFFFFFFF0u,
-                 base + (uint32_t)(L::X + L::W) + 256u * (uint32_t)((L::COPIES - 6) * wave + i));
+            dma16(rw, there && at < kb ? (w_row + 16u * (uint32_t)(i - L::XC)) * kb + at : 0xFFFFFFF0u,
+                  base + (uint32_t)L::X + 1024u * (uint32_t)(L::WC * wave + i - L::XC));
+        } else {
+            const int32_t c = L::NC * wave + i - L::XC - L::WC, word = 64 * c + lane, g = st * PER + word / L::BN;
+            dma4(rp, there && word < L::WORDS && g < a.groups ? ((uint32_t)(word % L::BN) * (uint32_t)a.groups + (uint32_t)g) * 4u : 0xFFFFFFF0u,
+                 base + (uint32_t)(L::X + L::W) + 256u * (uint32_t)c);
         }
     };
-    copy(0, lds0);
-    copy(1, lds0 + L::STAGE);
+#pragma unroll
+    for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int i = 0; i < L::COPIES; ++i) copy(i, first + st, lds0 + (uint32_t)(st * L::STAGE));
 
     // The accumulators start from the groups' minima: acc[m][n][i] is row 8 (i / 4) + 4 h + i % 4 of
-    // tile m, column lane % 32 of tile n.
-    f32x16 acc[2][2];
+    // tile m, column lane % 32 of tile n.  16 groups to an instruction, loads of 32 at a time.
+    f32x16 acc[WM][WN];
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int m = 0; m < WM; ++m)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < WN; ++n)
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.f;
     {
-        const __bf16 *xp[2];
-        const uint32_t *np[2];
+        const int32_t lo = first * PER, hi = min(last * PER, a.groups);
+        const __bf16 *xp[WM];
+        const uint32_t *np[WN];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            xp[t] = a.parts + (int64_t)(m0 + min(64 * wm + 32 * t + r, rows - 1)) * a.groups16 + 8 * h;
-            np[t] = a.p + (int64_t)(n0 + min(64 * wn + 32 * t + r, cols - 1)) * a.groups + 8 * h;
-        }
-        for (int32_t g = 0; g < a.groups16; g += 16) {
-            u32x4 xh[2], xl[2];
+        for (int m = 0; m < WM; ++m) xp[m] = a.parts + (int64_t)(m0 + min(32 * (WM * wm + m) + r, rows - 1)) * a.groups16 + 8 * h;
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                xh[m] = *(const u32x4 *)(xp[m] + g);
-                xl[m] = *(const u32x4 *)(xp[m] + a.plane + g);
+        for (int n = 0; n < WN; ++n) np[n] = a.p + (int64_t)(n0 + min(32 * (WN * wn + n) + r, cols - 1)) * a.groups + 8 * h;
+        for (int32_t g = lo / 16 * 16; g < hi; g += 32) {
+            u32x4 xv[2][WM][2];
+            uint32_t nv[2][WN][8];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int32_t gu = min(g + 16 * u, a.groups16 - 16);
+#pragma unroll
+                for (int m = 0; m < WM; ++m) {
+                    xv[u][m][0] = *(const u32x4 *)(xp[m] + gu);
+                    xv[u][m][1] = *(const u32x4 *)(xp[m] + a.plane + gu);
+                }
+#pragma unroll
+                for (int n = 0; n < WN; ++n)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) nv[u][n][i] = np[n][min(g + 16 * u + i, a.groups - 1 - 8 * h)];
             }
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                u32x4 bh, bl;
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float b[2];
+                for (int n = 0; n < WN; ++n) {
+                    u32x4 bh, bl;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int32_t at = 2 * i + e;
-                        const uint32_t w = g + 8 * h + at < a.groups ? np[n][g + at] : 0u;
-                        b[e] = hi_f32<T>(w) - 16.0f * lo_f32<T>(w);
+                    for (int i = 0; i < 4; ++i) {
+                        float b[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int32_t at = g + 16 * u + 8 * h + 2 * i + e;
+                            const uint32_t w = at >= lo && at < hi ? nv[u][n][2 * i + e] : 0u;
+                            b[e] = hi_f32<T>(w) - 16.0f * lo_f32<T>(w);
+                        }
+                        bh[i] = pack2<__bf16>(b[0], b[1]);
+                        bl[i] = pack2<__bf16>(b[0] - lo_f32<__bf16>(bh[i]), b[1] - hi_f32<__bf16>(bh[i]));
                     }
-                    bh[i] = pack2<__bf16>(b[0], b[1]);
-                    bl[i] = pack2<__bf16>(b[0] - lo_f32<__bf16>(bh[i]), b[1] - hi_f32<__bf16>(bh[i]));
-                }
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    acc[m][n] = mfma32<__bf16>(xl[m], bh, acc[m][n]);
-                    acc[m][n] = mfma32<__bf16>(xh[m], bl, acc[m][n]);
-                    acc[m][n] = mfma32<__bf16>(xh[m], bh, acc[m][n]);
+                    for (int m = 0; m < WM; ++m) {
+                        acc[m][n] = mfma32<__bf16>(xv[u][m][1], bh, acc[m][n]);
+                        acc[m][n] = mfma32<__bf16>(xv[u][m][0], bl, acc[m][n]);
+                        acc[m][n] = mfma32<__bf16>(xv[u][m][0], bh, acc[m][n]);
+                    }
                 }
-            }
         }
     }
 
     const W4Const konst = w4_const<T>();
     // What a lane reads of a stage: x piece p of its rows, its columns' pieces, their numbers.
-    const uint32_t x_at = (uint32_t)(64 * wm + r) * 256u, w_at = (uint32_t)L::X + (uint32_t)(64 * wn + r) * 64u;
-    const uint32_t n_at = (uint32_t)(L::X + L::W) + 4u * (uint32_t)(64 * wn + r);
-    const int32_t steps = a.Kp / 128;
+    const uint32_t x_at = (uint32_t)(32 * WM * wm + r) * 256u, w_at = (uint32_t)L::X + (uint32_t)(32 * WN * wn + r) * 64u;
+    const uint32_t n_at = (uint32_t)(L::X + L::W) + 4u * (uint32_t)(32 * WN * wn + r);
     uint32_t at = 0, next = 2 * L::STAGE;
-    for (int32_t st = 0; st < steps; ++st) {
+    for (int32_t st = first; st < last; ++st) {
         wait_vm_barrier<L::COPIES>();
-        copy(st + 2, lds0 + next);
         const char *s0 = smem + at;
-        u32x4 x[8][2];
+        u32x4 x[8][WM];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
+            for (int m = 0; m < WM; ++m) {
                 // instruction j takes 8 weights of piece 2 (j / 4) + h, word j % 4; G = 32: of piece
                 // 2 (j / 4) + j / 2 % 2, word 2 (j % 2) + h
                 const uint32_t p = G == 32 ? (uint32_t)(4 * (2 * (j / 4) + j / 2 % 2) + 2 * (j % 2)) + (uint32_t)h
                                            : (uint32_t)(8 * (j / 4) + j % 4) + 4u * (uint32_t)h;
-                x[j][m] = *(const u32x4 *)(s0 + x_at + 8192u * (uint32_t)m + 16u * (p ^ (uint32_t)(r & 7)));
+                x[j][m] = *(const u32x4 *)(s0 + x_at + 8192u * (uint32_t)m + 16u * (p ^ (uint32_t)(r & 15)));
             }
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+        for (int n = 0; n < WN; ++n) {
             u32x4 w[2];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                w[t] = *(const u32x4 *)(s0 + w_at + 2048u * (uint32_t)n + 16u * ((uint32_t)(2 * t + h) ^ (uint32_t)((r >> 1) & 3)));
+                w[t] = *(const u32x4 *)(s0 + w_at + 2048u * (uint32_t)n + 16u * ((uint32_t)(2 * t + h) ^ (uint32_t)((r >> 2) & 3)));
                 if constexpr (G == 32) {
                     const auto c = __builtin_amdgcn_permlane32_swap(w[t][0], w[t][1], false, false);
                     const auto d = __builtin_amdgcn_permlane32_swap(w[t][2], w[t][3], false, false);
@@ -210,61 +222,198 @@ __global__ __launch_bounds__(512, 2) void w4_rows_kernel(RowsArgs a)
             }
 #pragma unroll
             for (int g = 0; g < PER; ++g) {
-                f32x16 sum[2];
+                f32x16 sum[WM];
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
+                for (int m = 0; m < WM; ++m)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) sum[m][i] = 0.f;
 #pragma unroll
                 for (int j = g * 8 / PER; j < (g + 1) * 8 / PER; ++j) {
                     const u32x4 lv = w4_levels<T>(w[j / 4][j % 4], konst);
 #pragma unroll
-                    for (int m = 0; m < 2; ++m) sum[m] = mfma32<T>(x[j][m], lv, sum[m]);
+                    for (int m = 0; m < WM; ++m) sum[m] = mfma32<T>(x[j][m], lv, sum[m]);
+                    // a copy of the stage after next now and then: all at once they would hold up
+                    // every wave at the start of a stage
+                    if (WN == 1) {
+                        if (j < L::COPIES) copy(j, st + 2, lds0 + next);
+                    } else if (j % 2 == 0 && 4 * n + j / 2 < L::COPIES) {
+                        copy(4 * n + j / 2, st + 2, lds0 + next);
+                    }
                 }
                 const float s = lo_f32<T>(*(const uint32_t *)(s0 + n_at + 128u * (uint32_t)n + 4u * (uint32_t)(L::BN * g)));
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
+                for (int m = 0; m < WM; ++m)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) acc[m][n][i] = __builtin_fmaf(s, sum[m][i], acc[m][n][i]);
             }
         }
+        static_assert(L::COPIES <= 8, "all copies are made");
         at = at == 2 * L::STAGE ? 0 : at + L::STAGE;
         next = next == 2 * L::STAGE ? 0 : next + L::STAGE;
     }
-    wait_vm_all();   // (the last two copies brought nothing)
+    wait_vm_all();   // (the last two stages' copies brought nothing)
 
+    if (a.splits > 1) {
+        float *out = (float *)a.out + (int64_t)part * a.M * a.ldo + (int64_t)m0 * a.ldo + n0;
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-        const int32_t col = 64 * wn + 32 * n + r;
-        if (col >= cols) continue;
-        const float bias = a.bias ? (float)((const T *)a.bias)[n0 + col] : 0.f;
+        for (int n = 0; n < WN; ++n) {
+            const int32_t col = 32 * (WN * wn + n) + r;
+            if (col >= cols) continue;
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+            for (int m = 0; m < WM; ++m)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int32_t row = 64 * wm + 32 * m + 8 * (i / 4) + 4 * h + i % 4;
-                if (row < rows) ((T *)a.out)[(int64_t)(m0 + row) * a.ldo + n0 + col] = (T)(acc[m][n][i] + bias);
-            }
+                for (int i = 0; i < 16; ++i) {
+                    const int32_t row = 32 * (WM * wm + m) + 8 * (i / 4) + 4 * h + i % 4;
+                    if (row < rows) out[row * a.ldo + col] = acc[m][n][i];
+                }
+        }
+        return;
+    }
+    // Out through LDS, so that rows are written in pieces of 16 bytes (directly, 2 bytes a lane, the
+    // stores take 19 us of 410 at 4096 x 11008 x 4096).
+    __syncthreads();
+    T *const tile = (T *)smem;
+#pragma unroll
+    for (int n = 0; n < WN; ++n) {
+        const int32_t col = 32 * (WN * wn + n) + r;
+        const float bias = a.bias && col < cols ? (float)((const T *)a.bias)[n0 + col] : 0.f;
+#pragma unroll
+        for (int m = 0; m < WM; ++m)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                tile[(32 * (WM * wm + m) + 8 * (i / 4) + 4 * h + i % 4) * L::OUT_LD + col] = (T)(acc[m][n][i] + bias);
+    }
+    __syncthreads();
+    T *const out = (T *)a.out + (int64_t)m0 * a.ldo + n0;
+    if (a.ldo % 8 == 0 && cols % 8 == 0) {
+        for (int32_t i = (int32_t)threadIdx.x; i < rows * (L::BN / 8); i += 512) {
+            const int32_t row = i / (L::BN / 8), c = i % (L::BN / 8) * 8;
+            if (c < cols) *(u32x4 *)(out + row * a.ldo + c) = *(const u32x4 *)(tile + row * L::OUT_LD + c);
+        }
+    } else {
+        for (int32_t i = (int32_t)threadIdx.x; i < rows * L::BN; i += 512) {
+            const int32_t row = i / L::BN, c = i % L::BN;
+            if (c < cols) out[row * a.ldo + c] = tile[row * L::OUT_LD + c];
+        }
     }
 }
 
-struct RowsSpace {
-    int64_t Kp, groups16, parts, bytes;
+// Parts of K added up, in their order: four columns to a thread.
+template <class T>
+__global__ __launch_bounds__(256) void w4_join_kernel(const float *__restrict__ parts, const T *__restrict__ bias, T *__restrict__ out,
+                                                      int64_t n, int64_t all, int32_t N, int32_t splits)
+{
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    if (N % 4 == 0) {
+        f32x4 v = *(const f32x4 *)(parts + i);
+        for (int32_t s = 1; s < splits; ++s) v += *(const f32x4 *)(parts + s * all + i);
+        const int32_t c = (int32_t)(i % N);
+        store_scaled<T>(bias, out, i, c, N - c, true, v);
+    } else {
+        for (int64_t e = i; e < i + 4 && e < n; ++e) {
+            float v = parts[e];
+            for (int32_t s = 1; s < splits; ++s) v += parts[s * all + e];
+            if (bias) v += (float)bias[e % N];
+            out[e] = (T)v;
+        }
+    }
+}
+
+// ---- planning --------------------------------------------------------------
+// A band of columns: its tiles and parts of K.
+struct RowsBand {
+    int tile;            // 0: 128 x 256, 1: 128 x 128, 2: 64 x 128
+    int64_t n0, cols, splits;
 };
-static RowsSpace rows_space(int64_t M, int64_t K, int64_t group)
+struct RowsPlan {
+    int bands;
+    RowsBand band[2];
+    double us;
+};
+static const int64_t kBM[3] = {128, 128, 64}, kBN[3] = {256, 128, 128};
+// Time of a band: rounds of workgroups, a stage's time in each tile as measured, and what a
+// workgroup takes besides.
+static double band_us(const RowsBand &b, int64_t M, int64_t stages, int cu)
+{
+    static const double per_stage[3] = {1.95, 1.15, 0.75}, rest[3] = {6, 5, 4.5};
+    const int64_t wgs = ((M + kBM[b.tile] - 1) / kBM[b.tile]) * ((b.cols + kBN[b.tile] - 1) / kBN[b.tile]) * b.splits;
+    const double each = rest[b.tile] + (double)((stages + b.splits - 1) / b.splits) * per_stage[b.tile];
+    double us = 2.0 + (double)((wgs + cu - 1) / cu) * each;
+    if (b.splits > 1) us += 3.0 + (double)(M * b.cols) * (double)(8 * b.splits + 2) / 4.5e6;
+    return us;
+}
+static RowsPlan rows_plan(int64_t M, int64_t N, int64_t K, int cu)
+{
+    const int64_t stages = (K + 127) / 128;
+    RowsPlan best{};
+    auto offer = [&](const RowsPlan &p) {
+        if (best.bands == 0 || p.us < best.us) best = p;
+    };
+    for (int t = 0; t < 3; ++t) {
+        RowsPlan p{1, {{t, 0, N, 1}, {}}, 0};
+        p.us = band_us(p.band[0], M, stages, cu);
+        offer(p);
+        // parts of K where there are too few tiles
+        const int64_t tiles = ((M + kBM[t] - 1) / kBM[t]) * ((N + kBN[t] - 1) / kBN[t]);
+        for (int64_t s = 2; s <= 16 && s * 2 <= stages && tiles * (s - 1) < cu; ++s) {
+            p.band[0].splits = s;
+            p.us = band_us(p.band[0], M, stages, cu);
+            offer(p);
+        }
+    }
+    // whole rounds of the largest tiles, and the columns that are left in smaller ones
+    const int64_t tm = (M + 127) / 128, full = (tm * (N / 256)) / cu * cu / tm * 256;
+    if (full > 0 && full < N)
+        for (int t = 1; t < 3; ++t) {
+            RowsPlan p{2, {{0, 0, full, 1}, {t, full, N - full, 1}}, 0};
+            p.us = band_us(p.band[0], M, stages, cu) + band_us(p.band[1], M, stages, cu);
+            offer(p);
+        }
+    return best;
+}
+
+struct RowsSpace {
+    int64_t Kp, groups16, parts, sums, bytes;
+};
+static RowsSpace rows_space(int64_t M, int64_t N, int64_t K, int64_t group, const RowsPlan &p)
 {
     RowsSpace s;
     s.Kp = (K + 127) / 128 * 128;
     s.groups16 = (K / group + 15) / 16 * 16;
     s.parts = (M * s.Kp * 2 + 255) / 256 * 256;
-    s.bytes = s.parts + (2 * M * s.groups16 * 2 + 255) / 256 * 256;
+    s.sums = s.parts + (2 * M * s.groups16 * 2 + 255) / 256 * 256;
+    s.bytes = s.sums + (p.band[0].splits > 1 ? p.band[0].splits * M * N * 4 : 0);
     return s;
 }
-int64_t linear_w4_rows_workspace(int64_t M, int64_t K, int64_t group) { return rows_space(M, K, group).bytes; }
-
-template <class T, int G> static hipError_t rows_t(const W4Args &a, void *workspace, hipStream_t s)
+int64_t linear_w4_rows_workspace(int64_t M, int64_t N, int64_t K, int64_t group, int cu)
 {
-    const RowsSpace sp = rows_space(a.M, a.K, G);
+    return rows_space(M, N, K, group, rows_plan(M, N, K, cu)).bytes;
+}
+
+template <class T, int G, int WM, int WN> static hipError_t rows_launch(RowsArgs r, hipStream_t s)
+{
+    typedef RowsLds<G, WM, WN> L;
+    const int64_t tn = (r.N + L::BN - 1) / L::BN, M = r.M, most = LAUNCH_THREADS / 512 / tn / r.splits * L::BM;
+    if (most < L::BM || (r.splits > 1 && most < M)) return hipErrorInvalidValue;
+    for (int64_t m = 0; m < M; m += most) {
+        RowsArgs q = r;
+        q.x = (const T *)r.x + m * r.Kp;
+        q.parts = r.parts + m * r.groups16;
+        q.out = (T *)r.out + m * r.ldo;   // (with parts of K, m is 0)
+        q.M = (int32_t)std::min(most, M - m);
+        q.tiles_m = (uint32_t)((q.M + L::BM - 1) / L::BM);
+        q.tiles_n = (uint32_t)tn;
+        hipLaunchKernelGGL((w4_rows_kernel<T, G, WM, WN>), dim3(q.tiles_m * q.tiles_n, (uint32_t)r.splits), dim3(512),
+                           (uint32_t)(L::STAGES * L::STAGE), s, q);
+    }
+    return hipGetLastError();
+}
+
+template <class T, int G> static hipError_t rows_t(const W4Args &a, int cu, void *workspace, hipStream_t s)
+{
+    const RowsPlan plan = rows_plan(a.M, a.N, a.K, cu);
+    const RowsSpace sp = rows_space(a.M, a.N, a.K, G, plan);
     T *x = (T *)workspace;
     __bf16 *parts = (__bf16 *)((char *)workspace + sp.parts);
     // (a thread for every 8 numbers, up to the last padded group's first)
@@ -274,38 +423,48 @@ template <class T, int G> static hipError_t rows_t(const W4Args &a, void *worksp
         hipLaunchKernelGGL((w4_prepare_kernel<T, G>), dim3((uint32_t)wide, (uint32_t)std::min(most, a.M - m)), dim3(256), 0, s,
                            (const T *)a.x + m * a.ldx, a.ldx, x + m * sp.Kp, parts + m * sp.groups16, (int32_t)a.M, (int32_t)a.K,
                            (int32_t)sp.Kp, (int32_t)sp.groups16);
-    typedef RowsLds<G> L;
-    const int64_t tn = (a.N + L::BN - 1) / L::BN, rows = LAUNCH_THREADS / 512 / tn * L::BM;
-    if (rows < L::BM) return hipErrorInvalidValue;
-    for (int64_t m = 0; m < a.M; m += rows) {
+    for (int i = 0; i < plan.bands; ++i) {
+        const RowsBand &b = plan.band[i];
         RowsArgs r;
-        r.x = x + m * sp.Kp;
-        r.parts = parts + m * sp.groups16;
+        r.x = x;
+        r.parts = parts;
         r.plane = a.M * sp.groups16;
-        r.w = a.w;
-        r.p = (const uint32_t *)a.p;
-        r.bias = a.bias;
-        r.out = (T *)a.out + m * a.N;
+        r.w = a.w + b.n0 * (a.K / 2);
+        r.p = (const uint32_t *)a.p + b.n0 * (a.K / G);
+        r.bias = a.bias ? (const T *)a.bias + b.n0 : nullptr;
+        r.out = b.splits > 1 ? (void *)((char *)workspace + sp.sums) : (void *)((T *)a.out + b.n0);
         r.ldo = a.N;
-        r.M = (int32_t)std::min(rows, a.M - m);
-        r.N = (int32_t)a.N;
+        r.M = (int32_t)a.M;
+        r.N = (int32_t)b.cols;
         r.K = (int32_t)a.K;
         r.Kp = (int32_t)sp.Kp;
         r.groups = (int32_t)(a.K / G);
         r.groups16 = (int32_t)sp.groups16;
-        r.tiles_m = (uint32_t)((r.M + L::BM - 1) / L::BM);
-        r.tiles_n = (uint32_t)tn;
-        hipLaunchKernelGGL((w4_rows_kernel<T, G>), dim3(r.tiles_m * r.tiles_n), dim3(512), (uint32_t)(L::STAGES * L::STAGE), s, r);
+        r.splits = (int32_t)b.splits;
+        const hipError_t e = b.tile == 0 ? rows_launch<T, G, 2, 2>(r, s) : b.tile == 1 ? rows_launch<T, G, 2, 1>(r, s) : rows_launch<T, G, 1, 1>(r, s);
+        if (e != hipSuccess) return e;
+        if (b.splits > 1) {
+            const int64_t n = a.M * a.N, each = LAUNCH_THREADS / 256 * 1024;
+            for (int64_t i0 = 0; i0 < n; i0 += each) {   // (one launch: a split product is small)
+                const int64_t here = std::min(each, n - i0);
+                if (i0) return hipErrorInvalidValue;
+                hipLaunchKernelGGL((w4_join_kernel<T>), dim3((uint32_t)((here + 1023) / 1024)), dim3(256), 0, s,
+                                   (const float *)((char *)workspace + sp.sums), (const T *)a.bias, (T *)a.out, here, n, (int32_t)a.N,
+                                   (int32_t)b.splits);
+            }
+        }
     }
     return hipGetLastError();
 }
 
-hipError_t launch_linear_w4_rows(int ftype, int group, const W4Args &a, void *workspace, hipStream_t s)
+hipError_t launch_linear_w4_rows(int ftype, int group, const W4Args &a, int cu, void *workspace, hipStream_t s)
 {
     if (ftype == LB_BF16)
-        return group == 32 ? rows_t<__bf16, 32>(a, workspace, s) : group == 64 ? rows_t<__bf16, 64>(a, workspace, s) : rows_t<__bf16, 128>(a, workspace, s);
+        return group == 32 ? rows_t<__bf16, 32>(a, cu, workspace, s) : group == 64 ? rows_t<__bf16, 64>(a, cu, workspace, s)
+                                                                                  : rows_t<__bf16, 128>(a, cu, workspace, s);
     if (ftype == LB_F16)
-        return group == 32 ? rows_t<_Float16, 32>(a, workspace, s) : group == 64 ? rows_t<_Float16, 64>(a, workspace, s) : rows_t<_Float16, 128>(a, workspace, s);
+        return group == 32 ? rows_t<_Float16, 32>(a, cu, workspace, s) : group == 64 ? rows_t<_Float16, 64>(a, cu, workspace, s)
+                                                                                    : rows_t<_Float16, 128>(a, cu, workspace, s);
     return hipErrorInvalidValue;
 }
 
