@@ -75,6 +75,7 @@ template <int G, int WM, int WN> struct RowsLds {
         XC = 2 * WM, WC = WN,                                  // a wave's copies of a stage: x, weights,
         NC = WORDS > 512 ? WORDS / 512 : 1,                    // numbers
         NUMBERS = NC * 2048, STAGE = X + W + NUMBERS, COPIES = XC + WC + NC,
+        UNITS = WN * 128 / G,                                  // (32 columns, group) of a stage
         OUT_LD = BN + 8                                        // the tile on its way out, 16-bit
     };
     static_assert(BM * OUT_LD * 2 <= STAGES * STAGE, "the tile over the ring");
@@ -194,10 +195,30 @@ __global__ __launch_bounds__(512, 2) void w4_rows_kernel(RowsArgs a)
     const uint32_t x_at = (uint32_t)(32 * WM * wm + r) * 256u, w_at = (uint32_t)L::X + (uint32_t)(32 * WN * wn + r) * 64u;
     const uint32_t n_at = (uint32_t)(L::X + L::W) + 4u * (uint32_t)(32 * WN * wn + r);
     uint32_t at = 0, next = 2 * L::STAGE;
+    constexpr bool PIPE = L::UNITS % 2 == 0;
+    f32x16 sum[2][WM];
+    float pending = 0.f;
+#pragma unroll
+    for (int m = 0; m < WM; ++m)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum[1][m][i] = 0.f;
     for (int32_t st = first; st < last; ++st) {
         wait_vm_barrier<L::COPIES>();
         const char *s0 = smem + at;
-        u32x4 x[8][WM];
+        // the columns' pieces and numbers first, then the rows in the order of their use: the first
+        // matrix instructions need not wait for the last reads
+        u32x4 wv[WN][2], x[8][WM];
+        float scale[WN][PER];
+#pragma unroll
+        for (int n = 0; n < WN; ++n)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                wv[n][t] = *(const u32x4 *)(s0 + w_at + 2048u * (uint32_t)n + 16u * ((uint32_t)(2 * t + h) ^ (uint32_t)((r >> 2) & 3)));
+#pragma unroll
+        for (int n = 0; n < WN; ++n)
+#pragma unroll
+            for (int g = 0; g < PER; ++g)
+                scale[n][g] = lo_f32<T>(*(const uint32_t *)(s0 + n_at + 128u * (uint32_t)n + 4u * (uint32_t)(L::BN * g)));
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -213,7 +234,7 @@ __global__ __launch_bounds__(512, 2) void w4_rows_kernel(RowsArgs a)
             u32x4 w[2];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                w[t] = *(const u32x4 *)(s0 + w_at + 2048u * (uint32_t)n + 16u * ((uint32_t)(2 * t + h) ^ (uint32_t)((r >> 2) & 3)));
+                w[t] = wv[n][t];
                 if constexpr (G == 32) {
                     const auto c = __builtin_amdgcn_permlane32_swap(w[t][0], w[t][1], false, false);
                     const auto d = __builtin_amdgcn_permlane32_swap(w[t][2], w[t][3], false, false);
@@ -222,16 +243,26 @@ __global__ __launch_bounds__(512, 2) void w4_rows_kernel(RowsArgs a)
             }
 #pragma unroll
             for (int g = 0; g < PER; ++g) {
-                f32x16 sum[WM];
+                constexpr int STEPS = 8 / PER;
+                // PIPE: the sums of the unit (columns, group) before are scaled step by step beside this
+                // one's matrix instructions, the last unit's in the next stage
+                const int now = PIPE ? (n * PER + g) % 2 : 0, was = 1 - now;
+                const int wn_ = (n * PER + g + L::UNITS - 1) % L::UNITS / PER;   // whose columns they are
 #pragma unroll
                 for (int m = 0; m < WM; ++m)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) sum[m][i] = 0.f;
+                    for (int i = 0; i < 16; ++i) sum[now][m][i] = 0.f;
 #pragma unroll
-                for (int j = g * 8 / PER; j < (g + 1) * 8 / PER; ++j) {
+                for (int j = g * STEPS; j < (g + 1) * STEPS; ++j) {
                     const u32x4 lv = w4_levels<T>(w[j / 4][j % 4], konst);
 #pragma unroll
-                    for (int m = 0; m < WM; ++m) sum[m] = mfma32<T>(x[j][m], lv, sum[m]);
+                    for (int m = 0; m < WM; ++m) {
+                        sum[now][m] = mfma32<T>(x[j][m], lv, sum[now][m]);
+                        if constexpr (PIPE)
+#pragma unroll
+                            for (int i = 16 / STEPS * (j % STEPS); i < 16 / STEPS * (j % STEPS + 1); ++i)
+                                acc[m][wn_][i] = __builtin_fmaf(pending, sum[was][m][i], acc[m][wn_][i]);
+                    }
                     // a copy of the stage after next now and then: all at once they would hold up
                     // every wave at the start of a stage
                     if (WN == 1) {
@@ -240,11 +271,14 @@ __global__ __launch_bounds__(512, 2) void w4_rows_kernel(RowsArgs a)
                         copy(4 * n + j / 2, st + 2, lds0 + next);
                     }
                 }
-                const float s = lo_f32<T>(*(const uint32_t *)(s0 + n_at + 128u * (uint32_t)n + 4u * (uint32_t)(L::BN * g)));
+                if constexpr (PIPE) {
+                    pending = scale[n][g];
+                } else {
 #pragma unroll
-                for (int m = 0; m < WM; ++m)
+                    for (int m = 0; m < WM; ++m)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[m][n][i] = __builtin_fmaf(s, sum[m][i], acc[m][n][i]);
+                        for (int i = 0; i < 16; ++i) acc[m][n][i] = __builtin_fmaf(scale[n][g], sum[now][m][i], acc[m][n][i]);
+                }
             }
         }
         static_assert(L::COPIES <= 8, "all copies are made");
@@ -252,6 +286,11 @@ __global__ __launch_bounds__(512, 2) void w4_rows_kernel(RowsArgs a)
         next = next == 2 * L::STAGE ? 0 : next + L::STAGE;
     }
     wait_vm_all();   // (the last two stages' copies brought nothing)
+    if constexpr (PIPE)
+#pragma unroll
+        for (int m = 0; m < WM; ++m)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[m][WN - 1][i] = __builtin_fmaf(pending, sum[1][m][i], acc[m][WN - 1][i]);
 
     if (a.splits > 1) {
         float *out = (float *)a.out + (int64_t)part * a.M * a.ldo + (int64_t)m0 * a.ldo + n0;
