@@ -68,6 +68,9 @@ struct RowsArgs {
     uint32_t tiles_m, tiles_n;
 };
 
+// Numbers from one part of K's sums to the next one's.
+__host__ __device__ inline int64_t rows_apart(int64_t M, int64_t N) { return (M * N + 3) / 4 * 4; }
+
 template <int G, int WM, int WN> struct RowsLds {
     enum : int {
         BM = 64 * WM, BN = 128 * WN, STAGES = 3,
@@ -244,6 +247,7 @@ __global__ __launch_bounds__(512, 2) void w4_rows_kernel(RowsArgs a)
 #pragma unroll
             for (int g = 0; g < PER; ++g) {
                 constexpr int STEPS = 8 / PER;
+                constexpr int CHAINS = WM == 1 && STEPS > 2 ? 2 : 1;   // one tile of rows: sums in two, or each instruction waits for the last
                 // PIPE: the sums of the unit (columns, group) before are scaled step by step beside this
                 // one's matrix instructions, the last unit's in the next stage
                 const int now = PIPE ? (n * PER + g) % 2 : 0, was = 1 - now;
@@ -252,12 +256,16 @@ __global__ __launch_bounds__(512, 2) void w4_rows_kernel(RowsArgs a)
                 for (int m = 0; m < WM; ++m)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) sum[now][m][i] = 0.f;
+                f32x16 other;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) other[i] = 0.f;
 #pragma unroll
                 for (int j = g * STEPS; j < (g + 1) * STEPS; ++j) {
                     const u32x4 lv = w4_levels<T>(w[j / 4][j % 4], konst);
 #pragma unroll
                     for (int m = 0; m < WM; ++m) {
-                        sum[now][m] = mfma32<T>(x[j][m], lv, sum[now][m]);
+                        if (CHAINS == 2 && j % 2) other = mfma32<T>(x[j][m], lv, other);
+                        else sum[now][m] = mfma32<T>(x[j][m], lv, sum[now][m]);
                         if constexpr (PIPE)
 #pragma unroll
                             for (int i = 16 / STEPS * (j % STEPS); i < 16 / STEPS * (j % STEPS + 1); ++i)
@@ -271,6 +279,9 @@ __global__ __launch_bounds__(512, 2) void w4_rows_kernel(RowsArgs a)
                         copy(4 * n + j / 2, st + 2, lds0 + next);
                     }
                 }
+                if constexpr (CHAINS == 2)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) sum[now][0][i] += other[i];
                 if constexpr (PIPE) {
                     pending = scale[n][g];
                 } else {
@@ -293,7 +304,7 @@ __global__ __launch_bounds__(512, 2) void w4_rows_kernel(RowsArgs a)
             for (int i = 0; i < 16; ++i) acc[m][WN - 1][i] = __builtin_fmaf(pending, sum[1][m][i], acc[m][WN - 1][i]);
 
     if (a.splits > 1) {
-        float *out = (float *)a.out + (int64_t)part * a.M * a.ldo + (int64_t)m0 * a.ldo + n0;
+        float *out = (float *)a.out + (int64_t)part * rows_apart(a.M, a.ldo) + (int64_t)m0 * a.ldo + n0;
 #pragma unroll
         for (int n = 0; n < WN; ++n) {
             const int32_t col = 32 * (WN * wn + n) + r;
@@ -337,26 +348,36 @@ __global__ __launch_bounds__(512, 2) void w4_rows_kernel(RowsArgs a)
     }
 }
 
-// Parts of K added up, in their order: four columns to a thread.
+// Parts of K added up, in their order: four numbers to a thread, whatever their columns (parts
+// are a multiple of four numbers apart).
 template <class T>
 __global__ __launch_bounds__(256) void w4_join_kernel(const float *__restrict__ parts, const T *__restrict__ bias, T *__restrict__ out,
-                                                      int64_t n, int64_t all, int32_t N, int32_t splits)
+                                                      int64_t n, int64_t apart, int32_t N, int32_t splits)
 {
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (i >= n) return;
-    if (N % 4 == 0) {
-        f32x4 v = *(const f32x4 *)(parts + i);
-        for (int32_t s = 1; s < splits; ++s) v += *(const f32x4 *)(parts + s * all + i);
-        const int32_t c = (int32_t)(i % N);
-        store_scaled<T>(bias, out, i, c, N - c, true, v);
-    } else {
-        for (int64_t e = i; e < i + 4 && e < n; ++e) {
-            float v = parts[e];
-            for (int32_t s = 1; s < splits; ++s) v += parts[s * all + e];
-            if (bias) v += (float)bias[e % N];
-            out[e] = (T)v;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    for (int32_t s0 = 0; s0 < splits; s0 += 4) {
+        f32x4 p[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) p[u] = *(const f32x4 *)(parts + min(s0 + u, splits - 1) * apart + i);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (s0 + u < splits)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] += p[u][e];
+    }
+    if (bias) {
+        int32_t c = (int32_t)(i % N);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[e] += (float)bias[c];
+            c = c + 1 == N ? 0 : c + 1;
         }
     }
+    if (i + 4 <= n) *(u32x2 *)(out + i) = u32x2{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3])};
+    else
+        for (int e = 0; i + e < n; ++e) out[i + e] = (T)v[e];
 }
 
 // ---- planning --------------------------------------------------------------
@@ -371,15 +392,17 @@ struct RowsPlan {
     double us;
 };
 static const int64_t kBM[3] = {128, 128, 64}, kBN[3] = {256, 128, 128};
-// Time of a band: rounds of workgroups, a stage's time in each tile as measured, and what a
-// workgroup takes besides.
+// Time of a band, us: rounds of workgroups of a stage's time in each tile, as measured, and what a
+// workgroup takes besides.  (Two workgroups of the smallest tile share a compute unit, which
+// gains them about a tenth.)
 static double band_us(const RowsBand &b, int64_t M, int64_t stages, int cu)
 {
-    static const double per_stage[3] = {1.95, 1.15, 0.75}, rest[3] = {6, 5, 4.5};
+    static const double per_stage[3] = {1.75, 1.05, 0.75}, rest[3] = {9, 7.5, 6.5};
     const int64_t wgs = ((M + kBM[b.tile] - 1) / kBM[b.tile]) * ((b.cols + kBN[b.tile] - 1) / kBN[b.tile]) * b.splits;
     const double each = rest[b.tile] + (double)((stages + b.splits - 1) / b.splits) * per_stage[b.tile];
-    double us = 2.0 + (double)((wgs + cu - 1) / cu) * each;
-    if (b.splits > 1) us += 3.0 + (double)(M * b.cols) * (double)(8 * b.splits + 2) / 4.5e6;
+    const double rounds = b.tile < 2 || wgs <= cu ? (double)((wgs + cu - 1) / cu) : 0.9 * (double)((2 * wgs + cu - 1) / cu) / 2;
+    double us = 2.5 + rounds * each;
+    if (b.splits > 1) us += 3.5 + (double)(M * b.cols) * (double)(4 * b.splits) / 4.5e6;
     return us;
 }
 static RowsPlan rows_plan(int64_t M, int64_t N, int64_t K, int cu)
@@ -422,7 +445,7 @@ static RowsSpace rows_space(int64_t M, int64_t N, int64_t K, int64_t group, cons
     s.groups16 = (K / group + 15) / 16 * 16;
     s.parts = (M * s.Kp * 2 + 255) / 256 * 256;
     s.sums = s.parts + (2 * M * s.groups16 * 2 + 255) / 256 * 256;
-    s.bytes = s.sums + (p.band[0].splits > 1 ? p.band[0].splits * M * N * 4 : 0);
+    s.bytes = s.sums + (p.band[0].splits > 1 ? p.band[0].splits * rows_apart(M, N) * 4 : 0);
     return s;
 }
 int64_t linear_w4_rows_workspace(int64_t M, int64_t N, int64_t K, int64_t group, int cu)
@@ -488,8 +511,8 @@ template <class T, int G> static hipError_t rows_t(const W4Args &a, int cu, void
                 const int64_t here = std::min(each, n - i0);
                 if (i0) return hipErrorInvalidValue;
                 hipLaunchKernelGGL((w4_join_kernel<T>), dim3((uint32_t)((here + 1023) / 1024)), dim3(256), 0, s,
-                                   (const float *)((char *)workspace + sp.sums), (const T *)a.bias, (T *)a.out, here, n, (int32_t)a.N,
-                                   (int32_t)b.splits);
+                                   (const float *)((char *)workspace + sp.sums), (const T *)a.bias, (T *)a.out, here, rows_apart(a.M, a.N),
+                                   (int32_t)a.N, (int32_t)b.splits);
             }
         }
     }
