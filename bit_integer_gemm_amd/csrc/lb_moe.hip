@@ -251,11 +251,10 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGri
             const int32_t m = i / (have * 16), c = i - m * have * 16, b = c / 16;
             const float *s = slots + (b / each * kw * 2 * each + b % each * 2) * slot + m * W4_SLOT_LD + c % 16;
             float v = 0.f, u = 0.f;
-            for (int32_t k = 0; k < kw; ++k)
-                if (k * lines / kw < (k + 1) * lines / kw) {
-                    v += s[k * 2 * each * slot];
-                    u += s[(k * 2 * each + 1) * slot];
-                }
+            for (int32_t k = 0; k < kw; ++k) {
+                v += s[k * 2 * each * slot];
+                u += s[(k * 2 * each + 1) * slot];
+            }
             put(at + m, c, v, u);
         }
     }
@@ -310,8 +309,7 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_kernel(MoeArgs a, MoeG
             const int32_t m = i / (have * 16), c = i - m * have * 16, t = c / 16;
             const float *s = slots + (t / each * kw * each + t % each) * slot + m * W4_SLOT_LD + c % 16;
             float v = 0.f;
-            for (int32_t k = 0; k < kw; ++k)
-                if (k * lines / kw < (k + 1) * lines / kw) v += s[k * each * slot];
+            for (int32_t k = 0; k < kw; ++k) v += s[k * each * slot];
             a.y[(int64_t)list.row[at + m] * a.H + t0 * 16 + c] = v;
         }
     }

@@ -7,6 +7,7 @@
 namespace lb {
 
 // Few rows: a workgroup takes 16 MT rows of x against some tiles of 16 columns (W4Split).
+// EARLY: weights are asked for before x (a row or two of x are there before the first weights).
 struct FewArgs {
     const uint8_t *w;
     const uint32_t *p;
@@ -15,7 +16,7 @@ struct FewArgs {
     W4Split sp;
     uint32_t tiles_m, tiles_n;   // workgroups
 };
-template <class T, int MT, int G>
+template <class T, int MT, int G, bool EARLY>
 __global__ __launch_bounds__(64 * W4_WAVES) void w4_few_kernel(const T *__restrict__ X, const T *__restrict__ bias,
                                                                   T *__restrict__ out, FewArgs a)
 {
@@ -28,22 +29,22 @@ __global__ __launch_bounds__(64 * W4_WAVES) void w4_few_kernel(const T *__restri
     const int32_t per = W4_WAVES / kw * each, t0 = (int32_t)tn * per;   // the workgroup's tiles
     const int32_t have = min(per, (a.N + 15) / 16 - t0), mine = wave / kw * each;
     float *const slots = (float *)(smem + W4Lds<G>::x_bytes(rows, a.sp.chunk) + W4Lds<G>::RINGS);
-    const int32_t slot = rows * W4_SLOT_LD, lines = (a.K + 255) / 256;
+    const int32_t slot = rows * W4_SLOT_LD;
     auto tile_at = [&](int32_t t) { return W4Tile{(int64_t)(t0 + mine + t) * 16, min(16, a.N - (t0 + mine + t) * 16)}; };
     W4Flow<T, T, MT, G, 1, decltype(tile_at)> flow(smem, W4Lds<G>::x_bytes(rows, a.sp.chunk), a.w, a.p, a.K, a.sp,
                                                    max(0, min(each, have - mine)), tile_at);
-    flow.run(rows, make_rsrc(X + (int64_t)m0 * a.ldx, 0xFFFFFFF0u), false,
+    if constexpr (EARLY) flow.start();
+    flow.run(rows, make_rsrc(X + (int64_t)m0 * a.ldx, 0xFFFFFFF0u), EARLY,
              [&](int32_t row) { return (uint32_t)row * (uint32_t)a.ldx * 2u; },
              [&](int32_t t, const f32x4(&acc)[MT], bool more) { w4_put<MT>(slots + (wave * each + t) * slot, rows, acc, more); });
     __syncthreads();
     for (int32_t i = (int32_t)threadIdx.x; i < rows * have * 16; i += 64 * W4_WAVES) {
         const int32_t m = i / (have * 16), c = i - m * have * 16, t = c / 16, n = t0 * 16 + c;
         if (n >= a.N) continue;
-        // tile t: the waves of group t / each, in order; a wave without lines left nothing
+        // tile t: the waves of group t / each, in order
         const float *s = slots + (t / each * kw * each + t % each) * slot + m * W4_SLOT_LD + c % 16;
         float v = 0.f;
-        for (int32_t k = 0; k < kw; ++k)
-            if (k * lines / kw < (k + 1) * lines / kw) v += s[k * each * slot];
+        for (int32_t k = 0; k < kw; ++k) v += s[k * each * slot];
         if (bias) v += (float)bias[n];
         out[(int64_t)(m0 + m) * a.N + n] = (T)v;
     }
@@ -65,8 +66,11 @@ template <class T, int MT, int G> static hipError_t w4_few_t(const W4Args &a, in
     for (int64_t m = 0; m < a.M; m += most) {
         const int64_t here = a.M - m < most ? a.M - m : most, tm = (here + 16 * MT - 1) / (16 * MT);
         const FewArgs f{a.w, (const uint32_t *)a.p, a.ldx, (int32_t)here, (int32_t)a.N, (int32_t)a.K, sp, (uint32_t)tm, (uint32_t)tn};
-        hipLaunchKernelGGL((w4_few_kernel<T, MT, G>), dim3((uint32_t)(tm * tn)), dim3(64 * W4_WAVES), lds, s,
-                           (const T *)a.x + m * a.ldx, (const T *)a.bias, (T *)a.out + m * a.N, f);
+        const dim3 grid((uint32_t)(tm * tn)), block(64 * W4_WAVES);
+        const T *x = (const T *)a.x + m * a.ldx;
+        T *out = (T *)a.out + m * a.N;
+        if (rows > 2) hipLaunchKernelGGL((w4_few_kernel<T, MT, G, true>), grid, block, lds, s, x, (const T *)a.bias, out, f);
+        else hipLaunchKernelGGL((w4_few_kernel<T, MT, G, false>), grid, block, lds, s, x, (const T *)a.bias, out, f);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }

@@ -131,7 +131,7 @@ template <int N> __device__ inline void w4_wait() { asm volatile("s_waitcnt vmcn
 template <class T, class PT, int MT, int G, int PLANES, class TileAt>
 struct W4Flow {
     typedef W4Lds<G> L;
-    enum : int { GROUPS = L::GROUPS, HALF = GROUPS / 2, STEPS = G / 32 };
+    enum : int { GROUPS = L::GROUPS, STEPS = G / 32 };
     char *const lds;
     const uint8_t *const W;
     const uint32_t *const P;
@@ -168,14 +168,16 @@ struct W4Flow {
         rw = make_rsrc(W + t.row * kb, (uint64_t)(uint32_t)t.rows * kb);
         rp = make_rsrc(P + t.row * groups, (uint64_t)(uint32_t)t.rows * groups * 4u);
     }
-    // The next line into the ring: lane l of a copy takes piece (l % 8) ^ (l / 8) of row l / 8, which
-    // keeps reads of eight rows off each other's banks.  Past the last one nothing is read.
+    // The next line into the ring: piece p of row i lies at p ^ i / 2 (the rows' pieces that 16 lanes
+    // read together then lie on all 64 banks).  Past the last line nothing is read.
     __device__ inline void copy()
     {
         const uint32_t at = (uint32_t)c_line * 128u;
-        const bool in = left && at + piece < kb;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) dma16(rw, in ? row_at + (uint32_t)(8 * i) * kb + at : 0xFFFFFFF0u, c_at + 1024u * (uint32_t)i);
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t p = at + (piece ^ (uint32_t)(64 * i));
+            dma16(rw, left && p < kb ? row_at + (uint32_t)(8 * i) * kb + p : 0xFFFFFFF0u, c_at + 1024u * (uint32_t)i);
+        }
 #pragma unroll
         for (int i = 0; i < L::COPIES - 2; ++i) {
             const int32_t q = lane >> 4, r = lane & 15;
@@ -213,34 +215,43 @@ struct W4Flow {
         else rw = rp = make_rsrc(W, 0);
         c_at = lds_addr(ring);
         c_slot = 0;
-        piece = 16u * (uint32_t)((lane & 7) ^ (lane >> 3));
-        row_at = (uint32_t)(lane >> 3) * kb + piece;
+        piece = 16u * (uint32_t)((lane & 7) ^ (lane >> 4));
+        row_at = (uint32_t)(lane >> 3) * kb;
 #pragma unroll
         for (int d = 0; d < L::DEPTH - 1; ++d) copy();
     }
 
-    // x of the chunk from line c on: piece p of row i lies at p ^ i % 8 of the row.
+    // x of the chunk from line c on: piece p of row i lies at p ^ i % 16 of the row.
     template <class XAt> __device__ inline void ask_x(int32_t c, int32_t xrows, const i32x4 rx, XAt &&x_at)
     {
         const int32_t per = min(sp.chunk, lines - c) * 32, all = per * xrows;
+        int32_t row = (wave * 64 + lane) / per, at = wave * 64 + lane - row * per;
         for (int32_t i0 = wave * 64; i0 < all; i0 += 64 * W4_WAVES) {
-            const int32_t i = min(i0 + lane, all - 1), row = i / per, p = (i - row * per) ^ (row & 7);
-            const int32_t k = c * 256 + 8 * p;
-            dma16(rx, i0 + lane < all && k < K ? x_at(row) + 2u * (uint32_t)k : 0xFFFFFFF0u, lds_addr(lds) + 16u * (uint32_t)i0);
+            const int32_t k = c * 256 + 8 * (at ^ (row & 15));
+            dma16(rx, i0 + lane < all && k < K ? x_at(min(row, xrows - 1)) + 2u * (uint32_t)k : 0xFFFFFFF0u,
+                  lds_addr(lds) + 16u * (uint32_t)i0);
+            for (at += 64 * W4_WAVES; at >= per; at -= per) ++row;
         }
     }
     __device__ inline void order_x(int32_t c, int32_t xrows)   // each lane what it copied itself
     {
+        constexpr int AT_ONCE = 4;
         const int32_t all = min(sp.chunk, lines - c) * 32 * xrows;
-        for (int32_t i = (int32_t)threadIdx.x; i < all; i += 64 * W4_WAVES) {
-            u32x4 *p = (u32x4 *)(lds + 16 * i);
-            *p = w4_order(*p);
+        u32x4 *const p = (u32x4 *)lds;
+        for (int32_t i = (int32_t)threadIdx.x; i < all; i += 64 * W4_WAVES * AT_ONCE) {
+            u32x4 v[AT_ONCE];
+#pragma unroll
+            for (int u = 0; u < AT_ONCE; ++u) v[u] = p[min(i + 64 * W4_WAVES * u, all - 1)];
+#pragma unroll
+            for (int u = 0; u < AT_ONCE; ++u)
+                if (i + 64 * W4_WAVES * u < all) p[i + 64 * W4_WAVES * u] = w4_order(v[u]);
         }
         __syncthreads();
     }
 
     // `rows` rows of x through rx, row i's first byte at x_at(i) (PLANES 2: rows from `rows` on are
-    // the second plane's).  started: start() has been called.
+    // the second plane's).  started: start() has been called, and the weights' latency runs beside the
+    // copy of x; else start() comes after it, and beside the putting in order.
     //   done(t, acc, more): sums of tile t over this wave's lines of a chunk, more: not the first
     //     chunk's; acc[m][i] is row 4 (lane / 16) + i of 16 rows m, column lane % 16.
     template <class XAt, class Done> __device__ inline void run(int32_t rows, const i32x4 rx, bool started, XAt &&x_at, Done &&done)
@@ -272,57 +283,62 @@ struct W4Flow {
             const uint32_t bytes = (uint32_t)min(sp.chunk, lines - c) * 512u;
             int32_t lo, hi;
             bounds(c, lo, hi);
-            if (lo == hi) continue;
-            for (int32_t tile = 0; tile < tiles; ++tile) {
+            if (lo == hi && c) continue;
+            for (int32_t tile = 0; tile < tiles; ++tile) {   // (without lines: sums of zero)
                 f32x4 acc[MT];
 #pragma unroll
                 for (int m = 0; m < MT; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
                 for (int32_t line = lo; line < hi; ++line) {
                     copy();
                     w4_wait<(L::DEPTH - 1) * L::COPIES>();
+                    // everything that the line needs from LDS at once: one latency
                     const char *st = ring + at;
+                    u32x4 w[2], x[8][MT][PLANES];
+                    uint32_t num[GROUPS];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {   // 128 weights
-                        u32x4 w = *(const u32x4 *)(st + 128 * r + 16 * ((4 * h + q) ^ (r & 7)));
-                        if constexpr (G != 128) w4_transpose(w);
-                        u32x4 x[4][MT][PLANES];
+                    for (int h = 0; h < 2; ++h) w[h] = *(const u32x4 *)(st + 128 * r + 16 * ((4 * h + q) ^ (r >> 1)));
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
+                    for (int g = 0; g < GROUPS; ++g) num[g] = *(const uint32_t *)(st + 2048 + 64 * g + 4 * r);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+#pragma unroll
+                        for (int m = 0; m < MT; ++m)
+#pragma unroll
+                            for (int pl = 0; pl < PLANES; ++pl) {
+                                const int32_t p = 16 * (j / 4) + (G == 128 ? 4 * q + j % 4 : 4 * (j % 4) + q);
+                                x[j][m][pl] = *(const u32x4 *)(lds + xrow[m][pl] * bytes + (uint32_t)(line - c) * 512u +
+                                                               16u * ((uint32_t)p ^ (xrow[m][pl] & 15u)));
+                            }
+                    __builtin_amdgcn_sched_barrier(0);
+                    if constexpr (G != 128) {
+                        w4_transpose(w[0]);
+                        w4_transpose(w[1]);
+                    }
+#pragma unroll
+                    for (int g = 0; g < GROUPS; ++g) {
+                        f32x4 sum[MT], xs[MT];
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) sum[m] = xs[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int j = g * STEPS; j < (g + 1) * STEPS; ++j) {   // 32 weights
+                            const u32x4 lv = w4_levels<T>(w[j / 4][j % 4], konst);
+                            const uint32_t one = one_pair<T>();
 #pragma unroll
                             for (int m = 0; m < MT; ++m)
 #pragma unroll
                                 for (int pl = 0; pl < PLANES; ++pl) {
-                                    const int32_t p = 16 * h + (G == 128 ? 4 * q + j : 4 * j + q);
-                                    x[j][m][pl] = *(const u32x4 *)(lds + xrow[m][pl] * bytes + (uint32_t)(line - c) * 512u +
-                                                                   16u * ((uint32_t)p ^ (xrow[m][pl] & 7u)));
-                                }
-#pragma unroll
-                        for (int g = 0; g < HALF; ++g) {
-                            f32x4 sum[MT], xs[MT];
-#pragma unroll
-                            for (int m = 0; m < MT; ++m) sum[m] = xs[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                            for (int j = g * STEPS; j < (g + 1) * STEPS; ++j) {
-                                const u32x4 lv = w4_levels<T>(w[j], konst);
-                                const uint32_t one = one_pair<T>();
-#pragma unroll
-                                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                                    for (int pl = 0; pl < PLANES; ++pl) {
-                                        xs[m] = mfma16<T>(x[j][m][pl], u32x4{one, one, one, one}, xs[m]);
-                                        sum[m] = mfma16<T>(x[j][m][pl], lv, sum[m]);
-                                    }
-                            }
-                            const uint32_t n = *(const uint32_t *)(st + 2048 + 64 * (h * HALF + g) + 4 * r);
-                            const float s = lo_f32<PT>(n), b = hi_f32<PT>(n) - 16.0f * s;
-#pragma unroll
-                            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    acc[m][i] = __builtin_fmaf(s, sum[m][i], acc[m][i]);
-                                    acc[m][i] = __builtin_fmaf(b, xs[m][i], acc[m][i]);
+                                    xs[m] = mfma16<T>(x[j][m][pl], u32x4{one, one, one, one}, xs[m]);
+                                    sum[m] = mfma16<T>(x[j][m][pl], lv, sum[m]);
                                 }
                         }
+                        const float s = lo_f32<PT>(num[g]), b = hi_f32<PT>(num[g]) - 16.0f * s;
+#pragma unroll
+                        for (int m = 0; m < MT; ++m)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                acc[m][i] = __builtin_fmaf(s, sum[m][i], acc[m][i]);
+                                acc[m][i] = __builtin_fmaf(b, xs[m][i], acc[m][i]);
+                            }
                     }
                     // the next copies overwrite what has been read here
                     asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
