@@ -116,8 +116,31 @@ template <int G> struct W4Lds {
         RINGS = W4_WAVES * RING
     };
     // (a copy fills 1 KiB)
-    static __host__ __device__ inline uint32_t x_bytes(int32_t rows, int32_t chunk) { return (uint32_t)(rows * chunk + 1) / 2u * 1024u; }
+    static __host__ __device__ inline uint32_t x_bytes(int32_t xrows, int32_t chunk) { return (uint32_t)(xrows * chunk + 1) / 2u * 1024u; }
 };
+
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// dma16 and dma4 with a second offset that is the same for all lanes.
+__device__ inline void w4_copy16(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %3\n\t"
+                 "s_nop 0\n\t"
+                 "buffer_load_dwordx4 %0, %1, %2 offen lds"
+                 :
+                 : "v"(voff), "s"(rsrc), "s"(soff), "s"(lds)
+                 : "memory", "m0");
+}
+__device__ inline void w4_copy4(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %3\n\t"
+                 "s_nop 0\n\t"
+                 "buffer_load_dword %0, %1, %2 offen lds"
+                 :
+                 : "v"(voff), "s"(rsrc), "s"(soff), "s"(lds)
+                 : "memory", "m0");
+}
+#pragma clang diagnostic pop
 
 template <int N> __device__ inline void w4_wait() { asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory"); }
 
@@ -145,7 +168,8 @@ struct W4Flow {
     int32_t c_chunk, c_tile, c_line, c_lo, c_hi;
     bool left;
     i32x4 rw, rp;
-    uint32_t c_at, c_slot, row_at, piece;
+    uint32_t c_at, c_slot;
+    uint32_t w_at[2], p_at[L::COPIES - 2];   // of a lane in a line of 16 rows of weights, of their numbers
 
     __device__ inline W4Flow(char *lds_, uint32_t x_bytes, const uint8_t *W_, const uint32_t *P_, int32_t K_, const W4Split &sp_,
                              int32_t tiles_, const TileAt &at_)
@@ -169,21 +193,18 @@ struct W4Flow {
         rp = make_rsrc(P + t.row * groups, (uint64_t)(uint32_t)t.rows * groups * 4u);
     }
     // The next line into the ring: piece p of row i lies at p ^ i / 2 (the rows' pieces that 16 lanes
-    // read together then lie on all 64 banks).  Past the last line nothing is read.
+    // read together then lie on all 64 banks).  Past the last line nothing is read.  (Past the end of
+    // a row the next one's weights are, which meet zeros of x; its groups' numbers are not taken.)
     __device__ inline void copy()
     {
-        const uint32_t at = (uint32_t)c_line * 128u;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t p = at + (piece ^ (uint32_t)(64 * i));
-            dma16(rw, left && p < kb ? row_at + (uint32_t)(8 * i) * kb + p : 0xFFFFFFF0u, c_at + 1024u * (uint32_t)i);
-        }
+        for (int i = 0; i < 2; ++i) w4_copy16(rw, w_at[i], (uint32_t)c_line * 128u, c_at + 1024u * (uint32_t)i);
+        const int32_t have = (int32_t)groups - c_line * GROUPS;
 #pragma unroll
         for (int i = 0; i < L::COPIES - 2; ++i) {
-            const int32_t q = lane >> 4, r = lane & 15;
-            const uint32_t g = (uint32_t)(c_line * GROUPS + 4 * i + q);
-            const bool there = left && (GROUPS >= 4 || q < GROUPS) && g < groups;
-            dma4(rp, there ? ((uint32_t)r * groups + g) * 4u : 0xFFFFFFF0u, c_at + 2048u + 256u * (uint32_t)i);
+            uint32_t at = p_at[i];
+            if (have < GROUPS && 4 * i + (lane >> 4) >= have) at = 0xFFFFFFF0u;
+            w4_copy4(rp, at, (uint32_t)(c_line * GROUPS) * 4u, c_at + 2048u + 256u * (uint32_t)i);
         }
         c_at += L::STAGE;
         if (++c_slot == L::DEPTH) {
@@ -202,6 +223,7 @@ struct W4Flow {
             }
             c_line = c_lo;
             if (left) aim();
+            else rw.z = rp.z = 0;
         }
     }
     // Asks for the first lines.
@@ -215,8 +237,13 @@ struct W4Flow {
         else rw = rp = make_rsrc(W, 0);
         c_at = lds_addr(ring);
         c_slot = 0;
-        piece = 16u * (uint32_t)((lane & 7) ^ (lane >> 4));
-        row_at = (uint32_t)(lane >> 3) * kb;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) w_at[i] = (uint32_t)(8 * i + (lane >> 3)) * kb + 16u * (uint32_t)((lane & 7) ^ (4 * i + (lane >> 4)));
+#pragma unroll
+        for (int i = 0; i < L::COPIES - 2; ++i) {
+            const uint32_t g = (uint32_t)(4 * i + (lane >> 4));
+            p_at[i] = g < GROUPS ? ((uint32_t)(lane & 15) * groups + g) * 4u : 0xFFFFFFF0u;
+        }
 #pragma unroll
         for (int d = 0; d < L::DEPTH - 1; ++d) copy();
     }
@@ -268,11 +295,6 @@ struct W4Flow {
 
         const W4Const konst = w4_const<T>();
         uint32_t at = 0, slot = 0;   // of the ring
-        uint32_t xrow[MT][PLANES];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int pl = 0; pl < PLANES; ++pl) xrow[m][pl] = (uint32_t)(min(16 * m + r, rows - 1) + pl * rows);
         for (int32_t c = 0; c < lines; c += sp.chunk) {
             if (c) {
                 __syncthreads();
@@ -280,9 +302,20 @@ struct W4Flow {
                 w4_wait<0>();
                 order_x(c, xrows);
             }
-            const uint32_t bytes = (uint32_t)min(sp.chunk, lines - c) * 512u;
             int32_t lo, hi;
             bounds(c, lo, hi);
+            // what a lane reads of x: its row's pieces j of a line's first half, any row's where it has none
+            uint32_t xa[4][MT][PLANES];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int pl = 0; pl < PLANES; ++pl) {
+                    const uint32_t row = (uint32_t)(min(16 * m + r, rows - 1) + pl * rows);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        xa[j][m][pl] = row * (uint32_t)min(sp.chunk, lines - c) * 512u +
+                                       16u * ((uint32_t)(G == 128 ? 4 * q + j : 4 * j + q) ^ (row & 15u));
+                }
             if (lo == hi && c) continue;
             for (int32_t tile = 0; tile < tiles; ++tile) {   // (without lines: sums of zero)
                 f32x4 acc[MT];
@@ -299,16 +332,14 @@ struct W4Flow {
                     for (int h = 0; h < 2; ++h) w[h] = *(const u32x4 *)(st + 128 * r + 16 * ((4 * h + q) ^ (r >> 1)));
 #pragma unroll
                     for (int g = 0; g < GROUPS; ++g) num[g] = *(const uint32_t *)(st + 2048 + 64 * g + 4 * r);
+                    const char *xl = lds + (uint32_t)(line - c) * 512u;
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
 #pragma unroll
                         for (int m = 0; m < MT; ++m)
 #pragma unroll
-                            for (int pl = 0; pl < PLANES; ++pl) {
-                                const int32_t p = 16 * (j / 4) + (G == 128 ? 4 * q + j % 4 : 4 * (j % 4) + q);
-                                x[j][m][pl] = *(const u32x4 *)(lds + xrow[m][pl] * bytes + (uint32_t)(line - c) * 512u +
-                                                               16u * ((uint32_t)p ^ (xrow[m][pl] & 15u)));
-                            }
+                            for (int pl = 0; pl < PLANES; ++pl)
+                                x[j][m][pl] = *(const u32x4 *)(xl + xa[j % 4][m][pl] + 256 * (j / 4));
                     __builtin_amdgcn_sched_barrier(0);
                     if constexpr (G != 128) {
                         w4_transpose(w[0]);
@@ -327,6 +358,7 @@ struct W4Flow {
                             for (int m = 0; m < MT; ++m)
 #pragma unroll
                                 for (int pl = 0; pl < PLANES; ++pl) {
+                                    // (x's own sum too: forming it beside the ordering of x takes longer)
                                     xs[m] = mfma16<T>(x[j][m][pl], u32x4{one, one, one, one}, xs[m]);
                                     sum[m] = mfma16<T>(x[j][m][pl], lv, sum[m]);
                                 }
