@@ -187,24 +187,43 @@ struct MoeRanks {
     }
 };
 
+// Expert, list of tokens and their number, once asked for: what both products begin with.  start():
+// called between, when the expert is known.
+template <class Start>
+__device__ inline int32_t moe_route(const MoeArgs &a, bool by_pair, int32_t &expert, MoeList &l, Start &&start)
+{
+    const int32_t slot = (int32_t)blockIdx.y;
+    if (by_pair && a.T == 1) {   // one token: slot j is its expert number j
+        expert = moe_slot(a, slot, true).expert;
+        start();
+        if (threadIdx.x == 0) l.rank[0] = l.row[0] = slot;
+        __syncthreads();
+        return 1;
+    }
+    MoeRanks ranks;
+    ranks.ask(a);
+    const MoeSlot ms = moe_slot(a, slot, by_pair);
+    expert = ms.expert;
+    ranks.count(a, expert);
+    start();
+    return ranks.list(a, ms, l);
+}
+
 // ---- gate and up, activation -----------------------------------------------
 // A workgroup: an expert, some blocks of 16 columns, g.rows of its tokens at a time.
+// EARLY: x, all tokens' (up: at most g.rows of them) or the one token's (down), is asked for
+// before the expert is known.
 struct MoeGrid {
-    bool by_pair;
+    bool by_pair, early;
     int32_t rows;    // tokens at a time, at most 16
     uint32_t x_bytes;
     W4Split sp;      // of blocks (up: a tile of gate rows and one of up rows each) or tiles (down)
 };
-template <class T, int G>
+template <class T, int G, bool EARLY>
 __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGrid g)
 {
     extern __shared__ __attribute__((aligned(1024))) char smem[];
     __shared__ MoeList list;
-    MoeRanks ranks;
-    ranks.ask(a);
-    const MoeSlot ms = moe_slot(a, (int32_t)blockIdx.y, g.by_pair);
-    const int32_t expert = ms.expert;
-    ranks.count(a, expert);
     const int32_t lane = (int32_t)(threadIdx.x & 63u), q = lane >> 4, r = lane & 15;
     const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int32_t kw = g.sp.kw, each = g.sp.each, lines = (a.H + 255) / 256;
@@ -213,64 +232,75 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGri
     float *const slots = (float *)(smem + g.x_bytes + W4Lds<G>::RINGS);
     __bf16 *const hi = (__bf16 *)a.h, *const lo = hi + (int64_t)a.T * a.top_k * a.I;
     auto put = [&](int32_t m, int32_t c, float gate, float up) {
+        int32_t row = list.row[m];
+        if constexpr (EARLY) {   // row m is token m, perhaps of other experts alone
+            if (list.rank[m] < 0) return;
+            row = m * a.top_k + list.rank[m];
+        }
+        // (a quotient and an exponential good to 2^-21)
         const float h = gate / (1.0f + __expf(-gate)) * up;
-        const int64_t o = (int64_t)list.row[m] * a.I + b0 * 16 + c;
+        const int64_t o = (int64_t)row * a.I + b0 * 16 + c;
         const __bf16 top = (__bf16)h;
         hi[o] = top;
         lo[o] = (__bf16)(h - (float)top);
     };
+    int32_t expert = 0;
     auto tile_at = [&](int32_t t) { return W4Tile{((int64_t)expert * 2 + t % 2) * a.I + (b0 + mine + t / 2) * 16, 16}; };
     W4Flow<T, T, 1, G, 1, decltype(tile_at)> flow(smem, g.x_bytes, a.w1, (const uint32_t *)a.p1, a.H, g.sp,
                                                   2 * max(0, min(each, have - mine)), tile_at);
+    const i32x4 rx = make_rsrc(a.x, 0xFFFFFFF0u);
+    if constexpr (EARLY) flow.ask_x(0, a.T, rx, [&](int32_t i) { return (uint32_t)i * (uint32_t)a.ldx * 2u; });
     // the first weights are on their way while the tokens are gathered
-    flow.start();
-    const int32_t count = ranks.list(a, ms, list);
+    const int32_t count = __builtin_amdgcn_readfirstlane(moe_route(a, g.by_pair, expert, list, [&] {
+        expert = __builtin_amdgcn_readfirstlane(expert);
+        flow.start();
+    }));
     if (count == 0) flow.finish();
     for (int32_t at = 0; at < count; at += g.rows) {
-        const int32_t rows = min(g.rows, count - at), slot = rows * W4_SLOT_LD;
+        const int32_t rows = EARLY ? a.T : min(g.rows, count - at), slot = rows * W4_SLOT_LD;
         const bool direct = kw == 1 && g.sp.chunk >= lines;   // a wave has whole sums
         f32x4 gate[1];
-        if (at) __syncthreads();
-        flow.run(
-            rows, make_rsrc(a.x, 0xFFFFFFF0u), at == 0,
-            [&](int32_t i) { return (uint32_t)(list.row[at + i] / a.top_k) * (uint32_t)a.ldx * 2u; },
-            [&](int32_t t, const f32x4(&acc)[1], bool more) {
-                if (!direct) {
-                    w4_put<1>(slots + (wave * 2 * each + t) * slot, rows, acc, more);
-                } else if (t % 2 == 0) {
-                    gate[0] = acc[0];
-                } else {
+        auto x_at = [&](int32_t i) { return (uint32_t)(list.row[at + i] / a.top_k) * (uint32_t)a.ldx * 2u; };
+        auto done = [&](int32_t t, const f32x4(&acc)[1], bool more) {
+            if (!direct) {
+                w4_put<1>(slots + (wave * 2 * each + t) * slot, rows, acc, more);
+            } else if (t % 2 == 0) {
+                gate[0] = acc[0];
+            } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (4 * q + i < rows) put(at + 4 * q + i, (mine + t / 2) * 16 + r, gate[0][i], acc[0][i]);
-                }
-            });
-        if (direct) continue;
-        __syncthreads();
-        for (int32_t i = (int32_t)threadIdx.x; i < rows * have * 16; i += 64 * W4_WAVES) {
-            const int32_t m = i / (have * 16), c = i - m * have * 16, b = c / 16;
-            const float *s = slots + (b / each * kw * 2 * each + b % each * 2) * slot + m * W4_SLOT_LD + c % 16;
-            float v = 0.f, u = 0.f;
-            for (int32_t k = 0; k < kw; ++k) {
-                v += s[k * 2 * each * slot];
-                u += s[(k * 2 * each + 1) * slot];
+                for (int i = 0; i < 4; ++i)
+                    if (4 * q + i < rows) put(at + 4 * q + i, (mine + t / 2) * 16 + r, gate[0][i], acc[0][i]);
             }
-            put(at + m, c, v, u);
+        };
+        if (at == 0) {
+            flow.template run<true, EARLY>(rows, rx, x_at, done);
+        } else if constexpr (!EARLY) {
+            __syncthreads();
+            flow.template run<false, false>(rows, rx, x_at, done);
         }
+        if (!direct) {
+            __syncthreads();
+            for (int32_t i = (int32_t)threadIdx.x; i < rows * have * 16; i += 64 * W4_WAVES) {
+                const int32_t m = i / (have * 16), c = i - m * have * 16, b = c / 16;
+                const float *s = slots + (b / each * kw * 2 * each + b % each * 2) * slot + m * W4_SLOT_LD + c % 16;
+                float v = 0.f, u = 0.f;
+                for (int32_t k = 0; k < kw; ++k) {
+                    v += s[k * 2 * each * slot];
+                    u += s[(k * 2 * each + 1) * slot];
+                }
+                put(at + m, c, v, u);
+            }
+        }
+        if constexpr (EARLY) return;
     }
 }
 
 // ---- down ------------------------------------------------------------------
-template <class T, int G>
+template <class T, int G, bool EARLY>
 __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_kernel(MoeArgs a, MoeGrid g)
 {
     extern __shared__ __attribute__((aligned(1024))) char smem[];
     __shared__ MoeList list;
-    MoeRanks ranks;
-    ranks.ask(a);
-    const MoeSlot ms = moe_slot(a, (int32_t)blockIdx.y, g.by_pair);
-    const int32_t expert = ms.expert;
-    ranks.count(a, expert);
     const int32_t lane = (int32_t)(threadIdx.x & 63u), q = lane >> 4, r = lane & 15;
     const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int32_t kw = g.sp.kw, each = g.sp.each, lines = (a.I + 255) / 256;
@@ -278,40 +308,51 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_kernel(MoeArgs a, MoeG
     const int32_t mine = wave / kw * each;
     float *const slots = (float *)(smem + g.x_bytes + W4Lds<G>::RINGS);
     const uint32_t plane = (uint32_t)(a.T * a.top_k) * (uint32_t)a.I * 2u;
+    int32_t expert = 0;
     auto tile_at = [&](int32_t t) { return W4Tile{(int64_t)expert * a.H + (t0 + mine + t) * 16, 16}; };
     W4Flow<__bf16, T, 1, G, 2, decltype(tile_at)> flow(smem, g.x_bytes, a.w2, (const uint32_t *)a.p2, a.I, g.sp,
                                                        max(0, min(each, have - mine)), tile_at);
-    flow.start();
-    const int32_t count = ranks.list(a, ms, list);
+    const i32x4 rx = make_rsrc(a.h, 0xFFFFFFF0u);
+    if constexpr (EARLY)   // (one token: slot j's row is j)
+        flow.ask_x(0, 2, rx, [&](int32_t i) { return blockIdx.y * (uint32_t)a.I * 2u + (i ? plane : 0u); });
+    const int32_t count = __builtin_amdgcn_readfirstlane(moe_route(a, g.by_pair, expert, list, [&] {
+        expert = __builtin_amdgcn_readfirstlane(expert);
+        flow.start();
+    }));
     if (count == 0) flow.finish();
     for (int32_t at = 0; at < count; at += g.rows) {
         const int32_t rows = min(g.rows, count - at), slot = rows * W4_SLOT_LD;
         const bool direct = kw == 1 && g.sp.chunk >= lines;
-        if (at) __syncthreads();
-        flow.run(
-            rows, make_rsrc(a.h, 0xFFFFFFF0u), at == 0,
-            [&](int32_t i) {
-                const int32_t second = i >= rows;
-                return (uint32_t)list.row[at + i - (second ? rows : 0)] * (uint32_t)a.I * 2u + (second ? plane : 0u);
-            },
-            [&](int32_t t, const f32x4(&acc)[1], bool more) {
-                if (!direct) {
-                    w4_put<1>(slots + (wave * each + t) * slot, rows, acc, more);
-                } else {
+        auto x_at = [&](int32_t i) {
+            const int32_t second = i >= rows;
+            return (uint32_t)list.row[at + i - (second ? rows : 0)] * (uint32_t)a.I * 2u + (second ? plane : 0u);
+        };
+        auto done = [&](int32_t t, const f32x4(&acc)[1], bool more) {
+            if (!direct) {
+                w4_put<1>(slots + (wave * each + t) * slot, rows, acc, more);
+            } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (4 * q + i < rows) a.y[(int64_t)list.row[at + 4 * q + i] * a.H + (t0 + mine + t) * 16 + r] = acc[0][i];
-                }
-            });
-        if (direct) continue;
-        __syncthreads();
-        for (int32_t i = (int32_t)threadIdx.x; i < rows * have * 16; i += 64 * W4_WAVES) {
-            const int32_t m = i / (have * 16), c = i - m * have * 16, t = c / 16;
-            const float *s = slots + (t / each * kw * each + t % each) * slot + m * W4_SLOT_LD + c % 16;
-            float v = 0.f;
-            for (int32_t k = 0; k < kw; ++k) v += s[k * each * slot];
-            a.y[(int64_t)list.row[at + m] * a.H + t0 * 16 + c] = v;
+                for (int i = 0; i < 4; ++i)
+                    if (4 * q + i < rows) a.y[(int64_t)list.row[at + 4 * q + i] * a.H + (t0 + mine + t) * 16 + r] = acc[0][i];
+            }
+        };
+        if (at == 0) {
+            flow.template run<true, EARLY>(rows, rx, x_at, done);
+        } else if constexpr (!EARLY) {
+            __syncthreads();
+            flow.template run<false, false>(rows, rx, x_at, done);
         }
+        if (!direct) {
+            __syncthreads();
+            for (int32_t i = (int32_t)threadIdx.x; i < rows * have * 16; i += 64 * W4_WAVES) {
+                const int32_t m = i / (have * 16), c = i - m * have * 16, t = c / 16;
+                const float *s = slots + (t / each * kw * each + t % each) * slot + m * W4_SLOT_LD + c % 16;
+                float v = 0.f;
+                for (int32_t k = 0; k < kw; ++k) v += s[k * each * slot];
+                a.y[(int64_t)list.row[at + m] * a.H + t0 * 16 + c] = v;
+            }
+        }
+        if constexpr (EARLY) return;
     }
 }
 
@@ -418,11 +459,15 @@ template <class T, int G> static hipError_t moe_t(const MoeArgs &a, int cu, hipS
 {
     const uint32_t slots = (uint32_t)min(a.T * a.top_k, a.E);
     const dim3 block(64 * W4_WAVES);
-    const MoeShape up = moe_shape<G>(a, a.I / 16, a.H, 1, 2, slots, cu), dn = moe_shape<G>(a, a.H / 16, a.I, 2, 1, slots, cu);
+    MoeShape up = moe_shape<G>(a, a.I / 16, a.H, 1, 2, slots, cu), dn = moe_shape<G>(a, a.H / 16, a.I, 2, 1, slots, cu);
+    up.g.early = a.T <= up.g.rows && up.g.sp.chunk >= (a.H + 255) / 256;   // all of x at once
+    dn.g.early = a.T == 1 && dn.g.by_pair;
     if (up.lds > MOE_LDS || dn.lds > MOE_LDS) return hipErrorInvalidValue;
     hipLaunchKernelGGL((moe_router_kernel<T>), dim3((uint32_t)(a.E + 15) / 16, (uint32_t)(a.T + 15) / 16), dim3(64 * ROUTER_WAVES), 0, s, a);
-    hipLaunchKernelGGL((moe_up_kernel<T, G>), dim3(up.x, slots), block, up.lds, s, a, up.g);
-    hipLaunchKernelGGL((moe_down_kernel<T, G>), dim3(dn.x, slots), block, dn.lds, s, a, dn.g);
+    if (up.g.early) hipLaunchKernelGGL((moe_up_kernel<T, G, true>), dim3(up.x, slots), block, up.lds, s, a, up.g);
+    else hipLaunchKernelGGL((moe_up_kernel<T, G, false>), dim3(up.x, slots), block, up.lds, s, a, up.g);
+    if (dn.g.early) hipLaunchKernelGGL((moe_down_kernel<T, G, true>), dim3(dn.x, slots), block, dn.lds, s, a, dn.g);
+    else hipLaunchKernelGGL((moe_down_kernel<T, G, false>), dim3(dn.x, slots), block, dn.lds, s, a, dn.g);
     hipLaunchKernelGGL((moe_combine_kernel<T>), dim3((uint32_t)(a.H + 4 * COMBINE_THREADS - 1) / (4 * COMBINE_THREADS), (uint32_t)a.T),
                        dim3(COMBINE_THREADS), 0, s, a);
     return hipGetLastError();

@@ -34,9 +34,10 @@ __global__ __launch_bounds__(64 * W4_WAVES) void w4_few_kernel(const T *__restri
     W4Flow<T, T, MT, G, 1, decltype(tile_at)> flow(smem, W4Lds<G>::x_bytes(rows, a.sp.chunk), a.w, a.p, a.K, a.sp,
                                                    max(0, min(each, have - mine)), tile_at);
     if constexpr (EARLY) flow.start();
-    flow.run(rows, make_rsrc(X + (int64_t)m0 * a.ldx, 0xFFFFFFF0u), EARLY,
-             [&](int32_t row) { return (uint32_t)row * (uint32_t)a.ldx * 2u; },
-             [&](int32_t t, const f32x4(&acc)[MT], bool more) { w4_put<MT>(slots + (wave * each + t) * slot, rows, acc, more); });
+    flow.template run<EARLY, false>(
+        rows, make_rsrc(X + (int64_t)m0 * a.ldx, 0xFFFFFFF0u),
+        [&](int32_t row) { return (uint32_t)row * (uint32_t)a.ldx * 2u; },
+        [&](int32_t t, const f32x4(&acc)[MT], bool more) { w4_put<MT>(slots + (wave * each + t) * slot, rows, acc, more); });
     __syncthreads();
     for (int32_t i = (int32_t)threadIdx.x; i < rows * have * 16; i += 64 * W4_WAVES) {
         const int32_t m = i / (have * 16), c = i - m * have * 16, t = c / 16, n = t0 * 16 + c;

@@ -277,20 +277,19 @@ struct W4Flow {
     }
 
     // `rows` rows of x through rx, row i's first byte at x_at(i) (PLANES 2: rows from `rows` on are
-    // the second plane's).  started: start() has been called, and the weights' latency runs beside the
-    // copy of x; else start() comes after it, and beside the putting in order.
+    // the second plane's).  STARTED: start() has been called, and the weights' latency runs beside
+    // the copy of x; else start() comes after it, and beside the putting in order.  ASKED: ask_x()
+    // has been called, before start().
     //   done(t, acc, more): sums of tile t over this wave's lines of a chunk, more: not the first
     //     chunk's; acc[m][i] is row 4 (lane / 16) + i of 16 rows m, column lane % 16.
-    template <class XAt, class Done> __device__ inline void run(int32_t rows, const i32x4 rx, bool started, XAt &&x_at, Done &&done)
+    template <bool STARTED, bool ASKED, class XAt, class Done>
+    __device__ inline void run(int32_t rows, const i32x4 rx, XAt &&x_at, Done &&done)
     {
         const int32_t q = lane >> 4, r = lane & 15, xrows = PLANES * rows;
-        ask_x(0, xrows, rx, x_at);
-        if (started) {
-            w4_wait<0>();
-        } else {
-            start();
-            w4_wait<(L::DEPTH - 1) * L::COPIES>();
-        }
+        if constexpr (!ASKED) ask_x(0, xrows, rx, x_at);
+        if constexpr (!STARTED) start();
+        if constexpr (STARTED && !ASKED) w4_wait<0>();
+        else w4_wait<(L::DEPTH - 1) * L::COPIES>();
         order_x(0, xrows);
 
         const W4Const konst = w4_const<T>();
