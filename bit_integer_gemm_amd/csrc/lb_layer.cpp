@@ -58,14 +58,14 @@ int check_moe(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k, int64_t
 }
 
 struct MoeSpace {
-    int64_t logits, h, y, bytes;
+    int64_t lists, h, y, bytes;
 };
 MoeSpace moe_space(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k)
 {
     const int64_t tokens = std::min<int64_t>(T, lb::MOE_TOKENS);
     MoeSpace m;
-    m.logits = 0;
-    m.h = round_up(tokens * E * 4, 256);
+    m.lists = round_up(tokens * E * 4, 256);   // (the logits come first)
+    m.h = m.lists + round_up(std::min(tokens * top_k, E) * (2 + lb::MOE_TOKENS) * 4, 256);
     m.y = m.h + round_up(tokens * top_k * I * 4, 256);
     m.bytes = m.y + round_up(tokens * top_k * H * 4, 256);
     return m;
@@ -255,6 +255,7 @@ int lb_moe_w4(const void *X, int64_t ldx, const void *Wr, const uint8_t *W1, con
         a.renorm = renorm != 0;
         a.scale = scale;
         a.logits = (float *)workspace;
+        a.lists = (int32_t *)((char *)workspace + m.lists);
         a.h = (char *)workspace + m.h;
         a.y = (float *)((char *)workspace + m.y);
         const hipError_t e = lb::launch_moe_w4(ftype, (int)group, a, cu, (hipStream_t)stream);

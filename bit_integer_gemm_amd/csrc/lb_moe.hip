@@ -69,6 +69,7 @@ __global__ __launch_bounds__(64 * ROUTER_WAVES) void moe_router_kernel(MoeArgs a
 // (token, rank) pairs where those are fewer; of pairs that name the same expert the first
 // one's workgroups work for all its tokens, the others end.
 enum { EXPERTS_MAX = 1024 };
+enum { MOE_LIST = 2 + MOE_TOKENS };   // in the workspace: count, expert, rows
 struct MoeList {
     int32_t rank[MOE_TOKENS];   // the expert's rank in each token's order, if below k, else -1
     int32_t row[MOE_TOKENS];    // token * k + rank of each of its tokens
@@ -187,8 +188,7 @@ struct MoeRanks {
     }
 };
 
-// Expert, list of tokens and their number, once asked for: what both products begin with.  start():
-// called between, when the expert is known.
+// Expert, list of tokens and their number.  start(): called between, when the expert is known.
 template <class Start>
 __device__ inline int32_t moe_route(const MoeArgs &a, bool by_pair, int32_t &expert, MoeList &l, Start &&start)
 {
@@ -255,6 +255,12 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGri
         expert = __builtin_amdgcn_readfirstlane(expert);
         flow.start();
     }));
+    if (blockIdx.x == 0) {   // for the down product
+        int32_t *const l = a.lists + blockIdx.y * MOE_LIST;
+        if (threadIdx.x < (uint32_t)count) l[2 + threadIdx.x] = list.row[threadIdx.x];
+        if (threadIdx.x == 64) l[0] = count;
+        if (threadIdx.x == 65) l[1] = expert;
+    }
     if (count == 0) flow.finish();
     for (int32_t at = 0; at < count; at += g.rows) {
         const int32_t rows = EARLY ? a.T : min(g.rows, count - at), slot = rows * W4_SLOT_LD;
@@ -315,11 +321,16 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_kernel(MoeArgs a, MoeG
     const i32x4 rx = make_rsrc(a.h, 0xFFFFFFF0u);
     if constexpr (EARLY)   // (one token: slot j's row is j)
         flow.ask_x(0, 2, rx, [&](int32_t i) { return blockIdx.y * (uint32_t)a.I * 2u + (i ? plane : 0u); });
-    const int32_t count = __builtin_amdgcn_readfirstlane(moe_route(a, g.by_pair, expert, list, [&] {
-        expert = __builtin_amdgcn_readfirstlane(expert);
-        flow.start();
-    }));
-    if (count == 0) flow.finish();
+    const int32_t *const l = a.lists + blockIdx.y * MOE_LIST;
+    const int32_t count = l[0];
+    expert = l[1];
+    if (count == 0) {
+        flow.finish();
+        return;
+    }
+    const int32_t mine_row = l[2 + min(lane, count - 1)];
+    list.row[lane] = mine_row;   // (every wave writes the same, and reads what it wrote)
+    flow.start();
     for (int32_t at = 0; at < count; at += g.rows) {
         const int32_t rows = min(g.rows, count - at), slot = rows * W4_SLOT_LD;
         const bool direct = kw == 1 && g.sp.chunk >= lines;

@@ -110,7 +110,7 @@ template <int G> struct W4Lds {
         GROUPS = 256 / G,
         NUMBERS = G == 32 ? 512 : 256,          // (scale, minimum) words of a line's 16 rows, group by group
         STAGE = 2048 + NUMBERS,
-        DEPTH = 4,
+        DEPTH = 3,
         COPIES = G == 32 ? 4 : 3,               // copies of a stage
         RING = DEPTH * STAGE,
         RINGS = W4_WAVES * RING
@@ -146,7 +146,7 @@ template <int N> __device__ inline void w4_wait() { asm volatile("s_waitcnt vmcn
 
 // The products of a wave's tiles: 16 MT rows of x at most by 16 columns each.
 //   lds: x (x_bytes of it; PLANES 2: x is the sum of two planes, whose rows follow each other),
-//     then the rings.  Copies of three lines are under way while a fourth is worked on; each
+//     then the rings.  Copies of two lines are under way while a third is worked on; each
 //     wave waits for its own by count.
 //   tiles: this wave's; tile_at(t): a W4Tile.
 //   T: the type of x as the matrix cores take it; PT: of the groups' numbers.
