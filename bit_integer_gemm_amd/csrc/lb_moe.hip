@@ -26,21 +26,19 @@ __device__ inline uint32_t order_of(float v)
 }
 
 // ---- router ----------------------------------------------------------------
-// 16 experts by 16 tokens to a workgroup, a share of H to each wave, whose loads (of up to 256
-// numbers of a row) are all under way at once.
-enum { ROUTER_WAVES = 16, ROUTER_STEPS = 8 };
-template <class T>
-__global__ __launch_bounds__(64 * ROUTER_WAVES) void moe_router_kernel(MoeArgs a)
+// 16 experts by 16 tokens, a share of H to each of NW waves, whose loads (of up to 256 numbers
+// of a row) are all under way at once.  sums: LDS for NW tiles; the logits of thread i < 256,
+// token t0 + i / 16 and expert e0 + i % 16, are returned to it.
+enum { ROUTER_WAVES = 16, ROUTER_STEPS = 8, ROUTER_TILE = 16 * W4_SLOT_LD };
+template <class T, int NW> __device__ inline float router_tile(const MoeArgs &a, int32_t e0, int32_t t0, float *sums)
 {
-    __shared__ float sums[ROUTER_WAVES][16 * W4_SLOT_LD];
     const int32_t lane = (int32_t)(threadIdx.x & 63u), q = lane >> 4, r = lane & 15;
     const int32_t wave = (int32_t)(threadIdx.x >> 6);
-    const int32_t e0 = (int32_t)blockIdx.x * 16, t0 = (int32_t)blockIdx.y * 16;
     const T *wrow = (const T *)a.wr + (int64_t)min(e0 + r, a.E - 1) * a.H;
     const T *xrow = (const T *)a.x + (int64_t)min(t0 + r, a.T - 1) * a.ldx;
-    const int32_t steps = a.H / 32, last = (wave + 1) * steps / ROUTER_WAVES;
+    const int32_t steps = a.H / 32, last = (wave + 1) * steps / NW;
     f32x4 acc[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
-    for (int32_t st = wave * steps / ROUTER_WAVES; st < last; st += ROUTER_STEPS) {
+    for (int32_t st = wave * steps / NW; st < last; st += ROUTER_STEPS) {
         u32x4 x[ROUTER_STEPS], w[ROUTER_STEPS];
 #pragma unroll
         for (int i = 0; i < ROUTER_STEPS; ++i) {
@@ -53,15 +51,22 @@ __global__ __launch_bounds__(64 * ROUTER_WAVES) void moe_router_kernel(MoeArgs a
 #pragma unroll
         for (int i = 0; i < ROUTER_STEPS; ++i) acc[0] = mfma16<T>(x[i], w[i], acc[0]);
     }
-    w4_put<1>(sums[wave], 16, acc, false);
+    w4_put<1>(sums + wave * ROUTER_TILE, 16, acc, false);
     __syncthreads();
-    if (threadIdx.x < 256) {
-        const int32_t m = (int32_t)threadIdx.x / 16, n = (int32_t)threadIdx.x % 16;
-        float v = 0.f;
+    float v = 0.f;
+    if (threadIdx.x < 256)
 #pragma unroll
-        for (int w = 0; w < ROUTER_WAVES; ++w) v += sums[w][m * W4_SLOT_LD + n];
-        if (t0 + m < a.T && e0 + n < a.E) a.logits[(t0 + m) * a.E + e0 + n] = v;
-    }
+        for (int w = 0; w < NW; ++w) v += sums[w * ROUTER_TILE + (int32_t)threadIdx.x / 16 * W4_SLOT_LD + (int32_t)threadIdx.x % 16];
+    return v;
+}
+template <class T>
+__global__ __launch_bounds__(64 * ROUTER_WAVES) void moe_router_kernel(MoeArgs a)
+{
+    __shared__ float sums[ROUTER_WAVES * ROUTER_TILE];
+    const int32_t e0 = (int32_t)blockIdx.x * 16, t0 = (int32_t)blockIdx.y * 16;
+    const float v = router_tile<T, ROUTER_WAVES>(a, e0, t0, sums);
+    const int32_t t = t0 + (int32_t)threadIdx.x / 16, e = e0 + (int32_t)threadIdx.x % 16;
+    if (threadIdx.x < 256 && t < a.T && e < a.E) a.logits[t * a.E + e] = v;
 }
 
 // ---- who goes where --------------------------------------------------------
@@ -73,6 +78,7 @@ enum { MOE_LIST = 2 + MOE_TOKENS };   // in the workspace: count, expert, rows
 struct MoeList {
     int32_t rank[MOE_TOKENS];   // the expert's rank in each token's order, if below k, else -1
     int32_t row[MOE_TOKENS];    // token * k + rank of each of its tokens
+    float logits[256];          // where a workgroup forms them itself: 16 experts, 16 tokens
 };
 
 // Number j (from 0) in a token's order of its logits, by every wave for itself: lane l holds
@@ -116,11 +122,11 @@ template <int NC> __device__ inline int32_t nth_expert(const float *row, int32_t
 struct MoeSlot {
     int32_t expert, first;
 };
-__device__ inline MoeSlot moe_slot(const MoeArgs &a, int32_t slot, bool by_pair)
+__device__ inline MoeSlot moe_slot(const MoeArgs &a, const float *logits, int32_t slot, bool by_pair)
 {
     if (!by_pair) return MoeSlot{slot, 0};
     const int32_t t = slot / a.top_k, j = slot - t * a.top_k;
-    const float *row = a.logits + t * a.E;
+    const float *row = logits + t * a.E;
     const int32_t e = a.E <= 64 ? nth_expert<1>(row, a.E, j) : a.E <= 128 ? nth_expert<2>(row, a.E, j)
                     : a.E <= 256 ? nth_expert<4>(row, a.E, j) : nth_expert<16>(row, a.E, j);
     return MoeSlot{__builtin_amdgcn_readfirstlane(e), t};
@@ -132,17 +138,17 @@ struct MoeRanks {
     enum : int { AHEAD = 2 };
     float v[AHEAD][MOE_EACH];
     int32_t above[MOE_EACH];
-    __device__ inline void load(const MoeArgs &a, int32_t f0)
+    __device__ inline void load(const MoeArgs &a, const float *logits, int32_t f0)
     {
         const int32_t lane = (int32_t)threadIdx.x & 63, wave = (int32_t)threadIdx.x >> 6;
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u)
 #pragma unroll
             for (int i = 0; i < MOE_EACH; ++i)
-                v[u][i] = a.logits[min(wave + W4_WAVES * i, a.T - 1) * a.E + min(f0 + 64 * u + lane, a.E - 1)];
+                v[u][i] = logits[min(wave + W4_WAVES * i, a.T - 1) * a.E + min(f0 + 64 * u + lane, a.E - 1)];
     }
-    __device__ inline void ask(const MoeArgs &a) { load(a, 0); }
-    __device__ inline void count(const MoeArgs &a, int32_t e)
+    __device__ inline void ask(const MoeArgs &a, const float *logits) { load(a, logits, 0); }
+    __device__ inline void count(const MoeArgs &a, const float *logits, int32_t e)
     {
         const int32_t lane = (int32_t)threadIdx.x & 63, wave = (int32_t)threadIdx.x >> 6;
         float own[MOE_EACH];
@@ -153,7 +159,7 @@ struct MoeRanks {
         }
         if (e >= 64 * AHEAD)
 #pragma unroll
-            for (int i = 0; i < MOE_EACH; ++i) own[i] = a.logits[min(wave + W4_WAVES * i, a.T - 1) * a.E + e];
+            for (int i = 0; i < MOE_EACH; ++i) own[i] = logits[min(wave + W4_WAVES * i, a.T - 1) * a.E + e];
         for (int32_t f0 = 0;;) {
 #pragma unroll
             for (int i = 0; i < MOE_EACH; ++i) {
@@ -169,7 +175,7 @@ struct MoeRanks {
             }
             f0 += 64 * AHEAD;
             if (f0 >= a.E) break;
-            load(a, f0);
+            load(a, logits, f0);
         }
     }
     // The list of the expert's tokens.  Returns how many; 0 where an earlier slot's workgroups work for
@@ -190,21 +196,21 @@ struct MoeRanks {
 
 // Expert, list of tokens and their number.  start(): called between, when the expert is known.
 template <class Start>
-__device__ inline int32_t moe_route(const MoeArgs &a, bool by_pair, int32_t &expert, MoeList &l, Start &&start)
+__device__ inline int32_t moe_route(const MoeArgs &a, const float *logits, bool by_pair, int32_t &expert, MoeList &l, Start &&start)
 {
     const int32_t slot = (int32_t)blockIdx.y;
     if (by_pair && a.T == 1) {   // one token: slot j is its expert number j
-        expert = moe_slot(a, slot, true).expert;
+        expert = moe_slot(a, logits, slot, true).expert;
         start();
         if (threadIdx.x == 0) l.rank[0] = l.row[0] = slot;
         __syncthreads();
         return 1;
     }
     MoeRanks ranks;
-    ranks.ask(a);
-    const MoeSlot ms = moe_slot(a, slot, by_pair);
+    ranks.ask(a, logits);
+    const MoeSlot ms = moe_slot(a, logits, slot, by_pair);
     expert = ms.expert;
-    ranks.count(a, expert);
+    ranks.count(a, logits, expert);
     start();
     return ranks.list(a, ms, l);
 }
@@ -213,13 +219,15 @@ __device__ inline int32_t moe_route(const MoeArgs &a, bool by_pair, int32_t &exp
 // A workgroup: an expert, some blocks of 16 columns, g.rows of its tokens at a time.
 // EARLY: x, all tokens' (up: at most g.rows of them) or the one token's (down), is asked for
 // before the expert is known.
+// ROUTE (at most 16 tokens and experts): every workgroup forms the logits for itself, which takes
+// a us where a launch for them takes five.
 struct MoeGrid {
     bool by_pair, early;
     int32_t rows;    // tokens at a time, at most 16
     uint32_t x_bytes;
     W4Split sp;      // of blocks (up: a tile of gate rows and one of up rows each) or tiles (down)
 };
-template <class T, int G, bool EARLY>
+template <class T, int G, bool EARLY, bool ROUTE>
 __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGrid g)
 {
     extern __shared__ __attribute__((aligned(1024))) char smem[];
@@ -250,8 +258,19 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGri
                                                   2 * max(0, min(each, have - mine)), tile_at);
     const i32x4 rx = make_rsrc(a.x, 0xFFFFFFF0u);
     if constexpr (EARLY) flow.ask_x(0, a.T, rx, [&](int32_t i) { return (uint32_t)i * (uint32_t)a.ldx * 2u; });
+    const float *logits = a.logits;
+    if constexpr (ROUTE) {
+        const float v = router_tile<T, W4_WAVES>(a, 0, 0, (float *)(smem + g.x_bytes));   // (where the rings will be)
+        const int32_t t = (int32_t)threadIdx.x / 16, e = (int32_t)threadIdx.x % 16;
+        if (threadIdx.x < 256 && t < a.T && e < a.E) {
+            list.logits[t * a.E + e] = v;
+            if (blockIdx.x + blockIdx.y == 0) a.logits[t * a.E + e] = v;
+        }
+        __syncthreads();
+        logits = list.logits;
+    }
     // the first weights are on their way while the tokens are gathered
-    const int32_t count = __builtin_amdgcn_readfirstlane(moe_route(a, g.by_pair, expert, list, [&] {
+    const int32_t count = __builtin_amdgcn_readfirstlane(moe_route(a, logits, g.by_pair, expert, list, [&] {
         expert = __builtin_amdgcn_readfirstlane(expert);
         flow.start();
     }));
@@ -474,9 +493,11 @@ template <class T, int G> static hipError_t moe_t(const MoeArgs &a, int cu, hipS
     up.g.early = a.T <= up.g.rows && up.g.sp.chunk >= (a.H + 255) / 256;   // all of x at once
     dn.g.early = a.T == 1 && dn.g.by_pair;
     if (up.lds > MOE_LDS || dn.lds > MOE_LDS) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((moe_router_kernel<T>), dim3((uint32_t)(a.E + 15) / 16, (uint32_t)(a.T + 15) / 16), dim3(64 * ROUTER_WAVES), 0, s, a);
-    if (up.g.early) hipLaunchKernelGGL((moe_up_kernel<T, G, true>), dim3(up.x, slots), block, up.lds, s, a, up.g);
-    else hipLaunchKernelGGL((moe_up_kernel<T, G, false>), dim3(up.x, slots), block, up.lds, s, a, up.g);
+    const bool route = up.g.early && a.E <= 16 && a.T <= 16 && a.E * a.H <= 65536;
+    if (!route) hipLaunchKernelGGL((moe_router_kernel<T>), dim3((uint32_t)(a.E + 15) / 16, (uint32_t)(a.T + 15) / 16), dim3(64 * ROUTER_WAVES), 0, s, a);
+    if (route) hipLaunchKernelGGL((moe_up_kernel<T, G, true, true>), dim3(up.x, slots), block, up.lds, s, a, up.g);
+    else if (up.g.early) hipLaunchKernelGGL((moe_up_kernel<T, G, true, false>), dim3(up.x, slots), block, up.lds, s, a, up.g);
+    else hipLaunchKernelGGL((moe_up_kernel<T, G, false, false>), dim3(up.x, slots), block, up.lds, s, a, up.g);
     if (dn.g.early) hipLaunchKernelGGL((moe_down_kernel<T, G, true>), dim3(dn.x, slots), block, dn.lds, s, a, dn.g);
     else hipLaunchKernelGGL((moe_down_kernel<T, G, false>), dim3(dn.x, slots), block, dn.lds, s, a, dn.g);
     hipLaunchKernelGGL((moe_combine_kernel<T>), dim3((uint32_t)(a.H + 4 * COMBINE_THREADS - 1) / (4 * COMBINE_THREADS), (uint32_t)a.T),
