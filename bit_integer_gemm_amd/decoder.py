@@ -1,10 +1,12 @@
-"""The attention half of a decoder layer in low bits, as a server runs it: int8 projections of
-floating activations, a paged cache of 4-bit keys and values, attention over the cache.
+"""A decoder layer in low bits, as a server runs it.  Its attention half: int8 projections of
+floating activations, a paged cache of 4-bit keys and values, attention over the cache.  The whole
+layer, around the same cache and attention: norms with the residual, rotary positions, an output
+projection with 4-bit weights, a mixture of experts of 4-bit weights.
 
     python -m bit_integer_gemm_amd.decoder
 
-runs prompts of several lengths and then single tokens (one captured graph, replayed) through a
-layer of random weights, checks the outputs against the formulas in 64 bits, and prints the times.
+runs prompts of several lengths and then single tokens (one captured graph, replayed) through both,
+with random weights, checks the outputs against the formulas in 64 bits, and prints the times.
 """
 import math
 import time
@@ -146,17 +148,26 @@ def run(hidden=4096, heads=32, kv_heads=8, D=128, prompts=(777, 1, 130, 600), st
     return prefill, clock(step, 50), clock(graph.replay, 50)
 
 
+def projection(name, got, want, bias):
+    """One rounding of the output, and fp32 scales, product and bias before it."""
+    eps, tiny = torch.finfo(got.dtype).eps, torch.finfo(got.dtype).tiny
+    bound = eps / 2 * (want.abs() + tiny) + 2 ** -21 * ((want - bias).abs() + bias.abs())
+    assert ((got.cpu().double() - want).abs() <= bound).all(), name
+
+
 def check(layer, cache, b, n, x, qkv, mixed, out):
     """One call's projections, cache and attention of sequence b against the formulas, each from what the step before
     it left."""
+    H, D, T = layer.heads, layer.D, x.shape[0]
+    check_middle(layer, cache, b, n, x, qkv, qkv, mixed)
+    projection("output projection", out, linear(mixed.reshape(T, H * D), layer.o, layer.o_s), torch.zeros(1).double())
+
+
+def check_middle(layer, cache, b, n, x, projected, qkv, mixed):
+    """The projection of x, and the cache and attention of qkv, which are its queries, keys and values, turned or not."""
     H, G, D = layer.heads, layer.kv_heads, layer.D
     T, eps, tiny = x.shape[0], torch.finfo(x.dtype).eps, torch.finfo(x.dtype).tiny
-    for name, got, want, bias in (
-            ("projection", qkv, linear(x, layer.qkv, layer.qkv_s, layer.bias), layer.bias.cpu().double()),
-            ("output projection", out, linear(mixed.reshape(T, H * D), layer.o, layer.o_s), torch.zeros(1).double())):
-        # one rounding of the output, and fp32 scales, product and bias before it
-        bound = eps / 2 * (want.abs() + tiny) + 2 ** -21 * ((want - bias).abs() + bias.abs())
-        assert ((got.cpu().double() - want).abs() <= bound).all(), name
+    projection("projection", projected, linear(x, layer.qkv, layer.qkv_s, layer.bias), layer.bias.cpu().double())
     K, V, largest = held(cache, b, n)
     kv = qkv.view(T, H + 2 * G, D)[:, H:].cpu().double()
     for new, kept in ((kv[:, :G], K[n - T:]), (kv[:, G:], V[n - T:])):
@@ -173,6 +184,171 @@ def check(layer, cache, b, n, x, qkv, mixed, out):
     assert ((mixed.cpu().double() - want).abs() <= bound).all(), "attention"
 
 
+def levels4(w, group, dtype, device):
+    """Weights (..., N, K) in 4 bits: packed levels, (scale, minimum) of each group of a row, and what they stand for."""
+    g = w.unflatten(-1, (w.shape[-1] // group, group))
+    low = g.amin(-1, keepdim=True).to(dtype)
+    scale = ((g.amax(-1, keepdim=True) - low.float()) / 15).to(dtype)
+    u = ((g - low.float()) / scale.float().clamp(min=1e-30)).round().clamp(0, 15)
+    value = (u.double() * scale.double() + low.double()).flatten(-2)
+    u = u.to(torch.uint8).flatten(-2)
+    return (u[..., 0::2] | (u[..., 1::2] << 4)).to(device), torch.cat([scale, low], -1).to(device), value
+
+
+class Layer:
+    """r += W_o attention(rope(W_qkv norm(r))), r += post-norm of experts(norm(r)): r, the residual stream, in fp32."""
+
+    def __init__(self, hidden, heads, kv_heads, D, experts=8, top_k=2, wide=256, group=64, dtype=torch.bfloat16,
+                 device="cuda", seed=0):
+        self.attention = Attention(hidden, heads, kv_heads, D, dtype, device, seed)
+        self.heads, self.kv_heads, self.D, self.top_k = heads, kv_heads, D, top_k
+        g = torch.Generator().manual_seed(seed + 1)
+
+        def normal(*shape, std=1.0):
+            return torch.randn(*shape, generator=g) * std
+
+        self.o, self.o_p, self.o_value = levels4(normal(hidden, heads * D, std=(heads * D) ** -0.5), group, dtype, device)
+        self.up, self.up_p, self.up_value = levels4(normal(experts, 2 * wide, hidden, std=hidden ** -0.5), group, dtype, device)
+        self.down, self.down_p, self.down_value = levels4(normal(experts, hidden, wide, std=wide ** -0.5), group, dtype, device)
+        self.router = normal(experts, hidden, std=2 * hidden ** -0.5).to(dtype).to(device)
+        self.before, self.between, self.after = ((1 + normal(hidden, std=0.2)).to(dtype).to(device) for _ in range(3))
+        self.freqs, self.mult = lb.lb_rope_freqs(D, scaling="parts", factor=4.0, before=4096.0, device=device)
+
+    def __call__(self, r, cache, seq, pos, q_off, lens, max_q, max_len):
+        """r (T, hidden) fp32, updated in place; the rest as for Attention.  Returns what each step left."""
+        T, H, G, D, dtype, dev = r.shape[0], self.heads, self.kv_heads, self.D, self.before.dtype, r.device
+        r0 = r.clone()   # (for the check)
+        x = torch.empty(r.shape, dtype=dtype, device=dev)
+        lb.lb_residual_norm(None, r, None, x, w=self.before)
+        qkv = torch.empty(T, self.attention.qkv.shape[0], dtype=dtype, device=dev)
+        lb.lb_linear_w8a8(x, self.attention.qkv, self.attention.qkv_s, qkv, bias=self.attention.bias)
+        straight = qkv.clone()
+        q, k, v = qkv.view(T, H + 2 * G, D).split((H, G, G), 1)
+        lb.lb_rope(q, k, pos, self.freqs, q, k, mult=self.mult)   # where they lie
+        lb.lb_kv4_write(k, v, cache.slots(seq, pos), *cache.tensors)
+        mixed = torch.empty(T, H, D, dtype=dtype, device=dev)
+        lb.lb_attn_kv4(q, *cache.tensors, cache.table, q_off, lens, mixed, max_q=max_q, max_len=max_len)
+        out = torch.empty_like(x)
+        lb.lb_linear_w4(mixed.view(T, H * D), self.o, self.o_p, out)
+        y = torch.empty_like(x)
+        lb.lb_residual_norm(out, r, r, y, w=self.between)
+        r1 = r.clone()
+        z, ids = torch.empty_like(x), torch.empty(T, self.top_k, dtype=torch.int32, device=dev)
+        lb.lb_moe_w4(y, self.router, self.up, self.up_p, self.down, self.down_p, z, top_k=self.top_k, renorm=True, ids=ids)
+        lb.lb_residual_norm(z, r, r, None, post_w=self.after)
+        return r0, x, straight, qkv, mixed, out, r1, y, ids, z, r.clone()
+
+
+EPS = 1e-5   # of the norms, lb_residual_norm's default
+STEP = 2.0 ** -24
+
+
+def near(name, got, want, before):
+    """One rounding of the output, and `before` ahead of it."""
+    eps, tiny = torch.finfo(got.dtype).eps, torch.finfo(got.dtype).tiny
+    bound = eps / 2 * (want.abs() + before + tiny) + before
+    assert ((got.cpu().double() - want).abs() <= bound).all(), name
+
+
+def norm(v, w):
+    return v / (v.square().mean(-1, keepdim=True) + EPS).sqrt() * w.cpu().double()
+
+
+def product4(x, value):
+    """x W^T in 64 bits, and how far fp32 sums over 16 + u in place of u may be off: a few hundred roundings of sums of
+    at most eight times the largest weight's products."""
+    return x @ value.T, 400 * STEP * 8 * x.abs().sum(-1, keepdim=True) * value.abs().max()
+
+
+def check_layer(layer, cache, b, n, pos, r0, x, straight, qkv, mixed, out, r1, y, ids, z, r2):
+    """One call's steps for sequence b against the formulas, each from what the step before it left."""
+    H, G, D = layer.heads, layer.kv_heads, layer.D
+    T, att = x.shape[0], layer.attention
+    r, d = r0.cpu().double(), lambda a: a.cpu().double()
+    near("norm", x, norm(r, layer.before), 40 * STEP * norm(r, layer.before).abs())
+    # queries and keys turned; the values as they were
+    angle = d(pos)[:, None] * layer.freqs.cpu()
+    c, s = (angle.cos() * layer.mult)[:, None], (angle.sin() * layer.mult)[:, None]
+    before = d(straight).view(T, H + 2 * G, D)
+    e, o = before[:, :H + G, :D // 2], before[:, :H + G, D // 2:]
+    size = torch.cat([e.abs() + o.abs()] * 2, -1)
+    after = qkv.view(T, H + 2 * G, D)
+    near("rotary positions", after[:, :H + G], torch.cat([e * c - o * s, o * c + e * s], -1), 16 * STEP * layer.mult * size)
+    assert torch.equal(after[:, H + G:], straight.view(T, H + 2 * G, D)[:, H + G:]), "values"
+    # projection, cache and attention
+    check_middle(att, cache, b, n, x, straight, qkv, mixed)
+    want, off = product4(d(mixed).reshape(T, H * D), layer.o_value)
+    near("output projection", out, want, off)
+    want = r + d(out)
+    near("residual", r1, want, STEP * want.abs())
+    near("norm between", y, norm(want, layer.between), 40 * STEP * norm(want, layer.between).abs() + 2 * STEP)
+    # experts: those that fp32 logits choose (two closer than their error could change places)
+    yd = d(y)
+    p = torch.softmax(yd @ d(layer.router).T, -1)
+    chosen = ids.cpu().long()
+    weight = p.gather(1, chosen)
+    assert (weight.min(1).values >= p.topk(layer.top_k).values[:, -1] * (1 - 1e-4)).all(), "experts"
+    weight = weight / weight.sum(1, keepdim=True)
+    want, off = torch.zeros_like(yd), torch.zeros_like(yd)
+    for t in range(T):
+        for j, e in enumerate(chosen[t].tolist()):
+            u, du = product4(yd[t:t + 1], layer.up_value[e])
+            gate, lift = u.chunk(2, -1)
+            h = gate * torch.sigmoid(gate) * lift
+            dh = 1.1 * du * (lift.abs() + gate.abs() + du) + 2 ** -16 * h.abs()
+            v, dv = product4(h, layer.down_value[e])
+            want[t] += weight[t, j] * v[0]
+            off[t] += weight[t, j] * (dv + dh @ layer.down_value[e].abs().T + 1e-4 * v.abs())[0]
+    near("experts", z, want, off)
+    want = d(r1) + norm(d(z), layer.after)
+    near("residual after", r2, want, 40 * STEP * (want - d(r1)).abs() + STEP * want.abs())
+
+
+def run_layer(hidden=4096, heads=32, kv_heads=8, D=128, experts=16, top_k=2, wide=1408, group=128, prompts=(100, 1, 30),
+              steps=4, dtype=torch.bfloat16):
+    """The whole layer: prompts, then `steps` single tokens of every sequence as a replayed graph; the times in us."""
+    dev = torch.device("cuda")
+    B, longest = len(prompts), max(prompts) + steps
+    layer = Layer(hidden, heads, kv_heads, D, experts, top_k, wide, group, dtype, dev)
+    cache = Pages(B, longest, kv_heads, D, dtype=dtype, device=dev)
+    g = torch.Generator().manual_seed(3)
+    start = torch.randn(sum(prompts), hidden, generator=g).to(dev)
+    off = torch.tensor([0, *prompts]).cumsum(0)
+    seq = torch.arange(B).repeat_interleave(torch.tensor(prompts)).to(dev)
+    pos = torch.cat([torch.arange(n) for n in prompts]).to(dev)
+    lens = torch.tensor(prompts, dtype=torch.int32, device=dev)
+    args = (cache, seq, pos, off.to(torch.int32).to(dev), lens, max(prompts), longest)
+    left = layer(start.clone(), *args)
+    for b, n in enumerate(prompts):
+        check_layer(layer, cache, b, n, pos[off[b]:off[b + 1]], *(a[off[b]:off[b + 1]] for a in left))
+    prefill = clock(lambda: layer(start.clone(), *args), 10)
+
+    one = torch.empty(B, hidden, device=dev)
+    every, each = torch.arange(B, device=dev), torch.arange(B + 1, dtype=torch.int32, device=dev)
+
+    def step():
+        return layer(one, cache, every, lens.long() - 1, each, lens, 1, longest)
+
+    one.copy_(torch.randn(B, hidden, generator=g))
+    lens.add_(1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):   # the first step, outside the graph
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        left = step()
+    for i in range(steps):
+        one.copy_(torch.randn(B, hidden, generator=g))
+        if i:
+            lens.add_(1)
+        graph.replay()
+        for b, n in enumerate(prompts):
+            check_layer(layer, cache, b, n + i + 1, lens[b:b + 1] - 1, *(a[b:b + 1] for a in left))
+    return prefill, clock(step, 20), clock(graph.replay, 20)
+
+
 def clock(f, n):
     """Microseconds a call, once the GPU is warm."""
     for _ in range(3):
@@ -186,5 +362,6 @@ def clock(f, n):
 
 
 if __name__ == "__main__":
-    prefill, eager, replayed = run()
-    print(f"outputs agree; prompts {prefill:.0f} us, single tokens {eager:.0f} us, as a graph {replayed:.0f} us")
+    for name, f in (("attention half", run), ("whole layer", run_layer)):
+        prefill, eager, replayed = f()
+        print(f"{name}: outputs agree; prompts {prefill:.0f} us, single tokens {eager:.0f} us, as a graph {replayed:.0f} us")
