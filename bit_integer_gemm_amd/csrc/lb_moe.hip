@@ -37,7 +37,7 @@ template <class T, int NW> __device__ inline float router_tile(const MoeArgs &a,
     const T *wrow = (const T *)a.wr + (int64_t)min(e0 + r, a.E - 1) * a.H;
     const T *xrow = (const T *)a.x + (int64_t)min(t0 + r, a.T - 1) * a.ldx;
     const int32_t steps = a.H / 32, last = (wave + 1) * steps / NW;
-    f32x4 acc[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     for (int32_t st = wave * steps / NW; st < last; st += ROUTER_STEPS) {
         u32x4 x[ROUTER_STEPS], w[ROUTER_STEPS];
 #pragma unroll
@@ -49,9 +49,9 @@ template <class T, int NW> __device__ inline float router_tile(const MoeArgs &a,
             }
         }
 #pragma unroll
-        for (int i = 0; i < ROUTER_STEPS; ++i) acc[0] = mfma16<T>(x[i], w[i], acc[0]);
+        for (int i = 0; i < ROUTER_STEPS; ++i) acc = mfma16<T>(x[i], w[i], acc);
     }
-    w4_put<1>(sums + wave * ROUTER_TILE, 16, acc, false);
+    w4_put(sums + wave * ROUTER_TILE, 16, acc, false);
     __syncthreads();
     float v = 0.f;
     if (threadIdx.x < 256)
@@ -74,7 +74,7 @@ __global__ __launch_bounds__(64 * ROUTER_WAVES) void moe_router_kernel(MoeArgs a
 // (token, rank) pairs where those are fewer; of pairs that name the same expert the first
 // one's workgroups work for all its tokens, the others end.
 enum { EXPERTS_MAX = 1024 };
-enum { MOE_LIST = 2 + MOE_TOKENS };   // in the workspace: count, expert, rows
+enum { MOE_LIST = 2 + MOE_TOKENS };   // in the workspace: count, expert, rows (one token: count, expert, row, logit)
 struct MoeList {
     int32_t rank[MOE_TOKENS];   // the expert's rank in each token's order, if below k, else -1
     int32_t row[MOE_TOKENS];    // token * k + rank of each of its tokens
@@ -254,7 +254,7 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGri
     };
     int32_t expert = 0;
     auto tile_at = [&](int32_t t) { return W4Tile{((int64_t)expert * 2 + t % 2) * a.I + (b0 + mine + t / 2) * 16, 16}; };
-    W4Flow<T, T, 1, G, 1, decltype(tile_at)> flow(smem, g.x_bytes, a.w1, (const uint32_t *)a.p1, a.H, g.sp,
+    W4Flow<T, T, G, 1, decltype(tile_at)> flow(smem, g.x_bytes, a.w1, (const uint32_t *)a.p1, a.H, g.sp,
                                                   2 * max(0, min(each, have - mine)), tile_at);
     const i32x4 rx = make_rsrc(a.x, 0xFFFFFFF0u);
     if constexpr (EARLY) flow.ask_x(0, a.T, rx, [&](int32_t i) { return (uint32_t)i * (uint32_t)a.ldx * 2u; });
@@ -276,6 +276,7 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGri
     }));
     if (blockIdx.x == 0) {   // for the down product
         int32_t *const l = a.lists + blockIdx.y * MOE_LIST;
+        if (a.T == 1 && threadIdx.x == 66) l[3] = (int32_t)__float_as_uint(logits[expert]);
         if (threadIdx.x < (uint32_t)count) l[2 + threadIdx.x] = list.row[threadIdx.x];
         if (threadIdx.x == 64) l[0] = count;
         if (threadIdx.x == 65) l[1] = expert;
@@ -284,17 +285,17 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGri
     for (int32_t at = 0; at < count; at += g.rows) {
         const int32_t rows = EARLY ? a.T : min(g.rows, count - at), slot = rows * W4_SLOT_LD;
         const bool direct = kw == 1 && g.sp.chunk >= lines;   // a wave has whole sums
-        f32x4 gate[1];
+        f32x4 gate = {0.f, 0.f, 0.f, 0.f};
         auto x_at = [&](int32_t i) { return (uint32_t)(list.row[at + i] / a.top_k) * (uint32_t)a.ldx * 2u; };
-        auto done = [&](int32_t t, const f32x4(&acc)[1], bool more) {
+        auto done = [&](int32_t t, const f32x4 &acc, bool more) {
             if (!direct) {
-                w4_put<1>(slots + (wave * 2 * each + t) * slot, rows, acc, more);
+                w4_put(slots + (wave * 2 * each + t) * slot, rows, acc, more);
             } else if (t % 2 == 0) {
-                gate[0] = acc[0];
+                gate = acc;
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (4 * q + i < rows) put(at + 4 * q + i, (mine + t / 2) * 16 + r, gate[0][i], acc[0][i]);
+                    if (4 * q + i < rows) put(at + 4 * q + i, (mine + t / 2) * 16 + r, gate[i], acc[i]);
             }
         };
         if (at == 0) {
@@ -321,7 +322,7 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGri
 }
 
 // ---- down ------------------------------------------------------------------
-template <class T, int G, bool EARLY>
+template <class T, int G>
 __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_kernel(MoeArgs a, MoeGrid g)
 {
     extern __shared__ __attribute__((aligned(1024))) char smem[];
@@ -335,11 +336,9 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_kernel(MoeArgs a, MoeG
     const uint32_t plane = (uint32_t)(a.T * a.top_k) * (uint32_t)a.I * 2u;
     int32_t expert = 0;
     auto tile_at = [&](int32_t t) { return W4Tile{(int64_t)expert * a.H + (t0 + mine + t) * 16, 16}; };
-    W4Flow<__bf16, T, 1, G, 2, decltype(tile_at)> flow(smem, g.x_bytes, a.w2, (const uint32_t *)a.p2, a.I, g.sp,
+    W4Flow<__bf16, T, G, 2, decltype(tile_at)> flow(smem, g.x_bytes, a.w2, (const uint32_t *)a.p2, a.I, g.sp,
                                                        max(0, min(each, have - mine)), tile_at);
     const i32x4 rx = make_rsrc(a.h, 0xFFFFFFF0u);
-    if constexpr (EARLY)   // (one token: slot j's row is j)
-        flow.ask_x(0, 2, rx, [&](int32_t i) { return blockIdx.y * (uint32_t)a.I * 2u + (i ? plane : 0u); });
     const int32_t *const l = a.lists + blockIdx.y * MOE_LIST;
     const int32_t count = l[0];
     expert = l[1];
@@ -357,18 +356,18 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_kernel(MoeArgs a, MoeG
             const int32_t second = i >= rows;
             return (uint32_t)list.row[at + i - (second ? rows : 0)] * (uint32_t)a.I * 2u + (second ? plane : 0u);
         };
-        auto done = [&](int32_t t, const f32x4(&acc)[1], bool more) {
+        auto done = [&](int32_t t, const f32x4 &acc, bool more) {
             if (!direct) {
-                w4_put<1>(slots + (wave * each + t) * slot, rows, acc, more);
+                w4_put(slots + (wave * each + t) * slot, rows, acc, more);
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (4 * q + i < rows) a.y[(int64_t)list.row[at + 4 * q + i] * a.H + (t0 + mine + t) * 16 + r] = acc[0][i];
+                    if (4 * q + i < rows) a.y[(int64_t)list.row[at + 4 * q + i] * a.H + (t0 + mine + t) * 16 + r] = acc[i];
             }
         };
         if (at == 0) {
-            flow.template run<true, EARLY>(rows, rx, x_at, done);
-        } else if constexpr (!EARLY) {
+            flow.template run<true, false>(rows, rx, x_at, done);
+        } else {
             __syncthreads();
             flow.template run<false, false>(rows, rx, x_at, done);
         }
@@ -382,7 +381,68 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_kernel(MoeArgs a, MoeG
                 a.y[(int64_t)list.row[at + m] * a.H + t0 * 16 + c] = v;
             }
         }
-        if constexpr (EARLY) return;
+    }
+}
+
+// One token: a workgroup's columns get all of its experts' sums, weighted here, one expert's lines
+// after the other's, and no launch follows.
+template <class T, int G>
+__global__ __launch_bounds__(64 * W4_WAVES) void moe_down_token_kernel(MoeArgs a, MoeGrid g)
+{
+    extern __shared__ __attribute__((aligned(1024))) char smem[];
+    const int32_t lane = (int32_t)(threadIdx.x & 63u), k = a.top_k;
+    const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int32_t kw = g.sp.kw, each = g.sp.each;
+    const int32_t per = W4_WAVES / kw * each, t0 = (int32_t)blockIdx.x * per, have = min(per, a.H / 16 - t0);
+    const int32_t mine = wave / kw * each, tiles = max(0, min(each, have - mine));
+    float *const slots = (float *)(smem + g.x_bytes + W4Lds<G>::RINGS);
+    int32_t expert = 0, row = 0;   // of slot `lane`
+    auto tile_at = [&](int32_t t) {
+        const int32_t j = t / max(tiles, 1), e = __builtin_amdgcn_readlane(expert, j);
+        return W4Tile{(int64_t)e * a.H + (t0 + mine + t - j * tiles) * 16, 16};
+    };
+    W4Flow<__bf16, T, G, 2, decltype(tile_at)> flow(smem, g.x_bytes, a.w2, (const uint32_t *)a.p2, a.I, g.sp, k * tiles, tile_at);
+    const i32x4 rx = make_rsrc(a.h, 0xFFFFFFF0u);
+    auto x_at = [&](int32_t i) { return (uint32_t)i * (uint32_t)a.I * 2u; };   // (the planes follow each other)
+    flow.ask_x(0, 2 * k, rx, x_at);
+    const int32_t *const l = a.lists + min(lane, k - 1) * MOE_LIST;
+    expert = l[1];
+    row = l[2];
+    const float logit = __uint_as_float((uint32_t)l[3]);
+    // the sum of all experts' exponentials, or of the chosen ones'; any NaN or infinity spoils it
+    const float other = !a.renorm ? a.logits[min(lane, a.E - 1)] : 0.f;
+    flow.start();
+    float largest = logit;
+#pragma unroll
+    for (int d = 32; d; d >>= 1) largest = fmaxf(largest, __shfl_xor(largest, d));
+    const float own = expf(logit - largest);
+    float total = lane < k ? own : 0.f;
+    if (!a.renorm) {
+        total = lane < a.E ? expf(other - largest) : 0.f;
+        for (int32_t e = lane + 64; e < a.E; e += 64) total += expf(a.logits[e] - largest);
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) total += __shfl_xor(total, d);
+    const float weight = a.scale * (own / total);
+    if (blockIdx.x == 0 && wave == 0 && lane < k) {
+        if (a.ids) a.ids[row] = expert;
+        if (a.weights) a.weights[row] = weight;
+    }
+    flow.template run<true, true, true>(
+        k, rx, x_at,
+        [&](int32_t t, const f32x4 &acc, bool) {
+            const int32_t j = t / tiles;
+            const float p = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(weight), j));
+            w4_put(slots + (wave * each + t - j * tiles) * W4_SLOT_LD, 1, acc * p, j > 0);
+        },
+        [&](int32_t t) { return __builtin_amdgcn_readlane(row, t / tiles); });
+    __syncthreads();
+    for (int32_t c = (int32_t)threadIdx.x; c < have * 16; c += 64 * W4_WAVES) {
+        const int32_t t = c / 16;
+        const float *s = slots + (t / each * kw * each + t % each) * W4_SLOT_LD + c % 16;
+        float v = 0.f;
+        for (int32_t i = 0; i < kw; ++i) v += s[i * each * W4_SLOT_LD];
+        ((T *)a.out)[t0 * 16 + c] = (T)v;
     }
 }
 
@@ -491,15 +551,28 @@ template <class T, int G> static hipError_t moe_t(const MoeArgs &a, int cu, hipS
     const dim3 block(64 * W4_WAVES);
     MoeShape up = moe_shape<G>(a, a.I / 16, a.H, 1, 2, slots, cu), dn = moe_shape<G>(a, a.H / 16, a.I, 2, 1, slots, cu);
     up.g.early = a.T <= up.g.rows && up.g.sp.chunk >= (a.H + 255) / 256;   // all of x at once
-    dn.g.early = a.T == 1 && dn.g.by_pair;
+    // one token: all of its experts' activations in LDS, or each expert for itself
+    MoeShape one = dn;
+    if (a.T == 1) {
+        const int64_t tiles = a.H / 16, lines = (a.I + 255) / 256;
+        one.g.sp = w4_split((tiles + cu - 1) / cu, lines, 1, MOE_LDS);
+        const int64_t wide = (int64_t)(W4_WAVES / one.g.sp.kw) * one.g.sp.each;
+        one.g.x_bytes = W4Lds<G>::x_bytes(2 * a.top_k, (int32_t)lines);
+        one.x = (uint32_t)((tiles + wide - 1) / wide);
+        one.lds = one.g.x_bytes + W4Lds<G>::RINGS + (uint32_t)(W4_WAVES * one.g.sp.each * W4_SLOT_LD * 4);
+        one.g.early = one.g.sp.chunk >= lines && one.lds <= MOE_LDS;
+    }
     if (up.lds > MOE_LDS || dn.lds > MOE_LDS) return hipErrorInvalidValue;
     const bool route = up.g.early && a.E <= 16 && a.T <= 16 && a.E * a.H <= 65536;
     if (!route) hipLaunchKernelGGL((moe_router_kernel<T>), dim3((uint32_t)(a.E + 15) / 16, (uint32_t)(a.T + 15) / 16), dim3(64 * ROUTER_WAVES), 0, s, a);
     if (route) hipLaunchKernelGGL((moe_up_kernel<T, G, true, true>), dim3(up.x, slots), block, up.lds, s, a, up.g);
     else if (up.g.early) hipLaunchKernelGGL((moe_up_kernel<T, G, true, false>), dim3(up.x, slots), block, up.lds, s, a, up.g);
     else hipLaunchKernelGGL((moe_up_kernel<T, G, false, false>), dim3(up.x, slots), block, up.lds, s, a, up.g);
-    if (dn.g.early) hipLaunchKernelGGL((moe_down_kernel<T, G, true>), dim3(dn.x, slots), block, dn.lds, s, a, dn.g);
-    else hipLaunchKernelGGL((moe_down_kernel<T, G, false>), dim3(dn.x, slots), block, dn.lds, s, a, dn.g);
+    if (a.T == 1 && one.g.early) {
+        hipLaunchKernelGGL((moe_down_token_kernel<T, G>), dim3(one.x), block, one.lds, s, a, one.g);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL((moe_down_kernel<T, G>), dim3(dn.x, slots), block, dn.lds, s, a, dn.g);
     hipLaunchKernelGGL((moe_combine_kernel<T>), dim3((uint32_t)(a.H + 4 * COMBINE_THREADS - 1) / (4 * COMBINE_THREADS), (uint32_t)a.T),
                        dim3(COMBINE_THREADS), 0, s, a);
     return hipGetLastError();

@@ -6,7 +6,7 @@
 
 namespace lb {
 
-// Few rows: a workgroup takes 16 MT rows of x against some tiles of 16 columns (W4Split).
+// Up to 16 rows: a workgroup takes all of x against some tiles of 16 columns (W4Split).
 // EARLY: weights are asked for before x (a row or two of x are there before the first weights).
 struct FewArgs {
     const uint8_t *w;
@@ -14,30 +14,25 @@ struct FewArgs {
     int64_t ldx;
     int32_t M, N, K;
     W4Split sp;
-    uint32_t tiles_m, tiles_n;   // workgroups
 };
-template <class T, int MT, int G, bool EARLY>
+template <class T, int G, bool EARLY>
 __global__ __launch_bounds__(64 * W4_WAVES) void w4_few_kernel(const T *__restrict__ X, const T *__restrict__ bias,
                                                                   T *__restrict__ out, FewArgs a)
 {
     extern __shared__ __attribute__((aligned(1024))) char smem[];
-    const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    uint32_t tm, tn;
-    tile_of_block(blockIdx.x, a.tiles_m, a.tiles_n, 4u, tm, tn);
-    const int32_t m0 = (int32_t)tm * 16 * MT, rows = min(16 * MT, a.M - m0);
+    const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), rows = a.M;
     const int32_t kw = a.sp.kw, each = a.sp.each;
-    const int32_t per = W4_WAVES / kw * each, t0 = (int32_t)tn * per;   // the workgroup's tiles
+    const int32_t per = W4_WAVES / kw * each, t0 = (int32_t)blockIdx.x * per;   // the workgroup's tiles
     const int32_t have = min(per, (a.N + 15) / 16 - t0), mine = wave / kw * each;
     float *const slots = (float *)(smem + W4Lds<G>::x_bytes(rows, a.sp.chunk) + W4Lds<G>::RINGS);
     const int32_t slot = rows * W4_SLOT_LD;
     auto tile_at = [&](int32_t t) { return W4Tile{(int64_t)(t0 + mine + t) * 16, min(16, a.N - (t0 + mine + t) * 16)}; };
-    W4Flow<T, T, MT, G, 1, decltype(tile_at)> flow(smem, W4Lds<G>::x_bytes(rows, a.sp.chunk), a.w, a.p, a.K, a.sp,
-                                                   max(0, min(each, have - mine)), tile_at);
+    W4Flow<T, T, G, 1, decltype(tile_at)> flow(smem, W4Lds<G>::x_bytes(rows, a.sp.chunk), a.w, a.p, a.K, a.sp,
+                                               max(0, min(each, have - mine)), tile_at);
     if constexpr (EARLY) flow.start();
     flow.template run<EARLY, false>(
-        rows, make_rsrc(X + (int64_t)m0 * a.ldx, 0xFFFFFFF0u),
-        [&](int32_t row) { return (uint32_t)row * (uint32_t)a.ldx * 2u; },
-        [&](int32_t t, const f32x4(&acc)[MT], bool more) { w4_put<MT>(slots + (wave * each + t) * slot, rows, acc, more); });
+        rows, make_rsrc(X, 0xFFFFFFF0u), [&](int32_t row) { return (uint32_t)row * (uint32_t)a.ldx * 2u; },
+        [&](int32_t t, const f32x4 &acc, bool more) { w4_put(slots + (wave * each + t) * slot, rows, acc, more); });
     __syncthreads();
     for (int32_t i = (int32_t)threadIdx.x; i < rows * have * 16; i += 64 * W4_WAVES) {
         const int32_t m = i / (have * 16), c = i - m * have * 16, t = c / 16, n = t0 * 16 + c;
@@ -47,40 +42,28 @@ __global__ __launch_bounds__(64 * W4_WAVES) void w4_few_kernel(const T *__restri
         float v = 0.f;
         for (int32_t k = 0; k < kw; ++k) v += s[k * each * slot];
         if (bias) v += (float)bias[n];
-        out[(int64_t)(m0 + m) * a.N + n] = (T)v;
+        out[(int64_t)m * a.N + n] = (T)v;
     }
 }
 
 enum { FEW_LDS = 160 * 1024 };
-template <class T, int MT, int G> static hipError_t w4_few_t(const W4Args &a, int cu, hipStream_t s)
-{
-    const int64_t rows = a.M < 16 * MT ? a.M : 16 * MT, passes = (a.M + 16 * MT - 1) / (16 * MT);
-    const int64_t tiles = (a.N + 15) / 16, lines = (a.K + 255) / 256;
-    int64_t per = (tiles * passes + cu - 1) / cu;
-    const int64_t slot = rows * W4_SLOT_LD * 4, room = 24 * 1024 / (W4_WAVES * slot);
-    if (per > room) per = room > 1 ? room : 1;
-    const W4Split sp = w4_split(per, lines, rows, FEW_LDS - 4096 - W4Lds<G>::RINGS - W4_WAVES * per * slot);
-    const int64_t wide = (int64_t)(W4_WAVES / sp.kw) * sp.each, tn = (tiles + wide - 1) / wide;
-    const int64_t most = LAUNCH_THREADS / (64 * W4_WAVES) / tn * 16 * MT;   // rows of one launch
-    const uint32_t lds = W4Lds<G>::x_bytes((int32_t)rows, sp.chunk) + W4Lds<G>::RINGS + (uint32_t)(W4_WAVES * sp.each * slot);
-    if (most < 16 * MT || lds > FEW_LDS) return hipErrorInvalidValue;
-    for (int64_t m = 0; m < a.M; m += most) {
-        const int64_t here = a.M - m < most ? a.M - m : most, tm = (here + 16 * MT - 1) / (16 * MT);
-        const FewArgs f{a.w, (const uint32_t *)a.p, a.ldx, (int32_t)here, (int32_t)a.N, (int32_t)a.K, sp, (uint32_t)tm, (uint32_t)tn};
-        const dim3 grid((uint32_t)(tm * tn)), block(64 * W4_WAVES);
-        const T *x = (const T *)a.x + m * a.ldx;
-        T *out = (T *)a.out + m * a.N;
-        if (rows > 2) hipLaunchKernelGGL((w4_few_kernel<T, MT, G, true>), grid, block, lds, s, x, (const T *)a.bias, out, f);
-        else hipLaunchKernelGGL((w4_few_kernel<T, MT, G, false>), grid, block, lds, s, x, (const T *)a.bias, out, f);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
-}
-
 template <class T, int G> static hipError_t w4_g(const W4Args &a, int cu, hipStream_t s)
 {
-    return w4_few_t<T, 1, G>(a, cu, s);
+    const int64_t tiles = (a.N + 15) / 16, lines = (a.K + 255) / 256;
+    // a workgroup to a compute unit, if its sums find room
+    int64_t per = (tiles + cu - 1) / cu;
+    const int64_t slot = a.M * W4_SLOT_LD * 4, room = 24 * 1024 / (W4_WAVES * slot);
+    if (per > room) per = room > 1 ? room : 1;
+    const W4Split sp = w4_split(per, lines, a.M, FEW_LDS - 4096 - W4Lds<G>::RINGS - W4_WAVES * per * slot);
+    const int64_t wide = (int64_t)(W4_WAVES / sp.kw) * sp.each, wgs = (tiles + wide - 1) / wide;
+    const uint32_t lds = W4Lds<G>::x_bytes((int32_t)a.M, sp.chunk) + W4Lds<G>::RINGS + (uint32_t)(W4_WAVES * sp.each * slot);
+    if (a.M > W4_FEW_ROWS || wgs * 64 * W4_WAVES > LAUNCH_THREADS || lds > FEW_LDS) return hipErrorInvalidValue;
+    const FewArgs f{a.w, (const uint32_t *)a.p, a.ldx, (int32_t)a.M, (int32_t)a.N, (int32_t)a.K, sp};
+    const dim3 grid((uint32_t)wgs), block(64 * W4_WAVES);
+    const T *x = (const T *)a.x, *bias = (const T *)a.bias;
+    if (a.M > 2) hipLaunchKernelGGL((w4_few_kernel<T, G, true>), grid, block, lds, s, x, bias, (T *)a.out, f);
+    else hipLaunchKernelGGL((w4_few_kernel<T, G, false>), grid, block, lds, s, x, bias, (T *)a.out, f);
+    return hipGetLastError();
 }
 
 template <class T> static hipError_t w4_t(const W4Args &a, int group, int cu, hipStream_t s)

@@ -144,14 +144,14 @@ __device__ inline void w4_copy4(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32
 
 template <int N> __device__ inline void w4_wait() { asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory"); }
 
-// The products of a wave's tiles: 16 MT rows of x at most by 16 columns each.
+// The products of a wave's tiles: 16 rows of x at most by 16 columns each.
 //   lds: x (x_bytes of it; PLANES 2: x is the sum of two planes, whose rows follow each other),
 //     then the rings.  Copies of two lines are under way while a third is worked on; each
 //     wave waits for its own by count.
 //   tiles: this wave's; tile_at(t): a W4Tile.
 //   T: the type of x as the matrix cores take it; PT: of the groups' numbers.
 // Every wave of a workgroup makes the same calls, also one without tiles (x is copied by all).
-template <class T, class PT, int MT, int G, int PLANES, class TileAt>
+template <class T, class PT, int G, int PLANES, class TileAt>
 struct W4Flow {
     typedef W4Lds<G> L;
     enum : int { GROUPS = L::GROUPS, STEPS = G / 32 };
@@ -279,11 +279,16 @@ struct W4Flow {
     // `rows` rows of x through rx, row i's first byte at x_at(i) (PLANES 2: rows from `rows` on are
     // the second plane's).  STARTED: start() has been called, and the weights' latency runs beside
     // the copy of x; else start() comes after it, and beside the putting in order.  ASKED: ask_x()
-    // has been called, before start().
+    // has been called, before start().  ROW_OF: each tile has one row of x to itself, row_of(tile).
     //   done(t, acc, more): sums of tile t over this wave's lines of a chunk, more: not the first
-    //     chunk's; acc[m][i] is row 4 (lane / 16) + i of 16 rows m, column lane % 16.
+    //     chunk's; acc[i] is row 4 (lane / 16) + i, column lane % 16.
     template <bool STARTED, bool ASKED, class XAt, class Done>
     __device__ inline void run(int32_t rows, const i32x4 rx, XAt &&x_at, Done &&done)
+    {
+        run<STARTED, ASKED, false>(rows, rx, x_at, done, [](int32_t) { return 0; });
+    }
+    template <bool STARTED, bool ASKED, bool ROW_OF, class XAt, class Done, class RowOf>
+    __device__ inline void run(int32_t rows, const i32x4 rx, XAt &&x_at, Done &&done, RowOf &&row_of)
     {
         const int32_t q = lane >> 4, r = lane & 15, xrows = PLANES * rows;
         if constexpr (!ASKED) ask_x(0, xrows, rx, x_at);
@@ -304,28 +309,28 @@ struct W4Flow {
             int32_t lo, hi;
             bounds(c, lo, hi);
             // what a lane reads of x: its row's pieces j of a line's first half, any row's where it has none
-            uint32_t xa[4][MT][PLANES];
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
+            uint32_t xa[4][PLANES];
+            auto aim_x = [&](int32_t first) {
 #pragma unroll
                 for (int pl = 0; pl < PLANES; ++pl) {
-                    const uint32_t row = (uint32_t)(min(16 * m + r, rows - 1) + pl * rows);
+                    const uint32_t row = (uint32_t)(first + pl * rows);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        xa[j][m][pl] = row * (uint32_t)min(sp.chunk, lines - c) * 512u +
-                                       16u * ((uint32_t)(G == 128 ? 4 * q + j : 4 * j + q) ^ (row & 15u));
+                        xa[j][pl] = row * (uint32_t)min(sp.chunk, lines - c) * 512u +
+                                    16u * ((uint32_t)(G == 128 ? 4 * q + j : 4 * j + q) ^ (row & 15u));
                 }
+            };
+            if constexpr (!ROW_OF) aim_x(min(r, rows - 1));
             if (lo == hi && c) continue;
             for (int32_t tile = 0; tile < tiles; ++tile) {   // (without lines: sums of zero)
-                f32x4 acc[MT];
-#pragma unroll
-                for (int m = 0; m < MT; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if constexpr (ROW_OF) aim_x(row_of(tile));
+                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
                 for (int32_t line = lo; line < hi; ++line) {
                     copy();
                     w4_wait<(L::DEPTH - 1) * L::COPIES>();
                     // everything that the line needs from LDS at once: one latency
                     const char *st = ring + at;
-                    u32x4 w[2], x[8][MT][PLANES];
+                    u32x4 w[2], x[8][PLANES];
                     uint32_t num[GROUPS];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) w[h] = *(const u32x4 *)(st + 128 * r + 16 * ((4 * h + q) ^ (r >> 1)));
@@ -335,10 +340,7 @@ struct W4Flow {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
 #pragma unroll
-                        for (int m = 0; m < MT; ++m)
-#pragma unroll
-                            for (int pl = 0; pl < PLANES; ++pl)
-                                x[j][m][pl] = *(const u32x4 *)(xl + xa[j % 4][m][pl] + 256 * (j / 4));
+                        for (int pl = 0; pl < PLANES; ++pl) x[j][pl] = *(const u32x4 *)(xl + xa[j % 4][pl] + 256 * (j / 4));
                     __builtin_amdgcn_sched_barrier(0);
                     if constexpr (G != 128) {
                         w4_transpose(w[0]);
@@ -346,30 +348,24 @@ struct W4Flow {
                     }
 #pragma unroll
                     for (int g = 0; g < GROUPS; ++g) {
-                        f32x4 sum[MT], xs[MT];
-#pragma unroll
-                        for (int m = 0; m < MT; ++m) sum[m] = xs[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+                        f32x4 sum = {0.f, 0.f, 0.f, 0.f}, xs = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                         for (int j = g * STEPS; j < (g + 1) * STEPS; ++j) {   // 32 weights
                             const u32x4 lv = w4_levels<T>(w[j / 4][j % 4], konst);
                             const uint32_t one = one_pair<T>();
 #pragma unroll
-                            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                                for (int pl = 0; pl < PLANES; ++pl) {
-                                    // (x's own sum too: forming it beside the ordering of x takes longer)
-                                    xs[m] = mfma16<T>(x[j][m][pl], u32x4{one, one, one, one}, xs[m]);
-                                    sum[m] = mfma16<T>(x[j][m][pl], lv, sum[m]);
-                                }
+                            for (int pl = 0; pl < PLANES; ++pl) {
+                                // (x's own sum too: forming it beside the ordering of x takes longer)
+                                xs = mfma16<T>(x[j][pl], u32x4{one, one, one, one}, xs);
+                                sum = mfma16<T>(x[j][pl], lv, sum);
+                            }
                         }
                         const float s = lo_f32<PT>(num[g]), b = hi_f32<PT>(num[g]) - 16.0f * s;
 #pragma unroll
-                        for (int m = 0; m < MT; ++m)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                acc[m][i] = __builtin_fmaf(s, sum[m][i], acc[m][i]);
-                                acc[m][i] = __builtin_fmaf(b, xs[m][i], acc[m][i]);
-                            }
+                        for (int i = 0; i < 4; ++i) {
+                            acc[i] = __builtin_fmaf(s, sum[i], acc[i]);
+                            acc[i] = __builtin_fmaf(b, xs[i], acc[i]);
+                        }
                     }
                     // the next copies overwrite what has been read here
                     asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
@@ -385,20 +381,18 @@ struct W4Flow {
     __device__ inline void finish() { w4_wait<0>(); }
 };
 
-// A wave's sums into LDS, or (more) onto what it left there: `rows` rows of x by 16 columns, rows 20 floats apart (a lane's four rows lie
-// on other banks).
+// A wave's sums into LDS, or (more) onto what it left there: `rows` rows of x by 16 columns, rows
+// 20 floats apart (a lane's four rows lie on other banks).
 enum { W4_SLOT_LD = 20 };
-template <int MT> __device__ inline void w4_put(float *slot, int32_t rows, const f32x4 (&acc)[MT], bool more)
+__device__ inline void w4_put(float *slot, int32_t rows, const f32x4 &acc, bool more)
 {
     const int lane = (int)(threadIdx.x & 63u), q = lane >> 4, r = lane & 15;
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (16 * m + 4 * q + i < rows) {
-                float *s = slot + (16 * m + 4 * q + i) * W4_SLOT_LD + r;
-                *s = more ? *s + acc[m][i] : acc[m][i];
-            }
+    for (int i = 0; i < 4; ++i)
+        if (4 * q + i < rows) {
+            float *s = slot + (4 * q + i) * W4_SLOT_LD + r;
+            *s = more ? *s + acc[i] : acc[i];
+        }
 }
 
 // The split of `tiles` tiles of `lines` lines, x in chunks of at most x_bytes: about the fewest lines

@@ -275,8 +275,14 @@ LINEAR = [(1, 1, 32, 32), (1, 16, 128, 128), (1, 4096, 512, 64), (1, 333, 4096, 
           (130, 515, 1024, 64), (331, 200, 2048, 128), (700, 1025, 544, 32), (513, 260, 4096, 128)]
 
 
+# tiles of each size with whole and odd ends, whole rounds beside a rest of columns, rows in parts of a long K
+LINEAR_WIDE = [(600, 9000, 256, 128), (601, 8999, 160, 32), (1030, 8193, 128, 64), (1030, 8200, 320, 64), (1000, 4001, 2048, 128),
+               (1000, 4000, 1952, 32), (3000, 2816, 256, 32), (40, 300, 8192, 128), (1, 40, 65536, 128), (2, 5, 131072, 32),
+               (16, 130, 11008, 64), (14, 20000, 96, 32), (1, 70000, 64, 64)]
+
+
 @pytest.mark.parametrize("dtype", [BF, HF])
-@pytest.mark.parametrize("M,N,K,group", LINEAR)
+@pytest.mark.parametrize("M,N,K,group", LINEAR + LINEAR_WIDE)
 def test_linear_w4(dtype, M, N, K, group):
     g = gen(M * 3 + N)
     x = (torch.randn(M, K, generator=g) * (1 + 20 * (torch.rand(K, generator=g) < 0.02))).to(dtype)
@@ -533,3 +539,63 @@ def test_streams_and_graphs(which):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(o, w) for o, w in zip(outs, want[i])), (name, i)
+
+
+def test_graphs_share_a_workspace():
+    """Two graphs of one workspace, replayed in turn: what the eager calls give."""
+    g = gen(11)
+    ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    made = []
+    for T, M in ((1, 40), (9, 300)):
+        x = torch.randn(T, 256, generator=g).to(BF).cuda()
+        big = torch.randn(M, 512, generator=g).to(BF).cuda()
+        w, p, _ = weights((), 200, 512, 64, BF, g)
+        w, p = w.cuda(), p.cuda()
+        wr, up, down = experts(16, 256, 128, 64, BF, g)
+        moe = [a.cuda() for a in (wr, up[0], up[1], down[0], down[1])]
+        out, many = torch.empty_like(x), torch.empty(M, 200, dtype=BF, device="cuda")
+
+        def call(x=x, moe=moe, out=out, big=big, w=w, p=p, many=many):
+            lb.lb_moe_w4(x, *moe, out, top_k=3, workspace=ws)
+            lb.lb_linear_w4(big, w, p, many, workspace=ws)
+
+        call()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        made.append((x, big, out, many, call, graph))
+    for i in range(4):
+        want = []
+        for x, big, out, many, call, _ in made:
+            x.mul_(-1.5)
+            big.add_(0.25)
+            call()
+            want.append((out.clone(), many.clone()))
+            out.zero_()
+            many.zero_()
+        for *_, graph in made:
+            graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w[0]) and torch.equal(m, w[1]) for (_, _, o, m, _, _), w in zip(made, want)), i
+
+
+def test_two_streams_at_once():
+    """The same weights used on two streams, each with a workspace of its own."""
+    g = gen(12)
+    wr, up, down = experts(32, 512, 256, 64, BF, g)
+    moe = [a.cuda() for a in (wr, up[0], up[1], down[0], down[1])]
+    xs = [torch.randn(n, 512, generator=g).to(BF).cuda() for n in (7, 40)]
+    want = []
+    for x in xs:
+        out = torch.empty_like(x)
+        lb.lb_moe_w4(x, *moe, out, top_k=4)
+        want.append(out)
+    streams = [torch.cuda.Stream() for _ in xs]
+    ws = [torch.empty(lb.lb_moe_w4_workspace(x.shape[0], 512, 256, 32, 4), dtype=torch.uint8, device="cuda") for x in xs]
+    outs = [torch.empty_like(x) for x in xs]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for x, o, w, s in zip(xs, outs, ws, streams):
+            lb.lb_moe_w4(x, *moe, o, top_k=4, workspace=w, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
