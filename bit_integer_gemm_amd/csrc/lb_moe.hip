@@ -247,14 +247,15 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGri
         }
         // (a quotient and an exponential good to 2^-21)
         const float h = gate / (1.0f + __expf(-gate)) * up;
-        const int64_t o = (int64_t)row * a.I + b0 * 16 + c;
+        // in the order in which the down product's nibbles come
+        const int64_t o = (int64_t)row * a.I + b0 * 16 + (c & ~7) + 2 * (c & 3) + (c >> 2 & 1);
         const __bf16 top = (__bf16)h;
         hi[o] = top;
         lo[o] = (__bf16)(h - (float)top);
     };
     int32_t expert = 0;
     auto tile_at = [&](int32_t t) { return W4Tile{((int64_t)expert * 2 + t % 2) * a.I + (b0 + mine + t / 2) * 16, 16}; };
-    W4Flow<T, T, G, 1, decltype(tile_at)> flow(smem, g.x_bytes, a.w1, (const uint32_t *)a.p1, a.H, g.sp,
+    W4Flow<T, T, G, 1, false, decltype(tile_at)> flow(smem, g.x_bytes, a.w1, (const uint32_t *)a.p1, a.H, g.sp,
                                                   2 * max(0, min(each, have - mine)), tile_at);
     const i32x4 rx = make_rsrc(a.x, 0xFFFFFFF0u);
     if constexpr (EARLY) flow.ask_x(0, a.T, rx, [&](int32_t i) { return (uint32_t)i * (uint32_t)a.ldx * 2u; });
@@ -336,7 +337,7 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_kernel(MoeArgs a, MoeG
     const uint32_t plane = (uint32_t)(a.T * a.top_k) * (uint32_t)a.I * 2u;
     int32_t expert = 0;
     auto tile_at = [&](int32_t t) { return W4Tile{(int64_t)expert * a.H + (t0 + mine + t) * 16, 16}; };
-    W4Flow<__bf16, T, G, 2, decltype(tile_at)> flow(smem, g.x_bytes, a.w2, (const uint32_t *)a.p2, a.I, g.sp,
+    W4Flow<__bf16, T, G, 2, false, decltype(tile_at)> flow(smem, g.x_bytes, a.w2, (const uint32_t *)a.p2, a.I, g.sp,
                                                        max(0, min(each, have - mine)), tile_at);
     const i32x4 rx = make_rsrc(a.h, 0xFFFFFFF0u);
     const int32_t *const l = a.lists + blockIdx.y * MOE_LIST;
@@ -401,10 +402,9 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_token_kernel(MoeArgs a
         const int32_t j = t / max(tiles, 1), e = __builtin_amdgcn_readlane(expert, j);
         return W4Tile{(int64_t)e * a.H + (t0 + mine + t - j * tiles) * 16, 16};
     };
-    W4Flow<__bf16, T, G, 2, decltype(tile_at)> flow(smem, g.x_bytes, a.w2, (const uint32_t *)a.p2, a.I, g.sp, k * tiles, tile_at);
+    W4Flow<__bf16, T, G, 2, true, decltype(tile_at)> flow(smem, g.x_bytes, a.w2, (const uint32_t *)a.p2, a.I, g.sp, k * tiles, tile_at, k);
     const i32x4 rx = make_rsrc(a.h, 0xFFFFFFF0u);
     auto x_at = [&](int32_t i) { return (uint32_t)i * (uint32_t)a.I * 2u; };   // (the planes follow each other)
-    flow.ask_x(0, 2 * k, rx, x_at);
     const int32_t *const l = a.lists + min(lane, k - 1) * MOE_LIST;
     expert = l[1];
     row = l[2];
@@ -428,7 +428,7 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_token_kernel(MoeArgs a
         if (a.ids) a.ids[row] = expert;
         if (a.weights) a.weights[row] = weight;
     }
-    flow.template run<true, true, true>(
+    flow.template run<true, false>(
         k, rx, x_at,
         [&](int32_t t, const f32x4 &acc, bool) {
             const int32_t j = t / tiles;
@@ -555,12 +555,13 @@ template <class T, int G> static hipError_t moe_t(const MoeArgs &a, int cu, hipS
     MoeShape one = dn;
     if (a.T == 1) {
         const int64_t tiles = a.H / 16, lines = (a.I + 255) / 256;
-        one.g.sp = w4_split((tiles + cu - 1) / cu, lines, 1, MOE_LDS);
+        one.g.sp = w4_split((tiles + cu - 1) / cu, lines * a.top_k, 1, INT32_MAX);
+        one.g.sp.chunk = (int32_t)lines;
         const int64_t wide = (int64_t)(W4_WAVES / one.g.sp.kw) * one.g.sp.each;
         one.g.x_bytes = W4Lds<G>::x_bytes(2 * a.top_k, (int32_t)lines);
         one.x = (uint32_t)((tiles + wide - 1) / wide);
         one.lds = one.g.x_bytes + W4Lds<G>::RINGS + (uint32_t)(W4_WAVES * one.g.sp.each * W4_SLOT_LD * 4);
-        one.g.early = one.g.sp.chunk >= lines && one.lds <= MOE_LDS;
+        one.g.early = one.lds <= MOE_LDS;
     }
     if (up.lds > MOE_LDS || dn.lds > MOE_LDS) return hipErrorInvalidValue;
     const bool route = up.g.early && a.E <= 16 && a.T <= 16 && a.E * a.H <= 65536;

@@ -27,7 +27,7 @@ __global__ __launch_bounds__(64 * W4_WAVES) void w4_few_kernel(const T *__restri
     float *const slots = (float *)(smem + W4Lds<G>::x_bytes(rows, a.sp.chunk) + W4Lds<G>::RINGS);
     const int32_t slot = rows * W4_SLOT_LD;
     auto tile_at = [&](int32_t t) { return W4Tile{(int64_t)(t0 + mine + t) * 16, min(16, a.N - (t0 + mine + t) * 16)}; };
-    W4Flow<T, T, G, 1, decltype(tile_at)> flow(smem, W4Lds<G>::x_bytes(rows, a.sp.chunk), a.w, a.p, a.K, a.sp,
+    W4Flow<T, T, G, 1, false, decltype(tile_at)> flow(smem, W4Lds<G>::x_bytes(rows, a.sp.chunk), a.w, a.p, a.K, a.sp,
                                                max(0, min(each, have - mine)), tile_at);
     if constexpr (EARLY) flow.start();
     flow.template run<EARLY, false>(

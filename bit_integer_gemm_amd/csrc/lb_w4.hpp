@@ -145,13 +145,15 @@ __device__ inline void w4_copy4(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32
 template <int N> __device__ inline void w4_wait() { asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory"); }
 
 // The products of a wave's tiles: 16 rows of x at most by 16 columns each.
-//   lds: x (x_bytes of it; PLANES 2: x is the sum of two planes, whose rows follow each other),
-//     then the rings.  Copies of two lines are under way while a third is worked on; each
-//     wave waits for its own by count.
+//   lds: x (x_bytes of it), then the rings.  Copies of two lines are under way while a third is
+//     worked on; each wave waits for its own by count.
+//   PLANES 2: x is the sum of two planes, whose rows follow each other, in order in memory.
+//   SEGMENTS: the tiles are `segments` times the same columns with other weights, each time with
+//     one other row of x (row_of(tile)); the waves share all their lines together.  One chunk.
 //   tiles: this wave's; tile_at(t): a W4Tile.
 //   T: the type of x as the matrix cores take it; PT: of the groups' numbers.
 // Every wave of a workgroup makes the same calls, also one without tiles (x is copied by all).
-template <class T, class PT, int G, int PLANES, class TileAt>
+template <class T, class PT, int G, int PLANES, bool SEGMENTS, class TileAt>
 struct W4Flow {
     typedef W4Lds<G> L;
     enum : int { GROUPS = L::GROUPS, STEPS = G / 32 };
@@ -161,7 +163,7 @@ struct W4Flow {
     const int32_t K, lines, tiles;
     const W4Split sp;
     const TileAt tile_at;
-    const int32_t lane, wave, share;
+    const int32_t lane, wave, share, segments;
     const uint32_t kb, groups;
     char *const ring;
     // what is copied next
@@ -172,19 +174,34 @@ struct W4Flow {
     uint32_t w_at[2], p_at[L::COPIES - 2];   // of a lane in a line of 16 rows of weights, of their numbers
 
     __device__ inline W4Flow(char *lds_, uint32_t x_bytes, const uint8_t *W_, const uint32_t *P_, int32_t K_, const W4Split &sp_,
-                             int32_t tiles_, const TileAt &at_)
+                             int32_t tiles_, const TileAt &at_, int32_t segments_ = 1)
         : lds(lds_), W(W_), P(P_), K(K_), lines((K_ + 255) / 256), tiles(tiles_), sp(sp_), tile_at(at_),
-          lane((int32_t)(threadIdx.x & 63u)), wave(__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6))), share(wave % sp_.kw),
+          lane((int32_t)(threadIdx.x & 63u)), wave(__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6))), share(wave % sp_.kw), segments(segments_),
           kb((uint32_t)K_ / 2u), groups((uint32_t)K_ / G), ring(lds_ + x_bytes + wave * L::RING)
     {
     }
 
-    // Lines of the chunk from line c on that are this wave's.
-    __device__ inline void bounds(int32_t c, int32_t &lo, int32_t &hi) const
+    // Lines of the chunk from line c on, for a tile, that are this wave's.
+    __device__ inline void bounds(int32_t c, int32_t tile, int32_t &lo, int32_t &hi) const
     {
-        const int32_t n = min(sp.chunk, lines - c);
-        lo = c + n * share / sp.kw;
-        hi = c + n * (share + 1) / sp.kw;
+        if constexpr (SEGMENTS) {
+            const int32_t all = lines * segments, before = tile / max(tiles / segments, 1) * lines;
+            lo = min(max(all * share / sp.kw - before, 0), lines);
+            hi = min(max(all * (share + 1) / sp.kw - before, 0), lines);
+        } else {
+            const int32_t n = min(sp.chunk, lines - c);
+            lo = c + n * share / sp.kw;
+            hi = c + n * (share + 1) / sp.kw;
+        }
+    }
+    // The tile that is copied next: SEGMENTS: the first from c_tile on of which this wave has lines.
+    __device__ inline void next_tile()
+    {
+        for (left = false; c_tile < tiles && !left; c_tile += !left) {
+            bounds(c_chunk, c_tile, c_lo, c_hi);
+            left = c_lo < c_hi;
+        }
+        c_line = c_lo;
     }
     __device__ inline void aim()
     {
@@ -212,16 +229,21 @@ struct W4Flow {
             c_at -= L::RING;
         }
         if (left && ++c_line == c_hi) {
-            if (++c_tile == tiles) {
-                c_tile = 0;
-                c_chunk += sp.chunk;
-                left = c_chunk < lines;
-                if (left) {
-                    bounds(c_chunk, c_lo, c_hi);
-                    left = c_lo < c_hi;   // (a last chunk of fewer lines than shares)
+            ++c_tile;
+            if constexpr (SEGMENTS) {
+                next_tile();
+            } else {
+                if (c_tile == tiles) {
+                    c_tile = 0;
+                    c_chunk += sp.chunk;
+                    left = c_chunk < lines;
+                    if (left) {
+                        bounds(c_chunk, 0, c_lo, c_hi);
+                        left = c_lo < c_hi;   // (a last chunk of fewer lines than shares)
+                    }
                 }
+                c_line = c_lo;
             }
-            c_line = c_lo;
             if (left) aim();
             else rw.z = rp.z = 0;
         }
@@ -229,10 +251,14 @@ struct W4Flow {
     // Asks for the first lines.
     __device__ inline void start()
     {
-        c_chunk = c_tile = 0;
-        bounds(0, c_lo, c_hi);
-        c_line = c_lo;
-        left = tiles > 0 && c_lo < c_hi;   // (no lines: only where there is one chunk)
+        c_chunk = c_tile = c_lo = 0;
+        if constexpr (SEGMENTS) {
+            next_tile();
+        } else {
+            bounds(0, 0, c_lo, c_hi);
+            c_line = c_lo;
+            left = tiles > 0 && c_lo < c_hi;   // (no lines: only where there is one chunk)
+        }
         if (left) aim();
         else rw = rp = make_rsrc(W, 0);
         c_at = lds_addr(ring);
@@ -262,6 +288,10 @@ struct W4Flow {
     }
     __device__ inline void order_x(int32_t c, int32_t xrows)   // each lane what it copied itself
     {
+        if constexpr (PLANES == 2) {
+            __syncthreads();
+            return;
+        }
         constexpr int AT_ONCE = 4;
         const int32_t all = min(sp.chunk, lines - c) * 32 * xrows;
         u32x4 *const p = (u32x4 *)lds;
@@ -279,15 +309,15 @@ struct W4Flow {
     // `rows` rows of x through rx, row i's first byte at x_at(i) (PLANES 2: rows from `rows` on are
     // the second plane's).  STARTED: start() has been called, and the weights' latency runs beside
     // the copy of x; else start() comes after it, and beside the putting in order.  ASKED: ask_x()
-    // has been called, before start().  ROW_OF: each tile has one row of x to itself, row_of(tile).
+    // has been called, before start().
     //   done(t, acc, more): sums of tile t over this wave's lines of a chunk, more: not the first
     //     chunk's; acc[i] is row 4 (lane / 16) + i, column lane % 16.
     template <bool STARTED, bool ASKED, class XAt, class Done>
     __device__ inline void run(int32_t rows, const i32x4 rx, XAt &&x_at, Done &&done)
     {
-        run<STARTED, ASKED, false>(rows, rx, x_at, done, [](int32_t) { return 0; });
+        run<STARTED, ASKED>(rows, rx, x_at, done, [](int32_t) { return 0; });
     }
-    template <bool STARTED, bool ASKED, bool ROW_OF, class XAt, class Done, class RowOf>
+    template <bool STARTED, bool ASKED, class XAt, class Done, class RowOf>
     __device__ inline void run(int32_t rows, const i32x4 rx, XAt &&x_at, Done &&done, RowOf &&row_of)
     {
         const int32_t q = lane >> 4, r = lane & 15, xrows = PLANES * rows;
@@ -307,7 +337,7 @@ struct W4Flow {
                 order_x(c, xrows);
             }
             int32_t lo, hi;
-            bounds(c, lo, hi);
+            bounds(c, 0, lo, hi);
             // what a lane reads of x: its row's pieces j of a line's first half, any row's where it has none
             uint32_t xa[4][PLANES];
             auto aim_x = [&](int32_t first) {
@@ -320,10 +350,13 @@ struct W4Flow {
                                     16u * ((uint32_t)(G == 128 ? 4 * q + j : 4 * j + q) ^ (row & 15u));
                 }
             };
-            if constexpr (!ROW_OF) aim_x(min(r, rows - 1));
+            if constexpr (!SEGMENTS) aim_x(min(r, rows - 1));
             if (lo == hi && c) continue;
             for (int32_t tile = 0; tile < tiles; ++tile) {   // (without lines: sums of zero)
-                if constexpr (ROW_OF) aim_x(row_of(tile));
+                if constexpr (SEGMENTS) {
+                    aim_x(row_of(tile));
+                    bounds(c, tile, lo, hi);
+                }
                 f32x4 acc = {0.f, 0.f, 0.f, 0.f};
                 for (int32_t line = lo; line < hi; ++line) {
                     copy();
