@@ -35,7 +35,7 @@ template <class T, int NW> __device__ inline float router_tile(const MoeArgs &a,
     const int32_t lane = (int32_t)(threadIdx.x & 63u), q = lane >> 4, r = lane & 15;
     const int32_t wave = (int32_t)(threadIdx.x >> 6);
     const T *wrow = (const T *)a.wr + (int64_t)min(e0 + r, a.E - 1) * a.H;
-    const T *xrow = (const T *)a.x + (int64_t)min(t0 + r, a.T - 1) * a.ldx;
+    const T *xrow = (const T *)a.x + (int64_t)min(t0 + 4 * (r & 3) + (r >> 2), a.T - 1) * a.ldx;   // (as w4_put has them)
     const int32_t steps = a.H / 32, last = (wave + 1) * steps / NW;
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     for (int32_t st = wave * steps / NW; st < last; st += ROUTER_STEPS) {
@@ -296,7 +296,7 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGri
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (4 * q + i < rows) put(at + 4 * q + i, (mine + t / 2) * 16 + r, gate[i], acc[i]);
+                    if (4 * i + q < rows) put(at + 4 * i + q, (mine + t / 2) * 16 + r, gate[i], acc[i]);
             }
         };
         if (at == 0) {
@@ -363,7 +363,7 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_kernel(MoeArgs a, MoeG
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (4 * q + i < rows) a.y[(int64_t)list.row[at + 4 * q + i] * a.H + (t0 + mine + t) * 16 + r] = acc[i];
+                    if (4 * i + q < rows) a.y[(int64_t)list.row[at + 4 * i + q] * a.H + (t0 + mine + t) * 16 + r] = acc[i];
             }
         };
         if (at == 0) {
@@ -428,7 +428,7 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_token_kernel(MoeArgs a
         if (a.ids) a.ids[row] = expert;
         if (a.weights) a.weights[row] = weight;
     }
-    flow.template run<true, false>(
+    flow.template run_n<1, true, false>(
         k, rx, x_at,
         [&](int32_t t, const f32x4 &acc, bool) {
             const int32_t j = t / tiles;

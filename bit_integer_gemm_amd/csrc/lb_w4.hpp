@@ -311,15 +311,23 @@ struct W4Flow {
     // the copy of x; else start() comes after it, and beside the putting in order.  ASKED: ask_x()
     // has been called, before start().
     //   done(t, acc, more): sums of tile t over this wave's lines of a chunk, more: not the first
-    //     chunk's; acc[i] is row 4 (lane / 16) + i, column lane % 16.
+    //     chunk's; acc[i] is row 4 i + lane / 16, column lane % 16.
     template <bool STARTED, bool ASKED, class XAt, class Done>
     __device__ inline void run(int32_t rows, const i32x4 rx, XAt &&x_at, Done &&done)
     {
-        run<STARTED, ASKED>(rows, rx, x_at, done, [](int32_t) { return 0; });
+        auto none = [](int32_t) { return 0; };
+        if (rows <= 4) run_n<1, STARTED, ASKED>(rows, rx, x_at, done, none);
+        else if (rows <= 8) run_n<2, STARTED, ASKED>(rows, rx, x_at, done, none);
+        else run_n<4, STARTED, ASKED>(rows, rx, x_at, done, none);
     }
-    template <bool STARTED, bool ASKED, class XAt, class Done, class RowOf>
-    __device__ inline void run(int32_t rows, const i32x4 rx, XAt &&x_at, Done &&done, RowOf &&row_of)
+    // RO: at most 4 RO rows.  A matrix instruction's row 4 q + i, whose sums are in lanes q of register
+    // i, takes row 4 i + q, so that few rows need few registers scaled.  Two planes of at most 8 rows
+    // are rows of one instruction, the second plane's sums RO registers behind the first's.
+    template <int RO, bool STARTED, bool ASKED, class XAt, class Done, class RowOf>
+    __device__ inline void run_n(int32_t rows, const i32x4 rx, XAt &&x_at, Done &&done, RowOf &&row_of)
     {
+        constexpr bool STACK = PLANES == 2 && RO < 4;
+        constexpr int PL = STACK ? 1 : PLANES, RI = STACK ? 2 * RO : RO;
         const int32_t q = lane >> 4, r = lane & 15, xrows = PLANES * rows;
         if constexpr (!ASKED) ask_x(0, xrows, rx, x_at);
         if constexpr (!STARTED) start();
@@ -339,18 +347,18 @@ struct W4Flow {
             int32_t lo, hi;
             bounds(c, 0, lo, hi);
             // what a lane reads of x: its row's pieces j of a line's first half, any row's where it has none
-            uint32_t xa[4][PLANES];
+            uint32_t xa[4][PL];
             auto aim_x = [&](int32_t first) {
 #pragma unroll
-                for (int pl = 0; pl < PLANES; ++pl) {
-                    const uint32_t row = (uint32_t)(first + pl * rows);
+                for (int pl = 0; pl < PL; ++pl) {
+                    const uint32_t row = (uint32_t)(first + (STACK ? min((r & 3) / RO, 1) : pl) * rows);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         xa[j][pl] = row * (uint32_t)min(sp.chunk, lines - c) * 512u +
                                     16u * ((uint32_t)(G == 128 ? 4 * q + j : 4 * j + q) ^ (row & 15u));
                 }
             };
-            if constexpr (!SEGMENTS) aim_x(min(r, rows - 1));
+            if constexpr (!SEGMENTS) aim_x(min((STACK ? (r & 3) % RO : r & 3) * 4 + (r >> 2), rows - 1));
             if (lo == hi && c) continue;
             for (int32_t tile = 0; tile < tiles; ++tile) {   // (without lines: sums of zero)
                 if constexpr (SEGMENTS) {
@@ -363,7 +371,7 @@ struct W4Flow {
                     w4_wait<(L::DEPTH - 1) * L::COPIES>();
                     // everything that the line needs from LDS at once: one latency
                     const char *st = ring + at;
-                    u32x4 w[2], x[8][PLANES];
+                    u32x4 w[2], x[8][PL];
                     uint32_t num[GROUPS];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) w[h] = *(const u32x4 *)(st + 128 * r + 16 * ((4 * h + q) ^ (r >> 1)));
@@ -373,7 +381,7 @@ struct W4Flow {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
 #pragma unroll
-                        for (int pl = 0; pl < PLANES; ++pl) x[j][pl] = *(const u32x4 *)(xl + xa[j % 4][pl] + 256 * (j / 4));
+                        for (int pl = 0; pl < PL; ++pl) x[j][pl] = *(const u32x4 *)(xl + xa[j % 4][pl] + 256 * (j / 4));
                     __builtin_amdgcn_sched_barrier(0);
                     if constexpr (G != 128) {
                         w4_transpose(w[0]);
@@ -387,7 +395,7 @@ struct W4Flow {
                             const u32x4 lv = w4_levels<T>(w[j / 4][j % 4], konst);
                             const uint32_t one = one_pair<T>();
 #pragma unroll
-                            for (int pl = 0; pl < PLANES; ++pl) {
+                            for (int pl = 0; pl < PL; ++pl) {
                                 // (x's own sum too: forming it beside the ordering of x takes longer)
                                 xs = mfma16<T>(x[j][pl], u32x4{one, one, one, one}, xs);
                                 sum = mfma16<T>(x[j][pl], lv, sum);
@@ -395,7 +403,7 @@ struct W4Flow {
                         }
                         const float s = lo_f32<PT>(num[g]), b = hi_f32<PT>(num[g]) - 16.0f * s;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < RI; ++i) {
                             acc[i] = __builtin_fmaf(s, sum[i], acc[i]);
                             acc[i] = __builtin_fmaf(b, xs[i], acc[i]);
                         }
@@ -405,6 +413,9 @@ struct W4Flow {
                     at += L::STAGE;
                     if (++slot == L::DEPTH) slot = at = 0;
                 }
+                if constexpr (STACK)
+#pragma unroll
+                    for (int i = 0; i < RO; ++i) acc[i] += acc[RO + i];
                 done(tile, acc, c > 0);
             }
         }
@@ -414,16 +425,15 @@ struct W4Flow {
     __device__ inline void finish() { w4_wait<0>(); }
 };
 
-// A wave's sums into LDS, or (more) onto what it left there: `rows` rows of x by 16 columns, rows
-// 20 floats apart (a lane's four rows lie on other banks).
-enum { W4_SLOT_LD = 20 };
+// A wave's sums into LDS, or (more) onto what it left there: `rows` rows of x by 16 columns.
+enum { W4_SLOT_LD = 16 };
 __device__ inline void w4_put(float *slot, int32_t rows, const f32x4 &acc, bool more)
 {
     const int lane = (int)(threadIdx.x & 63u), q = lane >> 4, r = lane & 15;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (4 * q + i < rows) {
-            float *s = slot + (4 * q + i) * W4_SLOT_LD + r;
+        if (4 * i + q < rows) {
+            float *s = slot + (4 * i + q) * W4_SLOT_LD + r;
             *s = more ? *s + acc[i] : acc[i];
         }
 }
