@@ -183,6 +183,7 @@ struct MoeArgs {
     int32_t renorm;
     float scale;
     float *logits;     // workspace: T x E
+    int32_t *found;    // how many experts have tokens
     int32_t *lists;    // and 2 + MOE_TOKENS for each expert or (token, rank) pair
     void *h;           // two planes of T top_k x I, bf16
     float *y;          // T top_k x H

@@ -65,7 +65,7 @@ MoeSpace moe_space(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k)
     const int64_t tokens = std::min<int64_t>(T, lb::MOE_TOKENS);
     MoeSpace m;
     m.lists = round_up(tokens * E * 4, 256);   // (the logits come first)
-    m.h = m.lists + round_up(std::min(tokens * top_k, E) * (2 + lb::MOE_TOKENS) * 4, 256);
+    m.h = m.lists + round_up((1 + std::min(tokens * top_k, E) * (2 + lb::MOE_TOKENS)) * 4, 256);
     m.y = m.h + round_up(tokens * top_k * I * 4, 256);
     m.bytes = m.y + round_up(tokens * top_k * H * 4, 256);
     return m;
@@ -255,7 +255,8 @@ int lb_moe_w4(const void *X, int64_t ldx, const void *Wr, const uint8_t *W1, con
         a.renorm = renorm != 0;
         a.scale = scale;
         a.logits = (float *)workspace;
-        a.lists = (int32_t *)((char *)workspace + m.lists);
+        a.found = (int32_t *)((char *)workspace + m.lists);
+        a.lists = a.found + 1;
         a.h = (char *)workspace + m.h;
         a.y = (float *)((char *)workspace + m.y);
         const hipError_t e = lb::launch_moe_w4(ftype, (int)group, a, cu, (hipStream_t)stream);

@@ -70,44 +70,68 @@ __global__ __launch_bounds__(64 * ROUTER_WAVES) void moe_router_kernel(MoeArgs a
 }
 
 // ---- who goes where --------------------------------------------------------
-// The expert of a workgroup and its tokens.  Slots are experts where tokens are many, and
-// (token, rank) pairs where those are fewer; of pairs that name the same expert the first
-// one's workgroups work for all its tokens, the others end.
+// Workgroups are shared out evenly among the experts that have tokens: each workgroup finds
+// these from the logits (or, where there are three pairs of a token and an expert for every
+// expert and few are without, shares them out among all).  With 5 tokens of 6 of 64 experts
+// about 24 are found where there could be 30, and the products take 10 us less of 58.
 enum { EXPERTS_MAX = 1024 };
 enum { MOE_LIST = 2 + MOE_TOKENS };   // in the workspace: count, expert, rows (one token: count, expert, row, logit)
 struct MoeList {
     int32_t rank[MOE_TOKENS];   // the expert's rank in each token's order, if below k, else -1
     int32_t row[MOE_TOKENS];    // token * k + rank of each of its tokens
+    uint32_t any[EXPERTS_MAX / 32];   // experts that have tokens, a bit each
     float logits[256];          // where a workgroup forms them itself: 16 experts, 16 tokens
 };
 
 // Number j (from 0) in a token's order of its logits, by every wave for itself: lane l holds
-// logits l, l + 64, ...; the value bit by bit from the top, by counting those not below a
-// candidate, and of equal ones the lowest index.
-template <int NC> __device__ inline int32_t nth_expert(const float *row, int32_t E, int32_t j)
+// o[i], the order of logit 64 i + l; the value bit by bit from the top, by counting those not
+// below a candidate.  above: how many are larger.
+//   Returns [value, upper) that holds it, and no others but equal ones.  WHOLE: all of the first
+//   j + 1 are in it or above, and no others.
+template <int NC, bool WHOLE> __device__ inline uint32_t nth_value(const uint32_t (&o)[NC], int32_t j, int32_t &above, uint32_t &upper)
 {
-    const int32_t lane = (int32_t)threadIdx.x & 63;
-    uint32_t o[NC];
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        const float v = row[min(64 * i + lane, E - 1)];
-        o[i] = 64 * i + lane < E ? order_of(v) : 0u;
-    }
     uint32_t value = 0;
-    int32_t above = 0;   // those over value's candidates that were too large
+    int32_t from = INT32_MAX;   // how many are not below value
+    above = 0;
+    upper = 0xFFFFFFFFu;        // (with above 0: all ones, which a NaN has, belongs to it)
 #pragma unroll 1
     for (uint32_t bit = 0x80000000u; bit; bit >>= 1) {
         int32_t n = 0;
 #pragma unroll
         for (int i = 0; i < NC; ++i) n += __popcll(__ballot(o[i] >= (value | bit)));
-        if (n > j) value |= bit;
-        else above = n;
+        if (n > j) {
+            value |= bit;
+            from = n;
+        } else {
+            above = n;
+            upper = value | bit;
+        }
+        if (WHOLE ? from == j + 1 : from - above == 1) break;
     }
-    int32_t left = j - above, e = 0;   // how many equal ones come before
+    return value;
+}
+template <int NC> __device__ inline void orders_of(const float *row, int32_t E, uint32_t (&o)[NC])
+{
+    const int32_t lane = (int32_t)threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const float v = row[min(64 * i + lane, E - 1)];
+        o[i] = 64 * i + lane < E ? order_of(v) : 0u;   // (every logit's is above 0)
+    }
+}
+// Expert number j: of equal logits the lowest index first.
+template <int NC> __device__ inline int32_t nth_expert(const float *row, int32_t E, int32_t j)
+{
+    uint32_t o[NC];
+    orders_of<NC>(row, E, o);
+    int32_t above, e = 0;
+    uint32_t upper;
+    const uint32_t value = nth_value<NC, false>(o, j, above, upper);
+    int32_t left = j - above;   // how many equal ones come before
     bool found = false;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-        uint64_t same = __ballot(o[i] == value && 64 * i + lane < E);
+        uint64_t same = __ballot(o[i] >= value && (o[i] < upper || above == 0));
         const int32_t n = __popcll(same);
         if (!found && left < n) {
             for (; left > 0; --left) same &= same - 1;
@@ -116,21 +140,51 @@ template <int NC> __device__ inline int32_t nth_expert(const float *row, int32_t
         }
         left -= n;
     }
-    return e;
+    return __builtin_amdgcn_readfirstlane(e);
 }
-// The expert of a slot, and the first token that has to be its.
-struct MoeSlot {
-    int32_t expert, first;
-};
-__device__ inline MoeSlot moe_slot(const MoeArgs &a, const float *logits, int32_t slot, bool by_pair)
+// The first k experts' bits.
+template <int NC> __device__ inline void mark_experts(const uint32_t (&o)[NC], int32_t k, uint32_t *any)
 {
-    if (!by_pair) return MoeSlot{slot, 0};
-    const int32_t t = slot / a.top_k, j = slot - t * a.top_k;
-    const float *row = logits + t * a.E;
-    const int32_t e = a.E <= 64 ? nth_expert<1>(row, a.E, j) : a.E <= 128 ? nth_expert<2>(row, a.E, j)
-                    : a.E <= 256 ? nth_expert<4>(row, a.E, j) : nth_expert<16>(row, a.E, j);
-    return MoeSlot{__builtin_amdgcn_readfirstlane(e), t};
+    int32_t above;
+    uint32_t upper;
+    const uint32_t value = nth_value<NC, true>(o, k - 1, above, upper);
+    int32_t left = k - above;   // of those in [value, upper), all or equal ones
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        uint64_t in = __ballot(o[i] >= upper && above > 0), same = __ballot(o[i] >= value) & ~in;
+        for (; left > 0 && same; --left) {
+            in |= same & -same;
+            same &= same - 1;
+        }
+        if (((int32_t)threadIdx.x & 63) == 0 && in) {
+            atomicOr(any + 2 * i, (uint32_t)in);
+            atomicOr(any + 2 * i + 1, (uint32_t)(in >> 32));
+        }
+    }
 }
+
+// What a workgroup does: a part of an expert's tiles.
+struct MoeGrid {
+    bool active;     // experts that have tokens share the workgroups, else all experts
+    bool one;        // all of K in a chunk
+    int32_t rows;    // tokens at a time, at most 16
+    int32_t tiles, chunk;
+    uint32_t x_bytes;
+};
+struct MoePlace {
+    int32_t slot, part, first, have;   // the expert's number; its tiles
+};
+// `experts` of them.  False: nothing to do.
+__device__ inline bool moe_place(const MoeGrid &g, int32_t experts, MoePlace &p)
+{
+    const int32_t wgs = max((int32_t)gridDim.x / experts, 1), per = (g.tiles + wgs - 1) / wgs;
+    p.slot = (int32_t)blockIdx.x / wgs;
+    p.part = (int32_t)blockIdx.x - p.slot * wgs;
+    p.first = p.part * per;
+    p.have = p.slot < experts ? min(per, g.tiles - p.first) : 0;
+    return p.have > 0;
+}
+
 // Ranks of an expert in the orders of the tokens of this wave (every eighth).  ask() loads the first
 // 128 logits of each, ahead of the search for the expert.
 constexpr int MOE_EACH = MOE_TOKENS / W4_WAVES;
@@ -178,9 +232,9 @@ struct MoeRanks {
             load(a, logits, f0);
         }
     }
-    // The list of the expert's tokens.  Returns how many; 0 where an earlier slot's workgroups work for
-    // them.  (Every wave writes the same list and reads what it wrote.)
-    __device__ inline int32_t list(const MoeArgs &a, const MoeSlot &s, MoeList &l) const
+    // The list of the expert's tokens.  Returns how many.  (Every wave writes the same list and reads
+    // what it wrote.)
+    __device__ inline int32_t list(const MoeArgs &a, MoeList &l) const
     {
         const int32_t lane = (int32_t)threadIdx.x & 63, wave = (int32_t)threadIdx.x >> 6;
         if (lane == 0)
@@ -190,54 +244,91 @@ struct MoeRanks {
         const int32_t rank = l.rank[lane];
         const uint64_t in = __ballot(rank >= 0);
         if (rank >= 0) l.row[__popcll(in & ((1ull << lane) - 1))] = lane * a.top_k + rank;
-        return in & ((1ull << s.first) - 1) ? 0 : __popcll(in);
+        return __popcll(in);
     }
 };
 
-// Expert, list of tokens and their number.  start(): called between, when the expert is known.
+// Place, expert, list of tokens and their number; 0: nothing to do.  start(): called between, when
+// place and expert are known.
 template <class Start>
-__device__ inline int32_t moe_route(const MoeArgs &a, const float *logits, bool by_pair, int32_t &expert, MoeList &l, Start &&start)
+__device__ inline int32_t moe_route(const MoeArgs &a, const MoeGrid &g, const float *logits, MoePlace &p, int32_t &expert,
+                                    MoeList &l, Start &&start)
 {
-    const int32_t slot = (int32_t)blockIdx.y;
-    if (by_pair && a.T == 1) {   // one token: slot j is its expert number j
-        expert = moe_slot(a, logits, slot, true).expert;
+    const int32_t tid = (int32_t)threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    if (a.T == 1) {   // slot j is expert number j
+        if (!moe_place(g, a.top_k, p)) return 0;
+        expert = a.E <= 64 ? nth_expert<1>(logits, a.E, p.slot) : a.E <= 128 ? nth_expert<2>(logits, a.E, p.slot)
+               : a.E <= 256 ? nth_expert<4>(logits, a.E, p.slot) : nth_expert<16>(logits, a.E, p.slot);
         start();
-        if (threadIdx.x == 0) l.rank[0] = l.row[0] = slot;
+        if (tid == 0) l.rank[0] = l.row[0] = p.slot;
         __syncthreads();
         return 1;
     }
     MoeRanks ranks;
     ranks.ask(a, logits);
-    const MoeSlot ms = moe_slot(a, logits, slot, by_pair);
-    expert = ms.expert;
+    int32_t experts = a.E;
+    if (g.active) {
+        if (tid < EXPERTS_MAX / 32) l.any[tid] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < MOE_EACH; ++i) {
+            const int32_t t = wave + W4_WAVES * i;
+            if (t >= a.T) break;
+            if (a.E <= 64) {
+                uint32_t o[1] = {(tid & 63) < a.E ? order_of(ranks.v[0][i]) : 0u};
+                mark_experts<1>(o, a.top_k, l.any);
+            } else if (a.E <= 64 * MoeRanks::AHEAD) {
+                uint32_t o[MoeRanks::AHEAD];
+#pragma unroll
+                for (int u = 0; u < MoeRanks::AHEAD; ++u) o[u] = 64 * u + (tid & 63) < a.E ? order_of(ranks.v[u][i]) : 0u;
+                mark_experts<MoeRanks::AHEAD>(o, a.top_k, l.any);
+            } else {
+                uint32_t o[EXPERTS_MAX / 64];
+                orders_of<EXPERTS_MAX / 64>(logits + t * a.E, a.E, o);
+                mark_experts<EXPERTS_MAX / 64>(o, a.top_k, l.any);
+            }
+        }
+        __syncthreads();
+        const uint32_t bits = l.any[tid % (EXPERTS_MAX / 32)];
+        const int32_t words = (a.E + 31) / 32;
+        experts = 0;
+        for (int32_t w = 0; w < words; ++w) experts += __builtin_popcount((uint32_t)__builtin_amdgcn_readlane((int)bits, w));
+        if (blockIdx.x == 0 && tid == 0) *a.found = experts;
+        if (!moe_place(g, experts, p)) return 0;
+        int32_t left = p.slot;
+        for (int32_t w = 0; w < words; ++w) {
+            uint32_t here = (uint32_t)__builtin_amdgcn_readlane((int)bits, w);
+            const int32_t n = __builtin_popcount(here);
+            if (left < n) {
+                for (; left > 0; --left) here &= here - 1;
+                expert = 32 * w + __builtin_ctz(here);
+                break;
+            }
+            left -= n;
+        }
+    } else {
+        if (!moe_place(g, experts, p)) return 0;
+        expert = p.slot;
+    }
     ranks.count(a, logits, expert);
     start();
-    return ranks.list(a, ms, l);
+    return ranks.list(a, l);
 }
 
 // ---- gate and up, activation -----------------------------------------------
-// A workgroup: an expert, some blocks of 16 columns, g.rows of its tokens at a time.
-// EARLY: x, all tokens' (up: at most g.rows of them) or the one token's (down), is asked for
-// before the expert is known.
+// A workgroup: an expert, some blocks of 16 columns (a tile of gate rows and one of up rows
+// each), g.rows of its tokens at a time.
+// ONE: all of a row of x is in LDS at once.  EARLY (and ONE): x, all tokens' (at most g.rows), is
+// asked for before the expert is known.
 // ROUTE (at most 16 tokens and experts): every workgroup forms the logits for itself, which takes
 // a us where a launch for them takes five.
-struct MoeGrid {
-    bool by_pair, early;
-    int32_t rows;    // tokens at a time, at most 16
-    uint32_t x_bytes;
-    W4Split sp;      // of blocks (up: a tile of gate rows and one of up rows each) or tiles (down)
-};
-template <class T, int G, bool EARLY, bool ROUTE>
+template <class T, int G, bool ONE, bool EARLY, bool ROUTE>
 __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGrid g)
 {
     extern __shared__ __attribute__((aligned(1024))) char smem[];
     __shared__ MoeList list;
-    const int32_t lane = (int32_t)(threadIdx.x & 63u), q = lane >> 4, r = lane & 15;
     const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int32_t kw = g.sp.kw, each = g.sp.each, lines = (a.H + 255) / 256;
-    const int32_t per = W4_WAVES / kw * each, b0 = (int32_t)blockIdx.x * per, have = min(per, a.I / 16 - b0);
-    const int32_t mine = wave / kw * each;
-    float *const slots = (float *)(smem + g.x_bytes + W4Lds<G>::RINGS);
+    MoePlace p = {};
     __bf16 *const hi = (__bf16 *)a.h, *const lo = hi + (int64_t)a.T * a.top_k * a.I;
     auto put = [&](int32_t m, int32_t c, float gate, float up) {
         int32_t row = list.row[m];
@@ -248,15 +339,14 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGri
         // (a quotient and an exponential good to 2^-21)
         const float h = gate / (1.0f + __expf(-gate)) * up;
         // in the order in which the down product's nibbles come
-        const int64_t o = (int64_t)row * a.I + b0 * 16 + (c & ~7) + 2 * (c & 3) + (c >> 2 & 1);
+        const int64_t o = (int64_t)row * a.I + p.first * 16 + (c & ~7) + 2 * (c & 3) + (c >> 2 & 1);
         const __bf16 top = (__bf16)h;
         hi[o] = top;
         lo[o] = (__bf16)(h - (float)top);
     };
     int32_t expert = 0;
-    auto tile_at = [&](int32_t t) { return W4Tile{((int64_t)expert * 2 + t % 2) * a.I + (b0 + mine + t / 2) * 16, 16}; };
-    W4Flow<T, T, G, 1, false, decltype(tile_at)> flow(smem, g.x_bytes, a.w1, (const uint32_t *)a.p1, a.H, g.sp,
-                                                  2 * max(0, min(each, have - mine)), tile_at);
+    auto tile_at = [&](int32_t t) { return W4Tile{((int64_t)expert * 2 + t % 2) * a.I + (p.first + t / 2) * 16, 16}; };
+    W4Flow<T, T, G, 1, decltype(tile_at)> flow(smem, g.x_bytes, a.w1, (const uint32_t *)a.p1, a.H, g.chunk, tile_at);
     const i32x4 rx = make_rsrc(a.x, 0xFFFFFFF0u);
     if constexpr (EARLY) flow.ask_x(0, a.T, rx, [&](int32_t i) { return (uint32_t)i * (uint32_t)a.ldx * 2u; });
     const float *logits = a.logits;
@@ -271,12 +361,12 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGri
         logits = list.logits;
     }
     // the first weights are on their way while the tokens are gathered
-    const int32_t count = __builtin_amdgcn_readfirstlane(moe_route(a, logits, g.by_pair, expert, list, [&] {
+    const int32_t count = __builtin_amdgcn_readfirstlane(moe_route(a, g, logits, p, expert, list, [&] {
         expert = __builtin_amdgcn_readfirstlane(expert);
-        flow.start();
+        flow.start(2 * p.have);
     }));
-    if (blockIdx.x == 0) {   // for the down product
-        int32_t *const l = a.lists + blockIdx.y * MOE_LIST;
+    if (p.part == 0 && p.have > 0) {   // for the down product
+        int32_t *const l = a.lists + p.slot * MOE_LIST;
         if (a.T == 1 && threadIdx.x == 66) l[3] = (int32_t)__float_as_uint(logits[expert]);
         if (threadIdx.x < (uint32_t)count) l[2 + threadIdx.x] = list.row[threadIdx.x];
         if (threadIdx.x == 64) l[0] = count;
@@ -284,125 +374,85 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGri
     }
     if (count == 0) flow.finish();
     for (int32_t at = 0; at < count; at += g.rows) {
-        const int32_t rows = EARLY ? a.T : min(g.rows, count - at), slot = rows * W4_SLOT_LD;
-        const bool direct = kw == 1 && g.sp.chunk >= lines;   // a wave has whole sums
+        const int32_t rows = EARLY ? a.T : min(g.rows, count - at);
+        const W4Sums<ONE> sums(smem + g.x_bytes + W4Lds<G>::RINGS, p.have, 2, rows);
         f32x4 gate = {0.f, 0.f, 0.f, 0.f};
         auto x_at = [&](int32_t i) { return (uint32_t)(list.row[at + i] / a.top_k) * (uint32_t)a.ldx * 2u; };
         auto done = [&](int32_t t, const f32x4 &acc, bool more) {
-            if (!direct) {
-                w4_put(slots + (wave * 2 * each + t) * slot, rows, acc, more);
-            } else if (t % 2 == 0) {
-                gate = acc;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (4 * i + q < rows) put(at + 4 * i + q, (mine + t / 2) * 16 + r, gate[i], acc[i]);
-            }
+            if (!sums.whole(wave, t / 2)) w4_put(sums.at(wave, t / 2, t % 2), rows, acc, more);
+            else if (t % 2 == 0) gate = acc;
+            else w4_rows(rows, [&](int32_t i, int32_t m, int32_t c) { put(at + m, t / 2 * 16 + c, gate[i], acc[i]); });
         };
         if (at == 0) {
-            flow.template run<true, EARLY>(rows, rx, x_at, done);
+            flow.template run<true, EARLY>(2 * p.have, rows, rx, x_at, done);
         } else if constexpr (!EARLY) {
             __syncthreads();
-            flow.template run<false, false>(rows, rx, x_at, done);
+            flow.template run<false, false>(2 * p.have, rows, rx, x_at, done);
         }
-        if (!direct) {
-            __syncthreads();
-            for (int32_t i = (int32_t)threadIdx.x; i < rows * have * 16; i += 64 * W4_WAVES) {
-                const int32_t m = i / (have * 16), c = i - m * have * 16, b = c / 16;
-                const float *s = slots + (b / each * kw * 2 * each + b % each * 2) * slot + m * W4_SLOT_LD + c % 16;
-                float v = 0.f, u = 0.f;
-                for (int32_t k = 0; k < kw; ++k) {
-                    v += s[k * 2 * each * slot];
-                    u += s[(k * 2 * each + 1) * slot];
-                }
-                put(at + m, c, v, u);
-            }
-        }
+        __syncthreads();
+        sums.each([&](int32_t u, int32_t m, int32_t c) { put(at + m, u * 16 + c, sums.sum(u, 0, m, c), sums.sum(u, 1, m, c)); });
         if constexpr (EARLY) return;
     }
 }
 
 // ---- down ------------------------------------------------------------------
-template <class T, int G>
+template <class T, int G, bool ONE>
 __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_kernel(MoeArgs a, MoeGrid g)
 {
     extern __shared__ __attribute__((aligned(1024))) char smem[];
     __shared__ MoeList list;
-    const int32_t lane = (int32_t)(threadIdx.x & 63u), q = lane >> 4, r = lane & 15;
-    const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int32_t kw = g.sp.kw, each = g.sp.each, lines = (a.I + 255) / 256;
-    const int32_t per = W4_WAVES / kw * each, t0 = (int32_t)blockIdx.x * per, have = min(per, a.H / 16 - t0);
-    const int32_t mine = wave / kw * each;
-    float *const slots = (float *)(smem + g.x_bytes + W4Lds<G>::RINGS);
+    const int32_t lane = (int32_t)(threadIdx.x & 63u), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    MoePlace p = {};
+    if (!moe_place(g, a.T == 1 ? a.top_k : g.active ? *a.found : a.E, p)) return;
+    const int32_t *const l = a.lists + p.slot * MOE_LIST;
+    const int32_t count = l[0], expert = l[1];
+    if (count == 0) return;
     const uint32_t plane = (uint32_t)(a.T * a.top_k) * (uint32_t)a.I * 2u;
-    int32_t expert = 0;
-    auto tile_at = [&](int32_t t) { return W4Tile{(int64_t)expert * a.H + (t0 + mine + t) * 16, 16}; };
-    W4Flow<__bf16, T, G, 2, false, decltype(tile_at)> flow(smem, g.x_bytes, a.w2, (const uint32_t *)a.p2, a.I, g.sp,
-                                                       max(0, min(each, have - mine)), tile_at);
+    auto tile_at = [&](int32_t t) { return W4Tile{(int64_t)expert * a.H + (p.first + t) * 16, 16}; };
+    W4Flow<__bf16, T, G, 2, decltype(tile_at)> flow(smem, g.x_bytes, a.w2, (const uint32_t *)a.p2, a.I, g.chunk, tile_at);
     const i32x4 rx = make_rsrc(a.h, 0xFFFFFFF0u);
-    const int32_t *const l = a.lists + blockIdx.y * MOE_LIST;
-    const int32_t count = l[0];
-    expert = l[1];
-    if (count == 0) {
-        flow.finish();
-        return;
-    }
     const int32_t mine_row = l[2 + min(lane, count - 1)];
     list.row[lane] = mine_row;   // (every wave writes the same, and reads what it wrote)
-    flow.start();
+    flow.start(p.have);
     for (int32_t at = 0; at < count; at += g.rows) {
-        const int32_t rows = min(g.rows, count - at), slot = rows * W4_SLOT_LD;
-        const bool direct = kw == 1 && g.sp.chunk >= lines;
+        const int32_t rows = min(g.rows, count - at);
+        const W4Sums<ONE> sums(smem + g.x_bytes + W4Lds<G>::RINGS, p.have, 1, rows);
+        auto put = [&](int32_t t, int32_t m, int32_t c, float v) { a.y[(int64_t)list.row[at + m] * a.H + (p.first + t) * 16 + c] = v; };
         auto x_at = [&](int32_t i) {
             const int32_t second = i >= rows;
             return (uint32_t)list.row[at + i - (second ? rows : 0)] * (uint32_t)a.I * 2u + (second ? plane : 0u);
         };
         auto done = [&](int32_t t, const f32x4 &acc, bool more) {
-            if (!direct) {
-                w4_put(slots + (wave * each + t) * slot, rows, acc, more);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (4 * i + q < rows) a.y[(int64_t)list.row[at + 4 * i + q] * a.H + (t0 + mine + t) * 16 + r] = acc[i];
-            }
+            if (!sums.whole(wave, t)) return w4_put(sums.at(wave, t, 0), rows, acc, more);
+            w4_rows(rows, [&](int32_t i, int32_t m, int32_t c) { put(t, m, c, acc[i]); });
         };
         if (at == 0) {
-            flow.template run<true, false>(rows, rx, x_at, done);
+            flow.template run<true, false>(p.have, rows, rx, x_at, done);
         } else {
             __syncthreads();
-            flow.template run<false, false>(rows, rx, x_at, done);
+            flow.template run<false, false>(p.have, rows, rx, x_at, done);
         }
-        if (!direct) {
-            __syncthreads();
-            for (int32_t i = (int32_t)threadIdx.x; i < rows * have * 16; i += 64 * W4_WAVES) {
-                const int32_t m = i / (have * 16), c = i - m * have * 16, t = c / 16;
-                const float *s = slots + (t / each * kw * each + t % each) * slot + m * W4_SLOT_LD + c % 16;
-                float v = 0.f;
-                for (int32_t k = 0; k < kw; ++k) v += s[k * each * slot];
-                a.y[(int64_t)list.row[at + m] * a.H + t0 * 16 + c] = v;
-            }
-        }
+        __syncthreads();
+        sums.each([&](int32_t t, int32_t m, int32_t c) { put(t, m, c, sums.sum(t, 0, m, c)); });
     }
 }
 
-// One token: a workgroup's columns get all of its experts' sums, weighted here, one expert's lines
-// after the other's, and no launch follows.
+// One token: a workgroup's columns get all of its experts' sums, weighted here (tile k c + j: column
+// tile c of expert j), and no launch follows.
 template <class T, int G>
-__global__ __launch_bounds__(64 * W4_WAVES) void moe_down_token_kernel(MoeArgs a, MoeGrid g)
+__global__ __launch_bounds__(64 * W4_WAVES) void moe_down_token_kernel(MoeArgs a, int32_t per, uint32_t x_bytes)
 {
     extern __shared__ __attribute__((aligned(1024))) char smem[];
     const int32_t lane = (int32_t)(threadIdx.x & 63u), k = a.top_k;
     const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int32_t kw = g.sp.kw, each = g.sp.each;
-    const int32_t per = W4_WAVES / kw * each, t0 = (int32_t)blockIdx.x * per, have = min(per, a.H / 16 - t0);
-    const int32_t mine = wave / kw * each, tiles = max(0, min(each, have - mine));
-    float *const slots = (float *)(smem + g.x_bytes + W4Lds<G>::RINGS);
+    const int32_t t0 = (int32_t)blockIdx.x * per, have = min(per, a.H / 16 - t0);
+    const W4Sums<false> sums(smem + x_bytes + W4Lds<G>::RINGS, k * have, 1, 1);
     int32_t expert = 0, row = 0;   // of slot `lane`
     auto tile_at = [&](int32_t t) {
-        const int32_t j = t / max(tiles, 1), e = __builtin_amdgcn_readlane(expert, j);
-        return W4Tile{(int64_t)e * a.H + (t0 + mine + t - j * tiles) * 16, 16};
+        const int32_t j = t % k;
+        return W4Tile{(int64_t)__builtin_amdgcn_readlane(expert, j) * a.H + (t0 + t / k) * 16, 16};
     };
-    W4Flow<__bf16, T, G, 2, true, decltype(tile_at)> flow(smem, g.x_bytes, a.w2, (const uint32_t *)a.p2, a.I, g.sp, k * tiles, tile_at, k);
+    W4Flow<__bf16, T, G, 2, decltype(tile_at)> flow(smem, x_bytes, a.w2, (const uint32_t *)a.p2, a.I, (a.I + 255) / 256, tile_at);
     const i32x4 rx = make_rsrc(a.h, 0xFFFFFFF0u);
     auto x_at = [&](int32_t i) { return (uint32_t)i * (uint32_t)a.I * 2u; };   // (the planes follow each other)
     const int32_t *const l = a.lists + min(lane, k - 1) * MOE_LIST;
@@ -411,7 +461,7 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_token_kernel(MoeArgs a
     const float logit = __uint_as_float((uint32_t)l[3]);
     // the sum of all experts' exponentials, or of the chosen ones'; any NaN or infinity spoils it
     const float other = !a.renorm ? a.logits[min(lane, a.E - 1)] : 0.f;
-    flow.start();
+    flow.start(k * have);
     float largest = logit;
 #pragma unroll
     for (int d = 32; d; d >>= 1) largest = fmaxf(largest, __shfl_xor(largest, d));
@@ -428,20 +478,17 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_token_kernel(MoeArgs a
         if (a.ids) a.ids[row] = expert;
         if (a.weights) a.weights[row] = weight;
     }
-    flow.template run_n<1, true, false>(
-        k, rx, x_at,
+    flow.template run_n<1, true, false, true>(
+        k * have, k, rx, x_at,
         [&](int32_t t, const f32x4 &acc, bool) {
-            const int32_t j = t / tiles;
-            const float p = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(weight), j));
-            w4_put(slots + (wave * each + t - j * tiles) * W4_SLOT_LD, 1, acc * p, j > 0);
+            const float q = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(weight), t % k));
+            w4_put(sums.at(wave, t, 0), 1, acc * q, false);
         },
-        [&](int32_t t) { return __builtin_amdgcn_readlane(row, t / tiles); });
+        [&](int32_t t) { return __builtin_amdgcn_readlane(row, t % k); });
     __syncthreads();
     for (int32_t c = (int32_t)threadIdx.x; c < have * 16; c += 64 * W4_WAVES) {
-        const int32_t t = c / 16;
-        const float *s = slots + (t / each * kw * each + t % each) * W4_SLOT_LD + c % 16;
         float v = 0.f;
-        for (int32_t i = 0; i < kw; ++i) v += s[i * each * W4_SLOT_LD];
+        for (int32_t j = 0; j < k; ++j) v += sums.sum(c / 16 * k + j, 0, 0, c % 16);
         ((T *)a.out)[t0 * 16 + c] = (T)v;
     }
 }
@@ -517,63 +564,57 @@ __global__ __launch_bounds__(COMBINE_THREADS) void moe_combine_kernel(MoeArgs a)
     *(u32x2 *)((T *)a.out + (int64_t)t * a.H + c) = u32x2{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3])};
 }
 
-// One of the two products' workgroups: `tiles` per expert, `slots` experts or pairs, sums of
-// `per_tile` tiles of 16 columns each in LDS.
+// One of the two products' launches: `tiles` of an expert, sums of `per_tile` tiles of 16 columns
+// each in LDS.
+enum { MOE_LDS = 156 * 1024 };
 struct MoeShape {
     MoeGrid g;
-    uint32_t x, lds;
+    uint32_t wgs, lds;
 };
-enum { MOE_LDS = 156 * 1024 };
-template <int G> static MoeShape moe_shape(const MoeArgs &a, int64_t tiles, int32_t K, int planes, int per_tile, int64_t slots, int cu)
+template <int G> static MoeShape moe_shape(const MoeArgs &a, int32_t tiles, int32_t K, int planes, int per_tile, int cu)
 {
     MoeShape m;
-    m.g.by_pair = a.T * a.top_k < a.E;
+    const int32_t lines = (K + 255) / 256, pairs = a.T * a.top_k;
+    m.g.active = pairs < 3 * a.E;
     m.g.rows = a.T < 16 ? a.T : 16;
-    const int64_t lines = (K + 255) / 256, slot = (int64_t)m.g.rows * W4_SLOT_LD * 4 * per_tile, xrows = planes * m.g.rows;
-    // a workgroup to a compute unit
-    const int64_t wgs = std::max<int64_t>(1, cu / slots);
-    for (int64_t per = (tiles + wgs - 1) / wgs;; --per) {
-        m.g.sp = w4_split(per, lines, xrows, 66 * 1024);
-        const bool direct = m.g.sp.kw == 1 && m.g.sp.chunk >= lines;
-        const int64_t sums = direct ? 0 : W4_WAVES * m.g.sp.each * slot;
-        m.g.x_bytes = W4Lds<G>::x_bytes((int32_t)xrows, m.g.sp.chunk);
-        m.lds = (uint32_t)(m.g.x_bytes + W4Lds<G>::RINGS + sums);
-        if (m.lds <= MOE_LDS || per == 1) break;
+    m.g.tiles = tiles;
+    m.g.chunk = w4_chunk(lines, planes * m.g.rows, 66 * 1024);
+    m.g.one = m.g.chunk >= lines;
+    m.g.x_bytes = W4Lds<G>::x_bytes(planes * m.g.rows, m.g.chunk);
+    // a workgroup to a compute unit, or more where their sums would not find room
+    const int32_t most = m.g.active ? std::min(pairs, a.E) : a.E;
+    for (int32_t wgs = std::max(cu, most);; wgs += most) {
+        const int32_t per = (tiles + wgs / most - 1) / (wgs / most);
+        m.wgs = (uint32_t)wgs;
+        m.lds = (uint32_t)std::min<int64_t>(m.g.x_bytes + W4Lds<G>::RINGS + w4_sums_bytes(m.g.one, per, per_tile, m.g.rows), INT32_MAX);
+        if (m.lds <= MOE_LDS || per == 1) return m;
     }
-    const int64_t wide = (int64_t)(W4_WAVES / m.g.sp.kw) * m.g.sp.each;
-    m.x = (uint32_t)((tiles + wide - 1) / wide);
-    return m;
 }
 
 template <class T, int G> static hipError_t moe_t(const MoeArgs &a, int cu, hipStream_t s)
 {
-    const uint32_t slots = (uint32_t)min(a.T * a.top_k, a.E);
     const dim3 block(64 * W4_WAVES);
-    MoeShape up = moe_shape<G>(a, a.I / 16, a.H, 1, 2, slots, cu), dn = moe_shape<G>(a, a.H / 16, a.I, 2, 1, slots, cu);
-    up.g.early = a.T <= up.g.rows && up.g.sp.chunk >= (a.H + 255) / 256;   // all of x at once
-    // one token: all of its experts' activations in LDS, or each expert for itself
-    MoeShape one = dn;
-    if (a.T == 1) {
-        const int64_t tiles = a.H / 16, lines = (a.I + 255) / 256;
-        one.g.sp = w4_split((tiles + cu - 1) / cu, lines * a.top_k, 1, INT32_MAX);
-        one.g.sp.chunk = (int32_t)lines;
-        const int64_t wide = (int64_t)(W4_WAVES / one.g.sp.kw) * one.g.sp.each;
-        one.g.x_bytes = W4Lds<G>::x_bytes(2 * a.top_k, (int32_t)lines);
-        one.x = (uint32_t)((tiles + wide - 1) / wide);
-        one.lds = one.g.x_bytes + W4Lds<G>::RINGS + (uint32_t)(W4_WAVES * one.g.sp.each * W4_SLOT_LD * 4);
-        one.g.early = one.lds <= MOE_LDS;
-    }
+    MoeShape up = moe_shape<G>(a, a.I / 16, a.H, 1, 2, cu), dn = moe_shape<G>(a, a.H / 16, a.I, 2, 1, cu);
+    const bool early = a.T <= up.g.rows && up.g.one;   // all of x at once
     if (up.lds > MOE_LDS || dn.lds > MOE_LDS) return hipErrorInvalidValue;
-    const bool route = up.g.early && a.E <= 16 && a.T <= 16 && a.E * a.H <= 65536;
+    const bool route = early && a.E <= 16 && a.T <= 16 && a.E * a.H <= 65536;
     if (!route) hipLaunchKernelGGL((moe_router_kernel<T>), dim3((uint32_t)(a.E + 15) / 16, (uint32_t)(a.T + 15) / 16), dim3(64 * ROUTER_WAVES), 0, s, a);
-    if (route) hipLaunchKernelGGL((moe_up_kernel<T, G, true, true>), dim3(up.x, slots), block, up.lds, s, a, up.g);
-    else if (up.g.early) hipLaunchKernelGGL((moe_up_kernel<T, G, true, false>), dim3(up.x, slots), block, up.lds, s, a, up.g);
-    else hipLaunchKernelGGL((moe_up_kernel<T, G, false, false>), dim3(up.x, slots), block, up.lds, s, a, up.g);
-    if (a.T == 1 && one.g.early) {
-        hipLaunchKernelGGL((moe_down_token_kernel<T, G>), dim3(one.x), block, one.lds, s, a, one.g);
-        return hipGetLastError();
+    if (route) hipLaunchKernelGGL((moe_up_kernel<T, G, true, true, true>), dim3(up.wgs), block, up.lds, s, a, up.g);
+    else if (early) hipLaunchKernelGGL((moe_up_kernel<T, G, true, true, false>), dim3(up.wgs), block, up.lds, s, a, up.g);
+    else if (up.g.one) hipLaunchKernelGGL((moe_up_kernel<T, G, true, false, false>), dim3(up.wgs), block, up.lds, s, a, up.g);
+    else hipLaunchKernelGGL((moe_up_kernel<T, G, false, false, false>), dim3(up.wgs), block, up.lds, s, a, up.g);
+    if (a.T == 1) {   // all of its experts' activations in LDS, if they find room there
+        const int32_t tiles = a.H / 16, per = (tiles + cu - 1) / cu;
+        const uint32_t x_bytes = W4Lds<G>::x_bytes(2 * a.top_k, (a.I + 255) / 256);
+        const int64_t lds = x_bytes + W4Lds<G>::RINGS + w4_sums_bytes(false, (int64_t)a.top_k * per, 1, 1);
+        if (lds <= MOE_LDS) {
+            hipLaunchKernelGGL((moe_down_token_kernel<T, G>), dim3((uint32_t)((tiles + per - 1) / per)), block, (uint32_t)lds, s, a, per,
+                               x_bytes);
+            return hipGetLastError();
+        }
     }
-    hipLaunchKernelGGL((moe_down_kernel<T, G>), dim3(dn.x, slots), block, dn.lds, s, a, dn.g);
+    if (dn.g.one) hipLaunchKernelGGL((moe_down_kernel<T, G, true>), dim3(dn.wgs), block, dn.lds, s, a, dn.g);
+    else hipLaunchKernelGGL((moe_down_kernel<T, G, false>), dim3(dn.wgs), block, dn.lds, s, a, dn.g);
     hipLaunchKernelGGL((moe_combine_kernel<T>), dim3((uint32_t)(a.H + 4 * COMBINE_THREADS - 1) / (4 * COMBINE_THREADS), (uint32_t)a.T),
                        dim3(COMBINE_THREADS), 0, s, a);
     return hipGetLastError();

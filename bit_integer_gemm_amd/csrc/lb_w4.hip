@@ -6,44 +6,40 @@
 
 namespace lb {
 
-// Up to 16 rows: a workgroup takes all of x against some tiles of 16 columns (W4Split).
+// Up to 16 rows: a workgroup takes all of x against some tiles of 16 columns.
 // EARLY: weights are asked for before x (a row or two of x are there before the first weights).
+// ONE: all of x is in LDS at once.
 struct FewArgs {
     const uint8_t *w;
     const uint32_t *p;
     int64_t ldx;
     int32_t M, N, K;
-    W4Split sp;
+    int32_t per, chunk;   // tiles of a workgroup, lines whose x is in LDS together
 };
-template <class T, int G, bool EARLY>
+template <class T, int G, bool EARLY, bool ONE>
 __global__ __launch_bounds__(64 * W4_WAVES) void w4_few_kernel(const T *__restrict__ X, const T *__restrict__ bias,
                                                                   T *__restrict__ out, FewArgs a)
 {
     extern __shared__ __attribute__((aligned(1024))) char smem[];
     const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), rows = a.M;
-    const int32_t kw = a.sp.kw, each = a.sp.each;
-    const int32_t per = W4_WAVES / kw * each, t0 = (int32_t)blockIdx.x * per;   // the workgroup's tiles
-    const int32_t have = min(per, (a.N + 15) / 16 - t0), mine = wave / kw * each;
-    float *const slots = (float *)(smem + W4Lds<G>::x_bytes(rows, a.sp.chunk) + W4Lds<G>::RINGS);
-    const int32_t slot = rows * W4_SLOT_LD;
-    auto tile_at = [&](int32_t t) { return W4Tile{(int64_t)(t0 + mine + t) * 16, min(16, a.N - (t0 + mine + t) * 16)}; };
-    W4Flow<T, T, G, 1, false, decltype(tile_at)> flow(smem, W4Lds<G>::x_bytes(rows, a.sp.chunk), a.w, a.p, a.K, a.sp,
-                                               max(0, min(each, have - mine)), tile_at);
-    if constexpr (EARLY) flow.start();
+    const int32_t t0 = (int32_t)blockIdx.x * a.per, tiles = min(a.per, (a.N + 15) / 16 - t0);
+    const uint32_t x_bytes = W4Lds<G>::x_bytes(rows, a.chunk);
+    const W4Sums<ONE> sums(smem + x_bytes + W4Lds<G>::RINGS, tiles, 1, rows);
+    auto put = [&](int32_t t, int32_t m, int32_t c, float v) {
+        const int32_t n = (t0 + t) * 16 + c;
+        if (n < a.N) out[(int64_t)m * a.N + n] = (T)(bias ? v + (float)bias[n] : v);
+    };
+    auto tile_at = [&](int32_t t) { return W4Tile{(int64_t)(t0 + t) * 16, min(16, a.N - (t0 + t) * 16)}; };
+    W4Flow<T, T, G, 1, decltype(tile_at)> flow(smem, x_bytes, a.w, a.p, a.K, a.chunk, tile_at);
+    if constexpr (EARLY) flow.start(tiles);
     flow.template run<EARLY, false>(
-        rows, make_rsrc(X, 0xFFFFFFF0u), [&](int32_t row) { return (uint32_t)row * (uint32_t)a.ldx * 2u; },
-        [&](int32_t t, const f32x4 &acc, bool more) { w4_put(slots + (wave * each + t) * slot, rows, acc, more); });
+        tiles, rows, make_rsrc(X, 0xFFFFFFF0u), [&](int32_t row) { return (uint32_t)row * (uint32_t)a.ldx * 2u; },
+        [&](int32_t t, const f32x4 &acc, bool more) {
+            if (!sums.whole(wave, t)) return w4_put(sums.at(wave, t, 0), rows, acc, more);
+            w4_rows(rows, [&](int32_t i, int32_t m, int32_t c) { put(t, m, c, acc[i]); });
+        });
     __syncthreads();
-    for (int32_t i = (int32_t)threadIdx.x; i < rows * have * 16; i += 64 * W4_WAVES) {
-        const int32_t m = i / (have * 16), c = i - m * have * 16, t = c / 16, n = t0 * 16 + c;
-        if (n >= a.N) continue;
-        // tile t: the waves of group t / each, in order
-        const float *s = slots + (t / each * kw * each + t % each) * slot + m * W4_SLOT_LD + c % 16;
-        float v = 0.f;
-        for (int32_t k = 0; k < kw; ++k) v += s[k * each * slot];
-        if (bias) v += (float)bias[n];
-        out[(int64_t)m * a.N + n] = (T)v;
-    }
+    sums.each([&](int32_t t, int32_t m, int32_t c) { put(t, m, c, sums.sum(t, 0, m, c)); });
 }
 
 enum { FEW_LDS = 160 * 1024 };
@@ -52,17 +48,20 @@ template <class T, int G> static hipError_t w4_g(const W4Args &a, int cu, hipStr
     const int64_t tiles = (a.N + 15) / 16, lines = (a.K + 255) / 256;
     // a workgroup to a compute unit, if its sums find room
     int64_t per = (tiles + cu - 1) / cu;
-    const int64_t slot = a.M * W4_SLOT_LD * 4, room = 24 * 1024 / (W4_WAVES * slot);
-    if (per > room) per = room > 1 ? room : 1;
-    const W4Split sp = w4_split(per, lines, a.M, FEW_LDS - 4096 - W4Lds<G>::RINGS - W4_WAVES * per * slot);
-    const int64_t wide = (int64_t)(W4_WAVES / sp.kw) * sp.each, wgs = (tiles + wide - 1) / wide;
-    const uint32_t lds = W4Lds<G>::x_bytes((int32_t)a.M, sp.chunk) + W4Lds<G>::RINGS + (uint32_t)(W4_WAVES * sp.each * slot);
+    int32_t chunk = w4_chunk(lines, a.M, FEW_LDS - 1024 - W4Lds<G>::RINGS - w4_sums_bytes(true, per, 1, a.M));
+    const bool one = chunk >= lines;
+    while (!one && per > 1 && w4_sums_bytes(false, per, 1, a.M) > 40 * 1024) per = (per + 1) / 2;
+    const int64_t sums = w4_sums_bytes(one, per, 1, a.M), wgs = (tiles + per - 1) / per;
+    if (!one) chunk = w4_chunk(lines, a.M, FEW_LDS - 1024 - W4Lds<G>::RINGS - sums);
+    const FewArgs f{a.w, (const uint32_t *)a.p, a.ldx, (int32_t)a.M, (int32_t)a.N, (int32_t)a.K, (int32_t)per, chunk};
+    const uint32_t lds = W4Lds<G>::x_bytes(f.M, f.chunk) + W4Lds<G>::RINGS + (uint32_t)sums;
     if (a.M > W4_FEW_ROWS || wgs * 64 * W4_WAVES > LAUNCH_THREADS || lds > FEW_LDS) return hipErrorInvalidValue;
-    const FewArgs f{a.w, (const uint32_t *)a.p, a.ldx, (int32_t)a.M, (int32_t)a.N, (int32_t)a.K, sp};
     const dim3 grid((uint32_t)wgs), block(64 * W4_WAVES);
     const T *x = (const T *)a.x, *bias = (const T *)a.bias;
-    if (a.M > 2) hipLaunchKernelGGL((w4_few_kernel<T, G, true>), grid, block, lds, s, x, bias, (T *)a.out, f);
-    else hipLaunchKernelGGL((w4_few_kernel<T, G, false>), grid, block, lds, s, x, bias, (T *)a.out, f);
+    T *out = (T *)a.out;
+    if (!one) hipLaunchKernelGGL((w4_few_kernel<T, G, false, false>), grid, block, lds, s, x, bias, out, f);
+    else if (a.M > 2) hipLaunchKernelGGL((w4_few_kernel<T, G, true, true>), grid, block, lds, s, x, bias, out, f);
+    else hipLaunchKernelGGL((w4_few_kernel<T, G, false, true>), grid, block, lds, s, x, bias, out, f);
     return hipGetLastError();
 }
 

@@ -95,13 +95,11 @@ struct W4Tile {
     int32_t rows;
 };
 
-// How a workgroup shares its work.  K is taken in chunks of `chunk` lines, whose activations are
-// in LDS together; of a chunk's lines `kw` waves take a share each, for the same `each` tiles of
-// 16 columns, the next kw waves for the next ones.
+// How a workgroup shares its work.  K is taken in chunks of lines whose activations are in LDS
+// together; a chunk's lines of all the workgroup's tiles, one tile's after the other's, are cut
+// into eight equal parts, one to a wave.  A wave has parts of tiles tiles w / 8 and following.
 constexpr int W4_WAVES = 8;
-struct W4Split {
-    int32_t kw, each, chunk;
-};
+__host__ __device__ inline int32_t w4_first(int32_t tiles, int32_t wave) { return tiles * wave / W4_WAVES; }
 
 // LDS of a workgroup: x (two planes: one row after the other's all), the rings, and what the
 // caller puts behind.
@@ -148,63 +146,59 @@ template <int N> __device__ inline void w4_wait() { asm volatile("s_waitcnt vmcn
 //   lds: x (x_bytes of it), then the rings.  Copies of two lines are under way while a third is
 //     worked on; each wave waits for its own by count.
 //   PLANES 2: x is the sum of two planes, whose rows follow each other, in order in memory.
-//   SEGMENTS: the tiles are `segments` times the same columns with other weights, each time with
-//     one other row of x (row_of(tile)); the waves share all their lines together.  One chunk.
-//   tiles: this wave's; tile_at(t): a W4Tile.
+//   tiles: the workgroup's; tile_at(t): a W4Tile.
 //   T: the type of x as the matrix cores take it; PT: of the groups' numbers.
-// Every wave of a workgroup makes the same calls, also one without tiles (x is copied by all).
-template <class T, class PT, int G, int PLANES, bool SEGMENTS, class TileAt>
+// Every wave of a workgroup makes the same calls, also one without lines (x is copied by all).
+template <class T, class PT, int G, int PLANES, class TileAt>
 struct W4Flow {
     typedef W4Lds<G> L;
     enum : int { GROUPS = L::GROUPS, STEPS = G / 32 };
     char *const lds;
     const uint8_t *const W;
     const uint32_t *const P;
-    const int32_t K, lines, tiles;
-    const W4Split sp;
+    const int32_t K, lines, chunk;
     const TileAt tile_at;
-    const int32_t lane, wave, share, segments;
+    const int32_t lane, wave;
+    int32_t tiles;
     const uint32_t kb, groups;
     char *const ring;
     // what is copied next
-    int32_t c_chunk, c_tile, c_line, c_lo, c_hi;
+    int32_t c_chunk, c_tile, c_line, c_hi;
     bool left;
     i32x4 rw, rp;
     uint32_t c_at, c_slot;
     uint32_t w_at[2], p_at[L::COPIES - 2];   // of a lane in a line of 16 rows of weights, of their numbers
 
-    __device__ inline W4Flow(char *lds_, uint32_t x_bytes, const uint8_t *W_, const uint32_t *P_, int32_t K_, const W4Split &sp_,
-                             int32_t tiles_, const TileAt &at_, int32_t segments_ = 1)
-        : lds(lds_), W(W_), P(P_), K(K_), lines((K_ + 255) / 256), tiles(tiles_), sp(sp_), tile_at(at_),
-          lane((int32_t)(threadIdx.x & 63u)), wave(__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6))), share(wave % sp_.kw), segments(segments_),
-          kb((uint32_t)K_ / 2u), groups((uint32_t)K_ / G), ring(lds_ + x_bytes + wave * L::RING)
+    __device__ inline W4Flow(char *lds_, uint32_t x_bytes, const uint8_t *W_, const uint32_t *P_, int32_t K_, int32_t chunk_,
+                             const TileAt &at_)
+        : lds(lds_), W(W_), P(P_), K(K_), lines((K_ + 255) / 256), chunk(chunk_), tile_at(at_), lane((int32_t)(threadIdx.x & 63u)),
+          wave(__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6))), tiles(0), kb((uint32_t)K_ / 2u), groups((uint32_t)K_ / G),
+          ring(lds_ + x_bytes + wave * L::RING)
     {
     }
 
+    __device__ inline int32_t first() const { return w4_first(tiles, wave); }
+    __device__ inline int32_t end() const { return (tiles * (wave + 1) + W4_WAVES - 1) / W4_WAVES; }
     // Lines of the chunk from line c on, for a tile, that are this wave's.
     __device__ inline void bounds(int32_t c, int32_t tile, int32_t &lo, int32_t &hi) const
     {
-        if constexpr (SEGMENTS) {
-            const int32_t all = lines * segments, before = tile / max(tiles / segments, 1) * lines;
-            lo = min(max(all * share / sp.kw - before, 0), lines);
-            hi = min(max(all * (share + 1) / sp.kw - before, 0), lines);
-        } else {
-            const int32_t n = min(sp.chunk, lines - c);
-            lo = c + n * share / sp.kw;
-            hi = c + n * (share + 1) / sp.kw;
-        }
+        const int32_t n = min(chunk, lines - c), all = tiles * n, before = tile * n;
+        lo = c + min(max(all * wave / W4_WAVES - before, 0), n);
+        hi = c + min(max(all * (wave + 1) / W4_WAVES - before, 0), n);
     }
-    // The tile that is copied next: SEGMENTS: the first from c_tile on of which this wave has lines.
+    // The tile that is copied next: the first from c_tile on of which this wave has lines.
     __device__ inline void next_tile()
     {
-        for (left = false; c_tile < tiles && !left; c_tile += !left) {
-            bounds(c_chunk, c_tile, c_lo, c_hi);
-            left = c_lo < c_hi;
+        for (left = false;; ++c_tile) {
+            if (c_tile >= end()) {
+                c_chunk += chunk;
+                c_tile = first();
+                if (c_chunk >= lines) return;
+            }
+            bounds(c_chunk, c_tile, c_line, c_hi);
+            left = c_line < c_hi;
+            if (left) break;
         }
-        c_line = c_lo;
-    }
-    __device__ inline void aim()
-    {
         const W4Tile t = tile_at(c_tile);
         rw = make_rsrc(W + t.row * kb, (uint64_t)(uint32_t)t.rows * kb);
         rp = make_rsrc(P + t.row * groups, (uint64_t)(uint32_t)t.rows * groups * 4u);
@@ -230,37 +224,18 @@ struct W4Flow {
         }
         if (left && ++c_line == c_hi) {
             ++c_tile;
-            if constexpr (SEGMENTS) {
-                next_tile();
-            } else {
-                if (c_tile == tiles) {
-                    c_tile = 0;
-                    c_chunk += sp.chunk;
-                    left = c_chunk < lines;
-                    if (left) {
-                        bounds(c_chunk, 0, c_lo, c_hi);
-                        left = c_lo < c_hi;   // (a last chunk of fewer lines than shares)
-                    }
-                }
-                c_line = c_lo;
-            }
-            if (left) aim();
-            else rw.z = rp.z = 0;
+            next_tile();
+            if (!left) rw.z = rp.z = 0;
         }
     }
-    // Asks for the first lines.
-    __device__ inline void start()
+    // Asks for the first lines of tiles_ tiles.
+    __device__ inline void start(int32_t tiles_)
     {
-        c_chunk = c_tile = c_lo = 0;
-        if constexpr (SEGMENTS) {
-            next_tile();
-        } else {
-            bounds(0, 0, c_lo, c_hi);
-            c_line = c_lo;
-            left = tiles > 0 && c_lo < c_hi;   // (no lines: only where there is one chunk)
-        }
-        if (left) aim();
-        else rw = rp = make_rsrc(W, 0);
+        tiles = tiles_;
+        c_chunk = c_line = 0;
+        c_tile = first();
+        rw = rp = make_rsrc(W, 0);
+        next_tile();
         c_at = lds_addr(ring);
         c_slot = 0;
 #pragma unroll
@@ -277,7 +252,7 @@ struct W4Flow {
     // x of the chunk from line c on: piece p of row i lies at p ^ i % 16 of the row.
     template <class XAt> __device__ inline void ask_x(int32_t c, int32_t xrows, const i32x4 rx, XAt &&x_at)
     {
-        const int32_t per = min(sp.chunk, lines - c) * 32, all = per * xrows;
+        const int32_t per = min(chunk, lines - c) * 32, all = per * xrows;
         int32_t row = (wave * 64 + lane) / per, at = wave * 64 + lane - row * per;
         for (int32_t i0 = wave * 64; i0 < all; i0 += 64 * W4_WAVES) {
             const int32_t k = c * 256 + 8 * (at ^ (row & 15));
@@ -293,7 +268,7 @@ struct W4Flow {
             return;
         }
         constexpr int AT_ONCE = 4;
-        const int32_t all = min(sp.chunk, lines - c) * 32 * xrows;
+        const int32_t all = min(chunk, lines - c) * 32 * xrows;
         u32x4 *const p = (u32x4 *)lds;
         for (int32_t i = (int32_t)threadIdx.x; i < all; i += 64 * W4_WAVES * AT_ONCE) {
             u32x4 v[AT_ONCE];
@@ -308,44 +283,44 @@ struct W4Flow {
 
     // `rows` rows of x through rx, row i's first byte at x_at(i) (PLANES 2: rows from `rows` on are
     // the second plane's).  STARTED: start() has been called, and the weights' latency runs beside
-    // the copy of x; else start() comes after it, and beside the putting in order.  ASKED: ask_x()
-    // has been called, before start().
-    //   done(t, acc, more): sums of tile t over this wave's lines of a chunk, more: not the first
-    //     chunk's; acc[i] is row 4 i + lane / 16, column lane % 16.
+    // the copy of x; else start(tiles_) comes after it, and beside the putting in order.  ASKED:
+    // ask_x() has been called, before start().
+    //   done(t, acc, more): sums of tile t over this wave's lines; acc[i] is row 4 i + lane / 16, column
+    //     lane % 16 of the tile.  Called for each chunk (more: not the first) and each of the
+    //     wave's tiles, also one without lines.
     template <bool STARTED, bool ASKED, class XAt, class Done>
-    __device__ inline void run(int32_t rows, const i32x4 rx, XAt &&x_at, Done &&done)
+    __device__ inline void run(int32_t tiles_, int32_t rows, const i32x4 rx, XAt &&x_at, Done &&done)
     {
         auto none = [](int32_t) { return 0; };
-        if (rows <= 4) run_n<1, STARTED, ASKED>(rows, rx, x_at, done, none);
-        else if (rows <= 8) run_n<2, STARTED, ASKED>(rows, rx, x_at, done, none);
-        else run_n<4, STARTED, ASKED>(rows, rx, x_at, done, none);
+        if (rows <= 4) run_n<1, STARTED, ASKED, false>(tiles_, rows, rx, x_at, done, none);
+        else if (rows <= 8) run_n<2, STARTED, ASKED, false>(tiles_, rows, rx, x_at, done, none);
+        else run_n<4, STARTED, ASKED, false>(tiles_, rows, rx, x_at, done, none);
     }
     // RO: at most 4 RO rows.  A matrix instruction's row 4 q + i, whose sums are in lanes q of register
     // i, takes row 4 i + q, so that few rows need few registers scaled.  Two planes of at most 8 rows
     // are rows of one instruction, the second plane's sums RO registers behind the first's.
-    template <int RO, bool STARTED, bool ASKED, class XAt, class Done, class RowOf>
-    __device__ inline void run_n(int32_t rows, const i32x4 rx, XAt &&x_at, Done &&done, RowOf &&row_of)
+    // OWN_ROW: a tile has one row of x, row_of(tile).
+    template <int RO, bool STARTED, bool ASKED, bool OWN_ROW, class XAt, class Done, class RowOf>
+    __device__ inline void run_n(int32_t tiles_, int32_t rows, const i32x4 rx, XAt &&x_at, Done &&done, RowOf &&row_of)
     {
         constexpr bool STACK = PLANES == 2 && RO < 4;
         constexpr int PL = STACK ? 1 : PLANES, RI = STACK ? 2 * RO : RO;
         const int32_t q = lane >> 4, r = lane & 15, xrows = PLANES * rows;
         if constexpr (!ASKED) ask_x(0, xrows, rx, x_at);
-        if constexpr (!STARTED) start();
+        if constexpr (!STARTED) start(tiles_);
         if constexpr (STARTED && !ASKED) w4_wait<0>();
         else w4_wait<(L::DEPTH - 1) * L::COPIES>();
         order_x(0, xrows);
 
         const W4Const konst = w4_const<T>();
         uint32_t at = 0, slot = 0;   // of the ring
-        for (int32_t c = 0; c < lines; c += sp.chunk) {
+        for (int32_t c = 0; c < lines; c += chunk) {
             if (c) {
                 __syncthreads();
                 ask_x(c, xrows, rx, x_at);
                 w4_wait<0>();
                 order_x(c, xrows);
             }
-            int32_t lo, hi;
-            bounds(c, 0, lo, hi);
             // what a lane reads of x: its row's pieces j of a line's first half, any row's where it has none
             uint32_t xa[4][PL];
             auto aim_x = [&](int32_t first) {
@@ -354,17 +329,16 @@ struct W4Flow {
                     const uint32_t row = (uint32_t)(first + (STACK ? min((r & 3) / RO, 1) : pl) * rows);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        xa[j][pl] = row * (uint32_t)min(sp.chunk, lines - c) * 512u +
+                        xa[j][pl] = row * (uint32_t)min(chunk, lines - c) * 512u +
                                     16u * ((uint32_t)(G == 128 ? 4 * q + j : 4 * j + q) ^ (row & 15u));
                 }
             };
-            if constexpr (!SEGMENTS) aim_x(min((STACK ? (r & 3) % RO : r & 3) * 4 + (r >> 2), rows - 1));
-            if (lo == hi && c) continue;
-            for (int32_t tile = 0; tile < tiles; ++tile) {   // (without lines: sums of zero)
-                if constexpr (SEGMENTS) {
-                    aim_x(row_of(tile));
-                    bounds(c, tile, lo, hi);
-                }
+            if constexpr (!OWN_ROW) aim_x(min((STACK ? (r & 3) % RO : r & 3) * 4 + (r >> 2), rows - 1));
+            const int32_t last = end();
+            for (int32_t tile = first(); tile < last; ++tile) {
+                if constexpr (OWN_ROW) aim_x(row_of(tile));
+                int32_t lo, hi;
+                bounds(c, tile, lo, hi);
                 f32x4 acc = {0.f, 0.f, 0.f, 0.f};
                 for (int32_t line = lo; line < hi; ++line) {
                     copy();
@@ -425,36 +399,76 @@ struct W4Flow {
     __device__ inline void finish() { w4_wait<0>(); }
 };
 
-// A wave's sums into LDS, or (more) onto what it left there: `rows` rows of x by 16 columns.
+// f(i, row, column) for the numbers acc[i] that a lane has of `rows` rows of x by 16 columns.
 enum { W4_SLOT_LD = 16 };
-__device__ inline void w4_put(float *slot, int32_t rows, const f32x4 &acc, bool more)
+template <class F> __device__ inline void w4_rows(int32_t rows, F &&f)
 {
     const int lane = (int)(threadIdx.x & 63u), q = lane >> 4, r = lane & 15;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (4 * i + q < rows) {
-            float *s = slot + (4 * i + q) * W4_SLOT_LD + r;
-            *s = more ? *s + acc[i] : acc[i];
+        if (4 * i + q < rows) f(i, 4 * i + q, r);
+}
+// A wave's sums into LDS, or (more) onto what it left there.
+__device__ inline void w4_put(float *slot, int32_t rows, const f32x4 &acc, bool more)
+{
+    w4_rows(rows, [&](int32_t i, int32_t row, int32_t column) {
+        float *s = slot + row * W4_SLOT_LD + column;
+        *s = more ? *s + acc[i] : acc[i];
+    });
+}
+// Sums of a workgroup's tiles, in units of `per` tiles that belong together, `rows` rows each.
+// EDGES (one chunk): a unit that is a wave's alone stays in its registers, and only a wave's
+// first and last unit, which others may have parts of, need LDS.  Else all units do.
+template <bool EDGES> struct W4Sums {
+    float *const slots;
+    const int32_t units, per, rows, most;
+    __device__ inline W4Sums(char *lds, int32_t units_, int32_t per_, int32_t rows_)
+        : slots((float *)lds), units(units_), per(per_), rows(rows_), most(EDGES ? 2 : units_ / W4_WAVES + 2)
+    {
+    }
+    __device__ inline bool whole(int32_t wave, int32_t u) const
+    {
+        return EDGES && wave * units <= W4_WAVES * u && W4_WAVES * (u + 1) <= (wave + 1) * units;
+    }
+    __device__ inline float *at(int32_t wave, int32_t u, int32_t i) const   // tile i of unit u
+    {
+        const int32_t n = u - w4_first(units, wave);
+        return slots + ((wave * most + (EDGES ? min(n, 1) : n)) * per + i) * rows * W4_SLOT_LD;
+    }
+    // From all waves that have a part, in their order.
+    __device__ inline float sum(int32_t u, int32_t i, int32_t row, int32_t column) const
+    {
+        const int32_t t = u * per + i, tiles = units * per, last = (W4_WAVES * (t + 1) + tiles - 1) / tiles;
+        float v = 0.f;
+        for (int32_t w = W4_WAVES * t / tiles; w < last; ++w) v += at(w, u, i)[row * W4_SLOT_LD + column];
+        return v;
+    }
+    // f(u, row, column) for what lies in LDS.
+    template <class F> __device__ inline void each(F &&f) const
+    {
+        const int32_t n = rows * W4_SLOT_LD;
+        for (int32_t i = (int32_t)threadIdx.x; i < (EDGES ? W4_WAVES - 1 : units) * n; i += 64 * W4_WAVES) {
+            int32_t u = i / n;
+            const int32_t rest = i - u * n;
+            if constexpr (EDGES) {   // the unit in which wave u + 1 begins, unless it begins there or another did
+                const int32_t at = (u + 1) * units, before = u * units;
+                if (at % W4_WAVES == 0 || (before % W4_WAVES && before / W4_WAVES == at / W4_WAVES)) continue;
+                u = at / W4_WAVES;
+            }
+            f(u, rest / W4_SLOT_LD, rest % W4_SLOT_LD);
         }
+    }
+};
+inline int64_t w4_sums_bytes(bool edges, int64_t units, int64_t per, int64_t rows)
+{
+    return W4_WAVES * (edges ? 2 : units / W4_WAVES + 2) * per * rows * W4_SLOT_LD * 4;
 }
 
-// The split of `tiles` tiles of `lines` lines, x in chunks of at most x_bytes: about the fewest lines
-// for the busiest wave (a tenth more, where that takes fewer shares and so fewer sums to join).
-inline W4Split w4_split(int64_t tiles, int64_t lines, int64_t xrows, int64_t x_bytes)
+// Lines whose x, xrows of it, finds room in x_bytes.
+inline int32_t w4_chunk(int64_t lines, int64_t xrows, int64_t x_bytes)
 {
-    int64_t chunk = x_bytes / (512 * xrows);
-    if (chunk > lines) chunk = lines;
-    if (chunk < 1) chunk = 1;
-    W4Split best{};
-    int64_t least = 0;
-    for (int kw = W4_WAVES; kw; kw /= 2) {
-        if (kw > 1 && chunk < lines && kw > chunk) continue;
-        const int64_t each = (tiles + W4_WAVES / kw - 1) / (W4_WAVES / kw), cost = (lines + kw - 1) / kw * each;
-        if (!least || cost < least) least = cost;
-        if (!best.kw || 10 * cost <= 11 * least) best = W4Split{kw, (int32_t)each, (int32_t)chunk};
-    }
-    if (chunk < lines) best.chunk = (int32_t)(chunk / best.kw * best.kw);   // equal shares of every whole chunk
-    return best;
+    const int64_t chunk = x_bytes / (512 * xrows);
+    return (int32_t)(chunk >= lines ? lines : chunk > 0 ? chunk : 1);
 }
 
 }  // namespace lb
