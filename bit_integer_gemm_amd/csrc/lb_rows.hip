@@ -164,20 +164,16 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a)
     const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
     const int32_t here = (int32_t)min((int64_t)a.tokens, a.T - t0), half = a.R / 2;
     const int32_t h0 = (int32_t)blockIdx.y * a.heads, heads = min(a.heads, a.Hq + a.Hk - h0);
-    for (int32_t i = (int32_t)threadIdx.x; i < here * half; i += 256) {
-        const double turns = (double)a.pos[t0 + i / half] * (a.freqs[i % half] * 0.15915494309189533577);
-        const float x = (float)(turns - __builtin_rint(turns));
-        float sn, cs;
-        sincospif(2.0f * x, &sn, &cs);
-        turn[i] = f32x2{cs * a.mult, sn * a.mult};
-    }
-    __syncthreads();
-    const int32_t turned = PAIRS ? a.R / 8 : a.R / 16;
-    const int32_t items = a.items;
-    for (int32_t n = (int32_t)threadIdx.x; n < here * heads * items; n += 256) {
-        const int32_t j = n % items, rest = n / items, h = h0 + rest % heads, t = rest / heads;
+    const int32_t turned = PAIRS ? a.R / 8 : a.R / 16, items = a.items, all = here * heads * items;
+    // item n's numbers, read ahead of the angles that they wait for
+    float x[8], b[8];
+    T *out;
+    int32_t j, t;
+    auto read = [&](int32_t n) {
+        j = n % items;
+        const int32_t rest = n / items, h = h0 + rest % heads;
+        t = rest / heads;
         const T *in;
-        T *out;
         if (h < a.Hq) {
             in = (const T *)a.q + (t0 + t) * a.ldq + (int64_t)h * a.D;
             out = (T *)a.qo + (t0 + t) * a.ldqo + (int64_t)h * a.D;
@@ -185,35 +181,52 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a)
             in = (const T *)a.k + (t0 + t) * a.ldk + (int64_t)(h - a.Hq) * a.D;
             out = (T *)a.ko + (t0 + t) * a.ldko + (int64_t)(h - a.Hq) * a.D;
         }
-        if (j >= turned) {   // not turned: copied
-            const int32_t at = a.R + 8 * (j - turned);
-            float x[8];
-            load8<T>(in + at, x);
-            store8<T>(out + at, x);
-            continue;
+        const int32_t at = j < turned ? 8 * j : a.R + 8 * (j - turned);   // (behind R: copied)
+        out += at;
+        load8<T>(in + at, x);
+        if (!PAIRS && j < turned) load8<T>(in + half + at, b);
+    };
+    int32_t n = (int32_t)threadIdx.x, i = n;
+    int64_t pos = a.pos[t0 + min(i / half, here - 1)];
+    double freq = a.freqs[i % half];
+    if (n < all) read(n);
+    for (; i < here * half; i += 256) {
+        if (i >= 256) {
+            pos = a.pos[t0 + i / half];
+            freq = a.freqs[i % half];
         }
+        const double turns = (double)pos * (freq * 0.15915494309189533577);
+        const float part = (float)(turns - __builtin_rint(turns));
+        float sn, cs;
+        sincospif(2.0f * part, &sn, &cs);
+        turn[i] = f32x2{cs * a.mult, sn * a.mult};
+    }
+    __syncthreads();
+    while (n < all) {
         const f32x2 *tn = turn + t * half;
-        float x[8], y[8];
-        load8<T>(in + 8 * j, x);
-        if constexpr (PAIRS) {
+        if (j < turned) {
+            if constexpr (PAIRS) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const f32x2 c = tn[4 * j + e];
-                y[2 * e] = x[2 * e] * c.x - x[2 * e + 1] * c.y;
-                y[2 * e + 1] = x[2 * e + 1] * c.x + x[2 * e] * c.y;
-            }
-        } else {
-            float b[8];
-            load8<T>(in + half + 8 * j, b);
+                for (int e = 0; e < 4; ++e) {
+                    const f32x2 c = tn[4 * j + e];
+                    const float first = x[2 * e];
+                    x[2 * e] = first * c.x - x[2 * e + 1] * c.y;
+                    x[2 * e + 1] = x[2 * e + 1] * c.x + first * c.y;
+                }
+            } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const f32x2 c = tn[8 * j + e];
-                y[e] = x[e] * c.x - b[e] * c.y;
-                b[e] = b[e] * c.x + x[e] * c.y;
+                for (int e = 0; e < 8; ++e) {
+                    const f32x2 c = tn[8 * j + e];
+                    const float first = x[e];
+                    x[e] = first * c.x - b[e] * c.y;
+                    b[e] = b[e] * c.x + first * c.y;
+                }
+                store8<T>(out + half, b);
             }
-            store8<T>(out + half + 8 * j, b);
         }
-        store8<T>(out + 8 * j, y);
+        store8<T>(out, x);
+        n += 256;
+        if (n < all) read(n);
     }
 }
 
@@ -221,15 +234,13 @@ template <class T> static hipError_t rope_t(RopeArgs a, bool pairs, bool in_plac
 {
     const int32_t heads = a.Hq + a.Hk, turned = pairs ? a.R / 8 : a.R / 16;
     a.items = in_place ? turned : turned + (a.D - a.R) / 8;
-    // Few tokens: workgroups of about one item to a thread.  Many: tokens together, until
-    // their angles fill a workgroup's threads, with all heads.
+    // Few tokens: workgroups of about one item to a thread.  Many: all heads of a token, or of several
+    // that give every thread an item (8191 tokens of 40 heads in workgroups of 1, 2, 4 and 8 tokens:
+    // 37, 38, 39 and 41 us).
     a.tokens = 1;
     a.heads = heads;
-    if (a.T >= 4 * (int64_t)cu) {
-        a.tokens = max(1, min(8, 512 / (a.R / 2)));
-    } else {
-        a.heads = max(1, min(heads, (256 + a.items - 1) / a.items));
-    }
+    if (a.T >= 4 * (int64_t)cu) a.tokens = max(1, min(256 / (heads * a.items), ROPE_ANGLES / (a.R / 2)));
+    else a.heads = max(1, min(heads, (256 + a.items - 1) / a.items));
     if (a.heads < (heads + 65534) / 65535) a.heads = (heads + 65534) / 65535;
     const int64_t most = LAUNCH_THREADS / 256 / ((heads + a.heads - 1) / a.heads) * a.tokens;
     const int64_t T_all = a.T;
