@@ -43,6 +43,7 @@ LB_ROPE_HALF, LB_ROPE_PAIRS = 0, 1   # lb_rope_layout
 LB_ROPE_PLAIN, LB_ROPE_LINEAR, LB_ROPE_BASE, LB_ROPE_PARTS, LB_ROPE_BANDS = range(5)   # lb_rope_scaling
 W4_GROUPS = (32, 64, 128)
 W4_K_MAX = 1048576
+W4_N_MAX = 16777216
 NORM_H_MAX = 32768
 MOE_EXPERTS_MAX = 1024
 MOE_TOP_MAX = 64

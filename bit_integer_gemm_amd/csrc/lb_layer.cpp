@@ -35,7 +35,7 @@ int check_w4(int64_t M, int64_t N, int64_t K, int64_t group, int ftype)
         return LB_ERR_SHAPE;
     if (K % group != 0) return LB_ERR_ALIGN;
     if (!short_ftype(ftype)) return LB_ERR_VARIANT;
-    if (K > LB_W4_K_MAX) return LB_ERR_OVERFLOW;
+    if (K > LB_W4_K_MAX || N > LB_W4_N_MAX) return LB_ERR_OVERFLOW;
     return LB_OK;
 }
 // Byte offsets between 64 rows of x are 32-bit.

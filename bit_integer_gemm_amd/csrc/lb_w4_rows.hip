@@ -456,8 +456,9 @@ int64_t linear_w4_rows_workspace(int64_t M, int64_t N, int64_t K, int64_t group,
 template <class T, int G, int WM, int WN> static hipError_t rows_launch(RowsArgs r, hipStream_t s)
 {
     typedef RowsLds<G, WM, WN> L;
+    // (N is bounded, and parts of K are made only of products of few tiles: one launch)
     const int64_t tn = (r.N + L::BN - 1) / L::BN, M = r.M, most = LAUNCH_THREADS / 512 / tn / r.splits * L::BM;
-    if (most < L::BM || (r.splits > 1 && most < M)) return hipErrorInvalidValue;
+    if (most < (r.splits > 1 ? M : L::BM)) return hipErrorInvalidValue;
     for (int64_t m = 0; m < M; m += most) {
         RowsArgs q = r;
         q.x = (const T *)r.x + m * r.Kp;
@@ -506,14 +507,10 @@ template <class T, int G> static hipError_t rows_t(const W4Args &a, int cu, void
         const hipError_t e = b.tile == 0 ? rows_launch<T, G, 2, 2>(r, s) : b.tile == 1 ? rows_launch<T, G, 2, 1>(r, s) : rows_launch<T, G, 1, 1>(r, s);
         if (e != hipSuccess) return e;
         if (b.splits > 1) {
-            const int64_t n = a.M * a.N, each = LAUNCH_THREADS / 256 * 1024;
-            for (int64_t i0 = 0; i0 < n; i0 += each) {   // (one launch: a split product is small)
-                const int64_t here = std::min(each, n - i0);
-                if (i0) return hipErrorInvalidValue;
-                hipLaunchKernelGGL((w4_join_kernel<T>), dim3((uint32_t)((here + 1023) / 1024)), dim3(256), 0, s,
-                                   (const float *)((char *)workspace + sp.sums), (const T *)a.bias, (T *)a.out, here, rows_apart(a.M, a.N),
-                                   (int32_t)a.N, (int32_t)b.splits);
-            }
+            const int64_t n = a.M * a.N;
+            hipLaunchKernelGGL((w4_join_kernel<T>), dim3((uint32_t)((n + 1023) / 1024)), dim3(256), 0, s,
+                               (const float *)((char *)workspace + sp.sums), (const T *)a.bias, (T *)a.out, n, rows_apart(a.M, a.N),
+                               (int32_t)a.N, (int32_t)b.splits);
         }
     }
     return hipGetLastError();

@@ -415,15 +415,18 @@ int lb_rope_freqs(double *freqs, float *mult, int64_t R, double base, int scalin
  *   W: N rows of K/2 bytes, levels u in 0..15, even k in the low nibble; Wp: N x K/group x
  *   2 of ftype, the scale s and the minimum b of each group (signed levels -8..7 with a
  *   scale alone: u = level + 8, b = -8 s, which is exact).  group is 32, 64 or 128 and
- *   divides K <= LB_W4_K_MAX.  X (ldx elements between rows), bias (N, or NULL) and out
- *   (dense) are of ftype, bf16 or fp16.
+ *   divides K <= LB_W4_K_MAX; N <= LB_W4_N_MAX.  X (ldx <= 2^24 elements between rows), bias
+ *   (N, or NULL) and out (dense) are of ftype, bf16 or fp16.
  * Products are exact, sums and the groups' numbers fp32, out is rounded once; what comes
  * from a row of X that holds an infinity or a NaN is not finite (NaN or infinite).  The sums run
- * over 16 + u in place of u: up to four times fp32's rounding of the sum.
+ * over 16 + u in place of u: up to four times fp32's rounding of the sum; with more than 16
+ * rows, the minima's part (b - 16 s) sum_k X is held in two bf16 parts each (2^-16 of it).
  * workspace: at least lb_linear_w4_workspace(M, K, N, group) bytes (LB_ERR_WORKSPACE
- * otherwise; NULL where that is 0).
+ * otherwise; NULL where that is 0, as for up to 16 rows).  It depends on the current device's
+ * number of compute units too: ask on the device that the call runs on.
  */
 #define LB_W4_K_MAX 1048576
+#define LB_W4_N_MAX 16777216
 int lb_linear_w4(const void *X, int64_t ldx, const uint8_t *W, const void *Wp, const void *bias, void *out,
                  int64_t M, int64_t N, int64_t K, int64_t group, int ftype, void *workspace,
                  int64_t workspace_bytes, void *stream);
@@ -435,14 +438,14 @@ int64_t lb_linear_w4_workspace(int64_t M, int64_t K, int64_t N, int64_t group);
  *   ones the lowest index first); q_j = scale * p_{e_j}, with renorm != 0 divided by the
  *   sum of the chosen p;
  *   out = sum_j q_j W2_{e_j} (silu(Wg_{e_j} x) * (Wu_{e_j} x)),  silu(v) = v / (1 + exp(-v)).
- *   X: T x H (ldx apart), Wr: E x H, out: T x H dense, all of ftype (bf16 or fp16).
+ *   X: T x H (ldx <= 2^24 apart), Wr: E x H, out: T x H dense, all of ftype (bf16 or fp16).
  *   W1, P1: E x 2I rows of H weights, the I gate rows of an expert before its I up rows;
  *   W2, P2: E x H rows of I weights; both laid out as lb_linear_w4's W and Wp.
  *   ids (T x top_k int32) and weights (T x top_k fp32) receive e_j and q_j; either may be
  *   NULL.
  * fp32 sums; between the two products silu(..) * (..) is held in two bf16 parts (2^-17 of
- * it).  A NaN among a token's logits counts as the largest and makes its row NaN.  Sums
- * have a fixed order: the same arguments give the same bits.
+ * it).  A NaN among a token's logits counts as the largest and makes its row NaN, as an
+ * infinite one does.  Sums have a fixed order: the same arguments give the same bits.
  * group divides H and I.  E <= LB_MOE_EXPERTS_MAX, top_k <= min(E, LB_MOE_TOP_MAX); H * I is
  * bounded (LB_ERR_OVERFLOW above about 2^33).  More than 64 tokens run 64 at a time, each time
  * reading the weights again.  workspace: at least lb_moe_w4_workspace() bytes

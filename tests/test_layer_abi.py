@@ -160,3 +160,16 @@ def test_binding_checks_without_a_gpu():
     w2, p2 = torch.zeros(2, 64, 16, dtype=torch.uint8), torch.zeros(2, 64, 1, 2, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="GPU"):
         lb.lb_moe_w4(x, torch.zeros(2, 64, dtype=torch.bfloat16), w1, p1, w2, p2, torch.zeros_like(x), top_k=1)
+
+
+def test_sizes_beyond_the_limits(lib):
+    """More columns than a launch covers; rows too far apart; the limit itself is the header's."""
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(lb.__file__), "..", "include", "lb_gemm.h")).read()
+    assert int(re.search(r"#define LB_W4_N_MAX (\d+)", text).group(1)) == lb.W4_N_MAX
+    a = Args(X=P, ldx=128, W=P, Wp=P, bias=NULL, out=P, M=3, N=64, K=128, group=64, ftype=lb.LB_BF16, ws=NULL, bytes=0, stream=NULL)
+    refusals(lib.lb_linear_w4, a, [(lb.LB_ERR_OVERFLOW, dict(N=lb.W4_N_MAX + 1)), (lb.LB_ERR_OVERFLOW, dict(M=40, N=lb.W4_N_MAX + 16)),
+                                   (lb.LB_ERR_OVERFLOW, dict(ldx=2 ** 24 + 8))])
+    assert lb.lb_linear_w4_workspace(40, 128, lb.W4_N_MAX + 16, 64) == 0
+    assert lb.lb_linear_w4_workspace(40, 128, lb.W4_N_MAX, 64) > 0
