@@ -186,14 +186,19 @@ struct W4Flow {
         lo = c + min(max(all * wave / W4_WAVES - before, 0), n);
         hi = c + min(max(all * (wave + 1) / W4_WAVES - before, 0), n);
     }
-    // The tile that is copied next: the first from c_tile on of which this wave has lines.
+    // The tile that is copied next: the first from c_tile on of which this wave has lines.  Behind the
+    // last one nothing is read: size 0, and no scalar offset, which the range check subtracts from
+    // the size (0 less an offset would let everything pass, and the line behind the weights be read).
     __device__ inline void next_tile()
     {
         for (left = false;; ++c_tile) {
             if (c_tile >= end()) {
                 c_chunk += chunk;
                 c_tile = first();
-                if (c_chunk >= lines) return;
+                if (c_chunk >= lines) {
+                    rw.z = rp.z = c_line = 0;
+                    return;
+                }
             }
             bounds(c_chunk, c_tile, c_line, c_hi);
             left = c_line < c_hi;
@@ -225,7 +230,6 @@ struct W4Flow {
         if (left && ++c_line == c_hi) {
             ++c_tile;
             next_tile();
-            if (!left) rw.z = rp.z = 0;
         }
     }
     // Asks for the first lines of tiles_ tiles.
