@@ -15,6 +15,14 @@
 // transposed between the 16-lane rows, so that each instruction covers 32 consecutive
 // weights.  Eight nibbles of a word come out in the order 0 4 1 5 2 6 3 7, and x is put in
 // the same order, once, in LDS.
+//
+// What bounds it: a line costs a wave some 100 vector instructions (G = 128; 170 for G = 32,
+// whose eight groups are each scaled) beside 16 matrix instructions, which eight waves hide
+// under 5 TB/s of weights, except for G = 32 (about 4 TB/s).  Beyond that a launch is latencies:
+// about 2 us until a kernel runs, 1 to 2 for x, 2 for the first weights, 1 for the join: 9 us
+// for the first product of 5 tokens where there is hardly a weight to read.  Rings of two, three
+// and four lines, and 16 waves in place of eight, are within 2% of each other; two workgroups
+// to a compute unit are slower.
 #pragma once
 
 #include "lb_float.hpp"
@@ -209,13 +217,18 @@ struct W4Flow {
         rp = make_rsrc(P + t.row * groups, (uint64_t)(uint32_t)t.rows * groups * 4u);
     }
     // The next line into the ring: piece p of row i lies at p ^ i / 2 (the rows' pieces that 16 lanes
-    // read together then lie on all 64 banks).  Past the last line nothing is read.  (Past the end of
-    // a row the next one's weights are, which meet zeros of x; its groups' numbers are not taken.)
+    // read together then lie on all 64 banks).  Past the last line nothing is read, nor past the end
+    // of a row: no copy relies on how a range check counts the scalar offset.
     __device__ inline void copy()
     {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) w4_copy16(rw, w_at[i], (uint32_t)c_line * 128u, c_at + 1024u * (uint32_t)i);
         const int32_t have = (int32_t)groups - c_line * GROUPS;
+        uint32_t at[2] = {w_at[0], w_at[1]};
+        if (have < GROUPS)   // the row ends in this line
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if ((uint32_t)c_line * 128u + 16u * (uint32_t)((lane & 7) ^ (4 * i + (lane >> 4))) >= kb) at[i] = 0xFFFFFFF0u;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) w4_copy16(rw, at[i], (uint32_t)c_line * 128u, c_at + 1024u * (uint32_t)i);
 #pragma unroll
         for (int i = 0; i < L::COPIES - 2; ++i) {
             uint32_t at = p_at[i];
