@@ -279,7 +279,7 @@ LINEAR = [(1, 1, 32, 32), (1, 16, 128, 128), (1, 4096, 512, 64), (1, 333, 4096, 
 LINEAR_WIDE = [(600, 9000, 256, 128), (601, 8999, 160, 32), (1030, 8193, 128, 64), (1030, 8200, 320, 64), (1000, 4001, 2048, 128),
                (1000, 4000, 1952, 32), (3000, 2816, 256, 32), (40, 300, 8192, 128), (1, 40, 65536, 128), (2, 5, 131072, 32),
                (16, 130, 11008, 64), (14, 20000, 96, 32), (1, 70000, 64, 64),
-               (1, 20480, 1024, 128), (9, 20480, 1024, 32)]   # (weights that fill an allocation of whole pages to its end)
+               (1, 20480, 1024, 128), (9, 20480, 1024, 32), (2, 32768, 640, 128)]   # (weights that fill an allocation of whole pages to its end)
 
 
 @pytest.mark.parametrize("dtype", [BF, HF])
