@@ -8,9 +8,10 @@ namespace lb {
 
 // Up to 16 rows: a workgroup takes all of x against some tiles of 16 columns.  1 x 4096 x 4096
 // (G = 128) in 5.9 us (a launch and three latencies; the bytes alone would take 1.8), 8 x 11008 x
-// 4096 (G = 64) in 11.5 us, 2.3 TB/s.
-// EARLY: weights are asked for before x; a row or two of x are there before the first weights, and
-// are asked for first.
+// 4096 (G = 64) in 10.5 us, 2.5 TB/s.  x is asked for first: with the weights first, the latter take
+// 11.7.  16 x 4096 x 4096 and 16 x 11008 x 4096 take 10.4 and 12.9 us, where the tiles for more
+// rows take 18.5 and 27.5 (their three launches); 17 x 4096 x 4096 takes 18.1 there, and would
+// take about 20 here, all weights twice.
 // ONE: all of x is in LDS at once.
 struct FewArgs {
     const uint8_t *w;
@@ -19,7 +20,7 @@ struct FewArgs {
     int32_t M, N, K;
     int32_t per, chunk;   // tiles of a workgroup, lines whose x is in LDS together
 };
-template <class T, int G, bool EARLY, bool ONE>
+template <class T, int G, bool ONE>
 __global__ __launch_bounds__(64 * W4_WAVES) void w4_few_kernel(const T *__restrict__ X, const T *__restrict__ bias,
                                                                   T *__restrict__ out, FewArgs a)
 {
@@ -34,8 +35,7 @@ __global__ __launch_bounds__(64 * W4_WAVES) void w4_few_kernel(const T *__restri
     };
     auto tile_at = [&](int32_t t) { return W4Tile{(int64_t)(t0 + t) * 16, min(16, a.N - (t0 + t) * 16)}; };
     W4Flow<T, T, G, 1, decltype(tile_at)> flow(smem, x_bytes, a.w, a.p, a.K, a.chunk, tile_at);
-    if constexpr (EARLY) flow.start(tiles);
-    flow.template run<EARLY, false>(
+    flow.template run<false, false>(
         tiles, rows, make_rsrc(X, 0xFFFFFFF0u), [&](int32_t row) { return (uint32_t)row * (uint32_t)a.ldx * 2u; },
         [&](int32_t t, const f32x4 &acc, bool more) {
             if (!sums.whole(wave, t)) return w4_put(sums.at(wave, t, 0), rows, acc, more);
@@ -62,9 +62,8 @@ template <class T, int G> static hipError_t w4_g(const W4Args &a, int cu, hipStr
     const dim3 grid((uint32_t)wgs), block(64 * W4_WAVES);
     const T *x = (const T *)a.x, *bias = (const T *)a.bias;
     T *out = (T *)a.out;
-    if (!one) hipLaunchKernelGGL((w4_few_kernel<T, G, false, false>), grid, block, lds, s, x, bias, out, f);
-    else if (a.M > 2) hipLaunchKernelGGL((w4_few_kernel<T, G, true, true>), grid, block, lds, s, x, bias, out, f);
-    else hipLaunchKernelGGL((w4_few_kernel<T, G, false, true>), grid, block, lds, s, x, bias, out, f);
+    if (one) hipLaunchKernelGGL((w4_few_kernel<T, G, true>), grid, block, lds, s, x, bias, out, f);
+    else hipLaunchKernelGGL((w4_few_kernel<T, G, false>), grid, block, lds, s, x, bias, out, f);
     return hipGetLastError();
 }
 
