@@ -270,7 +270,7 @@ __device__ inline int32_t moe_route(const MoeArgs &a, const MoeGrid &g, const fl
         expert = a.E <= 64 ? nth_expert<1>(logits, a.E, p.slot) : a.E <= 128 ? nth_expert<2>(logits, a.E, p.slot)
                : a.E <= 256 ? nth_expert<4>(logits, a.E, p.slot) : nth_expert<16>(logits, a.E, p.slot);
         start();
-        if (tid == 0) l.rank[0] = l.row[0] = p.slot;
+        if (tid == 0) l.row[0] = p.slot;
         __syncthreads();
         return 1;
     }
@@ -328,13 +328,14 @@ __device__ inline int32_t moe_route(const MoeArgs &a, const MoeGrid &g, const fl
 // ---- gate and up, activation -----------------------------------------------
 // A workgroup: an expert, some blocks of 16 columns (a tile of gate rows and one of up rows
 // each), g.rows of its tokens at a time.
-// ONE: all of a row of x is in LDS at once.  EARLY (and ONE): x, all tokens' (at most g.rows), is
-// asked for before the expert is known.
+// ONE: all of a row of x is in LDS at once.  x is asked for when the tokens are known: all tokens'
+// rows ahead of that take 1.5 us more of 26 (5 tokens of 6 of 64: more rows to put in order and to
+// scale).
 // ROUTE (one router tile, at most 16 tokens and experts, of at most 128 KB): every workgroup forms
 // the logits for itself, which takes a us where a launch for them takes five (one token of 2 of 8:
 // 46 us in all, 50 with the launch).  Beyond that each workgroup would read more than its share
 // of weights.
-template <class T, int G, bool ONE, bool EARLY, bool ROUTE>
+template <class T, int G, bool ONE, bool ROUTE>
 __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGrid g)
 {
     extern __shared__ __attribute__((aligned(1024))) char smem[];
@@ -343,15 +344,10 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGri
     MoePlace p = {};
     __bf16 *const hi = (__bf16 *)a.h, *const lo = hi + (int64_t)a.T * a.top_k * a.I;
     auto put = [&](int32_t m, int32_t c, float gate, float up) {
-        int32_t row = list.row[m];
-        if constexpr (EARLY) {   // row m is token m, perhaps of other experts alone
-            if (list.rank[m] < 0) return;
-            row = m * a.top_k + list.rank[m];
-        }
         // (a quotient and an exponential good to 2^-21)
         const float h = gate / (1.0f + __expf(-gate)) * up;
         // in the order in which the down product's nibbles come
-        const int64_t o = (int64_t)row * a.I + p.first * 16 + (c & ~7) + 2 * (c & 3) + (c >> 2 & 1);
+        const int64_t o = (int64_t)list.row[m] * a.I + p.first * 16 + (c & ~7) + 2 * (c & 3) + (c >> 2 & 1);
         const __bf16 top = (__bf16)h;
         hi[o] = top;
         lo[o] = (__bf16)(h - (float)top);
@@ -360,7 +356,6 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGri
     auto tile_at = [&](int32_t t) { return W4Tile{((int64_t)expert * 2 + t % 2) * a.I + (p.first + t / 2) * 16, 16}; };
     W4Flow<T, T, G, 1, decltype(tile_at)> flow(smem, g.x_bytes, a.w1, (const uint32_t *)a.p1, a.H, g.chunk, tile_at);
     const i32x4 rx = make_rsrc(a.x, 0xFFFFFFF0u);
-    if constexpr (EARLY) flow.ask_x(0, a.T, rx, [&](int32_t i) { return (uint32_t)i * (uint32_t)a.ldx * 2u; });
     const float *logits = a.logits;
     if constexpr (ROUTE) {
         const float v = router_tile<T, W4_WAVES>(a, 0, 0, (float *)(smem + g.x_bytes));   // (where the rings will be)
@@ -386,7 +381,7 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGri
     }
     if (count == 0) flow.finish();
     for (int32_t at = 0; at < count; at += g.rows) {
-        const int32_t rows = EARLY ? a.T : min(g.rows, count - at);
+        const int32_t rows = min(g.rows, count - at);
         const W4Sums<ONE> sums(smem + g.x_bytes + W4Lds<G>::RINGS, p.have, 2, rows);
         f32x4 gate = {0.f, 0.f, 0.f, 0.f};
         auto x_at = [&](int32_t i) { return (uint32_t)(list.row[at + i] / a.top_k) * (uint32_t)a.ldx * 2u; };
@@ -396,14 +391,13 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGri
             else w4_rows(rows, [&](int32_t i, int32_t m, int32_t c) { put(at + m, t / 2 * 16 + c, gate[i], acc[i]); });
         };
         if (at == 0) {
-            flow.template run<true, EARLY>(2 * p.have, rows, rx, x_at, done);
-        } else if constexpr (!EARLY) {
+            flow.template run<true>(2 * p.have, rows, rx, x_at, done);
+        } else {
             __syncthreads();
-            flow.template run<false, false>(2 * p.have, rows, rx, x_at, done);
+            flow.template run<false>(2 * p.have, rows, rx, x_at, done);
         }
         __syncthreads();
         sums.each([&](int32_t u, int32_t m, int32_t c) { put(at + m, u * 16 + c, sums.sum(u, 0, m, c), sums.sum(u, 1, m, c)); });
-        if constexpr (EARLY) return;
     }
 }
 
@@ -439,10 +433,10 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_kernel(MoeArgs a, MoeG
             w4_rows(rows, [&](int32_t i, int32_t m, int32_t c) { put(t, m, c, acc[i]); });
         };
         if (at == 0) {
-            flow.template run<true, false>(p.have, rows, rx, x_at, done);
+            flow.template run<true>(p.have, rows, rx, x_at, done);
         } else {
             __syncthreads();
-            flow.template run<false, false>(p.have, rows, rx, x_at, done);
+            flow.template run<false>(p.have, rows, rx, x_at, done);
         }
         __syncthreads();
         sums.each([&](int32_t t, int32_t m, int32_t c) { put(t, m, c, sums.sum(t, 0, m, c)); });
@@ -491,7 +485,7 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_token_kernel(MoeArgs a
         if (a.ids) a.ids[row] = expert;
         if (a.weights) a.weights[row] = weight;
     }
-    flow.template run_n<1, true, false, true>(
+    flow.template run_n<1, true, true>(
         k * have, k, rx, x_at,
         [&](int32_t t, const f32x4 &acc, bool) {
             const float q = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(weight), t % k));
@@ -608,14 +602,12 @@ template <class T, int G> static hipError_t moe_t(const MoeArgs &a, int cu, hipS
 {
     const dim3 block(64 * W4_WAVES);
     MoeShape up = moe_shape<G>(a, a.I / 16, a.H, 1, 2, cu), dn = moe_shape<G>(a, a.H / 16, a.I, 2, 1, cu);
-    const bool early = a.T <= up.g.rows && up.g.one;   // all of x at once
     if (up.lds > MOE_LDS || dn.lds > MOE_LDS) return hipErrorInvalidValue;
-    const bool route = early && a.E <= 16 && a.T <= 16 && a.E * a.H <= 65536;
+    const bool route = up.g.one && a.E <= 16 && a.T <= 16 && a.E * a.H <= 65536;
     if (!route) hipLaunchKernelGGL((moe_router_kernel<T>), dim3((uint32_t)(a.E + 15) / 16, (uint32_t)(a.T + 15) / 16), dim3(64 * ROUTER_WAVES), 0, s, a);
-    if (route) hipLaunchKernelGGL((moe_up_kernel<T, G, true, true, true>), dim3(up.wgs), block, up.lds, s, a, up.g);
-    else if (early) hipLaunchKernelGGL((moe_up_kernel<T, G, true, true, false>), dim3(up.wgs), block, up.lds, s, a, up.g);
-    else if (up.g.one) hipLaunchKernelGGL((moe_up_kernel<T, G, true, false, false>), dim3(up.wgs), block, up.lds, s, a, up.g);
-    else hipLaunchKernelGGL((moe_up_kernel<T, G, false, false, false>), dim3(up.wgs), block, up.lds, s, a, up.g);
+    if (route) hipLaunchKernelGGL((moe_up_kernel<T, G, true, true>), dim3(up.wgs), block, up.lds, s, a, up.g);
+    else if (up.g.one) hipLaunchKernelGGL((moe_up_kernel<T, G, true, false>), dim3(up.wgs), block, up.lds, s, a, up.g);
+    else hipLaunchKernelGGL((moe_up_kernel<T, G, false, false>), dim3(up.wgs), block, up.lds, s, a, up.g);
     if (a.T == 1) {   // all of its experts' activations in LDS, if they find room there
         const int32_t tiles = a.H / 16, per = (tiles + cu - 1) / cu;
         const uint32_t x_bytes = W4Lds<G>::x_bytes(2 * a.top_k, (a.I + 255) / 256);

@@ -35,7 +35,7 @@ __global__ __launch_bounds__(64 * W4_WAVES) void w4_few_kernel(const T *__restri
     };
     auto tile_at = [&](int32_t t) { return W4Tile{(int64_t)(t0 + t) * 16, min(16, a.N - (t0 + t) * 16)}; };
     W4Flow<T, T, G, 1, decltype(tile_at)> flow(smem, x_bytes, a.w, a.p, a.K, a.chunk, tile_at);
-    flow.template run<false, false>(
+    flow.template run<false>(
         tiles, rows, make_rsrc(X, 0xFFFFFFF0u), [&](int32_t row) { return (uint32_t)row * (uint32_t)a.ldx * 2u; },
         [&](int32_t t, const f32x4 &acc, bool more) {
             if (!sums.whole(wave, t)) return w4_put(sums.at(wave, t, 0), rows, acc, more);

@@ -300,32 +300,31 @@ struct W4Flow {
 
     // `rows` rows of x through rx, row i's first byte at x_at(i) (PLANES 2: rows from `rows` on are
     // the second plane's).  STARTED: start() has been called, and the weights' latency runs beside
-    // the copy of x; else start(tiles_) comes after it, and beside the putting in order.  ASKED:
-    // ask_x() has been called, before start().
+    // the copy of x; else start(tiles_) comes after it, and beside the putting in order.
     //   done(t, acc, more): sums of tile t over this wave's lines; acc[i] is row 4 i + lane / 16, column
     //     lane % 16 of the tile.  Called for each chunk (more: not the first) and each of the
     //     wave's tiles, also one without lines.
-    template <bool STARTED, bool ASKED, class XAt, class Done>
+    template <bool STARTED, class XAt, class Done>
     __device__ inline void run(int32_t tiles_, int32_t rows, const i32x4 rx, XAt &&x_at, Done &&done)
     {
         auto none = [](int32_t) { return 0; };
-        if (rows <= 4) run_n<1, STARTED, ASKED, false>(tiles_, rows, rx, x_at, done, none);
-        else if (rows <= 8) run_n<2, STARTED, ASKED, false>(tiles_, rows, rx, x_at, done, none);
-        else run_n<4, STARTED, ASKED, false>(tiles_, rows, rx, x_at, done, none);
+        if (rows <= 4) run_n<1, STARTED, false>(tiles_, rows, rx, x_at, done, none);
+        else if (rows <= 8) run_n<2, STARTED, false>(tiles_, rows, rx, x_at, done, none);
+        else run_n<4, STARTED, false>(tiles_, rows, rx, x_at, done, none);
     }
     // RO: at most 4 RO rows.  A matrix instruction's row 4 q + i, whose sums are in lanes q of register
     // i, takes row 4 i + q, so that few rows need few registers scaled.  Two planes of at most 8 rows
     // are rows of one instruction, the second plane's sums RO registers behind the first's.
     // OWN_ROW: a tile has one row of x, row_of(tile).
-    template <int RO, bool STARTED, bool ASKED, bool OWN_ROW, class XAt, class Done, class RowOf>
+    template <int RO, bool STARTED, bool OWN_ROW, class XAt, class Done, class RowOf>
     __device__ inline void run_n(int32_t tiles_, int32_t rows, const i32x4 rx, XAt &&x_at, Done &&done, RowOf &&row_of)
     {
         constexpr bool STACK = PLANES == 2 && RO < 4;
         constexpr int PL = STACK ? 1 : PLANES, RI = STACK ? 2 * RO : RO;
         const int32_t q = lane >> 4, r = lane & 15, xrows = PLANES * rows;
-        if constexpr (!ASKED) ask_x(0, xrows, rx, x_at);
+        ask_x(0, xrows, rx, x_at);
         if constexpr (!STARTED) start(tiles_);
-        if constexpr (STARTED && !ASKED) w4_wait<0>();
+        if constexpr (STARTED) w4_wait<0>();
         else w4_wait<(L::DEPTH - 1) * L::COPIES>();
         order_x(0, xrows);
 
