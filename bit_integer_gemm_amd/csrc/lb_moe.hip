@@ -16,7 +16,7 @@
 // Bound by the chosen experts' weights, read once (2 of 8 of 4096 x 11008: 98.6 MB in 27 us and
 // 48.8 in 15; 122 of 128 of 2048 x 1024, met by 48 tokens: 262 MB in 57 us, 4.6 TB/s, and 133 in
 // 36), and by what each launch takes before its first weights: 9 us for the first product of 5
-// tokens, 6 for the second.  5 tokens of 6 of 64 experts of 2048 x 1376, G = 32: 4.8 + 26.8 + 17.0
+// tokens, 6 for the second.  5 tokens of 6 of 64 experts of 2048 x 1376, G = 32: 4.8 + 25.9 + 17.0
 // + 5.0 us, where the bytes would take 26.
 #include <algorithm>
 
