@@ -2,10 +2,13 @@
 //
 // Per group g of G weights, with u' = 16 + u exact in 16 bits and b' = b - 16 s (lb_w4.hpp):
 //   out = sum_g b'[n,g] X[m,g] + sum_g s[n,g] sum_{k in g} x[m,k] u'[n,k],  X[m,g] = sum_{k in g} x[m,k].
-// The first term is a product of its own with K / G in place of K, from which the accumulators
-// start: X and b' in two bf16 parts each (2^-16 of a term).  The second is exact products summed
-// in fp32, a group at a time into a second set of accumulators, which are scaled into the
-// first: no weight is ever rounded.
+// The first term is a product of its own with K / G in place of K: X and b' in three bf16 parts
+// each (2^-23 of a term; two parts, 2^-16, cost fp16 outputs up to 1.4 times their rounding where
+// activations have a mean).  The second is exact products summed in fp32, a group at a time into a
+// second set of accumulators, which are scaled into the first: no weight is ever rounded.  The
+// terms have opposite signs, so that they enter the accumulators 16 groups of the one before the
+// same groups of the other: with all of the first ahead of the second, fp32's roundings of what
+// cancels later are as large as those of two parts (11008 weights in groups of 32).
 //
 // 4096 x 11008 x 4096 (G = 128): 342 us for ten whole rounds of 128 x 256 tiles and 43 for the
 // columns that are left, 960 TFLOP/s; the matrix cores are busy 46% of the time at the 2.04 GHz
@@ -26,7 +29,7 @@
 namespace lb {
 
 // ---- x in order, and its groups' sums --------------------------------------
-// 8 numbers to a thread.  x: M x Kp of T; parts: two planes of M x groups16 bf16, X = their sum.
+// 8 numbers to a thread.  x: M x Kp of T; parts: three planes of M x groups16 bf16, X = their sum.
 template <class T, int G>
 __global__ __launch_bounds__(256) void w4_prepare_kernel(const T *__restrict__ X, int64_t ldx, T *__restrict__ x,
                                                          __bf16 *__restrict__ parts, int32_t M, int32_t K, int32_t Kp,
@@ -43,9 +46,12 @@ __global__ __launch_bounds__(256) void w4_prepare_kernel(const T *__restrict__ X
     if (at < Kp) *(u32x4 *)(x + (int64_t)m * Kp + at) = w4_order(v);
     const int32_t g = at / G;
     if (at % G == 0 && g < groups16) {
-        const __bf16 hi = (__bf16)s, lo = (__bf16)(s - (float)hi);
-        parts[(int64_t)m * groups16 + g] = hi;
-        parts[((int64_t)M + m) * groups16 + g] = lo;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const __bf16 part = (__bf16)s;
+            parts[((int64_t)i * M + m) * groups16 + g] = part;
+            s -= (float)part;
+        }
     }
 }
 
@@ -66,7 +72,7 @@ template <class T> __device__ inline f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c)
 
 struct RowsArgs {
     const void *x;          // M x Kp, in order
-    const __bf16 *parts;    // M x groups16, and the second plane `plane` further on
+    const __bf16 *parts;    // M x groups16, and two more planes, each `plane` further on
     int64_t plane;
     const uint8_t *w;
     const uint32_t *p;
@@ -88,6 +94,7 @@ template <int G, int WM, int WN> struct RowsLds {
         NC = WORDS > 512 ? WORDS / 512 : 1,                    // numbers
         NUMBERS = NC * 2048, STAGE = X + W + NUMBERS, COPIES = XC + WC + NC,
         UNITS = WN * 128 / G,                                  // (32 columns, group) of a stage
+        BLOCK = 16 * G / 128,                                  // stages whose minima enter together
         OUT_LD = BN + 8                                        // the tile on its way out, 16-bit
     };
     static_assert(BM * OUT_LD * 2 <= STAGES * STAGE, "the tile over the ring");
@@ -142,8 +149,6 @@ __global__ __launch_bounds__(512, 2) void w4_rows_kernel(RowsArgs a)
 #pragma unroll
         for (int i = 0; i < L::COPIES; ++i) copy(i, first + st, lds0 + (uint32_t)(st * L::STAGE));
 
-    // The accumulators start from the groups' minima: acc[m][n][i] is row 8 (i / 4) + 4 h + i % 4 of
-    // tile m, column lane % 32 of tile n.  16 groups to an instruction, loads of 32 at a time.
     f32x16 acc[WM][WN];
 #pragma unroll
     for (int m = 0; m < WM; ++m)
@@ -151,56 +156,53 @@ __global__ __launch_bounds__(512, 2) void w4_rows_kernel(RowsArgs a)
         for (int n = 0; n < WN; ++n)
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.f;
-    {
-        const int32_t lo = first * PER, hi = min(last * PER, a.groups);
-        const __bf16 *xp[WM];
-        const uint32_t *np[WN];
+    const __bf16 *xp[WM];
+    const uint32_t *np[WN];
 #pragma unroll
-        for (int m = 0; m < WM; ++m) xp[m] = a.parts + (int64_t)(m0 + min(32 * (WM * wm + m) + r, rows - 1)) * a.groups16 + 8 * h;
+    for (int m = 0; m < WM; ++m) xp[m] = a.parts + (int64_t)(m0 + min(32 * (WM * wm + m) + r, rows - 1)) * a.groups16 + 8 * h;
 #pragma unroll
-        for (int n = 0; n < WN; ++n) np[n] = a.p + (int64_t)(n0 + min(32 * (WN * wn + n) + r, cols - 1)) * a.groups + 8 * h;
-        for (int32_t g = lo / 16 * 16; g < hi; g += 32) {
-            u32x4 xv[2][WM][2];
-            uint32_t nv[2][WN][8];
+    for (int n = 0; n < WN; ++n) np[n] = a.p + (int64_t)(n0 + min(32 * (WN * wn + n) + r, cols - 1)) * a.groups + 8 * h;
+    // The minima of groups lo .. hi, of the 16 from g on, into the accumulators: acc[m][n][i] is row
+    // 8 (i / 4) + 4 h + i % 4 of tile m, column lane % 32 of tile n.  Of the nine products of X's parts
+    // and b''s, the six down to 2^-16 of the first, smallest first.
+    auto minima = [&](int32_t g, int32_t lo, int32_t hi) {
+        u32x4 xv[WM][3];
+        uint32_t nv[WN][8];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int32_t gu = min(g + 16 * u, a.groups16 - 16);
+        for (int m = 0; m < WM; ++m)
 #pragma unroll
-                for (int m = 0; m < WM; ++m) {
-                    xv[u][m][0] = *(const u32x4 *)(xp[m] + gu);
-                    xv[u][m][1] = *(const u32x4 *)(xp[m] + a.plane + gu);
+            for (int i = 0; i < 3; ++i) xv[m][i] = *(const u32x4 *)(xp[m] + i * a.plane + g);
+#pragma unroll
+        for (int n = 0; n < WN; ++n)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) nv[n][i] = np[n][min(g + i, a.groups - 1 - 8 * h)];
+#pragma unroll
+        for (int n = 0; n < WN; ++n) {
+            u32x4 b[3];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float v[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int32_t at = g + 8 * h + 2 * i + e;
+                    const uint32_t w = at >= lo && at < hi ? nv[n][2 * i + e] : 0u;
+                    v[e] = hi_f32<T>(w) - 16.0f * lo_f32<T>(w);
                 }
 #pragma unroll
-                for (int n = 0; n < WN; ++n)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) nv[u][n][i] = np[n][min(g + 16 * u + i, a.groups - 1 - 8 * h)];
+                for (int part = 0; part < 3; ++part) {
+                    b[part][i] = pack2<__bf16>(v[0], v[1]);
+                    v[0] -= lo_f32<__bf16>(b[part][i]);
+                    v[1] -= hi_f32<__bf16>(b[part][i]);
+                }
             }
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int m = 0; m < WM; ++m)
 #pragma unroll
-                for (int n = 0; n < WN; ++n) {
-                    u32x4 bh, bl;
+                for (int both = 2; both >= 0; --both)   // part i of X with part both - i of b'
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float b[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int32_t at = g + 16 * u + 8 * h + 2 * i + e;
-                            const uint32_t w = at >= lo && at < hi ? nv[u][n][2 * i + e] : 0u;
-                            b[e] = hi_f32<T>(w) - 16.0f * lo_f32<T>(w);
-                        }
-                        bh[i] = pack2<__bf16>(b[0], b[1]);
-                        bl[i] = pack2<__bf16>(b[0] - lo_f32<__bf16>(bh[i]), b[1] - hi_f32<__bf16>(bh[i]));
-                    }
-#pragma unroll
-                    for (int m = 0; m < WM; ++m) {
-                        acc[m][n] = mfma32<__bf16>(xv[u][m][1], bh, acc[m][n]);
-                        acc[m][n] = mfma32<__bf16>(xv[u][m][0], bl, acc[m][n]);
-                        acc[m][n] = mfma32<__bf16>(xv[u][m][0], bh, acc[m][n]);
-                    }
-                }
+                    for (int i = both; i >= 0; --i) acc[m][n] = mfma32<__bf16>(xv[m][i], b[both - i], acc[m][n]);
         }
-    }
+    };
 
     const W4Const konst = w4_const<T>();
     // What a lane reads of a stage: x piece p of its rows, its columns' pieces, their numbers.
@@ -214,104 +216,110 @@ __global__ __launch_bounds__(512, 2) void w4_rows_kernel(RowsArgs a)
     for (int m = 0; m < WM; ++m)
 #pragma unroll
         for (int i = 0; i < 16; ++i) sum[1][m][i] = 0.f;
-    for (int32_t st = first; st < last; ++st) {
-        wait_vm_barrier<L::COPIES>();
-        const char *s0 = smem + at;
-        // the columns' pieces and numbers first, then the rows in the order of their use: the first
-        // matrix instructions need not wait for the last reads
-        u32x4 wv[WN][2], x[8][WM];
-        float scale[WN][PER];
+    for (int32_t st = first; st < last;) {
+        const int32_t block = st / L::BLOCK, more = min((block + 1) * L::BLOCK, last);
+        minima(16 * block, st * PER, min(more * PER, a.groups));
+        for (; st < more; ++st) {
+            wait_vm_barrier<L::COPIES>();
+            const char *s0 = smem + at;
+            // the columns' pieces and numbers first, then the rows in the order of their use: the first
+            // matrix instructions need not wait for the last reads
+            u32x4 wv[WN][2], x[8][WM];
+            float scale[WN][PER];
 #pragma unroll
-        for (int n = 0; n < WN; ++n)
+            for (int n = 0; n < WN; ++n)
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-                wv[n][t] = *(const u32x4 *)(s0 + w_at + 2048u * (uint32_t)n + 16u * ((uint32_t)(2 * t + h) ^ (uint32_t)((r >> 2) & 3)));
+                for (int t = 0; t < 2; ++t)
+                    wv[n][t] = *(const u32x4 *)(s0 + w_at + 2048u * (uint32_t)n + 16u * ((uint32_t)(2 * t + h) ^ (uint32_t)((r >> 2) & 3)));
 #pragma unroll
-        for (int n = 0; n < WN; ++n)
+            for (int n = 0; n < WN; ++n)
 #pragma unroll
-            for (int g = 0; g < PER; ++g)
-                scale[n][g] = lo_f32<T>(*(const uint32_t *)(s0 + n_at + 128u * (uint32_t)n + 4u * (uint32_t)(L::BN * g)));
+                for (int g = 0; g < PER; ++g)
+                    scale[n][g] = lo_f32<T>(*(const uint32_t *)(s0 + n_at + 128u * (uint32_t)n + 4u * (uint32_t)(L::BN * g)));
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int m = 0; m < WM; ++m) {
-                // instruction j takes 8 weights of piece 2 (j / 4) + h, word j % 4; G = 32: of piece
-                // 2 (j / 4) + j / 2 % 2, word 2 (j % 2) + h
-                const uint32_t p = G == 32 ? (uint32_t)(4 * (2 * (j / 4) + j / 2 % 2) + 2 * (j % 2)) + (uint32_t)h
-                                           : (uint32_t)(8 * (j / 4) + j % 4) + 4u * (uint32_t)h;
-                x[j][m] = *(const u32x4 *)(s0 + x_at + 8192u * (uint32_t)m + 16u * (p ^ (uint32_t)(r & 15)));
-            }
-#pragma unroll
-        for (int n = 0; n < WN; ++n) {
-            u32x4 w[2];
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                w[t] = wv[n][t];
-                if constexpr (G == 32) {
-                    const auto c = __builtin_amdgcn_permlane32_swap(w[t][0], w[t][1], false, false);
-                    const auto d = __builtin_amdgcn_permlane32_swap(w[t][2], w[t][3], false, false);
-                    w[t] = u32x4{c[0], d[0], c[1], d[1]};
+                for (int m = 0; m < WM; ++m) {
+                    // instruction j takes 8 weights of piece 2 (j / 4) + h, word j % 4; G = 32: of piece
+                    // 2 (j / 4) + j / 2 % 2, word 2 (j % 2) + h
+                    const uint32_t p = G == 32 ? (uint32_t)(4 * (2 * (j / 4) + j / 2 % 2) + 2 * (j % 2)) + (uint32_t)h
+                                               : (uint32_t)(8 * (j / 4) + j % 4) + 4u * (uint32_t)h;
+                    x[j][m] = *(const u32x4 *)(s0 + x_at + 8192u * (uint32_t)m + 16u * (p ^ (uint32_t)(r & 15)));
                 }
-            }
 #pragma unroll
-            for (int g = 0; g < PER; ++g) {
-                constexpr int STEPS = 8 / PER;
-                constexpr int CHAINS = WM == 1 && STEPS > 2 ? 2 : 1;   // one tile of rows: sums in two, or each instruction waits for the last
-                // PIPE: the sums of the unit (columns, group) before are scaled step by step beside this
-                // one's matrix instructions, the last unit's in the next stage
-                const int now = PIPE ? (n * PER + g) % 2 : 0, was = 1 - now;
-                const int wn_ = (n * PER + g + L::UNITS - 1) % L::UNITS / PER;   // whose columns they are
+            for (int n = 0; n < WN; ++n) {
+                u32x4 w[2];
 #pragma unroll
-                for (int m = 0; m < WM; ++m)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) sum[now][m][i] = 0.f;
-                f32x16 other;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) other[i] = 0.f;
-#pragma unroll
-                for (int j = g * STEPS; j < (g + 1) * STEPS; ++j) {
-                    const u32x4 lv = w4_levels<T>(w[j / 4][j % 4], konst);
-#pragma unroll
-                    for (int m = 0; m < WM; ++m) {
-                        if (CHAINS == 2 && j % 2) other = mfma32<T>(x[j][m], lv, other);
-                        else sum[now][m] = mfma32<T>(x[j][m], lv, sum[now][m]);
-                        if constexpr (PIPE)
-#pragma unroll
-                            for (int i = 16 / STEPS * (j % STEPS); i < 16 / STEPS * (j % STEPS + 1); ++i)
-                                acc[m][wn_][i] = __builtin_fmaf(pending, sum[was][m][i], acc[m][wn_][i]);
-                    }
-                    // a copy of the stage after next now and then: all at once they would hold up
-                    // every wave at the start of a stage
-                    if (WN == 1) {
-                        if (j < L::COPIES) copy(j, st + 2, lds0 + next);
-                    } else if (j % 2 == 0 && 4 * n + j / 2 < L::COPIES) {
-                        copy(4 * n + j / 2, st + 2, lds0 + next);
+                for (int t = 0; t < 2; ++t) {
+                    w[t] = wv[n][t];
+                    if constexpr (G == 32) {
+                        const auto c = __builtin_amdgcn_permlane32_swap(w[t][0], w[t][1], false, false);
+                        const auto d = __builtin_amdgcn_permlane32_swap(w[t][2], w[t][3], false, false);
+                        w[t] = u32x4{c[0], d[0], c[1], d[1]};
                     }
                 }
-                if constexpr (CHAINS == 2)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) sum[now][0][i] += other[i];
-                if constexpr (PIPE) {
-                    pending = scale[n][g];
-                } else {
+                for (int g = 0; g < PER; ++g) {
+                    constexpr int STEPS = 8 / PER;
+                    constexpr int CHAINS = WM == 1 && STEPS > 2 ? 2 : 1;   // one tile of rows: sums in two, or each instruction waits for the last
+                    // PIPE: the sums of the unit (columns, group) before are scaled step by step beside this
+                    // one's matrix instructions, the last unit's in the next stage or behind the loop
+                    const int now = PIPE ? (n * PER + g) % 2 : 0, was = 1 - now;
+                    const int wn_ = (n * PER + g + L::UNITS - 1) % L::UNITS / PER;   // whose columns they are
 #pragma unroll
                     for (int m = 0; m < WM; ++m)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) acc[m][n][i] = __builtin_fmaf(scale[n][g], sum[now][m][i], acc[m][n][i]);
+                        for (int i = 0; i < 16; ++i) sum[now][m][i] = 0.f;
+                    f32x16 other;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) other[i] = 0.f;
+#pragma unroll
+                    for (int j = g * STEPS; j < (g + 1) * STEPS; ++j) {
+                        const u32x4 lv = w4_levels<T>(w[j / 4][j % 4], konst);
+#pragma unroll
+                        for (int m = 0; m < WM; ++m) {
+                            if (CHAINS == 2 && j % 2) other = mfma32<T>(x[j][m], lv, other);
+                            else sum[now][m] = mfma32<T>(x[j][m], lv, sum[now][m]);
+                            if constexpr (PIPE)
+#pragma unroll
+                                for (int i = 16 / STEPS * (j % STEPS); i < 16 / STEPS * (j % STEPS + 1); ++i)
+                                    acc[m][wn_][i] = __builtin_fmaf(pending, sum[was][m][i], acc[m][wn_][i]);
+                        }
+                        // a copy of the stage after next now and then: all at once they would hold up
+                        // every wave at the start of a stage
+                        if (WN == 1) {
+                            if (j < L::COPIES) copy(j, st + 2, lds0 + next);
+                        } else if (j % 2 == 0 && 4 * n + j / 2 < L::COPIES) {
+                            copy(4 * n + j / 2, st + 2, lds0 + next);
+                        }
+                    }
+                    if constexpr (CHAINS == 2)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) sum[now][0][i] += other[i];
+                    if constexpr (PIPE) {
+                        pending = scale[n][g];
+                    } else {
+#pragma unroll
+                        for (int m = 0; m < WM; ++m)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) acc[m][n][i] = __builtin_fmaf(scale[n][g], sum[now][m][i], acc[m][n][i]);
+                    }
                 }
             }
+            static_assert(L::COPIES <= 8, "all copies are made");
+            at = at == 2 * L::STAGE ? 0 : at + L::STAGE;
+            next = next == 2 * L::STAGE ? 0 : next + L::STAGE;
         }
-        static_assert(L::COPIES <= 8, "all copies are made");
-        at = at == 2 * L::STAGE ? 0 : at + L::STAGE;
-        next = next == 2 * L::STAGE ? 0 : next + L::STAGE;
+        if constexpr (PIPE)
+#pragma unroll
+            for (int m = 0; m < WM; ++m)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    acc[m][WN - 1][i] = __builtin_fmaf(pending, sum[1][m][i], acc[m][WN - 1][i]);
+                    sum[1][m][i] = 0.f;
+                }
     }
     wait_vm_all();   // (the last two stages' copies brought nothing)
-    if constexpr (PIPE)
-#pragma unroll
-        for (int m = 0; m < WM; ++m)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[m][WN - 1][i] = __builtin_fmaf(pending, sum[1][m][i], acc[m][WN - 1][i]);
-
     if (a.splits > 1) {
         float *out = (float *)a.out + (int64_t)part * rows_apart(a.M, a.ldo) + (int64_t)m0 * a.ldo + n0;
 #pragma unroll
@@ -453,7 +461,7 @@ static RowsSpace rows_space(int64_t M, int64_t N, int64_t K, int64_t group, cons
     s.Kp = (K + 127) / 128 * 128;
     s.groups16 = (K / group + 15) / 16 * 16;
     s.parts = (M * s.Kp * 2 + 255) / 256 * 256;
-    s.sums = s.parts + (2 * M * s.groups16 * 2 + 255) / 256 * 256;
+    s.sums = s.parts + (3 * M * s.groups16 * 2 + 255) / 256 * 256;
     s.bytes = s.sums + (p.band[0].splits > 1 ? p.band[0].splits * rows_apart(M, N) * 4 : 0);
     return s;
 }

@@ -419,8 +419,9 @@ int lb_rope_freqs(double *freqs, float *mult, int64_t R, double base, int scalin
  *   (N, or NULL) and out (dense) are of ftype, bf16 or fp16.
  * Products are exact, sums and the groups' numbers fp32, out is rounded once; what comes
  * from a row of X that holds an infinity or a NaN is not finite (NaN or infinite).  The sums run
- * over 16 + u in place of u: up to four times fp32's rounding of the sum; with more than 16
- * rows, the minima's part (b - 16 s) sum_k X is held in two bf16 parts each (2^-16 of it).
+ * over 16 + u in place of u and b - 16 s in place of b, so that fp32's roundings are of larger
+ * sums; with more than 16 rows, (b - 16 s) sum_k X comes from three bf16 parts of each (2^-23
+ * of it).
  * workspace: at least lb_linear_w4_workspace(M, K, N, group) bytes (LB_ERR_WORKSPACE
  * otherwise; NULL where that is 0, as for up to 16 rows).  It depends on the current device's
  * number of compute units too: ask on the device that the call runs on.

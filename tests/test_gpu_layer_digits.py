@@ -1,0 +1,81 @@
+"""GPU tests of how many digits the decoder layer's 4-bit products keep before their output is rounded.
+
+An output in 16 bits hides what was lost before it.  A bias that cancels all of an output but its rounding shows it (the
+rows of x are equal, so that one bias cancels them all); where no bias does, outputs are held against the error that
+their rounding alone has."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+import bit_integer_gemm_amd as lb  # noqa: E402
+from test_gpu_layer import BF, HF, STEP, floor_of, gen, half_step, weights  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+# rows of each kernel: up to 16, and tiles of 64 x 128, 128 x 128 and 128 x 256
+MINIMA = [(16, 200, 128), (17, 300, 128), (64, 257, 64), (130, 515, 32), (600, 9000, 128), (601, 8999, 32)]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("M,N,group", MINIMA)
+def test_minima_of_a_group(dtype, M, N, group):
+    """Scales of zero leave the minima: b sum_k x, of one group here."""
+    g = gen(M + N)
+    x = (torch.rand(1, group, generator=g) + 1).to(dtype)
+    b = torch.randn(N, 1, generator=g).to(dtype)
+    p = torch.stack([torch.zeros_like(b), b], -1)
+    w = torch.randint(0, 256, (N, group // 2), generator=g, dtype=torch.uint8)
+    want = x.double().sum() * b.double().flatten()
+    bias = (-want).to(dtype)
+    out = torch.empty(M, N, dtype=dtype, device="cuda")
+    lb.lb_linear_w4(x.cuda().expand(M, group).contiguous(), w.cuda(), p.cuda(), out, bias=bias.cuda())
+    left = want + bias.double()
+    # half steps: the sum of x, 7 additions of a lane and 4 between lanes; what three parts leave of x's sum and of b, and
+    # the products that are not formed; the bias.  Whole ones: a product and its addition, of each of six parts.
+    before = (11 + 4 + 1 + 2 * 2 * 6) * STEP * want.abs()
+    tol = before + half_step(dtype) * (left.abs() + before) + floor_of(dtype)
+    off = (out.cpu().double() - left).abs()
+    assert (off <= tol).all(), (off / tol).max()
+
+
+def roundings(x, u, s, b, group, wide):
+    """Sum over all outputs of the expected squares of fp32's roundings: a whole step, evenly spread, of every partial sum
+    as its kernel forms it: the minima of 16 groups ahead of their products (wide), or each group's own beside it."""
+    xg, ug = x.unflatten(1, (-1, group)), (u + 16).unflatten(1, (-1, group))
+    sums, acc, total = xg.sum(-1), torch.zeros(x.shape[0], u.shape[0], dtype=torch.float64), 0.0
+    minima = b - 16 * s
+    for g in range(sums.shape[1]):
+        part = xg[:, g] @ ug[:, g].T * s[:, g]
+        total += group / 16 * part.square().sum()
+        if not wide:
+            total += (acc + part).square().sum()
+            acc = acc + sums[:, g, None] * minima[:, g]
+        elif g % 16 == 0:
+            acc = acc + sums[:, g:g + 16] @ minima[:, g:g + 16].T
+            total += 6 * acc.square().sum()
+        acc = acc + part
+        total += acc.square().sum()
+    return float(total) * (2 * STEP) ** 2 / 3
+
+
+@pytest.mark.parametrize("mean", [0.0, 1.0, 10.0])
+@pytest.mark.parametrize("M,N,K,group", [(16, 256, 4096, 128), (17, 256, 4096, 128), (64, 512, 4096, 128), (64, 256, 11008, 32),
+                                         (130, 300, 2048, 64), (520, 1024, 4096, 64), (1030, 8200, 1024, 64)])
+def test_activations_with_a_mean(M, N, K, group, mean):
+    """fp16 outputs are hardly further from the formula than their rounding, whatever the mean of x: minima and products
+    are large then, and cancel."""
+    g = gen(K + M)
+    x = (torch.randn(M, K, generator=g) + mean).to(HF)
+    w, p, wd = weights((), N, K, group, HF, g)
+    out = torch.empty(M, N, dtype=HF, device="cuda")
+    lb.lb_linear_w4(x.cuda(), w.cuda(), p.cuda(), out)
+    want = x.double() @ wd.T
+    u = torch.stack([w & 15, w >> 4], -1).flatten(-2).double()
+    some = slice(0, 256)   # of the columns, for the partial sums
+    before = roundings(x.double(), u[some], p[some, :, 0].double(), p[some, :, 1].double(), group, M > 16) * N / min(N, 256)
+    least = float((want.to(HF).double() - want).square().sum())
+    got = float((out.cpu().double() - want).square().sum())
+    # (two sums of squares of M N numbers, neither of which knows of the other)
+    assert got <= (least + before) * (1 + 8 / math.sqrt(M * N)), (math.sqrt(got / least), math.sqrt(before / least))
