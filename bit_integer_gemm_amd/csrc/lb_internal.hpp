@@ -185,7 +185,7 @@ struct MoeArgs {
     float *logits;     // workspace: T x E
     int32_t *found;    // how many experts have tokens
     int32_t *lists;    // and 2 + MOE_TOKENS for each expert or (token, rank) pair
-    void *h;           // two planes of T top_k x I, bf16
+    float *h;          // T top_k x I
     float *y;          // T top_k x H
 };
 hipError_t launch_moe_w4(int ftype, int group, const MoeArgs &a, int cu, hipStream_t s);

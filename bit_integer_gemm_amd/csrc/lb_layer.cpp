@@ -257,7 +257,7 @@ int lb_moe_w4(const void *X, int64_t ldx, const void *Wr, const uint8_t *W1, con
         a.logits = (float *)workspace;
         a.found = (int32_t *)((char *)workspace + m.lists);
         a.lists = a.found + 1;
-        a.h = (char *)workspace + m.h;
+        a.h = (float *)((char *)workspace + m.h);
         a.y = (float *)((char *)workspace + m.y);
         const hipError_t e = lb::launch_moe_w4(ftype, (int)group, a, cu, (hipStream_t)stream);
         if (e != hipSuccess) return LB_ERR_HIP;

@@ -10,8 +10,8 @@
 // token's order is the number of larger logits, a few ballots), and results lie at (token,
 // rank), so that every sum has a fixed order.  One token needs no last launch, few experts no
 // first one.
-// Between the products h is two bf16 planes, hi + lo (2^-17 of it), in the down product's nibble
-// order; the down product's outputs are fp32.
+// Between the products h is fp32, in the down product's nibble order, and the down product's outputs
+// are fp32.
 //
 // Bound by the chosen experts' weights, read once (2 of 8 of 4096 x 11008: 98.6 MB in 27 us and
 // 48.8 in 15; 122 of 128 of 2048 x 1024, met by 48 tokens: 262 MB in 57 us, 4.6 TB/s, and 133 in
@@ -342,15 +342,9 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_up_kernel(MoeArgs a, MoeGri
     __shared__ MoeList list;
     const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     MoePlace p = {};
-    __bf16 *const hi = (__bf16 *)a.h, *const lo = hi + (int64_t)a.T * a.top_k * a.I;
     auto put = [&](int32_t m, int32_t c, float gate, float up) {
-        // (a quotient and an exponential good to 2^-21)
-        const float h = gate / (1.0f + __expf(-gate)) * up;
         // in the order in which the down product's nibbles come
-        const int64_t o = (int64_t)list.row[m] * a.I + p.first * 16 + (c & ~7) + 2 * (c & 3) + (c >> 2 & 1);
-        const __bf16 top = (__bf16)h;
-        hi[o] = top;
-        lo[o] = (__bf16)(h - (float)top);
+        a.h[(int64_t)list.row[m] * a.I + p.first * 16 + (c & ~7) + 2 * (c & 3) + (c >> 2 & 1)] = gate / (1.0f + expf(-gate)) * up;
     };
     int32_t expert = 0;
     auto tile_at = [&](int32_t t) { return W4Tile{((int64_t)expert * 2 + t % 2) * a.I + (p.first + t / 2) * 16, 16}; };
@@ -413,9 +407,8 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_kernel(MoeArgs a, MoeG
     const int32_t *const l = a.lists + p.slot * MOE_LIST;
     const int32_t count = l[0], expert = l[1];
     if (count == 0) return;
-    const uint32_t plane = (uint32_t)(a.T * a.top_k) * (uint32_t)a.I * 2u;
     auto tile_at = [&](int32_t t) { return W4Tile{(int64_t)expert * a.H + (p.first + t) * 16, 16}; };
-    W4Flow<__bf16, T, G, 2, decltype(tile_at)> flow(smem, g.x_bytes, a.w2, (const uint32_t *)a.p2, a.I, g.chunk, tile_at);
+    W4Flow<_Float16, T, G, 2, decltype(tile_at)> flow(smem, g.x_bytes, a.w2, (const uint32_t *)a.p2, a.I, g.chunk, tile_at);
     const i32x4 rx = make_rsrc(a.h, 0xFFFFFFF0u);
     const int32_t mine_row = l[2 + min(lane, count - 1)];
     list.row[lane] = mine_row;   // (every wave writes the same, and reads what it wrote)
@@ -424,10 +417,7 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_kernel(MoeArgs a, MoeG
         const int32_t rows = min(g.rows, count - at);
         const W4Sums<ONE> sums(smem + g.x_bytes + W4Lds<G>::RINGS, p.have, 1, rows);
         auto put = [&](int32_t t, int32_t m, int32_t c, float v) { a.y[(int64_t)list.row[at + m] * a.H + (p.first + t) * 16 + c] = v; };
-        auto x_at = [&](int32_t i) {
-            const int32_t second = i >= rows;
-            return (uint32_t)list.row[at + i - (second ? rows : 0)] * (uint32_t)a.I * 2u + (second ? plane : 0u);
-        };
+        auto x_at = [&](int32_t i) { return (uint32_t)list.row[at + i] * (uint32_t)a.I * 4u; };
         auto done = [&](int32_t t, const f32x4 &acc, bool more) {
             if (!sums.whole(wave, t)) return w4_put(sums.at(wave, t, 0), rows, acc, more);
             w4_rows(rows, [&](int32_t i, int32_t m, int32_t c) { put(t, m, c, acc[i]); });
@@ -459,9 +449,9 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_token_kernel(MoeArgs a
         const int32_t j = t % k;
         return W4Tile{(int64_t)__builtin_amdgcn_readlane(expert, j) * a.H + (t0 + t / k) * 16, 16};
     };
-    W4Flow<__bf16, T, G, 2, decltype(tile_at)> flow(smem, x_bytes, a.w2, (const uint32_t *)a.p2, a.I, (a.I + 255) / 256, tile_at);
+    W4Flow<_Float16, T, G, 2, decltype(tile_at)> flow(smem, x_bytes, a.w2, (const uint32_t *)a.p2, a.I, (a.I + 255) / 256, tile_at);
     const i32x4 rx = make_rsrc(a.h, 0xFFFFFFF0u);
-    auto x_at = [&](int32_t i) { return (uint32_t)i * (uint32_t)a.I * 2u; };   // (the planes follow each other)
+    auto x_at = [&](int32_t i) { return (uint32_t)i * (uint32_t)a.I * 4u; };
     const int32_t *const l = a.lists + min(lane, k - 1) * MOE_LIST;
     expert = l[1];
     row = l[2];
@@ -587,7 +577,7 @@ template <int G> static MoeShape moe_shape(const MoeArgs &a, int32_t tiles, int3
     m.g.tiles = tiles;
     m.g.chunk = w4_chunk(lines, planes * m.g.rows, 66 * 1024);
     m.g.one = m.g.chunk >= lines;
-    m.g.x_bytes = W4Lds<G>::x_bytes(planes * m.g.rows, m.g.chunk);
+    m.g.x_bytes = W4Lds<G>::x_bytes(planes, m.g.rows, m.g.chunk);
     // a workgroup to a compute unit, or more where their sums would not find room
     const int32_t most = m.g.active ? std::min(pairs, a.E) : a.E;
     for (int32_t wgs = std::max(cu, most);; wgs += most) {
@@ -610,7 +600,7 @@ template <class T, int G> static hipError_t moe_t(const MoeArgs &a, int cu, hipS
     else hipLaunchKernelGGL((moe_up_kernel<T, G, false, false>), dim3(up.wgs), block, up.lds, s, a, up.g);
     if (a.T == 1) {   // all of its experts' activations in LDS, if they find room there
         const int32_t tiles = a.H / 16, per = (tiles + cu - 1) / cu;
-        const uint32_t x_bytes = W4Lds<G>::x_bytes(2 * a.top_k, (a.I + 255) / 256);
+        const uint32_t x_bytes = W4Lds<G>::x_bytes(2, a.top_k, (a.I + 255) / 256);
         const int64_t lds = x_bytes + W4Lds<G>::RINGS + w4_sums_bytes(false, (int64_t)a.top_k * per, 1, 1);
         if (lds <= MOE_LDS) {
             hipLaunchKernelGGL((moe_down_token_kernel<T, G>), dim3((uint32_t)((tiles + per - 1) / per)), block, (uint32_t)lds, s, a, per,

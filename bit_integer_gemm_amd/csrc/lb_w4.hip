@@ -27,7 +27,7 @@ __global__ __launch_bounds__(64 * W4_WAVES) void w4_few_kernel(const T *__restri
     extern __shared__ __attribute__((aligned(1024))) char smem[];
     const int32_t wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), rows = a.M;
     const int32_t t0 = (int32_t)blockIdx.x * a.per, tiles = min(a.per, (a.N + 15) / 16 - t0);
-    const uint32_t x_bytes = W4Lds<G>::x_bytes(rows, a.chunk);
+    const uint32_t x_bytes = W4Lds<G>::x_bytes(1, rows, a.chunk);
     const W4Sums<ONE> sums(smem + x_bytes + W4Lds<G>::RINGS, tiles, 1, rows);
     auto put = [&](int32_t t, int32_t m, int32_t c, float v) {
         const int32_t n = (t0 + t) * 16 + c;
@@ -57,7 +57,7 @@ template <class T, int G> static hipError_t w4_g(const W4Args &a, int cu, hipStr
     const int64_t sums = w4_sums_bytes(one, per, 1, a.M), wgs = (tiles + per - 1) / per;
     if (!one) chunk = w4_chunk(lines, a.M, FEW_LDS - 1024 - W4Lds<G>::RINGS - sums);
     const FewArgs f{a.w, (const uint32_t *)a.p, a.ldx, (int32_t)a.M, (int32_t)a.N, (int32_t)a.K, (int32_t)per, chunk};
-    const uint32_t lds = W4Lds<G>::x_bytes(f.M, f.chunk) + W4Lds<G>::RINGS + (uint32_t)sums;
+    const uint32_t lds = W4Lds<G>::x_bytes(1, f.M, f.chunk) + W4Lds<G>::RINGS + (uint32_t)sums;
     if (a.M > W4_FEW_ROWS || wgs * 64 * W4_WAVES > LAUNCH_THREADS || lds > FEW_LDS) return hipErrorInvalidValue;
     const dim3 grid((uint32_t)wgs), block(64 * W4_WAVES);
     const T *x = (const T *)a.x, *bias = (const T *)a.bias;

@@ -96,6 +96,17 @@ __device__ inline void w4_transpose(u32x4 &p)
     p[3] = d[1];
 }
 
+// The largest of 32 lanes' numbers, those of a line of x: of 16 by rotations, of both by a swap.
+__device__ inline uint32_t w4_most_of_line(uint32_t v)
+{
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x128, 0xF, 0xF, true));   // row_ror:8, then 4, 2 and 1
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x124, 0xF, 0xF, true));
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x122, 0xF, 0xF, true));
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x121, 0xF, 0xF, true));
+    const auto both = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return max((uint32_t)both[0], (uint32_t)both[1]);
+}
+
 // The sixteen rows of weights of a tile, from row `row` of the operand; rows from `rows` on do not
 // exist and read as zeros.
 struct W4Tile {
@@ -109,8 +120,8 @@ struct W4Tile {
 constexpr int W4_WAVES = 8;
 __host__ __device__ inline int32_t w4_first(int32_t tiles, int32_t wave) { return tiles * wave / W4_WAVES; }
 
-// LDS of a workgroup: x (two planes: one row after the other's all), the rings, and what the
-// caller puts behind.
+// LDS of a workgroup: x (two planes: the second behind the first, then a scale for each line of
+// each row), the rings, and what the caller puts behind.
 template <int G> struct W4Lds {
     enum : int {
         GROUPS = 256 / G,
@@ -122,7 +133,11 @@ template <int G> struct W4Lds {
         RINGS = W4_WAVES * RING
     };
     // (a copy fills 1 KiB)
-    static __host__ __device__ inline uint32_t x_bytes(int32_t xrows, int32_t chunk) { return (uint32_t)(xrows * chunk + 1) / 2u * 1024u; }
+    static __host__ __device__ inline uint32_t plane_bytes(int32_t rows, int32_t lines) { return (uint32_t)(rows * lines + 1) / 2u * 1024u; }
+    static __host__ __device__ inline uint32_t x_bytes(int planes, int32_t rows, int32_t chunk)
+    {
+        return planes * plane_bytes(rows, chunk) + (planes > 1 ? (uint32_t)(rows * chunk + 255) / 256u * 1024u : 0u);
+    }
 };
 
 #pragma clang diagnostic push
@@ -153,7 +168,9 @@ template <int N> __device__ inline void w4_wait() { asm volatile("s_waitcnt vmcn
 // The products of a wave's tiles: 16 rows of x at most by 16 columns each.
 //   lds: x (x_bytes of it), then the rings.  Copies of two lines are under way while a third is
 //     worked on; each wave waits for its own by count.
-//   PLANES 2: x is the sum of two planes, whose rows follow each other, in order in memory.
+//   PLANES 2: x is fp32, in order in memory.  In LDS it is two planes of fp16 under a power of two
+//     for each line, which puts the line's largest number into [2^14, 2^15): off by 2^-23 of a number,
+//     and 2^-39 of the line's largest where that is more.
 //   tiles: the workgroup's; tile_at(t): a W4Tile.
 //   T: the type of x as the matrix cores take it; PT: of the groups' numbers.
 // Every wave of a workgroup makes the same calls, also one without lines (x is copied by all).
@@ -266,41 +283,80 @@ struct W4Flow {
         for (int d = 0; d < L::DEPTH - 1; ++d) copy();
     }
 
-    // x of the chunk from line c on: piece p of row i lies at p ^ i % 16 of the row.
-    template <class XAt> __device__ inline void ask_x(int32_t c, int32_t xrows, const i32x4 rx, XAt &&x_at)
+    // x of the chunk from line c on: piece p of row i lies at p ^ i % 16 of the row.  fp32: the halves of
+    // a piece's numbers where its planes will be.
+    template <class XAt> __device__ inline void ask_x(int32_t c, int32_t rows, const i32x4 rx, XAt &&x_at)
     {
-        const int32_t per = min(chunk, lines - c) * 32, all = per * xrows;
+        const int32_t per = min(chunk, lines - c) * 32, all = per * rows;
+        const uint32_t plane = L::plane_bytes(rows, per / 32);
         int32_t row = (wave * 64 + lane) / per, at = wave * 64 + lane - row * per;
         for (int32_t i0 = wave * 64; i0 < all; i0 += 64 * W4_WAVES) {
             const int32_t k = c * 256 + 8 * (at ^ (row & 15));
-            dma16(rx, i0 + lane < all && k < K ? x_at(min(row, xrows - 1)) + 2u * (uint32_t)k : 0xFFFFFFF0u,
-                  lds_addr(lds) + 16u * (uint32_t)i0);
+            const bool there = i0 + lane < all && k < K;
+            const uint32_t from = x_at(min(row, rows - 1)) + 2u * PLANES * (uint32_t)k;
+#pragma unroll
+            for (int pl = 0; pl < PLANES; ++pl)
+                dma16(rx, there ? from + 16u * (uint32_t)pl : 0xFFFFFFF0u, lds_addr(lds) + plane * (uint32_t)pl + 16u * (uint32_t)i0);
             for (at += 64 * W4_WAVES; at >= per; at -= per) ++row;
         }
     }
-    __device__ inline void order_x(int32_t c, int32_t xrows)   // each lane what it copied itself
+    // Each lane what it copied itself: numbers in order; fp32 into two planes.
+    __device__ inline void order_x(int32_t c, int32_t rows)
     {
-        if constexpr (PLANES == 2) {
-            __syncthreads();
-            return;
-        }
-        constexpr int AT_ONCE = 4;
-        const int32_t all = min(chunk, lines - c) * 32 * xrows;
+        const int32_t all = min(chunk, lines - c) * 32 * rows;
         u32x4 *const p = (u32x4 *)lds;
-        for (int32_t i = (int32_t)threadIdx.x; i < all; i += 64 * W4_WAVES * AT_ONCE) {
-            u32x4 v[AT_ONCE];
+        if constexpr (PLANES == 2) {
+            const uint32_t plane = L::plane_bytes(rows, min(chunk, lines - c));
+            u32x4 *const p1 = (u32x4 *)(lds + plane);
+            float *const scale = (float *)(lds + 2 * plane);
+            constexpr int AT_ONCE = 2;
+            for (int32_t i0 = (int32_t)threadIdx.x; i0 < all; i0 += 64 * W4_WAVES * AT_ONCE) {
+                u32x4 v[AT_ONCE][2];
 #pragma unroll
-            for (int u = 0; u < AT_ONCE; ++u) v[u] = p[min(i + 64 * W4_WAVES * u, all - 1)];
+                for (int u = 0; u < AT_ONCE; ++u) {
+                    const int32_t i = min(i0 + 64 * W4_WAVES * u, all - 1);
+                    v[u][0] = p[i];
+                    v[u][1] = p1[i];
+                }
 #pragma unroll
-            for (int u = 0; u < AT_ONCE; ++u)
-                if (i + 64 * W4_WAVES * u < all) p[i + 64 * W4_WAVES * u] = w4_order(v[u]);
+                for (int u = 0; u < AT_ONCE; ++u) {
+                    const int32_t i = i0 + 64 * W4_WAVES * u;
+                    if (i >= all) break;   // (for whole lines: half a wave has one)
+                    uint32_t most = 0;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) most = max(most, v[u][e / 4][e % 4] & 0x7FFFFFFFu);
+                    // infinities and NaN are above all, and stay so
+                    const uint32_t up = min(268u - (w4_most_of_line(most) >> 23), 253u);   // the power's exponent
+                    u32x4 hi, lo;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float a = __uint_as_float(v[u][e / 2][e % 2 * 2]) * __uint_as_float(up << 23);
+                        const float b = __uint_as_float(v[u][e / 2][e % 2 * 2 + 1]) * __uint_as_float(up << 23);
+                        hi[e] = pack2<_Float16>(a, b);
+                        lo[e] = pack2<_Float16>(a - lo_f32<_Float16>(hi[e]), b - hi_f32<_Float16>(hi[e]));
+                    }
+                    p[i] = hi;
+                    p1[i] = lo;
+                    if (i % 32 == 0) scale[i / 32] = __uint_as_float((254u - up) << 23);
+                }
+            }
+        } else {
+            constexpr int AT_ONCE = 4;
+            for (int32_t i = (int32_t)threadIdx.x; i < all; i += 64 * W4_WAVES * AT_ONCE) {
+                u32x4 v[AT_ONCE];
+#pragma unroll
+                for (int u = 0; u < AT_ONCE; ++u) v[u] = p[min(i + 64 * W4_WAVES * u, all - 1)];
+#pragma unroll
+                for (int u = 0; u < AT_ONCE; ++u)
+                    if (i + 64 * W4_WAVES * u < all) p[i + 64 * W4_WAVES * u] = w4_order(v[u]);
+            }
         }
         __syncthreads();
     }
 
-    // `rows` rows of x through rx, row i's first byte at x_at(i) (PLANES 2: rows from `rows` on are
-    // the second plane's).  STARTED: start() has been called, and the weights' latency runs beside
-    // the copy of x; else start(tiles_) comes after it, and beside the putting in order.
+    // `rows` rows of x through rx, row i's first byte at x_at(i).  STARTED: start() has been called, and
+    // the weights' latency runs beside the copy of x; else start(tiles_) comes after it, and beside
+    // the putting in order.
     //   done(t, acc, more): sums of tile t over this wave's lines; acc[i] is row 4 i + lane / 16, column
     //     lane % 16 of the tile.  Called for each chunk (more: not the first) and each of the
     //     wave's tiles, also one without lines.
@@ -321,33 +377,37 @@ struct W4Flow {
     {
         constexpr bool STACK = PLANES == 2 && RO < 4;
         constexpr int PL = STACK ? 1 : PLANES, RI = STACK ? 2 * RO : RO;
-        const int32_t q = lane >> 4, r = lane & 15, xrows = PLANES * rows;
-        ask_x(0, xrows, rx, x_at);
+        const int32_t q = lane >> 4, r = lane & 15;
+        ask_x(0, rows, rx, x_at);
         if constexpr (!STARTED) start(tiles_);
         if constexpr (STARTED) w4_wait<0>();
         else w4_wait<(L::DEPTH - 1) * L::COPIES>();
-        order_x(0, xrows);
+        order_x(0, rows);
 
         const W4Const konst = w4_const<T>();
         uint32_t at = 0, slot = 0;   // of the ring
         for (int32_t c = 0; c < lines; c += chunk) {
             if (c) {
                 __syncthreads();
-                ask_x(c, xrows, rx, x_at);
+                ask_x(c, rows, rx, x_at);
                 w4_wait<0>();
-                order_x(c, xrows);
+                order_x(c, rows);
             }
-            // what a lane reads of x: its row's pieces j of a line's first half, any row's where it has none
-            uint32_t xa[4][PL];
+            // what a lane reads of x: its row's pieces j of a line's first half, any row's where it has none;
+            // and, of two planes, the scales of the rows whose sums it has
+            const int32_t here = min(chunk, lines - c);
+            const uint32_t plane = L::plane_bytes(rows, here);
+            uint32_t xa[4][PL], sa[RO];
             auto aim_x = [&](int32_t first) {
 #pragma unroll
                 for (int pl = 0; pl < PL; ++pl) {
-                    const uint32_t row = (uint32_t)(first + (STACK ? min((r & 3) / RO, 1) : pl) * rows);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        xa[j][pl] = row * (uint32_t)min(chunk, lines - c) * 512u +
-                                    16u * ((uint32_t)(G == 128 ? 4 * q + j : 4 * j + q) ^ (row & 15u));
+                        xa[j][pl] = (uint32_t)(STACK ? min((r & 3) / RO, 1) : pl) * plane + (uint32_t)(first * here) * 512u +
+                                    16u * ((uint32_t)(G == 128 ? 4 * q + j : 4 * j + q) ^ (uint32_t)(first & 15));
                 }
+#pragma unroll
+                for (int i = 0; i < RO; ++i) sa[i] = 2 * plane + 4u * (uint32_t)((OWN_ROW ? first : min(4 * i + q, rows - 1)) * here);
             };
             if constexpr (!OWN_ROW) aim_x(min((STACK ? (r & 3) % RO : r & 3) * 4 + (r >> 2), rows - 1));
             const int32_t last = end();
@@ -363,6 +423,7 @@ struct W4Flow {
                     const char *st = ring + at;
                     u32x4 w[2], x[8][PL];
                     uint32_t num[GROUPS];
+                    float scale[RO];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) w[h] = *(const u32x4 *)(st + 128 * r + 16 * ((4 * h + q) ^ (r >> 1)));
 #pragma unroll
@@ -372,11 +433,16 @@ struct W4Flow {
                     for (int j = 0; j < 8; ++j)
 #pragma unroll
                         for (int pl = 0; pl < PL; ++pl) x[j][pl] = *(const u32x4 *)(xl + xa[j % 4][pl] + 256 * (j / 4));
+                    if constexpr (PLANES == 2)
+#pragma unroll
+                        for (int i = 0; i < RO; ++i) scale[i] = *(const float *)(lds + sa[i] + 4u * (uint32_t)(line - c));
                     __builtin_amdgcn_sched_barrier(0);
                     if constexpr (G != 128) {
                         w4_transpose(w[0]);
                         w4_transpose(w[1]);
                     }
+                    f32x4 of_line = {0.f, 0.f, 0.f, 0.f};
+                    f32x4 &to = PLANES == 2 ? of_line : acc;
 #pragma unroll
                     for (int g = 0; g < GROUPS; ++g) {
                         f32x4 sum = {0.f, 0.f, 0.f, 0.f}, xs = {0.f, 0.f, 0.f, 0.f};
@@ -394,18 +460,18 @@ struct W4Flow {
                         const float s = lo_f32<PT>(num[g]), b = hi_f32<PT>(num[g]) - 16.0f * s;
 #pragma unroll
                         for (int i = 0; i < RI; ++i) {
-                            acc[i] = __builtin_fmaf(s, sum[i], acc[i]);
-                            acc[i] = __builtin_fmaf(b, xs[i], acc[i]);
+                            to[i] = __builtin_fmaf(s, sum[i], to[i]);
+                            to[i] = __builtin_fmaf(b, xs[i], to[i]);
                         }
                     }
+                    if constexpr (PLANES == 2)
+#pragma unroll
+                        for (int i = 0; i < RO; ++i) acc[i] = __builtin_fmaf(scale[i], STACK ? of_line[i] + of_line[RO + i] : of_line[i], acc[i]);
                     // the next copies overwrite what has been read here
                     asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
                     at += L::STAGE;
                     if (++slot == L::DEPTH) slot = at = 0;
                 }
-                if constexpr (STACK)
-#pragma unroll
-                    for (int i = 0; i < RO; ++i) acc[i] += acc[RO + i];
                 done(tile, acc, c > 0);
             }
         }

@@ -444,9 +444,10 @@ int64_t lb_linear_w4_workspace(int64_t M, int64_t K, int64_t N, int64_t group);
  *   W2, P2: E x H rows of I weights; both laid out as lb_linear_w4's W and Wp.
  *   ids (T x top_k int32) and weights (T x top_k fp32) receive e_j and q_j; either may be
  *   NULL.
- * fp32 sums; between the two products silu(..) * (..) is held in two bf16 parts (2^-17 of
- * it).  A NaN among a token's logits counts as the largest and makes its row NaN, as an
- * infinite one does.  Sums have a fixed order: the same arguments give the same bits.
+ * fp32 sums; silu(..) * (..) is fp32 and enters the second product as two fp16 parts under a
+ * power of two for each 256 of them (2^-23 of it, 2^-39 of the largest).  A NaN among a token's
+ * logits counts as the largest and makes its row NaN, as an infinite one does.  Sums have a
+ * fixed order: the same arguments give the same bits.
  * group divides H and I.  E <= LB_MOE_EXPERTS_MAX, top_k <= min(E, LB_MOE_TOP_MAX); H * I is
  * bounded (LB_ERR_OVERFLOW above about 2^33).  More than 64 tokens run 64 at a time, each time
  * reading the weights again.  workspace: at least lb_moe_w4_workspace() bytes

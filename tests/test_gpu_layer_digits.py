@@ -79,3 +79,39 @@ def test_activations_with_a_mean(M, N, K, group, mean):
     got = float((out.cpu().double() - want).square().sum())
     # (two sums of squares of M N numbers, neither of which knows of the other)
     assert got <= (least + before) * (1 + 8 / math.sqrt(M * N)), (math.sqrt(got / least), math.sqrt(before / least))
+
+
+@pytest.mark.parametrize("T", [1, 3, 7, 12, 20])
+def test_between_the_experts_products(T):
+    """What passes between an expert's products keeps fp32's digits: rows of the second one take the difference of two
+    numbers that are nearly equal."""
+    group, H, wide = 32, 64, 64
+    I = group * wide
+    g = gen(T)
+    place = torch.randint(0, group, (wide,), generator=g) + torch.arange(wide) * group   # one number in each group, the rest zeros
+    gate = (0.2 * (1 + 0.05 * torch.rand(wide, generator=g))).to(HF)
+    lift = (0.025 * (1 + 0.1 * torch.rand(wide, generator=g))).to(HF)
+    w1 = torch.zeros(1, 2 * I, H // 2, dtype=torch.uint8)
+    p1 = torch.zeros(1, 2 * I, H // group, 2, dtype=HF)
+    for rows, s in ((place, gate), (I + place, lift)):
+        w1[0, rows] = 255
+        p1[0, rows, :, 0] = s[:, None]
+    a, u = 15 * gate.double(), 15 * lift.double()
+    h = a / (1 + torch.exp(-a)) * u
+    order = torch.sort(h).indices
+    first, second = order[torch.arange(H) % (wide - 1)], order[torch.arange(H) % (wide - 1) + 1]
+    p2 = torch.zeros(1, H, wide, 2, dtype=HF)
+    p2[0, torch.arange(H), first, 0] = -1.0
+    p2[0, torch.arange(H), second, 0] = 1.0
+    w2 = torch.full((1, H, I // 2), 255, dtype=torch.uint8)
+    x = torch.zeros(T, H, dtype=HF)
+    x[torch.arange(T), torch.arange(T)] = 1.0
+    out = torch.empty(T, H, dtype=HF, device="cuda")
+    lb.lb_moe_w4(x.cuda(), torch.ones(1, H, dtype=HF, device="cuda"), w1.cuda(), p1.cuda(), w2.cuda(), p2.cuda(), out, top_k=1)
+    want, both = 15 * (h[second] - h[first]), 15 * (h[second] + h[first])
+    # of each number, in half steps: exponential 2, its sum, quotient and product 3, its parts 2; then of 31 and of 16 times
+    # it, 15 of which are left: two whole steps of each in products, two in their scaling, and ten of 15 times it in joins
+    before = (7 + (31 * 4 + 16 * 4 + 31 * 2) / 15 + 10) * STEP * both
+    tol = before + half_step(HF) * (want.abs() + before) + floor_of(HF)
+    off = (out.cpu().double() - want).abs()
+    assert (off <= tol).all(), (off / tol).max()
