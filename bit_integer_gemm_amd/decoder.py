@@ -250,14 +250,53 @@ def near(name, got, want, before):
     assert ((got.cpu().double() - want).abs() <= bound).all(), name
 
 
+def near_rows(name, got, want, before):
+    """The same, and each row's error as a whole: half steps of the output bound it, with a sixteenth for what came before."""
+    near(name, got, want, before)
+    off = (got.cpu().double() - want).norm(dim=-1)
+    assert (off <= torch.finfo(got.dtype).eps / 2 * (1 + 2 ** -4) * want.norm(dim=-1) + torch.finfo(got.dtype).tiny).all(), name
+
+
 def norm(v, w):
     return v / (v.square().mean(-1, keepdim=True) + EPS).sqrt() * w.cpu().double()
 
 
-def product4(x, value):
-    """x W^T in 64 bits, and how far fp32 sums over 16 + u in place of u may be off: a few hundred roundings of sums of
-    at most eight times the largest weight's products."""
-    return x @ value.T, 400 * STEP * 8 * x.abs().sum(-1, keepdim=True) * value.abs().max()
+def product4(x, value, numbers, off=None):
+    """x W^T in 64 bits, and the square of fp32's error in it as sums of random signs have it: roundings of sums over
+    16 + u in place of u and b - 16 s in place of b, two for each 16 weights and three for each group; off: the same of x."""
+    scale, low = numbers.cpu().double().unbind(-1)
+    size = (31 * scale.abs() + (low - 16 * scale).abs()).repeat_interleave(value.shape[-1] // scale.shape[-1], -1)
+    steps = value.shape[-1] / 8 + 3 * scale.shape[-1]
+    square = steps * STEP ** 2 * (x.square() @ size.square().T)
+    return x @ value.T, square if off is None else square + off @ value.square().T
+
+
+def check_projection(layer, mixed, out):
+    want, off = product4(mixed.cpu().double().flatten(1), layer.o_value, layer.o_p)
+    near_rows("output projection", out, want, 8 * off.sqrt())
+
+
+def check_experts(layer, y, ids, z):
+    """Experts that fp32 logits choose (two closer than their error could change places), and their products."""
+    y, chosen = y.cpu().double(), ids.cpu().long()
+    p = torch.softmax(y @ layer.router.cpu().double().T, -1)
+    weight = p.gather(1, chosen)
+    assert (weight.min(1).values >= p.topk(layer.top_k).values[:, -1] * (1 - 1e-4)).all(), "experts"
+    assert all(len(set(row)) == layer.top_k for row in chosen.tolist()), "experts"
+    weight = weight / weight.sum(1, keepdim=True)
+    want, off = torch.zeros_like(y), torch.zeros_like(y)
+    for e in chosen.unique().tolist():
+        t, j = (chosen == e).nonzero(as_tuple=True)
+        u, du = product4(y[t], layer.up_value[e], layer.up_p[e])
+        (gate, lift), (dgate, dlift) = u.chunk(2, -1), du.chunk(2, -1)
+        s = gate * torch.sigmoid(gate)
+        # silu's slope is below 1.1; its own roundings and the product's: 2^-20
+        dh = 1.21 * dgate * lift.square() + s.square() * dlift + (2 ** -20 * s * lift).square()
+        v, dv = product4(s * lift, layer.down_value[e], layer.down_p[e], dh)
+        want[t] += weight[t, j, None] * v
+        # (weights: exponentials of logits off by some 2^-18)
+        off[t] += weight[t, j, None] ** 2 * (dv + (2 ** -16 * v).square())
+    near_rows("experts", z, want, 8 * off.sqrt())
 
 
 def check_layer(layer, cache, b, n, pos, r0, x, straight, qkv, mixed, out, r1, y, ids, z, r2):
@@ -277,29 +316,11 @@ def check_layer(layer, cache, b, n, pos, r0, x, straight, qkv, mixed, out, r1, y
     assert torch.equal(after[:, H + G:], straight.view(T, H + 2 * G, D)[:, H + G:]), "values"
     # projection, cache and attention
     check_middle(att, cache, b, n, x, straight, qkv, mixed)
-    want, off = product4(d(mixed).reshape(T, H * D), layer.o_value)
-    near("output projection", out, want, off)
+    check_projection(layer, mixed, out)
     want = r + d(out)
     near("residual", r1, want, STEP * want.abs())
     near("norm between", y, norm(want, layer.between), 40 * STEP * norm(want, layer.between).abs() + 2 * STEP)
-    # experts: those that fp32 logits choose (two closer than their error could change places)
-    yd = d(y)
-    p = torch.softmax(yd @ d(layer.router).T, -1)
-    chosen = ids.cpu().long()
-    weight = p.gather(1, chosen)
-    assert (weight.min(1).values >= p.topk(layer.top_k).values[:, -1] * (1 - 1e-4)).all(), "experts"
-    weight = weight / weight.sum(1, keepdim=True)
-    want, off = torch.zeros_like(yd), torch.zeros_like(yd)
-    for t in range(T):
-        for j, e in enumerate(chosen[t].tolist()):
-            u, du = product4(yd[t:t + 1], layer.up_value[e])
-            gate, lift = u.chunk(2, -1)
-            h = gate * torch.sigmoid(gate) * lift
-            dh = 1.1 * du * (lift.abs() + gate.abs() + du) + 2 ** -16 * h.abs()
-            v, dv = product4(h, layer.down_value[e])
-            want[t] += weight[t, j] * v[0]
-            off[t] += weight[t, j] * (dv + dh @ layer.down_value[e].abs().T + 1e-4 * v.abs())[0]
-    near("experts", z, want, off)
+    check_experts(layer, y, ids, z)
     want = d(r1) + norm(d(z), layer.after)
     near("residual after", r2, want, 40 * STEP * (want - d(r1)).abs() + STEP * want.abs())
 
