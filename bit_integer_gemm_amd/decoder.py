@@ -214,15 +214,17 @@ class Layer:
         self.before, self.between, self.after = ((1 + normal(hidden, std=0.2)).to(dtype).to(device) for _ in range(3))
         self.freqs, self.mult = lb.lb_rope_freqs(D, scaling="parts", factor=4.0, before=4096.0, device=device)
 
-    def __call__(self, r, cache, seq, pos, q_off, lens, max_q, max_len):
-        """r (T, hidden) fp32, updated in place; the rest as for Attention.  Returns what each step left."""
+    def __call__(self, r, cache, seq, pos, q_off, lens, max_q, max_len, left=None):
+        """r (T, hidden) fp32, updated in place and returned; the rest as for Attention.  left: a list that receives
+        what each step left, for check_layer (copies where a later step overwrites it)."""
         T, H, G, D, dtype, dev = r.shape[0], self.heads, self.kv_heads, self.D, self.before.dtype, r.device
-        r0 = r.clone()   # (for the check)
+        keep = [] if left is None else [r.clone()]
         x = torch.empty(r.shape, dtype=dtype, device=dev)
         lb.lb_residual_norm(None, r, None, x, w=self.before)
         qkv = torch.empty(T, self.attention.qkv.shape[0], dtype=dtype, device=dev)
         lb.lb_linear_w8a8(x, self.attention.qkv, self.attention.qkv_s, qkv, bias=self.attention.bias)
-        straight = qkv.clone()
+        if left is not None:
+            keep += [x, qkv.clone()]
         q, k, v = qkv.view(T, H + 2 * G, D).split((H, G, G), 1)
         lb.lb_rope(q, k, pos, self.freqs, q, k, mult=self.mult)   # where they lie
         lb.lb_kv4_write(k, v, cache.slots(seq, pos), *cache.tensors)
@@ -232,11 +234,14 @@ class Layer:
         lb.lb_linear_w4(mixed.view(T, H * D), self.o, self.o_p, out)
         y = torch.empty_like(x)
         lb.lb_residual_norm(out, r, r, y, w=self.between)
-        r1 = r.clone()
+        if left is not None:
+            keep += [qkv, mixed, out, r.clone()]
         z, ids = torch.empty_like(x), torch.empty(T, self.top_k, dtype=torch.int32, device=dev)
         lb.lb_moe_w4(y, self.router, self.up, self.up_p, self.down, self.down_p, z, top_k=self.top_k, renorm=True, ids=ids)
         lb.lb_residual_norm(z, r, r, None, post_w=self.after)
-        return r0, x, straight, qkv, mixed, out, r1, y, ids, z, r.clone()
+        if left is not None:
+            left[:] = keep + [y, ids, z, r]
+        return r
 
 
 EPS = 1e-5   # of the norms, lb_residual_norm's default
@@ -339,16 +344,17 @@ def run_layer(hidden=4096, heads=32, kv_heads=8, D=128, experts=16, top_k=2, wid
     pos = torch.cat([torch.arange(n) for n in prompts]).to(dev)
     lens = torch.tensor(prompts, dtype=torch.int32, device=dev)
     args = (cache, seq, pos, off.to(torch.int32).to(dev), lens, max(prompts), longest)
-    left = layer(start.clone(), *args)
+    left = []
+    layer(start.clone(), *args, left)
     for b, n in enumerate(prompts):
         check_layer(layer, cache, b, n, pos[off[b]:off[b + 1]], *(a[off[b]:off[b + 1]] for a in left))
-    prefill = clock(lambda: layer(start.clone(), *args), 10)
+    prefill = clock(lambda: layer(start, *args), 10)
 
     one = torch.empty(B, hidden, device=dev)
     every, each = torch.arange(B, device=dev), torch.arange(B + 1, dtype=torch.int32, device=dev)
 
-    def step():
-        return layer(one, cache, every, lens.long() - 1, each, lens, 1, longest)
+    def step(left=None):
+        layer(one, cache, every, lens.long() - 1, each, lens, 1, longest, left)
 
     one.copy_(torch.randn(B, hidden, generator=g))
     lens.add_(1)
@@ -357,16 +363,25 @@ def run_layer(hidden=4096, heads=32, kv_heads=8, D=128, experts=16, top_k=2, wid
     with torch.cuda.stream(side):   # the first step, outside the graph
         step()
     torch.cuda.current_stream().wait_stream(side)
-    graph = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(graph):
-        left = step()
+    checked, graph = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(checked):
+        step(left)
     for i in range(steps):
         one.copy_(torch.randn(B, hidden, generator=g))
         if i:
             lens.add_(1)
-        graph.replay()
+        checked.replay()
         for b, n in enumerate(prompts):
             check_layer(layer, cache, b, n + i + 1, lens[b:b + 1] - 1, *(a[b:b + 1] for a in left))
+    with torch.cuda.graph(graph):   # as it is served: without the check's copies
+        step()
+    one.copy_(torch.randn(B, hidden, generator=g))
+    again = one.clone()
+    checked.replay()
+    want = one.clone()
+    one.copy_(again)
+    graph.replay()
+    assert torch.equal(one, want), "replayed without copies"
     return prefill, clock(step, 20), clock(graph.replay, 20)
 
 
