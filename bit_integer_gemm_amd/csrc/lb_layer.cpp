@@ -8,7 +8,7 @@
 #include <algorithm>
 #include <cmath>
 
-#include "lb_internal.hpp"
+#include "lb_layer.hpp"
 
 namespace {
 

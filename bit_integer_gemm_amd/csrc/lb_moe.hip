@@ -20,7 +20,7 @@
 // + 5.0 us, where the bytes would take 26.
 #include <algorithm>
 
-#include "lb_internal.hpp"
+#include "lb_layer.hpp"
 #include "lb_w4.hpp"
 
 namespace lb {

@@ -1,7 +1,7 @@
 // lb_rows.hip -- what stands between the products of a decoder layer, row by row: the norms
 // on both sides of a block with its gate and the residual, and rotary positions.
 #include "lb_float.hpp"
-#include "lb_internal.hpp"
+#include "lb_layer.hpp"
 
 namespace lb {
 

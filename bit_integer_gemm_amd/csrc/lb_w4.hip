@@ -1,7 +1,7 @@
 // lb_w4.hip -- linear layer with 4-bit weights and group scales on 16-bit activations.
 //
 //   out[m,n] = round(sum_k x[m,k] (u[n,k] s[n,g] + b[n,g]) + bias[n]),  g = k / G
-#include "lb_internal.hpp"
+#include "lb_layer.hpp"
 #include "lb_w4.hpp"
 
 namespace lb {

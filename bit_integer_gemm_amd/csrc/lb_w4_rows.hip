@@ -23,7 +23,7 @@
 // whole stages with zeros, and forms X.
 #include <algorithm>
 
-#include "lb_internal.hpp"
+#include "lb_layer.hpp"
 #include "lb_w4.hpp"
 
 namespace lb {
