@@ -16,7 +16,6 @@ struct NormArgs {
     int32_t H;
     float alpha, eps;
 };
-enum { NORM_H_MAX = 32768 };   // a row in the registers of 1024 threads
 hipError_t launch_residual_norm(int ftype, int rtype, const NormArgs &a, int64_t M, hipStream_t s);
 
 // Rotary positions of Hq heads of q and Hk of k (k may be null, Hk 0).  tokens, heads: those of

@@ -84,7 +84,9 @@ __global__ __launch_bounds__(64 * ROUTER_WAVES) void moe_router_kernel(MoeArgs a
 // expert and few are without, shares them out among all).  With 5 tokens of 6 of 64 experts
 // about 24 are found where there could be 30: 44 us for both products, where workgroups for all
 // 30 took 48.  48 tokens of 8 of 128 meet all experts but six, and no search pays.
-enum { EXPERTS_MAX = 1024 };
+enum { EXPERTS_MAX = LB_MOE_EXPERTS_MAX, MOE_TOP_MAX = LB_MOE_TOP_MAX };
+static_assert(EXPERTS_MAX <= 16 * 64 && EXPERTS_MAX % 32 == 0, "the logits of a token in 16 registers of a wave, a bit each");
+static_assert(MOE_TOP_MAX <= 64 && MOE_TOKENS <= 64, "a lane to each of a token's experts, to each token");
 enum { MOE_LIST = 2 + MOE_TOKENS };   // in the workspace: count, expert, rows (one token: count, expert, row, logit)
 struct MoeList {
     int32_t rank[MOE_TOKENS];   // the expert's rank in each token's order, if below k, else -1
@@ -503,7 +505,8 @@ __device__ inline int32_t rank_of(const uint32_t *order, int32_t E, int32_t e, u
     return above;
 }
 
-enum { COMBINE_THREADS = 256, MOE_TOP_MAX = 64 };
+enum { COMBINE_THREADS = 256 };
+static_assert(MOE_TOP_MAX <= COMBINE_THREADS, "a thread to each of a token's weights");
 template <class T>
 __global__ __launch_bounds__(COMBINE_THREADS) void moe_combine_kernel(MoeArgs a)
 {

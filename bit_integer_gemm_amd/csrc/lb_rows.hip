@@ -121,6 +121,7 @@ __global__ __launch_bounds__(1024) void residual_norm_kernel(NormArgs a)
 template <class T, class RT> static hipError_t residual_norm_t(const NormArgs &a, int64_t M, hipStream_t s)
 {
     const int32_t chunks = a.H / 8;
+    static_assert(LB_NORM_H_MAX <= 8 * 4 * 1024, "a row in the registers of 1024 threads");
     const int c = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : 4;
     const uint32_t threads = (uint32_t)(((chunks + c - 1) / c + 63) / 64 * 64);
     const int64_t most = LAUNCH_THREADS / threads;
@@ -163,6 +164,7 @@ hipError_t launch_residual_norm(int ftype, int rtype, const NormArgs &a, int64_t
 // An item is the 8 numbers from 8 j on that a thread loads: of a head in halves the first
 // R / 16 items are pairs of them, R / 2 apart.
 constexpr int32_t ROPE_ANGLES = 2048;   // angles of a workgroup's tokens, at most
+static_assert(LB_ROPE_R_MAX / 2 <= ROPE_ANGLES, "one token's at least");
 
 template <class T, bool PAIRS>
 __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a)

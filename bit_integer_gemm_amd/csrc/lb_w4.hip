@@ -46,6 +46,7 @@ __global__ __launch_bounds__(64 * W4_WAVES) void w4_few_kernel(const T *__restri
 }
 
 enum { FEW_LDS = 160 * 1024 };
+static_assert((int64_t)LB_W4_N_MAX / 16 * 64 * W4_WAVES <= LAUNCH_THREADS, "all columns in a launch");
 template <class T, int G> static hipError_t w4_g(const W4Args &a, int cu, hipStream_t s)
 {
     const int64_t tiles = (a.N + 15) / 16, lines = (a.K + 255) / 256;
