@@ -128,6 +128,7 @@ int lb_rope_freqs(double *freqs, float *mult, int64_t R, double base, int scalin
         auto pair_of = [&](double n) { return (double)R * std::log(before / (n * turn)) / (2.0 * std::log(base)); };
         first = std::max(std::floor(pair_of(high)), 0.0);
         last = std::min(std::ceil(pair_of(low)), (double)(R - 1));
+        if (last <= 0.0) first = last = -1.0;   // no pair turns more than `low` times
         if (factor > 1.0) *mult = (float)(0.1 * std::log(factor) + 1.0);
     }
     for (int64_t i = 0; i < R / 2; ++i) {

@@ -173,3 +173,16 @@ def test_sizes_beyond_the_limits(lib):
                                    (lb.LB_ERR_OVERFLOW, dict(ldx=2 ** 24 + 8))])
     assert lb.lb_linear_w4_workspace(40, 128, lb.W4_N_MAX + 16, 64) == 0
     assert lb.lb_linear_w4_workspace(40, 128, lb.W4_N_MAX, 64) > 0
+
+
+@pytest.mark.parametrize("before,low,high", [(4.0, 1.0, 32.0), (6.0, 1.0, 4.0), (40.0, 8.0, 32.0), (100.0, 16.0, 17.0), (200.0, 1.0, 32.0)])
+@pytest.mark.parametrize("R", [2, 4, 64])
+def test_rope_freqs_parts_of_short_contexts(lib, R, before, low, high):
+    """A pair that turns at most `low` times is stretched, one that turns `high` times is not, the first pair too."""
+    f = 10000.0 ** (-2 * np.arange(R // 2) / R)
+    turns = before * f / (2 * math.pi)
+    got, _ = freqs(R, 10000.0, lb.LB_ROPE_PARTS, 8.0, before, low, high)
+    near = dict(rtol=1e-13, atol=0)
+    np.testing.assert_allclose(got[turns <= low * (1 - 1e-9)], f[turns <= low * (1 - 1e-9)] / 8, **near)
+    np.testing.assert_allclose(got[turns >= high * (1 + 1e-9)], f[turns >= high * (1 + 1e-9)], **near)
+    assert (got <= f * (1 + 1e-15)).all() and (got >= f / 8 * (1 - 1e-15)).all()
