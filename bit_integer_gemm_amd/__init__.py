@@ -589,7 +589,8 @@ def lb_rope_freqs(R: int, base: float = 10000.0, scaling="plain", factor: float 
                   low: float = 1.0, high: float = 32.0, device="cuda"):
     """(freqs, mult) for lb_rope: R/2 frequencies, a float64 tensor on `device`, and the factor of the turned
     numbers.  scaling: "plain", "linear", "base", "parts" or "bands" (see the header), for contexts `factor` times
-    longer than `before`."""
+    longer than `before`.  low, high: turns; the defaults are those usual with "parts" ("bands" is mostly used with
+    high 4)."""
     T = _torch()
     f, m = (ctypes.c_double * max(R // 2, 1))(), ctypes.c_float()
     _raise(load().lb_rope_freqs(f, ctypes.byref(m), R, base, _ROPE_SCALINGS.get(scaling, scaling), factor, before, low,

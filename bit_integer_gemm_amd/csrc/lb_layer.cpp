@@ -47,8 +47,8 @@ int check_moe(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k, int64_t
     int st = check_w4(T, H, I, group, ftype);
     if (st == LB_OK) st = check_w4(T, I, H, group, ftype);
     if (st != LB_OK) return st;
-    // byte offsets between an expert's gate and up rows, and numbers of (token, rank) pairs
-    // times columns, are 32-bit; one launch covers all experts
+    // experts of up to 4 GiB a matrix; byte offsets and numbers of (token, rank) pairs times columns
+    // are 32-bit; one launch covers all experts
     if ((double)(I + 256) * (double)H >= 8589934592.0) return LB_ERR_OVERFLOW;
     const int64_t tokens = std::min<int64_t>(T, lb::MOE_TOKENS);
     if (tokens * top_k * I * 4 >= (int64_t)0xFFFF0000 || tokens * top_k * H >= kLim) return LB_ERR_OVERFLOW;

@@ -421,7 +421,8 @@ int lb_rope_freqs(double *freqs, float *mult, int64_t R, double base, int scalin
  * from a row of X that holds an infinity or a NaN is not finite (NaN or infinite).  The sums run
  * over 16 + u in place of u and b - 16 s in place of b, so that fp32's roundings are of larger
  * sums; with more than 16 rows, (b - 16 s) sum_k X comes from three bf16 parts of each (2^-23
- * of it).
+ * of it).  A group's sum of X (16 + u) has to be in fp32's range, and s times it: in bf16, X up to
+ * 2^116 in magnitude (fp16: any); beyond, out may be infinite or NaN where the formula is finite.
  * workspace: at least lb_linear_w4_workspace(M, K, N, group) bytes (LB_ERR_WORKSPACE
  * otherwise; NULL where that is 0, as for up to 16 rows).  It depends on the current device's
  * number of compute units too: ask on the device that the call runs on.
@@ -444,10 +445,10 @@ int64_t lb_linear_w4_workspace(int64_t M, int64_t K, int64_t N, int64_t group);
  *   W2, P2: E x H rows of I weights; both laid out as lb_linear_w4's W and Wp.
  *   ids (T x top_k int32) and weights (T x top_k fp32) receive e_j and q_j; either may be
  *   NULL.
- * fp32 sums; silu(..) * (..) is fp32 and enters the second product as two fp16 parts under a
- * power of two for each 256 of them (2^-23 of it, 2^-39 of the largest).  A NaN among a token's
- * logits counts as the largest and makes its row NaN, as an infinite one does.  Sums have a
- * fixed order: the same arguments give the same bits.
+ * fp32 sums, X's range as lb_linear_w4's; silu(..) * (..) is fp32 and enters the second product
+ * as two fp16 parts under a power of two for each 256 of them (2^-23 of it, 2^-39 of the
+ * largest).  A NaN among a token's logits counts as the largest and makes its row NaN, as an
+ * infinite one does.  Sums have a fixed order: the same arguments give the same bits.
  * group divides H and I.  E <= LB_MOE_EXPERTS_MAX, top_k <= min(E, LB_MOE_TOP_MAX); H * I is
  * bounded (LB_ERR_OVERFLOW above about 2^33).  More than 64 tokens run 64 at a time, each time
  * reading the weights again.  workspace: at least lb_moe_w4_workspace() bytes

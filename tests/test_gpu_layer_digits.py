@@ -9,7 +9,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 import bit_integer_gemm_amd as lb  # noqa: E402
-from test_gpu_layer import BF, HF, STEP, floor_of, gen, half_step, weights  # noqa: E402
+from test_gpu_layer import BF, HF, STEP, check_output, floor_of, gen, half_step, product_bound, weights  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -115,3 +115,21 @@ def test_between_the_experts_products(T):
     tol = before + half_step(HF) * (want.abs() + before) + floor_of(HF)
     off = (out.cpu().double() - want).abs()
     assert (off <= tol).all(), (off / tol).max()
+
+
+@pytest.mark.parametrize("M", [3, 40, 300])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_largest_activations(M, group):
+    """bf16 x of 2^116 in magnitude, whole groups of one sign and the largest levels: the sums stay in fp32's range."""
+    N, K = 70, 512
+    g = gen(M)
+    sign = 1 - 2.0 * torch.randint(0, 2, (M, K // group), generator=g)
+    x = (2.0 ** 116 * sign.repeat_interleave(group, 1)).to(BF)
+    w = torch.full((N, K // 2), 255, dtype=torch.uint8)
+    s = 2.0 ** -60 * (1 + torch.rand(N, K // group, generator=g))
+    p = torch.stack([s, -7.5 * s], -1).to(BF)
+    wd = (15 * p[..., 0].double() + p[..., 1].double()).repeat_interleave(group, 1)
+    out = torch.empty(M, N, dtype=BF, device="cuda")
+    lb.lb_linear_w4(x.cuda(), w.cuda(), p.cuda(), out)
+    assert out.isfinite().all()
+    check_output(out, x.double() @ wd.T, product_bound(x, p, K), BF)
