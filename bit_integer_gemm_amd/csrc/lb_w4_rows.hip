@@ -95,6 +95,12 @@ template <int G, int WM, int WN> struct RowsLds {
         NUMBERS = NC * 2048, STAGE = X + W + NUMBERS, COPIES = XC + WC + NC,
         UNITS = WN * 128 / G,                                  // (32 columns, group) of a stage
         BLOCK = 16 * G / 128,                                  // stages whose minima enter together
+        // How the loop over stages is written, by registers and by times.  NEST: a loop for each block, and
+        // the pipelined sums end with it; FRESH: addresses of the minima are formed for each block.  Groups of
+        // 64 in one tile of columns: 34.6 us for 128 x 11008 x 4096 with one loop and fresh addresses, 38.3 with
+        // nested ones.  Two tiles: without both, groups of 32 and 64 spill (800 and 690 us for 4096 x 11008 x
+        // 4096 in place of 680 and 505); groups of 128 take 400 us with fresh addresses, 392 without.
+        NEST = WN == 2 || G != 64, FRESH = G == 64 || (G == 32 && WN == 2),
         OUT_LD = BN + 8                                        // the tile on its way out, 16-bit
     };
     static_assert(BM * OUT_LD * 2 <= STAGES * STAGE, "the tile over the ring");
@@ -158,14 +164,22 @@ __global__ __launch_bounds__(512, 2) void w4_rows_kernel(RowsArgs a)
             for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.f;
     const __bf16 *xp[WM];
     const uint32_t *np[WN];
+    auto aim = [&](int32_t at) {
 #pragma unroll
-    for (int m = 0; m < WM; ++m) xp[m] = a.parts + (int64_t)(m0 + min(32 * (WM * wm + m) + r, rows - 1)) * a.groups16 + 8 * h;
+        for (int m = 0; m < WM; ++m) xp[m] = a.parts + (int64_t)(m0 + min(32 * (WM * wm + m) + (at & 31), rows - 1)) * a.groups16 + 8 * (at >> 5);
 #pragma unroll
-    for (int n = 0; n < WN; ++n) np[n] = a.p + (int64_t)(n0 + min(32 * (WN * wn + n) + r, cols - 1)) * a.groups + 8 * h;
+        for (int n = 0; n < WN; ++n) np[n] = a.p + (int64_t)(n0 + min(32 * (WN * wn + n) + (at & 31), cols - 1)) * a.groups + 8 * (at >> 5);
+    };
+    if constexpr (!L::FRESH) aim(lane);
     // The minima of groups lo .. hi, of the 16 from g on, into the accumulators: acc[m][n][i] is row
     // 8 (i / 4) + 4 h + i % 4 of tile m, column lane % 32 of tile n.  Of the nine products of X's parts
     // and b''s, the six down to 2^-16 of the first, smallest first.
     auto minima = [&](int32_t g, int32_t lo, int32_t hi) {
+        if constexpr (L::FRESH) {
+            int32_t at = lane;
+            asm volatile("" : "+v"(at));
+            aim(at);
+        }
         u32x4 xv[WM][3];
         uint32_t nv[WN][8];
 #pragma unroll
@@ -184,8 +198,8 @@ __global__ __launch_bounds__(512, 2) void w4_rows_kernel(RowsArgs a)
                 float v[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int32_t at = g + 8 * h + 2 * i + e;
-                    const uint32_t w = at >= lo && at < hi ? nv[n][2 * i + e] : 0u;
+                    const int32_t k = g + 8 * h + 2 * i + e;
+                    const uint32_t w = k >= lo && k < hi ? nv[n][2 * i + e] : 0u;
                     v[e] = hi_f32<T>(w) - 16.0f * lo_f32<T>(w);
                 }
 #pragma unroll
@@ -216,100 +230,98 @@ __global__ __launch_bounds__(512, 2) void w4_rows_kernel(RowsArgs a)
     for (int m = 0; m < WM; ++m)
 #pragma unroll
         for (int i = 0; i < 16; ++i) sum[1][m][i] = 0.f;
-    for (int32_t st = first; st < last;) {
-        const int32_t block = st / L::BLOCK, more = min((block + 1) * L::BLOCK, last);
-        minima(16 * block, st * PER, min(more * PER, a.groups));
-        for (; st < more; ++st) {
-            wait_vm_barrier<L::COPIES>();
-            const char *s0 = smem + at;
-            // the columns' pieces and numbers first, then the rows in the order of their use: the first
-            // matrix instructions need not wait for the last reads
-            u32x4 wv[WN][2], x[8][WM];
-            float scale[WN][PER];
+    auto stage = [&](int32_t st) {
+        wait_vm_barrier<L::COPIES>();
+        const char *s0 = smem + at;
+        // the columns' pieces and numbers first, then the rows in the order of their use: the first
+        // matrix instructions need not wait for the last reads
+        u32x4 wv[WN][2], x[8][WM];
+        float scale[WN][PER];
 #pragma unroll
-            for (int n = 0; n < WN; ++n)
+        for (int n = 0; n < WN; ++n)
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    wv[n][t] = *(const u32x4 *)(s0 + w_at + 2048u * (uint32_t)n + 16u * ((uint32_t)(2 * t + h) ^ (uint32_t)((r >> 2) & 3)));
+            for (int t = 0; t < 2; ++t)
+                wv[n][t] = *(const u32x4 *)(s0 + w_at + 2048u * (uint32_t)n + 16u * ((uint32_t)(2 * t + h) ^ (uint32_t)((r >> 2) & 3)));
 #pragma unroll
-            for (int n = 0; n < WN; ++n)
+        for (int n = 0; n < WN; ++n)
 #pragma unroll
-                for (int g = 0; g < PER; ++g)
-                    scale[n][g] = lo_f32<T>(*(const uint32_t *)(s0 + n_at + 128u * (uint32_t)n + 4u * (uint32_t)(L::BN * g)));
+            for (int g = 0; g < PER; ++g)
+                scale[n][g] = lo_f32<T>(*(const uint32_t *)(s0 + n_at + 128u * (uint32_t)n + 4u * (uint32_t)(L::BN * g)));
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 8; ++j)
 #pragma unroll
-                for (int m = 0; m < WM; ++m) {
-                    // instruction j takes 8 weights of piece 2 (j / 4) + h, word j % 4; G = 32: of piece
-                    // 2 (j / 4) + j / 2 % 2, word 2 (j % 2) + h
-                    const uint32_t p = G == 32 ? (uint32_t)(4 * (2 * (j / 4) + j / 2 % 2) + 2 * (j % 2)) + (uint32_t)h
-                                               : (uint32_t)(8 * (j / 4) + j % 4) + 4u * (uint32_t)h;
-                    x[j][m] = *(const u32x4 *)(s0 + x_at + 8192u * (uint32_t)m + 16u * (p ^ (uint32_t)(r & 15)));
+            for (int m = 0; m < WM; ++m) {
+                // instruction j takes 8 weights of piece 2 (j / 4) + h, word j % 4; G = 32: of piece
+                // 2 (j / 4) + j / 2 % 2, word 2 (j % 2) + h
+                const uint32_t p = G == 32 ? (uint32_t)(4 * (2 * (j / 4) + j / 2 % 2) + 2 * (j % 2)) + (uint32_t)h
+                                           : (uint32_t)(8 * (j / 4) + j % 4) + 4u * (uint32_t)h;
+                x[j][m] = *(const u32x4 *)(s0 + x_at + 8192u * (uint32_t)m + 16u * (p ^ (uint32_t)(r & 15)));
+            }
+#pragma unroll
+        for (int n = 0; n < WN; ++n) {
+            u32x4 w[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                w[t] = wv[n][t];
+                if constexpr (G == 32) {
+                    const auto c = __builtin_amdgcn_permlane32_swap(w[t][0], w[t][1], false, false);
+                    const auto d = __builtin_amdgcn_permlane32_swap(w[t][2], w[t][3], false, false);
+                    w[t] = u32x4{c[0], d[0], c[1], d[1]};
                 }
+            }
 #pragma unroll
-            for (int n = 0; n < WN; ++n) {
-                u32x4 w[2];
+            for (int g = 0; g < PER; ++g) {
+                constexpr int STEPS = 8 / PER;
+                constexpr int CHAINS = WM == 1 && STEPS > 2 ? 2 : 1;   // one tile of rows: sums in two, or each instruction waits for the last
+                // PIPE: the sums of the unit (columns, group) before are scaled step by step beside this
+                // one's matrix instructions, the last unit's in the next stage or behind the loop
+                const int now = PIPE ? (n * PER + g) % 2 : 0, was = 1 - now;
+                const int wn_ = (n * PER + g + L::UNITS - 1) % L::UNITS / PER;   // whose columns they are
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    w[t] = wv[n][t];
-                    if constexpr (G == 32) {
-                        const auto c = __builtin_amdgcn_permlane32_swap(w[t][0], w[t][1], false, false);
-                        const auto d = __builtin_amdgcn_permlane32_swap(w[t][2], w[t][3], false, false);
-                        w[t] = u32x4{c[0], d[0], c[1], d[1]};
+                for (int m = 0; m < WM; ++m)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) sum[now][m][i] = 0.f;
+                f32x16 other;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) other[i] = 0.f;
+#pragma unroll
+                for (int j = g * STEPS; j < (g + 1) * STEPS; ++j) {
+                    const u32x4 lv = w4_levels<T>(w[j / 4][j % 4], konst);
+#pragma unroll
+                    for (int m = 0; m < WM; ++m) {
+                        if (CHAINS == 2 && j % 2) other = mfma32<T>(x[j][m], lv, other);
+                        else sum[now][m] = mfma32<T>(x[j][m], lv, sum[now][m]);
+                        if constexpr (PIPE)
+#pragma unroll
+                            for (int i = 16 / STEPS * (j % STEPS); i < 16 / STEPS * (j % STEPS + 1); ++i)
+                                acc[m][wn_][i] = __builtin_fmaf(pending, sum[was][m][i], acc[m][wn_][i]);
+                    }
+                    // a copy of the stage after next now and then: all at once they would hold up
+                    // every wave at the start of a stage
+                    if (WN == 1) {
+                        if (j < L::COPIES) copy(j, st + 2, lds0 + next);
+                    } else if (j % 2 == 0 && 4 * n + j / 2 < L::COPIES) {
+                        copy(4 * n + j / 2, st + 2, lds0 + next);
                     }
                 }
+                if constexpr (CHAINS == 2)
 #pragma unroll
-                for (int g = 0; g < PER; ++g) {
-                    constexpr int STEPS = 8 / PER;
-                    constexpr int CHAINS = WM == 1 && STEPS > 2 ? 2 : 1;   // one tile of rows: sums in two, or each instruction waits for the last
-                    // PIPE: the sums of the unit (columns, group) before are scaled step by step beside this
-                    // one's matrix instructions, the last unit's in the next stage or behind the loop
-                    const int now = PIPE ? (n * PER + g) % 2 : 0, was = 1 - now;
-                    const int wn_ = (n * PER + g + L::UNITS - 1) % L::UNITS / PER;   // whose columns they are
+                    for (int i = 0; i < 16; ++i) sum[now][0][i] += other[i];
+                if constexpr (PIPE) {
+                    pending = scale[n][g];
+                } else {
 #pragma unroll
                     for (int m = 0; m < WM; ++m)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) sum[now][m][i] = 0.f;
-                    f32x16 other;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) other[i] = 0.f;
-#pragma unroll
-                    for (int j = g * STEPS; j < (g + 1) * STEPS; ++j) {
-                        const u32x4 lv = w4_levels<T>(w[j / 4][j % 4], konst);
-#pragma unroll
-                        for (int m = 0; m < WM; ++m) {
-                            if (CHAINS == 2 && j % 2) other = mfma32<T>(x[j][m], lv, other);
-                            else sum[now][m] = mfma32<T>(x[j][m], lv, sum[now][m]);
-                            if constexpr (PIPE)
-#pragma unroll
-                                for (int i = 16 / STEPS * (j % STEPS); i < 16 / STEPS * (j % STEPS + 1); ++i)
-                                    acc[m][wn_][i] = __builtin_fmaf(pending, sum[was][m][i], acc[m][wn_][i]);
-                        }
-                        // a copy of the stage after next now and then: all at once they would hold up
-                        // every wave at the start of a stage
-                        if (WN == 1) {
-                            if (j < L::COPIES) copy(j, st + 2, lds0 + next);
-                        } else if (j % 2 == 0 && 4 * n + j / 2 < L::COPIES) {
-                            copy(4 * n + j / 2, st + 2, lds0 + next);
-                        }
-                    }
-                    if constexpr (CHAINS == 2)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) sum[now][0][i] += other[i];
-                    if constexpr (PIPE) {
-                        pending = scale[n][g];
-                    } else {
-#pragma unroll
-                        for (int m = 0; m < WM; ++m)
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) acc[m][n][i] = __builtin_fmaf(scale[n][g], sum[now][m][i], acc[m][n][i]);
-                    }
+                        for (int i = 0; i < 16; ++i) acc[m][n][i] = __builtin_fmaf(scale[n][g], sum[now][m][i], acc[m][n][i]);
                 }
             }
-            static_assert(L::COPIES <= 8, "all copies are made");
-            at = at == 2 * L::STAGE ? 0 : at + L::STAGE;
-            next = next == 2 * L::STAGE ? 0 : next + L::STAGE;
         }
+        static_assert(L::COPIES <= 8, "all copies are made");
+        at = at == 2 * L::STAGE ? 0 : at + L::STAGE;
+        next = next == 2 * L::STAGE ? 0 : next + L::STAGE;
+    };
+    auto flush = [&] {   // the last unit's sums
         if constexpr (PIPE)
 #pragma unroll
             for (int m = 0; m < WM; ++m)
@@ -318,6 +330,25 @@ __global__ __launch_bounds__(512, 2) void w4_rows_kernel(RowsArgs a)
                     acc[m][WN - 1][i] = __builtin_fmaf(pending, sum[1][m][i], acc[m][WN - 1][i]);
                     sum[1][m][i] = 0.f;
                 }
+    };
+    auto block_end = [&](int32_t st) { return min((st / L::BLOCK + 1) * L::BLOCK, last); };
+    auto enter = [&](int32_t st, int32_t end) { minima(16 * (st / L::BLOCK), st * PER, min(end * PER, a.groups)); };
+    if constexpr (L::NEST) {
+        for (int32_t st = first; st < last;) {
+            const int32_t end = block_end(st);
+            enter(st, end);
+            for (; st < end; ++st) stage(st);
+            flush();
+        }
+    } else {
+        for (int32_t st = first, end = first; st < last; ++st) {
+            if (st == end) {
+                end = block_end(st);
+                enter(st, end);
+            }
+            stage(st);
+        }
+        flush();
     }
     wait_vm_all();   // (the last two stages' copies brought nothing)
     if (a.splits > 1) {
