@@ -80,10 +80,10 @@ __global__ __launch_bounds__(64 * ROUTER_WAVES) void moe_router_kernel(MoeArgs a
 
 // ---- who goes where --------------------------------------------------------
 // Workgroups are shared out evenly among the experts that have tokens: each workgroup finds
-// these from the logits (or, where there are three pairs of a token and an expert for every
-// expert and few are without, shares them out among all).  With 5 tokens of 6 of 64 experts
-// about 24 are found where there could be 30: 44 us for both products, where workgroups for all
-// 30 took 48.  48 tokens of 8 of 128 meet all experts but six, and no search pays.
+// these from the logits, or, where there are five pairs of a token and an expert for every four
+// experts, shares them out among all.  Both products of 13 tokens of 6 of 64 experts take 98 us with the
+// search and 110 without, 18 of 8 of 128 92 and 95, 60 of 1 of 60 100 and 118; 20 of 8 of 128 102 and 96,
+// 47 of them 127 and 113, 16 of 6 of 64 111 and 109, 12 of 2 of 16 47 and 45 (whole calls).
 enum { EXPERTS_MAX = LB_MOE_EXPERTS_MAX, MOE_TOP_MAX = LB_MOE_TOP_MAX };
 static_assert(EXPERTS_MAX <= 16 * 64 && EXPERTS_MAX % 32 == 0, "the logits of a token in 16 registers of a wave, a bit each");
 static_assert(MOE_TOP_MAX <= 64 && MOE_TOKENS <= 64, "a lane to each of a token's experts, to each token");
@@ -575,7 +575,7 @@ template <int G> static MoeShape moe_shape(const MoeArgs &a, int32_t tiles, int3
 {
     MoeShape m;
     const int32_t lines = (K + 255) / 256, pairs = a.T * a.top_k;
-    m.g.active = pairs < 3 * a.E;
+    m.g.active = 4 * pairs < 5 * a.E;   // (never without where there are fewer pairs than experts: lists are for as many)
     m.g.rows = a.T < 16 ? a.T : 16;
     m.g.tiles = tiles;
     m.g.chunk = w4_chunk(lines, planes * m.g.rows, 66 * 1024);

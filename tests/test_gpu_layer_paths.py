@@ -24,9 +24,13 @@ TOKEN = [(1, 8, 8, 256, 4096, 32),      # its experts' activations do not fit to
          (1, 200, 4, 256, 64, 64), (1, 129, 1, 128, 96, 32), (1, 300, 7, 128, 64, 64),   # more than 128 experts, than 256
          (1, 1000, 8, 64, 32, 32), (1, 1024, 64, 96, 32, 32)]
 
+# as many pairs of a token and an expert as experts, and around five for every four, where the search for those met ends
+SHARED = [(16, 16, 1, 128, 64, 32), (19, 16, 1, 128, 64, 32), (20, 16, 1, 128, 64, 32), (21, 16, 1, 128, 64, 32),
+          (13, 64, 6, 128, 96, 32), (14, 64, 6, 128, 96, 32), (30, 200, 8, 64, 64, 32), (32, 200, 8, 64, 64, 32)]
+
 
 @pytest.mark.parametrize("dtype", [BF, HF])
-@pytest.mark.parametrize("T,E,k,H,I,group", CHUNKS + TOKEN)
+@pytest.mark.parametrize("T,E,k,H,I,group", CHUNKS + TOKEN + SHARED)
 def test_moe_w4(dtype, T, E, k, H, I, group):
     layer.test_moe_w4(dtype, T, E, k, H, I, group)
 
