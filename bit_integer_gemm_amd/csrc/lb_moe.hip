@@ -578,6 +578,9 @@ template <int G> static MoeShape moe_shape(const MoeArgs &a, int32_t tiles, int3
     m.g.active = 4 * pairs < 5 * a.E;   // (never without where there are fewer pairs than experts: lists are for as many)
     m.g.rows = a.T < 16 ? a.T : 16;
     m.g.tiles = tiles;
+    // 66 KiB of x: 16 rows of it, the longest rings and a first product's sums fill MOE_LDS.  Longer rows come
+    // in chunks: 16 tokens of 2 of 8 of 2048 x 4096 take 45 us, of 2304 x 4096 67 (which the router's launch
+    // adds 5 to)
     m.g.chunk = w4_chunk(lines, planes * m.g.rows, 66 * 1024);
     m.g.one = m.g.chunk >= lines;
     m.g.x_bytes = W4Lds<G>::x_bytes(planes, m.g.rows, m.g.chunk);

@@ -284,7 +284,8 @@ struct W4Flow {
     }
 
     // x of the chunk from line c on: piece p of row i lies at p ^ i % 16 of the row.  fp32: the halves of
-    // a piece's numbers where its planes will be.
+    // a piece's numbers in the two planes, of which the second has piece p at p ^ i % 16 ^ 8 in the end (both
+    // planes of 8 rows then lie on all 64 banks).
     template <class XAt> __device__ inline void ask_x(int32_t c, int32_t rows, const i32x4 rx, XAt &&x_at)
     {
         const int32_t per = min(chunk, lines - c) * 32, all = per * rows;
@@ -336,7 +337,7 @@ struct W4Flow {
                         lo[e] = pack2<_Float16>(a - lo_f32<_Float16>(hi[e]), b - hi_f32<_Float16>(hi[e]));
                     }
                     p[i] = hi;
-                    p1[i] = lo;
+                    p1[i ^ 8] = lo;   // (a lane of this wave's, which has read what lay there)
                     if (i % 32 == 0) scale[i / 32] = __uint_as_float((254u - up) << 23);
                 }
             }
@@ -401,10 +402,11 @@ struct W4Flow {
             auto aim_x = [&](int32_t first) {
 #pragma unroll
                 for (int pl = 0; pl < PL; ++pl) {
+                    const uint32_t second = (uint32_t)(STACK ? min((r & 3) / RO, 1) : pl);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        xa[j][pl] = (uint32_t)(STACK ? min((r & 3) / RO, 1) : pl) * plane + (uint32_t)(first * here) * 512u +
-                                    16u * ((uint32_t)(G == 128 ? 4 * q + j : 4 * j + q) ^ (uint32_t)(first & 15));
+                        xa[j][pl] = second * plane + (uint32_t)(first * here) * 512u +
+                                    16u * ((uint32_t)(G == 128 ? 4 * q + j : 4 * j + q) ^ (uint32_t)(first & 15) ^ (8u * second));
                 }
 #pragma unroll
                 for (int i = 0; i < RO; ++i) sa[i] = 2 * plane + 4u * (uint32_t)((OWN_ROW ? first : min(4 * i + q, rows - 1)) * here);
