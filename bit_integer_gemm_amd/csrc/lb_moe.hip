@@ -13,10 +13,10 @@
 // Between the products h is fp32, in the down product's nibble order, and the down product's outputs
 // are fp32.
 //
-// Bound by the chosen experts' weights, read once (2 of 8 of 4096 x 11008: 98.6 MB in 27 us and
-// 48.8 in 15; 122 of 128 of 2048 x 1024, met by 48 tokens: 262 MB in 57 us, 4.6 TB/s, and 133 in
-// 36), and by what each launch takes before its first weights: 9 us for the first product of 5
-// tokens, 6 for the second.  5 tokens of 6 of 64 experts of 2048 x 1376, G = 32: 4.8 + 25.9 + 17.0
+// Bound by the chosen experts' weights, read once (2 of 8 of 4096 x 11008: 98.6 MB in 28 us and
+// 48.8 in 16.6; about 118 of 128 of 2048 x 1024, met by 48 tokens: 262 MB in 56 us, 4.6 TB/s, and 133
+// in 37), and by what each launch takes before its first weights: 9 us for the first product of 5
+// tokens, 6 for the second.  5 tokens of 6 of 64 experts of 2048 x 1376, G = 32: 4.9 + 25.9 + 17.1
 // + 5.0 us, where the bytes would take 26.
 #include <algorithm>
 
@@ -436,8 +436,8 @@ __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_kernel(MoeArgs a, MoeG
 }
 
 // One token: a workgroup's columns get all of its experts' sums, weighted here (tile k c + j: column
-// tile c of expert j), and no launch follows.  15 us for 2 experts of 4096 x 11008, where a product
-// and the weighted sum took 15.4 + 4.6.
+// tile c of expert j), and no launch follows.  16.6 us for 2 experts of 4096 x 11008 (15 before what
+// passes between the products kept fp32's digits, where a product and the weighted sum took 15.4 + 4.6).
 template <class T, int G>
 __global__ __launch_bounds__(64 * W4_WAVES) void moe_down_token_kernel(MoeArgs a, int32_t per, uint32_t x_bytes)
 {

@@ -8,10 +8,10 @@ namespace lb {
 
 // Up to 16 rows: a workgroup takes all of x against some tiles of 16 columns.  1 x 4096 x 4096
 // (G = 128) in 5.9 us (a launch and three latencies; the bytes alone would take 1.8), 8 x 11008 x
-// 4096 (G = 64) in 10.5 us, 2.5 TB/s.  x is asked for first: with the weights first, the latter take
-// 11.7.  16 x 4096 x 4096 and 16 x 11008 x 4096 take 10.4 and 12.9 us, where the tiles for more
-// rows take 18.5 and 27.5 (their three launches); 17 x 4096 x 4096 takes 18.1 there, and would
-// take about 20 here, all weights twice.
+// 4096 (G = 64) in 10.7 us, 2.5 TB/s.  x is asked for first: with the weights first, the latter took
+// 1.2 us more.  As calls in a graph 16 x 4096 x 4096 and 16 x 11008 x 4096 (G = 128) take 10.8 and 13.4 us,
+// where the tiles for more rows take 14.8 and 22.4 (their three launches); 16 x 4096 x 11008 (G = 64)
+// 21.4 and 22.0.  17 rows of them take 14.8, 22.3 and 21.8 there, and would read all weights twice here.
 // ONE: all of x is in LDS at once.
 struct FewArgs {
     const uint8_t *w;

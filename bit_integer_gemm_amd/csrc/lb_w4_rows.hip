@@ -10,14 +10,10 @@
 // same groups of the other: with all of the first ahead of the second, fp32's roundings of what
 // cancels later are as large as those of two parts (11008 weights in groups of 32).
 //
-// 4096 x 11008 x 4096 (G = 128): 342 us for ten whole rounds of 128 x 256 tiles and 43 for the
-// columns that are left, 960 TFLOP/s; the matrix cores are busy 46% of the time at the 2.04 GHz
-// that the card allows (2.29 GHz with the copies taken out, where a large library product in
-// bf16, without levels to make, reaches 1217 TFLOP/s): nine vector instructions, which make levels
-// and scale sums, go with every matrix instruction.  Tile order:
-// groups of 2, 4, 8 and 16 tiles of rows 361, 355, 355 and 361 us; all copies at a stage's start
-// or early in it 361; a schedule prescribed instruction by instruction 342 where the compiler's
-// own took 326 of the same loop.
+// 4096 x 11008 x 4096 (G = 128): 346 us for five whole rounds of 128 x 256 tiles and 42 for the
+// columns that are left, 950 TFLOP/s; the matrix cores are busy 47% of the time at the 2 GHz that
+// the card allows (a large library product in bf16, without levels to make, reaches 1217): nine
+// vector instructions, which make levels and scale sums, go with every matrix instruction.
 //
 // A launch of its own puts x in the order in which nibbles come out of a word, rows padded to
 // whole stages with zeros, and forms X.
@@ -368,7 +364,7 @@ __global__ __launch_bounds__(512, 2) void w4_rows_kernel(RowsArgs a)
         return;
     }
     // Out through LDS, so that rows are written in pieces of 16 bytes (directly, 2 bytes a lane, the
-    // stores take 19 us of 410 at 4096 x 11008 x 4096).
+    // stores took 19 us more at 4096 x 11008 x 4096).
     __syncthreads();
     T *const tile = (T *)smem;
 #pragma unroll
