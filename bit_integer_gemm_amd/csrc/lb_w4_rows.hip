@@ -3,8 +3,8 @@
 // Per group g of G weights, with u' = 16 + u exact in 16 bits and b' = b - 16 s (lb_w4.hpp):
 //   out = sum_g b'[n,g] X[m,g] + sum_g s[n,g] sum_{k in g} x[m,k] u'[n,k],  X[m,g] = sum_{k in g} x[m,k].
 // The first term is a product of its own with K / G in place of K: X and b' in three bf16 parts
-// each (2^-23 of a term; two parts, 2^-16, cost fp16 outputs up to 1.4 times their rounding where
-// activations have a mean).  The second is exact products summed in fp32, a group at a time into a
+// each (2^-23 of a term; with two, 2^-16, the error of fp16 outputs was up to 1.3 times that of their
+// rounding where activations have a mean).  The second is exact products summed in fp32, a group at a time into a
 // second set of accumulators, which are scaled into the first: no weight is ever rounded.  The
 // terms have opposite signs, so that they enter the accumulators 16 groups of the one before the
 // same groups of the other: with all of the first ahead of the second, fp32's roundings of what

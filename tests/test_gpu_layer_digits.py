@@ -133,3 +133,54 @@ def test_largest_activations(M, group):
     lb.lb_linear_w4(x.cuda(), w.cuda(), p.cuda(), out)
     assert out.isfinite().all()
     check_output(out, x.double() @ wd.T, product_bound(x, p, K), BF)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("M", [2, 40])
+def test_subnormal_activations(dtype, M):
+    """Activations below the smallest normal number count as much as others."""
+    K, N = 128, 40
+    least = torch.finfo(dtype).smallest_normal
+    x = torch.zeros(M, K, dtype=torch.float64)
+    x[torch.arange(M), torch.arange(M)] = least * torch.linspace(0.25, 0.75, M, dtype=torch.float64)
+    x = x.to(dtype)
+    assert ((x.double() > 0).sum(1) == 1).all()
+    w = torch.full((N, K // 2), 255, dtype=torch.uint8)
+    p = torch.tensor([2.0 ** 7, 0.0], dtype=dtype).expand(N, 1, 2).contiguous()
+    out = torch.empty(M, N, dtype=dtype, device="cuda")
+    lb.lb_linear_w4(x.cuda(), w.cuda(), p.cuda(), out)
+    want = 15 * 2.0 ** 7 * x.double().sum(1, keepdim=True).expand(M, N)
+    tol = 64 * STEP * want * 3 + half_step(dtype) * want * (1 + 2 ** -12)   # (31 - 16 of them)
+    assert ((out.cpu().double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("T", [1, 3, 7, 12])
+def test_small_beside_large_between_the_products(T):
+    """What passes between an expert's products may differ by 2^30 within the 256 numbers that share a power of two."""
+    group, H, I = 32, 64, 512
+    place = torch.arange(16) * 32 + 5
+    size = 2.0 ** -(2.0 * torch.arange(16) % 32)   # of each line's eight: 1, 2^-2 .. 2^-14, and 2^-16 .. 2^-30
+    size[8] = 1.0
+    w1 = torch.zeros(1, 2 * I, H // 2, dtype=torch.uint8)
+    p1 = torch.zeros(1, 2 * I, H // group, 2, dtype=BF)
+    w1[0, place] = w1[0, I + place] = 255
+    p1[0, place, :, 0] = 0.25
+    p1[0, I + place, :, 0] = size[:, None].to(BF)
+    gate = torch.tensor(15 * 0.25, dtype=torch.float64)
+    h = gate / (1 + torch.exp(-gate)) * 15 * size.double()
+    p2 = torch.zeros(1, H, I // group, 2, dtype=BF)
+    n = torch.arange(H)
+    p2[0, n, n % 16, 0] = 1.0
+    w2 = torch.full((1, H, I // 2), 255, dtype=torch.uint8)
+    x = torch.zeros(T, H, dtype=BF)
+    x[torch.arange(T), torch.arange(T)] = 1.0
+    out = torch.empty(T, H, dtype=BF, device="cuda")
+    lb.lb_moe_w4(x.cuda(), torch.ones(1, H, dtype=BF, device="cuda"), w1.cuda(), p1.cuda(), w2.cuda(), p2.cuda(), out, top_k=1)
+    want = 15 * h[n % 16]
+    largest = h.view(2, 8).amax(1)[n % 16 // 8]
+    # of the number itself as between nearly equal ones; its parts' last steps: 2^-39 of the largest, 31 and 16 times
+    before = (7 + (31 * 4 + 16 * 4 + 31 * 2) / 15 + 10) * STEP * want + 47 * 2.0 ** -39 * largest
+    tol = before + half_step(BF) * (want + before)
+    off = (out.cpu().double() - want).abs()
+    assert (off <= tol).all(), (off / tol).max()
+    assert (before[n % 16 == 15] < want[n % 16 == 15] / 8).all()   # (the smallest says something)
