@@ -582,7 +582,7 @@ def lb_residual_norm(Y, R, R_out, X, w=None, post_w=None, gate=None, alpha: floa
 
 _ROPE_LAYOUTS = {"half": LB_ROPE_HALF, "pairs": LB_ROPE_PAIRS, LB_ROPE_HALF: LB_ROPE_HALF, LB_ROPE_PAIRS: LB_ROPE_PAIRS}
 _ROPE_SCALINGS = {"plain": LB_ROPE_PLAIN, "linear": LB_ROPE_LINEAR, "base": LB_ROPE_BASE, "parts": LB_ROPE_PARTS,
-                  "bands": LB_ROPE_BANDS}
+                  "bands": LB_ROPE_BANDS, **{k: k for k in range(LB_ROPE_BANDS + 1)}}
 
 
 def lb_rope_freqs(R: int, base: float = 10000.0, scaling="plain", factor: float = 1.0, before: float = 0.0,
@@ -592,9 +592,11 @@ def lb_rope_freqs(R: int, base: float = 10000.0, scaling="plain", factor: float 
     longer than `before`.  low, high: turns; the defaults are those usual with "parts" ("bands" is mostly used with
     high 4)."""
     T = _torch()
+    kind = _ROPE_SCALINGS.get(scaling)
+    if kind is None:
+        raise ValueError(f"scaling: {scaling!r}, expected one of {tuple(k for k in _ROPE_SCALINGS if isinstance(k, str))}")
     f, m = (ctypes.c_double * max(R // 2, 1))(), ctypes.c_float()
-    _raise(load().lb_rope_freqs(f, ctypes.byref(m), R, base, _ROPE_SCALINGS.get(scaling, scaling), factor, before, low,
-                                high), "lb_rope_freqs")
+    _raise(load().lb_rope_freqs(f, ctypes.byref(m), R, base, kind, factor, before, low, high), "lb_rope_freqs")
     return T.torch.tensor(list(f), dtype=T.torch.float64, device=device), m.value
 
 

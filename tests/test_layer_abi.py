@@ -186,3 +186,15 @@ def test_rope_freqs_parts_of_short_contexts(lib, R, before, low, high):
     np.testing.assert_allclose(got[turns <= low * (1 - 1e-9)], f[turns <= low * (1 - 1e-9)] / 8, **near)
     np.testing.assert_allclose(got[turns >= high * (1 + 1e-9)], f[turns >= high * (1 + 1e-9)], **near)
     assert (got <= f * (1 + 1e-15)).all() and (got >= f / 8 * (1 - 1e-15)).all()
+
+
+def test_rope_freqs_names(lib):
+    pytest.importorskip("torch")
+    for name, number in (("plain", lb.LB_ROPE_PLAIN), ("linear", lb.LB_ROPE_LINEAR), ("base", lb.LB_ROPE_BASE),
+                         ("parts", lb.LB_ROPE_PARTS), ("bands", lb.LB_ROPE_BANDS)):
+        args = dict(factor=4.0, before=4096.0, device="cpu")
+        (f, m), (g, n) = (lb.lb_rope_freqs(64, scaling=s, **args) for s in (name, number))
+        assert (f == g).all() and m == n and len(f) == 32
+    for other in ("longer", 5, -1, None):
+        with pytest.raises(ValueError, match="scaling"):
+            lb.lb_rope_freqs(64, scaling=other, device="cpu")
